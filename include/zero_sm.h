@@ -253,7 +253,11 @@ enum {
 /* 16-bit storage formats (ZERO_OPT_DTYPE).  The pages account gradients and
  * parameters at 2 bytes and name fp16 as a communication type ([M] section 3.3
  * configuration); bf16 is the default. */
-enum { ZERO_DTYPE_BF16 = 0, ZERO_DTYPE_F16 = 1 };
+enum {
+  ZERO_DTYPE_BF16 = 0,
+  ZERO_DTYPE_F16 = 1,
+  ZERO_DTYPE_F32 = 2  /* the zero_mx4_* calls' dense matrices only; ZERO_OPT_DTYPE refuses it */
+};
 
 /* Fused-step kernels (ZERO_OPT_KERNEL).  Both compute the same bits, and the
  * choice also applies to the two passes of a clipped step (zero_set_clip),
@@ -757,7 +761,8 @@ zero_status zero_read_stats(zero_ctx* ctx, void* stream, zero_step_stats* out);
 zero_status zero_check_guards(zero_ctx* ctx, void* stream, int64_t out[3]);
 
 /* Message of the last failure on ctx (never NULL; "" when none).  With
- * ctx == NULL: the reason the calling thread's last zero_init failed.
+ * ctx == NULL: the reason the calling thread's last zero_init, or a later
+ * zero_mx4_* call without a context, failed.
  * Library plumbing: no passage of the pages defines it.
  */
 const char* zero_last_error(const zero_ctx* ctx);
@@ -772,6 +777,118 @@ const char* zero_last_error(const zero_ctx* ctx);
  * Library plumbing: no passage of the pages defines it.
  */
 void zero_destroy(zero_ctx* ctx);
+
+/* ------------------------------------------- microscaled 4-bit (MX4) data -- */
+/*
+ * What ZeRO's collectives move, at 4.25 bits an element instead of 16: the
+ * gathered parameters of a layer ([T] section "ZeRO-3"; [M] section 2 on
+ * ZeRO-3's 1.5 times volume), the gradients that are reduce-scattered ([T]
+ * section "ZeRO-2"), and the product that reads a gathered layer without
+ * expanding it.  The pages describe 16-bit buffers only; the format is the
+ * public microscaling (MX) one with 4-bit elements.
+ *
+ * A matrix is kept row by row in blocks of 32 consecutive elements (the last
+ * block of a row is filled up with zeros).  A block has one scale byte s,
+ * standing for 2^(s - 127) (255: every element is NaN), and 16 bytes of
+ * codes: element 2i of the block in the low half of byte i, element 2i + 1 in
+ * the high half.  A code's top bit is the sign, its low three bits the
+ * magnitude 0, .5, 1, 1.5, 2, 3, 4 or 6.  A block whose largest magnitude is
+ * m gets s = max(floor(log2 m) - 2 + 127, 0); an element x becomes
+ * x * 2^(127 - s) rounded to the grid, magnitudes above 6 becoming 6.  A
+ * block that holds an infinity or a NaN gets s = 255 and codes 0, so that
+ * the step's non-finite count sees it.
+ *
+ * Rounding is to nearest even, or stochastic: floor(t + u) with t the scaled
+ * magnitude in units of its grid step and u a number of 16 random bits /
+ * 2^16, so that the mean of the result is the value (up to 2^-16 of a step).
+ * Element e of block b -- b counting the result's blocks row by row -- takes
+ * 16-bit number e % 8 (low half first) of Philox4x32-10 with key `seed` and
+ * counter 4 b + e / 8: the same bits for the same seed, and no random numbers
+ * in memory.
+ *
+ * The calls that take no context report errors through zero_last_error(NULL);
+ * the matrices must be on the current CUDA device.  They keep no state
+ * between calls and may be captured in CUDA graphs.  Matrices without rows
+ * or columns are accepted and do nothing (a product over no columns is 0).
+ * Outputs must not overlap inputs.
+ */
+#define ZERO_MX4_BLOCK 32
+
+typedef struct zero_mx4 {
+  void* codes;          /* device, 16-byte aligned */
+  void* scales;         /* device, one byte per block (4-byte aligned rows load faster) */
+  int64_t rows, cols;   /* elements; each below 2^31 - 256 */
+  int64_t code_pitch;   /* bytes between rows of codes: a multiple of 16, >= 16 * ceil(cols / 32) */
+  int64_t scale_pitch;  /* bytes between rows of scales, >= ceil(cols / 32) */
+} zero_mx4;
+
+enum { ZERO_MX4_NEAREST = 0, ZERO_MX4_STOCHASTIC = 1 };
+
+/* Quantise the dense matrix src (rows x cols of `dtype`, ld elements between
+ * rows; 16-byte aligned rows load faster): `out` (rows x cols) in blocks
+ * along the rows, `out_t` (cols x rows) its transpose, in blocks along the
+ * columns of src -- the operands of products that sum over the one axis and
+ * the other.  Either may be NULL; both together read src once.  `seed` is
+ * used by ZERO_MX4_STOCHASTIC only.  Errors: ZERO_EINVAL, ZERO_ECUDA.
+ * No passage of the pages defines it. */
+zero_status zero_mx4_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t rounding,
+                              uint64_t seed, const zero_mx4* out, const zero_mx4* out_t, void* stream);
+
+/* Quantise the transpose of an MX4 matrix: out (in->cols x in->rows) holds
+ * the values of `in`, in new blocks along the other axis.  The backward
+ * product of a gathered layer needs it.  No passage of the pages defines it. */
+zero_status zero_mx4_transpose(const zero_mx4* in, int32_t rounding, uint64_t seed, const zero_mx4* out, void* stream);
+
+/* Read an MX4 matrix back: element * 2^(s - 127), exact in bf16 and binary32,
+ * rounded to nearest even in binary16.  dst: in->rows x in->cols of `dtype`,
+ * ld elements between rows.  No passage of the pages defines it. */
+zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, int64_t ld, void* stream);
+
+/* out[i][j] = sum over k of a[i][k] b[j][k] (a->rows x b->rows of `dtype`, ld
+ * elements between rows), for two MX4 matrices of the same number of columns,
+ * on the block-scaled tensor cores: the elements' products are exact and
+ * their sum is held in binary32, rounded once to `dtype`.  The same bits on
+ * every run.  No passage of the pages defines it (the layer's use, [T]
+ * section "ZeRO-3", parts "1. 前向" and "2. 反向"). */
+zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int32_t dtype, int64_t ld, void* stream);
+
+/* The forward product of a linear layer whose weight w (outputs x inputs) is
+ * an MX4 matrix, for one token or many: y = Q(x) w^T, x (tokens x inputs of
+ * `dtype`) quantised along its rows into the caller's xq (tokens x inputs),
+ * y tokens x outputs of `y_dtype`.  The same as zero_mx4_quantize and
+ * zero_mx4_matmul.  [T] section "ZeRO-3", part "1. 前向". */
+zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t ld, const zero_mx4* w,
+                            const zero_mx4* xq, void* y, int32_t y_dtype, int64_t ld_y, void* stream);
+
+/* Wait for `stream` and report whether a bounded wait inside a product kernel
+ * on the current device ran out since the last call: ZERO_ECUDA (that
+ * product's result is invalid) or ZERO_OK.  No passage of the pages defines
+ * it. */
+zero_status zero_mx4_check(void* stream);
+
+/*
+ * All-gather of [lo, hi) into MX4 buffers: as zero_all_gather, the owners'
+ * 16-bit parameters go to every rank, here quantised (to nearest even) in
+ * blocks of 32 flat elements counted from lo.  rank_codes / rank_scales: host
+ * arrays of N device pointers to 16 * ceil((hi - lo) / 32) bytes (16-byte
+ * aligned) and ceil((hi - lo) / 32) bytes.  A tensor whose rows are a multiple
+ * of 32 long and whose flat offset from lo is one too lies in them as an MX4
+ * matrix (code_pitch cols / 2, scale_pitch cols / 32), ready for
+ * zero_mx4_linear.  [T] section "ZeRO-3", the gather before a layer's use.
+ */
+zero_status zero_mx4_all_gather(zero_ctx* ctx, int64_t lo, int64_t hi, void* const* rank_codes, void* const* rank_scales,
+                                void* stream);
+
+/*
+ * Reduce-scatter of [lo, hi) from MX4 gradients: as zero_reduce_scatter (the
+ * values summed in binary32 in rank order, times fp32(1/N), rounded to the
+ * 16-bit format, into the owners' shards; the norm and non-finite count
+ * accumulated), with rank r's gradient of [lo, hi) in rank_codes[r] /
+ * rank_scales[r], laid out as zero_mx4_all_gather writes them.  Stage 2 and 3
+ * only.  [T] section "ZeRO-2", part on reduce-scatter.
+ */
+zero_status zero_mx4_reduce_scatter(zero_ctx* ctx, int64_t lo, int64_t hi, const void* const* rank_codes,
+                                    const void* const* rank_scales, void* stream);
 
 /* ------------------------------------------------ one logical rank per GPU -- */
 /*

@@ -53,7 +53,9 @@ ZERO_OPT_STORE_HINT = 16
 ZERO_OPT_GUARD = 17
 ZERO_OPT_NVTX = 18
 ZERO_OPT_LAYERED = 19
-ZERO_DTYPE_BF16, ZERO_DTYPE_F16 = 0, 1
+ZERO_DTYPE_BF16, ZERO_DTYPE_F16, ZERO_DTYPE_F32 = 0, 1, 2
+ZERO_MX4_BLOCK = 32
+ZERO_MX4_NEAREST, ZERO_MX4_STOCHASTIC = 0, 1
 (ZERO_VIEW_MASTER, ZERO_VIEW_EXP_AVG, ZERO_VIEW_EXP_AVG_SQ, ZERO_VIEW_PARAM, ZERO_VIEW_GRAD_SHARD,
  ZERO_VIEW_GRAD_BUF, ZERO_VIEW_GATHER) = range(7)
 
@@ -80,6 +82,11 @@ class zero_step_stats(ctypes.Structure):
                 ("comm_elems", ctypes.c_int64 * 3), ("clip_coef", ctypes.c_double), ("skipped", ctypes.c_int64)]
 
 
+class zero_mx4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("code_pitch", ctypes.c_int64), ("scale_pitch", ctypes.c_int64)]
+
+
 zero_grad_fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                 ctypes.c_int64, ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p)
 zero_gather_fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
@@ -87,6 +94,7 @@ zero_gather_fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int32,
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _PTRS = ctypes.POINTER(ctypes.c_void_p)
+_MX4 = ctypes.POINTER(zero_mx4)
 _SIGS = {
     "zero_version": (_i32, []),
     "zero_init": (_i32, [ctypes.POINTER(zero_layout), _i32, _i32, _i64, ctypes.POINTER(_vp)]),
@@ -125,6 +133,14 @@ _SIGS = {
     "zero_check_guards": (_i32, [_vp, _vp, ctypes.POINTER(ctypes.c_int64)]),
     "zero_fused_step_static": (_i32, [_i32, _i64, _PTRS, _vp, _vp, _vp, _PTRS,
                                       ctypes.POINTER(zero_adam_hparams), _i64, _vp, _vp]),
+    "zero_mx4_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, ctypes.c_uint64, _MX4, _MX4, _vp]),
+    "zero_mx4_transpose": (_i32, [_MX4, _i32, ctypes.c_uint64, _MX4, _vp]),
+    "zero_mx4_dequantize": (_i32, [_MX4, _vp, _i32, _i64, _vp]),
+    "zero_mx4_matmul": (_i32, [_MX4, _MX4, _vp, _i32, _i64, _vp]),
+    "zero_mx4_linear": (_i32, [_vp, _i32, _i64, _i64, _MX4, _MX4, _vp, _i32, _i64, _vp]),
+    "zero_mx4_check": (_i32, [_vp]),
+    "zero_mx4_all_gather": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
+    "zero_mx4_reduce_scatter": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
     "zero_dist_init": (_i32, [ctypes.POINTER(zero_layout), _i32, _i32, _i32, ctypes.POINTER(_vp)]),
     "zero_dist_sizes": (_i32, [_vp, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
     "zero_dist_tensor_offsets": (_i32, [_vp, ctypes.POINTER(_i64), _i32]),
@@ -153,7 +169,9 @@ for _name, (_res, _args) in _SIGS.items():
     globals()[_name] = _fn
 
 __all__ = list(_SIGS) + ["ZeroOptimizer", "ZeroDist", "AdamHParams", "ZeroError", "lib", "LIB_PATH",
-                         "options_from_config", "exchange_records", "rank_ordered_norm", "ordered_step"]
+                         "options_from_config", "exchange_records", "rank_ordered_norm", "ordered_step",
+                         "MX4", "mx4_empty", "mx4_quantize", "mx4_quantize_both", "mx4_transpose", "mx4_dequantize", "mx4_matmul",
+                         "mx4_linear", "mx4_linear_backward", "mx4_check"]
 ZERO_DIST_ARENA_GRAD, ZERO_DIST_ARENA_PARAM, ZERO_DIST_ARENA_STATES, ZERO_DIST_ARENA_SCRATCH = 0, 1, 2, 3
 ZERO_DIST_ARENA_GATHER = 4
 ZERO_DIST_NUM_ARENAS = 5
@@ -615,6 +633,268 @@ class ZeroOptimizer:
     def all_gather(self, lo: int, hi: int, rank_out: Optional[Sequence[int]] = None, stream=None):
         ptrs = None if rank_out is None else _ptr_array(rank_out)
         self._check(zero_all_gather(self.ctx, lo, hi, ptrs, self._stream(stream)), "zero_all_gather")
+
+    # -- MX4 collectives --
+    def _mx4_ptrs(self, lo: int, hi: int, codes, scales):
+        """The N ranks' buffers of [lo, hi): uint8 tensors (or one with a
+        leading dimension of N) that hold the interval's blocks."""
+        nb = (int(hi) - int(lo) + ZERO_MX4_BLOCK - 1) // ZERO_MX4_BLOCK
+        out = []
+        for name, bufs, need in (("codes", codes, 16 * nb), ("scales", scales, nb)):
+            if len(bufs) != self.n_ranks:
+                raise ValueError(f"{name}: {len(bufs)} buffers for {self.n_ranks} ranks")
+            one = bufs if isinstance(bufs, self._torch.Tensor) else None
+            for b in ((one,) if one is not None else bufs):
+                if b.dtype != self._torch.uint8 or not b.is_contiguous() or b.device != self.device:
+                    raise ValueError(f"{name}: contiguous uint8 tensors on {self.device} are needed")
+                if b.numel() < need * (self.n_ranks if one is not None else 1):
+                    raise ValueError(f"{name}: {need} bytes a rank are needed for [{lo}, {hi})")
+            if one is not None:
+                step = one.numel() // self.n_ranks
+                out.append(_ptr_array([one.data_ptr() + r * step for r in range(self.n_ranks)]))
+            else:
+                out.append(_ptr_array([b.data_ptr() for b in bufs]))
+        return out
+
+    def all_gather_mx4(self, lo: int, hi: int, codes, scales, stream=None):
+        """The owners' parameters [lo, hi) quantised into every rank's MX4
+        buffers: ``codes[r]`` 16 bytes and ``scales[r]`` one byte for each 32
+        elements (zero_mx4_all_gather)."""
+        c, s = self._mx4_ptrs(lo, hi, codes, scales)
+        with _on(self.device):
+            self._check(zero_mx4_all_gather(self.ctx, lo, hi, c, s, self._stream(stream)), "zero_mx4_all_gather")
+
+    def reduce_scatter_mx4(self, lo: int, hi: int, codes, scales, stream=None):
+        """The mean of the ranks' MX4 gradients of [lo, hi) into the owners'
+        reduced-gradient shards (zero_mx4_reduce_scatter)."""
+        c, s = self._mx4_ptrs(lo, hi, codes, scales)
+        with _on(self.device):
+            self._check(zero_mx4_reduce_scatter(self.ctx, lo, hi, c, s, self._stream(stream)),
+                        "zero_mx4_reduce_scatter")
+
+
+# ------------------------------------------------------ MX4 matrices ----
+
+class _on:
+    """Makes ``device`` the current CUDA device for a call (free when it is)."""
+
+    def __init__(self, device):
+        self._index = device.index
+
+    def __enter__(self):
+        import torch
+
+        now = torch.cuda.current_device()
+        self._back = now if self._index is not None and self._index != now else None
+        if self._back is not None:
+            torch.cuda.set_device(self._index)
+
+    def __exit__(self, *exc):
+        if self._back is not None:
+            import torch
+
+            torch.cuda.set_device(self._back)
+        return False
+
+
+class MX4:
+    """A microscaled 4-bit matrix of rows x cols elements (zero_mx4 in
+    include/zero_sm.h): uint8 CUDA tensors ``codes`` [rows, pitch] and
+    ``scales`` [rows, pitch], each with contiguous rows."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "_c")
+
+    def __init__(self, codes, scales, rows: int, cols: int):
+        self.codes, self.scales, self.rows, self.cols = codes, scales, int(rows), int(cols)
+        nb = -(-self.cols // ZERO_MX4_BLOCK)
+        for name, t, need in (("codes", codes, 16 * nb), ("scales", scales, nb)):
+            if str(t.dtype) != "torch.uint8" or t.dim() != 2 or t.shape[0] != self.rows or t.shape[1] < need or \
+                    (t.shape[1] > 1 and t.stride(1) != 1):
+                raise ValueError(f"{name}: a uint8 tensor of {self.rows} rows of at least {need} bytes is needed")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales are on different devices")
+        pitch = [t.stride(0) if self.rows > 1 else t.shape[1] for t in (codes, scales)]
+        self._c = zero_mx4(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, pitch[0], pitch[1])
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def mx4_empty(rows: int, cols: int, device=None) -> MX4:
+    """An MX4 matrix of uninitialised memory; its scale rows are padded to 4 bytes."""
+    import torch
+
+    nb = -(-int(cols) // ZERO_MX4_BLOCK)
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    return MX4(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
+               torch.empty(rows, -(-nb // 4) * 4, dtype=torch.uint8, device=device), rows, cols)
+
+
+def _dtype_code(dtype) -> int:
+    name = str(dtype)
+    if name == "torch.bfloat16":
+        return ZERO_DTYPE_BF16
+    if name == "torch.float16":
+        return ZERO_DTYPE_F16
+    if name == "torch.float32":
+        return ZERO_DTYPE_F32
+    raise ValueError(f"{name}: matrices are bfloat16, float16 or float32")
+
+
+def _dense(t, name: str):
+    """(pointer, dtype code, elements between rows) of a matrix with contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA matrix is needed")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the rows must be contiguous (stride {t.stride(1)})")
+    return t.data_ptr(), _dtype_code(t.dtype), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _mx4_stream(device, stream) -> int:
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return int(getattr(stream, "cuda_stream", stream))
+
+
+def _mx4_check(st: int, where: str):
+    if st != ZERO_OK:
+        raise ZeroError(st, where, zero_last_error(None).decode())
+
+
+def _same_device(*named):
+    first, device = named[0][0], named[0][1].device
+    for name, t in named[1:]:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, {first} on {device}")
+    return device
+
+
+def _result(out, rows: int, cols: int, dtype, device, name: str = "out"):
+    import torch
+
+    if out is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"{name} is {tuple(out.shape)}, not {(rows, cols)}")
+    return out
+
+
+def _rounding(seed):
+    return (ZERO_MX4_NEAREST, 0) if seed is None else (ZERO_MX4_STOCHASTIC, int(seed) & 0xFFFFFFFFFFFFFFFF)
+
+
+def mx4_quantize(x, transpose: bool = False, seed: Optional[int] = None, out: Optional[MX4] = None, stream=None) -> MX4:
+    """Quantise a matrix in blocks along its rows or, with ``transpose``, its
+    transpose (blocks down x's columns).  ``seed`` rounds stochastically;
+    None rounds to nearest even (zero_mx4_quantize)."""
+    ptr, code, ld = _dense(x, "x")
+    rows, cols = x.shape
+    if out is None:
+        out = mx4_empty(cols, rows, x.device) if transpose else mx4_empty(rows, cols, x.device)
+    device = _same_device(("x", x), ("out", out))
+    rounding, seed = _rounding(seed)
+    c = ctypes.byref(out._c)
+    with _on(device):
+        _mx4_check(zero_mx4_quantize(ptr, code, rows, cols, ld, rounding, seed, None if transpose else c,
+                                     c if transpose else None, _mx4_stream(device, stream)), "zero_mx4_quantize")
+    return out
+
+
+def mx4_quantize_both(x, seed: Optional[int] = None, out: Optional[MX4] = None, out_t: Optional[MX4] = None, stream=None):
+    """(x, its transpose) as MX4 matrices, reading x once."""
+    ptr, code, ld = _dense(x, "x")
+    rows, cols = x.shape
+    out = mx4_empty(rows, cols, x.device) if out is None else out
+    out_t = mx4_empty(cols, rows, x.device) if out_t is None else out_t
+    device = _same_device(("x", x), ("out", out), ("out_t", out_t))
+    rounding, seed = _rounding(seed)
+    with _on(device):
+        _mx4_check(zero_mx4_quantize(ptr, code, rows, cols, ld, rounding, seed, ctypes.byref(out._c),
+                                     ctypes.byref(out_t._c), _mx4_stream(device, stream)), "zero_mx4_quantize")
+    return out, out_t
+
+
+def mx4_transpose(m: MX4, seed: Optional[int] = None, out: Optional[MX4] = None, stream=None) -> MX4:
+    """The transpose of an MX4 matrix, quantised in blocks along the other axis."""
+    out = mx4_empty(m.cols, m.rows, m.device) if out is None else out
+    device = _same_device(("m", m), ("out", out))
+    rounding, seed = _rounding(seed)
+    with _on(device):
+        _mx4_check(zero_mx4_transpose(ctypes.byref(m._c), rounding, seed, ctypes.byref(out._c),
+                                      _mx4_stream(device, stream)), "zero_mx4_transpose")
+    return out
+
+
+def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
+    """The values of an MX4 matrix (bfloat16 unless ``dtype`` or ``out`` says otherwise)."""
+    import torch
+
+    out = _result(out, m.rows, m.cols, dtype or torch.bfloat16, m.device)
+    ptr, code, ld = _dense(out, "out")
+    device = _same_device(("m", m), ("out", out))
+    with _on(device):
+        _mx4_check(zero_mx4_dequantize(ctypes.byref(m._c), ptr, code, ld, _mx4_stream(device, stream)),
+                   "zero_mx4_dequantize")
+    return out
+
+
+def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
+    """a b^T of two MX4 matrices with the same number of columns."""
+    import torch
+
+    out = _result(out, a.rows, b.rows, dtype or torch.bfloat16, a.device)
+    ptr, code, ld = _dense(out, "out")
+    device = _same_device(("a", a), ("b", b), ("out", out))
+    with _on(device):
+        _mx4_check(zero_mx4_matmul(ctypes.byref(a._c), ctypes.byref(b._c), ptr, code, ld,
+                                   _mx4_stream(device, stream)), "zero_mx4_matmul")
+    return out
+
+
+def mx4_linear(x, w: MX4, out=None, xq: Optional[MX4] = None, stream=None):
+    """y = Q(x) w^T for x [tokens, inputs] and an MX4 weight [outputs, inputs];
+    y has x's type unless ``out`` is given.  ``xq`` receives the quantised x."""
+    ptr, code, ld = _dense(x, "x")
+    tokens = x.shape[0]
+    if x.shape[1] != w.cols:
+        raise ValueError(f"x has {x.shape[1]} inputs, w {w.cols}")
+    xq = mx4_empty(tokens, w.cols, x.device) if xq is None else xq
+    y = _result(out, tokens, w.rows, x.dtype, x.device)
+    yptr, ycode, ldy = _dense(y, "out")
+    device = _same_device(("x", x), ("w", w), ("xq", xq), ("out", y))
+    with _on(device):
+        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, ctypes.byref(w._c), ctypes.byref(xq._c), yptr, ycode, ldy,
+                                   _mx4_stream(device, stream)), "zero_mx4_linear")
+    return y
+
+
+def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=None, stream=None):
+    """(dx, dw) of ``mx4_linear``: dx = Q(dy) Q(w^T)^T and dw = Q(dy^T) Q(x^T)^T,
+    each operand quantised in blocks along the axis its product sums over (dy
+    stochastically when ``seed`` is given); the roundings' own gradients are
+    taken as one.  dx has x's type and dw dy's unless given (dw may be a view
+    of a rank's gradient buffer)."""
+    if x.dim() != 2 or dy.dim() != 2 or x.shape[1] != w.cols or dy.shape != (x.shape[0], w.rows):
+        raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} do not fit w {(w.rows, w.cols)}")
+    _same_device(("dy", dy), ("x", x), ("w", w))
+    dyq, dyq_t = mx4_quantize_both(dy, seed, stream=stream)
+    xq_t = mx4_quantize(x, transpose=True, stream=stream)
+    wq_t = mx4_transpose(w, stream=stream)
+    dx = mx4_matmul(dyq, wq_t, x.dtype, dx, stream)
+    dw = mx4_matmul(dyq_t, xq_t, dy.dtype, dw, stream)
+    return dx, dw
+
+
+def mx4_check(device=None, stream=None):
+    """Wait for the stream; raise ZeroError if a bounded wait of a product kernel ran out."""
+    import torch
+
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _on(device):
+        _mx4_check(zero_mx4_check(_mx4_stream(device, stream)), "zero_mx4_check")
 
 
 # ------------------------------------------------ one logical rank per GPU ----

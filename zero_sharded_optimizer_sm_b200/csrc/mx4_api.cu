@@ -1,0 +1,225 @@
+// Entry points of the MX4 operators that need no context (zero_mx4_*):
+// argument checks and launches.  The collectives' are in zero_api.cu.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "../../include/zero_sm.h"
+#include "mx4.cuh"
+
+static_assert(ZERO_DTYPE_BF16 == zsm::kMxBf16 && ZERO_DTYPE_F16 == zsm::kMxF16 && ZERO_DTYPE_F32 == zsm::kMxF32,
+              "element types");
+static_assert(ZERO_MX4_BLOCK == zsm::kMxBlock, "block length");
+
+namespace {
+
+zero_status fail(zero_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  zsm::set_thread_error(buf);
+  return s;
+}
+
+zero_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(ZERO_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+constexpr int64_t kMaxDim = 0x7FFFFFFF - 255;  // row and column numbers of a tile stay in 32 bits
+
+int elem_bytes(int32_t dtype) { return dtype == ZERO_DTYPE_F32 ? 4 : 2; }
+
+zero_status check_dtype(int32_t dtype) {
+  if (dtype != ZERO_DTYPE_BF16 && dtype != ZERO_DTYPE_F16 && dtype != ZERO_DTYPE_F32)
+    return fail(ZERO_EINVAL, "unknown dtype %d", dtype);
+  return ZERO_OK;
+}
+
+zero_status check_dense(const char* name, const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
+  const zero_status st = check_dtype(dtype);
+  if (st != ZERO_OK) return st;
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim)
+    return fail(ZERO_EINVAL, "%s: %lld x %lld is out of range", name, (long long)rows, (long long)cols);
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  if (!p || (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem_bytes(dtype) - 1)))
+    return fail(ZERO_EINVAL, "%s is null or not aligned to its elements", name);
+  if (ld < cols && rows > 1)
+    return fail(ZERO_EINVAL, "%s: %lld elements between rows of %lld", name, (long long)ld, (long long)cols);
+  return ZERO_OK;
+}
+
+zero_status check_mx4(const char* name, const zero_mx4* m) {
+  if (!m) return fail(ZERO_EINVAL, "%s is NULL", name);
+  if (m->rows < 0 || m->cols < 0 || m->rows > kMaxDim || m->cols > kMaxDim)
+    return fail(ZERO_EINVAL, "%s: %lld x %lld is out of range", name, (long long)m->rows, (long long)m->cols);
+  if (m->rows == 0 || m->cols == 0) return ZERO_OK;
+  const int64_t nb = zsm::mx_blocks(m->cols);
+  if (!m->codes || (reinterpret_cast<uintptr_t>(m->codes) & 15u) || !m->scales)
+    return fail(ZERO_EINVAL, "%s: codes must be 16-byte aligned and neither codes nor scales NULL", name);
+  if (m->code_pitch % 16 || m->code_pitch < 16 * nb)
+    return fail(ZERO_EINVAL, "%s: code_pitch %lld must be a multiple of 16, at least 16 * %lld blocks", name,
+                (long long)m->code_pitch, (long long)nb);
+  if (m->scale_pitch < nb)
+    return fail(ZERO_EINVAL, "%s: scale_pitch %lld is less than the row's %lld blocks", name, (long long)m->scale_pitch,
+                (long long)nb);
+  return ZERO_OK;
+}
+
+zsm::MxMatrix matrix(const zero_mx4& m) {
+  return {static_cast<uint8_t*>(m.codes), static_cast<uint8_t*>(m.scales), m.rows, m.cols, m.code_pitch, m.scale_pitch};
+}
+
+// SMs of the current device, asked for once per device.
+cudaError_t sm_count(int* n) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*n = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*n, std::memory_order_relaxed);
+  return e;
+}
+
+zero_status check_rounding(int32_t rounding) {
+  if (rounding != ZERO_MX4_NEAREST && rounding != ZERO_MX4_STOCHASTIC)
+    return fail(ZERO_EINVAL, "unknown rounding %d", rounding);
+  return ZERO_OK;
+}
+
+zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtype, int64_t ld, int pdl, int sms,
+                   cudaStream_t s) {
+  zsm::MxMatmulArgs m = {};
+  m.a = matrix(a);
+  m.b = matrix(b);
+  m.out = out;
+  m.type = dtype;
+  m.ld = b.rows == 1 ? std::max<int64_t>(ld, 1) : ld;
+  m.pdl = pdl;
+  const cudaError_t e = zsm::launch_mx_matmul(m, sms, s);
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 product launch");
+}
+
+// A product over no elements: zeros.
+zero_status zero_fill(void* out, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, cudaStream_t s) {
+  const int es = elem_bytes(dtype);
+  const cudaError_t e = cudaMemset2DAsync(out, (size_t)(rows > 1 ? ld : cols) * es, 0, (size_t)cols * es, (size_t)rows, s);
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "clearing the product");
+}
+
+}  // namespace
+
+extern "C" {
+
+zero_status zero_mx4_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t rounding,
+                              uint64_t seed, const zero_mx4* out, const zero_mx4* out_t, void* stream) {
+  zero_status st = check_dense("src", src, dtype, rows, cols, ld);
+  if (st != ZERO_OK) return st;
+  if ((st = check_rounding(rounding)) != ZERO_OK) return st;
+  if (!out && !out_t) return fail(ZERO_EINVAL, "neither out nor out_t is given");
+  if (out && (st = check_mx4("out", out)) != ZERO_OK) return st;
+  if (out_t && (st = check_mx4("out_t", out_t)) != ZERO_OK) return st;
+  if (out && (out->rows != rows || out->cols != cols))
+    return fail(ZERO_EINVAL, "out is not %lld x %lld", (long long)rows, (long long)cols);
+  if (out_t && (out_t->rows != cols || out_t->cols != rows))
+    return fail(ZERO_EINVAL, "out_t is not %lld x %lld", (long long)cols, (long long)rows);
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  zsm::MxQuantArgs a = {};
+  a.src = src;
+  a.type = dtype;
+  a.rows = rows, a.cols = cols, a.ld = rows > 1 ? ld : cols;
+  if (out) a.out = matrix(*out);
+  if (out_t) a.out_t = matrix(*out_t);
+  a.stochastic = rounding == ZERO_MX4_STOCHASTIC;
+  a.seed = seed;
+  e = zsm::launch_mx_quantize(a, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 quantise launch");
+}
+
+zero_status zero_mx4_transpose(const zero_mx4* in, int32_t rounding, uint64_t seed, const zero_mx4* out, void* stream) {
+  zero_status st = check_mx4("in", in);
+  if (st != ZERO_OK) return st;
+  if ((st = check_mx4("out", out)) != ZERO_OK) return st;
+  if ((st = check_rounding(rounding)) != ZERO_OK) return st;
+  if (out->rows != in->cols || out->cols != in->rows)
+    return fail(ZERO_EINVAL, "out is not %lld x %lld", (long long)in->cols, (long long)in->rows);
+  if (in->rows == 0 || in->cols == 0) return ZERO_OK;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  zsm::MxQuantArgs a = {};
+  a.from = matrix(*in);
+  a.rows = in->rows, a.cols = in->cols;
+  a.out_t = matrix(*out);
+  a.stochastic = rounding == ZERO_MX4_STOCHASTIC;
+  a.seed = seed;
+  e = zsm::launch_mx_quantize(a, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 transpose launch");
+}
+
+zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, int64_t ld, void* stream) {
+  zero_status st = check_mx4("in", in);
+  if (st != ZERO_OK) return st;
+  if ((st = check_dense("dst", dst, dtype, in->rows, in->cols, ld)) != ZERO_OK) return st;
+  if (in->rows == 0 || in->cols == 0) return ZERO_OK;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  zsm::MxDequantArgs a = {matrix(*in), dst, dtype, in->rows > 1 ? ld : in->cols};
+  e = zsm::launch_mx_dequantize(a, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 read-back launch");
+}
+
+zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int32_t dtype, int64_t ld, void* stream) {
+  zero_status st = check_mx4("a", a);
+  if (st != ZERO_OK) return st;
+  if ((st = check_mx4("b", b)) != ZERO_OK) return st;
+  if (a->cols != b->cols)
+    return fail(ZERO_EINVAL, "a has %lld columns, b %lld", (long long)a->cols, (long long)b->cols);
+  if ((st = check_dense("out", out, dtype, a->rows, b->rows, ld)) != ZERO_OK) return st;
+  if (a->rows == 0 || b->rows == 0) return ZERO_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->cols == 0) return zero_fill(out, dtype, a->rows, b->rows, ld, s);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  return matmul(*a, *b, out, dtype, ld, 0, sms, s);
+}
+
+zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t ld, const zero_mx4* w, const zero_mx4* xq,
+                            void* y, int32_t y_dtype, int64_t ld_y, void* stream) {
+  zero_status st = check_mx4("w", w);
+  if (st != ZERO_OK) return st;
+  if ((st = check_mx4("xq", xq)) != ZERO_OK) return st;
+  if ((st = check_dense("x", x, dtype, tokens, w->cols, ld)) != ZERO_OK) return st;
+  if ((st = check_dense("y", y, y_dtype, tokens, w->rows, ld_y)) != ZERO_OK) return st;
+  if (xq->rows != tokens || xq->cols != w->cols)
+    return fail(ZERO_EINVAL, "xq is not %lld x %lld", (long long)tokens, (long long)w->cols);
+  if (tokens == 0 || w->rows == 0) return ZERO_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (w->cols == 0) return zero_fill(y, y_dtype, tokens, w->rows, ld_y, s);
+  if ((st = zero_mx4_quantize(x, dtype, tokens, w->cols, ld, ZERO_MX4_NEAREST, 0, xq, nullptr, stream)) != ZERO_OK)
+    return st;
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  return matmul(*xq, *w, y, y_dtype, ld_y, 1, sms, s);
+}
+
+zero_status zero_mx4_check(void* stream) {
+  unsigned flag = 0;
+  const cudaError_t e = zsm::mx_matmul_error(&flag, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "reading the MX4 product's error flag");
+  return flag ? fail(ZERO_ECUDA, "a bounded wait in the MX4 product kernel ran out: the product's result is invalid") : ZERO_OK;
+}
+
+}  // extern "C"

@@ -23,6 +23,7 @@
 #include "zero_sm.h"
 #include "guards.cuh"
 #include "kernels.cuh"
+#include "mx4.cuh"
 #include "two_pass_bulk.cuh"
 #include "plan.hpp"
 
@@ -86,6 +87,16 @@ class NvtxRange {
 };
 
 }  // namespace
+
+namespace zsm {
+void set_thread_error(const char* msg) {
+  try {
+    g_init_error = msg;
+  } catch (...) {  // out of host memory: no message
+    g_init_error.clear();
+  }
+}
+}  // namespace zsm
 
 struct zero_ctx {
   zsm::Plan plan;
@@ -1914,6 +1925,70 @@ zero_status zero_all_gather(zero_ctx* c, int64_t lo, int64_t hi, void* const* ra
     cudaError_t e = counted(c, zsm::launch_gather(g, grid_for(g.n_vec, c->grid_simple), s));
     if (e != cudaSuccess) return cuda_fail(c, e, "all-gather kernel launch");
   }
+  return ZERO_OK;
+}
+
+zero_status zero_mx4_all_gather(zero_ctx* c, int64_t lo, int64_t hi, void* const* rank_codes, void* const* rank_scales,
+                                void* stream) {
+  zero_status st = check_ready(c, false);
+  if (st != ZERO_OK) return st;
+  const NvtxRange range(c->nvtx, "MX4 all-gather [%lld, %lld)", (long long)lo, (long long)hi);
+  if ((st = check_interval(c, lo, hi)) != ZERO_OK) return st;
+  if (!rank_codes || !rank_scales) return fail(c, ZERO_EINVAL, "rank_codes or rank_scales is NULL");
+  const int N = c->plan.n_ranks;
+  zsm::MxGatherArgs a;
+  std::memset(&a, 0, sizeof a);
+  for (int r = 0; r < N; ++r) {
+    if (!rank_codes[r] || !aligned16(rank_codes[r]))
+      return fail(c, ZERO_EINVAL, "rank_codes[%d] is null or not 16-byte aligned", r);
+    if (!rank_scales[r]) return fail(c, ZERO_EINVAL, "rank_scales[%d] is null", r);
+    a.codes[r] = static_cast<uint8_t*>(rank_codes[r]);
+    a.scales[r] = static_cast<uint8_t*>(rank_scales[r]);
+    a.src[r] = param_ptr(c, r);
+  }
+  if (hi == lo) return ZERO_OK;
+  a.lo = lo;
+  a.n = hi - lo;
+  a.shard = c->plan.shard;
+  a.n_ranks = N;
+  a.uniform = c->stage == ZERO_STAGE_3 ? 1 : 0;
+  a.fmt = c->fmt;
+  const cudaError_t e = counted(c, zsm::launch_mx_gather(a, c->sm_count, static_cast<cudaStream_t>(stream)));
+  if (e != cudaSuccess) return cuda_fail(c, e, "MX4 all-gather kernel launch");
+  return ZERO_OK;
+}
+
+zero_status zero_mx4_reduce_scatter(zero_ctx* c, int64_t lo, int64_t hi, const void* const* rank_codes,
+                                    const void* const* rank_scales, void* stream) {
+  zero_status st = check_ready(c, false);
+  if (st != ZERO_OK) return st;
+  const NvtxRange range(c->nvtx, "MX4 reduce-scatter [%lld, %lld)", (long long)lo, (long long)hi);
+  if (c->stage == ZERO_STAGE_1) return fail(c, ZERO_EINVAL, "stage 1 keeps full gradients: it has no reduce-scatter");
+  if (!c->arena[ZERO_ARENA_GRAD_SHARDS])
+    return fail(c, ZERO_ESTATE, "gradient shards were dropped (ZERO_OPT_KEEP_GRAD_SHARDS = 0)");
+  if ((st = check_interval(c, lo, hi)) != ZERO_OK) return st;
+  if (!rank_codes || !rank_scales) return fail(c, ZERO_EINVAL, "rank_codes or rank_scales is NULL");
+  const int N = c->plan.n_ranks;
+  zsm::MxReduceArgs a;
+  std::memset(&a, 0, sizeof a);
+  for (int r = 0; r < N; ++r) {
+    if (!rank_codes[r] || !aligned16(rank_codes[r]))
+      return fail(c, ZERO_EINVAL, "rank_codes[%d] is null or not 16-byte aligned", r);
+    if (!rank_scales[r]) return fail(c, ZERO_EINVAL, "rank_scales[%d] is null", r);
+    a.codes[r] = static_cast<const uint8_t*>(rank_codes[r]);
+    a.scales[r] = static_cast<const uint8_t*>(rank_scales[r]);
+  }
+  if (hi == lo) return ZERO_OK;
+  a.shard_out = grad_shard_ptr(c) + lo;
+  a.n = hi - lo;
+  a.n_ranks = N;
+  a.accumulate = c->norm_fresh ? 0 : 1;
+  a.fmt = c->fmt;
+  a.inv_n = (float)(1.0 / (double)N);
+  a.ns = norm_scratch(c);
+  const cudaError_t e = counted(c, zsm::launch_mx_reduce(a, c->sm_count, static_cast<cudaStream_t>(stream)));
+  if (e != cudaSuccess) return cuda_fail(c, e, "MX4 reduce-scatter kernel launch");
+  c->norm_fresh = false;
   return ZERO_OK;
 }
 
