@@ -674,26 +674,40 @@ class ZeroOptimizer:
 
 
 # ------------------------------------------------------ MX4 matrices ----
+#
+# These calls run once per product of a small layer, so the wrapper keeps its
+# own time short: torch is looked up once, tensors' properties are read once.
+
+_DTYPE_CODES: dict = {}
+
+
+def _torch():
+    import torch
+
+    if not _DTYPE_CODES:
+        _DTYPE_CODES.update({torch.bfloat16: ZERO_DTYPE_BF16, torch.float16: ZERO_DTYPE_F16,
+                             torch.float32: ZERO_DTYPE_F32})
+    return torch
+
 
 class _on:
     """Makes ``device`` the current CUDA device for a call (free when it is)."""
+
+    __slots__ = ("_index", "_back")
 
     def __init__(self, device):
         self._index = device.index
 
     def __enter__(self):
-        import torch
-
-        now = torch.cuda.current_device()
+        cuda = _torch().cuda
+        now = cuda.current_device()
         self._back = now if self._index is not None and self._index != now else None
         if self._back is not None:
-            torch.cuda.set_device(self._index)
+            cuda.set_device(self._index)
 
     def __exit__(self, *exc):
         if self._back is not None:
-            import torch
-
-            torch.cuda.set_device(self._back)
+            _torch().cuda.set_device(self._back)
         return False
 
 
@@ -702,61 +716,78 @@ class MX4:
     include/zero_sm.h): uint8 CUDA tensors ``codes`` [rows, pitch] and
     ``scales`` [rows, pitch], each with contiguous rows."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "_c")
+    __slots__ = ("codes", "scales", "rows", "cols", "device", "_c")
 
     def __init__(self, codes, scales, rows: int, cols: int):
-        self.codes, self.scales, self.rows, self.cols = codes, scales, int(rows), int(cols)
-        nb = -(-self.cols // ZERO_MX4_BLOCK)
+        uint8 = _torch().uint8
+        nb = -(-cols // ZERO_MX4_BLOCK)
+        pitches = []
         for name, t, need in (("codes", codes, 16 * nb), ("scales", scales, nb)):
-            if str(t.dtype) != "torch.uint8" or t.dim() != 2 or t.shape[0] != self.rows or t.shape[1] < need or \
-                    (t.shape[1] > 1 and t.stride(1) != 1):
-                raise ValueError(f"{name}: a uint8 tensor of {self.rows} rows of at least {need} bytes is needed")
-        if codes.device != scales.device:
-            raise ValueError("codes and scales are on different devices")
-        pitch = [t.stride(0) if self.rows > 1 else t.shape[1] for t in (codes, scales)]
-        self._c = zero_mx4(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, pitch[0], pitch[1])
+            shape = t.shape
+            if t.dtype != uint8 or len(shape) != 2 or shape[0] != rows or shape[1] < need:
+                raise ValueError(f"{name}: a uint8 tensor of {rows} rows of at least {need} bytes is needed")
+            pitch, one = t.stride()
+            if one != 1 and shape[1] > 1:
+                raise ValueError(f"{name}: the rows must be contiguous (stride {one})")
+            pitches.append(pitch if rows > 1 else shape[1])
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self.device = codes.device
+        if not codes.is_cuda or scales.device != self.device:
+            raise ValueError("codes and scales must be on the same CUDA device")
+        self._c = zero_mx4(codes.data_ptr(), scales.data_ptr(), rows, cols, pitches[0], pitches[1])
 
-    @property
-    def device(self):
-        return self.codes.device
+
+def _mx4_bytes(rows: int, cols: int) -> tuple:
+    """(code pitch, scale pitch) that mx4_empty uses: scale rows padded to 16 bytes."""
+    nb = -(-cols // ZERO_MX4_BLOCK)
+    return 16 * nb, -(-nb // 16) * 16
 
 
 def mx4_empty(rows: int, cols: int, device=None) -> MX4:
-    """An MX4 matrix of uninitialised memory; its scale rows are padded to 4 bytes."""
-    import torch
-
-    nb = -(-int(cols) // ZERO_MX4_BLOCK)
+    """An MX4 matrix of uninitialised memory; its scale rows are padded to 16
+    bytes, the alignment that the product loads fastest."""
+    torch = _torch()
+    if rows < 0 or cols < 0:
+        raise ValueError(f"{rows} x {cols}")
+    cp, sp = _mx4_bytes(rows, cols)
     device = device or torch.device("cuda", torch.cuda.current_device())
-    return MX4(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
-               torch.empty(rows, -(-nb // 4) * 4, dtype=torch.uint8, device=device), rows, cols)
-
-
-def _dtype_code(dtype) -> int:
-    name = str(dtype)
-    if name == "torch.bfloat16":
-        return ZERO_DTYPE_BF16
-    if name == "torch.float16":
-        return ZERO_DTYPE_F16
-    if name == "torch.float32":
-        return ZERO_DTYPE_F32
-    raise ValueError(f"{name}: matrices are bfloat16, float16 or float32")
+    whole = torch.empty(rows * (cp + sp), dtype=torch.uint8, device=device)
+    return MX4(whole[:rows * cp].view(rows, cp), whole[rows * cp:].view(rows, sp), rows, cols)
 
 
 def _dense(t, name: str):
-    """(pointer, dtype code, elements between rows) of a matrix with contiguous rows."""
-    if t.dim() != 2 or not t.is_cuda:
+    """(pointer, dtype code, elements between rows, rows, cols) of a CUDA matrix with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA matrix is needed")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the rows must be contiguous (stride {t.stride(1)})")
-    return t.data_ptr(), _dtype_code(t.dtype), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        _torch()
+        code = _DTYPE_CODES.get(t.dtype)
+        if code is None:
+            raise ValueError(f"{name} is {t.dtype}: bfloat16, float16 or float32 is needed")
+    ld, one = t.stride()
+    rows, cols = shape
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}: the rows must be contiguous (stride {one})")
+    return t.data_ptr(), code, ld if rows > 1 else cols, rows, cols
 
 
-def _mx4_stream(device, stream) -> int:
-    import torch
-
+def _stream_of(device, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _torch().cuda.current_stream(device).cuda_stream
     return int(getattr(stream, "cuda_stream", stream))
+
+
+def _lend(stream, *tensors):
+    """Keeps memory that this call allocated from being reused before the work
+    given to another stream than the current one has run."""
+    if stream is None:
+        return
+    torch = _torch()
+    for t in tensors:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=t.device)
+        t.record_stream(s)
 
 
 def _mx4_check(st: int, where: str):
@@ -764,21 +795,27 @@ def _mx4_check(st: int, where: str):
         raise ZeroError(st, where, zero_last_error(None).decode())
 
 
-def _same_device(*named):
-    first, device = named[0][0], named[0][1].device
-    for name, t in named[1:]:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, {first} on {device}")
-    return device
+def _same_device(device, **others):
+    for name, t in others.items():
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not {device}")
 
 
-def _result(out, rows: int, cols: int, dtype, device, name: str = "out"):
-    import torch
-
+def _result(out, rows: int, cols: int, dtype, device, stream, name: str = "out"):
     if out is None:
-        return torch.empty(rows, cols, dtype=dtype, device=device)
-    if tuple(out.shape) != (rows, cols):
+        out = _torch().empty((rows, cols), dtype=dtype, device=device)
+        _lend(stream, out)
+    elif tuple(out.shape) != (rows, cols):
         raise ValueError(f"{name} is {tuple(out.shape)}, not {(rows, cols)}")
+    return out
+
+
+def _mx4_result(out, rows: int, cols: int, device, stream, name: str = "out"):
+    if out is None:
+        out = mx4_empty(rows, cols, device)
+        _lend(stream, out.codes)
+    elif (out.rows, out.cols) != (rows, cols):
+        raise ValueError(f"{name} is {(out.rows, out.cols)}, not {(rows, cols)}")
     return out
 
 
@@ -786,88 +823,100 @@ def _rounding(seed):
     return (ZERO_MX4_NEAREST, 0) if seed is None else (ZERO_MX4_STOCHASTIC, int(seed) & 0xFFFFFFFFFFFFFFFF)
 
 
+def _quantize(x, seed, out, out_t, stream):
+    ptr, code, ld, rows, cols = _dense(x, "x")
+    rounding, seed = _rounding(seed)
+    device = x.device
+    for o in (out, out_t):
+        if o is not None:
+            _same_device(device, out=o)
+    with _on(device):
+        _mx4_check(zero_mx4_quantize(ptr, code, rows, cols, ld, rounding, seed, out and ctypes.byref(out._c),
+                                     out_t and ctypes.byref(out_t._c), _stream_of(device, stream)),
+                   "zero_mx4_quantize")
+
+
 def mx4_quantize(x, transpose: bool = False, seed: Optional[int] = None, out: Optional[MX4] = None, stream=None) -> MX4:
     """Quantise a matrix in blocks along its rows or, with ``transpose``, its
     transpose (blocks down x's columns).  ``seed`` rounds stochastically;
     None rounds to nearest even (zero_mx4_quantize)."""
-    ptr, code, ld = _dense(x, "x")
     rows, cols = x.shape
-    if out is None:
-        out = mx4_empty(cols, rows, x.device) if transpose else mx4_empty(rows, cols, x.device)
-    device = _same_device(("x", x), ("out", out))
-    rounding, seed = _rounding(seed)
-    c = ctypes.byref(out._c)
-    with _on(device):
-        _mx4_check(zero_mx4_quantize(ptr, code, rows, cols, ld, rounding, seed, None if transpose else c,
-                                     c if transpose else None, _mx4_stream(device, stream)), "zero_mx4_quantize")
+    if transpose:
+        out = _mx4_result(out, cols, rows, x.device, stream)
+        _quantize(x, seed, None, out, stream)
+    else:
+        out = _mx4_result(out, rows, cols, x.device, stream)
+        _quantize(x, seed, out, None, stream)
     return out
 
 
 def mx4_quantize_both(x, seed: Optional[int] = None, out: Optional[MX4] = None, out_t: Optional[MX4] = None, stream=None):
     """(x, its transpose) as MX4 matrices, reading x once."""
-    ptr, code, ld = _dense(x, "x")
     rows, cols = x.shape
-    out = mx4_empty(rows, cols, x.device) if out is None else out
-    out_t = mx4_empty(cols, rows, x.device) if out_t is None else out_t
-    device = _same_device(("x", x), ("out", out), ("out_t", out_t))
-    rounding, seed = _rounding(seed)
-    with _on(device):
-        _mx4_check(zero_mx4_quantize(ptr, code, rows, cols, ld, rounding, seed, ctypes.byref(out._c),
-                                     ctypes.byref(out_t._c), _mx4_stream(device, stream)), "zero_mx4_quantize")
+    out = _mx4_result(out, rows, cols, x.device, stream)
+    out_t = _mx4_result(out_t, cols, rows, x.device, stream, "out_t")
+    _quantize(x, seed, out, out_t, stream)
     return out, out_t
 
 
 def mx4_transpose(m: MX4, seed: Optional[int] = None, out: Optional[MX4] = None, stream=None) -> MX4:
     """The transpose of an MX4 matrix, quantised in blocks along the other axis."""
-    out = mx4_empty(m.cols, m.rows, m.device) if out is None else out
-    device = _same_device(("m", m), ("out", out))
+    device = m.device
+    out = _mx4_result(out, m.cols, m.rows, device, stream)
+    _same_device(device, out=out)
     rounding, seed = _rounding(seed)
     with _on(device):
         _mx4_check(zero_mx4_transpose(ctypes.byref(m._c), rounding, seed, ctypes.byref(out._c),
-                                      _mx4_stream(device, stream)), "zero_mx4_transpose")
+                                      _stream_of(device, stream)), "zero_mx4_transpose")
     return out
 
 
 def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
     """The values of an MX4 matrix (bfloat16 unless ``dtype`` or ``out`` says otherwise)."""
-    import torch
-
-    out = _result(out, m.rows, m.cols, dtype or torch.bfloat16, m.device)
-    ptr, code, ld = _dense(out, "out")
-    device = _same_device(("m", m), ("out", out))
+    device = m.device
+    out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, stream)
+    ptr, code, ld, _, _ = _dense(out, "out")
+    _same_device(device, out=out)
     with _on(device):
-        _mx4_check(zero_mx4_dequantize(ctypes.byref(m._c), ptr, code, ld, _mx4_stream(device, stream)),
+        _mx4_check(zero_mx4_dequantize(ctypes.byref(m._c), ptr, code, ld, _stream_of(device, stream)),
                    "zero_mx4_dequantize")
     return out
 
 
 def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
     """a b^T of two MX4 matrices with the same number of columns."""
-    import torch
-
-    out = _result(out, a.rows, b.rows, dtype or torch.bfloat16, a.device)
-    ptr, code, ld = _dense(out, "out")
-    device = _same_device(("a", a), ("b", b), ("out", out))
+    device = a.device
+    out = _result(out, a.rows, b.rows, dtype or _torch().bfloat16, device, stream)
+    ptr, code, ld, _, _ = _dense(out, "out")
+    _same_device(device, b=b, out=out)
     with _on(device):
         _mx4_check(zero_mx4_matmul(ctypes.byref(a._c), ctypes.byref(b._c), ptr, code, ld,
-                                   _mx4_stream(device, stream)), "zero_mx4_matmul")
+                                   _stream_of(device, stream)), "zero_mx4_matmul")
     return out
 
 
 def mx4_linear(x, w: MX4, out=None, xq: Optional[MX4] = None, stream=None):
     """y = Q(x) w^T for x [tokens, inputs] and an MX4 weight [outputs, inputs];
     y has x's type unless ``out`` is given.  ``xq`` receives the quantised x."""
-    ptr, code, ld = _dense(x, "x")
-    tokens = x.shape[0]
-    if x.shape[1] != w.cols:
-        raise ValueError(f"x has {x.shape[1]} inputs, w {w.cols}")
-    xq = mx4_empty(tokens, w.cols, x.device) if xq is None else xq
-    y = _result(out, tokens, w.rows, x.dtype, x.device)
-    yptr, ycode, ldy = _dense(y, "out")
-    device = _same_device(("x", x), ("w", w), ("xq", xq), ("out", y))
+    ptr, code, ld, tokens, inputs = _dense(x, "x")
+    device = x.device
+    if inputs != w.cols:
+        raise ValueError(f"x has {inputs} inputs, w {w.cols}")
+    y = _result(out, tokens, w.rows, x.dtype, device, stream)
+    yptr, ycode, ldy, _, _ = _dense(y, "out")
+    _same_device(device, w=w, out=y)
+    if xq is None:
+        cp, sp = _mx4_bytes(tokens, inputs)
+        space = _torch().empty(tokens * (cp + sp), dtype=_torch().uint8, device=device)
+        _lend(stream, space)
+        at = space.data_ptr()
+        q = zero_mx4(at, at + tokens * cp, tokens, inputs, cp, sp)
+    else:
+        _same_device(device, xq=xq)
+        q = xq._c
     with _on(device):
-        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, ctypes.byref(w._c), ctypes.byref(xq._c), yptr, ycode, ldy,
-                                   _mx4_stream(device, stream)), "zero_mx4_linear")
+        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, ctypes.byref(w._c), ctypes.byref(q), yptr, ycode, ldy,
+                                   _stream_of(device, stream)), "zero_mx4_linear")
     return y
 
 
@@ -877,9 +926,9 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
     stochastically when ``seed`` is given); the roundings' own gradients are
     taken as one.  dx has x's type and dw dy's unless given (dw may be a view
     of a rank's gradient buffer)."""
-    if x.dim() != 2 or dy.dim() != 2 or x.shape[1] != w.cols or dy.shape != (x.shape[0], w.rows):
+    if x.dim() != 2 or dy.dim() != 2 or x.shape[1] != w.cols or tuple(dy.shape) != (x.shape[0], w.rows):
         raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} do not fit w {(w.rows, w.cols)}")
-    _same_device(("dy", dy), ("x", x), ("w", w))
+    _same_device(x.device, dy=dy, w=w)
     dyq, dyq_t = mx4_quantize_both(dy, seed, stream=stream)
     xq_t = mx4_quantize(x, transpose=True, stream=stream)
     wq_t = mx4_transpose(w, stream=stream)
@@ -890,11 +939,10 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
 
 def mx4_check(device=None, stream=None):
     """Wait for the stream; raise ZeroError if a bounded wait of a product kernel ran out."""
-    import torch
-
+    torch = _torch()
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with _on(device):
-        _mx4_check(zero_mx4_check(_mx4_stream(device, stream)), "zero_mx4_check")
+        _mx4_check(zero_mx4_check(_stream_of(device, stream)), "zero_mx4_check")
 
 
 # ------------------------------------------------ one logical rank per GPU ----

@@ -12,8 +12,8 @@
 // memory into TMEM and issues the products; 4-7 read the accumulator and
 // store; 8-11 load scales.  The scales lie in memory one row after another,
 // and the tensor core wants, for each 128 rows and 128 k elements, a 512-byte
-// piece with row r's four bytes at 16 (r % 32) + 4 (r / 32): four-byte
-// asynchronous copies put them there.
+// piece with row r's four bytes at 16 (r % 32) + 4 (r / 32): a thread loads
+// 16 bytes of a row into registers and stores four words at their places.
 //
 // Few tiles and a long k: a cluster of up to 8 CTAs splits k, each CTA sends
 // the columns another one owns into that one's shared memory, and the owner
@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "device_math.cuh"
 #include "mx4.cuh"
@@ -50,7 +51,7 @@ struct MmArgs {
   const uint8_t* q_scales;
   int64_t p_scale_pitch, q_scale_pitch;
   int p_rows, q_rows, k_blocks, k_tiles;
-  int p_words, q_words;  // 1: that operand's scale rows are 4-byte aligned
+  int p_align, q_align;  // 16, 8, 4 or 1: alignment of that operand's scale rows
   int p_tiles, n_tiles, split;
   void* out;
   int64_t p_stride, q_stride;  // elements between rows of P / of Q in the result
@@ -218,27 +219,33 @@ __device__ __forceinline__ void store_run(const MmArgs& a, int64_t p, int64_t q,
 
 // ------------------------------------------------------------ scale loader --
 
-// The 8 scale bytes of row `row` for k tile kt, as two words put at their
-// places in the pieces c = 0, 1 (piece bytes apart); zero past the matrix.
-__device__ __forceinline__ void load_scales(const uint8_t* scales, int64_t pitch, int rows, int k_blocks, int words,
-                                            int row, int kt, uint32_t dst, uint32_t piece) {
-  const int left = row < rows ? k_blocks - 8 * kt : 0;
-  const uint8_t* src = scales + (left > 0 ? (int64_t)row * pitch + 8 * kt : 0);
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int n = min(max(left - 4 * c, 0), 4);
-    if (words) {
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + c * piece), "l"(src + (n > 0 ? 4 * c : 0)),
-                   "r"(n)
-                   : "memory");
-    } else {
-      uint32_t w = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) w |= (uint32_t)src[4 * c + j] << (8 * j);
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + c * piece), "r"(w) : "memory");
-    }
+// 16 scale bytes (two k tiles) of one row, of which the first n exist (the
+// others are 0), by loads as wide as the rows' alignment allows.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, int align) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (n >= 16 && align == 16) return *reinterpret_cast<const uint4*>(p);
+  if (n >= 16 && align == 8) {
+    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + 8);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
+  if (align >= 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n >= 4 * j + 4) w[j] = *reinterpret_cast<const uint32_t*>(p + 4 * j);
+      else
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (n > 4 * j + i) w[j] |= (uint32_t)p[4 * j + i] << (8 * i);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (n > j) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void st_word(uint32_t addr, uint32_t w) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -350,40 +357,49 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
       }
     }
   } else if (warp >= 8) {
+    // Thread t holds row t of P and rows t (and t + 128) of Q, two k tiles at
+    // a time, the next two loaded before the present ones are stored.
     const int t = threadIdx.x - 256;  // 0..127
-    constexpr int kLag = STAGES - 1 < 4 ? STAGES - 1 : 4;
     const uint32_t at = 16u * (t & 31) + 4u * (t >> 5);
+    uint4 cur[1 + kQ], nxt[1 + kQ];
+    auto fetch = [&](int tile, int kt, uint4 (&r)[1 + kQ]) {
+      const int left = a.k_blocks - 8 * kt, most = kt & 1 ? 8 : 16;
+      const int64_t p = (int64_t)(tile % a.p_tiles) * kLanes + t, q = (int64_t)(tile / a.p_tiles) * BN + t;
+      r[0] = load_scales(a.p_scales + p * a.p_scale_pitch + 8 * kt, p < a.p_rows ? left : 0, min(a.p_align, most));
+#pragma unroll
+      for (int j = 0; j < kQ; ++j)
+        r[1 + j] = load_scales(a.q_scales + (q + 128 * j) * a.q_scale_pitch + 8 * kt,
+                               q + 128 * j < a.q_rows && t + 128 * j < BN ? left : 0,
+                               min(a.q_align, most));
+    };
     int it = 0;
     bool ok = true;
+    if (first < a.n_tiles && k0 < k1) fetch(first, k0, nxt);
     for (int tile = first; tile < a.n_tiles && ok; tile += step) {
-      const int p0 = (tile % a.p_tiles) * kLanes, q0 = (tile / a.p_tiles) * BN;
-      for (int kt = k0; kt < k1; ++kt, ++it) {
-        const int s = it % STAGES;
-        if (it >= STAGES &&
-            !(ok = __all_sync(0xFFFFFFFFu, wait(&sh.empty[s], ((it / STAGES) - 1) & 1))))
-          break;  // the whole warp
-        const uint32_t scales = smem_u32(smem + s * kStage) + stage_codes(BN);
-        load_scales(a.p_scales, a.p_scale_pitch, a.p_rows, a.k_blocks, a.p_words, p0 + t, kt, scales + at, 512);
+      for (int kt = k0; kt < k1 && ok; kt += 2) {
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-          const int row = 128 * q + t;
-          load_scales(a.q_scales, a.q_scale_pitch, row < BN ? a.q_rows : 0, a.k_blocks, a.q_words, q0 + row, kt,
-                      scales + 1024 + 512 * q + at, 512 * kQ);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (it >= kLag) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+        for (int j = 0; j < 1 + kQ; ++j) cur[j] = nxt[j];
+        if (kt + 2 < k1) fetch(tile, kt + 2, nxt);
+        else if (tile + step < a.n_tiles) fetch(tile + step, k0, nxt);
+        for (int h = 0; h < 2 && kt + h < k1; ++h, ++it) {
+          const int s = it % STAGES;
+          if (it >= STAGES &&
+              !(ok = __all_sync(0xFFFFFFFFu, wait(&sh.empty[s], ((it / STAGES) - 1) & 1))))
+            break;  // the whole warp
+          const uint32_t dst = smem_u32(smem + s * kStage) + stage_codes(BN) + at;
+          st_word(dst, h ? cur[0].z : cur[0].x);
+          st_word(dst + 512, h ? cur[0].w : cur[0].y);
+#pragma unroll
+          for (int j = 0; j < kQ; ++j) {
+            st_word(dst + 1024 + 512 * j, h ? cur[1 + j].z : cur[1 + j].x);
+            st_word(dst + 1024 + 512 * (kQ + j), h ? cur[1 + j].w : cur[1 + j].y);
+          }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.scales_full[(it - kLag) % STAGES]);
+          if (lane == 0) mbar_arrive(&sh.scales_full[s]);
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0)
-      for (int j = it > kLag ? it - kLag : 0; j < it; ++j) mbar_arrive(&sh.scales_full[j % STAGES]);
   } else if (warp >= 4 && a.split == 1) {
     const int w = warp - 4;
     int n = 0;
@@ -485,8 +501,17 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, int sm_count,
   static_assert(kSmem <= 227 * 1024 - 1024, "stages fit shared memory");
   static_assert(STAGES * stage_bytes(BN) >= (BN + 8) * kLanes * 4 || BN > 128, "the split's parts fit the stages");
   auto kernel = mx_matmul_kernel<BN, STAGES>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  // the large dynamic shared memory is opted into once per device
+  static std::atomic<uint64_t> opted{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!bit || !(opted.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    opted.fetch_or(bit, std::memory_order_release);
+  }
   a.p_tiles = (a.p_rows + kLanes - 1) / kLanes;
   const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + BN - 1) / BN);
   if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
@@ -520,7 +545,10 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, int sm_count,
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
-  const bool swap = m.a.rows <= 128;
+  // Plain orientation, 128 x 256 tiles, when they give every SM one; below
+  // that the swapped one (a's rows are the columns of the tile), where the
+  // parts of a split k end in stores that run along the result's rows.
+  const bool swap = ((m.a.rows + kLanes - 1) / kLanes) * ((m.b.rows + 255) / 256) < sm_count;
   const MxMatrix& p = swap ? m.b : m.a;
   const MxMatrix& q = swap ? m.a : m.b;
   MmArgs a = {};
@@ -529,34 +557,37 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   a.p_rows = (int)p.rows, a.q_rows = (int)q.rows;
   a.k_blocks = (int)mx_blocks(p.cols);
   a.k_tiles = (a.k_blocks + 7) / 8;
-  auto words = [](const MxMatrix& x) {
-    return ((reinterpret_cast<uintptr_t>(x.scales) | (uintptr_t)x.scale_pitch) & 3u) == 0 ? 1 : 0;
+  auto align = [](const MxMatrix& x) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(x.scales) | (uintptr_t)x.scale_pitch;
+    return bits & 3u ? 1 : bits & 7u ? 4 : bits & 15u ? 8 : 16;
   };
-  a.p_words = words(p), a.q_words = words(q);
+  a.p_align = align(p), a.q_align = align(q);
   a.out = m.out, a.type = m.type, a.pdl = m.pdl;
   a.p_stride = swap ? 1 : m.ld, a.q_stride = swap ? m.ld : 1;
   const int64_t row_bytes = m.ld * (m.type == kMxF32 ? 4 : 2);
   a.vec = !swap && ((reinterpret_cast<uintptr_t>(m.out) | (uintptr_t)row_bytes) & 31u) == 0;
   a.split = 1;
+  if (!swap) return launch<256, 4>(p, q, a, sm_count, s);
   const int64_t p_tiles = (p.rows + kLanes - 1) / kLanes;
   auto split_for = [&](int bn, int slots) {
     const int64_t tiles = p_tiles * ((q.rows + bn - 1) / bn);
-    int64_t n = std::min<int64_t>(std::min<int64_t>(8, a.k_tiles / 2), slots / std::max<int64_t>(1, tiles));
+    const int64_t n = std::min<int64_t>(std::min<int64_t>(8, a.k_tiles), slots / tiles);
     a.split = (int)std::max<int64_t>(1, n);
   };
   if (q.rows <= 16) {
     split_for(16, 2 * sm_count);
     return launch<16, 5>(p, q, a, sm_count, s);
   }
-  if (q.rows <= 32) {
+  if (p_tiles * ((q.rows + 31) / 32) <= sm_count) {
     split_for(32, 2 * sm_count);
     return launch<32, 4>(p, q, a, sm_count, s);
   }
-  if (p_tiles * ((q.rows + 255) / 256) < sm_count) {
-    split_for(128, sm_count);
-    return launch<128, 5>(p, q, a, sm_count, s);
+  if (p_tiles * ((q.rows + 63) / 64) <= sm_count) {
+    split_for(64, 2 * sm_count);
+    return launch<64, 4>(p, q, a, sm_count, s);
   }
-  return launch<256, 4>(p, q, a, sm_count, s);
+  split_for(128, sm_count);
+  return launch<128, 5>(p, q, a, sm_count, s);
 }
 
 // The flag of a bounded wait that ran out (current device), cleared as it is read (waits for `s`).
