@@ -844,21 +844,32 @@ zero_status zero_mx4_transpose(const zero_mx4* in, int32_t rounding, uint64_t se
  * ld elements between rows.  No passage of the pages defines it. */
 zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, int64_t ld, void* stream);
 
+/* Bytes of workspace that zero_mx4_matmul needs for an m x n result over k
+ * columns on the current device (0 for small results). */
+zero_status zero_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t* bytes);
+
 /* out[i][j] = sum over k of a[i][k] b[j][k] (a->rows x b->rows of `dtype`, ld
  * elements between rows), for two MX4 matrices of the same number of columns,
  * on the block-scaled tensor cores: the elements' products are exact and
  * their sum is held in binary32, rounded once to `dtype`.  The same bits on
- * every run.  No passage of the pages defines it (the layer's use, [T]
- * section "ZeRO-3", parts "1. 前向" and "2. 反向"). */
-zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int32_t dtype, int64_t ld, void* stream);
+ * every run.  workspace: device memory, 16-byte aligned, the call's own until
+ * its work on `stream` has run (two calls that may run at once need two).  No
+ * passage of the pages defines it (the layer's use, [T] section "ZeRO-3",
+ * parts "1. 前向" and "2. 反向"). */
+zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int32_t dtype, int64_t ld, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that zero_mx4_linear needs on the current device. */
+zero_status zero_mx4_linear_workspace(int64_t tokens, int64_t outputs, int64_t inputs, int64_t* bytes);
 
 /* The forward product of a linear layer whose weight w (outputs x inputs) is
  * an MX4 matrix, for one token or many: y = Q(x) w^T, x (tokens x inputs of
- * `dtype`) quantised along its rows into the caller's xq (tokens x inputs),
- * y tokens x outputs of `y_dtype`.  The same as zero_mx4_quantize and
- * zero_mx4_matmul.  [T] section "ZeRO-3", part "1. 前向". */
-zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t ld, const zero_mx4* w,
-                            const zero_mx4* xq, void* y, int32_t y_dtype, int64_t ld_y, void* stream);
+ * `dtype`) quantised along its rows to nearest even in the workspace,
+ * y tokens x outputs of `y_dtype`.  The same values as zero_mx4_quantize and
+ * zero_mx4_matmul give.  workspace as for zero_mx4_matmul.  [T] section
+ * "ZeRO-3", part "1. 前向". */
+zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t ld, const zero_mx4* w, void* y,
+                            int32_t y_dtype, int64_t ld_y, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Wait for `stream` and report whether a bounded wait inside a product kernel
  * on the current device ran out since the last call: ZERO_ECUDA (that

@@ -162,7 +162,7 @@ def _assert_product(got, a, b, what):
 
 PRODUCTS = [(1, 1, 1), (1, 128, 32), (1, 130, 33), (2, 100, 64), (8, 256, 256), (9, 257, 300), (17, 1000, 771),
             (32, 128, 512), (33, 129, 257), (64, 640, 2048), (100, 200, 4100), (128, 128, 128), (129, 300, 96),
-            (256, 256, 1024), (300, 1000, 771), (1000, 333, 100), (513, 768, 2304), (1, 4096, 4096), (2048, 2304, 768),
+            (256, 256, 1024), (300, 1000, 771), (1000, 333, 100), (2048, 2047, 100), (1999, 1800, 300), (513, 768, 2304), (1, 4096, 4096), (2048, 2304, 768),
             (2500, 2700, 544)]
 
 

@@ -136,8 +136,10 @@ _SIGS = {
     "zero_mx4_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, ctypes.c_uint64, _MX4, _MX4, _vp]),
     "zero_mx4_transpose": (_i32, [_MX4, _i32, ctypes.c_uint64, _MX4, _vp]),
     "zero_mx4_dequantize": (_i32, [_MX4, _vp, _i32, _i64, _vp]),
-    "zero_mx4_matmul": (_i32, [_MX4, _MX4, _vp, _i32, _i64, _vp]),
-    "zero_mx4_linear": (_i32, [_vp, _i32, _i64, _i64, _MX4, _MX4, _vp, _i32, _i64, _vp]),
+    "zero_mx4_matmul_workspace": (_i32, [_i64, _i64, _i64, ctypes.POINTER(_i64)]),
+    "zero_mx4_matmul": (_i32, [_MX4, _MX4, _vp, _i32, _i64, _vp, _i64, _vp]),
+    "zero_mx4_linear_workspace": (_i32, [_i64, _i64, _i64, ctypes.POINTER(_i64)]),
+    "zero_mx4_linear": (_i32, [_vp, _i32, _i64, _i64, _MX4, _vp, _i32, _i64, _vp, _i64, _vp]),
     "zero_mx4_check": (_i32, [_vp]),
     "zero_mx4_all_gather": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
     "zero_mx4_reduce_scatter": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
@@ -883,6 +885,17 @@ def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
     return out
 
 
+def _workspace(query, m: int, n: int, k: int, device, stream):
+    """(pointer, bytes, tensor) of the workspace that the query asks for."""
+    need = ctypes.c_int64()
+    _mx4_check(query(m, n, k, ctypes.byref(need)), "workspace size")
+    if need.value == 0:
+        return None, 0, None
+    space = _torch().empty(need.value, dtype=_torch().uint8, device=device)
+    _lend(stream, space)
+    return space.data_ptr(), need.value, space
+
+
 def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
     """a b^T of two MX4 matrices with the same number of columns."""
     device = a.device
@@ -890,14 +903,15 @@ def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
     ptr, code, ld, _, _ = _dense(out, "out")
     _same_device(device, b=b, out=out)
     with _on(device):
-        _mx4_check(zero_mx4_matmul(ctypes.byref(a._c), ctypes.byref(b._c), ptr, code, ld,
+        at, size, space = _workspace(zero_mx4_matmul_workspace, a.rows, b.rows, a.cols, device, stream)
+        _mx4_check(zero_mx4_matmul(ctypes.byref(a._c), ctypes.byref(b._c), ptr, code, ld, at, size,
                                    _stream_of(device, stream)), "zero_mx4_matmul")
     return out
 
 
-def mx4_linear(x, w: MX4, out=None, xq: Optional[MX4] = None, stream=None):
+def mx4_linear(x, w: MX4, out=None, stream=None):
     """y = Q(x) w^T for x [tokens, inputs] and an MX4 weight [outputs, inputs];
-    y has x's type unless ``out`` is given.  ``xq`` receives the quantised x."""
+    y has x's type unless ``out`` is given."""
     ptr, code, ld, tokens, inputs = _dense(x, "x")
     device = x.device
     if inputs != w.cols:
@@ -905,17 +919,9 @@ def mx4_linear(x, w: MX4, out=None, xq: Optional[MX4] = None, stream=None):
     y = _result(out, tokens, w.rows, x.dtype, device, stream)
     yptr, ycode, ldy, _, _ = _dense(y, "out")
     _same_device(device, w=w, out=y)
-    if xq is None:
-        cp, sp = _mx4_bytes(tokens, inputs)
-        space = _torch().empty(tokens * (cp + sp), dtype=_torch().uint8, device=device)
-        _lend(stream, space)
-        at = space.data_ptr()
-        q = zero_mx4(at, at + tokens * cp, tokens, inputs, cp, sp)
-    else:
-        _same_device(device, xq=xq)
-        q = xq._c
     with _on(device):
-        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, ctypes.byref(w._c), ctypes.byref(q), yptr, ycode, ldy,
+        at, size, space = _workspace(zero_mx4_linear_workspace, tokens, w.rows, inputs, device, stream)
+        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, ctypes.byref(w._c), yptr, ycode, ldy, at, size,
                                    _stream_of(device, stream)), "zero_mx4_linear")
     return y
 

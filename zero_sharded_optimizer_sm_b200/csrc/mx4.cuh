@@ -94,6 +94,7 @@ struct MxMatmulArgs {
   void* out;
   int type;
   int64_t ld;
+  void* workspace;  // mx_matmul_workspace bytes, 16-byte aligned
   int pdl;  // 1: programmatic launch; the kernel waits for the grid before it before it reads `a`
 };
 
@@ -102,6 +103,7 @@ cudaError_t launch_mx_dequantize(const MxDequantArgs& a, int sm_count, cudaStrea
 cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int sm_count, cudaStream_t s);
+int64_t mx_matmul_workspace(int64_t m, int64_t n, int64_t k, int sm_count);
 cudaError_t mx_matmul_error(unsigned* flag, cudaStream_t s);
 
 // The message zero_last_error(NULL) returns to the calling thread.

@@ -93,14 +93,24 @@ zero_status check_rounding(int32_t rounding) {
   return ZERO_OK;
 }
 
-zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtype, int64_t ld, int pdl, int sms,
-                   cudaStream_t s) {
+zero_status check_workspace(const void* workspace, int64_t have, int64_t need) {
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || have < need))
+    return fail(ZERO_EINVAL, "the workspace must be 16-byte aligned and of at least %lld bytes (%lld given)",
+                (long long)need, (long long)have);
+  return ZERO_OK;
+}
+
+int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
+
+zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtype, int64_t ld, void* workspace, int pdl,
+                   int sms, cudaStream_t s) {
   zsm::MxMatmulArgs m = {};
   m.a = matrix(a);
   m.b = matrix(b);
   m.out = out;
   m.type = dtype;
-  m.ld = b.rows == 1 ? std::max<int64_t>(ld, 1) : ld;
+  m.ld = a.rows == 1 ? std::max<int64_t>(ld, b.rows) : ld;
+  m.workspace = workspace;
   m.pdl = pdl;
   const cudaError_t e = zsm::launch_mx_matmul(m, sms, s);
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 product launch");
@@ -179,7 +189,20 @@ zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, in
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 read-back launch");
 }
 
-zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int32_t dtype, int64_t ld, void* stream) {
+zero_status zero_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t* bytes) {
+  if (!bytes) return fail(ZERO_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  if (m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim)
+    return fail(ZERO_EINVAL, "%lld x %lld x %lld is out of range", (long long)m, (long long)n, (long long)k);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  *bytes = m && n && k ? zsm::mx_matmul_workspace(m, n, k, sms) : 0;
+  return ZERO_OK;
+}
+
+zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int32_t dtype, int64_t ld, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
   zero_status st = check_mx4("a", a);
   if (st != ZERO_OK) return st;
   if ((st = check_mx4("b", b)) != ZERO_OK) return st;
@@ -192,27 +215,42 @@ zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  return matmul(*a, *b, out, dtype, ld, 0, sms, s);
+  const int64_t need = zsm::mx_matmul_workspace(a->rows, b->rows, a->cols, sms);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return st;
+  return matmul(*a, *b, out, dtype, ld, workspace, 0, sms, s);
 }
 
-zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t ld, const zero_mx4* w, const zero_mx4* xq,
-                            void* y, int32_t y_dtype, int64_t ld_y, void* stream) {
+zero_status zero_mx4_linear_workspace(int64_t tokens, int64_t outputs, int64_t inputs, int64_t* bytes) {
+  const zero_status st = zero_mx4_matmul_workspace(tokens, outputs, inputs, bytes);
+  if (st != ZERO_OK) return st;
+  const int64_t nb = zsm::mx_blocks(inputs);
+  *bytes += tokens * (16 * nb + align16(nb));
+  return ZERO_OK;
+}
+
+zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t ld, const zero_mx4* w, void* y,
+                            int32_t y_dtype, int64_t ld_y, void* workspace, int64_t workspace_bytes, void* stream) {
   zero_status st = check_mx4("w", w);
   if (st != ZERO_OK) return st;
-  if ((st = check_mx4("xq", xq)) != ZERO_OK) return st;
   if ((st = check_dense("x", x, dtype, tokens, w->cols, ld)) != ZERO_OK) return st;
   if ((st = check_dense("y", y, y_dtype, tokens, w->rows, ld_y)) != ZERO_OK) return st;
-  if (xq->rows != tokens || xq->cols != w->cols)
-    return fail(ZERO_EINVAL, "xq is not %lld x %lld", (long long)tokens, (long long)w->cols);
   if (tokens == 0 || w->rows == 0) return ZERO_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (w->cols == 0) return zero_fill(y, y_dtype, tokens, w->rows, ld_y, s);
-  if ((st = zero_mx4_quantize(x, dtype, tokens, w->cols, ld, ZERO_MX4_NEAREST, 0, xq, nullptr, stream)) != ZERO_OK)
-    return st;
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  return matmul(*xq, *w, y, y_dtype, ld_y, 1, sms, s);
+  const int64_t nb = zsm::mx_blocks(w->cols);
+  const int64_t own = tokens * (16 * nb + align16(nb));
+  if ((st = check_workspace(workspace, workspace_bytes, own + zsm::mx_matmul_workspace(tokens, w->rows, w->cols, sms))) !=
+      ZERO_OK)
+    return st;
+  // the workspace: x's codes, its scales, the product's own part
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  const zero_mx4 xq = {at, at + tokens * 16 * nb, tokens, w->cols, 16 * nb, align16(nb)};
+  st = zero_mx4_quantize(x, dtype, tokens, w->cols, ld, ZERO_MX4_NEAREST, 0, &xq, nullptr, stream);
+  if (st != ZERO_OK) return st;
+  return matmul(xq, *w, y, y_dtype, ld_y, at + own, 1, sms, s);
 }
 
 zero_status zero_mx4_check(void* stream) {

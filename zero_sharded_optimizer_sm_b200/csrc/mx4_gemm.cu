@@ -111,8 +111,9 @@ __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
 // Instruction descriptor: both operands 4-bit (format 1), scales a power of
 // two (bit 23), N / 8 at bit 17, M / 128 at bit 27, and which two of the four
 // scale bytes of a TMEM column the 64 elements use (0 or 2) at bits 4 and 29.
-__host__ __device__ constexpr uint32_t inst_desc(int n, uint32_t id) {
-  return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 29);
+__host__ __device__ constexpr uint32_t inst_desc(int n, uint32_t id, int m = 128) {
+  return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27) |
+         (id << 29);
 }
 __device__ __forceinline__ void mma(uint32_t d, uint64_t pd, uint64_t qd, uint32_t idesc, uint32_t ps, uint32_t qs,
                                     bool accumulate) {
@@ -127,15 +128,82 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                : "memory");
 }
 
+// The same for a pair of CTAs: both hold a part of either operand in their
+// shared memory and half of the accumulator's rows in their TMEM; one thread
+// of the even CTA issues for both.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, int cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, int cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t pd, uint64_t qd, uint32_t idesc, uint32_t ps, uint32_t qs,
+                                         bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(pd), "l"(qd), "r"(idesc), "r"(ps), "r"(qs), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+// One arrival on that barrier of each of the pair's CTAs.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// A load into this CTA's shared memory whose bytes count on a barrier of the
+// pair's even CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t address_in(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+// mbar_try_wait for a barrier on which the other CTA's threads arrive too.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // N consecutive accumulator columns of this warp's 32 lanes.
 template <int N>
 __device__ __forceinline__ void tmem_read(uint32_t addr, float (&v)[N]) {
-  static_assert(N == 8 || N == 32, "built widths");
+  static_assert(N == 8 || N == 16 || N == 32, "built widths");
   uint32_t r[N];
   if constexpr (N == 8) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(addr));
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
   } else {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -219,33 +287,103 @@ __device__ __forceinline__ void store_run(const MmArgs& a, int64_t p, int64_t q,
 
 // ------------------------------------------------------------ scale loader --
 
-// 16 scale bytes (two k tiles) of one row, of which the first n exist (the
-// others are 0), by loads as wide as the rows' alignment allows.
+// 16 scale bytes (two k tiles) of a row of which the first n exist (the
+// others are 0).  Words: rows 4-byte aligned and n a multiple of 4; every
+// load is predicated and none sits in a branch, whose end would wait for it.
+template <bool kWords>
 __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, int align) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (n >= 16 && align == 16) return *reinterpret_cast<const uint4*>(p);
-  if (n >= 16 && align == 8) {
-    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + 8);
-    return make_uint4(lo.x, lo.y, hi.x, hi.y);
-  }
-  if (align >= 4) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n >= 4 * j + 4) w[j] = *reinterpret_cast<const uint32_t*>(p + 4 * j);
-      else
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (n > 4 * j + i) w[j] |= (uint32_t)p[4 * j + i] << (8 * i);
+  if constexpr (kWords) {
+    const bool all = align == 16 && n >= 16;
+    const bool lo = !all && align >= 8 && n >= 8, hi = !all && align >= 8 && n >= 16;
+    const bool w0 = !all && !lo && n >= 4, w1 = !all && !lo && n >= 8;
+    const bool w2 = !all && !hi && n >= 12, w3 = !all && !hi && n >= 16;
+    uint4 r;
+    asm volatile(
+        "{\n\t.reg .pred q, l, h, a, b, c, d;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 l, %6, 0;\n\tsetp.ne.b32 h, %7, 0;\n\t"
+        "setp.ne.b32 a, %8, 0;\n\tsetp.ne.b32 b, %9, 0;\n\tsetp.ne.b32 c, %10, 0;\n\tsetp.ne.b32 d, %11, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+        "@l ld.global.v2.b32 {%0, %1}, [%4];\n\t"
+        "@h ld.global.v2.b32 {%2, %3}, [%4 + 8];\n\t"
+        "@a ld.global.b32 %0, [%4];\n\t"
+        "@b ld.global.b32 %1, [%4 + 4];\n\t"
+        "@c ld.global.b32 %2, [%4 + 8];\n\t"
+        "@d ld.global.b32 %3, [%4 + 12];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+        : "l"(p), "r"((int)all), "r"((int)lo), "r"((int)hi), "r"((int)w0), "r"((int)w1), "r"((int)w2), "r"((int)w3)
+        : "memory");
+    return r;
   } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < 16; ++j)
       if (n > j) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ void st_word(uint32_t addr, uint32_t w) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
+}
+
+// A loader thread's whole run: the scale bytes of its R rows for every k tile
+// of every tile, in order.  The loads are kAhead times two k tiles ahead of
+// the stores (their latency under a full load of code copies is several k
+// tiles long).  rows(tile, ptr) gives the R rows' starts (null: no such row),
+// put(w) stores one k tile's two words of each row when its stage is free,
+// and says whether to go on.  One warp's instructions between two k tiles
+// are what bounds this, so everything that depends on the tile alone is kept.
+template <int R, int kAhead, bool kWords, class Rows, class Put>
+__device__ __forceinline__ void stream_scales(int first, int step, int n_tiles, int k0, int k1, int k_blocks, int align,
+                                              Rows rows, Put put) {
+  if (k0 >= k1 || first >= n_tiles) return;
+  uint4 ring[kAhead][R];
+  const uint8_t* ptr[R];
+  int next = first, next_kt = k0;  // what is fetched next
+  if (k0 & 1) align = min(align, 8);
+  rows(first, ptr);
+  auto fetch_next = [&](uint4 (&r)[R]) {
+    if (next >= n_tiles) return;
+    const int n = k_blocks - 8 * next_kt;
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      r[j] = load_scales<kWords>(ptr[j] + 8 * next_kt, ptr[j] ? n : 0, align);
+    next_kt += 2;
+    if (next_kt >= k1) {
+      next_kt = k0;
+      next += step;
+      if (next < n_tiles) rows(next, ptr);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) fetch_next(ring[u]);
+  int tile = first, kt = k0;
+  while (true) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      uint2 w[R];
+      uint4 now[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        now[j] = ring[u][j];
+        w[j] = make_uint2(now[j].x, now[j].y);
+      }
+      fetch_next(ring[u]);
+      if (!put(w)) return;
+      if (kt + 1 < k1) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) w[j] = make_uint2(now[j].z, now[j].w);
+        if (!put(w)) return;
+      }
+      kt += 2;
+      if (kt >= k1) {
+        kt = k0;
+        tile += step;
+        if (tile >= n_tiles) return;
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -357,49 +495,43 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
       }
     }
   } else if (warp >= 8) {
-    // Thread t holds row t of P and rows t (and t + 128) of Q, two k tiles at
-    // a time, the next two loaded before the present ones are stored.
+    // thread t: row t of P and rows t (and t + 128) of Q
     const int t = threadIdx.x - 256;  // 0..127
     const uint32_t at = 16u * (t & 31) + 4u * (t >> 5);
-    uint4 cur[1 + kQ], nxt[1 + kQ];
-    auto fetch = [&](int tile, int kt, uint4 (&r)[1 + kQ]) {
-      const int left = a.k_blocks - 8 * kt, most = kt & 1 ? 8 : 16;
+    int st = 0, turn = 0;  // the stage and whether it has been used before
+    unsigned parity = 1;
+    auto rows = [&](int tile, const uint8_t* (&ptr)[1 + kQ]) {
       const int64_t p = (int64_t)(tile % a.p_tiles) * kLanes + t, q = (int64_t)(tile / a.p_tiles) * BN + t;
-      r[0] = load_scales(a.p_scales + p * a.p_scale_pitch + 8 * kt, p < a.p_rows ? left : 0, min(a.p_align, most));
+      ptr[0] = p < a.p_rows ? a.p_scales + p * a.p_scale_pitch : nullptr;
 #pragma unroll
       for (int j = 0; j < kQ; ++j)
-        r[1 + j] = load_scales(a.q_scales + (q + 128 * j) * a.q_scale_pitch + 8 * kt,
-                               q + 128 * j < a.q_rows && t + 128 * j < BN ? left : 0,
-                               min(a.q_align, most));
+        ptr[1 + j] = q + 128 * j < a.q_rows && t + 128 * j < BN ? a.q_scales + (q + 128 * j) * a.q_scale_pitch : nullptr;
     };
-    int it = 0;
-    bool ok = true;
-    if (first < a.n_tiles && k0 < k1) fetch(first, k0, nxt);
-    for (int tile = first; tile < a.n_tiles && ok; tile += step) {
-      for (int kt = k0; kt < k1 && ok; kt += 2) {
+    auto put = [&](const uint2 (&w)[1 + kQ]) {
+      if (turn && !__all_sync(0xFFFFFFFFu, wait(&sh.empty[st], parity))) return false;
+      const uint32_t dst = smem_u32(smem) + st * kStage + stage_codes(BN) + at;
 #pragma unroll
-        for (int j = 0; j < 1 + kQ; ++j) cur[j] = nxt[j];
-        if (kt + 2 < k1) fetch(tile, kt + 2, nxt);
-        else if (tile + step < a.n_tiles) fetch(tile + step, k0, nxt);
-        for (int h = 0; h < 2 && kt + h < k1; ++h, ++it) {
-          const int s = it % STAGES;
-          if (it >= STAGES &&
-              !(ok = __all_sync(0xFFFFFFFFu, wait(&sh.empty[s], ((it / STAGES) - 1) & 1))))
-            break;  // the whole warp
-          const uint32_t dst = smem_u32(smem + s * kStage) + stage_codes(BN) + at;
-          st_word(dst, h ? cur[0].z : cur[0].x);
-          st_word(dst + 512, h ? cur[0].w : cur[0].y);
-#pragma unroll
-          for (int j = 0; j < kQ; ++j) {
-            st_word(dst + 1024 + 512 * j, h ? cur[1 + j].z : cur[1 + j].x);
-            st_word(dst + 1024 + 512 * (kQ + j), h ? cur[1 + j].w : cur[1 + j].y);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.scales_full[s]);
-        }
+      for (int j = 0; j < 1 + kQ; ++j) {
+        const uint32_t to = dst + (j == 0 ? 0 : 1024 + 512 * (j - 1));
+        st_word(to, w[j].x);
+        st_word(to + (j == 0 ? 512 : 512 * kQ), w[j].y);
       }
-    }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.scales_full[st]);
+      if (++st == STAGES) {
+        st = 0;
+        turn = 1;
+        parity ^= 1;
+      }
+      return true;
+    };
+    const int align = min(a.p_align, a.q_align);
+    constexpr int kAhead = BN <= 64 ? 2 : 4;
+    if (align >= 4 && a.k_blocks % 4 == 0)
+      stream_scales<1 + kQ, kAhead, true>(first, step, a.n_tiles, k0, k1, a.k_blocks, align, rows, put);
+    else
+      stream_scales<1 + kQ, 1, false>(first, step, a.n_tiles, k0, k1, a.k_blocks, align, rows, put);
   } else if (warp >= 4 && a.split == 1) {
     const int w = warp - 4;
     int n = 0;
@@ -465,6 +597,231 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
   if (warp == 1) tmem_free(tmem, tmem_cols(BN));
 }
 
+// ------------------------------------------------------- kernel, CTA pairs --
+
+// Tiles of 256 x 256 by pairs of CTAs (one cluster of two per pair of SMs,
+// walking the tiles): each CTA loads 128 rows of P and 128 of Q, and the
+// pair's instruction reads both halves of Q, so that a stage brings 32 KB
+// into each SM where a CTA alone (128 x 256) would need 48.  Every CTA keeps
+// the scales of its own rows of P and of all 256 rows of Q.
+//
+// The scales come in the tensor core's order, from a workspace that
+// mx_scale_pieces_kernel filled: the 1024 bytes of 128 rows and one k tile
+// lie together, one row of the tensor map s_map.  (Warps
+// that gather them from the rows while the products run could not keep up:
+// 1900 cycles a k tile, of which the products need 512.)
+//
+// Two accumulators of 256 columns share 48 of TMEM's 512 with each other
+// (the rest holds two sets of scales): the epilogue empties the shared
+// columns first and lets the next tile start, then the others while it runs.
+constexpr int kPairN = 256;
+constexpr int kPairStages = 6;
+constexpr int kPairCodes = 2 * kLanes * kTileKBytes;     // per CTA
+constexpr int kPieces = 1024;                            // scale bytes of 128 rows and one k tile
+constexpr int kPairStage = kPairCodes + 3 * kPieces;     // per CTA
+constexpr int kPairThreads = 256;
+constexpr int kPairScaleCols = 24;
+constexpr int kPairScales = 512 - 2 * kPairScaleCols;    // first column of the scales
+constexpr int kPairSecond = kPairScales - kPairN;        // first column of the second accumulator
+constexpr int kPairShared = kPairN - kPairSecond;        // columns in both
+static_assert(kPairShared % 16 == 0 && kPairShared == 48, "the epilogue's order");
+
+struct PairShared {
+  uint64_t full[kPairStages], empty[kPairStages];
+  uint64_t acc_full[2], acc_empty, drained;
+  uint32_t tmem;
+  int abort;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    mx_matmul_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                          const __grid_constant__ CUtensorMap s_map, const __grid_constant__ MmArgs a) {
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ PairShared sh;
+  uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    mbar_init(&sh.acc_full[0], 1);
+    mbar_init(&sh.acc_full[1], 1);
+    mbar_init(&sh.acc_empty, 8);
+    mbar_init(&sh.drained, 1);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc_pair(&sh.tmem, 512);
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
+    if (try_wait_cluster(bar, parity)) return true;
+    const unsigned long long t0 = now_ns();
+    while (!try_wait_cluster(bar, parity)) {
+      if (*abort_flag) return false;
+      if (now_ns() - t0 > kWaitNs) {
+        *abort_flag = 1;
+        atomicOr(&g_mx_error, 1u);
+        return false;
+      }
+    }
+    return true;
+  };
+  if (a.pdl) dev::pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0, s = 0;
+      unsigned parity = 1;
+      bool ok = true;
+      const uint32_t full = address_in(&sh.full[0], 0);
+      for (int tile = first; tile < a.n_tiles && ok; tile += step) {
+        const int pb = (tile % a.p_tiles) * 2, qb = (tile / a.p_tiles) * 2;  // blocks of 128 rows
+        const int py = (pb + rank) * a.k_tiles, qy = (2 * a.p_tiles + qb) * a.k_tiles;  // their rows in s_map
+        for (int kt = 0; kt < a.k_tiles; ++kt) {
+          if (it >= kPairStages && !(ok = wait(&sh.empty[s], parity))) break;
+          uint8_t* st = smem + s * kPairStage;
+          if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * kPairStage);
+          tma_load_2d_pair(st, &p_map, kt * kTileKBytes, (pb + rank) * kLanes, full + 8 * s);
+          tma_load_2d_pair(st + kLanes * kTileKBytes, &q_map, kt * kTileKBytes, (qb + rank) * kLanes, full + 8 * s);
+          uint8_t* sc = st + kPairCodes;
+          tma_load_2d_pair(sc, &s_map, 0, py + kt, full + 8 * s);
+          tma_load_2d_pair(sc + kPieces, &s_map, 0, qy + kt, full + 8 * s);
+          tma_load_2d_pair(sc + 2 * kPieces, &s_map, 0, qy + a.k_tiles + kt, full + 8 * s);
+          ++it;
+          if (++s == kPairStages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+      }
+      if (!ok && it > 0) {  // the copies in flight land long before this has passed
+        const unsigned long long t0 = now_ns();
+        while (now_ns() - t0 < 20000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    if (lane == 0) {
+      int n = 0, s = 0, set = 0;
+      unsigned parity = 0;
+      bool ok = true, issued = false;
+      const uint32_t base = smem_u32(smem);
+      for (int tile = first; tile < a.n_tiles && ok; tile += step, ++n) {
+        if (n > 0 && !(ok = wait(&sh.acc_empty, (n - 1) & 1))) break;
+        fence_after();
+        const uint32_t acc = tmem + (n & 1 ? kPairSecond : 0);
+        for (int kt = 0; kt < a.k_tiles; ++kt) {
+          if (!(ok = wait(&sh.full[s], parity))) break;
+          fence_after();
+          const uint32_t at = base + s * kPairStage;
+          const uint64_t pd = tile_desc(at), qd = tile_desc(at + kLanes * kTileKBytes);
+          const uint64_t sd = scale_desc(at + kPairCodes);
+          const uint32_t ts = tmem + kPairScales + set * kPairScaleCols;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            copy_scales_pair(ts + 4 * c, sd + 32 * c);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) copy_scales_pair(ts + 8 + 4 * (2 * c + q), sd + 64 + 64 * q + 32 * c);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_pair(acc, pd + 2 * j, qd + 2 * j, inst_desc(kPairN, (j & 1) * 2, 256), ts + 4 * (j >> 1),
+                     ts + 8 + 8 * (j >> 1), kt > 0 || j > 0);
+          issued = true;
+          mma_commit_pair(&sh.empty[s]);
+          set ^= 1;
+          if (++s == kPairStages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+        if (ok) mma_commit_pair(&sh.acc_full[n & 1]);
+      }
+      if (!ok && issued) {  // products in flight end before TMEM is freed
+        mma_commit_pair(&sh.drained);
+        mbar_wait(&sh.drained, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int w = warp - 4;
+    int n = 0;
+    for (int tile = first; tile < a.n_tiles; tile += step, ++n) {
+      if (!__all_sync(0xFFFFFFFFu, wait(&sh.acc_full[n & 1], (n >> 1) & 1))) break;
+      fence_after();
+      const int64_t p = (int64_t)(tile % a.p_tiles) * 2 * kLanes + rank * kLanes + 32 * w + lane;
+      const int64_t q0 = (int64_t)(tile / a.p_tiles) * kPairN;
+      const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + (n & 1 ? kPairSecond : 0);
+      const int turn = n & 1 ? 0 : kPairSecond;  // this accumulator's first column that the other one shares
+      for (int c = 0; c < kPairN; c += 16) {
+        const int col = (turn + c) & (kPairN - 1);
+        float v[16];
+        tmem_read<16>(acc + col, v);
+        if (c + 16 == kPairShared) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(address_in(&sh.acc_empty, 0));
+        }
+        store_run<16>(a, p, q0 + col, v);
+      }
+      fence_before();
+    }
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA ends while the other may still reach its memory
+  fence_after();
+  if (warp == 1) tmem_free_pair(tmem, 512);
+}
+
+// The scales of both operands in the pair kernel's order: 1024 bytes for each
+// 128 rows and k tile, row r's byte for block b of the tile at
+// 512 (b / 4) + 16 (r % 32) + 4 (r / 32 % 4) + b % 4; 0 past the matrix (the
+// codes there are 0 too, but a product with a NaN scale would not be).  A
+// warp takes 32 rows and one k tile, a lane a row.
+struct PieceArgs {
+  const uint8_t* scales[2];
+  int64_t pitch[2];
+  int rows[2], align[2];
+  uint8_t* out[2];
+  int warps0, warps;  // 32-row pieces of the first operand, of both
+  int k_blocks, k_tiles;
+};
+
+__global__ void __launch_bounds__(256) mx_scale_pieces_kernel(const __grid_constant__ PieceArgs a) {
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  int w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (w >= a.warps) return;
+  const int o = w >= a.warps0 ? 1 : 0;
+  if (o) w -= a.warps0;
+  const int kt = w % a.k_tiles, r32 = w / a.k_tiles;
+  const int64_t row = 32ll * r32 + lane;
+  const int n = row < a.rows[o] ? min(a.k_blocks - 8 * kt, 8) : 0;
+  const uint8_t* p = a.scales[o] + (n > 0 ? row * a.pitch[o] + 8 * kt : 0);
+  uint32_t v[2] = {0u, 0u};
+  if (a.align[o] >= 8 && n == 8) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v[0] = x.x, v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) v[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  }
+  uint8_t* out = a.out[o] + ((int64_t)(r32 >> 2) * a.k_tiles + kt) * kPieces + 16 * lane + 4 * (r32 & 3);
+  *reinterpret_cast<uint32_t*>(out) = v[0];
+  *reinterpret_cast<uint32_t*>(out + 512) = v[1];
+}
+
 // -------------------------------------------------------------------- host --
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -493,6 +850,29 @@ bool codes_map(CUtensorMap* map, const MxMatrix& m, int rows) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The large dynamic shared memory, opted into once per device (`opted`: a bit for each).
+template <class K>
+cudaError_t opt_in(K kernel, int bytes, std::atomic<uint64_t>& opted) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (opted.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) opted.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+// A workspace of scale pieces as rows of 1024 bytes.
+bool pieces_map(CUtensorMap* map, uint8_t* pieces, int64_t rows) {
+  const cuuint64_t dims[2] = {kPieces / 4, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {kPieces};
+  const cuuint32_t box[2] = {kPieces / 4, 1}, one[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, pieces, dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, int STAGES>
 cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, int sm_count, cudaStream_t s) {
   CUtensorMap pm, qm;
@@ -501,17 +881,9 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, int sm_count,
   static_assert(kSmem <= 227 * 1024 - 1024, "stages fit shared memory");
   static_assert(STAGES * stage_bytes(BN) >= (BN + 8) * kLanes * 4 || BN > 128, "the split's parts fit the stages");
   auto kernel = mx_matmul_kernel<BN, STAGES>;
-  // the large dynamic shared memory is opted into once per device
   static std::atomic<uint64_t> opted{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = opt_in(kernel, kSmem, opted);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!bit || !(opted.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    opted.fetch_or(bit, std::memory_order_release);
-  }
   a.p_tiles = (a.p_rows + kLanes - 1) / kLanes;
   const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + BN - 1) / BN);
   if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
@@ -541,14 +913,68 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, int sm_count,
   return cudaLaunchKernelEx(&cfg, kernel, pm, qm, a);
 }
 
+// Row blocks of 128 that the pair kernel reads for `rows` rows (whole pairs).
+int64_t pair_blocks(int64_t rows) { return 2 * ((rows + 255) / 256); }
+
+cudaError_t launch_pair(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* workspace, int sm_count, cudaStream_t s) {
+  PieceArgs g = {};
+  g.scales[0] = a.p_scales, g.scales[1] = a.q_scales;
+  g.pitch[0] = a.p_scale_pitch, g.pitch[1] = a.q_scale_pitch;
+  g.rows[0] = a.p_rows, g.rows[1] = a.q_rows;
+  g.align[0] = a.p_align, g.align[1] = a.q_align;
+  CUtensorMap pm, qm, sm;
+  const int64_t row = (int64_t)a.k_tiles * kPieces, pb = pair_blocks(p.rows), qb = pair_blocks(q.rows);
+  if ((pb + qb) * 4 * a.k_tiles > 0x7FFFFFFF - 8) return cudaErrorInvalidValue;
+  if (!codes_map(&pm, p, kLanes) || !codes_map(&qm, q, kLanes) || !pieces_map(&sm, workspace, (pb + qb) * a.k_tiles))
+    return cudaErrorInvalidValue;
+  g.out[0] = workspace, g.out[1] = workspace + pb * row;
+  g.k_blocks = a.k_blocks, g.k_tiles = a.k_tiles;
+  g.warps0 = (int)(pb * 4 * a.k_tiles), g.warps = (int)((pb + qb) * 4 * a.k_tiles);
+  cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, a.pdl != 0, g);
+  if (e != cudaSuccess) return e;
+  a.pdl = 1;
+  constexpr int kSmem = kPairStages * kPairStage + 1024;
+  static_assert(kSmem <= 227 * 1024 - 1024, "stages fit shared memory");
+  static std::atomic<uint64_t> opted{0};
+  e = opt_in(mx_matmul_pair_kernel, kSmem, opted);
+  if (e != cudaSuccess) return e;
+  a.p_tiles = (a.p_rows + 2 * kLanes - 1) / (2 * kLanes);
+  const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + kPairN - 1) / kPairN);
+  if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
+  a.n_tiles = (int)tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)std::min<int64_t>(tiles, sm_count / 2));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mx_matmul_pair_kernel, pm, qm, sm, a);
+}
+
 }  // namespace
+
+// Whether the product runs on CTA pairs: enough 256 x 256 tiles for half of them.
+bool by_pairs(int64_t m, int64_t n, int sm_count) { return ((m + 255) / 256) * ((n + 255) / 256) >= sm_count / 4; }
+
+int64_t mx_matmul_workspace(int64_t m, int64_t n, int64_t k, int sm_count) {
+  if (!by_pairs(m, n, sm_count)) return 0;
+  return (pair_blocks(m) + pair_blocks(n)) * ((mx_blocks(k) + 7) / 8) * kPieces;
+}
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
-  // Plain orientation, 128 x 256 tiles, when they give every SM one; below
-  // that the swapped one (a's rows are the columns of the tile), where the
-  // parts of a split k end in stores that run along the result's rows.
-  const bool swap = ((m.a.rows + kLanes - 1) / kLanes) * ((m.b.rows + 255) / 256) < sm_count;
+  // Many tiles: CTA pairs, a's rows as lanes, whose results go out 32 bytes at
+  // a time along a row -- or b's rows as lanes where the result's rows are not
+  // 32-byte aligned, which makes a warp's 32 lanes neighbours in memory.  Few
+  // tiles: b's rows as lanes, narrower tiles, k split over a cluster.
+  const int64_t row_bytes = m.ld * (m.type == kMxF32 ? 4 : 2);
+  const bool aligned = ((reinterpret_cast<uintptr_t>(m.out) | (uintptr_t)row_bytes) & 31u) == 0;
+  const bool many = by_pairs(m.a.rows, m.b.rows, sm_count);
+  const bool swap = !many || !aligned;
   const MxMatrix& p = swap ? m.b : m.a;
   const MxMatrix& q = swap ? m.a : m.b;
   MmArgs a = {};
@@ -564,10 +990,9 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   a.p_align = align(p), a.q_align = align(q);
   a.out = m.out, a.type = m.type, a.pdl = m.pdl;
   a.p_stride = swap ? 1 : m.ld, a.q_stride = swap ? m.ld : 1;
-  const int64_t row_bytes = m.ld * (m.type == kMxF32 ? 4 : 2);
-  a.vec = !swap && ((reinterpret_cast<uintptr_t>(m.out) | (uintptr_t)row_bytes) & 31u) == 0;
+  a.vec = !swap;
   a.split = 1;
-  if (!swap) return launch<256, 4>(p, q, a, sm_count, s);
+  if (many) return launch_pair(p, q, a, static_cast<uint8_t*>(m.workspace), sm_count, s);
   const int64_t p_tiles = (p.rows + kLanes - 1) / kLanes;
   auto split_for = [&](int bn, int slots) {
     const int64_t tiles = p_tiles * ((q.rows + bn - 1) / bn);
