@@ -139,9 +139,6 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, int cols) {
 __device__ __forceinline__ void tmem_free_pair(uint32_t addr, int cols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
-__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t pd, uint64_t qd, uint32_t idesc, uint32_t ps, uint32_t qs,
                                          bool accumulate) {
   asm volatile(
@@ -177,7 +174,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, unsigned parity)
   unsigned ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -185,7 +182,23 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, unsigned parity)
   return ok != 0;
 }
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A wait of at most kWaitCycles: 0 done, 1 ran out, 2 another role stopped.
+// Bounded by the SM's own clock: a read of the global timer takes about a
+// microsecond, which would be added to every wait that has to poll.
+constexpr long long kWaitCycles = 4000000000ll;  // two seconds at 2 GHz
+template <bool kCluster>
+__device__ __forceinline__ int wait_bounded(uint64_t* bar, unsigned parity, volatile int* abort_flag) {
+  auto done = [&] { return kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return 0;
+  const long long t0 = clock64();
+  while (!done()) {
+    if (*abort_flag) return 2;
+    if (clock64() - t0 > kWaitCycles) return 1;
+  }
+  return 0;
 }
 
 // N consecutive accumulator columns of this warp's 32 lanes.
@@ -217,6 +230,20 @@ __device__ __forceinline__ void tmem_read(uint32_t addr, float (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 24 consecutive columns of this warp's 32 lanes, from registers.
+__device__ __forceinline__ void tmem_write24(uint32_t addr, const uint4 (&v)[6]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w),
+      "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
+      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr + 16),
+               "r"(v[4].x), "r"(v[4].y), "r"(v[4].z), "r"(v[4].w), "r"(v[5].x), "r"(v[5].y), "r"(v[5].z), "r"(v[5].w)
+               : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -429,7 +456,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
-    const int r = mbar_wait_or_abort(bar, parity, abort_flag, kWaitNs);
+    const int r = wait_bounded<false>(bar, parity, abort_flag);
     if (r == 1) {
       *abort_flag = 1;
       atomicOr(&g_mx_error, 1u);
@@ -611,23 +638,30 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
 // that gather them from the rows while the products run could not keep up:
 // 1900 cycles a k tile, of which the products need 512.)
 //
-// Two accumulators of 256 columns share 48 of TMEM's 512 with each other
-// (the rest holds two sets of scales): the epilogue empties the shared
+// From the stage four warps of each CTA carry them on to TMEM (a thread's 16
+// bytes of a piece are its lane's four columns).  The tensor core's own copy
+// instruction takes 58 cycles for each 512 bytes in turn with the products:
+// 350 cycles a k tile beside their 512.
+//
+// Two accumulators of 256 columns share 96 of TMEM's 512 with each other
+// (the rest holds four sets of scales): the epilogue empties the shared
 // columns first and lets the next tile start, then the others while it runs.
 constexpr int kPairN = 256;
 constexpr int kPairStages = 6;
 constexpr int kPairCodes = 2 * kLanes * kTileKBytes;     // per CTA
 constexpr int kPieces = 1024;                            // scale bytes of 128 rows and one k tile
 constexpr int kPairStage = kPairCodes + 3 * kPieces;     // per CTA
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 384;
+constexpr int kPairSets = 4;
 constexpr int kPairScaleCols = 24;
-constexpr int kPairScales = 512 - 2 * kPairScaleCols;    // first column of the scales
-constexpr int kPairSecond = kPairScales - kPairN;        // first column of the second accumulator
-constexpr int kPairShared = kPairN - kPairSecond;        // columns in both
-static_assert(kPairShared % 16 == 0 && kPairShared == 48, "the epilogue's order");
+constexpr int kPairScales = 512 - kPairSets * kPairScaleCols;  // first column of the scales
+constexpr int kPairSecond = kPairScales - kPairN;              // first column of the second accumulator
+constexpr int kPairShared = kPairN - kPairSecond;              // columns in both
+static_assert(kPairShared % 16 == 0 && kPairShared > 0, "the epilogue's order");
+static_assert(kPairSets <= kPairStages, "a set is written again after its stage's products");
 
 struct PairShared {
-  uint64_t full[kPairStages], empty[kPairStages];
+  uint64_t full[kPairStages], pieces_full[kPairStages], scales_full[kPairStages], empty[kPairStages];
   uint64_t acc_full[2], acc_empty, drained;
   uint32_t tmem;
   int abort;
@@ -646,6 +680,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
       mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.pieces_full[s], 1);
+      mbar_init(&sh.scales_full[s], 8);
       mbar_init(&sh.empty[s], 1);
     }
     mbar_init(&sh.acc_full[0], 1);
@@ -663,17 +699,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
-    if (try_wait_cluster(bar, parity)) return true;
-    const unsigned long long t0 = now_ns();
-    while (!try_wait_cluster(bar, parity)) {
-      if (*abort_flag) return false;
-      if (now_ns() - t0 > kWaitNs) {
-        *abort_flag = 1;
-        atomicOr(&g_mx_error, 1u);
-        return false;
-      }
+    const int r = wait_bounded<true>(bar, parity, abort_flag);
+    if (r == 1) {
+      *abort_flag = 1;
+      atomicOr(&g_mx_error, 1u);
     }
-    return true;
+    return r == 0;
   };
   if (a.pdl) dev::pdl_wait();
 
@@ -682,25 +713,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int it = 0, s = 0;
       unsigned parity = 1;
       bool ok = true;
-      const uint32_t full = address_in(&sh.full[0], 0);
+      const uint32_t full = address_in(&sh.full[0], 0), mine = address_in(&sh.pieces_full[0], rank);
       for (int tile = first; tile < a.n_tiles && ok; tile += step) {
         const int pb = (tile % a.p_tiles) * 2, qb = (tile / a.p_tiles) * 2;  // blocks of 128 rows
         const int py = (pb + rank) * a.k_tiles, qy = (2 * a.p_tiles + qb) * a.k_tiles;  // their rows in s_map
         for (int kt = 0; kt < a.k_tiles; ++kt) {
           if (it >= kPairStages && !(ok = wait(&sh.empty[s], parity))) break;
+          fence_proxy_async_smem();  // the scale warps' reads of the stage, before it is written again
           uint8_t* st = smem + s * kPairStage;
-          if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * kPairStage);
+          if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * kPairCodes);
+          mbar_expect_tx(&sh.pieces_full[s], 3 * kPieces);
+          uint8_t* sc = st + kPairCodes;
+          tma_load_2d_pair(sc, &s_map, 0, py + kt, mine + 8 * s);
+          tma_load_2d_pair(sc + kPieces, &s_map, 0, qy + kt, mine + 8 * s);
+          tma_load_2d_pair(sc + 2 * kPieces, &s_map, 0, qy + a.k_tiles + kt, mine + 8 * s);
           tma_load_2d_pair(st, &p_map, kt * kTileKBytes, (pb + rank) * kLanes, full + 8 * s);
           tma_load_2d_pair(st + kLanes * kTileKBytes, &q_map, kt * kTileKBytes, (qb + rank) * kLanes, full + 8 * s);
-          uint8_t* sc = st + kPairCodes;
-          tma_load_2d_pair(sc, &s_map, 0, py + kt, full + 8 * s);
-          tma_load_2d_pair(sc + kPieces, &s_map, 0, qy + kt, full + 8 * s);
-          tma_load_2d_pair(sc + 2 * kPieces, &s_map, 0, qy + a.k_tiles + kt, full + 8 * s);
           ++it;
           if (++s == kPairStages) {
             s = 0;
             parity ^= 1;
           }
+        }
+      }
+      // the last products' arrivals here, before this CTA may end
+      if (it < kPairStages) s = 0, parity = 0;
+      for (int j = min(it, kPairStages); j > 0 && ok; --j) {
+        ok = wait(&sh.empty[s], parity);
+        if (++s == kPairStages) {
+          s = 0;
+          parity ^= 1;
         }
       }
       if (!ok && it > 0) {  // the copies in flight land long before this has passed
@@ -721,24 +763,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t acc = tmem + (n & 1 ? kPairSecond : 0);
         for (int kt = 0; kt < a.k_tiles; ++kt) {
           if (!(ok = wait(&sh.full[s], parity))) break;
+          if (!(ok = wait(&sh.scales_full[s], parity))) break;
           fence_after();
           const uint32_t at = base + s * kPairStage;
           const uint64_t pd = tile_desc(at), qd = tile_desc(at + kLanes * kTileKBytes);
-          const uint64_t sd = scale_desc(at + kPairCodes);
           const uint32_t ts = tmem + kPairScales + set * kPairScaleCols;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            copy_scales_pair(ts + 4 * c, sd + 32 * c);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) copy_scales_pair(ts + 8 + 4 * (2 * c + q), sd + 64 + 64 * q + 32 * c);
-          }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             mma_pair(acc, pd + 2 * j, qd + 2 * j, inst_desc(kPairN, (j & 1) * 2, 256), ts + 4 * (j >> 1),
                      ts + 8 + 8 * (j >> 1), kt > 0 || j > 0);
           issued = true;
           mma_commit_pair(&sh.empty[s]);
-          set ^= 1;
+          if (++set == kPairSets) set = 0;
           if (++s == kPairStages) {
             s = 0;
             parity ^= 1;
@@ -751,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_wait(&sh.drained, 0);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     const int w = warp - 4;
     int n = 0;
     for (int tile = first; tile < a.n_tiles; tile += step, ++n) {
@@ -773,6 +809,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         store_run<16>(a, p, q0 + col, v);
       }
       fence_before();
+    }
+  } else if (warp >= 8) {
+    const int w = warp - 8;
+    const int tiles = first < a.n_tiles ? (a.n_tiles - 1 - first) / step + 1 : 0;
+    const int64_t total = (int64_t)tiles * a.k_tiles;
+    const uint32_t ready = address_in(&sh.scales_full[0], 0);
+    const uint32_t ts = tmem + ((uint32_t)(32 * w) << 16) + kPairScales;
+    int s = 0, set = 0, s_old = 0;  // s_old: the stage whose products used this set before
+    unsigned parity = 0, parity_old = 0;
+    for (int64_t it = 0; it < total; ++it) {
+      bool ok = wait(&sh.pieces_full[s], parity);
+      if (it >= kPairSets) {
+        ok = ok && wait(&sh.empty[s_old], parity_old);
+        if (++s_old == kPairStages) {
+          s_old = 0;
+          parity_old ^= 1;
+        }
+      }
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      fence_after();
+      const uint8_t* sc = smem + s * kPairStage + kPairCodes + 16 * lane;
+      // columns: P's two pieces, then Q's of rows 0-127 and 128-255 for each half of the k tile
+      uint4 v[6];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        v[c] = *reinterpret_cast<const uint4*>(sc + 512 * c);
+        v[2 + 2 * c] = *reinterpret_cast<const uint4*>(sc + kPieces + 512 * c);
+        v[3 + 2 * c] = *reinterpret_cast<const uint4*>(sc + 2 * kPieces + 512 * c);
+      }
+      tmem_write24(ts + set * kPairScaleCols, v);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(ready + 8 * s);
+      if (++set == kPairSets) set = 0;
+      if (++s == kPairStages) {
+        s = 0;
+        parity ^= 1;
+      }
     }
   }
   fence_before();
