@@ -816,7 +816,7 @@ void zero_destroy(zero_ctx* ctx);
 
 typedef struct zero_mx4 {
   void* codes;          /* device, 16-byte aligned */
-  void* scales;         /* device, one byte per block (4-byte aligned rows load faster) */
+  void* scales;         /* device, one byte per block (a product loads 16-byte aligned rows faster) */
   int64_t rows, cols;   /* elements; each below 2^31 - 256 */
   int64_t code_pitch;   /* bytes between rows of codes: a multiple of 16, >= 16 * ceil(cols / 32) */
   int64_t scale_pitch;  /* bytes between rows of scales, >= ceil(cols / 32) */
@@ -844,9 +844,10 @@ zero_status zero_mx4_transpose(const zero_mx4* in, int32_t rounding, uint64_t se
  * ld elements between rows.  No passage of the pages defines it. */
 zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, int64_t ld, void* stream);
 
-/* Bytes of workspace that zero_mx4_matmul needs for an m x n result over k
- * columns on the current device (0 for small results). */
-zero_status zero_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t* bytes);
+/* Bytes of workspace that zero_mx4_matmul needs for these matrices (16 bytes
+ * for each row and 512 columns of a matrix whose rows of scales are not
+ * 16-byte aligned, none for one whose rows are).  Host only. */
+zero_status zero_mx4_matmul_workspace(const zero_mx4* a, const zero_mx4* b, int64_t* bytes);
 
 /* out[i][j] = sum over k of a[i][k] b[j][k] (a->rows x b->rows of `dtype`, ld
  * elements between rows), for two MX4 matrices of the same number of columns,
@@ -859,8 +860,9 @@ zero_status zero_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t* 
 zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int32_t dtype, int64_t ld, void* workspace,
                             int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that zero_mx4_linear needs on the current device. */
-zero_status zero_mx4_linear_workspace(int64_t tokens, int64_t outputs, int64_t inputs, int64_t* bytes);
+/* Bytes of workspace that zero_mx4_linear needs for `tokens` rows of x and
+ * this w.  Host only. */
+zero_status zero_mx4_linear_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes);
 
 /* The forward product of a linear layer whose weight w (outputs x inputs) is
  * an MX4 matrix, for one token or many: y = Q(x) w^T, x (tokens x inputs of

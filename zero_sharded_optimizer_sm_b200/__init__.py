@@ -136,9 +136,9 @@ _SIGS = {
     "zero_mx4_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, ctypes.c_uint64, _MX4, _MX4, _vp]),
     "zero_mx4_transpose": (_i32, [_MX4, _i32, ctypes.c_uint64, _MX4, _vp]),
     "zero_mx4_dequantize": (_i32, [_MX4, _vp, _i32, _i64, _vp]),
-    "zero_mx4_matmul_workspace": (_i32, [_i64, _i64, _i64, ctypes.POINTER(_i64)]),
+    "zero_mx4_matmul_workspace": (_i32, [_MX4, _MX4, ctypes.POINTER(_i64)]),
     "zero_mx4_matmul": (_i32, [_MX4, _MX4, _vp, _i32, _i64, _vp, _i64, _vp]),
-    "zero_mx4_linear_workspace": (_i32, [_i64, _i64, _i64, ctypes.POINTER(_i64)]),
+    "zero_mx4_linear_workspace": (_i32, [_i64, _MX4, ctypes.POINTER(_i64)]),
     "zero_mx4_linear": (_i32, [_vp, _i32, _i64, _i64, _MX4, _vp, _i32, _i64, _vp, _i64, _vp]),
     "zero_mx4_check": (_i32, [_vp]),
     "zero_mx4_all_gather": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
@@ -885,10 +885,10 @@ def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
     return out
 
 
-def _workspace(query, m: int, n: int, k: int, device, stream):
+def _workspace(query, a, b, device, stream):
     """(pointer, bytes, tensor) of the workspace that the query asks for."""
     need = ctypes.c_int64()
-    _mx4_check(query(m, n, k, ctypes.byref(need)), "workspace size")
+    _mx4_check(query(a, b, ctypes.byref(need)), "workspace size")
     if need.value == 0:
         return None, 0, None
     space = _torch().empty(need.value, dtype=_torch().uint8, device=device)
@@ -903,8 +903,9 @@ def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
     ptr, code, ld, _, _ = _dense(out, "out")
     _same_device(device, b=b, out=out)
     with _on(device):
-        at, size, space = _workspace(zero_mx4_matmul_workspace, a.rows, b.rows, a.cols, device, stream)
-        _mx4_check(zero_mx4_matmul(ctypes.byref(a._c), ctypes.byref(b._c), ptr, code, ld, at, size,
+        ac, bc = ctypes.byref(a._c), ctypes.byref(b._c)
+        at, size, space = _workspace(zero_mx4_matmul_workspace, ac, bc, device, stream)
+        _mx4_check(zero_mx4_matmul(ac, bc, ptr, code, ld, at, size,
                                    _stream_of(device, stream)), "zero_mx4_matmul")
     return out
 
@@ -920,8 +921,9 @@ def mx4_linear(x, w: MX4, out=None, stream=None):
     yptr, ycode, ldy, _, _ = _dense(y, "out")
     _same_device(device, w=w, out=y)
     with _on(device):
-        at, size, space = _workspace(zero_mx4_linear_workspace, tokens, w.rows, inputs, device, stream)
-        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, ctypes.byref(w._c), yptr, ycode, ldy, at, size,
+        wc = ctypes.byref(w._c)
+        at, size, space = _workspace(zero_mx4_linear_workspace, tokens, wc, device, stream)
+        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, wc, yptr, ycode, ldy, at, size,
                                    _stream_of(device, stream)), "zero_mx4_linear")
     return y
 

@@ -103,7 +103,7 @@ cudaError_t launch_mx_dequantize(const MxDequantArgs& a, int sm_count, cudaStrea
 cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int sm_count, cudaStream_t s);
-int64_t mx_matmul_workspace(int64_t m, int64_t n, int64_t k, int sm_count);
+int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b);
 cudaError_t mx_matmul_error(unsigned* flag, cudaStream_t s);
 
 // The message zero_last_error(NULL) returns to the calling thread.

@@ -116,6 +116,17 @@ zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtyp
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 product launch");
 }
 
+// zero_mx4_linear's workspace: x's codes, its scales (rows of 16-byte
+// multiples), then the product's own part.
+zero_mx4 quantised_x(uint8_t* at, int64_t tokens, int64_t inputs) {
+  const int64_t nb = zsm::mx_blocks(inputs);
+  return {at, at ? at + tokens * 16 * nb : nullptr, tokens, inputs, 16 * nb, align16(nb)};
+}
+int64_t linear_own(int64_t tokens, int64_t inputs) {
+  const int64_t nb = zsm::mx_blocks(inputs);
+  return tokens * (16 * nb + align16(nb));
+}
+
 // A product over no elements: zeros.
 zero_status zero_fill(void* out, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, cudaStream_t s) {
   const int es = elem_bytes(dtype);
@@ -189,15 +200,13 @@ zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, in
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 read-back launch");
 }
 
-zero_status zero_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t* bytes) {
+zero_status zero_mx4_matmul_workspace(const zero_mx4* a, const zero_mx4* b, int64_t* bytes) {
   if (!bytes) return fail(ZERO_EINVAL, "bytes is NULL");
   *bytes = 0;
-  if (m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim)
-    return fail(ZERO_EINVAL, "%lld x %lld x %lld is out of range", (long long)m, (long long)n, (long long)k);
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return cuda_fail(e, "device query");
-  *bytes = m && n && k ? zsm::mx_matmul_workspace(m, n, k, sms) : 0;
+  zero_status st = check_mx4("a", a);
+  if (st != ZERO_OK) return st;
+  if ((st = check_mx4("b", b)) != ZERO_OK) return st;
+  if (a->rows && b->rows && a->cols) *bytes = zsm::mx_matmul_workspace(matrix(*a), matrix(*b));
   return ZERO_OK;
 }
 
@@ -215,16 +224,21 @@ zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  const int64_t need = zsm::mx_matmul_workspace(a->rows, b->rows, a->cols, sms);
+  const int64_t need = zsm::mx_matmul_workspace(matrix(*a), matrix(*b));
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return st;
   return matmul(*a, *b, out, dtype, ld, workspace, 0, sms, s);
 }
 
-zero_status zero_mx4_linear_workspace(int64_t tokens, int64_t outputs, int64_t inputs, int64_t* bytes) {
-  const zero_status st = zero_mx4_matmul_workspace(tokens, outputs, inputs, bytes);
+zero_status zero_mx4_linear_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes) {
+  if (!bytes) return fail(ZERO_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  const zero_status st = check_mx4("w", w);
   if (st != ZERO_OK) return st;
-  const int64_t nb = zsm::mx_blocks(inputs);
-  *bytes += tokens * (16 * nb + align16(nb));
+  if (tokens < 0 || tokens > kMaxDim) return fail(ZERO_EINVAL, "%lld tokens", (long long)tokens);
+  if (tokens && w->rows && w->cols) {
+    const zero_mx4 xq = quantised_x(nullptr, tokens, w->cols);
+    *bytes = linear_own(tokens, w->cols) + zsm::mx_matmul_workspace(matrix(xq), matrix(*w));
+  }
   return ZERO_OK;
 }
 
@@ -240,14 +254,11 @@ zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  const int64_t nb = zsm::mx_blocks(w->cols);
-  const int64_t own = tokens * (16 * nb + align16(nb));
-  if ((st = check_workspace(workspace, workspace_bytes, own + zsm::mx_matmul_workspace(tokens, w->rows, w->cols, sms))) !=
-      ZERO_OK)
-    return st;
-  // the workspace: x's codes, its scales, the product's own part
+  const int64_t own = linear_own(tokens, w->cols);
   uint8_t* at = static_cast<uint8_t*>(workspace);
-  const zero_mx4 xq = {at, at + tokens * 16 * nb, tokens, w->cols, 16 * nb, align16(nb)};
+  const zero_mx4 xq = quantised_x(at, tokens, w->cols);
+  st = check_workspace(workspace, workspace_bytes, own + zsm::mx_matmul_workspace(matrix(xq), matrix(*w)));
+  if (st != ZERO_OK) return st;
   st = zero_mx4_quantize(x, dtype, tokens, w->cols, ld, ZERO_MX4_NEAREST, 0, &xq, nullptr, stream);
   if (st != ZERO_OK) return st;
   return matmul(xq, *w, y, y_dtype, ld_y, at + own, 1, sms, s);

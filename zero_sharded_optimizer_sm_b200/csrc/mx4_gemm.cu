@@ -8,12 +8,19 @@
 // are filled by b's).  A k tile is 256 elements: one 128-byte swizzled row of
 // codes and 8 scale bytes per matrix row, four instructions of 64 elements.
 //
-// Roles of a CTA's warps: 0 loads codes (TMA); 1 copies scales from shared
-// memory into TMEM and issues the products; 4-7 read the accumulator and
-// store; 8-11 load scales.  The scales lie in memory one row after another,
-// and the tensor core wants, for each 128 rows and 128 k elements, a 512-byte
-// piece with row r's four bytes at 16 (r % 32) + 4 (r / 32): a thread loads
-// 16 bytes of a row into registers and stores four words at their places.
+// Roles of a CTA's warps: 0 loads codes and scales (TMA); 1 issues the
+// products; 4-7 read the accumulator and store; 8-11 bring scales into TMEM.
+//
+// Scales: the tensor core wants the four scale bytes that row r has for 128 k
+// elements in lane r % 32 of every 32 lanes, column r / 32.  They come two k
+// tiles (16 bytes of a row) at a time through shared memory, either as they
+// lie -- 16 bytes of each of 128 rows, where the rows are 16-byte aligned --
+// or, where they are not, from a workspace in which a small kernel has put
+// the words in that order (scale pieces).  Each of the four warps then writes
+// the same words to its own lanes, from registers: the copy instruction that
+// would take them from shared memory runs in turn with the products, 58
+// cycles for 512 bytes, 350 cycles a k tile of 256 x 256 beside the products'
+// 512.
 //
 // Few tiles and a long k: a cluster of up to 8 CTAs splits k, each CTA sends
 // the columns another one owns into that one's shared memory, and the owner
@@ -42,34 +49,31 @@ constexpr int kLanes = 128;            // rows of P in a tile
 constexpr int kTileK = 256;            // elements of k in a stage
 constexpr int kTileKBytes = kTileK / 2;
 constexpr int kThreadsMm = 384;
-constexpr int kLoaderWarps = 4;
+constexpr int kScaleWarps = 4;
 
 __device__ unsigned g_mx_error;        // a bounded wait that ran out (zero_mx4_check)
 
 struct MmArgs {
-  const uint8_t* p_scales;
-  const uint8_t* q_scales;
-  int64_t p_scale_pitch, q_scale_pitch;
-  int p_rows, q_rows, k_blocks, k_tiles;
-  int p_align, q_align;  // 16, 8, 4 or 1: alignment of that operand's scale rows
+  int p_rows, q_rows, k_tiles;
+  int p_pieces, q_pieces;  // 1: that operand's scales come as pieces
   int p_tiles, n_tiles, split;
   void* out;
   int64_t p_stride, q_stride;  // elements between rows of P / of Q in the result
   int type, vec;               // vec: 32-byte stores along q are aligned
-  int pdl;
+  int pdl;                     // launched early: the grid before this one writes (some of) the operands,
+  int p_early;                 //   but not P and its scales
 };
 
-__host__ __device__ constexpr int q_chunks(int bn) { return (bn + 127) / 128; }
-// Bytes of one stage: codes of both operands, scale pieces of both (two per
-// 128 rows), rounded up to the 1024 bytes a swizzled tile starts on.
-__host__ __device__ constexpr int stage_codes(int bn) { return (kLanes + bn) * kTileKBytes; }
-__host__ __device__ constexpr int stage_scales(int bn) { return 1024 * (1 + q_chunks(bn)); }
-__host__ __device__ constexpr int stage_bytes(int bn) { return stage_codes(bn) + stage_scales(bn); }
-// TMEM columns: the accumulator, then two sets of scales used by turns.
-__host__ __device__ constexpr int scale_cols(int bn) { return 8 * (1 + q_chunks(bn)); }
+// A stage: the codes of both operands for one k tile.  A group of scales: 16
+// bytes for each row (up to 128 of P, then of Q) for two k tiles.
+__host__ __device__ constexpr int stage_bytes(int bn) { return (kLanes + bn) * kTileKBytes; }
+constexpr int kGroup = 2048;  // of 128 rows
+// TMEM columns: the accumulator, then four sets of scales used by turns.
+constexpr int kSets = 4;
+constexpr int kScaleCols = 16;
 __host__ __device__ constexpr int acc_cols(int bn) { return bn < 32 ? 32 : bn; }
 __host__ __device__ constexpr int tmem_cols(int bn) {
-  int need = acc_cols(bn) + 2 * scale_cols(bn), n = 32;
+  int need = acc_cols(bn) + kSets * kScaleCols, n = 32;
   while (n < need) n *= 2;
   return n;
 }
@@ -95,17 +99,10 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, int cols) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Shared-memory descriptors: a K-major tile of 128-byte swizzled rows (groups
-// of 8 rows 1024 bytes apart), and 32 unswizzled rows of 16 bytes (groups of
-// 8 rows 128 bytes apart).
+// Shared-memory descriptor of a K-major tile of 128-byte swizzled rows
+// (groups of 8 rows 1024 bytes apart).
 __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
-}
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
 // Instruction descriptor: both operands 4-bit (format 1), scales a power of
@@ -169,18 +166,9 @@ __device__ __forceinline__ uint32_t address_in(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-// mbar_try_wait for a barrier on which the other CTA's threads arrive too.
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+// An arrival on a barrier of either CTA, in order at CTA scope: what it
+// announces is in TMEM, ordered by the tcgen05 fences.  (Release at cluster
+// scope cost 1900 cycles an arrival.)
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -189,16 +177,20 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
 // Bounded by the SM's own clock: a read of the global timer takes about a
 // microsecond, which would be added to every wait that has to poll.
 constexpr long long kWaitCycles = 4000000000ll;  // two seconds at 2 GHz
-template <bool kCluster>
 __device__ __forceinline__ int wait_bounded(uint64_t* bar, unsigned parity, volatile int* abort_flag) {
-  auto done = [&] { return kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-  if (done()) return 0;
+  if (mbar_try_wait(bar, parity)) return 0;
   const long long t0 = clock64();
-  while (!done()) {
+  while (!mbar_try_wait(bar, parity)) {
     if (*abort_flag) return 2;
     if (clock64() - t0 > kWaitCycles) return 1;
   }
   return 0;
+}
+// Long enough for every copy in flight to have landed (after a failed wait only).
+__device__ __forceinline__ void linger() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < 40000000ll) {
+  }
 }
 
 // N consecutive accumulator columns of this warp's 32 lanes.
@@ -232,19 +224,21 @@ __device__ __forceinline__ void tmem_read(uint32_t addr, float (&v)[N]) {
   for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 24 consecutive columns of this warp's 32 lanes, from registers.
-__device__ __forceinline__ void tmem_write24(uint32_t addr, const uint4 (&v)[6]) {
+// 16 or 8 consecutive columns of this warp's 32 lanes, from registers.
+__device__ __forceinline__ void tmem_write16(uint32_t addr, const uint4 (&v)[4]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16};" ::"r"(addr),
       "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w),
       "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
       : "memory");
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr + 16),
-               "r"(v[4].x), "r"(v[4].y), "r"(v[4].z), "r"(v[4].w), "r"(v[5].x), "r"(v[5].y), "r"(v[5].z), "r"(v[5].w)
-               : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_write8(uint32_t addr, const uint4 (&v)[2]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+               "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_write() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -312,136 +306,119 @@ __device__ __forceinline__ void store_run(const MmArgs& a, int64_t p, int64_t q,
     if (q + i < a.q_rows) store_one(a, at + i * a.q_stride, v[i]);
 }
 
-// ------------------------------------------------------------ scale loader --
+// ------------------------------------------------------------------ scales --
 
-// 16 scale bytes (two k tiles) of a row of which the first n exist (the
-// others are 0).  Words: rows 4-byte aligned and n a multiple of 4; every
-// load is predicated and none sits in a branch, whose end would wait for it.
-template <bool kWords>
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, int align) {
-  if constexpr (kWords) {
-    const bool all = align == 16 && n >= 16;
-    const bool lo = !all && align >= 8 && n >= 8, hi = !all && align >= 8 && n >= 16;
-    const bool w0 = !all && !lo && n >= 4, w1 = !all && !lo && n >= 8;
-    const bool w2 = !all && !hi && n >= 12, w3 = !all && !hi && n >= 16;
-    uint4 r;
-    asm volatile(
-        "{\n\t.reg .pred q, l, h, a, b, c, d;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 l, %6, 0;\n\tsetp.ne.b32 h, %7, 0;\n\t"
-        "setp.ne.b32 a, %8, 0;\n\tsetp.ne.b32 b, %9, 0;\n\tsetp.ne.b32 c, %10, 0;\n\tsetp.ne.b32 d, %11, 0;\n\t"
-        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-        "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t"
-        "@l ld.global.v2.b32 {%0, %1}, [%4];\n\t"
-        "@h ld.global.v2.b32 {%2, %3}, [%4 + 8];\n\t"
-        "@a ld.global.b32 %0, [%4];\n\t"
-        "@b ld.global.b32 %1, [%4 + 4];\n\t"
-        "@c ld.global.b32 %2, [%4 + 8];\n\t"
-        "@d ld.global.b32 %3, [%4 + 12];\n\t}"
-        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
-        : "l"(p), "r"((int)all), "r"((int)lo), "r"((int)hi), "r"((int)w0), "r"((int)w1), "r"((int)w2), "r"((int)w3)
-        : "memory");
-    return r;
-  } else {
+// The four TMEM columns (rows lane, lane + 32, lane + 64, lane + 96) of half c
+// of k tile h of a group, for a lane: from rows as they lie, m[j] holds row
+// lane + 32 j's 16 bytes; from pieces, m[2 h + c] the four rows' words.
+struct ScaleGroup {
+  uint4 m[4];
+  __device__ __forceinline__ void load(const uint8_t* group, int lane, bool pieces, int rows) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m[j] = pieces || lane + 32 * j < rows ? *reinterpret_cast<const uint4*>(group + 16 * lane + 512 * j)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+    if (!pieces) {  // words [row][k] to [k][row]
+      const uint4 r0 = m[0], r1 = m[1], r2 = m[2], r3 = m[3];
+      m[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
+      m[1] = make_uint4(r0.y, r1.y, r2.y, r3.y);
+      m[2] = make_uint4(r0.z, r1.z, r2.z, r3.z);
+      m[3] = make_uint4(r0.w, r1.w, r2.w, r3.w);
+    }
+  }
+};
+
+// The same for the BN rows that start at row `part` (a multiple of BN) of a
+// 128-row piece: row part + lane + 32 j's words lie where its row number says.
+template <int BN>
+__device__ __forceinline__ void load_part(ScaleGroup& g, const uint8_t* piece, int lane, int part) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (n > j) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < (BN + 31) / 32; ++j) {
+      const int r = part + lane + 32 * j;
+      if (lane + 32 * j < BN)
+        w[j] = *reinterpret_cast<const uint32_t*>(piece + 512 * k + 16 * (r & 31) + 4 * (r >> 5));
+    }
+    g.m[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-__device__ __forceinline__ void st_word(uint32_t addr, uint32_t w) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
-}
+// Scales in the order above: 2048 bytes for each 128 rows and two k tiles,
+// row r's byte for block b of the 16 at 512 (b / 4) + 16 (r % 32) +
+// 4 (r / 32 % 4) + b % 4; 0 past the matrix (the codes there are 0 too, but a
+// product with a NaN scale would not be).  A warp takes 32 rows and two k
+// tiles, a lane a row.
+struct PieceArgs {
+  const uint8_t* scales[2];
+  int64_t pitch[2];
+  int rows[2];
+  uint8_t* out[2];
+  int warps0, warps;  // 32-row parts of the first operand, of both
+  int k_blocks, groups;
+  int pdl;
+};
 
-// A loader thread's whole run: the scale bytes of its R rows for every k tile
-// of every tile, in order.  The loads are kAhead times two k tiles ahead of
-// the stores (their latency under a full load of code copies is several k
-// tiles long).  rows(tile, ptr) gives the R rows' starts (null: no such row),
-// put(w) stores one k tile's two words of each row when its stage is free,
-// and says whether to go on.  One warp's instructions between two k tiles
-// are what bounds this, so everything that depends on the tile alone is kept.
-template <int R, int kAhead, bool kWords, class Rows, class Put>
-__device__ __forceinline__ void stream_scales(int first, int step, int n_tiles, int k0, int k1, int k_blocks, int align,
-                                              Rows rows, Put put) {
-  if (k0 >= k1 || first >= n_tiles) return;
-  uint4 ring[kAhead][R];
-  const uint8_t* ptr[R];
-  int next = first, next_kt = k0;  // what is fetched next
-  if (k0 & 1) align = min(align, 8);
-  rows(first, ptr);
-  auto fetch_next = [&](uint4 (&r)[R]) {
-    if (next >= n_tiles) return;
-    const int n = k_blocks - 8 * next_kt;
+__global__ void __launch_bounds__(256) mx_scale_pieces_kernel(const __grid_constant__ PieceArgs a) {
+  if (a.pdl) dev::pdl_wait();
+  const int lane = threadIdx.x & 31;
+  int w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (w >= a.warps) return;
+  const int o = w >= a.warps0 ? 1 : 0;
+  if (o) w -= a.warps0;
+  const int g = w % a.groups, r32 = w / a.groups;
+  const int64_t row = 32ll * r32 + lane;
+  const int n = row < a.rows[o] ? min(a.k_blocks - 16 * g, 16) : 0;
+  const uint8_t* p = a.scales[o] + (n > 0 ? row * a.pitch[o] + 16 * g : 0);
+  uint32_t v[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int j = 0; j < R; ++j)
-      r[j] = load_scales<kWords>(ptr[j] + 8 * next_kt, ptr[j] ? n : 0, align);
-    next_kt += 2;
-    if (next_kt >= k1) {
-      next_kt = k0;
-      next += step;
-      if (next < n_tiles) rows(next, ptr);
-    }
-  };
+  for (int j = 0; j < 16; ++j)
+    if (j < n) v[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  uint8_t* out = a.out[o] + ((int64_t)(r32 >> 2) * a.groups + g) * kGroup + 16 * lane + 4 * (r32 & 3);
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) fetch_next(ring[u]);
-  int tile = first, kt = k0;
-  while (true) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      uint2 w[R];
-      uint4 now[R];
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        now[j] = ring[u][j];
-        w[j] = make_uint2(now[j].x, now[j].y);
-      }
-      fetch_next(ring[u]);
-      if (!put(w)) return;
-      if (kt + 1 < k1) {
-#pragma unroll
-        for (int j = 0; j < R; ++j) w[j] = make_uint2(now[j].z, now[j].w);
-        if (!put(w)) return;
-      }
-      kt += 2;
-      if (kt >= k1) {
-        kt = k0;
-        tile += step;
-        if (tile >= n_tiles) return;
-      }
-    }
-  }
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(out + 512 * j) = v[j];
 }
 
 // ------------------------------------------------------------------ kernel --
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, int GROUPS>
 struct Shared {
   uint64_t codes_full[STAGES], scales_full[STAGES], empty[STAGES];
+  uint64_t group_full[GROUPS], group_empty[GROUPS];
   uint64_t acc_full, acc_empty, drained;
   uint32_t tmem;
   int abort;
+  static_assert(kSets <= STAGES, "a set is written again after its stage's products");
 };
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, int GROUPS>
 __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                     const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
                      const __grid_constant__ MmArgs a) {
   extern __shared__ uint8_t raw_smem[];
-  __shared__ Shared<BN, STAGES> sh;
-  constexpr int kQ = q_chunks(BN);
+  __shared__ Shared<BN, STAGES, GROUPS> sh;
   constexpr int kStage = stage_bytes(BN);
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+  uint8_t* group_smem = smem + STAGES * kStage;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
-  const int k0 = (int)((int64_t)a.k_tiles * rank / a.split), k1 = (int)((int64_t)a.k_tiles * (rank + 1) / a.split);
+  // this CTA's k tiles: whole groups
+  const int groups = (a.k_tiles + 1) / 2;
+  const int g0 = (int)((int64_t)groups * rank / a.split), g1 = (int)((int64_t)groups * (rank + 1) / a.split);
+  const int k0 = 2 * g0, k1 = min(2 * g1, a.k_tiles);
   const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&sh.codes_full[s], 1);
-      mbar_init(&sh.scales_full[s], kLoaderWarps);
+      mbar_init(&sh.scales_full[s], kScaleWarps);
       mbar_init(&sh.empty[s], 1);
+    }
+    for (int g = 0; g < GROUPS; ++g) {
+      mbar_init(&sh.group_full[g], 1);
+      mbar_init(&sh.group_empty[g], kScaleWarps);
     }
     mbar_init(&sh.acc_full, 1);
     mbar_init(&sh.acc_empty, 4);
@@ -456,63 +433,103 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
-    const int r = wait_bounded<false>(bar, parity, abort_flag);
+    const int r = wait_bounded(bar, parity, abort_flag);
     if (r == 1) {
       *abort_flag = 1;
       atomicOr(&g_mx_error, 1u);
     }
     return r == 0;
   };
-  if (a.pdl) dev::pdl_wait();
 
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0;
+      // P's part of a stage or group and Q's: the first ones of P go out
+      // before the wait for the grid that writes Q.
+      auto load_codes = [&](bool p, int tile, int kt, int s) {
+        uint8_t* st = smem + s * kStage;
+        if (p) tma_load_2d(st, &p_map, kt * kTileKBytes, (tile % a.p_tiles) * kLanes, &sh.codes_full[s]);
+        else tma_load_2d(st + kLanes * kTileKBytes, &q_map, kt * kTileKBytes, (tile / a.p_tiles) * BN, &sh.codes_full[s]);
+      };
+      auto load_group = [&](bool p, int tile, int g, int s) {
+        uint8_t* to = group_smem + s * 2 * kGroup + (p ? 0 : kGroup);
+        const CUtensorMap* map = p ? &ps_map : &qs_map;
+        const int row = p ? (tile % a.p_tiles) * kLanes : (tile / a.p_tiles) * BN;
+        if (p ? a.p_pieces : a.q_pieces)  // Q's 128-row pieces: BN divides 128, see q_part
+          tma_load_2d(to, map, 0, 2 * ((row / kLanes) * groups + g), &sh.group_full[s]);
+        else tma_load_2d(to, map, 16 * g, row, &sh.group_full[s]);
+      };
+      const int q_bytes = a.q_pieces ? kGroup : 16 * BN;
+      const int early = a.pdl && a.p_early && first < a.n_tiles ? min(k1 - k0, STAGES) : 0;
+      const int early_groups = min((early + 1) / 2, GROUPS);
+      for (int j = 0; j < early; ++j) {
+        if (j % 2 == 0 && j / 2 < early_groups) {
+          mbar_expect_tx(&sh.group_full[j / 2], kGroup + q_bytes);
+          load_group(true, first, g0 + j / 2, j / 2);
+        }
+        mbar_expect_tx(&sh.codes_full[j], stage_bytes(BN));
+        load_codes(true, first, k0 + j, j);
+      }
+      if (a.pdl) dev::pdl_wait();
+      int it = 0, s = 0, gt = 0, gs = 0;
+      unsigned parity = 1, gparity = 1;
       bool ok = true;
       for (int tile = first; tile < a.n_tiles && ok; tile += step) {
-        const int p0 = (tile % a.p_tiles) * kLanes, q0 = (tile / a.p_tiles) * BN;
-        for (int kt = k0; kt < k1; ++kt, ++it) {
-          const int s = it % STAGES;
-          if (it >= STAGES && !(ok = wait(&sh.empty[s], ((it / STAGES) - 1) & 1))) break;
-          uint8_t* st = smem + s * kStage;
-          mbar_expect_tx(&sh.codes_full[s], (kLanes + BN) * kTileKBytes);
-          tma_load_2d(st, &p_map, kt * kTileKBytes, p0, &sh.codes_full[s]);
-          tma_load_2d(st + kLanes * kTileKBytes, &q_map, kt * kTileKBytes, q0, &sh.codes_full[s]);
+        for (int kt = k0; kt < k1; ++kt) {
+          if (((kt - k0) & 1) == 0) {
+            if (gt >= GROUPS && !(ok = wait(&sh.group_empty[gs], gparity))) break;
+            fence_proxy_async_smem();  // the scale warps' reads of the group, before it is written again
+            if (gt >= early_groups) {
+              mbar_expect_tx(&sh.group_full[gs], kGroup + q_bytes);
+              load_group(true, tile, kt / 2, gs);
+            }
+            load_group(false, tile, kt / 2, gs);
+            ++gt;
+            if (++gs == GROUPS) {
+              gs = 0;
+              gparity ^= 1;
+            }
+          }
+          if (it >= STAGES && !(ok = wait(&sh.empty[s], parity))) break;
+          if (it >= early) {
+            mbar_expect_tx(&sh.codes_full[s], stage_bytes(BN));
+            load_codes(true, tile, kt, s);
+          }
+          load_codes(false, tile, kt, s);
+          ++it;
+          if (++s == STAGES) {
+            s = 0;
+            parity ^= 1;
+          }
         }
       }
-      if (!ok)  // the copies in flight land before the CTA may end
-        for (int j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-          mbar_wait(&sh.codes_full[j % STAGES], (j / STAGES) & 1);
+      if (!ok) linger();  // the copies in flight land before the CTA may end
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      int it = 0, n = 0;
+      int it = 0, n = 0, s = 0;
+      unsigned parity = 0;
       bool ok = true, issued = false;
+      const uint32_t base = smem_u32(smem);
       for (int tile = first; tile < a.n_tiles && ok; tile += step, ++n) {
         if (n > 0 && !(ok = wait(&sh.acc_empty, (n - 1) & 1))) break;
         fence_after();
         for (int kt = k0; kt < k1; ++kt, ++it) {
-          const int s = it % STAGES;
-          if (!(ok = wait(&sh.codes_full[s], (it / STAGES) & 1))) break;
-          if (!(ok = wait(&sh.scales_full[s], (it / STAGES) & 1))) break;
+          if (!(ok = wait(&sh.codes_full[s], parity))) break;
+          if (!(ok = wait(&sh.scales_full[s], parity))) break;
           fence_after();
-          const uint32_t base = smem_u32(smem + s * kStage);
-          const uint32_t scales = base + stage_codes(BN);
-          const uint32_t ts = tmem + acc_cols(BN) + (it & 1) * scale_cols(BN);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            copy_scales(ts + 4 * c, scale_desc(scales + 512 * c));
-#pragma unroll
-            for (int q = 0; q < kQ; ++q)
-              copy_scales(ts + 8 + 4 * (c * kQ + q), scale_desc(scales + 1024 + 512 * (c * kQ + q)));
-          }
-          const uint64_t pd = tile_desc(base), qd = tile_desc(base + kLanes * kTileKBytes);
+          const uint32_t at = base + s * kStage;
+          const uint32_t ts = tmem + acc_cols(BN) + (it % kSets) * kScaleCols;
+          const uint64_t pd = tile_desc(at), qd = tile_desc(at + kLanes * kTileKBytes);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma(tmem, pd + 2 * j, qd + 2 * j, inst_desc(BN, (j & 1) * 2), ts + 4 * (j >> 1), ts + 8 + 4 * kQ * (j >> 1),
+            mma(tmem, pd + 2 * j, qd + 2 * j, inst_desc(BN, (j & 1) * 2), ts + 4 * (j >> 1), ts + 8 + 4 * (j >> 1),
                 kt > k0 || j > 0);
           issued = true;
           mma_commit(&sh.empty[s]);
+          if (++s == STAGES) {
+            s = 0;
+            parity ^= 1;
+          }
         }
         if (ok) mma_commit(&sh.acc_full);
       }
@@ -522,43 +539,48 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
       }
     }
   } else if (warp >= 8) {
-    // thread t: row t of P and rows t (and t + 128) of Q
-    const int t = threadIdx.x - 256;  // 0..127
-    const uint32_t at = 16u * (t & 31) + 4u * (t >> 5);
-    int st = 0, turn = 0;  // the stage and whether it has been used before
-    unsigned parity = 1;
-    auto rows = [&](int tile, const uint8_t* (&ptr)[1 + kQ]) {
-      const int64_t p = (int64_t)(tile % a.p_tiles) * kLanes + t, q = (int64_t)(tile / a.p_tiles) * BN + t;
-      ptr[0] = p < a.p_rows ? a.p_scales + p * a.p_scale_pitch : nullptr;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp - 8)) << 16) + acc_cols(BN);
+    int it = 0, s = 0, gs = 0, old = 0;  // old: the stage whose products used this set of scales before
+    unsigned gparity = 0, parity_old = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.n_tiles && ok; tile += step) {
+      // Q's rows start inside a piece of 128 when BN is less: q_part turns lane + 32 j into them
+      const int q_part = a.q_pieces ? (tile / a.p_tiles) * BN % kLanes : 0;
+      for (int kt = k0; kt < k1 && ok; kt += 2) {
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity)))) break;
+        ScaleGroup p, q;
+        const uint8_t* group = group_smem + gs * 2 * kGroup;
+        p.load(group, lane, a.p_pieces, kLanes);
+        if (!a.q_pieces || BN == kLanes) q.load(group + kGroup, lane, a.q_pieces, BN);
+        else load_part<BN>(q, group + kGroup, lane, q_part);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
+        if (++gs == GROUPS) {
+          gs = 0;
+          gparity ^= 1;
+        }
 #pragma unroll
-      for (int j = 0; j < kQ; ++j)
-        ptr[1 + j] = q + 128 * j < a.q_rows && t + 128 * j < BN ? a.q_scales + (q + 128 * j) * a.q_scale_pitch : nullptr;
-    };
-    auto put = [&](const uint2 (&w)[1 + kQ]) {
-      if (turn && !__all_sync(0xFFFFFFFFu, wait(&sh.empty[st], parity))) return false;
-      const uint32_t dst = smem_u32(smem) + st * kStage + stage_codes(BN) + at;
-#pragma unroll
-      for (int j = 0; j < 1 + kQ; ++j) {
-        const uint32_t to = dst + (j == 0 ? 0 : 1024 + 512 * (j - 1));
-        st_word(to, w[j].x);
-        st_word(to + (j == 0 ? 512 : 512 * kQ), w[j].y);
+        for (int h = 0; h < 2; ++h) {
+          if (kt + h >= k1) break;
+          if (it >= kSets) {
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.empty[old], parity_old)))) break;
+            if (++old == STAGES) {
+              old = 0;
+              parity_old ^= 1;
+            }
+          }
+          fence_after();
+          const uint4 v[4] = {p.m[2 * h], p.m[2 * h + 1], q.m[2 * h], q.m[2 * h + 1]};
+          tmem_write16(ts + (it % kSets) * kScaleCols, v);
+          tmem_wait_write();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.scales_full[s]);
+          ++it;
+          if (++s == STAGES) s = 0;
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.scales_full[st]);
-      if (++st == STAGES) {
-        st = 0;
-        turn = 1;
-        parity ^= 1;
-      }
-      return true;
-    };
-    const int align = min(a.p_align, a.q_align);
-    constexpr int kAhead = BN <= 64 ? 2 : 4;
-    if (align >= 4 && a.k_blocks % 4 == 0)
-      stream_scales<1 + kQ, kAhead, true>(first, step, a.n_tiles, k0, k1, a.k_blocks, align, rows, put);
-    else
-      stream_scales<1 + kQ, 1, false>(first, step, a.n_tiles, k0, k1, a.k_blocks, align, rows, put);
+    }
   } else if (warp >= 4 && a.split == 1) {
     const int w = warp - 4;
     int n = 0;
@@ -567,7 +589,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
       fence_after();
       const int64_t p = (int64_t)(tile % a.p_tiles) * kLanes + 32 * w + lane, q0 = (int64_t)(tile / a.p_tiles) * BN;
       constexpr int kStep = BN < 32 ? 8 : 32;
-      for (int c = 0; c < BN; c += kStep) {
+      for (int c = 0; c < BN && q0 + c < a.q_rows; c += kStep) {
         float v[kStep];
         tmem_read<kStep>(tmem + ((uint32_t)(32 * w) << 16) + c, v);
         store_run<kStep>(a, p, q0 + c, v);
@@ -579,10 +601,11 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
   }
 
   if (a.split > 1) {
-    // Column c of the tile belongs to rank c / own; its part from rank r goes
-    // to that rank's [r][c % own][lane], in the stages' memory, which every
-    // CTA of the cluster has finished with after the first barrier.
-    const int own = (BN + a.split - 1) / a.split;
+    // Column c of the tile belongs to rank c / own (own = BN / split, a power
+    // of two); its part from rank r goes to that rank's [r][c % own][lane], in
+    // the stages' memory, which every CTA of the cluster has finished with
+    // after the first barrier.
+    const int shift = __ffs(BN / a.split) - 1, own = 1 << shift;
     const int w = warp - 4;
     bool ok = true;
     if (warp >= 4 && warp < 8) {
@@ -593,27 +616,25 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     cluster_sync();
     if (warp >= 4 && warp < 8 && ok) {
       constexpr int kStep = BN < 32 ? 8 : 32;
-      const uint32_t base = smem_u32(smem);
+      const uint32_t base = smem_u32(smem) + 4u * (rank * own * kLanes + 32 * w + lane);
       for (int c = 0; c < BN; c += kStep) {
         float v[kStep];
         tmem_read<kStep>(tmem + ((uint32_t)(32 * w) << 16) + c, v);
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) {
-          const uint32_t to = (uint32_t)(c + i) / own, at = (uint32_t)(c + i) % own;
-          store_remote(base + 4u * ((rank * own + at) * kLanes + 32 * w + lane), to, v[i]);
-        }
+        for (int i = 0; i < kStep; ++i)
+          store_remote(base + 4u * kLanes * ((c + i) & (own - 1)), (uint32_t)(c + i) >> shift, v[i]);
       }
     }
     __syncwarp();
     cluster_sync();
     if (warp >= 4 && warp < 8) {
-      const float* part = reinterpret_cast<const float*>(smem);
+      const float* part = reinterpret_cast<const float*>(smem) + 32 * w + lane;
       const int64_t p = (int64_t)(first % a.p_tiles) * kLanes + 32 * w + lane, q0 = (int64_t)(first / a.p_tiles) * BN;
       for (int i = 0; i < own; ++i) {
         const int c = rank * own + i;
-        if (c >= BN || p >= a.p_rows || q0 + c >= a.q_rows) continue;
-        float v = part[i * kLanes + 32 * w + lane];
-        for (int r = 1; r < a.split; ++r) v = __fadd_rn(v, part[(r * own + i) * kLanes + 32 * w + lane]);
+        if (p >= a.p_rows || q0 + c >= a.q_rows) break;
+        float v = part[i * kLanes];
+        for (int r = 1; r < a.split; ++r) v = __fadd_rn(v, part[(r * own + i) * kLanes]);
         store_one(a, p * a.p_stride + (q0 + c) * a.q_stride, v);
       }
     }
@@ -632,25 +653,14 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
 // into each SM where a CTA alone (128 x 256) would need 48.  Every CTA keeps
 // the scales of its own rows of P and of all 256 rows of Q.
 //
-// The scales come in the tensor core's order, from a workspace that
-// mx_scale_pieces_kernel filled: the 1024 bytes of 128 rows and one k tile
-// lie together, one row of the tensor map s_map.  (Warps
-// that gather them from the rows while the products run could not keep up:
-// 1900 cycles a k tile, of which the products need 512.)
-//
-// From the stage four warps of each CTA carry them on to TMEM (a thread's 16
-// bytes of a piece are its lane's four columns).  The tensor core's own copy
-// instruction takes 58 cycles for each 512 bytes in turn with the products:
-// 350 cycles a k tile beside their 512.
-//
 // Two accumulators of 256 columns share 96 of TMEM's 512 with each other
 // (the rest holds four sets of scales): the epilogue empties the shared
 // columns first and lets the next tile start, then the others while it runs.
 constexpr int kPairN = 256;
 constexpr int kPairStages = 6;
 constexpr int kPairCodes = 2 * kLanes * kTileKBytes;     // per CTA
-constexpr int kPieces = 1024;                            // scale bytes of 128 rows and one k tile
-constexpr int kPairStage = kPairCodes + 3 * kPieces;     // per CTA
+constexpr int kPairGroups = 3;
+constexpr int kPairGroup = 3 * kGroup;                   // per CTA: 128 rows of P, 256 of Q
 constexpr int kPairThreads = 384;
 constexpr int kPairSets = 4;
 constexpr int kPairScaleCols = 24;
@@ -661,7 +671,8 @@ static_assert(kPairShared % 16 == 0 && kPairShared > 0, "the epilogue's order");
 static_assert(kPairSets <= kPairStages, "a set is written again after its stage's products");
 
 struct PairShared {
-  uint64_t full[kPairStages], pieces_full[kPairStages], scales_full[kPairStages], empty[kPairStages];
+  uint64_t full[kPairStages], scales_full[kPairStages], empty[kPairStages];
+  uint64_t group_full[kPairGroups], group_empty[kPairGroups];
   uint64_t acc_full[2], acc_empty, drained;
   uint32_t tmem;
   int abort;
@@ -669,20 +680,26 @@ struct PairShared {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_matmul_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
-                          const __grid_constant__ CUtensorMap s_map, const __grid_constant__ MmArgs a) {
+                          const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
+                          const __grid_constant__ MmArgs a) {
   extern __shared__ uint8_t raw_smem[];
   __shared__ PairShared sh;
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
+  uint8_t* group_smem = smem + kPairStages * kPairCodes;
+  const int groups = (a.k_tiles + 1) / 2;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.pieces_full[s], 1);
       mbar_init(&sh.scales_full[s], 8);
       mbar_init(&sh.empty[s], 1);
+    }
+    for (int g = 0; g < kPairGroups; ++g) {
+      mbar_init(&sh.group_full[g], 1);
+      mbar_init(&sh.group_empty[g], kScaleWarps);
     }
     mbar_init(&sh.acc_full[0], 1);
     mbar_init(&sh.acc_full[1], 1);
@@ -699,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
-    const int r = wait_bounded<true>(bar, parity, abort_flag);
+    const int r = wait_bounded(bar, parity, abort_flag);
     if (r == 1) {
       *abort_flag = 1;
       atomicOr(&g_mx_error, 1u);
@@ -713,20 +730,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int it = 0, s = 0;
       unsigned parity = 1;
       bool ok = true;
-      const uint32_t full = address_in(&sh.full[0], 0), mine = address_in(&sh.pieces_full[0], rank);
+      const uint32_t full = address_in(&sh.full[0], 0), mine = address_in(&sh.group_full[0], rank);
+      int gt = 0, gs = 0;
+      unsigned gparity = 1;
+      auto load_group = [&](uint8_t* to, const CUtensorMap* map, int pieces, int block, int g, uint32_t bar) {
+        if (pieces) tma_load_2d_pair(to, map, 0, 2 * (block * groups + g), bar);
+        else tma_load_2d_pair(to, map, 16 * g, block * kLanes, bar);
+      };
       for (int tile = first; tile < a.n_tiles && ok; tile += step) {
         const int pb = (tile % a.p_tiles) * 2, qb = (tile / a.p_tiles) * 2;  // blocks of 128 rows
-        const int py = (pb + rank) * a.k_tiles, qy = (2 * a.p_tiles + qb) * a.k_tiles;  // their rows in s_map
         for (int kt = 0; kt < a.k_tiles; ++kt) {
+          if ((kt & 1) == 0) {
+            if (gt >= kPairGroups && !(ok = wait(&sh.group_empty[gs], gparity))) break;
+            fence_proxy_async_smem();  // the scale warps' reads of the group, before it is written again
+            mbar_expect_tx(&sh.group_full[gs], kPairGroup);
+            uint8_t* to = group_smem + gs * kPairGroup;
+            load_group(to, &ps_map, a.p_pieces, pb + rank, kt / 2, mine + 8 * gs);
+            load_group(to + kGroup, &qs_map, a.q_pieces, qb, kt / 2, mine + 8 * gs);
+            load_group(to + 2 * kGroup, &qs_map, a.q_pieces, qb + 1, kt / 2, mine + 8 * gs);
+            ++gt;
+            if (++gs == kPairGroups) {
+              gs = 0;
+              gparity ^= 1;
+            }
+          }
           if (it >= kPairStages && !(ok = wait(&sh.empty[s], parity))) break;
-          fence_proxy_async_smem();  // the scale warps' reads of the stage, before it is written again
-          uint8_t* st = smem + s * kPairStage;
+          uint8_t* st = smem + s * kPairCodes;
           if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * kPairCodes);
-          mbar_expect_tx(&sh.pieces_full[s], 3 * kPieces);
-          uint8_t* sc = st + kPairCodes;
-          tma_load_2d_pair(sc, &s_map, 0, py + kt, mine + 8 * s);
-          tma_load_2d_pair(sc + kPieces, &s_map, 0, qy + kt, mine + 8 * s);
-          tma_load_2d_pair(sc + 2 * kPieces, &s_map, 0, qy + a.k_tiles + kt, mine + 8 * s);
           tma_load_2d_pair(st, &p_map, kt * kTileKBytes, (pb + rank) * kLanes, full + 8 * s);
           tma_load_2d_pair(st + kLanes * kTileKBytes, &q_map, kt * kTileKBytes, (qb + rank) * kLanes, full + 8 * s);
           ++it;
@@ -745,11 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           parity ^= 1;
         }
       }
-      if (!ok && it > 0) {  // the copies in flight land long before this has passed
-        const unsigned long long t0 = now_ns();
-        while (now_ns() - t0 < 20000000ull) {
-        }
-      }
+      if (!ok) linger();  // the copies in flight land before the CTA may end
     }
   } else if (warp == 1 && rank == 0) {
     if (lane == 0) {
@@ -765,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (!(ok = wait(&sh.full[s], parity))) break;
           if (!(ok = wait(&sh.scales_full[s], parity))) break;
           fence_after();
-          const uint32_t at = base + s * kPairStage;
+          const uint32_t at = base + s * kPairCodes;
           const uint64_t pd = tile_desc(at), qd = tile_desc(at + kLanes * kTileKBytes);
           const uint32_t ts = tmem + kPairScales + set * kPairScaleCols;
 #pragma unroll
@@ -811,41 +837,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       fence_before();
     }
   } else if (warp >= 8) {
-    const int w = warp - 8;
-    const int tiles = first < a.n_tiles ? (a.n_tiles - 1 - first) / step + 1 : 0;
-    const int64_t total = (int64_t)tiles * a.k_tiles;
     const uint32_t ready = address_in(&sh.scales_full[0], 0);
-    const uint32_t ts = tmem + ((uint32_t)(32 * w) << 16) + kPairScales;
-    int s = 0, set = 0, s_old = 0;  // s_old: the stage whose products used this set before
-    unsigned parity = 0, parity_old = 0;
-    for (int64_t it = 0; it < total; ++it) {
-      bool ok = wait(&sh.pieces_full[s], parity);
-      if (it >= kPairSets) {
-        ok = ok && wait(&sh.empty[s_old], parity_old);
-        if (++s_old == kPairStages) {
-          s_old = 0;
-          parity_old ^= 1;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp - 8)) << 16) + kPairScales;
+    int it = 0, s = 0, gs = 0, set = 0, old = 0;  // old: the stage whose products used this set before
+    unsigned gparity = 0, parity_old = 0;
+    bool ok = true;
+    for (int tile = first; tile < a.n_tiles && ok; tile += step) {
+      for (int kt = 0; kt < a.k_tiles && ok; kt += 2) {
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity)))) break;
+        ScaleGroup p, q, r;
+        const uint8_t* group = group_smem + gs * kPairGroup;
+        p.load(group, lane, a.p_pieces, kLanes);
+        q.load(group + kGroup, lane, a.q_pieces, kLanes);
+        r.load(group + 2 * kGroup, lane, a.q_pieces, kLanes);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
+        if (++gs == kPairGroups) {
+          gs = 0;
+          gparity ^= 1;
         }
-      }
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      fence_after();
-      const uint8_t* sc = smem + s * kPairStage + kPairCodes + 16 * lane;
-      // columns: P's two pieces, then Q's of rows 0-127 and 128-255 for each half of the k tile
-      uint4 v[6];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        v[c] = *reinterpret_cast<const uint4*>(sc + 512 * c);
-        v[2 + 2 * c] = *reinterpret_cast<const uint4*>(sc + kPieces + 512 * c);
-        v[3 + 2 * c] = *reinterpret_cast<const uint4*>(sc + 2 * kPieces + 512 * c);
-      }
-      tmem_write24(ts + set * kPairScaleCols, v);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_at(ready + 8 * s);
-      if (++set == kPairSets) set = 0;
-      if (++s == kPairStages) {
-        s = 0;
-        parity ^= 1;
+        for (int h = 0; h < 2; ++h) {
+          if (kt + h >= a.k_tiles) break;
+          if (it >= kPairSets) {
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.empty[old], parity_old)))) break;
+            if (++old == kPairStages) {
+              old = 0;
+              parity_old ^= 1;
+            }
+          }
+          fence_after();
+          // columns: P's for each half of the k tile, then Q's of rows 0-127 and 128-255 for each half
+          const uint4 v[4] = {p.m[2 * h], p.m[2 * h + 1], q.m[2 * h], r.m[2 * h]};
+          const uint4 w[2] = {q.m[2 * h + 1], r.m[2 * h + 1]};
+          tmem_write16(ts + set * kPairScaleCols, v);
+          tmem_write8(ts + set * kPairScaleCols + 16, w);
+          tmem_wait_write();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(ready + 8 * s);
+          ++it;
+          if (++set == kPairSets) set = 0;
+          if (++s == kPairStages) s = 0;
+        }
       }
     }
   }
@@ -854,46 +888,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();  // neither CTA ends while the other may still reach its memory
   fence_after();
   if (warp == 1) tmem_free_pair(tmem, 512);
-}
-
-// The scales of both operands in the pair kernel's order: 1024 bytes for each
-// 128 rows and k tile, row r's byte for block b of the tile at
-// 512 (b / 4) + 16 (r % 32) + 4 (r / 32 % 4) + b % 4; 0 past the matrix (the
-// codes there are 0 too, but a product with a NaN scale would not be).  A
-// warp takes 32 rows and one k tile, a lane a row.
-struct PieceArgs {
-  const uint8_t* scales[2];
-  int64_t pitch[2];
-  int rows[2], align[2];
-  uint8_t* out[2];
-  int warps0, warps;  // 32-row pieces of the first operand, of both
-  int k_blocks, k_tiles;
-};
-
-__global__ void __launch_bounds__(256) mx_scale_pieces_kernel(const __grid_constant__ PieceArgs a) {
-  dev::pdl_wait();
-  dev::pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  int w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= a.warps) return;
-  const int o = w >= a.warps0 ? 1 : 0;
-  if (o) w -= a.warps0;
-  const int kt = w % a.k_tiles, r32 = w / a.k_tiles;
-  const int64_t row = 32ll * r32 + lane;
-  const int n = row < a.rows[o] ? min(a.k_blocks - 8 * kt, 8) : 0;
-  const uint8_t* p = a.scales[o] + (n > 0 ? row * a.pitch[o] + 8 * kt : 0);
-  uint32_t v[2] = {0u, 0u};
-  if (a.align[o] >= 8 && n == 8) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    v[0] = x.x, v[1] = x.y;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) v[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-  }
-  uint8_t* out = a.out[o] + ((int64_t)(r32 >> 2) * a.k_tiles + kt) * kPieces + 16 * lane + 4 * (r32 & 3);
-  *reinterpret_cast<uint32_t*>(out) = v[0];
-  *reinterpret_cast<uint32_t*>(out + 512) = v[1];
 }
 
 // -------------------------------------------------------------------- host --
@@ -937,43 +931,56 @@ cudaError_t opt_in(K kernel, int bytes, std::atomic<uint64_t>& opted) {
   return e;
 }
 
-// A workspace of scale pieces as rows of 1024 bytes.
-bool pieces_map(CUtensorMap* map, uint8_t* pieces, int64_t rows) {
-  const cuuint64_t dims[2] = {kPieces / 4, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {kPieces};
-  const cuuint32_t box[2] = {kPieces / 4, 1}, one[2] = {1, 1};
-  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, pieces, dims, strides, box, one,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+// The scales as they lie -- boxes of 16 bytes of `rows` rows -- or, from a
+// workspace of pieces, boxes of one piece (two rows of 1024 bytes).
+bool scales_map(CUtensorMap* map, const MxMatrix& m, int rows, uint8_t* pieces, int64_t n_pieces) {
+  if (pieces) {
+    const cuuint64_t dims[2] = {kGroup / 8, (cuuint64_t)(2 * n_pieces)};
+    const cuuint64_t strides[1] = {kGroup / 2};
+    const cuuint32_t box[2] = {kGroup / 8, 2}, one[2] = {1, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, pieces, dims, strides, box, one,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)mx_blocks(m.cols), (cuuint64_t)m.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)m.scale_pitch};
+  const cuuint32_t box[2] = {16, (cuuint32_t)rows}, one[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.scales, dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int STAGES>
-cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, int sm_count, cudaStream_t s) {
-  CUtensorMap pm, qm;
-  if (!codes_map(&pm, p, kLanes) || !codes_map(&qm, q, BN)) return cudaErrorInvalidValue;
-  constexpr int kSmem = STAGES * stage_bytes(BN) + 1024;
-  static_assert(kSmem <= 227 * 1024 - 1024, "stages fit shared memory");
-  static_assert(STAGES * stage_bytes(BN) >= (BN + 8) * kLanes * 4 || BN > 128, "the split's parts fit the stages");
-  auto kernel = mx_matmul_kernel<BN, STAGES>;
-  static std::atomic<uint64_t> opted{0};
-  const cudaError_t e = opt_in(kernel, kSmem, opted);
-  if (e != cudaSuccess) return e;
-  a.p_tiles = (a.p_rows + kLanes - 1) / kLanes;
-  const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + BN - 1) / BN);
-  if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
-  a.n_tiles = (int)tiles;
-  // one cluster (a CTA when k is not split) per tile, or one CTA per SM walking the tiles
-  const int grid = a.split > 1 ? a.n_tiles * a.split : std::min<int>(a.n_tiles, sm_count * (BN <= 64 ? 2 : 1));
+// Whether a matrix's scale rows can be loaded as they lie (the tensor map's
+// alignment).
+bool rows_load(const MxMatrix& m) {
+  return ((reinterpret_cast<uintptr_t>(m.scales) | (uintptr_t)m.scale_pitch) & 15u) == 0;
+}
+// Pieces of a matrix: blocks of 128 rows (whole pairs of them) times groups of two k tiles.
+int64_t row_blocks(const MxMatrix& m) { return 2 * ((m.rows + 255) / 256); }
+int64_t groups_of(const MxMatrix& m) { return (mx_blocks(m.cols) + 15) / 16; }
+int64_t pieces_bytes(const MxMatrix& m) { return rows_load(m) ? 0 : row_blocks(m) * groups_of(m) * kGroup; }
+
+struct Maps {
+  CUtensorMap p, q, ps, qs;
+};
+bool make_maps(Maps* t, const MxMatrix& p, const MxMatrix& q, int q_rows, uint8_t* p_pieces, uint8_t* q_pieces) {
+  return codes_map(&t->p, p, kLanes) && codes_map(&t->q, q, q_rows) &&
+         scales_map(&t->ps, p, kLanes, p_pieces, row_blocks(p) * groups_of(p)) &&
+         scales_map(&t->qs, q, q_rows, q_pieces, row_blocks(q) * groups_of(q));
+}
+
+template <class K>
+cudaError_t launch_product(K kernel, int grid, int smem, int cluster, const Maps& t, const MmArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreadsMm);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
-  if (a.split > 1) {
+  if (cluster > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = (unsigned)a.split;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
     attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
     ++n;
   }
@@ -984,60 +991,54 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, int sm_count,
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, pm, qm, a);
+  return cudaLaunchKernelEx(&cfg, kernel, t.p, t.q, t.ps, t.qs, a);
 }
 
-// Row blocks of 128 that the pair kernel reads for `rows` rows (whole pairs).
-int64_t pair_blocks(int64_t rows) { return 2 * ((rows + 255) / 256); }
-
-cudaError_t launch_pair(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* workspace, int sm_count, cudaStream_t s) {
-  PieceArgs g = {};
-  g.scales[0] = a.p_scales, g.scales[1] = a.q_scales;
-  g.pitch[0] = a.p_scale_pitch, g.pitch[1] = a.q_scale_pitch;
-  g.rows[0] = a.p_rows, g.rows[1] = a.q_rows;
-  g.align[0] = a.p_align, g.align[1] = a.q_align;
-  CUtensorMap pm, qm, sm;
-  const int64_t row = (int64_t)a.k_tiles * kPieces, pb = pair_blocks(p.rows), qb = pair_blocks(q.rows);
-  if ((pb + qb) * 4 * a.k_tiles > 0x7FFFFFFF - 8) return cudaErrorInvalidValue;
-  if (!codes_map(&pm, p, kLanes) || !codes_map(&qm, q, kLanes) || !pieces_map(&sm, workspace, (pb + qb) * a.k_tiles))
-    return cudaErrorInvalidValue;
-  g.out[0] = workspace, g.out[1] = workspace + pb * row;
-  g.k_blocks = a.k_blocks, g.k_tiles = a.k_tiles;
-  g.warps0 = (int)(pb * 4 * a.k_tiles), g.warps = (int)((pb + qb) * 4 * a.k_tiles);
-  cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, a.pdl != 0, g);
-  if (e != cudaSuccess) return e;
-  a.pdl = 1;
-  constexpr int kSmem = kPairStages * kPairStage + 1024;
-  static_assert(kSmem <= 227 * 1024 - 1024, "stages fit shared memory");
+template <int BN, int STAGES, int GROUPS>
+cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pieces, uint8_t* q_pieces, int sm_count,
+                   cudaStream_t s) {
+  constexpr int kSmem = STAGES * stage_bytes(BN) + GROUPS * 2 * kGroup + 1024;
+  static_assert(kSmem <= (BN <= 64 ? 113 : 226) * 1024, "stages fit shared memory (twice for narrow tiles)");
+  static_assert(STAGES * stage_bytes(BN) >= BN * kLanes * 4, "the split's parts fit the stages");
   static std::atomic<uint64_t> opted{0};
-  e = opt_in(mx_matmul_pair_kernel, kSmem, opted);
+  const cudaError_t e = opt_in(mx_matmul_kernel<BN, STAGES, GROUPS>, kSmem, opted);
   if (e != cudaSuccess) return e;
+  Maps t;
+  if (!make_maps(&t, p, q, BN, p_pieces, q_pieces)) return cudaErrorInvalidValue;
+  a.p_tiles = (a.p_rows + kLanes - 1) / kLanes;
+  const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + BN - 1) / BN);
+  if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
+  a.n_tiles = (int)tiles;
+  // one cluster (a CTA when k is not split) per tile, or every SM's CTAs walking the tiles
+  const int grid = a.split > 1 ? a.n_tiles * a.split : std::min<int>(a.n_tiles, sm_count * (BN <= 64 ? 2 : 1));
+  return launch_product(mx_matmul_kernel<BN, STAGES, GROUPS>, grid, kSmem, a.split, t, a, s);
+}
+
+cudaError_t launch_pair(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pieces, uint8_t* q_pieces, int sm_count,
+                        cudaStream_t s) {
+  constexpr int kSmem = kPairStages * kPairCodes + kPairGroups * kPairGroup + 1024;
+  static_assert(kSmem <= 226 * 1024, "stages fit shared memory");
+  static std::atomic<uint64_t> opted{0};
+  const cudaError_t e = opt_in(mx_matmul_pair_kernel, kSmem, opted);
+  if (e != cudaSuccess) return e;
+  Maps t;
+  if (!make_maps(&t, p, q, kLanes, p_pieces, q_pieces)) return cudaErrorInvalidValue;
   a.p_tiles = (a.p_rows + 2 * kLanes - 1) / (2 * kLanes);
   const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + kPairN - 1) / kPairN);
   if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
   a.n_tiles = (int)tiles;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)std::min<int64_t>(tiles, sm_count / 2));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_matmul_pair_kernel, pm, qm, sm, a);
+  return launch_product(mx_matmul_pair_kernel, 2 * (int)std::min<int64_t>(tiles, sm_count / 2), kSmem, 1, t, a, s);
+}
+
+// Whether the product runs on CTA pairs: more than 128 rows on both sides, and
+// 256 x 256 tiles for half of the pairs.
+bool by_pairs(int64_t m, int64_t n, int sm_count) {
+  return std::min(m, n) > kLanes && ((m + 255) / 256) * ((n + 255) / 256) >= sm_count / 4;
 }
 
 }  // namespace
 
-// Whether the product runs on CTA pairs: enough 256 x 256 tiles for half of them.
-bool by_pairs(int64_t m, int64_t n, int sm_count) { return ((m + 255) / 256) * ((n + 255) / 256) >= sm_count / 4; }
-
-int64_t mx_matmul_workspace(int64_t m, int64_t n, int64_t k, int sm_count) {
-  if (!by_pairs(m, n, sm_count)) return 0;
-  return (pair_blocks(m) + pair_blocks(n)) * ((mx_blocks(k) + 7) / 8) * kPieces;
-}
+int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b) { return pieces_bytes(a) + pieces_bytes(b); }
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
@@ -1051,42 +1052,64 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   const bool swap = !many || !aligned;
   const MxMatrix& p = swap ? m.b : m.a;
   const MxMatrix& q = swap ? m.a : m.b;
+
   MmArgs a = {};
-  a.p_scales = p.scales, a.q_scales = q.scales;
-  a.p_scale_pitch = p.scale_pitch, a.q_scale_pitch = q.scale_pitch;
   a.p_rows = (int)p.rows, a.q_rows = (int)q.rows;
-  a.k_blocks = (int)mx_blocks(p.cols);
-  a.k_tiles = (a.k_blocks + 7) / 8;
-  auto align = [](const MxMatrix& x) {
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(x.scales) | (uintptr_t)x.scale_pitch;
-    return bits & 3u ? 1 : bits & 7u ? 4 : bits & 15u ? 8 : 16;
-  };
-  a.p_align = align(p), a.q_align = align(q);
-  a.out = m.out, a.type = m.type, a.pdl = m.pdl;
+  a.k_tiles = (int)((mx_blocks(p.cols) + 7) / 8);
+  a.out = m.out, a.type = m.type;
   a.p_stride = swap ? 1 : m.ld, a.q_stride = swap ? m.ld : 1;
   a.vec = !swap;
   a.split = 1;
-  if (many) return launch_pair(p, q, a, static_cast<uint8_t*>(m.workspace), sm_count, s);
+  a.pdl = m.pdl;
+
+  uint8_t* space = static_cast<uint8_t*>(m.workspace);
+  uint8_t *p_pieces = nullptr, *q_pieces = nullptr;
+  if (!rows_load(p)) p_pieces = space, space += pieces_bytes(p);
+  if (!rows_load(q)) q_pieces = space;
+  a.p_pieces = p_pieces != nullptr, a.q_pieces = q_pieces != nullptr;
+  if (p_pieces || q_pieces) {
+    PieceArgs g = {};
+    const MxMatrix* of[2] = {p_pieces ? &p : &q, q_pieces ? &q : nullptr};
+    uint8_t* to[2] = {p_pieces ? p_pieces : q_pieces, q_pieces};
+    const int n = p_pieces && q_pieces ? 2 : 1;
+    g.groups = (int)groups_of(p);
+    g.k_blocks = (int)mx_blocks(p.cols);
+    int64_t warps = 0;
+    for (int i = 0; i < n; ++i) {
+      g.scales[i] = of[i]->scales, g.pitch[i] = of[i]->scale_pitch, g.rows[i] = (int)of[i]->rows, g.out[i] = to[i];
+      warps += 4 * row_blocks(*of[i]) * g.groups;
+      if (i == 0) g.warps0 = (int)std::min<int64_t>(warps, 0x7FFFFFFF);
+    }
+    if (warps > 0x7FFFFFFF - 8) return cudaErrorInvalidValue;
+    g.warps = (int)warps;
+    g.pdl = m.pdl;
+    const cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, m.pdl != 0, g);
+    if (e != cudaSuccess) return e;
+    a.pdl = 1;
+  }
+  a.p_early = swap && m.pdl && !p_pieces && !q_pieces;  // then the grid before this one writes only a
+
+  if (many) return launch_pair(p, q, a, p_pieces, q_pieces, sm_count, s);
   const int64_t p_tiles = (p.rows + kLanes - 1) / kLanes;
   auto split_for = [&](int bn, int slots) {
     const int64_t tiles = p_tiles * ((q.rows + bn - 1) / bn);
-    const int64_t n = std::min<int64_t>(std::min<int64_t>(8, a.k_tiles), slots / tiles);
-    a.split = (int)std::max<int64_t>(1, n);
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(8, (a.k_tiles + 1) / 2), slots / tiles);
+    for (a.split = 1; 2 * a.split <= most;) a.split *= 2;
   };
   if (q.rows <= 16) {
     split_for(16, 2 * sm_count);
-    return launch<16, 5>(p, q, a, sm_count, s);
+    return launch<16, 5, 3>(p, q, a, p_pieces, q_pieces, sm_count, s);
   }
   if (p_tiles * ((q.rows + 31) / 32) <= sm_count) {
     split_for(32, 2 * sm_count);
-    return launch<32, 4>(p, q, a, sm_count, s);
+    return launch<32, 4, 3>(p, q, a, p_pieces, q_pieces, sm_count, s);
   }
   if (p_tiles * ((q.rows + 63) / 64) <= sm_count) {
     split_for(64, 2 * sm_count);
-    return launch<64, 4>(p, q, a, sm_count, s);
+    return launch<64, 4, 2>(p, q, a, p_pieces, q_pieces, sm_count, s);
   }
   split_for(128, sm_count);
-  return launch<128, 5>(p, q, a, sm_count, s);
+  return launch<128, 6, 3>(p, q, a, p_pieces, q_pieces, sm_count, s);
 }
 
 // The flag of a bounded wait that ran out (current device), cleared as it is read (waits for `s`).
