@@ -637,80 +637,72 @@ class ZeroOptimizer:
         self._check(zero_all_gather(self.ctx, lo, hi, ptrs, self._stream(stream)), "zero_all_gather")
 
     # -- MX4 collectives --
-    def _mx4_ptrs(self, lo: int, hi: int, codes, scales):
-        """The N ranks' buffers of [lo, hi): uint8 tensors (or one with a
-        leading dimension of N) that hold the interval's blocks."""
-        nb = (int(hi) - int(lo) + ZERO_MX4_BLOCK - 1) // ZERO_MX4_BLOCK
-        out = []
-        for name, bufs, need in (("codes", codes, 16 * nb), ("scales", scales, nb)):
-            if len(bufs) != self.n_ranks:
-                raise ValueError(f"{name}: {len(bufs)} buffers for {self.n_ranks} ranks")
-            one = bufs if isinstance(bufs, self._torch.Tensor) else None
-            for b in ((one,) if one is not None else bufs):
-                if b.dtype != self._torch.uint8 or not b.is_contiguous() or b.device != self.device:
-                    raise ValueError(f"{name}: contiguous uint8 tensors on {self.device} are needed")
-                if b.numel() < need * (self.n_ranks if one is not None else 1):
-                    raise ValueError(f"{name}: {need} bytes a rank are needed for [{lo}, {hi})")
-            if one is not None:
-                step = one.numel() // self.n_ranks
-                out.append(_ptr_array([one.data_ptr() + r * step for r in range(self.n_ranks)]))
-            else:
-                out.append(_ptr_array([b.data_ptr() for b in bufs]))
-        return out
+    def _mx4_ptrs(self, lo: int, hi: int, name: str, bufs, need: int):
+        """The N ranks' buffers of [lo, hi) as a C array: uint8 tensors, or one
+        with a leading dimension of N, of at least ``need`` bytes a rank."""
+        n = self.n_ranks
+        whole = isinstance(bufs, self._torch.Tensor)
+        if len(bufs) != n:
+            raise ValueError(f"{name}: {len(bufs)} buffers for {n} ranks")
+        for b in ((bufs,) if whole else bufs):
+            if b.dtype != self._torch.uint8 or not b.is_contiguous() or b.device != self.device:
+                raise ValueError(f"{name}: contiguous uint8 tensors on {self.device} are needed")
+            if b.numel() < (need * n if whole else need):
+                raise ValueError(f"{name}: {need} bytes a rank are needed for [{lo}, {hi})")
+        if not whole:
+            return _ptr_array([b.data_ptr() for b in bufs])
+        at, step = bufs.data_ptr(), bufs.numel() // n
+        return (ctypes.c_void_p * n)(*range(at, at + n * step, step)) if step else _ptr_array([at] * n)
+
+    def _mx4_collective(self, fn, where: str, lo: int, hi: int, codes, scales, stream):
+        nb = (hi - lo + ZERO_MX4_BLOCK - 1) // ZERO_MX4_BLOCK
+        c, s = self._mx4_ptrs(lo, hi, "codes", codes, 16 * nb), self._mx4_ptrs(lo, hi, "scales", scales, nb)
+        self._check(_on_device(self.device, stream, fn, self.ctx, lo, hi, c, s), where)
 
     def all_gather_mx4(self, lo: int, hi: int, codes, scales, stream=None):
         """The owners' parameters [lo, hi) quantised into every rank's MX4
         buffers: ``codes[r]`` 16 bytes and ``scales[r]`` one byte for each 32
         elements (zero_mx4_all_gather)."""
-        c, s = self._mx4_ptrs(lo, hi, codes, scales)
-        with _on(self.device):
-            self._check(zero_mx4_all_gather(self.ctx, lo, hi, c, s, self._stream(stream)), "zero_mx4_all_gather")
+        self._mx4_collective(zero_mx4_all_gather, "zero_mx4_all_gather", lo, hi, codes, scales, stream)
 
     def reduce_scatter_mx4(self, lo: int, hi: int, codes, scales, stream=None):
         """The mean of the ranks' MX4 gradients of [lo, hi) into the owners'
         reduced-gradient shards (zero_mx4_reduce_scatter)."""
-        c, s = self._mx4_ptrs(lo, hi, codes, scales)
-        with _on(self.device):
-            self._check(zero_mx4_reduce_scatter(self.ctx, lo, hi, c, s, self._stream(stream)),
-                        "zero_mx4_reduce_scatter")
+        self._mx4_collective(zero_mx4_reduce_scatter, "zero_mx4_reduce_scatter", lo, hi, codes, scales, stream)
 
 
 # ------------------------------------------------------ MX4 matrices ----
 #
-# These calls run once per product of a small layer, so the wrapper keeps its
-# own time short: torch is looked up once, tensors' properties are read once.
+# A product of a small layer takes a few microseconds on the GPU, so these
+# wrappers keep their own time short: torch is looked up once, a tensor's
+# properties are read once, views are made when they are asked for.
 
+_T = None            # torch, after the first use
+_RAW_STREAM = None   # device index -> the current stream's handle
 _DTYPE_CODES: dict = {}
 
 
 def _torch():
-    import torch
+    global _T, _RAW_STREAM
+    if _T is None:
+        import torch
 
-    if not _DTYPE_CODES:
         _DTYPE_CODES.update({torch.bfloat16: ZERO_DTYPE_BF16, torch.float16: ZERO_DTYPE_F16,
                              torch.float32: ZERO_DTYPE_F32})
-    return torch
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _T = torch
+    return _T
 
 
-class _on:
-    """Makes ``device`` the current CUDA device for a call (free when it is)."""
-
-    __slots__ = ("_index", "_back")
-
-    def __init__(self, device):
-        self._index = device.index
-
-    def __enter__(self):
-        cuda = _torch().cuda
-        now = cuda.current_device()
-        self._back = now if self._index is not None and self._index != now else None
-        if self._back is not None:
-            cuda.set_device(self._index)
-
-    def __exit__(self, *exc):
-        if self._back is not None:
-            _torch().cuda.set_device(self._back)
-        return False
+def _on_device(device, stream, fn, *args) -> int:
+    """fn(*args, stream handle) with ``device`` as the current CUDA device."""
+    cuda = (_T or _torch()).cuda
+    index, now = device.index, cuda.current_device()
+    if index is None or index == now:
+        return fn(*args, _RAW_STREAM(now) if stream is None else int(getattr(stream, "cuda_stream", stream)))
+    with cuda.device(index):
+        return fn(*args, _RAW_STREAM(index) if stream is None else int(getattr(stream, "cuda_stream", stream)))
 
 
 class MX4:
@@ -718,29 +710,47 @@ class MX4:
     include/zero_sm.h): uint8 CUDA tensors ``codes`` [rows, pitch] and
     ``scales`` [rows, pitch], each with contiguous rows."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "device", "_c")
+    __slots__ = ("_codes", "_scales", "_space", "rows", "cols", "device", "_c")
 
     def __init__(self, codes, scales, rows: int, cols: int):
-        uint8 = _torch().uint8
+        torch = _T or _torch()
         nb = -(-cols // ZERO_MX4_BLOCK)
         pitches = []
         for name, t, need in (("codes", codes, 16 * nb), ("scales", scales, nb)):
             shape = t.shape
-            if t.dtype != uint8 or len(shape) != 2 or shape[0] != rows or shape[1] < need:
+            if t.dtype != torch.uint8 or len(shape) != 2 or shape[0] != rows or shape[1] < need:
                 raise ValueError(f"{name}: a uint8 tensor of {rows} rows of at least {need} bytes is needed")
             pitch, one = t.stride()
             if one != 1 and shape[1] > 1:
                 raise ValueError(f"{name}: the rows must be contiguous (stride {one})")
             pitches.append(pitch if rows > 1 else shape[1])
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self._codes, self._scales, self._space, self.rows, self.cols = codes, scales, None, rows, cols
         self.device = codes.device
         if not codes.is_cuda or scales.device != self.device:
             raise ValueError("codes and scales must be on the same CUDA device")
         self._c = zero_mx4(codes.data_ptr(), scales.data_ptr(), rows, cols, pitches[0], pitches[1])
 
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._views()
+        return self._codes
 
-def _mx4_bytes(rows: int, cols: int) -> tuple:
-    """(code pitch, scale pitch) that mx4_empty uses: scale rows padded to 16 bytes."""
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._views()
+        return self._scales
+
+    def _views(self):
+        c = self._c
+        n = self.rows * c.code_pitch
+        self._codes = self._space[:n].view(self.rows, c.code_pitch)
+        self._scales = self._space[n:].view(self.rows, c.scale_pitch)
+
+
+def _mx4_pitches(cols: int) -> tuple:
+    """(codes, scales): mx4_empty's bytes of a row, scales padded to 16."""
     nb = -(-cols // ZERO_MX4_BLOCK)
     return 16 * nb, -(-nb // 16) * 16
 
@@ -748,13 +758,19 @@ def _mx4_bytes(rows: int, cols: int) -> tuple:
 def mx4_empty(rows: int, cols: int, device=None) -> MX4:
     """An MX4 matrix of uninitialised memory; its scale rows are padded to 16
     bytes, the alignment that the product loads fastest."""
-    torch = _torch()
+    torch = _T or _torch()
     if rows < 0 or cols < 0:
         raise ValueError(f"{rows} x {cols}")
-    cp, sp = _mx4_bytes(rows, cols)
-    device = device or torch.device("cuda", torch.cuda.current_device())
-    whole = torch.empty(rows * (cp + sp), dtype=torch.uint8, device=device)
-    return MX4(whole[:rows * cp].view(rows, cp), whole[rows * cp:].view(rows, sp), rows, cols)
+    cp, sp = _mx4_pitches(cols)
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    m = MX4.__new__(MX4)
+    m._space = torch.empty(rows * (cp + sp), dtype=torch.uint8, device=device)
+    m._codes = m._scales = None
+    m.rows, m.cols, m.device = rows, cols, m._space.device
+    at = m._space.data_ptr()
+    m._c = zero_mx4(at, at + rows * cp, rows, cols, cp, sp)
+    return m
 
 
 def _dense(t, name: str):
@@ -762,12 +778,11 @@ def _dense(t, name: str):
     shape = t.shape
     if len(shape) != 2 or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA matrix is needed")
+    if _T is None:
+        _torch()
     code = _DTYPE_CODES.get(t.dtype)
     if code is None:
-        _torch()
-        code = _DTYPE_CODES.get(t.dtype)
-        if code is None:
-            raise ValueError(f"{name} is {t.dtype}: bfloat16, float16 or float32 is needed")
+        raise ValueError(f"{name} is {t.dtype}: bfloat16, float16 or float32 is needed")
     ld, one = t.stride()
     rows, cols = shape
     if one != 1 and cols > 1:
@@ -775,21 +790,11 @@ def _dense(t, name: str):
     return t.data_ptr(), code, ld if rows > 1 else cols, rows, cols
 
 
-def _stream_of(device, stream) -> int:
-    if stream is None:
-        return _torch().cuda.current_stream(device).cuda_stream
-    return int(getattr(stream, "cuda_stream", stream))
-
-
-def _lend(stream, *tensors):
+def _lend(stream, t):
     """Keeps memory that this call allocated from being reused before the work
     given to another stream than the current one has run."""
-    if stream is None:
-        return
-    torch = _torch()
-    for t in tensors:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=t.device)
-        t.record_stream(s)
+    s = stream if isinstance(stream, _T.cuda.Stream) else _T.cuda.ExternalStream(int(stream), device=t.device)
+    t.record_stream(s)
 
 
 def _mx4_check(st: int, where: str):
@@ -797,27 +802,32 @@ def _mx4_check(st: int, where: str):
         raise ZeroError(st, where, zero_last_error(None).decode())
 
 
-def _same_device(device, **others):
-    for name, t in others.items():
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not {device}")
+def _need_device(device, name: str, t):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
 
 
 def _result(out, rows: int, cols: int, dtype, device, stream, name: str = "out"):
     if out is None:
-        out = _torch().empty((rows, cols), dtype=dtype, device=device)
-        _lend(stream, out)
-    elif tuple(out.shape) != (rows, cols):
-        raise ValueError(f"{name} is {tuple(out.shape)}, not {(rows, cols)}")
+        out = _T.empty((rows, cols), dtype=dtype, device=device)
+        if stream is not None:
+            _lend(stream, out)
+    else:
+        if tuple(out.shape) != (rows, cols):
+            raise ValueError(f"{name} is {tuple(out.shape)}, not {(rows, cols)}")
+        _need_device(device, name, out)
     return out
 
 
 def _mx4_result(out, rows: int, cols: int, device, stream, name: str = "out"):
     if out is None:
         out = mx4_empty(rows, cols, device)
-        _lend(stream, out.codes)
-    elif (out.rows, out.cols) != (rows, cols):
-        raise ValueError(f"{name} is {(out.rows, out.cols)}, not {(rows, cols)}")
+        if stream is not None:
+            _lend(stream, out._space)
+    else:
+        if (out.rows, out.cols) != (rows, cols):
+            raise ValueError(f"{name} is {(out.rows, out.cols)}, not {(rows, cols)}")
+        _need_device(device, name, out)
     return out
 
 
@@ -825,39 +835,32 @@ def _rounding(seed):
     return (ZERO_MX4_NEAREST, 0) if seed is None else (ZERO_MX4_STOCHASTIC, int(seed) & 0xFFFFFFFFFFFFFFFF)
 
 
-def _quantize(x, seed, out, out_t, stream):
-    ptr, code, ld, rows, cols = _dense(x, "x")
-    rounding, seed = _rounding(seed)
-    device = x.device
-    for o in (out, out_t):
-        if o is not None:
-            _same_device(device, out=o)
-    with _on(device):
-        _mx4_check(zero_mx4_quantize(ptr, code, rows, cols, ld, rounding, seed, out and ctypes.byref(out._c),
-                                     out_t and ctypes.byref(out_t._c), _stream_of(device, stream)),
-                   "zero_mx4_quantize")
-
-
 def mx4_quantize(x, transpose: bool = False, seed: Optional[int] = None, out: Optional[MX4] = None, stream=None) -> MX4:
     """Quantise a matrix in blocks along its rows or, with ``transpose``, its
     transpose (blocks down x's columns).  ``seed`` rounds stochastically;
     None rounds to nearest even (zero_mx4_quantize)."""
-    rows, cols = x.shape
+    ptr, code, ld, rows, cols = _dense(x, "x")
+    device = x.device
+    rounding, seed = _rounding(seed)
     if transpose:
-        out = _mx4_result(out, cols, rows, x.device, stream)
-        _quantize(x, seed, None, out, stream)
+        out = _mx4_result(out, cols, rows, device, stream)
+        st = _on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, None, out._c)
     else:
-        out = _mx4_result(out, rows, cols, x.device, stream)
-        _quantize(x, seed, out, None, stream)
+        out = _mx4_result(out, rows, cols, device, stream)
+        st = _on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, out._c, None)
+    _mx4_check(st, "zero_mx4_quantize")
     return out
 
 
 def mx4_quantize_both(x, seed: Optional[int] = None, out: Optional[MX4] = None, out_t: Optional[MX4] = None, stream=None):
     """(x, its transpose) as MX4 matrices, reading x once."""
-    rows, cols = x.shape
-    out = _mx4_result(out, rows, cols, x.device, stream)
-    out_t = _mx4_result(out_t, cols, rows, x.device, stream, "out_t")
-    _quantize(x, seed, out, out_t, stream)
+    ptr, code, ld, rows, cols = _dense(x, "x")
+    device = x.device
+    out = _mx4_result(out, rows, cols, device, stream)
+    out_t = _mx4_result(out_t, cols, rows, device, stream, "out_t")
+    rounding, seed = _rounding(seed)
+    _mx4_check(_on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, out._c, out_t._c),
+               "zero_mx4_quantize")
     return out, out_t
 
 
@@ -865,11 +868,8 @@ def mx4_transpose(m: MX4, seed: Optional[int] = None, out: Optional[MX4] = None,
     """The transpose of an MX4 matrix, quantised in blocks along the other axis."""
     device = m.device
     out = _mx4_result(out, m.cols, m.rows, device, stream)
-    _same_device(device, out=out)
     rounding, seed = _rounding(seed)
-    with _on(device):
-        _mx4_check(zero_mx4_transpose(ctypes.byref(m._c), rounding, seed, ctypes.byref(out._c),
-                                      _stream_of(device, stream)), "zero_mx4_transpose")
+    _mx4_check(_on_device(device, stream, zero_mx4_transpose, m._c, rounding, seed, out._c), "zero_mx4_transpose")
     return out
 
 
@@ -878,22 +878,8 @@ def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
     device = m.device
     out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, stream)
     ptr, code, ld, _, _ = _dense(out, "out")
-    _same_device(device, out=out)
-    with _on(device):
-        _mx4_check(zero_mx4_dequantize(ctypes.byref(m._c), ptr, code, ld, _stream_of(device, stream)),
-                   "zero_mx4_dequantize")
+    _mx4_check(_on_device(device, stream, zero_mx4_dequantize, m._c, ptr, code, ld), "zero_mx4_dequantize")
     return out
-
-
-def _workspace(query, a, b, device, stream):
-    """(pointer, bytes, tensor) of the workspace that the query asks for."""
-    need = ctypes.c_int64()
-    _mx4_check(query(a, b, ctypes.byref(need)), "workspace size")
-    if need.value == 0:
-        return None, 0, None
-    space = _torch().empty(need.value, dtype=_torch().uint8, device=device)
-    _lend(stream, space)
-    return space.data_ptr(), need.value, space
 
 
 def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
@@ -901,12 +887,16 @@ def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
     device = a.device
     out = _result(out, a.rows, b.rows, dtype or _torch().bfloat16, device, stream)
     ptr, code, ld, _, _ = _dense(out, "out")
-    _same_device(device, b=b, out=out)
-    with _on(device):
-        ac, bc = ctypes.byref(a._c), ctypes.byref(b._c)
-        at, size, space = _workspace(zero_mx4_matmul_workspace, ac, bc, device, stream)
-        _mx4_check(zero_mx4_matmul(ac, bc, ptr, code, ld, at, size,
-                                   _stream_of(device, stream)), "zero_mx4_matmul")
+    _need_device(device, "b", b)
+    need = ctypes.c_int64()
+    _mx4_check(zero_mx4_matmul_workspace(a._c, b._c, need), "zero_mx4_matmul_workspace")
+    at = None
+    if need.value:
+        space = _T.empty(need.value, dtype=_T.uint8, device=device)
+        at = space.data_ptr()
+        if stream is not None:
+            _lend(stream, space)
+    _mx4_check(_on_device(device, stream, zero_mx4_matmul, a._c, b._c, ptr, code, ld, at, need.value), "zero_mx4_matmul")
     return out
 
 
@@ -917,14 +907,19 @@ def mx4_linear(x, w: MX4, out=None, stream=None):
     device = x.device
     if inputs != w.cols:
         raise ValueError(f"x has {inputs} inputs, w {w.cols}")
+    _need_device(device, "w", w)
     y = _result(out, tokens, w.rows, x.dtype, device, stream)
-    yptr, ycode, ldy, _, _ = _dense(y, "out")
-    _same_device(device, w=w, out=y)
-    with _on(device):
-        wc = ctypes.byref(w._c)
-        at, size, space = _workspace(zero_mx4_linear_workspace, tokens, wc, device, stream)
-        _mx4_check(zero_mx4_linear(ptr, code, tokens, ld, wc, yptr, ycode, ldy, at, size,
-                                   _stream_of(device, stream)), "zero_mx4_linear")
+    if out is None:
+        yptr, ycode, ldy = y.data_ptr(), code, w.rows
+    else:
+        yptr, ycode, ldy, _, _ = _dense(y, "out")
+    need = ctypes.c_int64()
+    _mx4_check(zero_mx4_linear_workspace(tokens, w._c, need), "zero_mx4_linear_workspace")
+    space = _T.empty(need.value, dtype=_T.uint8, device=device)
+    if stream is not None:
+        _lend(stream, space)
+    _mx4_check(_on_device(device, stream, zero_mx4_linear, ptr, code, tokens, ld, w._c, yptr, ycode, ldy,
+                          space.data_ptr(), need.value), "zero_mx4_linear")
     return y
 
 
@@ -936,7 +931,8 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
     of a rank's gradient buffer)."""
     if x.dim() != 2 or dy.dim() != 2 or x.shape[1] != w.cols or tuple(dy.shape) != (x.shape[0], w.rows):
         raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} do not fit w {(w.rows, w.cols)}")
-    _same_device(x.device, dy=dy, w=w)
+    _need_device(x.device, "dy", dy)
+    _need_device(x.device, "w", w)
     dyq, dyq_t = mx4_quantize_both(dy, seed, stream=stream)
     xq_t = mx4_quantize(x, transpose=True, stream=stream)
     wq_t = mx4_transpose(w, stream=stream)
@@ -949,8 +945,7 @@ def mx4_check(device=None, stream=None):
     """Wait for the stream; raise ZeroError if a bounded wait of a product kernel ran out."""
     torch = _torch()
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _on(device):
-        _mx4_check(zero_mx4_check(_stream_of(device, stream)), "zero_mx4_check")
+    _mx4_check(_on_device(device, stream, zero_mx4_check), "zero_mx4_check")
 
 
 # ------------------------------------------------ one logical rank per GPU ----

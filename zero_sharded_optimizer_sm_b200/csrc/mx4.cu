@@ -20,124 +20,131 @@ namespace {
 using namespace dev;
 using namespace mx;
 
-struct TBf16 {
+// Eight consecutive elements of a storage type, kept as loaded: their values,
+// and the binary32 pattern of the largest magnitude (an infinity or NaN
+// counts as larger than any number).
+template <class F>
+struct Vec16 {  // bf16 or binary16
   using raw = uint16_t;
-  static __device__ __forceinline__ float f32(raw h) { return Bf16::f32(h); }
-  static __device__ __forceinline__ raw rn(float x) { return Bf16::rn(x); }
+  static constexpr int kUnits = 4;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const raw* p) {
+    const uint4 x = ld_stream(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  }
+  __device__ __forceinline__ void load(const raw* p, int64_t n) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = (2 * j < n ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)p[2 * j + 1] << 16 : 0u);
+  }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  static __device__ __forceinline__ float lo(uint32_t x) { return F::lo(x); }
+  static __device__ __forceinline__ float hi(uint32_t x) { return F::hi(x); }
+  __device__ __forceinline__ uint32_t max_bits() const {
+    // 16-bit patterns without their signs order as their magnitudes do
+    uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    m = max(m & 0xFFFFu, m >> 16);
+    return __float_as_uint(F::f32((uint16_t)m));
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[2 * j] = F::lo(w[j]), v[2 * j + 1] = F::hi(w[j]);
+  }
 };
-struct TF16 {
-  using raw = uint16_t;
-  static __device__ __forceinline__ float f32(raw h) { return F16::f32(h); }
-  static __device__ __forceinline__ raw rn(float x) { return F16::rn(x); }
-};
-struct TF32 {
+struct Vec32 {  // binary32
   using raw = float;
-  static __device__ __forceinline__ float f32(raw x) { return x; }
-  static __device__ __forceinline__ raw rn(float x) { return x; }
+  static constexpr int kUnits = 2;
+  float x[8];
+  __device__ __forceinline__ void load(const raw* p) {
+    const float4 a = ld_stream(p), b = ld_stream(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ void load(const raw* p, int64_t n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j < n ? p[j] : 0.0f;
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+  }
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x[j];
+  }
 };
 
-// Eight consecutive elements, of which the first n exist (the others are 0).
-// vec: the address is 16-byte aligned whenever n = 8.
-template <class T>
-__device__ __forceinline__ void load8(const typename T::raw* p, int64_t n, bool vec, typename T::raw (&r)[8]) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(typename T::raw) == 2) {
-      const uint4 w = ld_stream(reinterpret_cast<const uint16_t*>(p));
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r[2 * j] = (uint16_t)(x[j] & 0xFFFFu);
-        r[2 * j + 1] = (uint16_t)(x[j] >> 16);
-      }
-    } else {
-      const float4 a = ld_stream(reinterpret_cast<const float*>(p)), b = ld_stream(reinterpret_cast<const float*>(p) + 4);
-      r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = j < n ? p[j] : typename T::raw(0);
-  }
+// vec: a whole vector's address is 16-byte aligned.
+template <class V>
+__device__ __forceinline__ void load8(V& x, const typename V::raw* p, int64_t n, int vec) {
+  if (n >= 8 && vec) x.load(p);
+  else if (n > 0) x.load(p, n);
+  else x.clear();
 }
 
-template <class T>
-__device__ __forceinline__ void store8(typename T::raw* p, int64_t n, bool vec, const float (&v)[8]) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(typename T::raw) == 2) {
-      const uint16_t h[8] = {T::rn(v[0]), T::rn(v[1]), T::rn(v[2]), T::rn(v[3]),
-                             T::rn(v[4]), T::rn(v[5]), T::rn(v[6]), T::rn(v[7])};
-      st_stream(reinterpret_cast<uint16_t*>(p), pack8(h));
-    } else {
-      st_stream(reinterpret_cast<float*>(p), make_float4(v[0], v[1], v[2], v[3]));
-      st_stream(reinterpret_cast<float*>(p) + 4, make_float4(v[4], v[5], v[6], v[7]));
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = T::rn(v[j]);
-  }
-}
-
-__device__ __forceinline__ uint32_t max_bits8(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return m;
-}
-
-// A quarter block (8 elements) held by one lane of four: its codes and, the
-// same in the four lanes, the block's scale byte.  `block` and the lane's
-// place in the block number the random numbers.
-__device__ __forceinline__ uint32_t encode_quarter(float (&v)[8], int stochastic, uint64_t block, int c, uint64_t seed,
-                                                   uint32_t& s) {
-  uint32_t m = max_bits8(v);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  s = scale_code(m);
+// The codes of eight elements from their block's scale byte.  `block` and c
+// (the vector's place in the block) number the random numbers.
+template <bool kStochastic, class V>
+__device__ __forceinline__ uint32_t encode(const V& x, uint32_t s, uint64_t block, int c, uint64_t seed) {
+  float v[8];
+  x.values(v);
   const float inv = inverse_scale(s);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
-  const uint32_t w = stochastic ? encode8_stochastic(v, block, c, seed) : encode8(v);
+  const uint32_t w = kStochastic ? encode8_stochastic(v, block, c, seed) : encode8(v);
   return s == 255u ? 0u : w;
+}
+
+__device__ __forceinline__ uint32_t max_of_four(uint32_t m) {  // over four neighbouring lanes
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 
 // ---------------------------------------------------- quantise along rows --
 
 // A warp takes 256 consecutive columns of one row at a time, a lane 8 of them
-// and four lanes a block; kUnits such pieces are loaded before any is used.
+// and four lanes a block; V::kUnits such pieces go through each step side by
+// side, which hides the loads, the exchange between the four lanes and the
+// conversions (16 a clock and SM) behind one another.
 constexpr int kRowThreads = 256;
-constexpr int kUnits = 2;
 
-template <class T>
+template <class V, bool kStochastic>
 __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_constant__ MxQuantArgs a,
                                                               const FastDiv per_row, const uint32_t units, const int vec) {
-  using raw = typename T::raw;
-  const raw* src = static_cast<const raw*>(a.src);
+  constexpr int kUnits = V::kUnits;
+  pdl_trigger();
+  const typename V::raw* src = static_cast<const typename V::raw*>(a.src);
   const uint32_t warps = gridDim.x * (kRowThreads / 32);
   const int lane = threadIdx.x & 31;
   const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
   for (uint32_t u0 = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += kUnits * warps) {
-    raw x[kUnits][8];
-    int64_t row[kUnits], col[kUnits];
+    V x[kUnits];
+    uint32_t row[kUnits], m[kUnits];
+    int64_t col[kUnits];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      const uint32_t u = u0 + k * warps;
-      if (u < units) {
-        const uint32_t r = div_by(u, per_row);
-        row[k] = r;
-        col[k] = (int64_t)(u - r * per_row.d) * 256 + lane * 8;
-        load8<T>(src + row[k] * a.ld + col[k], a.cols - col[k], vec, x[k]);
-      }
+      const uint32_t u = min(u0 + k * warps, units - 1);  // past the end: the last piece again, not stored
+      row[k] = div_by(u, per_row);
+      col[k] = (int64_t)(u - row[k] * per_row.d) * 256 + lane * 8;
+      load8(x[k], src + row[k] * a.ld + col[k], a.cols - col[k], vec);
     }
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      if (u0 + k * warps >= units) break;  // the same for the whole warp
-      float v[8];
+    for (int k = 0; k < kUnits; ++k) m[k] = x[k].max_bits();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = T::f32(x[k][j]);
+    for (int k = 0; k < kUnits; ++k) m[k] = max(m[k], __shfl_xor_sync(0xFFFFFFFFu, m[k], 1));
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) m[k] = max(m[k], __shfl_xor_sync(0xFFFFFFFFu, m[k], 2));
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const uint32_t s = scale_code(m[k]);
       const int64_t b = col[k] >> 5;
-      uint32_t s;
-      const uint32_t w = encode_quarter(v, a.stochastic, (uint64_t)(row[k] * nb + b), lane & 3, a.seed, s);
-      if (b < nb) {
+      const uint32_t w = encode<kStochastic>(x[k], s, (uint64_t)(row[k] * nb + b), lane & 3, a.seed);
+      if (b < nb && u0 + k * warps < units) {
         *reinterpret_cast<uint32_t*>(a.out.codes + row[k] * a.out.code_pitch + (col[k] >> 1)) = w;
         if ((lane & 3) == 0) a.out.scales[row[k] * a.out.scale_pitch + b] = (uint8_t)s;
       }
@@ -147,35 +154,40 @@ __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_const
 
 // --------------------------------------- quantise down columns (and rows) --
 
-// A CTA takes a tile of 128 rows and 64 columns: 16-byte loads (kept in
-// registers for the blocks along the rows when those are wanted too) go
-// through shared memory, from which a thread reads one block of 32 elements
-// of one column.  Four neighbouring lanes take the four blocks of a column
-// (64 contiguous bytes of the result).  Row r's eight chunks of 8 elements
-// are rotated by r / 32 chunks, which puts the four blocks' reads on
-// different banks.
+// A CTA takes a tile of 128 rows and 128 columns of 16-bit elements (64 of
+// 32-bit ones): 16-byte loads, kept in registers for the blocks along the
+// rows when those are wanted too, go through shared memory, from which a
+// thread reads one block of 32 elements of each of the columns that share a
+// 32-bit word.  Four neighbouring lanes take the four blocks of a column (64
+// contiguous bytes of the result).  Row r's words are rotated by 8 (r / 32),
+// which puts the four blocks' reads on different banks.
 constexpr int kTileRows = 128;
-constexpr int kTileCols = 64;
+constexpr int kTileWords = 64;  // 32-bit words of a tile's row
 
-template <class T, bool kFromMx>
-__global__ void __launch_bounds__(256) mx_tile_kernel(const __grid_constant__ MxQuantArgs a, const uint32_t tiles_x,
-                                                      const int vec) {
-  using raw = typename T::raw;
-  __shared__ __align__(16) raw tile[kTileRows][kTileCols];
+template <class V, bool kFromMx, bool kRows, bool kStochastic>
+__global__ void __launch_bounds__(256, 3) mx_tile_kernel(const __grid_constant__ MxQuantArgs a, const uint32_t tiles_x,
+                                                         const int vec) {
+  using raw = typename V::raw;
+  constexpr int kPer = 4 / sizeof(raw);           // columns in a word
+  constexpr int kTileCols = kTileWords * kPer;
+  constexpr int kVecs = kTileCols / 8;            // vectors of a tile's row
+  constexpr int kLoads = kTileRows * kVecs / 256; // of a thread
+  constexpr int kChunks = 2 / kPer;               // 16-byte chunks of a vector
+  __shared__ __align__(16) uint32_t tile[kTileRows][kTileWords];
   const raw* src = static_cast<const raw*>(a.src);
   const int64_t r0 = (int64_t)(blockIdx.x / tiles_x) * kTileRows;
   const int64_t c0 = (int64_t)(blockIdx.x % tiles_x) * kTileCols;
   const int t = threadIdx.x;
-  const int cv = t & 7;
+  const int cv = t % kVecs, rv = t / kVecs;
   const int64_t col = c0 + 8 * cv;
-  raw x[4][8];
+  V x[kLoads];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = r0 + (t >> 3) + 32 * i;
+  for (int i = 0; i < kLoads; ++i) {
+    const int64_t row = r0 + rv + (256 / kVecs) * i;
     const int64_t left = row < a.rows ? a.cols - col : 0;
     if constexpr (kFromMx) {
-      // the elements' values are exact in bf16 (three significant bits and
-      // the same exponent range as binary32)
+      // the elements' values are exact in bf16: three significant bits and
+      // the same exponent range as binary32
       uint32_t h[4] = {0u, 0u, 0u, 0u};
       float sc = 0.0f;
       if (left > 0) {
@@ -185,36 +197,33 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(const __grid_constant__ Mx
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = half2_float2(h[j]);
-        x[i][2 * j] = T::rn(__fmul_rn(f.x, sc));
-        x[i][2 * j + 1] = T::rn(__fmul_rn(f.y, sc));
+        x[i].w[j] = pack2(Bf16::rn(__fmul_rn(f.x, sc)), Bf16::rn(__fmul_rn(f.y, sc)));
+        if (2 * j + 1 >= left) x[i].w[j] = 2 * j >= left ? 0u : x[i].w[j] & 0xFFFFu;
       }
     } else {
-      load8<T>(src + row * a.ld + col, left, vec, x[i]);
+      load8(x[i], src + row * a.ld + col, left, vec);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (t >> 3) + 32 * i;
-    raw* d = &tile[r][8 * ((cv + i) & 7)];
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = rv + (256 / kVecs) * i;
+    const uint4* p = reinterpret_cast<const uint4*>(&x[i]);
 #pragma unroll
-    for (int j = 0; j < 8; j += 16 / sizeof(raw)) {
-      uint4 w;
-      raw* p = reinterpret_cast<raw*>(&w);
-#pragma unroll
-      for (int k = 0; k < (int)(16 / sizeof(raw)); ++k) p[k] = x[i][j + k];
-      *reinterpret_cast<uint4*>(d + j) = w;
-    }
+    for (int k = 0; k < kChunks; ++k)
+      *reinterpret_cast<uint4*>(&tile[r][4 * ((kChunks * cv + k + 2 * (r >> 5)) & 15)]) = p[k];
   }
-  if (a.out.codes) {
+  if constexpr (kRows) {
     const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock, b = col >> 5;
+    uint32_t m[kLoads];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = r0 + (t >> 3) + 32 * i;
-      float v[8];
+    for (int i = 0; i < kLoads; ++i) m[i] = x[i].max_bits();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = T::f32(x[i][j]);
-      uint32_t s;
-      const uint32_t w = encode_quarter(v, a.stochastic, (uint64_t)(row * nb + b), cv & 3, a.seed, s);
+    for (int i = 0; i < kLoads; ++i) m[i] = max_of_four(m[i]);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int64_t row = r0 + rv + (256 / kVecs) * i;
+      const uint32_t s = scale_code(m[i]);
+      const uint32_t w = encode<kStochastic>(x[i], s, (uint64_t)(row * nb + b), cv & 3, a.seed);
       if (row < a.rows && b < nb) {
         *reinterpret_cast<uint32_t*>(a.out.codes + row * a.out.code_pitch + (col >> 1)) = w;
         if ((cv & 3) == 0) a.out.scales[row * a.out.scale_pitch + b] = (uint8_t)s;
@@ -223,61 +232,86 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(const __grid_constant__ Mx
   }
   __syncthreads();
   const int64_t nbt = (a.rows + kMxBlock - 1) / kMxBlock;
-  const int q = t & 3, c = t >> 2;
-  const int64_t b = r0 / kMxBlock + q, oc = c0 + c;
+  const int q = t & 3, word = t >> 2;
+  const int64_t b = r0 / kMxBlock + q;
+  const int64_t oc = c0 + kPer * word;
   if (b >= nbt || oc >= a.cols) return;
-  const int at = (c + 8 * q) & 63;
-  float v[32];
+  const uint32_t* column = &tile[32 * q][(word + 8 * q) & (kTileWords - 1)];
+  uint32_t x32[32];
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    v[j] = T::f32(tile[32 * q + j][at]);
-    m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    x32[j] = column[j * kTileWords];
+    if constexpr (kPer == 2) m = __vmaxu2(m, x32[j] & 0x7FFF7FFFu);
+    else m = max(m, x32[j] & 0x7FFFFFFFu);
   }
-  const uint32_t s = scale_code(m);
-  const float inv = inverse_scale(s);
-  uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float e[8];
+  for (int h = 0; h < kPer; ++h) {
+    if (oc + h >= a.cols) break;
+    auto value = [&](int j) -> float {
+      if constexpr (kPer == 2) return h ? V::hi(x32[j]) : V::lo(x32[j]);
+      else return __uint_as_float(x32[j]);
+    };
+    uint32_t top;
+    if constexpr (kPer == 2) top = __float_as_uint(h ? V::hi(m) : V::lo(m));
+    else top = m;
+    const uint32_t s = scale_code(top);
+    const float inv = inverse_scale(s);
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = __fmul_rn(v[8 * k + j], inv);
-    w[k] = a.stochastic ? encode8_stochastic(e, (uint64_t)(oc * nbt + b), k, a.seed) : encode8(e);
-    if (s == 255u) w[k] = 0u;
+    for (int k = 0; k < 4; ++k) {
+      float e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = __fmul_rn(value(8 * k + j), inv);
+      w[k] = kStochastic ? encode8_stochastic(e, (uint64_t)((oc + h) * nbt + b), k, a.seed) : encode8(e);
+      if (s == 255u) w[k] = 0u;
+    }
+    *reinterpret_cast<uint4*>(a.out_t.codes + (oc + h) * a.out_t.code_pitch + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+    a.out_t.scales[(oc + h) * a.out_t.scale_pitch + b] = (uint8_t)s;
   }
-  *reinterpret_cast<uint4*>(a.out_t.codes + oc * a.out_t.code_pitch + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
-  a.out_t.scales[oc * a.out_t.scale_pitch + b] = (uint8_t)s;
 }
 
 // --------------------------------------------------------------- read back --
 
+struct TBf16 {
+  using raw = uint16_t;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack2(Bf16::rn(a), Bf16::rn(b)); }
+  static __device__ __forceinline__ raw rn(float x) { return Bf16::rn(x); }
+};
+struct TF16 {
+  using raw = uint16_t;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack2(F16::rn(a), F16::rn(b)); }
+  static __device__ __forceinline__ raw rn(float x) { return F16::rn(x); }
+};
+struct TF32 {
+  using raw = float;
+  static __device__ __forceinline__ raw rn(float x) { return x; }
+};
+
+// As mx_rows_kernel: a lane turns 4 bytes of codes into 8 elements, kUnits
+// pieces of 256 columns side by side.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads) mx_dequant_kernel(const __grid_constant__ MxDequantArgs a,
                                                                  const FastDiv per_row, const uint32_t units, const int vec) {
   using raw = typename T::raw;
+  constexpr int kUnits = 4;
   raw* dst = static_cast<raw*>(a.dst);
   const uint32_t warps = gridDim.x * (kRowThreads / 32);
   const int lane = threadIdx.x & 31;
   for (uint32_t u0 = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += kUnits * warps) {
-    uint32_t w[kUnits], s[kUnits];
-    int64_t row[kUnits], col[kUnits];
+    uint32_t w[kUnits], s[kUnits], row[kUnits];
+    int64_t col[kUnits];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      const uint32_t u = u0 + k * warps;
-      col[k] = a.in.cols;
-      if (u < units) {
-        const uint32_t r = div_by(u, per_row);
-        row[k] = r;
-        col[k] = (int64_t)(u - r * per_row.d) * 256 + lane * 8;
-        if (col[k] < a.in.cols) {
-          w[k] = *reinterpret_cast<const uint32_t*>(a.in.codes + row[k] * a.in.code_pitch + (col[k] >> 1));
-          s[k] = a.in.scales[row[k] * a.in.scale_pitch + (col[k] >> 5)];
-        }
-      }
+      const uint32_t u = min(u0 + k * warps, units - 1);
+      row[k] = div_by(u, per_row);
+      col[k] = (int64_t)(u - row[k] * per_row.d) * 256 + lane * 8;
+      const int64_t at = min(col[k], a.in.cols - 1);  // lanes past the row read its last block, and store nothing
+      w[k] = __ldcs(reinterpret_cast<const uint32_t*>(a.in.codes + row[k] * a.in.code_pitch + ((at >> 3) << 2)));
+      s[k] = a.in.scales[row[k] * a.in.scale_pitch + (at >> 5)];
     }
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      if (col[k] >= a.in.cols) continue;
       uint32_t h[4];
       decode8(w[k], h);
       const float sc = scale_value(s[k]);
@@ -288,7 +322,21 @@ __global__ void __launch_bounds__(kRowThreads) mx_dequant_kernel(const __grid_co
         v[2 * j] = __fmul_rn(f.x, sc);
         v[2 * j + 1] = __fmul_rn(f.y, sc);
       }
-      store8<T>(dst + row[k] * a.ld + col[k], a.in.cols - col[k], vec, v);
+      const int64_t n = u0 + k * warps < units ? a.in.cols - col[k] : 0;
+      raw* p = dst + row[k] * a.ld + col[k];
+      if (n >= 8 && vec) {
+        if constexpr (sizeof(raw) == 2) {
+          st_stream(reinterpret_cast<uint16_t*>(p), make_uint4(T::pack(v[0], v[1]), T::pack(v[2], v[3]), T::pack(v[4], v[5]),
+                                                               T::pack(v[6], v[7])));
+        } else {
+          st_stream(reinterpret_cast<float*>(p), make_float4(v[0], v[1], v[2], v[3]));
+          st_stream(reinterpret_cast<float*>(p) + 4, make_float4(v[4], v[5], v[6], v[7]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) p[j] = T::rn(v[j]);
+      }
     }
   }
 }
@@ -306,14 +354,14 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_consta
   const int64_t n_lanes = ((n_blocks * 4 + 31) / 32) * 32;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n_lanes; i += stride) {
     const int64_t e = i * 8;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    Vec16<F> x;
+    x.clear();
     if (e < a.n) {
       const uint16_t* src = a.uniform ? a.src[0] : a.src[(a.lo + e) / a.shard];
-      x = ld_stream(src + a.lo + e);
+      x.load(src + a.lo + e);
     }
-    float v[8] = {F::lo(x.x), F::hi(x.x), F::lo(x.y), F::hi(x.y), F::lo(x.z), F::hi(x.z), F::lo(x.w), F::hi(x.w)};
-    uint32_t s;
-    const uint32_t w = encode_quarter(v, 0, 0, 0, 0, s);
+    const uint32_t s = scale_code(max_of_four(x.max_bits()));
+    const uint32_t w = encode<false>(x, s, 0, 0, 0);
     if ((i >> 2) < n_blocks) {
       for (int r = 0; r < a.n_ranks; ++r) {
         *reinterpret_cast<uint32_t*>(a.codes[r] + 4 * i) = w;
@@ -325,14 +373,30 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_consta
 
 // ---------------------------------------------------------- reduce-scatter --
 
+// The square of an averaged gradient, added in binary64 as mean_bf16 does.
+// The widening to binary64 is put together from the bits of a normal number
+// (whose value has at most 11 significant bits): the conversion instruction
+// shares a unit of 16 a clock with the decoding, which needs all of it.
+__device__ __forceinline__ void add_square(float g, double& sq, unsigned& nf) {
+  const uint32_t m = __float_as_uint(g) & 0x7FFFFFFFu;
+  if (m - 0x00800000u < 0x7F000000u) {
+    const double d = __hiloint2double((int)((m >> 3) + 0x38000000u), (int)(m << 29));
+    sq = __fma_rn(d, d, sq);  // the square is exact, so one rounding as with a separate product
+  } else if (m != 0u) {
+    const double d = (double)g;
+    sq = __dadd_rn(sq, __dmul_rn(d, d));
+    nf += m >= 0x7F800000u ? 1u : 0u;
+  }
+}
+
 // A lane sums 8 elements (4 bytes of codes and the block's scale byte from
-// each rank), in rank order.  element * scale is exact in binary32 (three
-// significant bits), so the fused multiply-add rounds once, as adding the
-// element's value does.
+// each rank), in rank order; eight ranks' loads are out at a time.
+// element * scale is exact in binary32 (three significant bits), so the fused
+// multiply-add rounds once, as adding the element's value does.
 template <class F>
 __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_constant__ MxReduceArgs a) {
   double sq = 0.0;
-  unsigned long long nf = 0;
+  unsigned nf = 0;
   const int64_t stride = (int64_t)gridDim.x * kThreads;
   const int64_t n_vec = a.n / kVec;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n_vec; i += stride) {
@@ -342,11 +406,13 @@ __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_consta
     for (int r0 = 0; r0 < a.n_ranks; r0 += 8) {
       uint32_t w[8], s[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < 8; ++k) {
+        w[k] = 0u, s[k] = 127u;
         if (r0 + k < a.n_ranks) {
           w[k] = __ldcs(reinterpret_cast<const uint32_t*>(a.codes[r0 + k]) + i);
-          s[k] = a.scales[r0 + k][i >> 2];
+          s[k] = __ldcs(a.scales[r0 + k] + (i >> 2));
         }
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (r0 + k < a.n_ranks) {
@@ -362,11 +428,14 @@ __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_consta
         }
     }
     uint16_t g16[kVec];
-    float g[kVec];
-    mean_bf16<F>(acc, a.inv_n, g16, g, sq, nf);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      g16[j] = F::rn(__fmul_rn(acc[j], a.inv_n));
+      add_square(F::f32(g16[j]), sq, nf);
+    }
     st_stream(a.shard_out + i * kVec, pack8(g16));
   }
-  norm_epilogue<kThreads>(a.ns, sq, nf, a.accumulate);
+  norm_epilogue<kThreads>(a.ns, sq, (unsigned long long)nf, a.accumulate);
 }
 
 int cap_grid(int64_t want, int cap) { return (int)std::max<int64_t>(1, std::min<int64_t>(want, cap)); }
@@ -393,32 +462,42 @@ bool pieces_of(int64_t rows, int64_t cols, bool end_to_end, Pieces* p) {
   return true;
 }
 
-template <class T>
+template <class V>
 cudaError_t quantize_rows(MxQuantArgs a, int sm_count, cudaStream_t s) {
   const bool flat = a.cols % kMxBlock == 0 && a.ld == a.cols && a.out.code_pitch == a.cols / 2 &&
                     a.out.scale_pitch == a.cols / kMxBlock;
   Pieces p;
   if (!pieces_of(a.rows, a.cols, flat, &p)) return cudaErrorInvalidValue;
   a.rows = p.rows, a.cols = p.cols;
-  const int vec = aligned(a.src, flat ? 0 : a.ld * (int64_t)sizeof(typename T::raw)) ? 1 : 0;
-  const int per_cta = kUnits * kRowThreads / 32;
-  mx_rows_kernel<T><<<cap_grid((p.units + per_cta - 1) / per_cta, 8 * sm_count), kRowThreads, 0, s>>>(a, p.per_row,
-                                                                                                     p.units, vec);
+  const int vec = aligned(a.src, flat ? 0 : a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
+  const int per_cta = V::kUnits * kRowThreads / 32;
+  const int grid = cap_grid((p.units + per_cta - 1) / per_cta, 8 * sm_count);
+  if (a.stochastic) mx_rows_kernel<V, true><<<grid, kRowThreads, 0, s>>>(a, p.per_row, p.units, vec);
+  else mx_rows_kernel<V, false><<<grid, kRowThreads, 0, s>>>(a, p.per_row, p.units, vec);
   return cudaGetLastError();
 }
 
-template <class T, bool kFromMx>
+template <class V, bool kFromMx>
 cudaError_t quantize_tiles(const MxQuantArgs& a, cudaStream_t s) {
-  const int64_t tx = (a.cols + kTileCols - 1) / kTileCols, ty = (a.rows + kTileRows - 1) / kTileRows;
+  constexpr int kCols = kTileWords * 4 / (int)sizeof(typename V::raw);
+  const int64_t tx = (a.cols + kCols - 1) / kCols, ty = (a.rows + kTileRows - 1) / kTileRows;
   if (tx * ty > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const int vec = kFromMx || aligned(a.src, a.ld * (int64_t)sizeof(typename T::raw)) ? 1 : 0;
-  mx_tile_kernel<T, kFromMx><<<(unsigned)(tx * ty), 256, 0, s>>>(a, (uint32_t)tx, vec);
+  const int vec = kFromMx || aligned(a.src, a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
+  const unsigned grid = (unsigned)(tx * ty);
+  const uint32_t x = (uint32_t)tx;
+  if (a.out.codes) {
+    if (a.stochastic) mx_tile_kernel<V, kFromMx, true, true><<<grid, 256, 0, s>>>(a, x, vec);
+    else mx_tile_kernel<V, kFromMx, true, false><<<grid, 256, 0, s>>>(a, x, vec);
+  } else {
+    if (a.stochastic) mx_tile_kernel<V, kFromMx, false, true><<<grid, 256, 0, s>>>(a, x, vec);
+    else mx_tile_kernel<V, kFromMx, false, false><<<grid, 256, 0, s>>>(a, x, vec);
+  }
   return cudaGetLastError();
 }
 
-template <class T>
+template <class V>
 cudaError_t quantize_from(const MxQuantArgs& a, int sm_count, cudaStream_t s) {
-  return a.out_t.codes ? quantize_tiles<T, false>(a, s) : quantize_rows<T>(a, sm_count, s);
+  return a.out_t.codes ? quantize_tiles<V, false>(a, s) : quantize_rows<V>(a, sm_count, s);
 }
 
 template <class T>
@@ -429,7 +508,7 @@ cudaError_t dequantize_to(MxDequantArgs a, int sm_count, cudaStream_t s) {
   if (!pieces_of(a.in.rows, a.in.cols, flat, &p)) return cudaErrorInvalidValue;
   a.in.rows = p.rows, a.in.cols = p.cols;
   const int vec = aligned(a.dst, flat ? 0 : a.ld * (int64_t)sizeof(typename T::raw)) ? 1 : 0;
-  const int per_cta = kUnits * kRowThreads / 32;
+  const int per_cta = 4 * kRowThreads / 32;
   mx_dequant_kernel<T><<<cap_grid((p.units + per_cta - 1) / per_cta, 8 * sm_count), kRowThreads, 0, s>>>(
       a, p.per_row, p.units, vec);
   return cudaGetLastError();
@@ -438,11 +517,11 @@ cudaError_t dequantize_to(MxDequantArgs a, int sm_count, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, int sm_count, cudaStream_t s) {
-  if (a.from.codes) return quantize_tiles<TBf16, true>(a, s);
+  if (a.from.codes) return quantize_tiles<Vec16<Bf16>, true>(a, s);  // an MX4 matrix's transpose
   switch (a.type) {
-    case kMxBf16: return quantize_from<TBf16>(a, sm_count, s);
-    case kMxF16: return quantize_from<TF16>(a, sm_count, s);
-    case kMxF32: return quantize_from<TF32>(a, sm_count, s);
+    case kMxBf16: return quantize_from<Vec16<Bf16>>(a, sm_count, s);
+    case kMxF16: return quantize_from<Vec16<F16>>(a, sm_count, s);
+    case kMxF32: return quantize_from<Vec32>(a, sm_count, s);
     default: return cudaErrorInvalidValue;
   }
 }
