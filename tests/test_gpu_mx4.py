@@ -237,3 +237,376 @@ def test_matmul_without_columns_or_rows(z):
     assert z.mx4_matmul(z.mx4_empty(0, 64), z.mx4_empty(5, 64)).shape == (0, 5)
     assert z.mx4_linear(torch.empty(0, 64, device="cuda"), z.mx4_empty(5, 64)).shape == (0, 5)
     assert z.mx4_quantize(torch.empty(0, 64, device="cuda")).rows == 0
+
+
+# ------------------------------------------------------------------- linear --
+
+LINEAR = [(1, 128, 32), (1, 2304, 768), (1, 1000, 771), (3, 300, 256), (16, 640, 512), (17, 640, 544), (100, 768, 2304),
+          (257, 513, 1000), (1000, 2304, 768), (2300, 2200, 512)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("tokens,out,inner", LINEAR)
+def test_linear_is_quantize_and_matmul(z, dtype, tokens, out, inner):
+    x = _normal(tokens, inner, dtype, tokens)
+    x[tokens // 2:] *= 0 if tokens > 4 else 1  # padded tokens
+    w = z.mx4_quantize(_normal(out, inner, "bf16", out, 0.02))
+    xq = z.mx4_quantize(x)
+    y = z.mx4_linear(x, w)
+    assert y.dtype == x.dtype and torch.equal(y, z.mx4_matmul(xq, w, x.dtype))
+    _assert_product(y, xq, w, "linear")
+    # a weight whose scale rows lie end to end, and rows of x apart
+    tight = z.MX4(w.codes, w.scales[:, :ref.blocks_of(inner)].contiguous(), out, inner)
+    wide = torch.zeros(tokens, inner + 5, dtype=x.dtype, device="cuda")
+    wide[:, :inner] = x
+    assert torch.equal(z.mx4_linear(wide[:, :inner], tight), y)
+
+
+def test_linear_wants_no_more_than_its_workspace(z):
+    """The bytes around the workspace, the operands and the result stay."""
+    import ctypes
+
+    for tokens, out, inner, pitch in ((1, 300, 771, 25), (40, 300, 768, 24), (700, 2600, 800, 25), (1, 256, 512, 16)):
+        x = _normal(tokens, inner, "bf16", 3)
+        c, s = ref.pack(*ref.quantize(_normal(out, inner, "f32", 4, 0.02)), scale_pitch=pitch)
+        w = z.MX4(c, s, out, inner)
+        need = ctypes.c_int64()
+        assert z.zero_mx4_linear_workspace(tokens, w._c, need) == 0
+        space = torch.full((need.value + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        y = torch.full((tokens + 2, out), 3.0, dtype=torch.bfloat16, device="cuda")
+        at = space.data_ptr() + 256
+        args = (x.data_ptr(), z.ZERO_DTYPE_BF16, tokens, inner, w._c, y[1:].data_ptr(), z.ZERO_DTYPE_BF16, out, at)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert z.zero_mx4_linear(*args, need.value - 1, stream) == z.ZERO_EINVAL
+        assert z.zero_mx4_linear(*args[:-1], None, need.value, stream) == z.ZERO_EINVAL
+        assert z.zero_mx4_linear(*args[:-1], at + 8, need.value, stream) == z.ZERO_EINVAL
+        assert z.zero_mx4_linear(*args, need.value, stream) == 0
+        assert torch.equal(y[1:-1], z.mx4_linear(x, w))
+        assert (y[0] == 3).all() and (y[-1] == 3).all()
+        assert (space[:256] == 0xA5).all() and (space[256 + need.value:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,out,inner", [(1, 64, 32), (33, 100, 77), (300, 768, 256), (1003, 520, 384)])
+@pytest.mark.parametrize("seed", [None, 12345])
+def test_linear_backward(z, dtype, tokens, out, inner, seed):
+    x, dy = _normal(tokens, inner, dtype, 1), _normal(tokens, out, dtype, 2, 0.25)
+    w = z.mx4_quantize(_normal(out, inner, "bf16", 3, 0.02))
+    dx, dw = z.mx4_linear_backward(dy, x, w, seed=seed)
+    dyq, dyq_t = z.mx4_quantize_both(dy, seed)
+    _assert_mx4(dyq, *ref.quantize(dy, seed), "dy")
+    _assert_mx4(dyq_t, *ref.quantize(dy.t(), seed), "dy^T")
+    _assert_product(dx, dyq, z.mx4_transpose(w), "dx")
+    _assert_product(dw, dyq_t, z.mx4_quantize(x, transpose=True), "dw")
+    assert dx.shape == x.shape and dw.shape == (out, inner)
+
+
+def test_linear_backward_against_differences(z):
+    """On inputs that every quantisation keeps exactly -- whole numbers of
+    magnitude 4 or 6 or 0, one of them in each block along either axis, so
+    that every block's scale is 1 -- y is linear in x and in w, and its
+    differences are the gradients, exactly."""
+    t, o, k = 64, 96, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def pick(rows, cols):
+        v = torch.tensor([4.0, -4.0, 6.0, -6.0], device="cuda")
+        return v[torch.randint(0, 4, (rows, cols), generator=g, device="cuda")]
+
+    x, wv, dy = pick(t, k), pick(o, k), pick(t, o)
+    w = z.mx4_quantize(wv)
+    dx, dw = z.mx4_linear_backward(dy, x, w, dx=torch.empty(t, k, device="cuda"), dw=torch.empty(o, k, device="cuda"))
+    loss = lambda x, w: (z.mx4_linear(x, w).double() * dy.double()).sum()  # noqa: E731
+    for i, j in ((0, 0), (5, 77), (63, 127)):
+        moved = x.clone()
+        moved[i, j] = -moved[i, j]
+        assert float(loss(moved, w) - loss(x, w)) == float((moved - x)[i, j] * dx[i, j])
+    for i, j in ((0, 0), (50, 3), (95, 127)):
+        moved = wv.clone()
+        moved[i, j] = -moved[i, j]
+        assert float(loss(x, z.mx4_quantize(moved)) - loss(x, w)) == float((moved - wv)[i, j] * dw[i, j])
+
+
+# -------------------------------------------------------------- collectives --
+
+def _context(z, stage, n_ranks, numel, dtype="bf16", seed=0, **kw):
+    opt = z.ZeroOptimizer([n for n, _ in numel], [layer for _, layer in numel], n_ranks, stage,
+                          dtype=z.ZERO_DTYPE_F16 if dtype == "f16" else z.ZERO_DTYPE_BF16, **kw)
+    master = opt.view(z.ZERO_VIEW_MASTER)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    master.copy_(0.02 * torch.randn(opt.psi_pad, generator=g, device="cuda"))
+    opt.load_master()
+    return opt
+
+
+@pytest.mark.parametrize("stage", [1, 2, 3])
+@pytest.mark.parametrize("n_ranks", [1, 3, 8, 11])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_all_gather_quantises_the_owners_parameters(z, stage, n_ranks, dtype):
+    """Every rank's buffers, every shard boundary, a ragged last block, guard
+    bytes after each buffer; the replicas of stages 1 and 2 differ here, so
+    that only the owner's copy gives the right answer."""
+    opt = _context(z, stage, n_ranks, [(1000, 0), (333, 0), (4100, 1)], dtype)
+    S = opt.shard
+    if stage == 3:
+        flat = opt.view(z.ZERO_VIEW_PARAM).view(DTYPES[dtype])
+    else:
+        for r in range(n_ranks):
+            own = opt.view(z.ZERO_VIEW_PARAM, r).view(DTYPES[dtype])
+            own[:r * S] = 9.0
+            own[(r + 1) * S:] = 9.0
+        flat = torch.cat([opt.view(z.ZERO_VIEW_PARAM, r).view(DTYPES[dtype])[r * S:(r + 1) * S] for r in range(n_ranks)])
+    for lo, hi in ((0, opt.psi_pad), (8, 8), (8, 16), (1000, 1336), (16, opt.psi_pad - 8)):
+        nb = ref.blocks_of(hi - lo)
+        codes = torch.full((n_ranks, 16 * nb + 64), 0xA5, dtype=torch.uint8, device="cuda")
+        scales = torch.full((n_ranks, nb + 64), 0xA5, dtype=torch.uint8, device="cuda")
+        opt.all_gather_mx4(lo, hi, codes, scales)
+        if hi == lo:
+            assert (codes == 0xA5).all()
+            continue
+        want = ref.quantize(flat[lo:hi].view(1, -1))
+        for r in range(n_ranks):
+            m = z.MX4(codes[r, :16 * nb].view(1, -1), scales[r, :nb].view(1, -1), 1, hi - lo)
+            _assert_mx4(m, *want, f"rank {r} of [{lo}, {hi})")
+        assert (codes[:, 16 * nb:] == 0xA5).all() and (scales[:, nb:] == 0xA5).all()
+    opt.close()
+
+
+@pytest.mark.parametrize("stage", [2, 3])
+@pytest.mark.parametrize("n_ranks", [1, 2, 8, 9, 16, 19])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_reduce_scatter_gives_the_bits_of_the_16_bit_one(z, stage, n_ranks, dtype):
+    """The same shard, norm and non-finite count as zero_reduce_scatter of the
+    gradients read back (exact in bf16; in binary16 for values of this size).
+    The norm's partial sums are added in another order."""
+    opt = _context(z, stage, n_ranks, [(4096 + 8 * 37, 0)], dtype, grad_buffers=False)
+    lo, hi = 16, opt.psi_pad - 8
+    nb = ref.blocks_of(hi - lo)
+    codes = torch.empty(n_ranks, 16 * nb, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(n_ranks, nb, dtype=torch.uint8, device="cuda")
+    dense = torch.zeros(n_ranks, hi - lo, dtype=DTYPES[dtype], device="cuda")
+    for r in range(n_ranks):
+        x = _normal(1, hi - lo, "f32", 100 + r, 2.0 ** (r % 5))
+        x[0, 64:96] = 0.0
+        if r == n_ranks - 1:
+            x[0, 200] = float("nan")
+        m = z.MX4(codes[r].view(1, -1), scales[r].view(1, -1), 1, hi - lo)
+        z.mx4_quantize(x, seed=r, out=m)
+        z.mx4_dequantize(m, out=dense[r].view(1, -1))
+    shard = opt.view(z.ZERO_VIEW_GRAD_SHARD)
+    shard.fill_(77)
+    opt.reduce_scatter_mx4(lo, hi, codes, scales)
+    got, stats = shard.clone(), opt.read_stats()
+    shard.fill_(77)
+    opt.load_master()
+    shard.fill_(77)
+    opt.reduce_scatter(lo, hi, [d.data_ptr() for d in dense])
+    want = opt.read_stats()
+    a, b = got.view(DTYPES[dtype]), shard.view(DTYPES[dtype])
+    assert torch.equal(torch.where(a.isnan(), 0, got), torch.where(b.isnan(), 0, shard))
+    assert torch.equal(a.isnan(), b.isnan()) and int(a[lo:hi].isnan().sum()) == 32
+    assert (got[:lo] == 77).all() and (got[hi:] == 77).all()
+    assert stats["nonfinite"] == want["nonfinite"] == 32
+    opt.close()
+
+
+@pytest.mark.parametrize("top", [1, 130, 239, 240, 241, 252, 254])
+def test_reduce_scatter_over_the_whole_range_of_scales(z, top):
+    """Scales from the least to the greatest, in bf16's own range; sums that
+    overflow become infinite as the 16-bit sum's do."""
+    n, n_ranks = 1024, 3
+    opt = _context(z, 2, n_ranks, [(n, 0)], grad_buffers=False)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(top)
+    code = torch.randint(0, 16, (n_ranks, n // 32, 32), generator=g, device="cuda")
+    s = torch.randint(max(0, top - 3), top + 1, (n_ranks, n // 32), generator=g, device="cuda")
+    codes, scales = ref.pack(code, s)
+    dense = ref.values(code, s, n).to(torch.bfloat16).contiguous()
+    opt.reduce_scatter_mx4(0, n, codes, scales)
+    got = opt.view(z.ZERO_VIEW_GRAD_SHARD)[:n].clone()
+    opt.reduce_scatter(0, n, [d.data_ptr() for d in dense])
+    want = opt.view(z.ZERO_VIEW_GRAD_SHARD)[:n]
+    a, b = got.view(torch.bfloat16), want.view(torch.bfloat16)
+    assert torch.equal(a.isnan(), b.isnan())
+    assert torch.equal(torch.where(a.isnan(), 0, got), torch.where(b.isnan(), 0, want))
+    opt.close()
+
+
+def test_collectives_norm_is_the_sum_over_intervals(z):
+    """Two intervals of one step add up; the norm is that of the stored means."""
+    opt = _context(z, 2, 4, [(8192, 0)], grad_buffers=False)
+    total = 0.0
+    for lo, hi in ((0, 4096), (4096, 8192)):
+        codes, scales = [], []
+        for r in range(4):
+            m = z.mx4_quantize(_normal(1, hi - lo, "f32", r + lo, 0.01))
+            codes.append(m.codes.reshape(-1).contiguous())
+            scales.append(m.scales[0, :128].contiguous())
+        opt.reduce_scatter_mx4(lo, hi, codes, scales)
+        total += float(opt.view(z.ZERO_VIEW_GRAD_SHARD)[lo:hi].view(torch.bfloat16).double().square().sum())
+    assert abs(opt.read_stats()["grad_norm"] - total ** 0.5) <= 1e-12 * total ** 0.5
+    opt.close()
+
+
+def test_collectives_refuse(z):
+    opt = _context(z, 2, 2, [(4096, 0)])
+    good_c, good_s = torch.empty(2, 2048, dtype=torch.uint8, device="cuda"), torch.empty(2, 128, dtype=torch.uint8, device="cuda")
+    for call in (opt.all_gather_mx4, opt.reduce_scatter_mx4):
+        for lo, hi in ((4, 64), (0, 4), (0, 8192), (-8, 8), (64, 32)):
+            with pytest.raises((z.ZeroError, ValueError)):
+                call(lo, hi, good_c, good_s)
+        with pytest.raises(ValueError, match="buffers for 2 ranks"):
+            call(0, 4096, good_c[:1], good_s[:1])
+        with pytest.raises(ValueError, match="bytes a rank"):
+            call(0, 4096, good_c[:, :1024].contiguous(), good_s)
+        with pytest.raises(ValueError, match="contiguous"):
+            call(0, 32, good_c[:, ::2], good_s)
+        with pytest.raises(ValueError, match="uint8"):
+            call(0, 4096, good_c.view(torch.int8), good_s)
+        with pytest.raises(z.ZeroError, match="16-byte"):
+            call(0, 32, [good_c[0, 8:], good_c[1]], [good_s[0], good_s[1]])
+    opt.close()
+    opt = _context(z, 1, 2, [(4096, 0)])
+    with pytest.raises(z.ZeroError, match="stage 1"):
+        opt.reduce_scatter_mx4(0, 4096, good_c, good_s)
+    opt.close()
+    opt = _context(z, 2, 2, [(4096, 0)], keep_grad_shards=False)
+    with pytest.raises(z.ZeroError, match="dropped"):
+        opt.reduce_scatter_mx4(0, 4096, good_c, good_s)
+    opt.close()
+
+
+# ------------------------------------------------- streams, graphs, devices --
+
+def test_captured_and_replayed(z):
+    """A captured linear layer forward and backward, replayed on new inputs,
+    beside a second graph and eager calls."""
+    t, o, k = 200, 2304, 768
+    w = z.mx4_quantize(_normal(o, k, "bf16", 1, 0.02))
+    tight = z.MX4(w.codes, w.scales[:, :24].contiguous(), o, k)
+    x, dy = _normal(t, k, "bf16", 2), _normal(t, o, "bf16", 3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        z.mx4_linear(x, tight), z.mx4_linear_backward(dy, x, tight)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for weight in (w, tight):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = z.mx4_linear(x, weight)
+            one = z.mx4_linear(x[:1], weight)
+            dx, dw = z.mx4_linear_backward(dy, x, weight)
+        graphs.append((g, y, one, dx, dw))
+    for seed in (5, 6, 7):
+        x.copy_(_normal(t, k, "bf16", seed))
+        dy.copy_(_normal(t, o, "bf16", seed + 50))
+        want = (z.mx4_linear(x, w), z.mx4_linear(x[:1], w), *z.mx4_linear_backward(dy, x, w))
+        for g, *outs in graphs:
+            g.replay()
+        for _, *outs in graphs:
+            for a, b in zip(outs, want):
+                assert torch.equal(a, b)
+
+
+def test_two_streams_at_once_and_a_stream_argument(z):
+    """Products of many shapes on two streams side by side, each given its
+    stream explicitly while another one is current."""
+    shapes = [(1, 2304, 768), (100, 1000, 771), (1000, 2304, 768), (16, 4096, 512)]
+    ws = [z.mx4_quantize(_normal(o, k, "bf16", o, 0.02)) for _, o, k in shapes]
+    xs = [_normal(t, k, "bf16", t) for t, _, k in shapes]
+    want = [z.mx4_linear(x, w) for x, w in zip(xs, ws)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            got[i] = [z.mx4_linear(x, w, stream=s) for x, w in zip(xs, ws)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b in zip(got[i], want):
+            assert torch.equal(a, b)
+
+
+def test_linear_right_after_its_operands_are_written(z):
+    """The product's early loads of w must not run ahead of the work that
+    writes w: all-gather and product in one stream, new parameters each time."""
+    o, k, n_ranks = 2304, 768, 4
+    opt = _context(z, 3, n_ranks, [(o * k, 0)], seed=3)
+    x = _normal(1, k, "bf16", 1)
+    codes = torch.zeros(n_ranks, o, k // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n_ranks, o, k // 32, dtype=torch.uint8, device="cuda")
+    params = opt.view(z.ZERO_VIEW_PARAM)
+    news = [_normal(1, o * k, "bf16", 20 + i, 0.02)[0] for i in range(6)]
+    got = []
+    for p in news:
+        params[:o * k].view(torch.bfloat16).copy_(p)
+        opt.all_gather_mx4(0, o * k, codes, scales)
+        got.append([z.mx4_linear(x, z.MX4(c, s, o, k)) for c, s in zip(codes, scales)])
+    for p, ys in zip(news, got):
+        want = z.mx4_linear(x, z.mx4_quantize(p.view(o, k)))
+        for y in ys:
+            assert torch.equal(y, want)
+    opt.close()
+
+
+def test_wrappers_refuse_what_does_not_fit(z):
+    w = z.mx4_empty(64, 96)
+    with pytest.raises(ValueError, match="inputs"):
+        z.mx4_linear(torch.zeros(3, 64, device="cuda"), w)
+    with pytest.raises(ValueError, match="out is"):
+        z.mx4_linear(torch.zeros(3, 96, device="cuda"), w, out=torch.zeros(3, 65, device="cuda"))
+    with pytest.raises(ValueError, match="needed"):
+        z.mx4_quantize(torch.zeros(3, 96, device="cuda", dtype=torch.float64))
+    with pytest.raises(ValueError, match="contiguous"):
+        z.mx4_quantize(torch.zeros(96, 3, device="cuda").t())
+    with pytest.raises(ValueError, match="CUDA matrix"):
+        z.mx4_quantize(torch.zeros(96, device="cuda"))
+    with pytest.raises(ValueError, match="out is"):
+        z.mx4_quantize(torch.zeros(3, 96, device="cuda"), out=w)
+    with pytest.raises(z.ZeroError, match="columns"):
+        z.mx4_matmul(w, z.mx4_empty(64, 128))
+    with pytest.raises(ValueError, match="fit"):
+        z.mx4_linear_backward(torch.zeros(3, 60, device="cuda"), torch.zeros(3, 96, device="cuda"), w)
+
+
+# --------------------------------------------------------- all of them together --
+
+def test_a_training_step_in_four_bits(z):
+    """ZeRO-3 training steps of one linear layer over four ranks: the layer is
+    gathered in MX4, each rank's forward and backward read it, the gradients
+    go out stochastically rounded, are reduce-scattered from MX4 and applied.
+    Every part against plain arithmetic on the library's own inputs to it."""
+    n_ranks, t, o, k = 4, 96, 256, 512
+    opt = _context(z, 3, n_ranks, [(o * k, 0)], seed=11, grad_buffers=False)
+    codes = torch.empty(n_ranks, o, k // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(n_ranks, o, k // 32, dtype=torch.uint8, device="cuda")
+    gcodes, gscales = torch.empty_like(codes), torch.empty_like(scales)
+    target = 0.02 * torch.randn(o, k, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    for step in range(1, 4):
+        opt.all_gather_mx4(0, o * k, codes, scales)
+        params = opt.view(z.ZERO_VIEW_PARAM)[:o * k].view(torch.bfloat16).view(o, k)
+        sent = torch.zeros(o, k, device="cuda")  # binary32, in rank order
+        for r in range(n_ranks):
+            w = z.MX4(codes[r], scales[r], o, k)
+            _assert_mx4(w, *ref.quantize(params), "gathered layer")
+            x = _normal(t, k, "bf16", 10 * step + r)
+            y = z.mx4_linear(x, w)
+            _assert_product(y, z.mx4_quantize(x), w, "forward")
+            dy = ((y.float() - x.float() @ target.t()) / t).to(torch.bfloat16)
+            dx, dw = z.mx4_linear_backward(dy, x, w, seed=step)
+            assert dx.shape == x.shape and torch.isfinite(dx).all()
+            g = z.MX4(gcodes[r], gscales[r], o, k)
+            z.mx4_quantize(dw, seed=1000 * step + r, out=g)
+            _assert_mx4(g, *ref.quantize(dw, 1000 * step + r), "sent gradient")
+            sent = sent + ref.read(g).float()
+        opt.reduce_scatter_mx4(0, o * k, gcodes, gscales)
+        shard = opt.view(z.ZERO_VIEW_GRAD_SHARD)[:o * k].view(torch.bfloat16).view(o, k)
+        assert torch.equal(shard, (sent * 0.25).to(torch.bfloat16))
+        before = opt.view(z.ZERO_VIEW_MASTER).clone()
+        opt.adam_shard(-1)
+        assert opt.t == step and not torch.equal(before, opt.view(z.ZERO_VIEW_MASTER))
+    opt.close()
+    z.mx4_check()

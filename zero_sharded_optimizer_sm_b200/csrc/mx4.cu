@@ -188,16 +188,17 @@ __global__ void __launch_bounds__(256, 3) mx_tile_kernel(const __grid_constant__
     if constexpr (kFromMx) {
       // the elements' values are exact in bf16: three significant bits and
       // the same exponent range as binary32
-      uint32_t h[4] = {0u, 0u, 0u, 0u};
-      float sc = 0.0f;
+      uint32_t w = 0u, sc = 0u;
       if (left > 0) {
-        decode8(*reinterpret_cast<const uint32_t*>(a.from.codes + row * a.from.code_pitch + (col >> 1)), h);
-        sc = scale_value(a.from.scales[row * a.from.scale_pitch + (col >> 5)]);
+        w = *reinterpret_cast<const uint32_t*>(a.from.codes + row * a.from.code_pitch + (col >> 1));
+        sc = a.from.scales[row * a.from.scale_pitch + (col >> 5)];
       }
+      float2 e[4];
+      values8(w, sc, e);
+      const float v[8] = {e[0].x, e[1].x, e[2].x, e[3].x, e[0].y, e[1].y, e[2].y, e[3].y};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 f = half2_float2(h[j]);
-        x[i].w[j] = pack2(Bf16::rn(__fmul_rn(f.x, sc)), Bf16::rn(__fmul_rn(f.y, sc)));
+        x[i].w[j] = pack2(Bf16::rn(v[2 * j]), Bf16::rn(v[2 * j + 1]));
         if (2 * j + 1 >= left) x[i].w[j] = 2 * j >= left ? 0u : x[i].w[j] & 0xFFFFu;
       }
     } else {
@@ -312,16 +313,9 @@ __global__ void __launch_bounds__(kRowThreads) mx_dequant_kernel(const __grid_co
     }
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      uint32_t h[4];
-      decode8(w[k], h);
-      const float sc = scale_value(s[k]);
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = half2_float2(h[j]);
-        v[2 * j] = __fmul_rn(f.x, sc);
-        v[2 * j + 1] = __fmul_rn(f.y, sc);
-      }
+      float2 e[4];
+      values8(w[k], s[k], e);
+      const float v[8] = {e[0].x, e[1].x, e[2].x, e[3].x, e[0].y, e[1].y, e[2].y, e[3].y};
       const int64_t n = u0 + k * warps < units ? a.in.cols - col[k] : 0;
       raw* p = dst + row[k] * a.ld + col[k];
       if (n >= 8 && vec) {
@@ -389,7 +383,7 @@ __device__ __forceinline__ void add_square(float g, double& sq, unsigned& nf) {
   }
 }
 
-// A lane sums 8 elements (4 bytes of codes and the block's scale byte from
+// A lane sums 16 elements (8 bytes of codes and the block's scale byte from
 // each rank), in rank order; eight ranks' loads are out at a time.
 // element * scale is exact in binary32 (three significant bits), so the fused
 // multiply-add rounds once, as adding the element's value does.
@@ -398,42 +392,58 @@ __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_consta
   double sq = 0.0;
   unsigned nf = 0;
   const int64_t stride = (int64_t)gridDim.x * kThreads;
-  const int64_t n_vec = a.n / kVec;
+  const int64_t n_vec = (a.n + 15) / 16;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n_vec; i += stride) {
-    float acc[kVec];
+    float2 acc[8];  // elements p and p + 4 of the first eight, then of the second
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.0f, 0.0f);
     for (int r0 = 0; r0 < a.n_ranks; r0 += 8) {
-      uint32_t w[8], s[8];
+      uint2 w[8];
+      uint32_t s[8], top = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        w[k] = 0u, s[k] = 127u;
+        w[k] = make_uint2(0u, 0u), s[k] = 0u;
         if (r0 + k < a.n_ranks) {
-          w[k] = __ldcs(reinterpret_cast<const uint32_t*>(a.codes[r0 + k]) + i);
-          s[k] = __ldcs(a.scales[r0 + k] + (i >> 2));
+          w[k] = __ldcs(reinterpret_cast<const uint2*>(a.codes[r0 + k]) + i);
+          s[k] = __ldcs(a.scales[r0 + k] + (i >> 1));
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (r0 + k < a.n_ranks) {
-          uint32_t h[4];
-          decode8(w[k], h);
-          const float sc = scale_value(s[k]);
+      for (int k = 0; k < 8; ++k) top = max(top, s[k]);
+      if (top <= kPlainScale) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = half2_float2(h[j]);
-            acc[2 * j] = __fmaf_rn(f.x, sc, acc[2 * j]);
-            acc[2 * j + 1] = __fmaf_rn(f.y, sc, acc[2 * j + 1]);
+        for (int k = 0; k < 8; ++k)
+          if (r0 + k < a.n_ranks) {
+            uint32_t h[8];
+            decode8_pairs(w[k].x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
+            decode8_pairs(w[k].y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
+            const float sc = scale_value_up(s[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = fma2(half2_float2(h[j]), make_float2(sc, sc), acc[j]);
           }
-        }
-    }
-    uint16_t g16[kVec];
+      } else {  // a scale near the top of the range, or NaN
+#pragma unroll 1
+        for (int k = 0; k < 8 && r0 + k < a.n_ranks; ++k) {
+          float2 v[8];
+          values8(w[k].x, s[k], reinterpret_cast<float2(&)[4]>(v[0]));
+          values8(w[k].y, s[k], reinterpret_cast<float2(&)[4]>(v[4]));
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      g16[j] = F::rn(__fmul_rn(acc[j], a.inv_n));
-      add_square(F::f32(g16[j]), sq, nf);
+          for (int j = 0; j < 8; ++j) acc[j] = make_float2(__fadd_rn(acc[j].x, v[j].x), __fadd_rn(acc[j].y, v[j].y));
+        }
+      }
     }
-    st_stream(a.shard_out + i * kVec, pack8(g16));
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (i * 16 + 8 * g >= a.n) break;
+      uint16_t g16[kVec];
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const float2 t = acc[4 * g + (j & 3)];
+        g16[j] = F::rn(__fmul_rn(j < 4 ? t.x : t.y, a.inv_n));
+        add_square(F::f32(g16[j]), sq, nf);
+      }
+      st_stream(a.shard_out + i * 16 + 8 * g, pack8(g16));
+    }
   }
   norm_epilogue<kThreads>(a.ns, sq, (unsigned long long)nf, a.accumulate);
 }
@@ -543,7 +553,7 @@ cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s
 }
 
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s) {
-  const int grid = cap_grid((a.n / kVec + kThreads - 1) / kThreads, std::min(8 * sm_count, kMaxGrid));
+  const int grid = cap_grid((a.n / 16 + kThreads) / kThreads, std::min(8 * sm_count, kMaxGrid));
   if (a.fmt == kFmtF16) mx_reduce_kernel<F16><<<grid, kThreads, 0, s>>>(a);
   else mx_reduce_kernel<Bf16><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
