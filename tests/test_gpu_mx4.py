@@ -277,9 +277,10 @@ def test_linear_wants_no_more_than_its_workspace(z):
         at = space.data_ptr() + 256
         args = (x.data_ptr(), z.ZERO_DTYPE_BF16, tokens, inner, w._c, y[1:].data_ptr(), z.ZERO_DTYPE_BF16, out, at)
         stream = torch.cuda.current_stream().cuda_stream
-        assert z.zero_mx4_linear(*args, need.value - 1, stream) == z.ZERO_EINVAL
-        assert z.zero_mx4_linear(*args[:-1], None, need.value, stream) == z.ZERO_EINVAL
-        assert z.zero_mx4_linear(*args[:-1], at + 8, need.value, stream) == z.ZERO_EINVAL
+        if need.value:
+            assert z.zero_mx4_linear(*args, need.value - 1, stream) == z.ZERO_EINVAL
+            assert z.zero_mx4_linear(*args[:-1], None, need.value, stream) == z.ZERO_EINVAL
+            assert z.zero_mx4_linear(*args[:-1], at + 8, need.value, stream) == z.ZERO_EINVAL
         assert z.zero_mx4_linear(*args, need.value, stream) == 0
         assert torch.equal(y[1:-1], z.mx4_linear(x, w))
         assert (y[0] == 3).all() and (y[-1] == 3).all()

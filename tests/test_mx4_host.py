@@ -112,8 +112,9 @@ def test_workspace_of_a_matrix(rows, cols, pitch, want):
     assert z.zero_mx4_matmul_workspace(m, other, n) == 0 and n.value == want
     assert z.zero_mx4_matmul_workspace(other, m, n) == 0 and n.value == want
     nb = ref.blocks_of(cols)
-    assert z.zero_mx4_linear_workspace(5, m, n) == 0
-    assert n.value == want + 5 * (16 * nb + (nb + 15) // 16 * 16)
+    assert z.zero_mx4_linear_workspace(40, m, n) == 0
+    assert n.value == want + 40 * (16 * nb + (nb + 15) // 16 * 16)
+    assert z.zero_mx4_linear_workspace(16, m, n) == 0 and n.value == want  # quantised inside the product
 
 
 def test_a_short_workspace_is_refused():

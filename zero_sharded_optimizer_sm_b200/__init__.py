@@ -908,18 +908,24 @@ def mx4_linear(x, w: MX4, out=None, stream=None):
     if inputs != w.cols:
         raise ValueError(f"x has {inputs} inputs, w {w.cols}")
     _need_device(device, "w", w)
-    y = _result(out, tokens, w.rows, x.dtype, device, stream)
     if out is None:
+        y = x.new_empty((tokens, w.rows))
+        if stream is not None:
+            _lend(stream, y)
         yptr, ycode, ldy = y.data_ptr(), code, w.rows
     else:
+        y = _result(out, tokens, w.rows, x.dtype, device, stream)
         yptr, ycode, ldy, _, _ = _dense(y, "out")
     need = ctypes.c_int64()
     _mx4_check(zero_mx4_linear_workspace(tokens, w._c, need), "zero_mx4_linear_workspace")
-    space = _T.empty(need.value, dtype=_T.uint8, device=device)
-    if stream is not None:
-        _lend(stream, space)
-    _mx4_check(_on_device(device, stream, zero_mx4_linear, ptr, code, tokens, ld, w._c, yptr, ycode, ldy,
-                          space.data_ptr(), need.value), "zero_mx4_linear")
+    at, size = None, need.value
+    if size:
+        space = _T.empty(size, dtype=_T.uint8, device=device)
+        at = space.data_ptr()
+        if stream is not None:
+            _lend(stream, space)
+    _mx4_check(_on_device(device, stream, zero_mx4_linear, ptr, code, tokens, ld, w._c, yptr, ycode, ldy, at, size),
+               "zero_mx4_linear")
     return y
 
 

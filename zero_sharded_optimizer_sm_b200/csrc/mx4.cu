@@ -13,92 +13,13 @@
 
 #include "device_math.cuh"
 #include "mx4.cuh"
+#include "mx4_quant.cuh"
 
 namespace zsm {
 namespace {
 
 using namespace dev;
 using namespace mx;
-
-// Eight consecutive elements of a storage type, kept as loaded: their values,
-// and the binary32 pattern of the largest magnitude (an infinity or NaN
-// counts as larger than any number).
-template <class F>
-struct Vec16 {  // bf16 or binary16
-  using raw = uint16_t;
-  static constexpr int kUnits = 4;
-  uint32_t w[4];
-  __device__ __forceinline__ void load(const raw* p) {
-    const uint4 x = ld_stream(p);
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-  }
-  __device__ __forceinline__ void load(const raw* p, int64_t n) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (2 * j < n ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)p[2 * j + 1] << 16 : 0u);
-  }
-  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
-  static __device__ __forceinline__ float lo(uint32_t x) { return F::lo(x); }
-  static __device__ __forceinline__ float hi(uint32_t x) { return F::hi(x); }
-  __device__ __forceinline__ uint32_t max_bits() const {
-    // 16-bit patterns without their signs order as their magnitudes do
-    uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-    m = max(m & 0xFFFFu, m >> 16);
-    return __float_as_uint(F::f32((uint16_t)m));
-  }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[2 * j] = F::lo(w[j]), v[2 * j + 1] = F::hi(w[j]);
-  }
-};
-struct Vec32 {  // binary32
-  using raw = float;
-  static constexpr int kUnits = 2;
-  float x[8];
-  __device__ __forceinline__ void load(const raw* p) {
-    const float4 a = ld_stream(p), b = ld_stream(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  __device__ __forceinline__ void load(const raw* p, int64_t n) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j < n ? p[j] : 0.0f;
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-  }
-  __device__ __forceinline__ uint32_t max_bits() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-    return m;
-  }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = x[j];
-  }
-};
-
-// vec: a whole vector's address is 16-byte aligned.
-template <class V>
-__device__ __forceinline__ void load8(V& x, const typename V::raw* p, int64_t n, int vec) {
-  if (n >= 8 && vec) x.load(p);
-  else if (n > 0) x.load(p, n);
-  else x.clear();
-}
-
-// The codes of eight elements from their block's scale byte.  `block` and c
-// (the vector's place in the block) number the random numbers.
-template <bool kStochastic, class V>
-__device__ __forceinline__ uint32_t encode(const V& x, uint32_t s, uint64_t block, int c, uint64_t seed) {
-  float v[8];
-  x.values(v);
-  const float inv = inverse_scale(s);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
-  const uint32_t w = kStochastic ? encode8_stochastic(v, block, c, seed) : encode8(v);
-  return s == 255u ? 0u : w;
-}
 
 __device__ __forceinline__ uint32_t max_of_four(uint32_t m) {  // over four neighbouring lanes
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));

@@ -96,7 +96,11 @@ struct MxMatmulArgs {
   int64_t ld;
   void* workspace;  // mx_matmul_workspace bytes, 16-byte aligned
   int pdl;  // 1: programmatic launch; the kernel waits for the grid before it before it reads `a`
+  const void* x;    // when set, a's rows x cols as a dense matrix of x_type, which the kernel quantises itself
+  int x_type;       //   (a's codes and scales are not used)
+  int64_t x_ld;
 };
+constexpr int kMxFewRows = 16;  // rows of x that launch_mx_matmul can quantise itself
 
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, int sm_count, cudaStream_t s);

@@ -117,12 +117,13 @@ zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtyp
 }
 
 // zero_mx4_linear's workspace: x's codes, its scales (rows of 16-byte
-// multiples), then the product's own part.
+// multiples) unless the rows are few, then the product's own part.
 zero_mx4 quantised_x(uint8_t* at, int64_t tokens, int64_t inputs) {
   const int64_t nb = zsm::mx_blocks(inputs);
   return {at, at ? at + tokens * 16 * nb : nullptr, tokens, inputs, 16 * nb, align16(nb)};
 }
 int64_t linear_own(int64_t tokens, int64_t inputs) {
+  if (tokens <= zsm::kMxFewRows) return 0;  // quantised inside the product
   const int64_t nb = zsm::mx_blocks(inputs);
   return tokens * (16 * nb + align16(nb));
 }
@@ -259,6 +260,18 @@ zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_
   const zero_mx4 xq = quantised_x(at, tokens, w->cols);
   st = check_workspace(workspace, workspace_bytes, own + zsm::mx_matmul_workspace(matrix(xq), matrix(*w)));
   if (st != ZERO_OK) return st;
+  if (tokens <= zsm::kMxFewRows) {
+    zsm::MxMatmulArgs m = {};
+    m.a = matrix(xq);
+    m.b = matrix(*w);
+    m.out = y, m.type = y_dtype;
+    m.ld = tokens == 1 ? std::max<int64_t>(ld_y, w->rows) : ld_y;
+    m.workspace = at;
+    m.x = x, m.x_type = dtype;
+    m.x_ld = tokens == 1 ? w->cols : ld;
+    const cudaError_t er = zsm::launch_mx_matmul(m, sms, s);
+    return er == cudaSuccess ? ZERO_OK : cuda_fail(er, "MX4 product launch");
+  }
   st = zero_mx4_quantize(x, dtype, tokens, w->cols, ld, ZERO_MX4_NEAREST, 0, &xq, nullptr, stream);
   if (st != ZERO_OK) return st;
   return matmul(xq, *w, y, y_dtype, ld_y, at + own, 1, sms, s);

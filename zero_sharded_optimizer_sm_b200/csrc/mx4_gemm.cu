@@ -35,9 +35,11 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "device_math.cuh"
 #include "mx4.cuh"
+#include "mx4_quant.cuh"
 #include "tma_pipe.cuh"
 
 namespace zsm {
@@ -60,6 +62,9 @@ struct MmArgs {
   void* out;
   int64_t p_stride, q_stride;  // elements between rows of P / of Q in the result
   int type, vec;               // vec: 32-byte stores along q are aligned
+  const void* x;               // Q as a dense matrix (kernels with a vector type V)
+  int64_t x_ld;
+  int x_cols, x_vec;           // x_vec: its vectors are 16-byte aligned
   int pdl;                     // launched early: the grid before this one writes (some of) the operands,
   int p_early;                 //   but not P and its scales
 };
@@ -86,6 +91,10 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
           smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, int cols) {
@@ -392,13 +401,34 @@ struct Shared {
   static_assert(kSets <= STAGES, "a set is written again after its stage's products");
 };
 
-template <int BN, int STAGES, int GROUPS>
+// One block of 32 elements of a dense row, the first `left` of them existing.
+template <class V>
+struct Block {
+  V x[4];
+  __device__ __forceinline__ void load(const typename V::raw* p, int left, int vec) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mx::load8(x[j], p + 8 * j, left - 8 * j, vec);
+  }
+  // Its codes; s: its scale byte.
+  __device__ __forceinline__ uint4 quantize(uint32_t& s) const {
+    s = mx::scale_code(max(max(x[0].max_bits(), x[1].max_bits()), max(x[2].max_bits(), x[3].max_bits())));
+    return make_uint4(mx::encode<false>(x[0], s, 0, 0, 0), mx::encode<false>(x[1], s, 0, 0, 0),
+                      mx::encode<false>(x[2], s, 0, 0, 0), mx::encode<false>(x[3], s, 0, 0, 0));
+  }
+};
+
+// V: void when Q is an MX4 matrix; else the vector type of the dense matrix
+// that Q is (at most 16 rows), which the scale warps quantise on its way: a
+// thread takes one block of the k tile, 8 neighbouring threads a row.
+template <int BN, int STAGES, int GROUPS, class V>
 __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
                      const __grid_constant__ MmArgs a) {
   extern __shared__ uint8_t raw_smem[];
   __shared__ Shared<BN, STAGES, GROUPS> sh;
+  constexpr bool kDense = !std::is_void<V>::value;
+  __shared__ uint32_t x_scales[kDense ? 2 : 1][2 * kMxFewRows];  // of two k tiles by turns: a row's 8 bytes
   constexpr int kStage = stage_bytes(BN);
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   uint8_t* group_smem = smem + STAGES * kStage;
@@ -445,6 +475,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     if (lane == 0) {
       // P's part of a stage or group and Q's: the first ones of P go out
       // before the wait for the grid that writes Q.
+      for (const CUtensorMap* map : {&p_map, &q_map, &ps_map, &qs_map}) prefetch_map(map);
       auto load_codes = [&](bool p, int tile, int kt, int s) {
         uint8_t* st = smem + s * kStage;
         if (p) tma_load_2d(st, &p_map, kt * kTileKBytes, (tile % a.p_tiles) * kLanes, &sh.codes_full[s]);
@@ -458,7 +489,8 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
           tma_load_2d(to, map, 0, 2 * ((row / kLanes) * groups + g), &sh.group_full[s]);
         else tma_load_2d(to, map, 16 * g, row, &sh.group_full[s]);
       };
-      const int q_bytes = a.q_pieces ? kGroup : 16 * BN;
+      const int q_bytes = kDense ? 0 : a.q_pieces ? kGroup : 16 * BN;
+      constexpr int kCodes = kDense ? kLanes * kTileKBytes : stage_bytes(BN);
       const int early = a.pdl && a.p_early && first < a.n_tiles ? min(k1 - k0, STAGES) : 0;
       const int early_groups = min((early + 1) / 2, GROUPS);
       for (int j = 0; j < early; ++j) {
@@ -466,7 +498,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
           mbar_expect_tx(&sh.group_full[j / 2], kGroup + q_bytes);
           load_group(true, first, g0 + j / 2, j / 2);
         }
-        mbar_expect_tx(&sh.codes_full[j], stage_bytes(BN));
+        mbar_expect_tx(&sh.codes_full[j], kCodes);
         load_codes(true, first, k0 + j, j);
       }
       if (a.pdl) dev::pdl_wait();
@@ -482,7 +514,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
               mbar_expect_tx(&sh.group_full[gs], kGroup + q_bytes);
               load_group(true, tile, kt / 2, gs);
             }
-            load_group(false, tile, kt / 2, gs);
+            if (!kDense) load_group(false, tile, kt / 2, gs);
             ++gt;
             if (++gs == GROUPS) {
               gs = 0;
@@ -491,10 +523,10 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
           }
           if (it >= STAGES && !(ok = wait(&sh.empty[s], parity))) break;
           if (it >= early) {
-            mbar_expect_tx(&sh.codes_full[s], stage_bytes(BN));
+            mbar_expect_tx(&sh.codes_full[s], kCodes);
             load_codes(true, tile, kt, s);
           }
-          load_codes(false, tile, kt, s);
+          if (!kDense) load_codes(false, tile, kt, s);
           ++it;
           if (++s == STAGES) {
             s = 0;
@@ -543,6 +575,17 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     int it = 0, s = 0, gs = 0, old = 0;  // old: the stage whose products used this set of scales before
     unsigned gparity = 0, parity_old = 0;
     bool ok = true;
+    // a dense Q's block of the next k tile, loaded one k tile ahead
+    const int t = threadIdx.x - 256, x_row = t >> 3, x_block = t & 7;
+    using Dense = typename std::conditional<kDense, V, mx::Vec32>::type;
+    Block<Dense> next;
+    auto fetch = [&](int tile, int kt) {
+      const int64_t row = (int64_t)(tile / a.p_tiles) * BN + x_row;
+      const int col = kTileK * kt + kMxBlock * x_block;
+      next.load(static_cast<const typename Dense::raw*>(a.x) + row * a.x_ld + col, row < a.q_rows ? a.x_cols - col : 0,
+                a.x_vec);
+    };
+    if (kDense && first < a.n_tiles) fetch(first, k0);
     for (int tile = first; tile < a.n_tiles && ok; tile += step) {
       // Q's rows start inside a piece of 128 when BN is less: q_part turns lane + 32 j into them
       const int q_part = a.q_pieces ? (tile / a.p_tiles) * BN % kLanes : 0;
@@ -551,7 +594,8 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
         ScaleGroup p, q;
         const uint8_t* group = group_smem + gs * 2 * kGroup;
         p.load(group, lane, a.p_pieces, kLanes);
-        if (!a.q_pieces || BN == kLanes) q.load(group + kGroup, lane, a.q_pieces, BN);
+        if (kDense) q = ScaleGroup{};
+        else if (!a.q_pieces || BN == kLanes) q.load(group + kGroup, lane, a.q_pieces, BN);
         else load_part<BN>(q, group + kGroup, lane, q_part);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
@@ -568,6 +612,21 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
               old = 0;
               parity_old ^= 1;
             }
+          }
+          if constexpr (kDense) {
+            // the stage's last products are those of k tile it - STAGES, waited for with the set's
+            const Block<Dense> now = next;
+            if (kt + h + 1 < k1) fetch(tile, kt + h + 1);
+            else if (tile + step < a.n_tiles) fetch(tile + step, k0);
+            uint32_t sc;
+            const uint4 codes = now.quantize(sc);
+            uint8_t* to = smem + s * kStage + kLanes * kTileKBytes;
+            *reinterpret_cast<uint4*>(to + 128 * x_row + 16 * (x_block ^ (x_row & 7))) = codes;  // swizzled as TMA does
+            reinterpret_cast<uint8_t*>(x_scales[it & 1])[t] = (uint8_t)sc;
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the four scale warps
+            q.m[2 * h].x = lane < kMxFewRows ? x_scales[it & 1][2 * lane] : 0u;
+            q.m[2 * h + 1].x = lane < kMxFewRows ? x_scales[it & 1][2 * lane + 1] : 0u;
           }
           fence_after();
           const uint4 v[4] = {p.m[2 * h], p.m[2 * h + 1], q.m[2 * h], q.m[2 * h + 1]};
@@ -730,6 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int it = 0, s = 0;
       unsigned parity = 1;
       bool ok = true;
+      for (const CUtensorMap* map : {&p_map, &q_map, &ps_map, &qs_map}) prefetch_map(map);
       const uint32_t full = address_in(&sh.full[0], 0), mine = address_in(&sh.group_full[0], rank);
       int gt = 0, gs = 0;
       unsigned gparity = 1;
@@ -994,24 +1054,28 @@ cudaError_t launch_product(K kernel, int grid, int smem, int cluster, const Maps
   return cudaLaunchKernelEx(&cfg, kernel, t.p, t.q, t.ps, t.qs, a);
 }
 
-template <int BN, int STAGES, int GROUPS>
+template <int BN, int STAGES, int GROUPS, class V = void>
 cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pieces, uint8_t* q_pieces, int sm_count,
                    cudaStream_t s) {
   constexpr int kSmem = STAGES * stage_bytes(BN) + GROUPS * 2 * kGroup + 1024;
   static_assert(kSmem <= (BN <= 64 ? 113 : 226) * 1024, "stages fit shared memory (twice for narrow tiles)");
   static_assert(STAGES * stage_bytes(BN) >= BN * kLanes * 4, "the split's parts fit the stages");
   static std::atomic<uint64_t> opted{0};
-  const cudaError_t e = opt_in(mx_matmul_kernel<BN, STAGES, GROUPS>, kSmem, opted);
+  const cudaError_t e = opt_in(mx_matmul_kernel<BN, STAGES, GROUPS, V>, kSmem, opted);
   if (e != cudaSuccess) return e;
+  static_assert(std::is_void<V>::value || BN == kMxFewRows, "a dense Q has a thread for each block of a k tile");
   Maps t;
-  if (!make_maps(&t, p, q, BN, p_pieces, q_pieces)) return cudaErrorInvalidValue;
+  // a dense Q has no maps; P's stand in their places and are not read
+  if (!(std::is_void<V>::value ? make_maps(&t, p, q, BN, p_pieces, q_pieces)
+                               : make_maps(&t, p, p, kLanes, p_pieces, p_pieces)))
+    return cudaErrorInvalidValue;
   a.p_tiles = (a.p_rows + kLanes - 1) / kLanes;
   const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + BN - 1) / BN);
   if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
   a.n_tiles = (int)tiles;
   // one cluster (a CTA when k is not split) per tile, or every SM's CTAs walking the tiles
   const int grid = a.split > 1 ? a.n_tiles * a.split : std::min<int>(a.n_tiles, sm_count * (BN <= 64 ? 2 : 1));
-  return launch_product(mx_matmul_kernel<BN, STAGES, GROUPS>, grid, kSmem, a.split, t, a, s);
+  return launch_product(mx_matmul_kernel<BN, STAGES, GROUPS, V>, grid, kSmem, a.split, t, a, s);
 }
 
 cudaError_t launch_pair(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pieces, uint8_t* q_pieces, int sm_count,
@@ -1048,7 +1112,7 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   // tiles: b's rows as lanes, narrower tiles, k split over a cluster.
   const int64_t row_bytes = m.ld * (m.type == kMxF32 ? 4 : 2);
   const bool aligned = ((reinterpret_cast<uintptr_t>(m.out) | (uintptr_t)row_bytes) & 31u) == 0;
-  const bool many = by_pairs(m.a.rows, m.b.rows, sm_count);
+  const bool many = !m.x && by_pairs(m.a.rows, m.b.rows, sm_count);
   const bool swap = !many || !aligned;
   const MxMatrix& p = swap ? m.b : m.a;
   const MxMatrix& q = swap ? m.a : m.b;
@@ -1065,7 +1129,7 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   uint8_t* space = static_cast<uint8_t*>(m.workspace);
   uint8_t *p_pieces = nullptr, *q_pieces = nullptr;
   if (!rows_load(p)) p_pieces = space, space += pieces_bytes(p);
-  if (!rows_load(q)) q_pieces = space;
+  if (!m.x && !rows_load(q)) q_pieces = space;
   a.p_pieces = p_pieces != nullptr, a.q_pieces = q_pieces != nullptr;
   if (p_pieces || q_pieces) {
     PieceArgs g = {};
@@ -1093,12 +1157,18 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   const int64_t p_tiles = (p.rows + kLanes - 1) / kLanes;
   auto split_for = [&](int bn, int slots) {
     const int64_t tiles = p_tiles * ((q.rows + bn - 1) / bn);
-    const int64_t most = std::min<int64_t>(std::min<int64_t>(8, (a.k_tiles + 1) / 2), slots / tiles);
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(8, a.k_tiles / 4), slots / tiles);
     for (a.split = 1; 2 * a.split <= most;) a.split *= 2;
   };
-  if (q.rows <= 16) {
+  if (q.rows <= kMxFewRows) {
     split_for(16, 2 * sm_count);
-    return launch<16, 5, 3>(p, q, a, p_pieces, q_pieces, sm_count, s);
+    if (!m.x) return launch<16, 5, 3>(p, q, a, p_pieces, q_pieces, sm_count, s);
+    a.x = m.x, a.x_ld = m.x_ld, a.x_cols = (int)q.cols;
+    const int64_t bytes = m.x_ld * (m.x_type == kMxF32 ? 4 : 2);
+    a.x_vec = ((reinterpret_cast<uintptr_t>(m.x) | (uintptr_t)bytes) & 15u) == 0;
+    if (m.x_type == kMxBf16) return launch<16, 5, 3, mx::Vec16<dev::Bf16>>(p, q, a, p_pieces, q_pieces, sm_count, s);
+    if (m.x_type == kMxF16) return launch<16, 5, 3, mx::Vec16<dev::F16>>(p, q, a, p_pieces, q_pieces, sm_count, s);
+    return launch<16, 5, 3, mx::Vec32>(p, q, a, p_pieces, q_pieces, sm_count, s);
   }
   if (p_tiles * ((q.rows + 31) / 32) <= sm_count) {
     split_for(32, 2 * sm_count);
