@@ -861,7 +861,8 @@ zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int
                             int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace that zero_mx4_linear needs for `tokens` rows of x and
- * this w.  Host only. */
+ * this w (none for up to 16 tokens and 4-byte aligned rows of scales).  Host
+ * only. */
 zero_status zero_mx4_linear_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes);
 
 /* The forward product of a linear layer whose weight w (outputs x inputs) is

@@ -241,7 +241,7 @@ def test_matmul_without_columns_or_rows(z):
 
 # ------------------------------------------------------------------- linear --
 
-LINEAR = [(1, 128, 32), (1, 2304, 768), (1, 1000, 771), (3, 300, 256), (16, 640, 512), (17, 640, 544), (100, 768, 2304),
+LINEAR = [(1, 128, 32), (1, 2304, 768), (1, 1000, 771), (3, 300, 256), (16, 640, 512), (16, 300, 779), (5, 200, 2080), (2, 130, 800), (9, 70, 4000), (17, 640, 544), (100, 768, 2304),
           (257, 513, 1000), (1000, 2304, 768), (2300, 2200, 512)]
 
 

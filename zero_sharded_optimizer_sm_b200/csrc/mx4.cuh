@@ -108,6 +108,7 @@ cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int sm_count, cudaStream_t s);
 int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b);
+int64_t mx_few_rows_workspace(const MxMatrix& b);  // with x instead of a
 cudaError_t mx_matmul_error(unsigned* flag, cudaStream_t s);
 
 // The message zero_last_error(NULL) returns to the calling thread.

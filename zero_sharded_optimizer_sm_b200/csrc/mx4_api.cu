@@ -123,9 +123,12 @@ zero_mx4 quantised_x(uint8_t* at, int64_t tokens, int64_t inputs) {
   return {at, at ? at + tokens * 16 * nb : nullptr, tokens, inputs, 16 * nb, align16(nb)};
 }
 int64_t linear_own(int64_t tokens, int64_t inputs) {
-  if (tokens <= zsm::kMxFewRows) return 0;  // quantised inside the product
   const int64_t nb = zsm::mx_blocks(inputs);
   return tokens * (16 * nb + align16(nb));
+}
+int64_t linear_need(int64_t tokens, const zero_mx4* w) {
+  if (tokens <= zsm::kMxFewRows) return zsm::mx_few_rows_workspace(matrix(*w));  // x is quantised in the product
+  return linear_own(tokens, w->cols) + zsm::mx_matmul_workspace(matrix(quantised_x(nullptr, tokens, w->cols)), matrix(*w));
 }
 
 // A product over no elements: zeros.
@@ -237,8 +240,7 @@ zero_status zero_mx4_linear_workspace(int64_t tokens, const zero_mx4* w, int64_t
   if (st != ZERO_OK) return st;
   if (tokens < 0 || tokens > kMaxDim) return fail(ZERO_EINVAL, "%lld tokens", (long long)tokens);
   if (tokens && w->rows && w->cols) {
-    const zero_mx4 xq = quantised_x(nullptr, tokens, w->cols);
-    *bytes = linear_own(tokens, w->cols) + zsm::mx_matmul_workspace(matrix(xq), matrix(*w));
+    *bytes = linear_need(tokens, w);
   }
   return ZERO_OK;
 }
@@ -257,8 +259,8 @@ zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   const int64_t own = linear_own(tokens, w->cols);
   uint8_t* at = static_cast<uint8_t*>(workspace);
-  const zero_mx4 xq = quantised_x(at, tokens, w->cols);
-  st = check_workspace(workspace, workspace_bytes, own + zsm::mx_matmul_workspace(matrix(xq), matrix(*w)));
+  zero_mx4 xq = quantised_x(at, tokens, w->cols);
+  st = check_workspace(workspace, workspace_bytes, linear_need(tokens, w));
   if (st != ZERO_OK) return st;
   if (tokens <= zsm::kMxFewRows) {
     zsm::MxMatmulArgs m = {};

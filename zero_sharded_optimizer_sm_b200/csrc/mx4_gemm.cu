@@ -9,7 +9,8 @@
 // codes and 8 scale bytes per matrix row, four instructions of 64 elements.
 //
 // Roles of a CTA's warps: 0 loads codes and scales (TMA); 1 issues the
-// products; 4-7 read the accumulator and store; 8-11 bring scales into TMEM.
+// products; 2-5 bring scales into TMEM; 6-9 read the accumulator and store (a
+// warp reaches the 32 lanes of TMEM that its number modulo 4 says).
 //
 // Scales: the tensor core wants the four scale bytes that row r has for 128 k
 // elements in lane r % 32 of every 32 lanes, column r / 32.  They come two k
@@ -50,7 +51,7 @@ using namespace pipe;
 constexpr int kLanes = 128;            // rows of P in a tile
 constexpr int kTileK = 256;            // elements of k in a stage
 constexpr int kTileKBytes = kTileK / 2;
-constexpr int kThreadsMm = 384;
+constexpr int kThreadsMm = 320;
 constexpr int kScaleWarps = 4;
 
 __device__ unsigned g_mx_error;        // a bounded wait that ran out (zero_mx4_check)
@@ -58,6 +59,9 @@ __device__ unsigned g_mx_error;        // a bounded wait that ran out (zero_mx4_
 struct MmArgs {
   int p_rows, q_rows, k_tiles;
   int p_pieces, q_pieces;  // 1: that operand's scales come as pieces
+  const uint8_t* p_scales; // set: P's scales are read from their rows by the scale warps (dense Q only)
+  int64_t p_scale_pitch;
+  int p_align, k_blocks;   //   alignment of those rows: 8, 4 or 1
   int p_tiles, n_tiles, split;
   void* out;
   int64_t p_stride, q_stride;  // elements between rows of P / of Q in the result
@@ -327,15 +331,49 @@ struct ScaleGroup {
     for (int j = 0; j < 4; ++j)
       m[j] = pieces || lane + 32 * j < rows ? *reinterpret_cast<const uint4*>(group + 16 * lane + 512 * j)
                                             : make_uint4(0u, 0u, 0u, 0u);
-    if (!pieces) {  // words [row][k] to [k][row]
-      const uint4 r0 = m[0], r1 = m[1], r2 = m[2], r3 = m[3];
-      m[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
-      m[1] = make_uint4(r0.y, r1.y, r2.y, r3.y);
-      m[2] = make_uint4(r0.z, r1.z, r2.z, r3.z);
-      m[3] = make_uint4(r0.w, r1.w, r2.w, r3.w);
-    }
+    if (!pieces) transpose();
+  }
+  __device__ __forceinline__ void transpose() {  // words [row][k] to [k][row]
+    const uint4 r0 = m[0], r1 = m[1], r2 = m[2], r3 = m[3];
+    m[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
+    m[1] = make_uint4(r0.y, r1.y, r2.y, r3.y);
+    m[2] = make_uint4(r0.z, r1.z, r2.z, r3.z);
+    m[3] = make_uint4(r0.w, r1.w, r2.w, r3.w);
   }
 };
+
+// 16 scale bytes of a row, of which the first n exist (the others are 0), the
+// row 8-byte (align 8) or 4-byte aligned.  But for a row's last odd blocks
+// every load is predicated and none sits in a branch, whose end would wait
+// for it.
+__device__ __forceinline__ uint4 load_row(const uint8_t* p, int n, int align) {
+  const bool lo = align >= 8 && n >= 8, hi = align >= 8 && n >= 16;
+  const bool w0 = !lo && n >= 4, w1 = !lo && n >= 8, w2 = !hi && n >= 12, w3 = !hi && n >= 16;
+  uint4 r;
+  asm volatile(
+      "{\n\t.reg .pred l, h, a, b, c, d;\n\t"
+      "setp.ne.b32 l, %5, 0;\n\tsetp.ne.b32 h, %6, 0;\n\t"
+      "setp.ne.b32 a, %7, 0;\n\tsetp.ne.b32 b, %8, 0;\n\tsetp.ne.b32 c, %9, 0;\n\tsetp.ne.b32 d, %10, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@l ld.global.v2.b32 {%0, %1}, [%4];\n\t"
+      "@h ld.global.v2.b32 {%2, %3}, [%4 + 8];\n\t"
+      "@a ld.global.b32 %0, [%4];\n\t"
+      "@b ld.global.b32 %1, [%4 + 4];\n\t"
+      "@c ld.global.b32 %2, [%4 + 8];\n\t"
+      "@d ld.global.b32 %3, [%4 + 12];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+      : "l"(p), "r"((int)lo), "r"((int)hi), "r"((int)w0), "r"((int)w1), "r"((int)w2), "r"((int)w3)
+      : "memory");
+  if (n > 0 && n < 16 && (n & 3)) {  // the row's last block does not end a word
+    uint32_t w = 0;
+    for (int i = n & ~3; i < n; ++i) w |= (uint32_t)p[i] << (8 * (i & 3));
+    if (n < 4) r.x = w;
+    else if (n < 8) r.y = w;
+    else if (n < 12) r.z = w;
+    else r.w = w;
+  }
+  return r;
+}
 
 // The same for the BN rows that start at row `part` (a multiple of BN) of a
 // 128-row piece: row part + lane + 32 j's words lie where its row number says.
@@ -420,7 +458,10 @@ struct Block {
 // V: void when Q is an MX4 matrix; else the vector type of the dense matrix
 // that Q is (at most 16 rows), which the scale warps quantise on its way: a
 // thread takes one block of the k tile, 8 neighbouring threads a row.
-template <int BN, int STAGES, int GROUPS, class V>
+// kDirect (dense Q only): P's scales are read from their rows by those warps
+// too, for rows that are 4-byte aligned but not 16 -- with few tokens another
+// launch for pieces would cost more than the narrower loads.
+template <int BN, int STAGES, int GROUPS, class V, bool kDirect>
 __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
@@ -439,6 +480,8 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
   const int g0 = (int)((int64_t)groups * rank / a.split), g1 = (int)((int64_t)groups * (rank + 1) / a.split);
   const int k0 = 2 * g0, k1 = min(2 * g1, a.k_tiles);
   const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
+  constexpr bool by_group = !kDirect;  // scales through shared memory
+  static_assert(kDense || !kDirect, "Q's scales come in groups");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -492,7 +535,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
       const int q_bytes = kDense ? 0 : a.q_pieces ? kGroup : 16 * BN;
       constexpr int kCodes = kDense ? kLanes * kTileKBytes : stage_bytes(BN);
       const int early = a.pdl && a.p_early && first < a.n_tiles ? min(k1 - k0, STAGES) : 0;
-      const int early_groups = min((early + 1) / 2, GROUPS);
+      const int early_groups = by_group ? min((early + 1) / 2, GROUPS) : 0;
       for (int j = 0; j < early; ++j) {
         if (j % 2 == 0 && j / 2 < early_groups) {
           mbar_expect_tx(&sh.group_full[j / 2], kGroup + q_bytes);
@@ -507,7 +550,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
       bool ok = true;
       for (int tile = first; tile < a.n_tiles && ok; tile += step) {
         for (int kt = k0; kt < k1; ++kt) {
-          if (((kt - k0) & 1) == 0) {
+          if (by_group && ((kt - k0) & 1) == 0) {
             if (gt >= GROUPS && !(ok = wait(&sh.group_empty[gs], gparity))) break;
             fence_proxy_async_smem();  // the scale warps' reads of the group, before it is written again
             if (gt >= early_groups) {
@@ -570,13 +613,13 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
         mbar_wait(&sh.drained, 0);
       }
     }
-  } else if (warp >= 8) {
-    const uint32_t ts = tmem + ((uint32_t)(32 * (warp - 8)) << 16) + acc_cols(BN);
+  } else if (warp < 6) {
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc_cols(BN);
     int it = 0, s = 0, gs = 0, old = 0;  // old: the stage whose products used this set of scales before
     unsigned gparity = 0, parity_old = 0;
     bool ok = true;
     // a dense Q's block of the next k tile, loaded one k tile ahead
-    const int t = threadIdx.x - 256, x_row = t >> 3, x_block = t & 7;
+    const int t = threadIdx.x - 64, x_row = t >> 3, x_block = t & 7;
     using Dense = typename std::conditional<kDense, V, mx::Vec32>::type;
     Block<Dense> next;
     auto fetch = [&](int tile, int kt) {
@@ -586,22 +629,42 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
                 a.x_vec);
     };
     if (kDense && first < a.n_tiles) fetch(first, k0);
+    // P's scales straight from their rows, likewise ahead by a group
+    ScaleGroup direct;
+    auto fetch_scales = [&](int tile, int kt) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t row = (int64_t)(tile % a.p_tiles) * kLanes + lane + 32 * j;
+        direct.m[j] = load_row(a.p_scales + row * a.p_scale_pitch + 8 * kt, row < a.p_rows ? a.k_blocks - 8 * kt : 0,
+                               a.p_align);
+      }
+    };
+    if (kDirect && first < a.n_tiles) fetch_scales(first, k0);
     for (int tile = first; tile < a.n_tiles && ok; tile += step) {
       // Q's rows start inside a piece of 128 when BN is less: q_part turns lane + 32 j into them
       const int q_part = a.q_pieces ? (tile / a.p_tiles) * BN % kLanes : 0;
       for (int kt = k0; kt < k1 && ok; kt += 2) {
-        if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity)))) break;
         ScaleGroup p, q;
+        if (kDirect) {
+          p = direct;
+          p.transpose();
+          if (kt + 2 < k1) fetch_scales(tile, kt + 2);
+          else if (tile + step < a.n_tiles) fetch_scales(tile + step, k0);
+        } else if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity)))) {
+          break;
+        }
         const uint8_t* group = group_smem + gs * 2 * kGroup;
-        p.load(group, lane, a.p_pieces, kLanes);
+        if (by_group) p.load(group, lane, a.p_pieces, kLanes);
         if (kDense) q = ScaleGroup{};
         else if (!a.q_pieces || BN == kLanes) q.load(group + kGroup, lane, a.q_pieces, BN);
         else load_part<BN>(q, group + kGroup, lane, q_part);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
-        if (++gs == GROUPS) {
-          gs = 0;
-          gparity ^= 1;
+        if (by_group) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
+          if (++gs == GROUPS) {
+            gs = 0;
+            gparity ^= 1;
+          }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -640,8 +703,8 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
         }
       }
     }
-  } else if (warp >= 4 && a.split == 1) {
-    const int w = warp - 4;
+  } else if (a.split == 1) {
+    const int w = warp & 3;
     int n = 0;
     for (int tile = first; tile < a.n_tiles; tile += step, ++n) {
       if (!__all_sync(0xFFFFFFFFu, wait(&sh.acc_full, n & 1))) break;
@@ -665,15 +728,15 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     // the stages' memory, which every CTA of the cluster has finished with
     // after the first barrier.
     const int shift = __ffs(BN / a.split) - 1, own = 1 << shift;
-    const int w = warp - 4;
+    const int w = warp & 3;
     bool ok = true;
-    if (warp >= 4 && warp < 8) {
+    if (warp >= 6) {
       ok = __all_sync(0xFFFFFFFFu, wait(&sh.acc_full, 0));
       fence_after();
     }
     __syncwarp();
     cluster_sync();
-    if (warp >= 4 && warp < 8 && ok) {
+    if (warp >= 6 && ok) {
       constexpr int kStep = BN < 32 ? 8 : 32;
       const uint32_t base = smem_u32(smem) + 4u * (rank * own * kLanes + 32 * w + lane);
       for (int c = 0; c < BN; c += kStep) {
@@ -686,7 +749,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     }
     __syncwarp();
     cluster_sync();
-    if (warp >= 4 && warp < 8) {
+    if (warp >= 6) {
       const float* part = reinterpret_cast<const float*>(smem) + 32 * w + lane;
       const int64_t p = (int64_t)(first % a.p_tiles) * kLanes + 32 * w + lane, q0 = (int64_t)(first / a.p_tiles) * BN;
       for (int i = 0; i < own; ++i) {
@@ -720,7 +783,7 @@ constexpr int kPairStages = 6;
 constexpr int kPairCodes = 2 * kLanes * kTileKBytes;     // per CTA
 constexpr int kPairGroups = 3;
 constexpr int kPairGroup = 3 * kGroup;                   // per CTA: 128 rows of P, 256 of Q
-constexpr int kPairThreads = 384;
+constexpr int kPairThreads = kThreadsMm;
 constexpr int kPairSets = 4;
 constexpr int kPairScaleCols = 24;
 constexpr int kPairScales = 512 - kPairSets * kPairScaleCols;  // first column of the scales
@@ -873,8 +936,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_wait(&sh.drained, 0);
       }
     }
-  } else if (warp >= 4 && warp < 8) {
-    const int w = warp - 4;
+  } else if (warp >= 6) {
+    const int w = warp & 3;
     int n = 0;
     for (int tile = first; tile < a.n_tiles; tile += step, ++n) {
       if (!__all_sync(0xFFFFFFFFu, wait(&sh.acc_full[n & 1], (n >> 1) & 1))) break;
@@ -896,9 +959,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       fence_before();
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 2 && warp < 6) {
     const uint32_t ready = address_in(&sh.scales_full[0], 0);
-    const uint32_t ts = tmem + ((uint32_t)(32 * (warp - 8)) << 16) + kPairScales;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPairScales;
     int it = 0, s = 0, gs = 0, set = 0, old = 0;  // old: the stage whose products used this set before
     unsigned gparity = 0, parity_old = 0;
     bool ok = true;
@@ -1015,6 +1078,9 @@ bool scales_map(CUtensorMap* map, const MxMatrix& m, int rows, uint8_t* pieces, 
 bool rows_load(const MxMatrix& m) {
   return ((reinterpret_cast<uintptr_t>(m.scales) | (uintptr_t)m.scale_pitch) & 15u) == 0;
 }
+bool words_load(const MxMatrix& m) {
+  return ((reinterpret_cast<uintptr_t>(m.scales) | (uintptr_t)m.scale_pitch) & 3u) == 0;
+}
 // Pieces of a matrix: blocks of 128 rows (whole pairs of them) times groups of two k tiles.
 int64_t row_blocks(const MxMatrix& m) { return 2 * ((m.rows + 255) / 256); }
 int64_t groups_of(const MxMatrix& m) { return (mx_blocks(m.cols) + 15) / 16; }
@@ -1054,28 +1120,31 @@ cudaError_t launch_product(K kernel, int grid, int smem, int cluster, const Maps
   return cudaLaunchKernelEx(&cfg, kernel, t.p, t.q, t.ps, t.qs, a);
 }
 
-template <int BN, int STAGES, int GROUPS, class V = void>
+template <int BN, int STAGES, int GROUPS, class V = void, bool kDirect = false>
 cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pieces, uint8_t* q_pieces, int sm_count,
                    cudaStream_t s) {
   constexpr int kSmem = STAGES * stage_bytes(BN) + GROUPS * 2 * kGroup + 1024;
   static_assert(kSmem <= (BN <= 64 ? 113 : 226) * 1024, "stages fit shared memory (twice for narrow tiles)");
   static_assert(STAGES * stage_bytes(BN) >= BN * kLanes * 4, "the split's parts fit the stages");
   static std::atomic<uint64_t> opted{0};
-  const cudaError_t e = opt_in(mx_matmul_kernel<BN, STAGES, GROUPS, V>, kSmem, opted);
+  const cudaError_t e = opt_in(mx_matmul_kernel<BN, STAGES, GROUPS, V, kDirect>, kSmem, opted);
   if (e != cudaSuccess) return e;
   static_assert(std::is_void<V>::value || BN == kMxFewRows, "a dense Q has a thread for each block of a k tile");
   Maps t;
-  // a dense Q has no maps; P's stand in their places and are not read
-  if (!(std::is_void<V>::value ? make_maps(&t, p, q, BN, p_pieces, q_pieces)
-                               : make_maps(&t, p, p, kLanes, p_pieces, p_pieces)))
-    return cudaErrorInvalidValue;
+  if (std::is_void<V>::value) {
+    if (!make_maps(&t, p, q, BN, p_pieces, q_pieces)) return cudaErrorInvalidValue;
+  } else {  // maps that are not used are P's codes'
+    if (!codes_map(&t.p, p, kLanes)) return cudaErrorInvalidValue;
+    t.q = t.ps = t.qs = t.p;
+    if (!kDirect && !scales_map(&t.ps, p, kLanes, p_pieces, row_blocks(p) * groups_of(p))) return cudaErrorInvalidValue;
+  }
   a.p_tiles = (a.p_rows + kLanes - 1) / kLanes;
   const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + BN - 1) / BN);
   if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
   a.n_tiles = (int)tiles;
   // one cluster (a CTA when k is not split) per tile, or every SM's CTAs walking the tiles
   const int grid = a.split > 1 ? a.n_tiles * a.split : std::min<int>(a.n_tiles, sm_count * (BN <= 64 ? 2 : 1));
-  return launch_product(mx_matmul_kernel<BN, STAGES, GROUPS, V>, grid, kSmem, a.split, t, a, s);
+  return launch_product(mx_matmul_kernel<BN, STAGES, GROUPS, V, kDirect>, grid, kSmem, a.split, t, a, s);
 }
 
 cudaError_t launch_pair(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pieces, uint8_t* q_pieces, int sm_count,
@@ -1103,6 +1172,7 @@ bool by_pairs(int64_t m, int64_t n, int sm_count) {
 }  // namespace
 
 int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b) { return pieces_bytes(a) + pieces_bytes(b); }
+int64_t mx_few_rows_workspace(const MxMatrix& b) { return words_load(b) ? 0 : pieces_bytes(b); }
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
@@ -1128,7 +1198,14 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
 
   uint8_t* space = static_cast<uint8_t*>(m.workspace);
   uint8_t *p_pieces = nullptr, *q_pieces = nullptr;
-  if (!rows_load(p)) p_pieces = space, space += pieces_bytes(p);
+  const bool direct = m.x && !rows_load(p) && words_load(p);
+  if (direct) {
+    a.p_scales = p.scales, a.p_scale_pitch = p.scale_pitch;
+    a.p_align = (reinterpret_cast<uintptr_t>(p.scales) | (uintptr_t)p.scale_pitch) & 7u ? 4 : 8;
+    a.k_blocks = (int)mx_blocks(p.cols);
+  } else if (!rows_load(p)) {
+    p_pieces = space, space += pieces_bytes(p);
+  }
   if (!m.x && !rows_load(q)) q_pieces = space;
   a.p_pieces = p_pieces != nullptr, a.q_pieces = q_pieces != nullptr;
   if (p_pieces || q_pieces) {
@@ -1166,9 +1243,14 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
     a.x = m.x, a.x_ld = m.x_ld, a.x_cols = (int)q.cols;
     const int64_t bytes = m.x_ld * (m.x_type == kMxF32 ? 4 : 2);
     a.x_vec = ((reinterpret_cast<uintptr_t>(m.x) | (uintptr_t)bytes) & 15u) == 0;
-    if (m.x_type == kMxBf16) return launch<16, 5, 3, mx::Vec16<dev::Bf16>>(p, q, a, p_pieces, q_pieces, sm_count, s);
-    if (m.x_type == kMxF16) return launch<16, 5, 3, mx::Vec16<dev::F16>>(p, q, a, p_pieces, q_pieces, sm_count, s);
-    return launch<16, 5, 3, mx::Vec32>(p, q, a, p_pieces, q_pieces, sm_count, s);
+    auto dense = [&](auto v) {
+      using V = decltype(v);
+      return direct ? launch<16, 5, 3, V, true>(p, q, a, p_pieces, q_pieces, sm_count, s)
+                    : launch<16, 5, 3, V, false>(p, q, a, p_pieces, q_pieces, sm_count, s);
+    };
+    if (m.x_type == kMxBf16) return dense(mx::Vec16<dev::Bf16>{});
+    if (m.x_type == kMxF16) return dense(mx::Vec16<dev::F16>{});
+    return dense(mx::Vec32{});
   }
   if (p_tiles * ((q.rows + 31) / 32) <= sm_count) {
     split_for(32, 2 * sm_count);
