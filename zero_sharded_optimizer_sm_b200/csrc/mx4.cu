@@ -21,11 +21,6 @@ namespace {
 using namespace dev;
 using namespace mx;
 
-__device__ __forceinline__ uint32_t max_of_four(uint32_t m) {  // over four neighbouring lanes
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-}
-
 // ---------------------------------------------------- quantise along rows --
 
 // A warp takes 256 consecutive columns of one row at a time, a lane 8 of them

@@ -199,6 +199,17 @@ __device__ __forceinline__ int wait_bounded(uint64_t* bar, unsigned parity, vola
   }
   return 0;
 }
+// Whether all four scale warps' threads say yes (named barrier 1).
+__device__ __forceinline__ bool all_scale_warps(bool yes) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((int)yes)
+      : "memory");
+  return r != 0;
+}
 // Long enough for every copy in flight to have landed (after a failed wait only).
 __device__ __forceinline__ void linger() {
   const long long t0 = clock64();
@@ -439,30 +450,14 @@ struct Shared {
   static_assert(kSets <= STAGES, "a set is written again after its stage's products");
 };
 
-// One block of 32 elements of a dense row, the first `left` of them existing.
-template <class V>
-struct Block {
-  V x[4];
-  __device__ __forceinline__ void load(const typename V::raw* p, int left, int vec) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mx::load8(x[j], p + 8 * j, left - 8 * j, vec);
-  }
-  // Its codes; s: its scale byte.
-  __device__ __forceinline__ uint4 quantize(uint32_t& s) const {
-    s = mx::scale_code(max(max(x[0].max_bits(), x[1].max_bits()), max(x[2].max_bits(), x[3].max_bits())));
-    return make_uint4(mx::encode<false>(x[0], s, 0, 0, 0), mx::encode<false>(x[1], s, 0, 0, 0),
-                      mx::encode<false>(x[2], s, 0, 0, 0), mx::encode<false>(x[3], s, 0, 0, 0));
-  }
-};
-
 // V: void when Q is an MX4 matrix; else the vector type of the dense matrix
 // that Q is (at most 16 rows), which the scale warps quantise on its way: a
-// thread takes one block of the k tile, 8 neighbouring threads a row.
+// warp takes every fourth row's 256 elements of the k tile, 8 a lane.
 // kDirect (dense Q only): P's scales are read from their rows by those warps
 // too, for rows that are 4-byte aligned but not 16 -- with few tokens another
 // launch for pieces would cost more than the narrower loads.
 template <int BN, int STAGES, int GROUPS, class V, bool kDirect>
-__global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::Vec32>::value ? 2 : 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
                      const __grid_constant__ MmArgs a) {
@@ -618,17 +613,29 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
     int it = 0, s = 0, gs = 0, old = 0;  // old: the stage whose products used this set of scales before
     unsigned gparity = 0, parity_old = 0;
     bool ok = true;
-    // a dense Q's block of the next k tile, loaded one k tile ahead
-    const int t = threadIdx.x - 64, x_row = t >> 3, x_block = t & 7;
+    // a dense Q's vectors of the next k tile (rows wq, wq + 4, ...), loaded one k tile ahead
+    const int wq = warp - 2;
+    constexpr int kRowsOf = kDense ? kMxFewRows / kScaleWarps : 1;
     using Dense = typename std::conditional<kDense, V, mx::Vec32>::type;
-    Block<Dense> next;
-    auto fetch = [&](int tile, int kt) {
-      const int64_t row = (int64_t)(tile / a.p_tiles) * BN + x_row;
-      const int col = kTileK * kt + kMxBlock * x_block;
-      next.load(static_cast<const typename Dense::raw*>(a.x) + row * a.x_ld + col, row < a.q_rows ? a.x_cols - col : 0,
-                a.x_vec);
+    Dense next[kRowsOf];
+    auto fetch = [&](int kt) {
+      const int col = kTileK * kt + 8 * lane;
+#pragma unroll
+      for (int i = 0; i < kRowsOf; ++i) {
+        const int row = wq + kScaleWarps * i, left = row < a.q_rows ? a.x_cols - col : 0;
+        const auto* p = static_cast<const typename Dense::raw*>(a.x) + row * a.x_ld + col;
+        next[i].load_if(p, left >= 8 && a.x_vec);
+        if (left > 0 && !(left >= 8 && a.x_vec)) next[i].load(p, left);
+      }
     };
-    if (kDense && first < a.n_tiles) fetch(first, k0);
+    if (kDense) {
+      // the rows past Q's last stay zero in every stage
+      for (int i = threadIdx.x - 64; i < STAGES * kMxFewRows * 8; i += 32 * kScaleWarps)
+        *reinterpret_cast<uint4*>(smem + i / (8 * kMxFewRows) * kStage + kLanes * kTileKBytes +
+                                  16 * (i % (8 * kMxFewRows))) = make_uint4(0u, 0u, 0u, 0u);
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the four scale warps
+      if (first < a.n_tiles) fetch(k0);
+    }
     // P's scales straight from their rows, likewise ahead by a group
     ScaleGroup direct;
     auto fetch_scales = [&](int tile, int kt) {
@@ -650,8 +657,9 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
           p.transpose();
           if (kt + 2 < k1) fetch_scales(tile, kt + 2);
           else if (tile + step < a.n_tiles) fetch_scales(tile + step, k0);
-        } else if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity)))) {
-          break;
+        } else {
+          ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity));
+          if (!kDense && !ok) break;
         }
         const uint8_t* group = group_smem + gs * 2 * kGroup;
         if (by_group) p.load(group, lane, a.p_pieces, kLanes);
@@ -669,28 +677,37 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 ? 2 : 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (kt + h >= k1) break;
-          if (it >= kSets) {
-            if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.empty[old], parity_old)))) break;
+          if (it >= kSets) {  // the set is free, and with it (kSets <= STAGES) the stage
+            ok = ok && __all_sync(0xFFFFFFFFu, wait(&sh.empty[old], parity_old));
             if (++old == STAGES) {
               old = 0;
               parity_old ^= 1;
             }
           }
           if constexpr (kDense) {
-            // the stage's last products are those of k tile it - STAGES, waited for with the set's
-            const Block<Dense> now = next;
-            if (kt + h + 1 < k1) fetch(tile, kt + h + 1);
-            else if (tile + step < a.n_tiles) fetch(tile + step, k0);
-            uint32_t sc;
-            const uint4 codes = now.quantize(sc);
-            uint8_t* to = smem + s * kStage + kLanes * kTileKBytes;
-            *reinterpret_cast<uint4*>(to + 128 * x_row + 16 * (x_block ^ (x_row & 7))) = codes;  // swizzled as TMA does
-            reinterpret_cast<uint8_t*>(x_scales[it & 1])[t] = (uint8_t)sc;
-            fence_proxy_async_smem();
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // the four scale warps
-            q.m[2 * h].x = lane < kMxFewRows ? x_scales[it & 1][2 * lane] : 0u;
-            q.m[2 * h + 1].x = lane < kMxFewRows ? x_scales[it & 1][2 * lane + 1] : 0u;
+            if (ok) {
+              uint8_t* to = smem + s * kStage + kLanes * kTileKBytes + 4 * (lane & 3);
+              uint8_t* sc = reinterpret_cast<uint8_t*>(x_scales[it & 1]);
+#pragma unroll
+              for (int i = 0; i < kRowsOf; ++i) {
+                const int row = wq + kScaleWarps * i;
+                if (row >= a.q_rows) break;
+                const uint32_t sb = mx::scale_code(mx::max_of_four(next[i].max_bits()));
+                const uint32_t w = mx::encode<false>(next[i], sb, 0, 0, 0);
+                *reinterpret_cast<uint32_t*>(to + 128 * row + 16 * ((lane >> 2) ^ (row & 7))) = w;  // swizzled as TMA does
+                if ((lane & 3) == 0) sc[8 * row + (lane >> 2)] = (uint8_t)sb;
+              }
+              if (kt + h + 1 < k1) fetch(kt + h + 1);
+              else if (tile + step < a.n_tiles) fetch(k0);
+              fence_proxy_async_smem();
+            }
+            ok = all_scale_warps(ok);  // the row's scales are there; or all four stop together
+            if (ok) {
+              q.m[2 * h].x = lane < a.q_rows ? x_scales[it & 1][2 * lane] : 0u;
+              q.m[2 * h + 1].x = lane < a.q_rows ? x_scales[it & 1][2 * lane + 1] : 0u;
+            }
           }
+          if (!ok) break;
           fence_after();
           const uint4 v[4] = {p.m[2 * h], p.m[2 * h + 1], q.m[2 * h], q.m[2 * h + 1]};
           tmem_write16(ts + (it % kSets) * kScaleCols, v);
@@ -1129,7 +1146,7 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pi
   static std::atomic<uint64_t> opted{0};
   const cudaError_t e = opt_in(mx_matmul_kernel<BN, STAGES, GROUPS, V, kDirect>, kSmem, opted);
   if (e != cudaSuccess) return e;
-  static_assert(std::is_void<V>::value || BN == kMxFewRows, "a dense Q has a thread for each block of a k tile");
+  static_assert(std::is_void<V>::value || BN == kMxFewRows, "a dense Q is one tile wide");
   Maps t;
   if (std::is_void<V>::value) {
     if (!make_maps(&t, p, q, BN, p_pieces, q_pieces)) return cudaErrorInvalidValue;

@@ -23,6 +23,17 @@ struct Vec16 {  // bf16 or binary16
     const uint4 x = ld_stream(p);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
   }
+  // The whole vector, or zeros: one predicated load, without a branch whose
+  // end would wait for it.
+  __device__ __forceinline__ void load_if(const raw* p, bool yes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3])
+        : "l"(p), "r"((int)yes)
+        : "memory");
+  }
   __device__ __forceinline__ void load(const raw* p, int64_t n) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -49,6 +60,17 @@ struct Vec32 {  // binary32
   __device__ __forceinline__ void load(const raw* p) {
     const float4 a = ld_stream(p), b = ld_stream(p + 4);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ void load_if(const raw* p, bool yes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %9, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "mov.b32 %4, 0;\n\tmov.b32 %5, 0;\n\tmov.b32 %6, 0;\n\tmov.b32 %7, 0;\n\t"
+        "@q ld.global.v4.f32 {%0, %1, %2, %3}, [%8];\n\t"
+        "@q ld.global.v4.f32 {%4, %5, %6, %7}, [%8 + 16];\n\t}"
+        : "=&f"(x[0]), "=&f"(x[1]), "=&f"(x[2]), "=&f"(x[3]), "=&f"(x[4]), "=&f"(x[5]), "=&f"(x[6]), "=&f"(x[7])
+        : "l"(p), "r"((int)yes)
+        : "memory");
   }
   __device__ __forceinline__ void load(const raw* p, int64_t n) {
 #pragma unroll
@@ -89,6 +111,11 @@ __device__ __forceinline__ uint32_t encode(const V& x, uint32_t s, uint64_t bloc
   for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
   const uint32_t w = kStochastic ? encode8_stochastic(v, block, c, seed) : encode8(v);
   return s == 255u ? 0u : w;
+}
+
+__device__ __forceinline__ uint32_t max_of_four(uint32_t m) {  // over four neighbouring lanes
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 
 }  // namespace mx
