@@ -874,6 +874,22 @@ zero_status zero_mx4_linear_workspace(int64_t tokens, const zero_mx4* w, int64_t
 zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t ld, const zero_mx4* w, void* y,
                             int32_t y_dtype, int64_t ld_y, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Bytes of workspace that zero_mx4_linear_backward needs.  Host only. */
+zero_status zero_mx4_linear_backward_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes);
+
+/* The backward products of that layer: dx = Q(dy) Q(w^T)^T (tokens x inputs)
+ * and dw = Q(dy^T) Q(x^T)^T (outputs x inputs), each operand quantised in
+ * blocks along the axis that its product sums over: dy (tokens x outputs) by
+ * `rounding` and `seed`, the transpose as zero_mx4_quantize rounds it, x and w
+ * to nearest even.  The roundings' own derivatives are taken as one.  dw may
+ * be a rank's gradient buffer of the layer.  The same values as
+ * zero_mx4_quantize, zero_mx4_transpose and zero_mx4_matmul give.  workspace
+ * as for zero_mx4_matmul.  [T] section "ZeRO-3", part "2. 反向". */
+zero_status zero_mx4_linear_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* x, int32_t x_dtype,
+                                     int64_t ld_x, int64_t tokens, const zero_mx4* w, int32_t rounding, uint64_t seed,
+                                     void* dx, int32_t dx_dtype, int64_t ld_dx, void* dw, int32_t dw_dtype, int64_t ld_dw,
+                                     void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Wait for `stream` and report whether a bounded wait inside a product kernel
  * on the current device ran out since the last call: ZERO_ECUDA (that
  * product's result is invalid) or ZERO_OK.  No passage of the pages defines

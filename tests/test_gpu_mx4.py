@@ -302,6 +302,24 @@ def test_linear_backward(z, dtype, tokens, out, inner, seed):
     assert dx.shape == x.shape and dw.shape == (out, inner)
 
 
+def test_linear_backward_strides_types_and_empty_batches(z):
+    """Mixed types, rows apart, gradients into views (guarded), no tokens, no
+    outputs."""
+    t, o, k = 70, 96, 160
+    x, dy = _normal(t, k + 3, "f32", 1)[:, :k], _normal(t, o + 8, "bf16", 2)[:, 8:]
+    w = z.mx4_quantize(_normal(o, k, "bf16", 3, 0.02))
+    dxs = torch.full((t, k + 4), 3.0, dtype=torch.float16, device="cuda")
+    flat = torch.full((o * k + 16,), 3.0, dtype=torch.bfloat16, device="cuda")  # a rank's gradient buffer
+    dx, dw = z.mx4_linear_backward(dy, x, w, dx=dxs[:, :k], dw=flat[8:-8].view(o, k))
+    _assert_product(dx, z.mx4_quantize(dy), z.mx4_transpose(w), "dx")
+    _assert_product(dw, z.mx4_quantize(dy, transpose=True), z.mx4_quantize(x, transpose=True), "dw")
+    assert (dxs[:, k:] == 3).all() and (flat[:8] == 3).all() and (flat[-8:] == 3).all()
+    dx, dw = z.mx4_linear_backward(dy[:0], x[:0], w, dw=flat[8:-8].view(o, k))
+    assert dx.shape == (0, k) and (dw == 0).all()
+    dx, dw = z.mx4_linear_backward(dy[:, :0], x, z.mx4_empty(0, k))
+    assert (dx == 0).all() and dx.shape == (t, k) and dw.shape == (0, k)
+
+
 def test_linear_backward_against_differences(z):
     """On inputs that every quantisation keeps exactly -- whole numbers of
     magnitude 4 or 6 or 0, one of them in each block along either axis, so

@@ -89,6 +89,31 @@ def test_shapes_that_do_not_fit():
     _refused(z.zero_mx4_linear(A, 0, -2, 64, _m(), A, 0, 64, A, 1 << 30, None), "out of range")
 
 
+@pytest.mark.parametrize("kw,word", [
+    (dict(dy=None), "dy"), (dict(x=None), "x is null"), (dict(dx=None), "dx"), (dict(dw=None), "dw"),
+    (dict(dy_dtype=3), "dtype"), (dict(x_dtype=-1), "dtype"), (dict(dx_dtype=9), "dtype"), (dict(dw_dtype=9), "dtype"),
+    (dict(ld_dy=3), "dy: 3"), (dict(ld_x=63), "x: 63"), (dict(ld_dx=63), "dx: 63"), (dict(ld_dw=63), "dw: 63"),
+    (dict(rounding=5), "rounding"), (dict(tokens=-1), "out of range"), (dict(workspace=None), "workspace"),
+    (dict(workspace=A + 4), "workspace"), (dict(bytes=100), "workspace"), (dict(w=None), "w is NULL"),
+    (dict(w=_m(code_pitch=8)), "w: code_pitch"),
+])
+def test_linear_backward_arguments(kw, word):
+    a = dict(dy=A, dy_dtype=0, ld_dy=4, x=A, x_dtype=0, ld_x=64, tokens=5, w=_m(), rounding=0, seed=0, dx=A, dx_dtype=0,
+             ld_dx=64, dw=A, dw_dtype=0, ld_dw=64, workspace=A, bytes=1 << 20)
+    a.update(kw)
+    _refused(z.zero_mx4_linear_backward(*a.values(), None), word)
+
+
+def test_linear_backward_workspace():
+    """dy (5 x 4), its transpose, x's (64 x 5) and w's (64 x 4): one block of
+    codes and 16 bytes of scales to a row of each."""
+    n = ctypes.c_int64()
+    assert z.zero_mx4_linear_backward_workspace(5, _m(), n) == 0 and n.value == 32 * (5 + 4 + 64 + 64)
+    assert z.zero_mx4_linear_backward_workspace(0, _m(), n) == 0 and n.value == 0
+    _refused(z.zero_mx4_linear_backward_workspace(-1, _m(), n), "tokens")
+    _refused(z.zero_mx4_linear_backward_workspace(5, _m(), None), "NULL")
+
+
 def test_empty_matrices_do_nothing():
     e = _m(rows=0, codes=None, scales=None)
     n = ctypes.c_int64(-1)

@@ -140,6 +140,9 @@ _SIGS = {
     "zero_mx4_matmul": (_i32, [_MX4, _MX4, _vp, _i32, _i64, _vp, _i64, _vp]),
     "zero_mx4_linear_workspace": (_i32, [_i64, _MX4, ctypes.POINTER(_i64)]),
     "zero_mx4_linear": (_i32, [_vp, _i32, _i64, _i64, _MX4, _vp, _i32, _i64, _vp, _i64, _vp]),
+    "zero_mx4_linear_backward_workspace": (_i32, [_i64, _MX4, ctypes.POINTER(_i64)]),
+    "zero_mx4_linear_backward": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _MX4, _i32, ctypes.c_uint64, _vp, _i32,
+                                        _i64, _vp, _i32, _i64, _vp, _i64, _vp]),
     "zero_mx4_check": (_i32, [_vp]),
     "zero_mx4_all_gather": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
     "zero_mx4_reduce_scatter": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
@@ -935,15 +938,26 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
     stochastically when ``seed`` is given); the roundings' own gradients are
     taken as one.  dx has x's type and dw dy's unless given (dw may be a view
     of a rank's gradient buffer)."""
-    if x.dim() != 2 or dy.dim() != 2 or x.shape[1] != w.cols or tuple(dy.shape) != (x.shape[0], w.rows):
+    yptr, ycode, ldy, tokens, outputs = _dense(dy, "dy")
+    xptr, xcode, ldx, xtokens, inputs = _dense(x, "x")
+    if (tokens, outputs, inputs) != (xtokens, w.rows, w.cols):
         raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} do not fit w {(w.rows, w.cols)}")
-    _need_device(x.device, "dy", dy)
-    _need_device(x.device, "w", w)
-    dyq, dyq_t = mx4_quantize_both(dy, seed, stream=stream)
-    xq_t = mx4_quantize(x, transpose=True, stream=stream)
-    wq_t = mx4_transpose(w, stream=stream)
-    dx = mx4_matmul(dyq, wq_t, x.dtype, dx, stream)
-    dw = mx4_matmul(dyq_t, xq_t, dy.dtype, dw, stream)
+    device = x.device
+    _need_device(device, "dy", dy)
+    _need_device(device, "w", w)
+    dx = _result(dx, tokens, inputs, x.dtype, device, stream, "dx")
+    dw = _result(dw, outputs, inputs, dy.dtype, device, stream, "dw")
+    dxptr, dxcode, lddx, _, _ = _dense(dx, "dx")
+    dwptr, dwcode, lddw, _, _ = _dense(dw, "dw")
+    need = ctypes.c_int64()
+    _mx4_check(zero_mx4_linear_backward_workspace(tokens, w._c, need), "zero_mx4_linear_backward_workspace")
+    space = _T.empty(need.value, dtype=_T.uint8, device=device)
+    if stream is not None:
+        _lend(stream, space)
+    rounding, seed = _rounding(seed)
+    _mx4_check(_on_device(device, stream, zero_mx4_linear_backward, yptr, ycode, ldy, xptr, xcode, ldx, tokens, w._c,
+                          rounding, seed, dxptr, dxcode, lddx, dwptr, dwcode, lddw, space.data_ptr(), need.value),
+               "zero_mx4_linear_backward")
     return dx, dw
 
 

@@ -31,11 +31,16 @@ constexpr int kRowThreads = 256;
 
 template <class V, bool kStochastic>
 __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_constant__ MxQuantArgs a,
-                                                              const FastDiv per_row, const uint32_t units, const int vec) {
+                                                              const FastDiv per_row, const uint32_t units, const int vec,
+                                                              const uint32_t ctas) {
   constexpr int kUnits = V::kUnits;
   pdl_trigger();
+  if (blockIdx.x >= ctas) {  // the CTAs after those write another matrix's scale pieces
+    write_pieces(a.pieces, (blockIdx.x - ctas) * (kRowThreads / 32) + (threadIdx.x >> 5));
+    return;
+  }
   const typename V::raw* src = static_cast<const typename V::raw*>(a.src);
-  const uint32_t warps = gridDim.x * (kRowThreads / 32);
+  const uint32_t warps = ctas * (kRowThreads / 32);
   const int lane = threadIdx.x & 31;
   const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
   for (uint32_t u0 = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += kUnits * warps) {
@@ -81,18 +86,17 @@ constexpr int kTileRows = 128;
 constexpr int kTileWords = 64;  // 32-bit words of a tile's row
 
 template <class V, bool kFromMx, bool kRows, bool kStochastic>
-__global__ void __launch_bounds__(256, 3) mx_tile_kernel(const __grid_constant__ MxQuantArgs a, const uint32_t tiles_x,
-                                                         const int vec) {
+__device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t index, uint32_t tiles_x, int vec,
+                                              uint32_t (&tile)[kTileRows][kTileWords]) {
   using raw = typename V::raw;
   constexpr int kPer = 4 / sizeof(raw);           // columns in a word
   constexpr int kTileCols = kTileWords * kPer;
   constexpr int kVecs = kTileCols / 8;            // vectors of a tile's row
   constexpr int kLoads = kTileRows * kVecs / 256; // of a thread
   constexpr int kChunks = 2 / kPer;               // 16-byte chunks of a vector
-  __shared__ __align__(16) uint32_t tile[kTileRows][kTileWords];
   const raw* src = static_cast<const raw*>(a.src);
-  const int64_t r0 = (int64_t)(blockIdx.x / tiles_x) * kTileRows;
-  const int64_t c0 = (int64_t)(blockIdx.x % tiles_x) * kTileCols;
+  const int64_t r0 = (int64_t)(index / tiles_x) * kTileRows;
+  const int64_t c0 = (int64_t)(index % tiles_x) * kTileCols;
   const int t = threadIdx.x;
   const int cv = t % kVecs, rv = t / kVecs;
   const int64_t col = c0 + 8 * cv;
@@ -186,6 +190,30 @@ __global__ void __launch_bounds__(256, 3) mx_tile_kernel(const __grid_constant__
     *reinterpret_cast<uint4*>(a.out_t.codes + (oc + h) * a.out_t.code_pitch + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
     a.out_t.scales[(oc + h) * a.out_t.scale_pitch + b] = (uint8_t)s;
   }
+}
+
+template <class V, bool kFromMx, bool kRows, bool kStochastic>
+__global__ void __launch_bounds__(256, 3) mx_tile_kernel(const __grid_constant__ MxQuantArgs a, const uint32_t tiles_x,
+                                                         const int vec) {
+  __shared__ __align__(16) uint32_t tile[kTileRows][kTileWords];
+  pdl_trigger();
+  quantize_tile<V, kFromMx, kRows, kStochastic>(a, blockIdx.x, tiles_x, vec, tile);
+}
+
+// The three matrices of a linear layer's backward pass, one after another in
+// the grid.
+struct TileCounts {
+  uint32_t dy, x;           // CTAs of dy, of dy and x
+  uint32_t dy_x, x_x, w_x;  // tiles along a row
+  int dy_vec, x_vec;
+};
+template <class V, bool kStochastic>
+__global__ void __launch_bounds__(256, 3) mx_backward_kernel(const __grid_constant__ MxBackwardArgs a, const TileCounts n) {
+  __shared__ __align__(16) uint32_t tile[kTileRows][kTileWords];
+  pdl_trigger();
+  if (blockIdx.x < n.dy) quantize_tile<V, false, true, kStochastic>(a.dy, blockIdx.x, n.dy_x, n.dy_vec, tile);
+  else if (blockIdx.x < n.x) quantize_tile<V, false, false, false>(a.x, blockIdx.x - n.dy, n.x_x, n.x_vec, tile);
+  else quantize_tile<Vec16<Bf16>, true, false, false>(a.w, blockIdx.x - n.x, n.w_x, 1, tile);
 }
 
 // --------------------------------------------------------------- read back --
@@ -398,8 +426,9 @@ cudaError_t quantize_rows(MxQuantArgs a, int sm_count, cudaStream_t s) {
   const int vec = aligned(a.src, flat ? 0 : a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
   const int per_cta = V::kUnits * kRowThreads / 32;
   const int grid = cap_grid((p.units + per_cta - 1) / per_cta, 8 * sm_count);
-  if (a.stochastic) mx_rows_kernel<V, true><<<grid, kRowThreads, 0, s>>>(a, p.per_row, p.units, vec);
-  else mx_rows_kernel<V, false><<<grid, kRowThreads, 0, s>>>(a, p.per_row, p.units, vec);
+  const int more = (a.pieces.warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  if (a.stochastic) mx_rows_kernel<V, true><<<grid + more, kRowThreads, 0, s>>>(a, p.per_row, p.units, vec, grid);
+  else mx_rows_kernel<V, false><<<grid + more, kRowThreads, 0, s>>>(a, p.per_row, p.units, vec, grid);
   return cudaGetLastError();
 }
 
@@ -418,6 +447,24 @@ cudaError_t quantize_tiles(const MxQuantArgs& a, cudaStream_t s) {
     if (a.stochastic) mx_tile_kernel<V, kFromMx, false, true><<<grid, 256, 0, s>>>(a, x, vec);
     else mx_tile_kernel<V, kFromMx, false, false><<<grid, 256, 0, s>>>(a, x, vec);
   }
+  return cudaGetLastError();
+}
+
+template <class V>
+cudaError_t quantize_backward(const MxBackwardArgs& a, cudaStream_t s) {
+  constexpr int kCols = kTileWords * 4 / (int)sizeof(typename V::raw), kCols16 = 2 * kTileWords;
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  const int64_t dx = up(a.dy.cols, kCols), xx = up(a.x.cols, kCols), wx = up(a.w.cols, kCols16);
+  const int64_t nd = dx * up(a.dy.rows, kTileRows), nx = xx * up(a.x.rows, kTileRows), nw = wx * up(a.w.rows, kTileRows);
+  if (nd + nx + nw > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  TileCounts n;
+  n.dy = (uint32_t)nd, n.x = (uint32_t)(nd + nx);
+  n.dy_x = (uint32_t)dx, n.x_x = (uint32_t)xx, n.w_x = (uint32_t)wx;
+  n.dy_vec = aligned(a.dy.src, a.dy.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
+  n.x_vec = aligned(a.x.src, a.x.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
+  const unsigned grid = (unsigned)(nd + nx + nw);
+  if (a.dy.stochastic) mx_backward_kernel<V, true><<<grid, 256, 0, s>>>(a, n);
+  else mx_backward_kernel<V, false><<<grid, 256, 0, s>>>(a, n);
   return cudaGetLastError();
 }
 
@@ -450,6 +497,20 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, int sm_count, cudaStream_t 
     case kMxF32: return quantize_from<Vec32>(a, sm_count, s);
     default: return cudaErrorInvalidValue;
   }
+}
+
+cudaError_t launch_mx_backward(const MxBackwardArgs& a, int sm_count, cudaStream_t s) {
+  if (a.dy.type == a.x.type) {
+    switch (a.dy.type) {
+      case kMxBf16: return quantize_backward<Vec16<Bf16>>(a, s);
+      case kMxF16: return quantize_backward<Vec16<F16>>(a, s);
+      case kMxF32: return quantize_backward<Vec32>(a, s);
+      default: return cudaErrorInvalidValue;
+    }
+  }
+  cudaError_t e = launch_mx_quantize(a.dy, sm_count, s);
+  if (e == cudaSuccess) e = launch_mx_quantize(a.x, sm_count, s);
+  return e == cudaSuccess ? launch_mx_quantize(a.w, sm_count, s) : e;
 }
 
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, int sm_count, cudaStream_t s) {

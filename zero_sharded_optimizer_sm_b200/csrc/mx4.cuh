@@ -48,6 +48,24 @@ inline FastDiv fast_div(uint32_t d) {
   return f;
 }
 
+// Scale bytes in the tensor core's order ("pieces"), for matrices whose rows
+// of scales are not 16-byte aligned: kMxPiece bytes for each 128 rows and 16
+// blocks, row r's byte for block b at 512 (b / 4) + 16 (r % 32) +
+// 4 (r / 32 % 4) + b % 4; 0 past the matrix (the codes there are 0 too, but a
+// product with a NaN scale would not be).  Pieces of 128 rows follow one
+// another, a row block's groups of 16 blocks first, in whole pairs of blocks.
+constexpr int kMxPiece = 2048;
+struct MxPieceArgs {
+  const uint8_t* scales[2];
+  int64_t pitch[2];
+  int rows[2];
+  uint8_t* out[2];
+  int n;              // matrices
+  int warps0, warps;  // 32-row parts of the first, of all
+  int k_blocks, groups;
+  int pdl;
+};
+
 struct MxQuantArgs {
   const void* src;      // rows x cols of `type`, ld elements between rows; or an MX4 matrix:
   MxMatrix from;        //   (type ignored, codes set)
@@ -57,6 +75,13 @@ struct MxQuantArgs {
   MxMatrix out_t;       // blocks down the columns: cols x rows (codes null: not wanted)
   int stochastic;
   uint64_t seed;
+  MxPieceArgs pieces;   // written beside it when pieces.warps is not 0 (rows only)
+};
+
+// The backward pass of a linear layer's operands in one launch: dy along its
+// rows and down its columns, x down its columns (both of `type`), w's transpose.
+struct MxBackwardArgs {
+  MxQuantArgs dy, x, w;
 };
 
 struct MxDequantArgs {
@@ -95,7 +120,9 @@ struct MxMatmulArgs {
   int type;
   int64_t ld;
   void* workspace;  // mx_matmul_workspace bytes, 16-byte aligned
-  int pdl;  // 1: programmatic launch; the kernel waits for the grid before it before it reads `a`
+  int pdl;           // 1: programmatic launch: the grid before this one writes the operands
+  int b_ready;       // 1: but not b
+  int pieces_ready;  // 1: it writes b's pieces into the workspace
   const void* x;    // when set, a's rows x cols as a dense matrix of x_type, which the kernel quantises itself
   int x_type;       //   (a's codes and scales are not used)
   int64_t x_ld;
@@ -103,11 +130,14 @@ struct MxMatmulArgs {
 constexpr int kMxFewRows = 16;  // rows of x that launch_mx_matmul can quantise itself
 
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, int sm_count, cudaStream_t s);
+cudaError_t launch_mx_backward(const MxBackwardArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int sm_count, cudaStream_t s);
 int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b);
+// b's part of the workspace as pieces to be written (none when its rows load as they lie).
+bool mx_linear_pieces(const MxMatrix& b, void* workspace, MxPieceArgs* g);
 int64_t mx_few_rows_workspace(const MxMatrix& b);  // with x instead of a
 cudaError_t mx_matmul_error(unsigned* flag, cudaStream_t s);
 

@@ -103,7 +103,7 @@ zero_status check_workspace(const void* workspace, int64_t have, int64_t need) {
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 
 zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtype, int64_t ld, void* workspace, int pdl,
-                   int sms, cudaStream_t s) {
+                   int b_ready, int sms, cudaStream_t s) {
   zsm::MxMatmulArgs m = {};
   m.a = matrix(a);
   m.b = matrix(b);
@@ -112,6 +112,7 @@ zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtyp
   m.ld = a.rows == 1 ? std::max<int64_t>(ld, b.rows) : ld;
   m.workspace = workspace;
   m.pdl = pdl;
+  m.b_ready = m.pieces_ready = b_ready;
   const cudaError_t e = zsm::launch_mx_matmul(m, sms, s);
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 product launch");
 }
@@ -129,6 +130,28 @@ int64_t linear_own(int64_t tokens, int64_t inputs) {
 int64_t linear_need(int64_t tokens, const zero_mx4* w) {
   if (tokens <= zsm::kMxFewRows) return zsm::mx_few_rows_workspace(matrix(*w));  // x is quantised in the product
   return linear_own(tokens, w->cols) + zsm::mx_matmul_workspace(matrix(quantised_x(nullptr, tokens, w->cols)), matrix(*w));
+}
+
+// zero_mx4_linear_backward's workspace: dy, its transpose and x's and w's, each
+// with rows of scales of 16-byte multiples.
+struct Backward {
+  zero_mx4 dy, dy_t, x_t, w_t;
+  int64_t bytes;
+};
+Backward backward_parts(uint8_t* at, int64_t tokens, int64_t o, int64_t k) {
+  Backward p;
+  int64_t used = 0;
+  auto part = [&](int64_t rows, int64_t cols) {
+    const zero_mx4 m = quantised_x(at ? at + used : nullptr, rows, cols);
+    used += linear_own(rows, cols);
+    return m;
+  };
+  p.dy = part(tokens, o);
+  p.dy_t = part(o, tokens);
+  p.x_t = part(k, tokens);
+  p.w_t = part(k, o);
+  p.bytes = used;
+  return p;
 }
 
 // A product over no elements: zeros.
@@ -230,7 +253,7 @@ zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   const int64_t need = zsm::mx_matmul_workspace(matrix(*a), matrix(*b));
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return st;
-  return matmul(*a, *b, out, dtype, ld, workspace, 0, sms, s);
+  return matmul(*a, *b, out, dtype, ld, workspace, 0, 0, sms, s);
 }
 
 zero_status zero_mx4_linear_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes) {
@@ -274,9 +297,63 @@ zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_
     const cudaError_t er = zsm::launch_mx_matmul(m, sms, s);
     return er == cudaSuccess ? ZERO_OK : cuda_fail(er, "MX4 product launch");
   }
-  st = zero_mx4_quantize(x, dtype, tokens, w->cols, ld, ZERO_MX4_NEAREST, 0, &xq, nullptr, stream);
+  // one launch quantises x and, where they are needed, writes w's scale pieces
+  zsm::MxQuantArgs q = {};
+  q.src = x, q.type = dtype;
+  q.rows = tokens, q.cols = w->cols, q.ld = ld;
+  q.out = matrix(xq);
+  if (!zsm::mx_linear_pieces(matrix(*w), at + own, &q.pieces)) return cuda_fail(cudaErrorInvalidValue, "MX4 scale pieces");
+  const cudaError_t er = zsm::launch_mx_quantize(q, sms, s);
+  if (er != cudaSuccess) return cuda_fail(er, "MX4 quantise launch");
+  return matmul(xq, *w, y, y_dtype, ld_y, at + own, 1, 1, sms, s);
+}
+
+zero_status zero_mx4_linear_backward_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes) {
+  if (!bytes) return fail(ZERO_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  const zero_status st = check_mx4("w", w);
   if (st != ZERO_OK) return st;
-  return matmul(xq, *w, y, y_dtype, ld_y, at + own, 1, sms, s);
+  if (tokens < 0 || tokens > kMaxDim) return fail(ZERO_EINVAL, "%lld tokens", (long long)tokens);
+  if (tokens && w->rows && w->cols) *bytes = backward_parts(nullptr, tokens, w->rows, w->cols).bytes;
+  return ZERO_OK;
+}
+
+zero_status zero_mx4_linear_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* x, int32_t x_dtype,
+                                     int64_t ld_x, int64_t tokens, const zero_mx4* w, int32_t rounding, uint64_t seed,
+                                     void* dx, int32_t dx_dtype, int64_t ld_dx, void* dw, int32_t dw_dtype, int64_t ld_dw,
+                                     void* workspace, int64_t workspace_bytes, void* stream) {
+  zero_status st = check_mx4("w", w);
+  if (st != ZERO_OK) return st;
+  const int64_t o = w->rows, k = w->cols;
+  if ((st = check_dense("dy", dy, dy_dtype, tokens, o, ld_dy)) != ZERO_OK) return st;
+  if ((st = check_dense("x", x, x_dtype, tokens, k, ld_x)) != ZERO_OK) return st;
+  if ((st = check_rounding(rounding)) != ZERO_OK) return st;
+  if ((st = check_dense("dx", dx, dx_dtype, tokens, k, ld_dx)) != ZERO_OK) return st;
+  if ((st = check_dense("dw", dw, dw_dtype, o, k, ld_dw)) != ZERO_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (k == 0) return ZERO_OK;
+  if (tokens == 0) return o ? zero_fill(dw, dw_dtype, o, k, ld_dw, s) : ZERO_OK;
+  if (o == 0) return zero_fill(dx, dx_dtype, tokens, k, ld_dx, s);
+  const Backward p = backward_parts(static_cast<uint8_t*>(workspace), tokens, o, k);
+  if ((st = check_workspace(workspace, workspace_bytes, p.bytes)) != ZERO_OK) return st;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  zsm::MxBackwardArgs a = {};
+  a.dy.src = dy, a.dy.type = dy_dtype;
+  a.dy.rows = tokens, a.dy.cols = o, a.dy.ld = tokens > 1 ? ld_dy : o;
+  a.dy.out = matrix(p.dy), a.dy.out_t = matrix(p.dy_t);
+  a.dy.stochastic = rounding == ZERO_MX4_STOCHASTIC, a.dy.seed = seed;
+  a.x.src = x, a.x.type = x_dtype;
+  a.x.rows = tokens, a.x.cols = k, a.x.ld = tokens > 1 ? ld_x : k;
+  a.x.out_t = matrix(p.x_t);
+  a.w.from = matrix(*w);
+  a.w.rows = o, a.w.cols = k;
+  a.w.out_t = matrix(p.w_t);
+  e = zsm::launch_mx_backward(a, sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "MX4 backward quantise launch");
+  if ((st = matmul(p.dy, p.w_t, dx, dx_dtype, ld_dx, nullptr, 1, 0, sms, s)) != ZERO_OK) return st;
+  return matmul(p.dy_t, p.x_t, dw, dw_dtype, ld_dw, nullptr, 1, 0, sms, s);
 }
 
 zero_status zero_mx4_check(void* stream) {

@@ -9,8 +9,8 @@
 // codes and 8 scale bytes per matrix row, four instructions of 64 elements.
 //
 // Roles of a CTA's warps: 0 loads codes and scales (TMA); 1 issues the
-// products; 2-5 bring scales into TMEM; 6-9 read the accumulator and store (a
-// warp reaches the 32 lanes of TMEM that its number modulo 4 says).
+// products; 2-5 and 6-9 bring scales into TMEM; 6-9 read the accumulator and
+// store (a warp reaches the 32 lanes of TMEM that its number modulo 4 says).
 //
 // Scales: the tensor core wants the four scale bytes that row r has for 128 k
 // elements in lane r % 32 of every 32 lanes, column r / 32.  They come two k
@@ -76,7 +76,7 @@ struct MmArgs {
 // A stage: the codes of both operands for one k tile.  A group of scales: 16
 // bytes for each row (up to 128 of P, then of Q) for two k tiles.
 __host__ __device__ constexpr int stage_bytes(int bn) { return (kLanes + bn) * kTileKBytes; }
-constexpr int kGroup = 2048;  // of 128 rows
+constexpr int kGroup = kMxPiece;  // of 128 rows
 // TMEM columns: the accumulator, then four sets of scales used by turns.
 constexpr int kSets = 4;
 constexpr int kScaleCols = 16;
@@ -199,14 +199,14 @@ __device__ __forceinline__ int wait_bounded(uint64_t* bar, unsigned parity, vola
   }
   return 0;
 }
-// Whether all four scale warps' threads say yes (named barrier 1).
-__device__ __forceinline__ bool all_scale_warps(bool yes) {
+// Whether all of a team's 128 threads say yes (named barriers 1 and 2).
+__device__ __forceinline__ bool all_of_team(int team, bool yes) {
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((int)yes)
+      : "r"((int)yes), "r"(team + 1)
       : "memory");
   return r != 0;
 }
@@ -403,39 +403,9 @@ __device__ __forceinline__ void load_part(ScaleGroup& g, const uint8_t* piece, i
   }
 }
 
-// Scales in the order above: 2048 bytes for each 128 rows and two k tiles,
-// row r's byte for block b of the 16 at 512 (b / 4) + 16 (r % 32) +
-// 4 (r / 32 % 4) + b % 4; 0 past the matrix (the codes there are 0 too, but a
-// product with a NaN scale would not be).  A warp takes 32 rows and two k
-// tiles, a lane a row.
-struct PieceArgs {
-  const uint8_t* scales[2];
-  int64_t pitch[2];
-  int rows[2];
-  uint8_t* out[2];
-  int warps0, warps;  // 32-row parts of the first operand, of both
-  int k_blocks, groups;
-  int pdl;
-};
-
-__global__ void __launch_bounds__(256) mx_scale_pieces_kernel(const __grid_constant__ PieceArgs a) {
+__global__ void __launch_bounds__(256) mx_scale_pieces_kernel(const __grid_constant__ MxPieceArgs a) {
   if (a.pdl) dev::pdl_wait();
-  const int lane = threadIdx.x & 31;
-  int w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= a.warps) return;
-  const int o = w >= a.warps0 ? 1 : 0;
-  if (o) w -= a.warps0;
-  const int g = w % a.groups, r32 = w / a.groups;
-  const int64_t row = 32ll * r32 + lane;
-  const int n = row < a.rows[o] ? min(a.k_blocks - 16 * g, 16) : 0;
-  const uint8_t* p = a.scales[o] + (n > 0 ? row * a.pitch[o] + 16 * g : 0);
-  uint32_t v[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j < n) v[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-  uint8_t* out = a.out[o] + ((int64_t)(r32 >> 2) * a.groups + g) * kGroup + 16 * lane + 4 * (r32 & 3);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(out + 512 * j) = v[j];
+  mx::write_pieces(a, blockIdx.x * 8 + (threadIdx.x >> 5));
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -464,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
   extern __shared__ uint8_t raw_smem[];
   __shared__ Shared<BN, STAGES, GROUPS> sh;
   constexpr bool kDense = !std::is_void<V>::value;
-  __shared__ uint32_t x_scales[kDense ? 2 : 1][2 * kMxFewRows];  // of two k tiles by turns: a row's 8 bytes
+  __shared__ uint32_t x_scales[kDense ? 2 : 1][2][2 * kMxFewRows];  // a team's, of two k tiles by turns: a row's 8 bytes
   constexpr int kStage = stage_bytes(BN);
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   uint8_t* group_smem = smem + STAGES * kStage;
@@ -608,33 +578,40 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
         mbar_wait(&sh.drained, 0);
       }
     }
-  } else if (warp < 6) {
-    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc_cols(BN);
-    int it = 0, s = 0, gs = 0, old = 0;  // old: the stage whose products used this set of scales before
+  } else {
+    // Two teams of four warps (2-5, 6-9), a warp for each 32 lanes of TMEM,
+    // take the groups of scales by turns; the second then stores the tile.
+    const int team = warp < 6 ? 0 : 1, quarter = warp & 3;
+    const uint32_t ts = tmem + ((uint32_t)(32 * quarter) << 16) + acc_cols(BN);
+    int it = 0, s = 0, gs = 0, g_at = 0, old = 0;  // old: the stage whose products used this set of scales before
     unsigned gparity = 0, parity_old = 0;
     bool ok = true;
     // a dense Q's vectors of the next k tile (rows wq, wq + 4, ...), loaded one k tile ahead
-    const int wq = warp - 2;
+    const int wq = (warp - 2) & 3;
     constexpr int kRowsOf = kDense ? kMxFewRows / kScaleWarps : 1;
     using Dense = typename std::conditional<kDense, V, mx::Vec32>::type;
     Dense next[kRowsOf];
+    const typename Dense::raw* x_at[kRowsOf];
+#pragma unroll
+    for (int i = 0; i < kRowsOf; ++i)
+      x_at[i] = static_cast<const typename Dense::raw*>(a.x) + (wq + kScaleWarps * i) * a.x_ld + 8 * lane;
     auto fetch = [&](int kt) {
-      const int col = kTileK * kt + 8 * lane;
+      const int left = a.x_cols - kTileK * kt - 8 * lane;
+      const bool whole = left >= 8 && a.x_vec;
 #pragma unroll
       for (int i = 0; i < kRowsOf; ++i) {
-        const int row = wq + kScaleWarps * i, left = row < a.q_rows ? a.x_cols - col : 0;
-        const auto* p = static_cast<const typename Dense::raw*>(a.x) + row * a.x_ld + col;
-        next[i].load_if(p, left >= 8 && a.x_vec);
-        if (left > 0 && !(left >= 8 && a.x_vec)) next[i].load(p, left);
+        if (wq + kScaleWarps * i >= a.q_rows) break;  // the same for the warp
+        next[i].load_if(x_at[i] + kTileK * kt, whole);
+        if (left > 0 && !whole) next[i].load(x_at[i] + kTileK * kt, left);
       }
     };
     if (kDense) {
       // the rows past Q's last stay zero in every stage
-      for (int i = threadIdx.x - 64; i < STAGES * kMxFewRows * 8; i += 32 * kScaleWarps)
+      for (int i = threadIdx.x - 64; i < STAGES * kMxFewRows * 8; i += kThreadsMm - 64)
         *reinterpret_cast<uint4*>(smem + i / (8 * kMxFewRows) * kStage + kLanes * kTileKBytes +
                                   16 * (i % (8 * kMxFewRows))) = make_uint4(0u, 0u, 0u, 0u);
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the four scale warps
-      if (first < a.n_tiles) fetch(k0);
+      fence_proxy_async_smem();
+      asm volatile("bar.sync 3, %0;" ::"n"(kThreadsMm - 64) : "memory");  // both teams
     }
     // P's scales straight from their rows, likewise ahead by a group
     ScaleGroup direct;
@@ -646,17 +623,38 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
                                a.p_align);
       }
     };
-    if (kDirect && first < a.n_tiles) fetch_scales(first, k0);
-    for (int tile = first; tile < a.n_tiles && ok; tile += step) {
+    auto next_old = [&] {
+      if (++old == STAGES) {
+        old = 0;
+        parity_old ^= 1;
+      }
+    };
+    int n_tile = 0;
+    for (int tile = first; tile < a.n_tiles && ok; tile += step, ++n_tile) {
       // Q's rows start inside a piece of 128 when BN is less: q_part turns lane + 32 j into them
       const int q_part = a.q_pieces ? (tile / a.p_tiles) * BN % kLanes : 0;
-      for (int kt = k0; kt < k1 && ok; kt += 2) {
+      const int mine0 = k0 + 2 * ((g_at ^ team) & 1);  // this team's first k tile
+      if (mine0 < k1) {
+        if (kDense) fetch(mine0);
+        if (kDirect) fetch_scales(tile, mine0);
+      }
+      for (int kt = k0; kt < k1 && ok; kt += 2, ++g_at) {
+        if ((g_at & 1) != team) {
+          for (int h = 0; h < 2 && kt + h < k1; ++h, ++it) {
+            if (it >= kSets) next_old();
+            if (++s == STAGES) s = 0;
+          }
+          if (++gs == GROUPS) {
+            gs = 0;
+            gparity ^= 1;
+          }
+          continue;
+        }
         ScaleGroup p, q;
         if (kDirect) {
           p = direct;
           p.transpose();
-          if (kt + 2 < k1) fetch_scales(tile, kt + 2);
-          else if (tile + step < a.n_tiles) fetch_scales(tile + step, k0);
+          if (kt + 4 < k1) fetch_scales(tile, kt + 4);
         } else {
           ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity));
           if (!kDense && !ok) break;
@@ -669,25 +667,23 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
         if (by_group) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
-          if (++gs == GROUPS) {
-            gs = 0;
-            gparity ^= 1;
-          }
+        }
+        if (++gs == GROUPS) {
+          gs = 0;
+          gparity ^= 1;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (kt + h >= k1) break;
           if (it >= kSets) {  // the set is free, and with it (kSets <= STAGES) the stage
             ok = ok && __all_sync(0xFFFFFFFFu, wait(&sh.empty[old], parity_old));
-            if (++old == STAGES) {
-              old = 0;
-              parity_old ^= 1;
-            }
+            next_old();
           }
           if constexpr (kDense) {
+            uint32_t* x_scale = x_scales[team][it & 1];
             if (ok) {
               uint8_t* to = smem + s * kStage + kLanes * kTileKBytes + 4 * (lane & 3);
-              uint8_t* sc = reinterpret_cast<uint8_t*>(x_scales[it & 1]);
+              uint8_t* sc = reinterpret_cast<uint8_t*>(x_scale);
 #pragma unroll
               for (int i = 0; i < kRowsOf; ++i) {
                 const int row = wq + kScaleWarps * i;
@@ -697,14 +693,14 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
                 *reinterpret_cast<uint32_t*>(to + 128 * row + 16 * ((lane >> 2) ^ (row & 7))) = w;  // swizzled as TMA does
                 if ((lane & 3) == 0) sc[8 * row + (lane >> 2)] = (uint8_t)sb;
               }
-              if (kt + h + 1 < k1) fetch(kt + h + 1);
-              else if (tile + step < a.n_tiles) fetch(k0);
+              const int after = h == 0 && kt + 1 < k1 ? kt + 1 : kt + 4;
+              if (after < k1) fetch(after);
               fence_proxy_async_smem();
             }
-            ok = all_scale_warps(ok);  // the row's scales are there; or all four stop together
+            ok = all_of_team(team, ok);  // the row's scales are there; or all four stop together
             if (ok) {
-              q.m[2 * h].x = lane < a.q_rows ? x_scales[it & 1][2 * lane] : 0u;
-              q.m[2 * h + 1].x = lane < a.q_rows ? x_scales[it & 1][2 * lane + 1] : 0u;
+              q.m[2 * h].x = lane < a.q_rows ? x_scale[2 * lane] : 0u;
+              q.m[2 * h + 1].x = lane < a.q_rows ? x_scale[2 * lane + 1] : 0u;
             }
           }
           if (!ok) break;
@@ -719,18 +715,16 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
           if (++s == STAGES) s = 0;
         }
       }
-    }
-  } else if (a.split == 1) {
-    const int w = warp & 3;
-    int n = 0;
-    for (int tile = first; tile < a.n_tiles; tile += step, ++n) {
-      if (!__all_sync(0xFFFFFFFFu, wait(&sh.acc_full, n & 1))) break;
+      if (team == 0 || a.split > 1) continue;
+      ok = ok && __all_sync(0xFFFFFFFFu, wait(&sh.acc_full, n_tile & 1));
+      if (kDense) ok = all_of_team(team, ok);
+      if (!ok) break;
       fence_after();
-      const int64_t p = (int64_t)(tile % a.p_tiles) * kLanes + 32 * w + lane, q0 = (int64_t)(tile / a.p_tiles) * BN;
+      const int64_t p = (int64_t)(tile % a.p_tiles) * kLanes + 32 * quarter + lane, q0 = (int64_t)(tile / a.p_tiles) * BN;
       constexpr int kStep = BN < 32 ? 8 : 32;
       for (int c = 0; c < BN && q0 + c < a.q_rows; c += kStep) {
         float v[kStep];
-        tmem_read<kStep>(tmem + ((uint32_t)(32 * w) << 16) + c, v);
+        tmem_read<kStep>(tmem + ((uint32_t)(32 * quarter) << 16) + c, v);
         store_run<kStep>(a, p, q0 + c, v);
       }
       fence_before();
@@ -1103,6 +1097,18 @@ int64_t row_blocks(const MxMatrix& m) { return 2 * ((m.rows + 255) / 256); }
 int64_t groups_of(const MxMatrix& m) { return (mx_blocks(m.cols) + 15) / 16; }
 int64_t pieces_bytes(const MxMatrix& m) { return rows_load(m) ? 0 : row_blocks(m) * groups_of(m) * kGroup; }
 
+// Adds a matrix's pieces to the kernel's work (warps -1: too many).
+void add_pieces(MxPieceArgs* g, const MxMatrix& m, uint8_t* out) {
+  if (!out || g->warps < 0) return;
+  const int i = g->n++;
+  g->groups = (int)groups_of(m);
+  g->k_blocks = (int)mx_blocks(m.cols);
+  g->scales[i] = m.scales, g->pitch[i] = m.scale_pitch, g->rows[i] = (int)m.rows, g->out[i] = out;
+  const int64_t warps = g->warps + 4 * row_blocks(m) * g->groups;
+  g->warps = warps > 0x7FFFFFFF - 8 ? -1 : (int)warps;
+  if (i == 0) g->warps0 = g->warps;
+}
+
 struct Maps {
   CUtensorMap p, q, ps, qs;
 };
@@ -1189,6 +1195,12 @@ bool by_pairs(int64_t m, int64_t n, int sm_count) {
 }  // namespace
 
 int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b) { return pieces_bytes(a) + pieces_bytes(b); }
+bool mx_linear_pieces(const MxMatrix& b, void* workspace, MxPieceArgs* g) {
+  *g = MxPieceArgs{};
+  if (rows_load(b)) return true;
+  add_pieces(g, b, static_cast<uint8_t*>(workspace));
+  return g->warps >= 0;
+}
 int64_t mx_few_rows_workspace(const MxMatrix& b) { return words_load(b) ? 0 : pieces_bytes(b); }
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
@@ -1226,26 +1238,18 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   if (!m.x && !rows_load(q)) q_pieces = space;
   a.p_pieces = p_pieces != nullptr, a.q_pieces = q_pieces != nullptr;
   if (p_pieces || q_pieces) {
-    PieceArgs g = {};
-    const MxMatrix* of[2] = {p_pieces ? &p : &q, q_pieces ? &q : nullptr};
-    uint8_t* to[2] = {p_pieces ? p_pieces : q_pieces, q_pieces};
-    const int n = p_pieces && q_pieces ? 2 : 1;
-    g.groups = (int)groups_of(p);
-    g.k_blocks = (int)mx_blocks(p.cols);
-    int64_t warps = 0;
-    for (int i = 0; i < n; ++i) {
-      g.scales[i] = of[i]->scales, g.pitch[i] = of[i]->scale_pitch, g.rows[i] = (int)of[i]->rows, g.out[i] = to[i];
-      warps += 4 * row_blocks(*of[i]) * g.groups;
-      if (i == 0) g.warps0 = (int)std::min<int64_t>(warps, 0x7FFFFFFF);
-    }
-    if (warps > 0x7FFFFFFF - 8) return cudaErrorInvalidValue;
-    g.warps = (int)warps;
+    MxPieceArgs g = {};
+    add_pieces(&g, p, p_pieces);
+    add_pieces(&g, q, q_pieces);
+    if (g.warps < 0) return cudaErrorInvalidValue;
     g.pdl = m.pdl;
-    const cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, m.pdl != 0, g);
-    if (e != cudaSuccess) return e;
-    a.pdl = 1;
+    if (!m.pieces_ready) {
+      const cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, m.pdl != 0, g);
+      if (e != cudaSuccess) return e;
+      a.pdl = 1;
+    }
   }
-  a.p_early = swap && m.pdl && !p_pieces && !q_pieces;  // then the grid before this one writes only a
+  a.p_early = swap && m.b_ready && !p_pieces && !q_pieces;
 
   if (many) return launch_pair(p, q, a, p_pieces, q_pieces, sm_count, s);
   const int64_t p_tiles = (p.rows + kLanes - 1) / kLanes;

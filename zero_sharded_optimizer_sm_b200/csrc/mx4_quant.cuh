@@ -118,5 +118,23 @@ __device__ __forceinline__ uint32_t max_of_four(uint32_t m) {  // over four neig
   return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 
+// One warp's part of the pieces: 32 rows, 16 blocks, a lane a row.
+__device__ __forceinline__ void write_pieces(const MxPieceArgs& a, int w) {
+  if (w >= a.warps) return;
+  const int lane = threadIdx.x & 31, o = w >= a.warps0 ? 1 : 0;
+  if (o) w -= a.warps0;
+  const int g = w % a.groups, r32 = w / a.groups;
+  const int64_t row = 32ll * r32 + lane;
+  const int n = row < a.rows[o] ? min(a.k_blocks - 16 * g, 16) : 0;
+  const uint8_t* p = a.scales[o] + (n > 0 ? row * a.pitch[o] + 16 * g : 0);
+  uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < n) v[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  uint8_t* out = a.out[o] + ((int64_t)(r32 >> 2) * a.groups + g) * kMxPiece + 16 * lane + 4 * (r32 & 3);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(out + 512 * j) = v[j];
+}
+
 }  // namespace mx
 }  // namespace zsm
