@@ -844,10 +844,9 @@ zero_status zero_mx4_transpose(const zero_mx4* in, int32_t rounding, uint64_t se
  * ld elements between rows.  No passage of the pages defines it. */
 zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, int64_t ld, void* stream);
 
-/* Bytes of workspace that zero_mx4_matmul needs for these matrices: 16 bytes
+/* Bytes of workspace that zero_mx4_matmul needs for these matrices (16 bytes
  * for each row and 512 columns of a matrix whose rows of scales are not
- * 16-byte aligned, and of both for a large result; none otherwise.  Host
- * only. */
+ * 16-byte aligned, none for one whose rows are).  Host only. */
 zero_status zero_mx4_matmul_workspace(const zero_mx4* a, const zero_mx4* b, int64_t* bytes);
 
 /* out[i][j] = sum over k of a[i][k] b[j][k] (a->rows x b->rows of `dtype`, ld

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_const
       const uint32_t u = min(u0 + k * warps, units - 1);  // past the end: the last piece again, not stored
       row[k] = div_by(u, per_row);
       col[k] = (int64_t)(u - row[k] * per_row.d) * 256 + lane * 8;
-      load8(x[k], src + row[k] * a.ld + col[k], row[k] < a.rows ? a.cols - col[k] : 0, vec);
+      load8(x[k], src + row[k] * a.ld + col[k], a.cols - col[k], vec);
     }
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) m[k] = x[k].max_bits();
@@ -65,10 +65,10 @@ __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_const
       const uint32_t s = scale_code(m[k]);
       const int64_t b = col[k] >> 5;
       const uint32_t w = encode<kStochastic>(x[k], s, (uint64_t)(row[k] * nb + b), lane & 3, a.seed);
-      // (pieces reach past the matrix: zeros there)
-      const bool in = b < nb && row[k] < a.rows, live = u0 + k * warps < units;
-      if (in && live) *reinterpret_cast<uint32_t*>(a.out.codes + row[k] * a.out.code_pitch + (col[k] >> 1)) = w;
-      if ((in || a.out.tiled) && live && (lane & 3) == 0) *scale_at(a.out, row[k], b) = (uint8_t)s;
+      if (b < nb && u0 + k * warps < units) {
+        *reinterpret_cast<uint32_t*>(a.out.codes + row[k] * a.out.code_pitch + (col[k] >> 1)) = w;
+        if ((lane & 3) == 0) a.out.scales[row[k] * a.out.scale_pitch + b] = (uint8_t)s;
+      }
     }
   }
 }
@@ -84,11 +84,6 @@ __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_const
 // which puts the four blocks' reads on different banks.
 constexpr int kTileRows = 128;
 constexpr int kTileWords = 64;  // 32-bit words of a tile's row
-
-// Whether (row, block) lies in the pieces of a matrix of `rows` rows of nb blocks.
-__device__ __forceinline__ bool in_pieces(int64_t row, int64_t b, int64_t rows, int64_t nb) {
-  return row < (rows + 255) / 256 * 256 && b < (nb + 15) / 16 * 16;
-}
 
 template <class V, bool kFromMx, bool kRows, bool kStochastic>
 __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t index, uint32_t tiles_x, int vec,
@@ -150,9 +145,10 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
       const int64_t row = r0 + rv + (256 / kVecs) * i;
       const uint32_t s = scale_code(m[i]);
       const uint32_t w = encode<kStochastic>(x[i], s, (uint64_t)(row * nb + b), cv & 3, a.seed);
-      const bool in = row < a.rows && b < nb;
-      if (in) *reinterpret_cast<uint32_t*>(a.out.codes + row * a.out.code_pitch + (col >> 1)) = w;
-      if ((in || (a.out.tiled && in_pieces(row, b, a.rows, nb))) && (cv & 3) == 0) *scale_at(a.out, row, b) = (uint8_t)s;
+      if (row < a.rows && b < nb) {
+        *reinterpret_cast<uint32_t*>(a.out.codes + row * a.out.code_pitch + (col >> 1)) = w;
+        if ((cv & 3) == 0) a.out.scales[row * a.out.scale_pitch + b] = (uint8_t)s;
+      }
     }
   }
   __syncthreads();
@@ -160,7 +156,7 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
   const int q = t & 3, word = t >> 2;
   const int64_t b = r0 / kMxBlock + q;
   const int64_t oc = c0 + kPer * word;
-  if (a.out_t.tiled ? !in_pieces(oc, b, a.cols, nbt) : b >= nbt || oc >= a.cols) return;
+  if (b >= nbt || oc >= a.cols) return;
   const uint32_t* column = &tile[32 * q][(word + 8 * q) & (kTileWords - 1)];
   uint32_t x32[32];
   uint32_t m = 0;
@@ -172,7 +168,7 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
   }
 #pragma unroll
   for (int h = 0; h < kPer; ++h) {
-    if (oc + h >= a.cols && !a.out_t.tiled) break;
+    if (oc + h >= a.cols) break;
     auto value = [&](int j) -> float {
       if constexpr (kPer == 2) return h ? V::hi(x32[j]) : V::lo(x32[j]);
       else return __uint_as_float(x32[j]);
@@ -191,9 +187,8 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
       w[k] = kStochastic ? encode8_stochastic(e, (uint64_t)((oc + h) * nbt + b), k, a.seed) : encode8(e);
       if (s == 255u) w[k] = 0u;
     }
-    if (b < nbt && oc + h < a.cols)
-      *reinterpret_cast<uint4*>(a.out_t.codes + (oc + h) * a.out_t.code_pitch + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
-    *scale_at(a.out_t, oc + h, b) = (uint8_t)s;
+    *reinterpret_cast<uint4*>(a.out_t.codes + (oc + h) * a.out_t.code_pitch + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+    a.out_t.scales[(oc + h) * a.out_t.scale_pitch + b] = (uint8_t)s;
   }
 }
 
@@ -423,15 +418,11 @@ bool pieces_of(int64_t rows, int64_t cols, bool end_to_end, Pieces* p) {
 
 template <class V>
 cudaError_t quantize_rows(MxQuantArgs a, int sm_count, cudaStream_t s) {
-  const bool flat = !a.out.tiled && a.cols % kMxBlock == 0 && a.ld == a.cols && a.out.code_pitch == a.cols / 2 &&
+  const bool flat = a.cols % kMxBlock == 0 && a.ld == a.cols && a.out.code_pitch == a.cols / 2 &&
                     a.out.scale_pitch == a.cols / kMxBlock;
   Pieces p;
-  if (a.out.tiled) {  // every block of the pieces: padded rows, whole groups
-    if (!pieces_of(128 * mx_row_blocks(a.rows), 16 * kMxBlock * mx_groups(a.cols), false, &p)) return cudaErrorInvalidValue;
-  } else {
-    if (!pieces_of(a.rows, a.cols, flat, &p)) return cudaErrorInvalidValue;
-    a.rows = p.rows, a.cols = p.cols;
-  }
+  if (!pieces_of(a.rows, a.cols, flat, &p)) return cudaErrorInvalidValue;
+  a.rows = p.rows, a.cols = p.cols;
   const int vec = aligned(a.src, flat ? 0 : a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
   const int per_cta = V::kUnits * kRowThreads / 32;
   const int grid = cap_grid((p.units + per_cta - 1) / per_cta, 8 * sm_count);
@@ -441,21 +432,10 @@ cudaError_t quantize_rows(MxQuantArgs a, int sm_count, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Tiles along a row and down a column; pieces reach 512 columns and 256 rows
-// past the matrix, either way round.
-template <class V>
-void tiles_of(const MxQuantArgs& a, int64_t* tx, int64_t* ty) {
-  constexpr int kCols = kTileWords * 4 / (int)sizeof(typename V::raw);
-  const bool more = (a.out.codes && a.out.tiled) || (a.out_t.codes && a.out_t.tiled);
-  const int64_t cols = more ? (a.cols + 511) / 512 * 512 : a.cols, rows = more ? (a.rows + 511) / 512 * 512 : a.rows;
-  *tx = (cols + kCols - 1) / kCols;
-  *ty = (rows + kTileRows - 1) / kTileRows;
-}
-
 template <class V, bool kFromMx>
 cudaError_t quantize_tiles(const MxQuantArgs& a, cudaStream_t s) {
-  int64_t tx, ty;
-  tiles_of<V>(a, &tx, &ty);
+  constexpr int kCols = kTileWords * 4 / (int)sizeof(typename V::raw);
+  const int64_t tx = (a.cols + kCols - 1) / kCols, ty = (a.rows + kTileRows - 1) / kTileRows;
   if (tx * ty > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const int vec = kFromMx || aligned(a.src, a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
   const unsigned grid = (unsigned)(tx * ty);
@@ -472,11 +452,10 @@ cudaError_t quantize_tiles(const MxQuantArgs& a, cudaStream_t s) {
 
 template <class V>
 cudaError_t quantize_backward(const MxBackwardArgs& a, cudaStream_t s) {
-  int64_t dx, dyt, xx, xy, wx, wy;
-  tiles_of<V>(a.dy, &dx, &dyt);
-  tiles_of<V>(a.x, &xx, &xy);
-  tiles_of<Vec16<Bf16>>(a.w, &wx, &wy);
-  const int64_t nd = dx * dyt, nx = xx * xy, nw = wx * wy;
+  constexpr int kCols = kTileWords * 4 / (int)sizeof(typename V::raw), kCols16 = 2 * kTileWords;
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  const int64_t dx = up(a.dy.cols, kCols), xx = up(a.x.cols, kCols), wx = up(a.w.cols, kCols16);
+  const int64_t nd = dx * up(a.dy.rows, kTileRows), nx = xx * up(a.x.rows, kTileRows), nw = wx * up(a.w.rows, kTileRows);
   if (nd + nx + nw > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   TileCounts n;
   n.dy = (uint32_t)nd, n.x = (uint32_t)(nd + nx);

@@ -29,13 +29,9 @@ struct MxMatrix {
   int64_t rows, cols;
   int64_t code_pitch;   // bytes between rows, a multiple of 16
   int64_t scale_pitch;  // bytes between rows
-  int tiled = 0;        // 1: the scales are pieces (see kMxPiece), in a workspace
 };
 
 inline int64_t mx_blocks(int64_t n) { return (n + kMxBlock - 1) / kMxBlock; }
-// Row blocks of 128 (whole pairs) and groups of 16 blocks in a matrix's pieces.
-inline int64_t mx_row_blocks(int64_t rows) { return 2 * ((rows + 255) / 256); }
-inline int64_t mx_groups(int64_t cols) { return (mx_blocks(cols) + 15) / 16; }
 
 // Division by a fixed 32-bit divisor of dividends below 2^31: the rounded-up
 // reciprocal's high half, exact there because 2^(31 + l) (l = ceil(log2 d))
@@ -52,12 +48,12 @@ inline FastDiv fast_div(uint32_t d) {
   return f;
 }
 
-// Scale bytes in the tensor core's order ("pieces"): kMxPiece bytes for each
-// 128 rows and 16 blocks, row r's byte for block b at 512 (b / 4) +
-// 16 (r % 32) + 4 (r / 32 % 4) + b % 4; 0 past the matrix (the codes there
-// are 0 too, but a product with a NaN scale would not be).  Pieces of 128 rows
-// follow one another, a row block's groups of 16 blocks first, in whole pairs
-// of row blocks.
+// Scale bytes in the tensor core's order ("pieces"), for matrices whose rows
+// of scales are not 16-byte aligned: kMxPiece bytes for each 128 rows and 16
+// blocks, row r's byte for block b at 512 (b / 4) + 16 (r % 32) +
+// 4 (r / 32 % 4) + b % 4; 0 past the matrix (the codes there are 0 too, but a
+// product with a NaN scale would not be).  Pieces of 128 rows follow one
+// another, a row block's groups of 16 blocks first, in whole pairs of blocks.
 constexpr int kMxPiece = 2048;
 struct MxPieceArgs {
   const uint8_t* scales[2];
@@ -140,11 +136,8 @@ cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int sm_count, cudaStream_t s);
 int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b);
-// Whether an m x n product takes all its scales as pieces.
-bool mx_takes_pieces(int64_t m, int64_t n);
-// b's part of the workspace of a product with m rows, as pieces to be written
-// (none when its rows load as they lie).
-bool mx_linear_pieces(int64_t m, const MxMatrix& b, void* workspace, MxPieceArgs* g);
+// b's part of the workspace as pieces to be written (none when its rows load as they lie).
+bool mx_linear_pieces(const MxMatrix& b, void* workspace, MxPieceArgs* g);
 int64_t mx_few_rows_workspace(const MxMatrix& b);  // with x instead of a
 cudaError_t mx_matmul_error(unsigned* flag, cudaStream_t s);
 
@@ -171,14 +164,6 @@ __device__ __forceinline__ float inverse_scale(uint32_t s) { return s == 255u ? 
 // 2^(s - 127): subnormal for s = 0, NaN for s = 255.
 __device__ __forceinline__ float scale_value(uint32_t s) {
   return s == 0u ? __uint_as_float(0x00400000u) : s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23);
-}
-
-// Where the scale byte of a row's block lies.
-__device__ __forceinline__ uint8_t* scale_at(const MxMatrix& m, int64_t row, int64_t b) {
-  if (!m.tiled) return m.scales + row * m.scale_pitch + b;
-  const int64_t groups = (((m.cols + kMxBlock - 1) / kMxBlock) + 15) / 16;
-  return m.scales + ((row >> 7) * groups + (b >> 4)) * kMxPiece + 512 * ((b >> 2) & 3) + 16 * (row & 31) +
-         4 * ((row >> 5) & 3) + (b & 3);
 }
 
 // Eight scaled values to eight 4-bit elements, to nearest even (6 and above: 6).

@@ -72,9 +72,7 @@ zero_status check_mx4(const char* name, const zero_mx4* m) {
 }
 
 zsm::MxMatrix matrix(const zero_mx4& m) {
-  zsm::MxMatrix r = {static_cast<uint8_t*>(m.codes), static_cast<uint8_t*>(m.scales), m.rows, m.cols, m.code_pitch,
-                     m.scale_pitch};
-  return r;
+  return {static_cast<uint8_t*>(m.codes), static_cast<uint8_t*>(m.scales), m.rows, m.cols, m.code_pitch, m.scale_pitch};
 }
 
 // SMs of the current device, asked for once per device.
@@ -104,11 +102,11 @@ zero_status check_workspace(const void* workspace, int64_t have, int64_t need) {
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 
-zero_status matmul(const zsm::MxMatrix& a, const zsm::MxMatrix& b, void* out, int32_t dtype, int64_t ld, void* workspace, int pdl,
+zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtype, int64_t ld, void* workspace, int pdl,
                    int b_ready, int sms, cudaStream_t s) {
   zsm::MxMatmulArgs m = {};
-  m.a = a;
-  m.b = b;
+  m.a = matrix(a);
+  m.b = matrix(b);
   m.out = out;
   m.type = dtype;
   m.ld = a.rows == 1 ? std::max<int64_t>(ld, b.rows) : ld;
@@ -119,45 +117,39 @@ zero_status matmul(const zsm::MxMatrix& a, const zsm::MxMatrix& b, void* out, in
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 product launch");
 }
 
-// A quantised matrix in a workspace: its codes, then its scales -- in rows of
-// 16-byte multiples, or as pieces for a product that takes them.
-int64_t own_bytes(int64_t rows, int64_t cols, bool tiled) {
-  const int64_t nb = zsm::mx_blocks(cols);
-  return rows * 16 * nb + (tiled ? zsm::mx_row_blocks(rows) * zsm::mx_groups(cols) * zsm::kMxPiece : rows * align16(nb));
+// zero_mx4_linear's workspace: x's codes, its scales (rows of 16-byte
+// multiples) unless the rows are few, then the product's own part.
+zero_mx4 quantised_x(uint8_t* at, int64_t tokens, int64_t inputs) {
+  const int64_t nb = zsm::mx_blocks(inputs);
+  return {at, at ? at + tokens * 16 * nb : nullptr, tokens, inputs, 16 * nb, align16(nb)};
 }
-zsm::MxMatrix own_matrix(uint8_t* at, int64_t rows, int64_t cols, bool tiled) {
-  const int64_t nb = zsm::mx_blocks(cols);
-  zsm::MxMatrix m = {at, at ? at + rows * 16 * nb : nullptr, rows, cols, 16 * nb, align16(nb)};
-  m.tiled = tiled;
-  return m;
+int64_t linear_own(int64_t tokens, int64_t inputs) {
+  const int64_t nb = zsm::mx_blocks(inputs);
+  return tokens * (16 * nb + align16(nb));
 }
-
-// zero_mx4_linear's workspace: the quantised x unless the rows are few, then
-// the product's own part.
 int64_t linear_need(int64_t tokens, const zero_mx4* w) {
   if (tokens <= zsm::kMxFewRows) return zsm::mx_few_rows_workspace(matrix(*w));  // x is quantised in the product
-  const bool tiled = zsm::mx_takes_pieces(tokens, w->rows);
-  return own_bytes(tokens, w->cols, tiled) + zsm::mx_matmul_workspace(own_matrix(nullptr, tokens, w->cols, tiled), matrix(*w));
+  return linear_own(tokens, w->cols) + zsm::mx_matmul_workspace(matrix(quantised_x(nullptr, tokens, w->cols)), matrix(*w));
 }
 
-// zero_mx4_linear_backward's workspace: dy, its transpose and x's and w's.
+// zero_mx4_linear_backward's workspace: dy, its transpose and x's and w's, each
+// with rows of scales of 16-byte multiples.
 struct Backward {
-  zsm::MxMatrix dy, dy_t, x_t, w_t;
+  zero_mx4 dy, dy_t, x_t, w_t;
   int64_t bytes;
 };
 Backward backward_parts(uint8_t* at, int64_t tokens, int64_t o, int64_t k) {
-  const bool dx_tiled = zsm::mx_takes_pieces(tokens, k), dw_tiled = zsm::mx_takes_pieces(o, k);
   Backward p;
   int64_t used = 0;
-  auto part = [&](int64_t rows, int64_t cols, bool tiled) {
-    const zsm::MxMatrix m = own_matrix(at ? at + used : nullptr, rows, cols, tiled);
-    used += own_bytes(rows, cols, tiled);
+  auto part = [&](int64_t rows, int64_t cols) {
+    const zero_mx4 m = quantised_x(at ? at + used : nullptr, rows, cols);
+    used += linear_own(rows, cols);
     return m;
   };
-  p.dy = part(tokens, o, dx_tiled);
-  p.w_t = part(k, o, dx_tiled);
-  p.dy_t = part(o, tokens, dw_tiled);
-  p.x_t = part(k, tokens, dw_tiled);
+  p.dy = part(tokens, o);
+  p.dy_t = part(o, tokens);
+  p.x_t = part(k, tokens);
+  p.w_t = part(k, o);
   p.bytes = used;
   return p;
 }
@@ -261,7 +253,7 @@ zero_status zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, void* out, int
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   const int64_t need = zsm::mx_matmul_workspace(matrix(*a), matrix(*b));
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return st;
-  return matmul(matrix(*a), matrix(*b), out, dtype, ld, workspace, 0, 0, sms, s);
+  return matmul(*a, *b, out, dtype, ld, workspace, 0, 0, sms, s);
 }
 
 zero_status zero_mx4_linear_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes) {
@@ -288,15 +280,14 @@ zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  const bool tiled = zsm::mx_takes_pieces(tokens, w->rows);
-  const int64_t own = own_bytes(tokens, w->cols, tiled);
+  const int64_t own = linear_own(tokens, w->cols);
   uint8_t* at = static_cast<uint8_t*>(workspace);
-  const zsm::MxMatrix xq = own_matrix(at, tokens, w->cols, tiled);
+  zero_mx4 xq = quantised_x(at, tokens, w->cols);
   st = check_workspace(workspace, workspace_bytes, linear_need(tokens, w));
   if (st != ZERO_OK) return st;
   if (tokens <= zsm::kMxFewRows) {
     zsm::MxMatmulArgs m = {};
-    m.a = xq;
+    m.a = matrix(xq);
     m.b = matrix(*w);
     m.out = y, m.type = y_dtype;
     m.ld = tokens == 1 ? std::max<int64_t>(ld_y, w->rows) : ld_y;
@@ -310,11 +301,11 @@ zero_status zero_mx4_linear(const void* x, int32_t dtype, int64_t tokens, int64_
   zsm::MxQuantArgs q = {};
   q.src = x, q.type = dtype;
   q.rows = tokens, q.cols = w->cols, q.ld = ld;
-  q.out = xq;
-  if (!zsm::mx_linear_pieces(tokens, matrix(*w), at + own, &q.pieces)) return cuda_fail(cudaErrorInvalidValue, "MX4 scale pieces");
+  q.out = matrix(xq);
+  if (!zsm::mx_linear_pieces(matrix(*w), at + own, &q.pieces)) return cuda_fail(cudaErrorInvalidValue, "MX4 scale pieces");
   const cudaError_t er = zsm::launch_mx_quantize(q, sms, s);
   if (er != cudaSuccess) return cuda_fail(er, "MX4 quantise launch");
-  return matmul(xq, matrix(*w), y, y_dtype, ld_y, at + own, 1, 1, sms, s);
+  return matmul(xq, *w, y, y_dtype, ld_y, at + own, 1, 1, sms, s);
 }
 
 zero_status zero_mx4_linear_backward_workspace(int64_t tokens, const zero_mx4* w, int64_t* bytes) {
@@ -351,14 +342,14 @@ zero_status zero_mx4_linear_backward(const void* dy, int32_t dy_dtype, int64_t l
   zsm::MxBackwardArgs a = {};
   a.dy.src = dy, a.dy.type = dy_dtype;
   a.dy.rows = tokens, a.dy.cols = o, a.dy.ld = tokens > 1 ? ld_dy : o;
-  a.dy.out = p.dy, a.dy.out_t = p.dy_t;
+  a.dy.out = matrix(p.dy), a.dy.out_t = matrix(p.dy_t);
   a.dy.stochastic = rounding == ZERO_MX4_STOCHASTIC, a.dy.seed = seed;
   a.x.src = x, a.x.type = x_dtype;
   a.x.rows = tokens, a.x.cols = k, a.x.ld = tokens > 1 ? ld_x : k;
-  a.x.out_t = p.x_t;
+  a.x.out_t = matrix(p.x_t);
   a.w.from = matrix(*w);
   a.w.rows = o, a.w.cols = k;
-  a.w.out_t = p.w_t;
+  a.w.out_t = matrix(p.w_t);
   e = zsm::launch_mx_backward(a, sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "MX4 backward quantise launch");
   if ((st = matmul(p.dy, p.w_t, dx, dx_dtype, ld_dx, nullptr, 1, 0, sms, s)) != ZERO_OK) return st;

@@ -1128,27 +1128,26 @@ bool scales_map(CUtensorMap* map, const MxMatrix& m, int rows, uint8_t* pieces, 
 }
 
 // Whether a matrix's scale rows can be loaded as they lie (the tensor map's
-// alignment), or by words.
+// alignment).
 bool rows_load(const MxMatrix& m) {
   return ((reinterpret_cast<uintptr_t>(m.scales) | (uintptr_t)m.scale_pitch) & 15u) == 0;
 }
 bool words_load(const MxMatrix& m) {
   return ((reinterpret_cast<uintptr_t>(m.scales) | (uintptr_t)m.scale_pitch) & 3u) == 0;
 }
-int64_t piece_count(const MxMatrix& m) { return mx_row_blocks(m.rows) * mx_groups(m.cols); }
-// Bytes of workspace for its pieces; all: they are wanted although its rows load.
-int64_t pieces_bytes(const MxMatrix& m, bool all) {
-  return m.tiled || (rows_load(m) && !all) ? 0 : piece_count(m) * kGroup;
-}
+// Pieces of a matrix: blocks of 128 rows (whole pairs of them) times groups of two k tiles.
+int64_t row_blocks(const MxMatrix& m) { return 2 * ((m.rows + 255) / 256); }
+int64_t groups_of(const MxMatrix& m) { return (mx_blocks(m.cols) + 15) / 16; }
+int64_t pieces_bytes(const MxMatrix& m) { return rows_load(m) ? 0 : row_blocks(m) * groups_of(m) * kGroup; }
 
 // Adds a matrix's pieces to the kernel's work (warps -1: too many).
 void add_pieces(MxPieceArgs* g, const MxMatrix& m, uint8_t* out) {
   if (!out || g->warps < 0) return;
   const int i = g->n++;
-  g->groups = (int)mx_groups(m.cols);
+  g->groups = (int)groups_of(m);
   g->k_blocks = (int)mx_blocks(m.cols);
   g->scales[i] = m.scales, g->pitch[i] = m.scale_pitch, g->rows[i] = (int)m.rows, g->out[i] = out;
-  const int64_t warps = g->warps + 4 * mx_row_blocks(m.rows) * g->groups;
+  const int64_t warps = g->warps + 4 * row_blocks(m) * g->groups;
   g->warps = warps > 0x7FFFFFFF - 8 ? -1 : (int)warps;
   if (i == 0) g->warps0 = g->warps;
 }
@@ -1172,8 +1171,8 @@ struct Maps {
 };
 bool make_maps(Maps* t, const MxMatrix& p, const MxMatrix& q, int q_rows, uint8_t* p_pieces, uint8_t* q_pieces) {
   return codes_map(&t->p, p, kLanes) && codes_map(&t->q, q, q_rows) &&
-         scales_map(&t->ps, p, kLanes, p_pieces, piece_count(p)) &&
-         scales_map(&t->qs, q, q_rows, q_pieces, piece_count(q));
+         scales_map(&t->ps, p, kLanes, p_pieces, row_blocks(p) * groups_of(p)) &&
+         scales_map(&t->qs, q, q_rows, q_pieces, row_blocks(q) * groups_of(q));
 }
 
 template <class K, class... Args>
@@ -1217,7 +1216,7 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pi
   } else {  // maps that are not used are P's codes'
     if (!codes_map(&t.p, p, kLanes)) return cudaErrorInvalidValue;
     t.q = t.ps = t.qs = t.p;
-    if (!kDirect && !scales_map(&t.ps, p, kLanes, p_pieces, piece_count(p))) return cudaErrorInvalidValue;
+    if (!kDirect && !scales_map(&t.ps, p, kLanes, p_pieces, row_blocks(p) * groups_of(p))) return cudaErrorInvalidValue;
   }
   a.p_tiles = (a.p_rows + kLanes - 1) / kLanes;
   const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + BN - 1) / BN);
@@ -1257,24 +1256,14 @@ bool by_pairs(int64_t m, int64_t n, int sm_count) {
 
 }  // namespace
 
-// Two tiles or more for every CTA pair: then each row's 16 bytes of scales
-// would be loaded so often, as a request of its own, that the loads bound the
-// kernel (8192 x 4096 x 4096: 72 us, with pieces 64), and writing pieces
-// first (3 us beside the quantising kernel, or of its own) pays.
-bool mx_takes_pieces(int64_t m, int64_t n) {
-  return std::min(m, n) > kLanes && ((m + 255) / 256) * ((n + 255) / 256) >= 148;
-}
-int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b) {
-  const bool all = mx_takes_pieces(a.rows, b.rows);
-  return pieces_bytes(a, all) + pieces_bytes(b, all);
-}
-bool mx_linear_pieces(int64_t m, const MxMatrix& b, void* workspace, MxPieceArgs* g) {
+int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b) { return pieces_bytes(a) + pieces_bytes(b); }
+bool mx_linear_pieces(const MxMatrix& b, void* workspace, MxPieceArgs* g) {
   *g = MxPieceArgs{};
-  if (pieces_bytes(b, mx_takes_pieces(m, b.rows)) == 0) return true;
+  if (rows_load(b)) return true;
   add_pieces(g, b, static_cast<uint8_t*>(workspace));
   return g->warps >= 0;
 }
-int64_t mx_few_rows_workspace(const MxMatrix& b) { return words_load(b) ? 0 : pieces_bytes(b, false); }
+int64_t mx_few_rows_workspace(const MxMatrix& b) { return words_load(b) ? 0 : pieces_bytes(b); }
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
@@ -1305,37 +1294,30 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
     a.p_scales = p.scales, a.p_scale_pitch = p.scale_pitch;
     a.p_align = (reinterpret_cast<uintptr_t>(p.scales) | (uintptr_t)p.scale_pitch) & 7u ? 4 : 8;
     a.k_blocks = (int)mx_blocks(p.cols);
+  } else if (!rows_load(p)) {
+    p_pieces = space, space += pieces_bytes(p);
   }
-  MxPieceArgs g = {};
-  const bool all = !m.x && mx_takes_pieces(m.a.rows, m.b.rows);
-  auto pieces_for = [&](const MxMatrix& x) -> uint8_t* {
-    if (x.tiled) return x.scales;
-    const int64_t bytes = pieces_bytes(x, all);
-    if (bytes == 0) return nullptr;
-    uint8_t* at = space;
-    space += bytes;
-    add_pieces(&g, x, at);
-    return at;
-  };
-  if (!direct) p_pieces = pieces_for(p);
-  if (!m.x) q_pieces = pieces_for(q);
+  if (!m.x && !rows_load(q)) q_pieces = space;
   a.p_pieces = p_pieces != nullptr, a.q_pieces = q_pieces != nullptr;
-  if (g.warps < 0) return cudaErrorInvalidValue;
-  if (g.warps > 0 && !m.pieces_ready) {
+  if (p_pieces || q_pieces) {
+    MxPieceArgs g = {};
+    add_pieces(&g, p, p_pieces);
+    add_pieces(&g, q, q_pieces);
+    if (g.warps < 0) return cudaErrorInvalidValue;
     g.pdl = m.pdl;
-    const cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, m.pdl != 0, g);
-    if (e != cudaSuccess) return e;
-    a.pdl = 1;
+    if (!m.pieces_ready) {
+      const cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, m.pdl != 0, g);
+      if (e != cudaSuccess) return e;
+      a.pdl = 1;
+    }
   }
   a.p_early = swap && m.b_ready && !p_pieces && !q_pieces;
 
   if (many) return launch_pair(p, q, a, p_pieces, q_pieces, sm_count, s);
   const int64_t p_tiles = (p.rows + kLanes - 1) / kLanes;
-  // a part of k has at least 4 k tiles (16 columns: 12288 x 4096, 192 CTAs
-  // instead of 96: 15.2 -> 12.2 us) or 8, below which the exchange costs more
   auto split_for = [&](int bn, int slots) {
     const int64_t tiles = p_tiles * ((q.rows + bn - 1) / bn);
-    const int64_t most = std::min<int64_t>(std::min<int64_t>(8, a.k_tiles / (bn == 16 ? 4 : 8)), slots / tiles);
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(8, a.k_tiles / 4), slots / tiles);
     for (a.split = 1; 2 * a.split <= most;) a.split *= 2;
   };
   if (q.rows <= kMxFewRows) {
