@@ -65,7 +65,7 @@ struct MmArgs {
   int p_tiles, n_tiles, split;
   void* out;
   int64_t p_stride, q_stride;  // elements between rows of P / of Q in the result
-  int type, vec;               // vec: rows of the result along q, 16-byte aligned: TMA stores
+  int type, vec;               // vec: 32-byte stores along q are aligned
   const void* x;               // Q as a dense matrix (kernels with a vector type V)
   int64_t x_ld;
   int x_cols, x_vec;           // x_vec: its vectors are 16-byte aligned
@@ -97,13 +97,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// From shared memory to the part of the box inside the matrix, in the issuing
-// thread's bulk group.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
-               "r"(smem_u32(src)), "r"(x), "r"(y)
-               : "memory");
-}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -299,11 +292,39 @@ __device__ __forceinline__ void store_one(const MmArgs& a, int64_t at, float v) 
   else static_cast<float*>(a.out)[at] = v;
 }
 
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // N consecutive results along q of row p, starting at column q.
 template <int N>
 __device__ __forceinline__ void store_run(const MmArgs& a, int64_t p, int64_t q, const float (&v)[N]) {
   if (p >= a.p_rows) return;
   const int64_t at = p * a.p_stride + q * a.q_stride;
+  if (N >= 16 && a.vec && q + N <= a.q_rows) {
+    if (a.type == kMxF32) {
+#pragma unroll
+      for (int i = 0; i + 8 <= N; i += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+        store32(static_cast<float*>(a.out) + at + i, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i + 16 <= N; i += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j] = a.type == kMxBf16 ? pack_pair<dev::Bf16>(v[i + 2 * j], v[i + 2 * j + 1])
+                                   : pack_pair<dev::F16>(v[i + 2 * j], v[i + 2 * j + 1]);
+        store32(static_cast<uint16_t*>(a.out) + at + i, w);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (q + i < a.q_rows) store_one(a, at + i * a.q_stride, v[i]);
@@ -765,26 +786,21 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
 // into each SM where a CTA alone (128 x 256) would need 48.  Every CTA keeps
 // the scales of its own rows of P and of all 256 rows of Q.
 //
-// Two accumulators of 256 columns share half of them with each other (the
-// last quarter of TMEM holds four sets of scales): the epilogue empties the
-// shared columns first and lets the next tile start, then the others while it
-// runs.  Results go out through shared memory, 32 rows of 128 bytes at a time
-// for a warp, as TMA stores: 32-byte stores of each lane's own row, four to a
-// line, cost the loads of the codes a quarter of L2's requests.
+// Two accumulators of 256 columns share 96 of TMEM's 512 with each other
+// (the rest holds four sets of scales): the epilogue empties the shared
+// columns first and lets the next tile start, then the others while it runs.
 constexpr int kPairN = 256;
-constexpr int kPairStages = 5;
+constexpr int kPairStages = 6;
 constexpr int kPairCodes = 2 * kLanes * kTileKBytes;     // per CTA
 constexpr int kPairGroups = 3;
 constexpr int kPairGroup = 3 * kGroup;                   // per CTA: 128 rows of P, 256 of Q
-constexpr int kPairOut = 32 * 128;                       // a warp's buffer of results, two to a warp
-constexpr int kPairThreads = 448;
+constexpr int kPairThreads = kThreadsMm;
 constexpr int kPairSets = 4;
 constexpr int kPairScaleCols = 24;
-constexpr int kPairScales = 384;                               // first column of the scales
+constexpr int kPairScales = 512 - kPairSets * kPairScaleCols;  // first column of the scales
 constexpr int kPairSecond = kPairScales - kPairN;              // first column of the second accumulator
 constexpr int kPairShared = kPairN - kPairSecond;              // columns in both
-static_assert(kPairShared % 64 == 0 && kPairShared > 0, "the epilogue's order");
-static_assert(kPairScales + kPairSets * kPairScaleCols <= 512, "TMEM's columns");
+static_assert(kPairShared % 16 == 0 && kPairShared > 0, "the epilogue's order");
 static_assert(kPairSets <= kPairStages, "a set is written again after its stage's products");
 
 struct PairShared {
@@ -798,14 +814,13 @@ struct PairShared {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_matmul_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                           const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
-                          const __grid_constant__ CUtensorMap out_map, const __grid_constant__ MmArgs a) {
+                          const __grid_constant__ MmArgs a) {
   extern __shared__ uint8_t raw_smem[];
   __shared__ PairShared sh;
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   uint8_t* group_smem = smem + kPairStages * kPairCodes;
-  uint8_t* out_smem = smem + kPairStages * kPairCodes + kPairGroups * kPairGroup;
   const int groups = (a.k_tiles + 1) / 2;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
@@ -896,8 +911,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       if (!ok) linger();  // the copies in flight land before the CTA may end
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
+    if (lane == 0) {
       int n = 0, s = 0, set = 0;
       unsigned parity = 0;
       bool ok = true, issued = false;
@@ -932,103 +947,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_wait(&sh.drained, 0);
       }
     }
-  } else if (warp >= 6 && warp < 10) {
+  } else if (warp >= 6) {
     const int w = warp & 3;
-    int n = 0, stored = 0;
+    int n = 0;
     for (int tile = first; tile < a.n_tiles; tile += step, ++n) {
       if (!__all_sync(0xFFFFFFFFu, wait(&sh.acc_full[n & 1], (n >> 1) & 1))) break;
       fence_after();
-      const int p0 = (tile % a.p_tiles) * 2 * kLanes + rank * kLanes + 32 * w, q0 = (tile / a.p_tiles) * kPairN;
+      const int64_t p = (int64_t)(tile % a.p_tiles) * 2 * kLanes + rank * kLanes + 32 * w + lane;
+      const int64_t q0 = (int64_t)(tile / a.p_tiles) * kPairN;
       const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + (n & 1 ? kPairSecond : 0);
       const int turn = n & 1 ? 0 : kPairSecond;  // this accumulator's first column that the other one shares
-      auto shared_done = [&] {
-        fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(address_in(&sh.acc_empty, 0));
-      };
-      if (a.vec) {
-        const int wide = a.type == kMxF32 ? 32 : 64;  // columns in 128 bytes
-        for (int c = 0; c < kPairN; c += wide) {
-          const int col = (turn + c) & (kPairN - 1);
-          uint8_t* buffer = out_smem + (w * 2 + (stored & 1)) * kPairOut;
-          if (stored >= 2) {
-            if (lane == 0) bulk_wait_read<1>();
-            __syncwarp();
-          }
-          float v[32];
-          for (int j = 0; j < wide / 32; ++j) {
-            tmem_read<32>(acc + col + 32 * j, v);
-            // 16-byte chunks of the lane's row, placed as the 128-byte swizzle of the map has them
-            if (a.type == kMxF32) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4*>(buffer + 128 * lane + 16 * (i ^ (lane & 7))) =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  x[k] = a.type == kMxBf16 ? pack_pair<dev::Bf16>(v[8 * i + 2 * k], v[8 * i + 2 * k + 1])
-                                           : pack_pair<dev::F16>(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-                *reinterpret_cast<uint4*>(buffer + 128 * lane + 16 * ((4 * j + i) ^ (lane & 7))) =
-                    make_uint4(x[0], x[1], x[2], x[3]);
-              }
-            }
-          }
-          if (c + wide == kPairShared) shared_done();
-          fence_proxy_async_smem();
+      for (int c = 0; c < kPairN; c += 16) {
+        const int col = (turn + c) & (kPairN - 1);
+        float v[16];
+        tmem_read<16>(acc + col, v);
+        if (c + 16 == kPairShared) {
+          fence_before();
           __syncwarp();
-          if (lane == 0 && p0 < a.p_rows && q0 + col < a.q_rows) tma_store_2d(&out_map, q0 + col, p0, buffer);
-          if (lane == 0) bulk_commit();
-          ++stored;
+          if (lane == 0) arrive_at(address_in(&sh.acc_empty, 0));
         }
-      } else {
-        for (int c = 0; c < kPairN; c += 16) {
-          const int col = (turn + c) & (kPairN - 1);
-          float v[16];
-          tmem_read<16>(acc + col, v);
-          if (c + 16 == kPairShared) shared_done();
-          store_run<16>(a, p0 + lane, q0 + col, v);
-        }
+        store_run<16>(a, p, q0 + col, v);
       }
       fence_before();
     }
-    if (lane == 0) bulk_wait<0>();  // the stores have left shared memory and are done
-  } else {
-    // Two teams of four warps (2-5, 10-13) take the groups of scales by turns:
-    // one alone needs about 600 cycles a k tile, the products 512.
-    const int team = warp < 6 ? 0 : 1;
+  } else if (warp >= 2 && warp < 6) {
     const uint32_t ready = address_in(&sh.scales_full[0], 0);
     const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPairScales;
-    int it = 0, s = 0, gs = 0, g_at = 0, set = 0, old = 0;  // old: the stage whose products used this set before
+    int it = 0, s = 0, gs = 0, set = 0, old = 0;  // old: the stage whose products used this set before
     unsigned gparity = 0, parity_old = 0;
     bool ok = true;
-    auto next_old = [&] {
-      if (++old == kPairStages) {
-        old = 0;
-        parity_old ^= 1;
-      }
-    };
-    auto next_stage = [&] {
-      ++it;
-      if (++set == kPairSets) set = 0;
-      if (++s == kPairStages) s = 0;
-    };
     for (int tile = first; tile < a.n_tiles && ok; tile += step) {
-      for (int kt = 0; kt < a.k_tiles && ok; kt += 2, ++g_at) {
-        const bool mine = (g_at & 1) == team;
+      for (int kt = 0; kt < a.k_tiles && ok; kt += 2) {
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity)))) break;
         ScaleGroup p, q, r;
-        if (mine) {
-          if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.group_full[gs], gparity)))) break;
-          const uint8_t* group = group_smem + gs * kPairGroup;
-          p.load(group, lane, a.p_pieces, kLanes);
-          q.load(group + kGroup, lane, a.q_pieces, kLanes);
-          r.load(group + 2 * kGroup, lane, a.q_pieces, kLanes);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
-        }
+        const uint8_t* group = group_smem + gs * kPairGroup;
+        p.load(group, lane, a.p_pieces, kLanes);
+        q.load(group + kGroup, lane, a.q_pieces, kLanes);
+        r.load(group + 2 * kGroup, lane, a.q_pieces, kLanes);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.group_empty[gs]);
         if (++gs == kPairGroups) {
           gs = 0;
           gparity ^= 1;
@@ -1036,14 +993,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (kt + h >= a.k_tiles) break;
-          if (!mine) {
-            if (it >= kPairSets) next_old();
-            next_stage();
-            continue;
-          }
           if (it >= kPairSets) {
             if (!(ok = __all_sync(0xFFFFFFFFu, wait(&sh.empty[old], parity_old)))) break;
-            next_old();
+            if (++old == kPairStages) {
+              old = 0;
+              parity_old ^= 1;
+            }
           }
           fence_after();
           // columns: P's for each half of the k tile, then Q's of rows 0-127 and 128-255 for each half
@@ -1055,7 +1010,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_at(ready + 8 * s);
-          next_stage();
+          ++it;
+          if (++set == kPairSets) set = 0;
+          if (++s == kPairStages) s = 0;
         }
       }
     }
@@ -1152,20 +1109,6 @@ void add_pieces(MxPieceArgs* g, const MxMatrix& m, uint8_t* out) {
   if (i == 0) g->warps0 = g->warps;
 }
 
-// The result as a matrix of `rows` rows of 16- or 32-bit elements; a box is 128
-// bytes of 32 rows, swizzled.
-bool out_map(CUtensorMap* map, const MmArgs& a) {
-  const bool wide = a.type == kMxF32;
-  const cuuint64_t dims[2] = {(cuuint64_t)a.q_rows, (cuuint64_t)a.p_rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)a.p_stride * (wide ? 4 : 2)};
-  const cuuint32_t box[2] = {wide ? 32u : 64u, 32}, one[2] = {1, 1};
-  const CUtensorMapDataType type = wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                        : a.type == kMxBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return encode_fn()(map, type, 2, a.out, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct Maps {
   CUtensorMap p, q, ps, qs;
 };
@@ -1175,11 +1118,11 @@ bool make_maps(Maps* t, const MxMatrix& p, const MxMatrix& q, int q_rows, uint8_
          scales_map(&t->qs, q, q_rows, q_pieces, row_blocks(q) * groups_of(q));
 }
 
-template <class K, class... Args>
-cudaError_t launch_product(K kernel, int grid, int threads, int smem, int cluster, int pdl, cudaStream_t s, const Args&... args) {
+template <class K>
+cudaError_t launch_product(K kernel, int grid, int smem, int cluster, const Maps& t, const MmArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.blockDim = dim3(kThreadsMm);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -1190,14 +1133,14 @@ cudaError_t launch_product(K kernel, int grid, int threads, int smem, int cluste
     attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (pdl) {
+  if (a.pdl) {
     attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[n].val.programmaticStreamSerializationAllowed = 1;
     ++n;
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, kernel, t.p, t.q, t.ps, t.qs, a);
 }
 
 template <int BN, int STAGES, int GROUPS, class V = void, bool kDirect = false>
@@ -1224,14 +1167,12 @@ cudaError_t launch(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pi
   a.n_tiles = (int)tiles;
   // one cluster (a CTA when k is not split) per tile, or every SM's CTAs walking the tiles
   const int grid = a.split > 1 ? a.n_tiles * a.split : std::min<int>(a.n_tiles, sm_count * (BN <= 64 ? 2 : 1));
-  return launch_product(mx_matmul_kernel<BN, STAGES, GROUPS, V, kDirect>, grid, kThreadsMm, kSmem, a.split, a.pdl, s, t.p,
-                        t.q, t.ps, t.qs, a);
+  return launch_product(mx_matmul_kernel<BN, STAGES, GROUPS, V, kDirect>, grid, kSmem, a.split, t, a, s);
 }
 
 cudaError_t launch_pair(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t* p_pieces, uint8_t* q_pieces, int sm_count,
                         cudaStream_t s) {
-  constexpr int kSmem = kPairStages * kPairCodes + kPairGroups * kPairGroup + 8 * kPairOut + 1024;
-  static_assert((kPairStages * kPairCodes + kPairGroups * kPairGroup) % 1024 == 0, "a swizzled buffer's alignment");
+  constexpr int kSmem = kPairStages * kPairCodes + kPairGroups * kPairGroup + 1024;
   static_assert(kSmem <= 226 * 1024, "stages fit shared memory");
   static std::atomic<uint64_t> opted{0};
   const cudaError_t e = opt_in(mx_matmul_pair_kernel, kSmem, opted);
@@ -1242,10 +1183,7 @@ cudaError_t launch_pair(const MxMatrix& p, const MxMatrix& q, MmArgs a, uint8_t*
   const int64_t tiles = (int64_t)a.p_tiles * ((a.q_rows + kPairN - 1) / kPairN);
   if (tiles > 0x0FFFFFFF) return cudaErrorInvalidValue;
   a.n_tiles = (int)tiles;
-  CUtensorMap om = t.p;  // not used when the result's rows are not aligned
-  if (a.vec && !out_map(&om, a)) return cudaErrorInvalidValue;
-  return launch_product(mx_matmul_pair_kernel, 2 * (int)std::min<int64_t>(tiles, sm_count / 2), kPairThreads, kSmem, 1, a.pdl, s,
-                        t.p, t.q, t.ps, t.qs, om, a);
+  return launch_product(mx_matmul_pair_kernel, 2 * (int)std::min<int64_t>(tiles, sm_count / 2), kSmem, 1, t, a, s);
 }
 
 // Whether the product runs on CTA pairs: more than 128 rows on both sides, and
@@ -1267,12 +1205,12 @@ int64_t mx_few_rows_workspace(const MxMatrix& b) { return words_load(b) ? 0 : pi
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
-  // Many tiles: CTA pairs, a's rows as lanes, whose results go out as TMA
-  // stores -- or b's rows as lanes where the result's rows are not 16-byte
-  // aligned, which makes a warp's 32 lanes neighbours in memory.  Few tiles:
-  // b's rows as lanes, narrower tiles, k split over a cluster.
+  // Many tiles: CTA pairs, a's rows as lanes, whose results go out 32 bytes at
+  // a time along a row -- or b's rows as lanes where the result's rows are not
+  // 32-byte aligned, which makes a warp's 32 lanes neighbours in memory.  Few
+  // tiles: b's rows as lanes, narrower tiles, k split over a cluster.
   const int64_t row_bytes = m.ld * (m.type == kMxF32 ? 4 : 2);
-  const bool aligned = ((reinterpret_cast<uintptr_t>(m.out) | (uintptr_t)row_bytes) & 15u) == 0;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(m.out) | (uintptr_t)row_bytes) & 31u) == 0;
   const bool many = !m.x && by_pairs(m.a.rows, m.b.rows, sm_count);
   const bool swap = !many || !aligned;
   const MxMatrix& p = swap ? m.b : m.a;
