@@ -163,7 +163,7 @@ def _assert_product(got, a, b, what):
 PRODUCTS = [(1, 1, 1), (1, 128, 32), (1, 130, 33), (2, 100, 64), (8, 256, 256), (9, 257, 300), (17, 1000, 771),
             (32, 128, 512), (33, 129, 257), (64, 640, 2048), (100, 200, 4100), (128, 128, 128), (129, 300, 96),
             (256, 256, 1024), (300, 1000, 771), (1000, 333, 100), (2048, 2047, 100), (1999, 1800, 300), (513, 768, 2304), (1, 4096, 4096), (2048, 2304, 768),
-            (2500, 2700, 544)]
+            (2500, 2700, 544), (3330, 3200, 300), (3100, 3601, 1040)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
@@ -211,7 +211,7 @@ def test_matmul_pitches_and_alignments(z, m, scale_pitch, ld, off):
     assert (out[:, n:] == 5.0).all() and (whole[:off] == 5.0).all() and (whole[off + m * ld:] == 5.0).all()
 
 
-@pytest.mark.parametrize("m,n", [(5, 200), (200, 260), (2000, 2600)])
+@pytest.mark.parametrize("m,n", [(5, 200), (200, 260), (2000, 2600), (3400, 3400)])
 def test_matmul_zero_rows_nan_blocks_and_extreme_scales(z, m, n):
     k = 192
     x, y = _normal(m, k, "f32", 1), _normal(n, k, "f32", 2)
@@ -242,7 +242,8 @@ def test_matmul_without_columns_or_rows(z):
 # ------------------------------------------------------------------- linear --
 
 LINEAR = [(1, 128, 32), (1, 2304, 768), (1, 1000, 771), (3, 300, 256), (16, 640, 512), (16, 300, 779), (5, 200, 2080), (2, 130, 800), (9, 70, 4000), (17, 640, 544), (100, 768, 2304),
-          (257, 513, 1000), (1000, 2304, 768), (2300, 2200, 512)]
+          (257, 513, 1000), (1000, 2304, 768), (2300, 2200, 512),
+          (3330, 3300, 520), (3101, 3800, 771)]
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
@@ -266,7 +267,8 @@ def test_linear_wants_no_more_than_its_workspace(z):
     """The bytes around the workspace, the operands and the result stay."""
     import ctypes
 
-    for tokens, out, inner, pitch in ((1, 300, 771, 25), (40, 300, 768, 24), (700, 2600, 800, 25), (1, 256, 512, 16)):
+    for tokens, out, inner, pitch in ((1, 300, 771, 25), (40, 300, 768, 24), (700, 2600, 800, 25), (1, 256, 512, 16),
+                                      (3300, 3300, 96, 3), (3300, 3300, 600, 32)):
         x = _normal(tokens, inner, "bf16", 3)
         c, s = ref.pack(*ref.quantize(_normal(out, inner, "f32", 4, 0.02)), scale_pitch=pitch)
         w = z.MX4(c, s, out, inner)
@@ -288,7 +290,8 @@ def test_linear_wants_no_more_than_its_workspace(z):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("tokens,out,inner", [(1, 64, 32), (33, 100, 77), (300, 768, 256), (1003, 520, 384)])
+@pytest.mark.parametrize("tokens,out,inner", [(1, 64, 32), (33, 100, 77), (300, 768, 256), (1003, 520, 384),
+                                              (3330, 300, 3200), (300, 3330, 3201), (3100, 3400, 3600)])
 @pytest.mark.parametrize("seed", [None, 12345])
 def test_linear_backward(z, dtype, tokens, out, inner, seed):
     x, dy = _normal(tokens, inner, dtype, 1), _normal(tokens, out, dtype, 2, 0.25)
