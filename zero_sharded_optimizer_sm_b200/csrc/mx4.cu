@@ -21,6 +21,26 @@ namespace {
 using namespace dev;
 using namespace mx;
 
+// The two 16-bit formats: two values rounded into a word, infinity's pattern.
+template <class F>
+struct Half;
+template <>
+struct Half<Bf16> {
+  static constexpr uint32_t kInf = 0x7F80u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162_raw r = __floats2bfloat162_rn(a, b);
+    return (uint32_t)r.x | ((uint32_t)r.y << 16);
+  }
+};
+template <>
+struct Half<F16> {
+  static constexpr uint32_t kInf = 0x7C00u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2_raw r = __floats2half2_rn(a, b);
+    return (uint32_t)r.x | ((uint32_t)r.y << 16);
+  }
+};
+
 // ---------------------------------------------------- quantise along rows --
 
 // A warp takes 256 consecutive columns of one row at a time, a lane 8 of them
@@ -220,12 +240,12 @@ __global__ void __launch_bounds__(256, 3) mx_backward_kernel(const __grid_consta
 
 struct TBf16 {
   using raw = uint16_t;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack2(Bf16::rn(a), Bf16::rn(b)); }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return Half<Bf16>::pack(a, b); }
   static __device__ __forceinline__ raw rn(float x) { return Bf16::rn(x); }
 };
 struct TF16 {
   using raw = uint16_t;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack2(F16::rn(a), F16::rn(b)); }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return Half<F16>::pack(a, b); }
   static __device__ __forceinline__ raw rn(float x) { return F16::rn(x); }
 };
 struct TF32 {
@@ -311,27 +331,15 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_consta
 
 // ---------------------------------------------------------- reduce-scatter --
 
-// The square of an averaged gradient, added in binary64 as mean_bf16 does.
-// The widening to binary64 is put together from the bits of a normal number
-// (whose value has at most 11 significant bits): the conversion instruction
-// shares a unit of 16 a clock with the decoding, which needs all of it.
-__device__ __forceinline__ void add_square(float g, double& sq, unsigned& nf) {
-  const uint32_t m = __float_as_uint(g) & 0x7FFFFFFFu;
-  if (m - 0x00800000u < 0x7F000000u) {
-    const double d = __hiloint2double((int)((m >> 3) + 0x38000000u), (int)(m << 29));
-    sq = __fma_rn(d, d, sq);  // the square is exact, so one rounding as with a separate product
-  } else if (m != 0u) {
-    const double d = (double)g;
-    sq = __dadd_rn(sq, __dmul_rn(d, d));
-    nf += m >= 0x7F800000u ? 1u : 0u;
-  }
-}
-
 // A lane sums 16 elements (8 bytes of codes and the block's scale byte from
 // each rank), in rank order; eight ranks' loads are out at a time.
 // element * scale is exact in binary32 (three significant bits), so the fused
-// multiply-add rounds once, as adding the element's value does.
-template <class F>
+// multiply-add rounds once, as adding the element's value does.  What bounds
+// it is instructions: seven for an element of a rank, so the elements are
+// decoded by integer moves, two at a time (the conversion instruction runs at
+// an eighth of their rate), and the norm's terms use that unit instead.
+// kFull: the ranks are a multiple of 8.
+template <class F, bool kFull>
 __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_constant__ MxReduceArgs a) {
   double sq = 0.0;
   unsigned nf = 0;
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_consta
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         w[k] = make_uint2(0u, 0u), s[k] = 0u;
-        if (r0 + k < a.n_ranks) {
+        if (kFull || r0 + k < a.n_ranks) {
           w[k] = __ldcs(reinterpret_cast<const uint2*>(a.codes[r0 + k]) + i);
           s[k] = __ldcs(a.scales[r0 + k] + (i >> 1));
         }
@@ -357,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_consta
       if (top <= kPlainScale) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (r0 + k < a.n_ranks) {
+          if (kFull || r0 + k < a.n_ranks) {
             uint32_t h[8];
             decode8_pairs(w[k].x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
             decode8_pairs(w[k].y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
@@ -369,8 +377,10 @@ __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_consta
 #pragma unroll 1
         for (int k = 0; k < 8 && r0 + k < a.n_ranks; ++k) {
           float2 v[8];
-          values8(w[k].x, s[k], reinterpret_cast<float2(&)[4]>(v[0]));
-          values8(w[k].y, s[k], reinterpret_cast<float2(&)[4]>(v[4]));
+          const uint2 wk = __ldcs(reinterpret_cast<const uint2*>(a.codes[r0 + k]) + i);
+          const uint32_t sk = a.scales[r0 + k][i >> 1];
+          values8(wk.x, sk, reinterpret_cast<float2(&)[4]>(v[0]));
+          values8(wk.y, sk, reinterpret_cast<float2(&)[4]>(v[4]));
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] = make_float2(__fadd_rn(acc[j].x, v[j].x), __fadd_rn(acc[j].y, v[j].y));
         }
@@ -379,14 +389,26 @@ __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_consta
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       if (i * 16 + 8 * g >= a.n) break;
-      uint16_t g16[kVec];
+      uint32_t x[4], m = 0;
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float2 t = acc[4 * g + (j & 3)];
-        g16[j] = F::rn(__fmul_rn(j < 4 ? t.x : t.y, a.inv_n));
-        add_square(F::f32(g16[j]), sq, nf);
+      for (int j = 0; j < 4; ++j) {
+        const float2 lo = acc[4 * g + 2 * (j & 1)], hi = acc[4 * g + 2 * (j & 1) + 1];
+        x[j] = j < 2 ? Half<F>::pack(__fmul_rn(lo.x, a.inv_n), __fmul_rn(hi.x, a.inv_n))
+                     : Half<F>::pack(__fmul_rn(lo.y, a.inv_n), __fmul_rn(hi.y, a.inv_n));
+        m = __vmaxu2(m, x[j] & 0x7FFF7FFFu);
       }
-      st_stream(a.shard_out + i * 16 + 8 * g, pack8(g16));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // each square is exact, so one rounding as with a separate product
+        const double d = (double)F::lo(x[j]), e = (double)F::hi(x[j]);
+        sq = __fma_rn(d, d, sq);
+        sq = __fma_rn(e, e, sq);
+      }
+      if (max(m & 0xFFFFu, m >> 16) >= Half<F>::kInf) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          nf += ((x[j] & 0x7FFFu) >= Half<F>::kInf ? 1u : 0u) + ((x[j] >> 16 & 0x7FFFu) >= Half<F>::kInf ? 1u : 0u);
+      }
+      st_stream(a.shard_out + i * 16 + 8 * g, make_uint4(x[0], x[1], x[2], x[3]));
     }
   }
   norm_epilogue<kThreads>(a.ns, sq, (unsigned long long)nf, a.accumulate);
@@ -531,8 +553,14 @@ cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s
 
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s) {
   const int grid = cap_grid((a.n / 16 + kThreads) / kThreads, std::min(8 * sm_count, kMaxGrid));
-  if (a.fmt == kFmtF16) mx_reduce_kernel<F16><<<grid, kThreads, 0, s>>>(a);
-  else mx_reduce_kernel<Bf16><<<grid, kThreads, 0, s>>>(a);
+  const bool full = a.n_ranks % 8 == 0;
+  if (a.fmt == kFmtF16) {
+    if (full) mx_reduce_kernel<F16, true><<<grid, kThreads, 0, s>>>(a);
+    else mx_reduce_kernel<F16, false><<<grid, kThreads, 0, s>>>(a);
+  } else {
+    if (full) mx_reduce_kernel<Bf16, true><<<grid, kThreads, 0, s>>>(a);
+    else mx_reduce_kernel<Bf16, false><<<grid, kThreads, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 
