@@ -263,6 +263,51 @@ def test_linear_is_quantize_and_matmul(z, dtype, tokens, out, inner):
     assert torch.equal(z.mx4_linear(wide[:, :inner], tight), y)
 
 
+@pytest.mark.parametrize("tokens", [1, 7, 16, 40])
+def test_linear_of_tokens_that_are_zero_nan_or_infinite(z, tokens):
+    """A token's block that is not finite makes that token's outputs NaN and
+    no other's; an empty token's outputs are zero."""
+    x = _normal(tokens, 800, "bf16", 1)
+    x[0, 300] = float("nan") if tokens % 2 else float("-inf")
+    x[tokens - 1, :] = 0.0 if tokens > 1 else x[0]
+    w = z.mx4_quantize(_normal(200, 800, "bf16", 2))
+    y = z.mx4_linear(x, w)
+    assert y[0].isnan().all() and not y[1:].isnan().any()
+    if tokens > 1:
+        assert (y[-1] == 0).all()
+    _assert_product(y, z.mx4_quantize(x), w, "linear")
+
+
+def test_matrices_past_32_bit_offsets(z):
+    """4.6e9 elements: the ends of rows and of the matrix, quantised along the
+    rows and down the columns, read back, and as a product's result."""
+    rows, cols = 70016, 65600
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, 32768, 65535, 65536, rows - 33, rows - 1]
+    for i in at:
+        x[i] = _normal(1, cols, "bf16", i)[0]
+    m = z.mx4_quantize(x)
+    for i in at:
+        one = z.MX4(m.codes[i:i + 1], m.scales[i:i + 1], 1, cols)
+        _assert_mx4(one, *ref.quantize(x[i:i + 1]), f"row {i}")
+    back = z.mx4_dequantize(m)
+    for i in at:
+        _same_values(back[i:i + 1], ref.rounded(x[i:i + 1]), f"row {i} read back")
+    assert (back[2:100] == 0).all() and (back[rows - 32:rows - 1] == 0).all()
+    del m, back
+    t = z.mx4_quantize(x, transpose=True)
+    for j in (0, 40000, cols - 1):
+        one = z.MX4(t.codes[j:j + 1], t.scales[j:j + 1], 1, rows)
+        _assert_mx4(one, *ref.quantize(x[:, j:j + 1].t().contiguous()), f"column {j}")
+    del t, x
+    a, b = z.mx4_quantize(_normal(rows, 64, "bf16", 1)), z.mx4_quantize(_normal(cols, 64, "bf16", 2))
+    y = z.mx4_matmul(a, b)
+    pick = lambda m, i: z.MX4(m.codes[i:i + 40], m.scales[i:i + 40], 40, 64)  # noqa: E731
+    for i in (0, 65520, rows - 40):
+        for j in (0, 65500, cols - 40):
+            _assert_product(y[i:i + 40, j:j + 40], pick(a, i), pick(b, j), f"rows {i}, columns {j}")
+
+
 def test_linear_wants_no_more_than_its_workspace(z):
     """The bytes around the workspace, the operands and the result stay."""
     import ctypes

@@ -46,7 +46,8 @@ struct Half<F16> {
 // A warp takes 256 consecutive columns of one row at a time, a lane 8 of them
 // and four lanes a block; V::kUnits such pieces go through each step side by
 // side, which hides the loads, the exchange between the four lanes and the
-// conversions (16 a clock and SM) behind one another.
+// conversions behind one another (8192 x 2048 bf16: 20 us one by one, 13 side
+// by side; its 42 MB take 6.5 at the copy's rate).
 constexpr int kRowThreads = 256;
 
 template <class V, bool kStochastic>
@@ -302,7 +303,8 @@ __global__ void __launch_bounds__(kRowThreads) mx_dequant_kernel(const __grid_co
 // -------------------------------------------------------------- all-gather --
 
 // A lane quantises 8 of the owners' elements (four lanes a block) and writes
-// the block's codes and scale to every rank.
+// the block's codes and scale to every rank.  Eight ranks, 16.8M elements:
+// 19.6 us, 5.4 TB/s of its 105 MB.
 template <class F>
 __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_constant__ MxGatherArgs a) {
   const int lane = threadIdx.x & 31;
@@ -336,8 +338,10 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_consta
 // element * scale is exact in binary32 (three significant bits), so the fused
 // multiply-add rounds once, as adding the element's value does.  What bounds
 // it is instructions: seven for an element of a rank, so the elements are
-// decoded by integer moves, two at a time (the conversion instruction runs at
-// an eighth of their rate), and the norm's terms use that unit instead.
+// decoded by integer moves, two at a time, and the norm's terms use the
+// conversion unit instead.  Eight ranks, 50.3M elements: 90 us, 3.5 TB/s of
+// its 315 MB (with a predicate for each rank, separate roundings and the
+// squares put together from bits: 112).
 // kFull: the ranks are a multiple of 8.
 template <class F, bool kFull>
 __global__ void __launch_bounds__(kThreads) mx_reduce_kernel(const __grid_constant__ MxReduceArgs a) {
