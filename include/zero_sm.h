@@ -851,8 +851,9 @@ zero_status zero_mx4_matmul_workspace(const zero_mx4* a, const zero_mx4* b, int6
 
 /* out[i][j] = sum over k of a[i][k] b[j][k] (a->rows x b->rows of `dtype`, ld
  * elements between rows), for two MX4 matrices of the same number of columns,
- * on the block-scaled tensor cores: the elements' products are exact and
- * their sum is held in binary32, rounded once to `dtype`.  The same bits on
+ * on the block-scaled tensor cores (one row of a: on the ordinary units): the
+ * elements' products are exact and their sum is held in binary32, rounded
+ * once to `dtype`.  The same bits on
  * every run.  workspace: device memory, 16-byte aligned, the call's own until
  * its work on `stream` has run (two calls that may run at once need two).  No
  * passage of the pages defines it (the layer's use, [T] section "ZeRO-3",

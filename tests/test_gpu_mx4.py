@@ -230,6 +230,49 @@ def test_matmul_zero_rows_nan_blocks_and_extreme_scales(z, m, n):
     _assert_product(got, a, b, "extremes")
 
 
+@pytest.mark.parametrize("n,k", [(1, 1), (1, 32), (7, 33), (33, 771), (9500, 96), (130, 4128), (300, 2049), (40, 22528),
+                                 (40, 22529), (5000, 2080)])
+@pytest.mark.parametrize("low,high", [((100, 140), (100, 140)), ((0, 12), (90, 130)), ((0, 12), (244, 255)),
+                                      ((244, 255), (0, 12)), ((0, 40), (0, 120))])
+def test_matmul_of_one_row(z, n, k, low, high):
+    """Scales over their whole range, every code, rows of scales at odd
+    offsets, one block in 50 of b NaN; a sum that falls below the normal
+    numbers is off by at most half their smallest step for each of a block's
+    terms and the lanes' five additions (all terms here stay below 2^128)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n + k)
+    nb = ref.blocks_of(k)
+
+    def matrix(rows, scales, nan):
+        code = torch.randint(0, 16, (rows, nb, 32), generator=g, device="cuda")
+        code[:, -1, k - 32 * (nb - 1):] = 0
+        s = torch.randint(*scales, (rows, nb), generator=g, device="cuda")
+        if nan:
+            s[torch.rand(rows, nb, generator=g, device="cuda") < 1 / (50 * nb)] = 255
+        return z.MX4(*ref.pack(code, s, scale_pitch=nb + 1), rows, k)
+
+    a, b = matrix(1, low, False), matrix(n, high, True)
+    for t in (torch.float32, torch.bfloat16):
+        got = z.mx4_matmul(a, b, t)
+        u, v = ref.read(a), ref.read(b)
+        want, mag = u @ v.t(), u.abs() @ v.abs().t()
+        eps = 0.0 if t == torch.float32 else 2.0 ** -8
+        tiny = 2.0 ** -149 * (nb + 6) + (0.0 if t == torch.float32 else 2.0 ** -134)
+        tol = (nb / 32 + 7) * 2.0 ** -24 * mag * (1 + eps) + eps * want.abs() + tiny
+        fine = (got.double() - want).abs() <= tol
+        assert (fine | (got.isnan() & want.isnan())).all()
+
+
+def test_matmul_of_one_row_beyond_the_result_type(z):
+    """Positive elements of a large row: infinite where the type's range ends."""
+    one = lambda s: z.MX4(*ref.pack(torch.full((3, 2, 32), 2, device="cuda"), torch.full((3, 2), s, device="cuda")), 3, 64)  # noqa: E731
+    row = lambda s: z.MX4(*ref.pack(torch.full((1, 2, 32), 2, device="cuda"), torch.full((1, 2), s, device="cuda")), 1, 64)  # noqa: E731
+    assert (z.mx4_matmul(row(254), one(254), torch.float32) == float("inf")).all()
+    assert (z.mx4_matmul(row(137), one(127), torch.float16) == float("inf")).all()
+    assert (z.mx4_matmul(row(136), one(127), torch.float16) == 32768.0).all()
+    assert (z.mx4_matmul(row(0), one(0), torch.float32) == 0).all()
+
+
 def test_matmul_without_columns_or_rows(z):
     out = torch.full((3, 5), 9.0, device="cuda")
     z.mx4_matmul(z.mx4_empty(3, 0), z.mx4_empty(5, 0), out=out)

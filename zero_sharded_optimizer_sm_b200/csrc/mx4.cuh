@@ -135,6 +135,9 @@ cudaError_t launch_mx_dequantize(const MxDequantArgs& a, int sm_count, cudaStrea
 cudaError_t launch_mx_gather(const MxGatherArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_reduce(const MxReduceArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int sm_count, cudaStream_t s);
+// The same for one row of a (where mx_by_gemv says so), without the tensor cores or m.workspace.
+bool mx_by_gemv(int64_t rows, int64_t cols);
+cudaError_t launch_mx_gemv(const MxMatmulArgs& a, int sm_count, cudaStream_t s);
 int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b);
 // b's part of the workspace as pieces to be written (none when its rows load as they lie).
 bool mx_linear_pieces(const MxMatrix& b, void* workspace, MxPieceArgs* g);

@@ -1220,6 +1220,7 @@ bool mx_linear_pieces(const MxMatrix& b, void* workspace, MxPieceArgs* g) {
 int64_t mx_few_rows_workspace(const MxMatrix& b) { return words_load(b) ? 0 : pieces_bytes(b); }
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s) {
+  if (mx_by_gemv(m.a.rows, m.a.cols)) return launch_mx_gemv(m, sm_count, s);
   if (!encode_fn()) return cudaErrorNotSupported;
   // Many tiles: CTA pairs, a's rows as lanes, whose results go out 32 bytes at
   // a time along a row -- or b's rows as lanes where the result's rows are not
