@@ -284,7 +284,7 @@ def test_matmul_without_columns_or_rows(z):
 
 # ------------------------------------------------------------------- linear --
 
-LINEAR = [(1, 128, 32), (1, 2304, 768), (1, 1000, 771), (3, 300, 256), (16, 640, 512), (16, 300, 779), (5, 200, 2080), (2, 130, 800), (9, 70, 4000), (17, 640, 544), (100, 768, 2304),
+LINEAR = [(1, 128, 32), (1, 200, 22528), (1, 200, 22529), (1, 2304, 768), (1, 1000, 771), (3, 300, 256), (16, 640, 512), (16, 300, 779), (5, 200, 2080), (2, 130, 800), (9, 70, 4000), (17, 640, 544), (100, 768, 2304),
           (257, 513, 1000), (1000, 2304, 768), (2300, 2200, 512),
           (3330, 3300, 520), (3101, 3800, 771)]
 
@@ -541,6 +541,35 @@ def test_reduce_scatter_over_the_whole_range_of_scales(z, top):
     a, b = got.view(torch.bfloat16), want.view(torch.bfloat16)
     assert torch.equal(a.isnan(), b.isnan())
     assert torch.equal(torch.where(a.isnan(), 0, got), torch.where(b.isnan(), 0, want))
+    opt.close()
+
+
+@pytest.mark.parametrize("n_ranks", [1, 2, 3, 4, 5, 8, 9, 16, 19])
+@pytest.mark.parametrize("spread", [0, 3, 4, 5, 9, 40])
+def test_reduce_scatter_of_ranks_with_scales_apart(z, n_ranks, spread):
+    """Blocks whose scales differ between the ranks by up to `spread` steps and
+    by exactly that, largest elements of one sign and of both, against the
+    16-bit reduce-scatter of the same values, bit for bit."""
+    n, low = 2048, 100
+    opt = _context(z, 2, n_ranks, [(n, 0)], grad_buffers=False)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(100 * n_ranks + spread)
+    code = torch.randint(0, 16, (n_ranks, n // 32, 32), generator=g, device="cuda")
+    s = low + torch.randint(0, spread + 1, (n_ranks, n // 32), generator=g, device="cuda")
+    s[0, :32] = low  # the ends of the spread, at either end of the ranks
+    s[n_ranks - 1, 1:32] = low + spread
+    s[1:, :4], code[:, :2] = low + spread, 7  # 6 from every rank: the largest sum
+    code[:, 2:4] = 15
+    code[0, 4:6], s[1:, 4:6], code[1:, 4:6] = 1, low + spread, 7  # and a half beside it
+    code[:, 6], s[0, 6] = 0, 0  # rank 0's block empty
+    codes, scales = ref.pack(code, s)
+    dense = ref.values(code, s, n).to(torch.bfloat16).contiguous()
+    opt.reduce_scatter_mx4(0, n, codes, scales)
+    got, stats = opt.view(z.ZERO_VIEW_GRAD_SHARD)[:n].clone(), opt.read_stats()
+    opt.reduce_scatter(0, n, [d.data_ptr() for d in dense])
+    assert torch.equal(got, opt.view(z.ZERO_VIEW_GRAD_SHARD)[:n])
+    want = float(got.view(torch.bfloat16).double().square().sum()) ** 0.5
+    assert abs(stats["grad_norm"] - want) <= 1e-12 * want and stats["nonfinite"] == 0
     opt.close()
 
 

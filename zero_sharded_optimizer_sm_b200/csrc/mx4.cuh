@@ -219,39 +219,15 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// Eight elements by integer operations, times 2^-14, as binary16 pairs: pair p
-// holds elements p and p + 4.  An element's three magnitude bits at binary16's
-// exponent's low end are its value times 2^-14 (zero and one half among the
-// subnormal numbers), so its bits need only be moved.  scale_value_up(s) is
-// the scale times 2^14, for s up to kPlainScale.
-constexpr uint32_t kPlainScale = 240;
-__device__ __forceinline__ void decode8_pairs(uint32_t w, uint32_t (&h)[4]) {
-  h[0] = ((w << 9) & 0x0E000E00u) | ((w << 12) & 0x80008000u);
-  h[1] = ((w << 5) & 0x0E000E00u) | ((w << 8) & 0x80008000u);
-  h[2] = ((w << 1) & 0x0E000E00u) | ((w << 4) & 0x80008000u);
-  h[3] = ((w >> 3) & 0x0E000E00u) | (w & 0x80008000u);
-}
-__device__ __forceinline__ float scale_value_up(uint32_t s) { return __uint_as_float((s + 14u) << 23); }
-
-// Eight elements' values (elements p, p + 4 in v[p]).
-__device__ __forceinline__ void values8(uint32_t w, uint32_t s, float2 (&v)[4]) {
+// Eight elements' values.
+__device__ __forceinline__ void values8(uint32_t w, uint32_t s, float (&v)[8]) {
   uint32_t h[4];
-  if (s <= kPlainScale) {
-    decode8_pairs(w, h);
-    const float sc = scale_value_up(s);
+  decode8(w, h);
+  const float sc = scale_value(s);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) v[p] = mul2(half2_float2(h[p]), make_float2(sc, sc));
-  } else {
-    decode8(w, h);
-    const float sc = scale_value(s);
-    float x[8];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float2 f = half2_float2(h[p]);
-      x[2 * p] = __fmul_rn(f.x, sc), x[2 * p + 1] = __fmul_rn(f.y, sc);
-    }
-#pragma unroll
-    for (int p = 0; p < 4; ++p) v[p] = make_float2(x[p], x[p + 4]);
+  for (int p = 0; p < 4; ++p) {
+    const float2 f = mul2(half2_float2(h[p]), make_float2(sc, sc));
+    v[2 * p] = f.x, v[2 * p + 1] = f.y;
   }
 }
 
