@@ -429,11 +429,11 @@ struct Shared {
 // too, for rows that are 4-byte aligned but not 16 -- with few tokens another
 // launch for pieces would cost more than the narrower loads.
 //
-// One token through 12288 x 4096 (27 MB of weights) takes 10.9 us, 2.5 TB/s:
+// Two tokens through 12288 x 4096 (27 MB of weights) take 11.2 us, 2.4 TB/s:
 // the chain of one k tile's steps in the scale warps (load, quantise, meet,
 // write to TMEM, product) is about 0.6 us, and a CTA has 8 k tiles of it;
 // k tiles beyond the fourth wait for their sets.  Small matrices are launch
-// and first-load latency: 2304 x 768 takes 5.1 us.
+// and first-load latency: 2304 x 768 with four tokens takes 5.2 us.
 template <int BN, int STAGES, int GROUPS, class V, bool kDirect>
 __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::Vec32>::value ? 2 : 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
