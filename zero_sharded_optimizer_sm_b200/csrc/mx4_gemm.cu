@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
   extern __shared__ uint8_t raw_smem[];
   __shared__ Shared<BN, STAGES, GROUPS> sh;
   constexpr bool kDense = !std::is_void<V>::value;
-  __shared__ uint32_t x_scales[kDense ? 2 : 1][2][2 * kMxFewRows];  // a team's, of two k tiles by turns: a row's 8 bytes
+  __shared__ uint32_t x_scales[kDense ? 2 : 1][2][2 * kMxFewRows];  // a team's, of its k tiles by turns: a row's 8 bytes
   constexpr int kStage = stage_bytes(BN);
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   uint8_t* group_smem = smem + STAGES * kStage;
@@ -599,6 +599,12 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
     constexpr int kRowsOf = kDense ? kMxFewRows / kScaleWarps : 1;
     using Dense = typename std::conditional<kDense, V, mx::Vec32>::type;
     Dense next[kRowsOf];
+    // The half of x_scales for the team's next k tile.  It turns with the k
+    // tiles that the team itself takes -- both teams' count would bring the
+    // same half twice running where a CTA walks tiles with an odd number of
+    // them -- so that the team's meeting over the k tile between lies between
+    // the reads of a half and the writes for its next use.
+    int half = 0;
     const typename Dense::raw* x_at[kRowsOf];
 #pragma unroll
     for (int i = 0; i < kRowsOf; ++i)
@@ -688,7 +694,8 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
             next_old();
           }
           if constexpr (kDense) {
-            uint32_t* x_scale = x_scales[team][it & 1];
+            uint32_t* x_scale = x_scales[team][half];
+            half ^= 1;
             if (ok) {
               uint8_t* to = smem + s * kStage + kLanes * kTileKBytes + 4 * (lane & 3);
               uint8_t* sc = reinterpret_cast<uint8_t*>(x_scale);
