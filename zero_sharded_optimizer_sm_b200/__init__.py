@@ -679,6 +679,11 @@ class ZeroOptimizer:
 # A product of a small layer takes a few microseconds on the GPU, so these
 # wrappers keep their own time short: torch is looked up once, a tensor's
 # properties are read once, views are made when they are asked for.
+#
+# ``stream`` (a torch stream or a handle; None: the current one) is the stream
+# that the work goes to.  Results and workspaces are allocated for it; the
+# caller orders it after what wrote the operands, and what reads the results
+# after it.
 
 _T = None            # torch, after the first use
 _RAW_STREAM = None   # device index -> the current stream's handle
@@ -764,11 +769,15 @@ def mx4_empty(rows: int, cols: int, device=None) -> MX4:
     torch = _T or _torch()
     if rows < 0 or cols < 0:
         raise ValueError(f"{rows} x {cols}")
-    cp, sp = _mx4_pitches(cols)
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())
+    return _new_mx4(rows, cols, device, None)
+
+
+def _new_mx4(rows: int, cols: int, device, side) -> MX4:
+    cp, sp = _mx4_pitches(cols)
     m = MX4.__new__(MX4)
-    m._space = torch.empty(rows * (cp + sp), dtype=torch.uint8, device=device)
+    m._space = _empty(rows * (cp + sp), _T.uint8, device, side)
     m._codes = m._scales = None
     m.rows, m.cols, m.device = rows, cols, m._space.device
     at = m._space.data_ptr()
@@ -793,11 +802,33 @@ def _dense(t, name: str):
     return t.data_ptr(), code, ld if rows > 1 else cols, rows, cols
 
 
-def _lend(stream, t):
-    """Keeps memory that this call allocated from being reused before the work
-    given to another stream than the current one has run."""
-    s = stream if isinstance(stream, _T.cuda.Stream) else _T.cuda.ExternalStream(int(stream), device=t.device)
-    t.record_stream(s)
+def _beside(device, stream):
+    """torch's object of ``stream`` where it is another one than the device's
+    current stream, None where the call's work goes to that one."""
+    if stream is None:
+        return None
+    cuda = (_T or _torch()).cuda
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle == _RAW_STREAM(device.index):
+        return None
+    if isinstance(stream, cuda.Stream):
+        return stream
+    return cuda.default_stream(device) if handle in (0, 1) else cuda.ExternalStream(handle, device=device)
+
+
+def _empty(shape, dtype, device, side, result=True):
+    """Memory for work on ``side`` (None: the current stream), taken with that
+    stream current.  A block of the current stream's could still be in use by
+    work that is pending there -- freed, but read by a kernel in the queue --
+    and nothing orders ``side`` after it.  A result is also kept for what the
+    current stream has been given by the time it is freed."""
+    if side is None:
+        return _T.empty(shape, dtype=dtype, device=device)
+    with _T.cuda.stream(side):
+        t = _T.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(_T.cuda.current_stream(device))
+    return t
 
 
 def _mx4_check(st: int, where: str):
@@ -810,11 +841,9 @@ def _need_device(device, name: str, t):
         raise ValueError(f"{name} is on {t.device}, not {device}")
 
 
-def _result(out, rows: int, cols: int, dtype, device, stream, name: str = "out"):
+def _result(out, rows: int, cols: int, dtype, device, side, name: str = "out"):
     if out is None:
-        out = _T.empty((rows, cols), dtype=dtype, device=device)
-        if stream is not None:
-            _lend(stream, out)
+        out = _empty((rows, cols), dtype, device, side)
     else:
         if tuple(out.shape) != (rows, cols):
             raise ValueError(f"{name} is {tuple(out.shape)}, not {(rows, cols)}")
@@ -822,11 +851,9 @@ def _result(out, rows: int, cols: int, dtype, device, stream, name: str = "out")
     return out
 
 
-def _mx4_result(out, rows: int, cols: int, device, stream, name: str = "out"):
+def _mx4_result(out, rows: int, cols: int, device, side, name: str = "out"):
     if out is None:
-        out = mx4_empty(rows, cols, device)
-        if stream is not None:
-            _lend(stream, out._space)
+        out = _new_mx4(rows, cols, device, side)
     else:
         if (out.rows, out.cols) != (rows, cols):
             raise ValueError(f"{name} is {(out.rows, out.cols)}, not {(rows, cols)}")
@@ -844,12 +871,13 @@ def mx4_quantize(x, transpose: bool = False, seed: Optional[int] = None, out: Op
     None rounds to nearest even (zero_mx4_quantize)."""
     ptr, code, ld, rows, cols = _dense(x, "x")
     device = x.device
+    side = _beside(device, stream)
     rounding, seed = _rounding(seed)
     if transpose:
-        out = _mx4_result(out, cols, rows, device, stream)
+        out = _mx4_result(out, cols, rows, device, side)
         st = _on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, None, out._c)
     else:
-        out = _mx4_result(out, rows, cols, device, stream)
+        out = _mx4_result(out, rows, cols, device, side)
         st = _on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, out._c, None)
     _mx4_check(st, "zero_mx4_quantize")
     return out
@@ -859,8 +887,9 @@ def mx4_quantize_both(x, seed: Optional[int] = None, out: Optional[MX4] = None, 
     """(x, its transpose) as MX4 matrices, reading x once."""
     ptr, code, ld, rows, cols = _dense(x, "x")
     device = x.device
-    out = _mx4_result(out, rows, cols, device, stream)
-    out_t = _mx4_result(out_t, cols, rows, device, stream, "out_t")
+    side = _beside(device, stream)
+    out = _mx4_result(out, rows, cols, device, side)
+    out_t = _mx4_result(out_t, cols, rows, device, side, "out_t")
     rounding, seed = _rounding(seed)
     _mx4_check(_on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, out._c, out_t._c),
                "zero_mx4_quantize")
@@ -870,7 +899,7 @@ def mx4_quantize_both(x, seed: Optional[int] = None, out: Optional[MX4] = None, 
 def mx4_transpose(m: MX4, seed: Optional[int] = None, out: Optional[MX4] = None, stream=None) -> MX4:
     """The transpose of an MX4 matrix, quantised in blocks along the other axis."""
     device = m.device
-    out = _mx4_result(out, m.cols, m.rows, device, stream)
+    out = _mx4_result(out, m.cols, m.rows, device, _beside(device, stream))
     rounding, seed = _rounding(seed)
     _mx4_check(_on_device(device, stream, zero_mx4_transpose, m._c, rounding, seed, out._c), "zero_mx4_transpose")
     return out
@@ -879,7 +908,7 @@ def mx4_transpose(m: MX4, seed: Optional[int] = None, out: Optional[MX4] = None,
 def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
     """The values of an MX4 matrix (bfloat16 unless ``dtype`` or ``out`` says otherwise)."""
     device = m.device
-    out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, stream)
+    out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, _beside(device, stream))
     ptr, code, ld, _, _ = _dense(out, "out")
     _mx4_check(_on_device(device, stream, zero_mx4_dequantize, m._c, ptr, code, ld), "zero_mx4_dequantize")
     return out
@@ -888,17 +917,16 @@ def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
 def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
     """a b^T of two MX4 matrices with the same number of columns."""
     device = a.device
-    out = _result(out, a.rows, b.rows, dtype or _torch().bfloat16, device, stream)
+    side = _beside(device, stream)
+    out = _result(out, a.rows, b.rows, dtype or _torch().bfloat16, device, side)
     ptr, code, ld, _, _ = _dense(out, "out")
     _need_device(device, "b", b)
     need = ctypes.c_int64()
     _mx4_check(zero_mx4_matmul_workspace(a._c, b._c, need), "zero_mx4_matmul_workspace")
     at = None
     if need.value:
-        space = _T.empty(need.value, dtype=_T.uint8, device=device)
+        space = _empty(need.value, _T.uint8, device, side, False)
         at = space.data_ptr()
-        if stream is not None:
-            _lend(stream, space)
     _mx4_check(_on_device(device, stream, zero_mx4_matmul, a._c, b._c, ptr, code, ld, at, need.value), "zero_mx4_matmul")
     return out
 
@@ -911,22 +939,19 @@ def mx4_linear(x, w: MX4, out=None, stream=None):
     if inputs != w.cols:
         raise ValueError(f"x has {inputs} inputs, w {w.cols}")
     _need_device(device, "w", w)
+    side = _beside(device, stream)
     if out is None:
-        y = x.new_empty((tokens, w.rows))
-        if stream is not None:
-            _lend(stream, y)
+        y = x.new_empty((tokens, w.rows)) if side is None else _empty((tokens, w.rows), x.dtype, device, side)
         yptr, ycode, ldy = y.data_ptr(), code, w.rows
     else:
-        y = _result(out, tokens, w.rows, x.dtype, device, stream)
+        y = _result(out, tokens, w.rows, x.dtype, device, side)
         yptr, ycode, ldy, _, _ = _dense(y, "out")
     need = ctypes.c_int64()
     _mx4_check(zero_mx4_linear_workspace(tokens, w._c, need), "zero_mx4_linear_workspace")
     at, size = None, need.value
     if size:
-        space = _T.empty(size, dtype=_T.uint8, device=device)
+        space = _empty(size, _T.uint8, device, side, False)
         at = space.data_ptr()
-        if stream is not None:
-            _lend(stream, space)
     _mx4_check(_on_device(device, stream, zero_mx4_linear, ptr, code, tokens, ld, w._c, yptr, ycode, ldy, at, size),
                "zero_mx4_linear")
     return y
@@ -945,15 +970,14 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
     device = x.device
     _need_device(device, "dy", dy)
     _need_device(device, "w", w)
-    dx = _result(dx, tokens, inputs, x.dtype, device, stream, "dx")
-    dw = _result(dw, outputs, inputs, dy.dtype, device, stream, "dw")
+    side = _beside(device, stream)
+    dx = _result(dx, tokens, inputs, x.dtype, device, side, "dx")
+    dw = _result(dw, outputs, inputs, dy.dtype, device, side, "dw")
     dxptr, dxcode, lddx, _, _ = _dense(dx, "dx")
     dwptr, dwcode, lddw, _, _ = _dense(dw, "dw")
     need = ctypes.c_int64()
     _mx4_check(zero_mx4_linear_backward_workspace(tokens, w._c, need), "zero_mx4_linear_backward_workspace")
-    space = _T.empty(need.value, dtype=_T.uint8, device=device)
-    if stream is not None:
-        _lend(stream, space)
+    space = _empty(need.value, _T.uint8, device, side, False)
     rounding, seed = _rounding(seed)
     _mx4_check(_on_device(device, stream, zero_mx4_linear_backward, yptr, ycode, ldy, xptr, xcode, ldx, tokens, w._c,
                           rounding, seed, dxptr, dxcode, lddx, dwptr, dwcode, lddw, space.data_ptr(), need.value),
