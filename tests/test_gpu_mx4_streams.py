@@ -112,6 +112,58 @@ def test_a_result_outlives_the_current_streams_reads(z):
         _assert_mx4(m, *ref.quantize(other), "made after it")
 
 
+@pytest.mark.parametrize("name", list(CALLS))
+def test_operands_freed_after_the_call(z, name):
+    """The operands are freed while the call still waits on its stream, and
+    the current stream's next tensors are written at once."""
+    o = _operands(z)
+    want = _clone(CALLS[name](z, o))
+    side = torch.cuda.Stream()
+    sizes = [2 * T * K, 2 * T * O, O * K, T * K] + [t.untyped_storage().nbytes() for m in (o["w"], o["tight"], o["xq"])
+                                                    for t in (m.codes, m.scales)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # about 50 ms: what follows here runs meanwhile
+    got = CALLS[name](z, o, stream=side)
+    del o
+    late = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    torch.cuda.synchronize()
+    for a, b in zip(_tensors(got), want):
+        assert torch.equal(a, b)
+    assert all((t == 7).all() for t in late)
+
+
+@pytest.mark.parametrize("whole", [True, False])
+def test_a_collectives_buffers_freed_after_the_call(z, whole):
+    """The ranks' gradients, as one tensor or one a rank, freed while the
+    reduce-scatter still waits on its stream."""
+    n, ranks = 1 << 20, 4
+    opt = z.ZeroOptimizer([n], [0], ranks, z.ZERO_STAGE_2, grad_buffers=False)
+    opt.load_master()
+
+    def gradients():
+        m = z.mx4_quantize(_normal(ranks, n, "f32", 5, 0.01))
+        codes, scales = m.codes.clone(), m.scales[:, :n // 32].contiguous()
+        return (codes, scales) if whole else ([c.clone() for c in codes], [s.clone() for s in scales])
+
+    shard = opt.view(z.ZERO_VIEW_GRAD_SHARD)
+    opt.reduce_scatter_mx4(0, n, *gradients())
+    want = shard[:n].clone()
+    shard.zero_()
+    side = torch.cuda.Stream()
+    codes, scales = gradients()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    opt.reduce_scatter_mx4(0, n, codes, scales, stream=side)
+    del codes, scales
+    late = [torch.full((b,), 7, dtype=torch.uint8, device="cuda") for b in (ranks * n // 2, ranks * n // 32, n // 2, n // 32)
+            for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(shard[:n], want) and all((t == 7).all() for t in late)
+    opt.close()
+
+
 def test_inside_a_captured_graph(z):
     """A forked stream of a capture: its memory comes from the graph's pool."""
     o = _operands(z)

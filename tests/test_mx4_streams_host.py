@@ -140,6 +140,39 @@ def test_the_current_stream_takes_its_own_blocks(monkeypatch, name, given):
     assert all(not b.recorded for b in world.blocks)
 
 
+OUTS = {
+    "quantize": lambda w: dict(out=w.mx4(40, 96)),
+    "quantize both": lambda w: dict(out=w.mx4(40, 96), out_t=w.mx4(96, 40)),
+    "transpose": lambda w: dict(out=w.mx4(96, 40)),
+    "dequantize": lambda w: dict(out=w.matrix(40, 96)),
+    "matmul": lambda w: dict(out=w.matrix(40, 50)),
+    "linear": lambda w: dict(out=w.matrix(40, 50)),
+    "backward": lambda w: dict(dx=w.matrix(40, 96), dw=w.matrix(50, 96)),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS) + [f"{n}, results given" for n in OUTS])
+def test_operands_may_be_freed_after_the_call(monkeypatch, name):
+    """What the call was given -- an operand of the caller's that is freed at
+    once, a result's place -- is kept until the work on that stream has run.
+    Not for a stream that torch does not own: it may be destroyed before the
+    operand is freed, when torch would put an event on it."""
+    name, _, given = name.partition(", results")
+    for stream, kept in ((Stream(SIDE), True), (SIDE, False), (ExternalStream(SIDE), False)):
+        world = World(monkeypatch)
+        kw = OUTS[name](world) if given else {}
+        CALLS[name][0](world, stream=stream, **kw)
+        theirs = [b for b in world.blocks if b.taken_on == CURRENT]
+        assert theirs and all((SIDE in b.recorded) == kept for b in theirs)
+
+
+def test_an_mx4_matrix_of_the_librarys_own_memory_is_kept(monkeypatch):
+    world = World(monkeypatch)
+    m = z.mx4_quantize(world.matrix(40, 96))
+    z.mx4_dequantize(m, stream=Stream(SIDE))
+    assert SIDE in m._space.recorded
+
+
 @pytest.mark.parametrize("handle", [0, 1])
 def test_handles_of_the_default_stream(monkeypatch, handle):
     """0 and the legacy stream's handle 1 are torch's default stream."""

@@ -661,6 +661,10 @@ class ZeroOptimizer:
         nb = (hi - lo + ZERO_MX4_BLOCK - 1) // ZERO_MX4_BLOCK
         c, s = self._mx4_ptrs(lo, hi, "codes", codes, 16 * nb), self._mx4_ptrs(lo, hi, "scales", scales, nb)
         self._check(_on_device(self.device, stream, fn, self.ctx, lo, hi, c, s), where)
+        side = _beside(self.device, stream)
+        if side is not None:
+            for bufs in (codes, scales):
+                _keep(side, *((bufs,) if isinstance(bufs, self._torch.Tensor) else bufs))
 
     def all_gather_mx4(self, lo: int, hi: int, codes, scales, stream=None):
         """The owners' parameters [lo, hi) quantised into every rank's MX4
@@ -683,7 +687,9 @@ class ZeroOptimizer:
 # ``stream`` (a torch stream or a handle; None: the current one) is the stream
 # that the work goes to.  Results and workspaces are allocated for it; the
 # caller orders it after what wrote the operands, and what reads the results
-# after it.
+# after it.  Operands may be freed once the call returns, but for a stream that
+# torch does not own (a handle, an ExternalStream): those the caller keeps
+# until their work has run.
 
 _T = None            # torch, after the first use
 _RAW_STREAM = None   # device index -> the current stream's handle
@@ -831,6 +837,22 @@ def _empty(shape, dtype, device, side, result=True):
     return t
 
 
+def _keep(side, *operands):
+    """Keeps the operands' memory from being reused before the work given to
+    ``side`` has run.  (torch would wait for the stream when it is freed, so
+    not for one that may be destroyed by then.)"""
+    if isinstance(side, _T.cuda.ExternalStream):
+        return
+    for t in operands:
+        if not isinstance(t, MX4):
+            t.record_stream(side)
+        elif t._space is not None:
+            t._space.record_stream(side)
+        else:
+            t._codes.record_stream(side)
+            t._scales.record_stream(side)
+
+
 def _mx4_check(st: int, where: str):
     if st != ZERO_OK:
         raise ZeroError(st, where, zero_last_error(None).decode())
@@ -880,6 +902,8 @@ def mx4_quantize(x, transpose: bool = False, seed: Optional[int] = None, out: Op
         out = _mx4_result(out, rows, cols, device, side)
         st = _on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, out._c, None)
     _mx4_check(st, "zero_mx4_quantize")
+    if side is not None:
+        _keep(side, x, out)
     return out
 
 
@@ -893,24 +917,32 @@ def mx4_quantize_both(x, seed: Optional[int] = None, out: Optional[MX4] = None, 
     rounding, seed = _rounding(seed)
     _mx4_check(_on_device(device, stream, zero_mx4_quantize, ptr, code, rows, cols, ld, rounding, seed, out._c, out_t._c),
                "zero_mx4_quantize")
+    if side is not None:
+        _keep(side, x, out, out_t)
     return out, out_t
 
 
 def mx4_transpose(m: MX4, seed: Optional[int] = None, out: Optional[MX4] = None, stream=None) -> MX4:
     """The transpose of an MX4 matrix, quantised in blocks along the other axis."""
     device = m.device
-    out = _mx4_result(out, m.cols, m.rows, device, _beside(device, stream))
+    side = _beside(device, stream)
+    out = _mx4_result(out, m.cols, m.rows, device, side)
     rounding, seed = _rounding(seed)
     _mx4_check(_on_device(device, stream, zero_mx4_transpose, m._c, rounding, seed, out._c), "zero_mx4_transpose")
+    if side is not None:
+        _keep(side, m, out)
     return out
 
 
 def mx4_dequantize(m: MX4, dtype=None, out=None, stream=None):
     """The values of an MX4 matrix (bfloat16 unless ``dtype`` or ``out`` says otherwise)."""
     device = m.device
-    out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, _beside(device, stream))
+    side = _beside(device, stream)
+    out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, side)
     ptr, code, ld, _, _ = _dense(out, "out")
     _mx4_check(_on_device(device, stream, zero_mx4_dequantize, m._c, ptr, code, ld), "zero_mx4_dequantize")
+    if side is not None:
+        _keep(side, m, out)
     return out
 
 
@@ -928,6 +960,8 @@ def mx4_matmul(a: MX4, b: MX4, dtype=None, out=None, stream=None):
         space = _empty(need.value, _T.uint8, device, side, False)
         at = space.data_ptr()
     _mx4_check(_on_device(device, stream, zero_mx4_matmul, a._c, b._c, ptr, code, ld, at, need.value), "zero_mx4_matmul")
+    if side is not None:
+        _keep(side, a, b, out)
     return out
 
 
@@ -954,6 +988,8 @@ def mx4_linear(x, w: MX4, out=None, stream=None):
         at = space.data_ptr()
     _mx4_check(_on_device(device, stream, zero_mx4_linear, ptr, code, tokens, ld, w._c, yptr, ycode, ldy, at, size),
                "zero_mx4_linear")
+    if side is not None:
+        _keep(side, x, w, y)
     return y
 
 
@@ -982,6 +1018,8 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
     _mx4_check(_on_device(device, stream, zero_mx4_linear_backward, yptr, ycode, ldy, xptr, xcode, ldx, tokens, w._c,
                           rounding, seed, dxptr, dxcode, lddx, dwptr, dwcode, lddw, space.data_ptr(), need.value),
                "zero_mx4_linear_backward")
+    if side is not None:
+        _keep(side, dy, x, w, dx, dw)
     return dx, dw
 
 
