@@ -777,6 +777,8 @@ def mx4_empty(rows: int, cols: int, device=None) -> MX4:
         raise ValueError(f"{rows} x {cols}")
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())
+    elif torch.device(device).type != "cuda":
+        raise ValueError(f"an MX4 matrix lies on a CUDA device, not on {device}")
     return _new_mx4(rows, cols, device, None)
 
 
