@@ -319,7 +319,9 @@ class ZeroOptimizer:
         self.pipeline = int(pipeline)
         self.sizes = zero_sizes()
         self._check(zero_buffer_sizes(ctx, ctypes.byref(self.sizes)), "zero_buffer_sizes")
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        dev = torch.device("cuda" if device is None else device)
+        if dev.index is None:  # the tensors that are compared with it have one
+            dev = torch.device(dev.type, torch.cuda.current_device())
         self.device = dev
         self.arenas = []
         ptrs = (ctypes.c_void_p * ZERO_NUM_ARENAS)()
