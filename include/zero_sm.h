@@ -892,9 +892,10 @@ zero_status zero_mx4_linear_backward(const void* dy, int32_t dy_dtype, int64_t l
                                      void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Wait for `stream` and report whether a bounded wait inside a product kernel
- * on the current device ran out since the last call: ZERO_ECUDA (that
- * product's result is invalid) or ZERO_OK.  No passage of the pages defines
- * it. */
+ * on the current device -- on any of its streams -- ran out since the calling
+ * thread's last call (its first: since the library was loaded): ZERO_ECUDA
+ * (that product's result is invalid) or ZERO_OK.  Every thread that asks is
+ * told.  No passage of the pages defines it. */
 zero_status zero_mx4_check(void* stream);
 
 /*

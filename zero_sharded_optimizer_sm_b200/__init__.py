@@ -1028,7 +1028,8 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
 
 
 def mx4_check(device=None, stream=None):
-    """Wait for the stream; raise ZeroError if a bounded wait of a product kernel ran out."""
+    """Wait for the stream; raise ZeroError if a bounded wait of a product kernel
+    on the device ran out since the calling thread last asked."""
     torch = _torch()
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     _mx4_check(_on_device(device, stream, zero_mx4_check), "zero_mx4_check")

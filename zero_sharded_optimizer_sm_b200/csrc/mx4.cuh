@@ -142,7 +142,7 @@ int64_t mx_matmul_workspace(const MxMatrix& a, const MxMatrix& b);
 // b's part of the workspace as pieces to be written (none when its rows load as they lie).
 bool mx_linear_pieces(const MxMatrix& b, void* workspace, MxPieceArgs* g);
 int64_t mx_few_rows_workspace(const MxMatrix& b);  // with x instead of a
-cudaError_t mx_matmul_error(unsigned* flag, cudaStream_t s);
+cudaError_t mx_matmul_errors(unsigned* count, cudaStream_t s);
 
 // The message zero_last_error(NULL) returns to the calling thread.
 void set_thread_error(const char* msg);

@@ -10,6 +10,7 @@
 
 #include "../../include/zero_sm.h"
 #include "mx4.cuh"
+#include "mx4_errors.hpp"
 
 static_assert(ZERO_DTYPE_BF16 == zsm::kMxBf16 && ZERO_DTYPE_F16 == zsm::kMxF16 && ZERO_DTYPE_F32 == zsm::kMxF32,
               "element types");
@@ -357,10 +358,13 @@ zero_status zero_mx4_linear_backward(const void* dy, int32_t dy_dtype, int64_t l
 }
 
 zero_status zero_mx4_check(void* stream) {
-  unsigned flag = 0;
-  const cudaError_t e = zsm::mx_matmul_error(&flag, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "reading the MX4 product's error flag");
-  return flag ? fail(ZERO_ECUDA, "a bounded wait in the MX4 product kernel ran out: the product's result is invalid") : ZERO_OK;
+  unsigned count = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = zsm::mx_matmul_errors(&count, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "reading the MX4 products' error count");
+  if (!zsm::mx_errors_are_news(dev, count)) return ZERO_OK;
+  return fail(ZERO_ECUDA, "a bounded wait in an MX4 product kernel ran out: the product's result is invalid");
 }
 
 }  // extern "C"

@@ -29,8 +29,8 @@
 // the columns another one owns into that one's shared memory, and the owner
 // adds the parts in rank order -- no workspace, and the same bits every run.
 //
-// Every wait on a barrier is bounded; one that runs out sets a flag that
-// zero_mx4_check reports, after the CTA's own copies have landed.
+// Every wait on a barrier is bounded; one that runs out is counted for
+// zero_mx4_check, and the CTA ends after its own copies have landed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,7 +56,7 @@ constexpr int kTileKBytes = kTileK / 2;
 constexpr int kThreadsMm = 320;
 constexpr int kScaleWarps = 4;
 
-__device__ unsigned g_mx_error;        // a bounded wait that ran out (zero_mx4_check)
+__device__ unsigned g_mx_errors;       // bounded waits that ran out, ever (zero_mx4_check)
 
 struct MmArgs {
   int p_rows, q_rows, k_tiles;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
     const int r = wait_bounded(bar, parity, abort_flag);
     if (r == 1) {
       *abort_flag = 1;
-      atomicOr(&g_mx_error, 1u);
+      atomicAdd(&g_mx_errors, 1u);
     }
     return r == 0;
   };
@@ -875,7 +875,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int r = wait_bounded(bar, parity, abort_flag);
     if (r == 1) {
       *abort_flag = 1;
-      atomicOr(&g_mx_error, 1u);
+      atomicAdd(&g_mx_errors, 1u);
     }
     return r == 0;
   };
@@ -1311,16 +1311,10 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
   return launch<128, 6, 3>(p, q, a, p_pieces, q_pieces, sm_count, s);
 }
 
-// The flag of a bounded wait that ran out (current device), cleared as it is read (waits for `s`).
-cudaError_t mx_matmul_error(unsigned* flag, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_mx_error, sizeof *flag, 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && *flag) {
-    const unsigned zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_mx_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  }
-  return e;
+// How many bounded waits have run out on the current device (waits for `s`).
+cudaError_t mx_matmul_errors(unsigned* count, cudaStream_t s) {
+  const cudaError_t e = cudaMemcpyFromSymbolAsync(count, g_mx_errors, sizeof *count, 0, cudaMemcpyDeviceToHost, s);
+  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 
 }  // namespace zsm
