@@ -499,13 +499,15 @@ cudaError_t quantize_tiles(const MxQuantArgs& a, cudaStream_t s) {
   const int vec = kFromMx || aligned(a.src, a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
   const unsigned grid = (unsigned)(tx * ty);
   const uint32_t x = (uint32_t)tx;
-  if (a.out.codes) {
-    if (a.stochastic) mx_tile_kernel<V, kFromMx, true, true><<<grid, 256, 0, s>>>(a, x, vec);
-    else mx_tile_kernel<V, kFromMx, true, false><<<grid, 256, 0, s>>>(a, x, vec);
-  } else {
-    if (a.stochastic) mx_tile_kernel<V, kFromMx, false, true><<<grid, 256, 0, s>>>(a, x, vec);
-    else mx_tile_kernel<V, kFromMx, false, false><<<grid, 256, 0, s>>>(a, x, vec);
+  if constexpr (!kFromMx) {  // an MX4 matrix is only transposed
+    if (a.out.codes) {
+      if (a.stochastic) mx_tile_kernel<V, kFromMx, true, true><<<grid, 256, 0, s>>>(a, x, vec);
+      else mx_tile_kernel<V, kFromMx, true, false><<<grid, 256, 0, s>>>(a, x, vec);
+      return cudaGetLastError();
+    }
   }
+  if (a.stochastic) mx_tile_kernel<V, kFromMx, false, true><<<grid, 256, 0, s>>>(a, x, vec);
+  else mx_tile_kernel<V, kFromMx, false, false><<<grid, 256, 0, s>>>(a, x, vec);
   return cudaGetLastError();
 }
 

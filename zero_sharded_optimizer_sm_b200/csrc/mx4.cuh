@@ -63,7 +63,6 @@ struct MxPieceArgs {
   int n;              // matrices
   int warps0, warps;  // 32-row parts of the first, of all
   int k_blocks, groups;
-  int pdl;
 };
 
 struct MxQuantArgs {
@@ -120,9 +119,8 @@ struct MxMatmulArgs {
   int type;
   int64_t ld;
   void* workspace;  // mx_matmul_workspace bytes, 16-byte aligned
-  int pdl;           // 1: programmatic launch: the grid before this one writes the operands
-  int b_ready;       // 1: but not b
-  int pieces_ready;  // 1: it writes b's pieces into the workspace
+  int pdl;          // 1: programmatic launch: the grid before this one writes the operands
+  int b_ready;      // 1: but not b, whose pieces (if it needs any) it writes into the workspace
   const void* x;    // when set, a's rows x cols as a dense matrix of x_type, which the kernel quantises itself
   int x_type;       //   (a's codes and scales are not used)
   int64_t x_ld;

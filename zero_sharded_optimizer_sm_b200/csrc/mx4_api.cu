@@ -113,7 +113,7 @@ zero_status matmul(const zero_mx4& a, const zero_mx4& b, void* out, int32_t dtyp
   m.ld = a.rows == 1 ? std::max<int64_t>(ld, b.rows) : ld;
   m.workspace = workspace;
   m.pdl = pdl;
-  m.b_ready = m.pieces_ready = b_ready;
+  m.b_ready = b_ready;
   const cudaError_t e = zsm::launch_mx_matmul(m, sms, s);
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "MX4 product launch");
 }

@@ -63,11 +63,11 @@ struct MmArgs {
   int p_pieces, q_pieces;  // 1: that operand's scales come as pieces
   const uint8_t* p_scales; // set: P's scales are read from their rows by the scale warps (dense Q only)
   int64_t p_scale_pitch;
-  int p_align, k_blocks;   //   alignment of those rows: 8, 4 or 1
+  int p_align, k_blocks;   //   alignment of those rows: 8 or 4
   int p_tiles, n_tiles, split;
   void* out;
   int64_t p_stride, q_stride;  // elements between rows of P / of Q in the result
-  int type, vec;               // vec: 32-byte stores along q are aligned
+  int type, vec;               // vec: 32-byte stores along q are aligned (CTA pairs only)
   const void* x;               // Q as a dense matrix (kernels with a vector type V)
   int64_t x_ld;
   int x_cols, x_vec;           // x_vec: its vectors are 16-byte aligned
@@ -300,36 +300,34 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// N consecutive results along q of row p, starting at column q.
+// N results along q of row p, starting at column q, one by one.
 template <int N>
 __device__ __forceinline__ void store_run(const MmArgs& a, int64_t p, int64_t q, const float (&v)[N]) {
   if (p >= a.p_rows) return;
   const int64_t at = p * a.p_stride + q * a.q_stride;
-  if (N >= 16 && a.vec && q + N <= a.q_rows) {
-    if (a.type == kMxF32) {
-#pragma unroll
-      for (int i = 0; i + 8 <= N; i += 8) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
-        store32(static_cast<float*>(a.out) + at + i, w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i + 16 <= N; i += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          w[j] = a.type == kMxBf16 ? pack_pair<dev::Bf16>(v[i + 2 * j], v[i + 2 * j + 1])
-                                   : pack_pair<dev::F16>(v[i + 2 * j], v[i + 2 * j + 1]);
-        store32(static_cast<uint16_t*>(a.out) + at + i, w);
-      }
-    }
-    return;
-  }
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (q + i < a.q_rows) store_one(a, at + i * a.q_stride, v[i]);
+}
+// 16 of them, consecutive in memory and 32-byte aligned when a.vec.
+__device__ __forceinline__ void store_wide(const MmArgs& a, int64_t p, int64_t q, const float (&v)[16]) {
+  if (!a.vec || q + 16 > a.q_rows) return store_run(a, p, q, v);
+  if (p >= a.p_rows) return;
+  const int64_t at = p * a.p_stride + q;
+  uint32_t w[8];
+  if (a.type == kMxF32) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+      store32(static_cast<float*>(a.out) + at + i, w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = a.type == kMxBf16 ? pack_pair<dev::Bf16>(v[2 * j], v[2 * j + 1]) : pack_pair<dev::F16>(v[2 * j], v[2 * j + 1]);
+    store32(static_cast<uint16_t*>(a.out) + at, w);
+  }
 }
 
 // ------------------------------------------------------------------ scales --
@@ -406,7 +404,6 @@ __device__ __forceinline__ void load_part(ScaleGroup& g, const uint8_t* piece, i
 }
 
 __global__ void __launch_bounds__(256) mx_scale_pieces_kernel(const __grid_constant__ MxPieceArgs a) {
-  if (a.pdl) dev::pdl_wait();
   mx::write_pieces(a, blockIdx.x * 8 + (threadIdx.x >> 5));
 }
 
@@ -989,7 +986,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_at(address_in(&sh.acc_empty, 0));
         }
-        store_run<16>(a, p, q0 + col, v);
+        store_wide(a, p, q0 + col, v);
       }
       fence_before();
     }
@@ -1266,9 +1263,9 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& m, int sm_count, cudaStream_t s
     add_pieces(&g, p, p_pieces);
     add_pieces(&g, q, q_pieces);
     if (g.warps < 0) return cudaErrorInvalidValue;
-    g.pdl = m.pdl;
-    if (!m.pieces_ready) {
-      const cudaError_t e = launch_kernel(mx_scale_pieces_kernel, (g.warps + 7) / 8, 256, 0, s, m.pdl != 0, g);
+    if (!m.b_ready) {
+      mx_scale_pieces_kernel<<<(g.warps + 7) / 8, 256, 0, s>>>(g);
+      const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
       a.pdl = 1;
     }
