@@ -465,7 +465,9 @@ bool pieces_of(int64_t rows, int64_t cols, bool end_to_end, Pieces* p) {
     rows = 1;
   }
   const int64_t per = (cols + 255) / 256;
-  if (per * rows > 0x7FFFFFFFll - (1 << 24)) return false;  // (rows * cols < 2^38)
+  // as FastDiv and the kernels' counters allow; more than 2^31 pieces of
+  // whole rows are more memory than there is
+  if (per * rows > 0x7FFFFFFFll) return false;
   *p = Pieces{rows, cols, fast_div((uint32_t)per), (uint32_t)(per * rows)};
   return true;
 }
