@@ -839,8 +839,10 @@ zero_status zero_mx4_quantize(const void* src, int32_t dtype, int64_t rows, int6
  * product of a gathered layer needs it.  No passage of the pages defines it. */
 zero_status zero_mx4_transpose(const zero_mx4* in, int32_t rounding, uint64_t seed, const zero_mx4* out, void* stream);
 
-/* Read an MX4 matrix back: element * 2^(s - 127), exact in bf16 and binary32,
- * rounded to nearest even in binary16.  dst: in->rows x in->cols of `dtype`,
+/* Read an MX4 matrix back: element * 2^(s - 127), exact in bf16 and binary32
+ * (but values of 2^128 and more, which only scales of 253 and 254 can stand
+ * for and quantising never gives, are infinite), rounded to nearest even in
+ * binary16.  dst: in->rows x in->cols of `dtype`,
  * ld elements between rows.  No passage of the pages defines it. */
 zero_status zero_mx4_dequantize(const zero_mx4* in, void* dst, int32_t dtype, int64_t ld, void* stream);
 

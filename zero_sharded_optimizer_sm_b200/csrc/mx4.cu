@@ -47,7 +47,11 @@ struct Half<F16> {
 // and four lanes a block; V::kUnits such pieces go through each step side by
 // side, which hides the loads, the exchange between the four lanes and the
 // conversions behind one another (8192 x 2048 bf16: 20 us one by one, 11.3 side
-// by side; its 42 MB take 6.5 at the copy's rate).
+// by side; its 42 MB take 6.5 at the copy's rate).  No unit is at its limit
+// then: by the counters the issue slots are 60 % used, the integer units 58 %,
+// and 42 % of the warps that could be there are.  2048 x 6144 binary32 takes
+// 10.7 us to nearest and 22.5 stochastically: the generator and its rounding
+// double the instructions (integer units 67 %).
 constexpr int kRowThreads = 256;
 
 template <class V, bool kStochastic>
@@ -103,6 +107,12 @@ __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_const
 // 32-bit word.  Four neighbouring lanes take the four blocks of a column (64
 // contiguous bytes of the result).  Row r's words are rotated by 8 (r / 32),
 // which puts the four blocks' reads on different banks.
+//
+// 8192 x 2048 bf16 takes 10.2 us down the columns and 14.7 both ways (6.5 and
+// 7.9 at the copy's rate): loads that all CTAs of a wave wait for at once
+// (issue slots 48 % used, 41 % of the warps).  An MX4 matrix's transpose takes
+// 13.5 of 2.7: its elements go through the tile as 16-bit values, at twice the
+// instructions of a dense one's.
 constexpr int kTileRows = 128;
 constexpr int kTileWords = 64;  // 32-bit words of a tile's row
 
@@ -302,7 +312,7 @@ __global__ void __launch_bounds__(kRowThreads) mx_dequant_kernel(const __grid_co
 
 // A lane quantises a block of the owners' elements and writes its codes (16
 // bytes) and scale to every rank: a warp's scales fill a sector, and there is
-// nothing to exchange.  Eight ranks, 16.8M elements: 17.4 us, 6.0 TB/s of its
+// nothing to exchange.  Eight ranks, 16.8M elements: 17.8 us, 5.9 TB/s of its
 // 105 MB (four lanes to a block, with four bytes of codes each: 21.6).
 template <class F>
 __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_constant__ MxGatherArgs a) {
@@ -337,7 +347,8 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_consta
 // element * scale is exact in binary32 (three significant bits), so the fused
 // multiply-add rounds once, as adding the element's value does.
 //
-// What bounds it is instructions, so where the first ranks' scales for a block
+// What bounds it is mostly instructions (issue slots 65 % used by the counters,
+// the integer units 56 %), so where the first ranks' scales for a block
 // differ by no more than 2^4 -- nearly always, of gradients -- they are summed
 // in binary16, two elements at a time: with 2^low the smallest scale every
 // term is a whole number of 2^low / 2, up to 6 * 16 * 2, and eight of them
@@ -345,9 +356,9 @@ __global__ void __launch_bounds__(kThreads) mx_gather_kernel(const __grid_consta
 // that it stands for rounds anything, and they are equal; only one conversion
 // to binary32 is left for all ranks.  More ranks than that are added in
 // binary32.
-// Eight ranks, 16.8M elements: 24.9 us, 4.2 TB/s of its 105 MB (all in binary32
+// Eight ranks, 16.8M elements: 25.1 us, 4.2 TB/s of its 105 MB (all in binary32
 // 30.3, and 34.2 with the elements put together by integer operations instead
-// of the conversion unit); four ranks 19.5.
+// of the conversion unit); four ranks 20.0.
 // kWide ranks at a time; kFull: the ranks are a multiple of it.
 constexpr uint32_t kNearScales = 4;
 constexpr uint32_t kPlainScale = 240;  // up to it a rank's value, and what is added to it, stay finite

@@ -21,7 +21,7 @@
 // the same words to its own lanes, from registers: the copy instruction that
 // would take them from shared memory runs in turn with the products, 58
 // cycles for 512 bytes, 350 cycles a k tile of 256 x 256 beside the products'
-// 512 (8192 x 4096 x 4096: 81 us, from registers 67).  Reading the rows with
+// 512 (8192 x 4096 x 4096 took a fifth longer so).  Reading the rows with
 // ordinary loads instead of TMA cost 1900 cycles a k tile, most of it the
 // ordering of such stores before the tensor core's reads of shared memory.
 //
@@ -802,13 +802,20 @@ __global__ void __launch_bounds__(kThreadsMm, BN <= 64 && !std::is_same<V, mx::V
 // (the rest holds four sets of scales): the epilogue empties the shared
 // columns first and lets the next tile start, then the others while it runs.
 //
-// What bounds it is the way between L2 and the SMs: the 35 KB a CTA loads for
-// a k tile and the results it stores add up to 8-9 TB/s over the GPU.
-// 8192 x 4096 x 4096 (rows, rows, columns) takes 69 us, 4.0 PFLOP/s; without
-// its stores 60, without its products 53.  Tried and left out: stores through
-// shared memory by TMA (74: one stage fewer), a second team of scale warps (no
-// change), the scales of both operands as pieces (no change in the kernel,
-// 4 us more before it).
+// What bounds it is the way between L2 and the SMs, by the counters:
+// 8192 x 4096 x 4096 (rows, rows, columns) loads 638 MB and stores 67 in 74 us
+// at 1.72 GHz, 9.5 TB/s, with the tensor pipe 50 % active; 8192 x 8192 x 2048
+// moves 9.0 TB/s in 86 us at 1.75 GHz, 41 % active.  The time goes with the
+// clock that the power cap leaves: 72.8 us (3.8 PFLOP/s) in bursts of 12 and
+// 77.1 back to back at 1.68 GHz on one GPU, 69 on another.
+// Builds without the stores took 60 us where the whole took 69, without the
+// products 53; at 8192 x 8192 x 2048 64.7 us without the stores of 87.5.
+// Tried and left out: one change of the stores to TMA through shared memory,
+// five stages, more shared columns and a second team of scale warps, 74 us
+// where this took 69 (five stages alone: 71.1 and 70.2; the others were not
+// measured apart, so what TMA stores by themselves would give is not known);
+// the scales of both operands as pieces (no change in the kernel, 4 us more
+// before it).
 constexpr int kPairN = 256;
 constexpr int kPairStages = 6;
 constexpr int kPairCodes = 2 * kLanes * kTileKBytes;     // per CTA

@@ -14,9 +14,11 @@
 //
 // One token, weights not in L2 (us, here and on the tensor cores): 768 x 768
 // 2.2 and 5.1, 2304 x 768 2.2 and 5.0, 8192 x 2048 4.4 and 6.9, 12288 x 4096
-// 8.2 and 10.9, 50304 x 2048 13.6 and 15.0.  The large ones spend it on
-// instructions (a lane's block has 16 conversions, 16 multiply-adds, the loads,
-// the sums and scales): with two rows of a beside each other
+// 8.2 and 10.9, 50304 x 2048 13.6 and 15.0.  The large ones wait for nothing
+// alone: at 12288 x 4096 the counters have the issue slots 66 % used (a lane's
+// block has 16 conversions, 16 multiply-adds, the loads, the sums and scales),
+// the busiest unit 42 %, DRAM 29 %, the rest latency of the loads and of shared
+// memory.  With two rows of a beside each other
 // 12288 x 4096 took 12.8 us and with four 27, the tensor cores 11 for both, so
 // two tokens are theirs.  Two CTAs of 512 threads to an SM, not four of 256
 // or one of 1024: each quantises the whole of a, which 16384 columns make
