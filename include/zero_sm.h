@@ -256,7 +256,7 @@ enum {
 enum {
   ZERO_DTYPE_BF16 = 0,
   ZERO_DTYPE_F16 = 1,
-  ZERO_DTYPE_F32 = 2  /* the zero_mx4_* calls' dense matrices only; ZERO_OPT_DTYPE refuses it */
+  ZERO_DTYPE_F32 = 2  /* the dense matrices of the calls without a context only; ZERO_OPT_DTYPE refuses it */
 };
 
 /* Fused-step kernels (ZERO_OPT_KERNEL).  Both compute the same bits, and the
@@ -762,7 +762,8 @@ zero_status zero_check_guards(zero_ctx* ctx, void* stream, int64_t out[3]);
 
 /* Message of the last failure on ctx (never NULL; "" when none).  With
  * ctx == NULL: the reason the calling thread's last zero_init, or a later
- * zero_mx4_* call without a context, failed.
+ * call without a context (zero_mx4_*, zero_mx8_*, zero_rms_norm*,
+ * zero_embedding*), failed.
  * Library plumbing: no passage of the pages defines it.
  */
 const char* zero_last_error(const zero_ctx* ctx);
@@ -923,6 +924,120 @@ zero_status zero_mx4_all_gather(zero_ctx* ctx, int64_t lo, int64_t hi, void* con
  */
 zero_status zero_mx4_reduce_scatter(zero_ctx* ctx, int64_t lo, int64_t hi, const void* const* rank_codes,
                                     const void* const* rank_scales, void* stream);
+
+/* --------------------------------- around a layer's products: checkpoints -- */
+/*
+ * What a training step keeps between a layer's forward and backward passes, in
+ * 8 bits instead of 16 ([M] section 3.1 counts a layer's activations, and names
+ * checkpointing, beside the model states); the norm and the embedding that
+ * write those activations, and their gradients, which may go straight into a
+ * rank's gradient buffer.
+ *
+ * A microscaled 8-bit (MX8) matrix is kept as an MX4 one, with a byte to an
+ * element: rows in blocks of 32 consecutive elements (the last block of a row
+ * filled up with zeros), a scale byte s to a block, standing for 2^(s - 127)
+ * (255: every element is NaN), and 32 elements of one sign, four exponent and
+ * three mantissa bits (E4M3, at most 448).  A block whose largest magnitude is
+ * m gets the smallest s from 3 to 246 with m <= 448 * 2^(s - 127) (246 where
+ * there is none); an element x becomes x * 2^(127 - s) rounded to nearest even,
+ * at most 448.  A block that holds an infinity or a NaN gets s = 255 and codes
+ * 0.  Every value that quantising gives is exact in bf16 and binary32.
+ *
+ * These calls take no context; what the MX4 calls' introduction says of those
+ * holds for them: errors through zero_last_error(NULL), matrices on the current
+ * CUDA device, no state between calls, captures allowed, empty matrices
+ * accepted.  Outputs must not overlap inputs or one another, except where a
+ * call says so.  Sums over a row or a batch are held in binary32, in an order
+ * that depends on the sizes alone: the same bits on every run.
+ */
+#define ZERO_MX8_BLOCK 32
+
+typedef struct zero_mx8 {
+  void* codes;          /* device, 16-byte aligned */
+  void* scales;         /* device, one byte per block */
+  int64_t rows, cols;   /* elements; each below 2^31 - 256 */
+  int64_t code_pitch;   /* bytes between rows of codes: a multiple of 16, >= 32 * ceil(cols / 32) */
+  int64_t scale_pitch;  /* bytes between rows of scales, >= ceil(cols / 32) */
+} zero_mx8;
+
+/* Quantise the dense matrix src (rows x cols of `dtype`, ld elements between
+ * rows; 16-byte aligned rows load faster) along its rows.  [M] section 3.1. */
+zero_status zero_mx8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, const zero_mx8* out,
+                              void* stream);
+
+/* Read an MX8 matrix back: element * 2^(s - 127), exact in bf16 and binary32,
+ * rounded to nearest even in binary16 (a finite value past 65504 becomes
+ * 65504: an element near binary16's largest may have been rounded up).
+ * (Scales outside 3 .. 246, which quantising never gives: values of 2^128 and
+ * more are infinite, and values below 2^-133 are rounded in bf16.)  dst: in->rows x in->cols
+ * of `dtype`, ld elements between rows.  [M] section 3.1. */
+zero_status zero_mx8_dequantize(const zero_mx8* in, void* dst, int32_t dtype, int64_t ld, void* stream);
+
+/* zero_mx4_linear_backward with the layer's input x as it was kept in MX8:
+ * the same values as zero_mx8_dequantize to bf16 and that call give, without
+ * the 16-bit matrix between them.  x->rows tokens; workspace of
+ * zero_mx4_linear_backward_workspace(x->rows, w).  [T] section "ZeRO-3", part
+ * "2. 反向". */
+zero_status zero_mx4_linear_backward_mx8(const void* dy, int32_t dy_dtype, int64_t ld_dy, const zero_mx8* x,
+                                         const zero_mx4* w, int32_t rounding, uint64_t seed, void* dx, int32_t dx_dtype,
+                                         int64_t ld_dx, void* dw, int32_t dw_dtype, int64_t ld_dw, void* workspace,
+                                         int64_t workspace_bytes, void* stream);
+
+/* Root-mean-square norm of the rows of h = x + residual (rounded to `dtype`;
+ * residual NULL: h = x):
+ *   rstd = (mean(h^2) + eps)^(-1/2),   y = h * rstd * weight
+ * x, residual, y and h are rows x cols of `dtype` with ld_* elements between
+ * rows, weight has cols elements of `weight_dtype`, rstd rows binary32
+ * numbers.  Any of the results y, h, y8, h8, rstd may be NULL, not all: y8 and
+ * h8 are what zero_mx8_quantize gives of y and of h as they are rounded to
+ * `dtype`, the next layer's and this norm's checkpoint.  y or h may be x's or
+ * the residual's own memory, with the same ld.  eps > 0.  A row is computed in
+ * binary32 from the rounded h.  No passage of the pages defines it. */
+zero_status zero_rms_norm(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                          int64_t ld_residual, const void* weight, int32_t weight_dtype, double eps, void* y, int64_t ld_y,
+                          void* h, int64_t ld_h, const zero_mx8* y8, const zero_mx8* h8, float* rstd, void* stream);
+
+/* Bytes of workspace that zero_rms_norm_backward needs.  Host only. */
+zero_status zero_rms_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
+/* The gradients of that norm, from dy (of y), h or its checkpoint h8 (one of
+ * the two, the other NULL) and rstd as the forward pass gave it:
+ *   xh = h * rstd,  g = dy * weight
+ *   dx = rstd * (g - xh * mean(g * xh)) + dh,   dw = sum over the rows of dy * xh
+ * dh (may be NULL) is the gradient that reaches h by other ways (the residual
+ * stream); dx is x's gradient and the residual's.  dy, h, dh and dx are rows x
+ * cols of `dtype`, dw has cols elements of `dw_dtype`.  dx may be dy's or dh's
+ * own memory, with the same ld.  Without rows dw is 0.  workspace: device
+ * memory, 16-byte aligned, the call's own until its work on `stream` has run.
+ * No passage of the pages defines it. */
+zero_status zero_rms_norm_backward(const void* dy, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_dy, const void* h,
+                                   int64_t ld_h, const zero_mx8* h8, const void* weight, int32_t weight_dtype,
+                                   const float* rstd, const void* dh, int64_t ld_dh, void* dx, int64_t ld_dx, void* dw,
+                                   int32_t dw_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Rows of an embedding table: out[t] = scale * table[token[t]], rounded to
+ * `out_dtype`; a token outside [0, vocab) is padding and gives a row of zeros.
+ * tokens: n integers of token_bytes (4 or 8, signed).  The table is vocab x
+ * cols of `dtype` with ld elements between rows, or, with table NULL, the MX4
+ * matrix table4 (vocab x cols; dtype and ld unused), such as a rank's gathered
+ * copy.  No passage of the pages defines it. */
+zero_status zero_embedding(const void* tokens, int32_t token_bytes, int64_t n, const void* table, int32_t dtype, int64_t vocab,
+                           int64_t cols, int64_t ld, const zero_mx4* table4, double scale, void* out, int32_t out_dtype,
+                           int64_t ld_out, void* stream);
+
+/* Bytes of workspace that zero_embedding_backward needs.  Host only. */
+zero_status zero_embedding_backward_workspace(int64_t n, int64_t vocab, int64_t cols, int64_t* bytes);
+
+/* The gradient of the table: dtable[v] = scale * (the sum of dy[t] over the t
+ * with token[t] = v), rounded once to `dtable_dtype`.  Every row of dtable is
+ * written; rows without tokens are 0.  With accumulate = 1 that product is
+ * added to what the row holds, and rows without tokens stay as they are (a
+ * table that is also the output layer's weight).  dy: n x cols of `dtype`.
+ * workspace as for zero_rms_norm_backward.  No passage of the pages defines
+ * it. */
+zero_status zero_embedding_backward(const void* dy, int32_t dtype, int64_t n, int64_t cols, int64_t ld_dy, const void* tokens,
+                                    int32_t token_bytes, int64_t vocab, double scale, void* dtable, int32_t dtable_dtype,
+                                    int64_t ld, int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------ one logical rank per GPU -- */
 /*

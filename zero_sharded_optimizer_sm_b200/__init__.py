@@ -17,7 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Callable, List, Optional, Sequence
+from typing import Callable, List, NamedTuple, Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzero_sm.so")
@@ -54,7 +54,7 @@ ZERO_OPT_GUARD = 17
 ZERO_OPT_NVTX = 18
 ZERO_OPT_LAYERED = 19
 ZERO_DTYPE_BF16, ZERO_DTYPE_F16, ZERO_DTYPE_F32 = 0, 1, 2
-ZERO_MX4_BLOCK = 32
+ZERO_MX4_BLOCK = ZERO_MX8_BLOCK = 32
 ZERO_MX4_NEAREST, ZERO_MX4_STOCHASTIC = 0, 1
 (ZERO_VIEW_MASTER, ZERO_VIEW_EXP_AVG, ZERO_VIEW_EXP_AVG_SQ, ZERO_VIEW_PARAM, ZERO_VIEW_GRAD_SHARD,
  ZERO_VIEW_GRAD_BUF, ZERO_VIEW_GATHER) = range(7)
@@ -87,6 +87,10 @@ class zero_mx4(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("code_pitch", ctypes.c_int64), ("scale_pitch", ctypes.c_int64)]
 
 
+class zero_mx8(ctypes.Structure):
+    _fields_ = zero_mx4._fields_
+
+
 zero_grad_fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                 ctypes.c_int64, ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p)
 zero_gather_fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
@@ -95,6 +99,7 @@ zero_gather_fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int32,
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _PTRS = ctypes.POINTER(ctypes.c_void_p)
 _MX4 = ctypes.POINTER(zero_mx4)
+_MX8 = ctypes.POINTER(zero_mx8)
 _SIGS = {
     "zero_version": (_i32, []),
     "zero_init": (_i32, [ctypes.POINTER(zero_layout), _i32, _i32, _i64, ctypes.POINTER(_vp)]),
@@ -146,6 +151,19 @@ _SIGS = {
     "zero_mx4_check": (_i32, [_vp]),
     "zero_mx4_all_gather": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
     "zero_mx4_reduce_scatter": (_i32, [_vp, _i64, _i64, _PTRS, _PTRS, _vp]),
+    "zero_mx8_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _MX8, _vp]),
+    "zero_mx8_dequantize": (_i32, [_MX8, _vp, _i32, _i64, _vp]),
+    "zero_mx4_linear_backward_mx8": (_i32, [_vp, _i32, _i64, _MX8, _MX4, _i32, ctypes.c_uint64, _vp, _i32, _i64, _vp, _i32,
+                                            _i64, _vp, _i64, _vp]),
+    "zero_rms_norm": (_i32, [_vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, ctypes.c_double, _vp, _i64, _vp, _i64,
+                             _MX8, _MX8, _vp, _vp]),
+    "zero_rms_norm_backward_workspace": (_i32, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "zero_rms_norm_backward": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _MX8, _vp, _i32, _vp, _vp, _i64, _vp, _i64,
+                                      _vp, _i32, _vp, _i64, _vp]),
+    "zero_embedding": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, _MX4, ctypes.c_double, _vp, _i32, _i64, _vp]),
+    "zero_embedding_backward_workspace": (_i32, [_i64, _i64, _i64, ctypes.POINTER(_i64)]),
+    "zero_embedding_backward": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, ctypes.c_double, _vp, _i32, _i64,
+                                       _i32, _vp, _i64, _vp]),
     "zero_dist_init": (_i32, [ctypes.POINTER(zero_layout), _i32, _i32, _i32, ctypes.POINTER(_vp)]),
     "zero_dist_sizes": (_i32, [_vp, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
     "zero_dist_tensor_offsets": (_i32, [_vp, ctypes.POINTER(_i64), _i32]),
@@ -176,7 +194,9 @@ for _name, (_res, _args) in _SIGS.items():
 __all__ = list(_SIGS) + ["ZeroOptimizer", "ZeroDist", "AdamHParams", "ZeroError", "lib", "LIB_PATH",
                          "options_from_config", "exchange_records", "rank_ordered_norm", "ordered_step",
                          "MX4", "mx4_empty", "mx4_quantize", "mx4_quantize_both", "mx4_transpose", "mx4_dequantize", "mx4_matmul",
-                         "mx4_linear", "mx4_linear_backward", "mx4_check"]
+                         "mx4_linear", "mx4_linear_backward", "mx4_check",
+                         "MX8", "mx8_empty", "mx8_quantize", "mx8_dequantize", "RMSNorm", "rms_norm", "rms_norm_backward",
+                         "embedding", "embedding_backward"]
 ZERO_DIST_ARENA_GRAD, ZERO_DIST_ARENA_PARAM, ZERO_DIST_ARENA_STATES, ZERO_DIST_ARENA_SCRATCH = 0, 1, 2, 3
 ZERO_DIST_ARENA_GATHER = 4
 ZERO_DIST_NUM_ARENAS = 5
@@ -721,18 +741,19 @@ def _on_device(device, stream, fn, *args) -> int:
         return fn(*args, _RAW_STREAM(index) if stream is None else int(getattr(stream, "cuda_stream", stream)))
 
 
-class MX4:
-    """A microscaled 4-bit matrix of rows x cols elements (zero_mx4 in
-    include/zero_sm.h): uint8 CUDA tensors ``codes`` [rows, pitch] and
-    ``scales`` [rows, pitch], each with contiguous rows."""
+class _MX:
+    """A microscaled matrix of rows x cols elements: uint8 CUDA tensors
+    ``codes`` [rows, pitch] and ``scales`` [rows, pitch], each with contiguous
+    rows."""
 
     __slots__ = ("_codes", "_scales", "_space", "rows", "cols", "device", "_c")
+    _struct, _block_bytes = None, 0
 
     def __init__(self, codes, scales, rows: int, cols: int):
         torch = _T or _torch()
         nb = -(-cols // ZERO_MX4_BLOCK)
         pitches = []
-        for name, t, need in (("codes", codes, 16 * nb), ("scales", scales, nb)):
+        for name, t, need in (("codes", codes, self._block_bytes * nb), ("scales", scales, nb)):
             shape = t.shape
             if t.dtype != torch.uint8 or len(shape) != 2 or shape[0] != rows or shape[1] < need:
                 raise ValueError(f"{name}: a uint8 tensor of {rows} rows of at least {need} bytes is needed")
@@ -744,7 +765,7 @@ class MX4:
         self.device = codes.device
         if not codes.is_cuda or scales.device != self.device:
             raise ValueError("codes and scales must be on the same CUDA device")
-        self._c = zero_mx4(codes.data_ptr(), scales.data_ptr(), rows, cols, pitches[0], pitches[1])
+        self._c = self._struct(codes.data_ptr(), scales.data_ptr(), rows, cols, pitches[0], pitches[1])
 
     @property
     def codes(self):
@@ -764,35 +785,58 @@ class MX4:
         self._codes = self._space[:n].view(self.rows, c.code_pitch)
         self._scales = self._space[n:].view(self.rows, c.scale_pitch)
 
+    @classmethod
+    def _empty(cls, rows: int, cols: int, device):
+        torch = _T or _torch()
+        if rows < 0 or cols < 0:
+            raise ValueError(f"{rows} x {cols}")
+        if device is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        elif torch.device(device).type != "cuda":
+            raise ValueError(f"an {cls.__name__} matrix lies on a CUDA device, not on {device}")
+        return cls._new(rows, cols, device, None)
 
-def _mx4_pitches(cols: int) -> tuple:
-    """(codes, scales): mx4_empty's bytes of a row, scales padded to 16."""
-    nb = -(-cols // ZERO_MX4_BLOCK)
-    return 16 * nb, -(-nb // 16) * 16
+    @classmethod
+    def _new(cls, rows: int, cols: int, device, side):
+        """Memory for one; its scale rows are padded to 16 bytes."""
+        nb = -(-cols // ZERO_MX4_BLOCK)
+        cp, sp = cls._block_bytes * nb, -(-nb // 16) * 16
+        m = cls.__new__(cls)
+        m._space = _empty(rows * (cp + sp), _T.uint8, device, side)
+        m._codes = m._scales = None
+        m.rows, m.cols, m.device = rows, cols, m._space.device
+        at = m._space.data_ptr()
+        m._c = cls._struct(at, at + rows * cp, rows, cols, cp, sp)
+        return m
+
+
+class MX4(_MX):
+    """A microscaled 4-bit matrix of rows x cols elements (zero_mx4 in
+    include/zero_sm.h): uint8 CUDA tensors ``codes`` [rows, pitch] and
+    ``scales`` [rows, pitch], each with contiguous rows."""
+
+    __slots__ = ()
+    _struct, _block_bytes = zero_mx4, 16
+
+
+class MX8(_MX):
+    """A microscaled 8-bit matrix of rows x cols elements (zero_mx8 in
+    include/zero_sm.h): uint8 CUDA tensors ``codes`` [rows, pitch] and
+    ``scales`` [rows, pitch], each with contiguous rows."""
+
+    __slots__ = ()
+    _struct, _block_bytes = zero_mx8, 32
 
 
 def mx4_empty(rows: int, cols: int, device=None) -> MX4:
     """An MX4 matrix of uninitialised memory; its scale rows are padded to 16
     bytes, the alignment that the product loads fastest."""
-    torch = _T or _torch()
-    if rows < 0 or cols < 0:
-        raise ValueError(f"{rows} x {cols}")
-    if device is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    elif torch.device(device).type != "cuda":
-        raise ValueError(f"an MX4 matrix lies on a CUDA device, not on {device}")
-    return _new_mx4(rows, cols, device, None)
+    return MX4._empty(rows, cols, device)
 
 
-def _new_mx4(rows: int, cols: int, device, side) -> MX4:
-    cp, sp = _mx4_pitches(cols)
-    m = MX4.__new__(MX4)
-    m._space = _empty(rows * (cp + sp), _T.uint8, device, side)
-    m._codes = m._scales = None
-    m.rows, m.cols, m.device = rows, cols, m._space.device
-    at = m._space.data_ptr()
-    m._c = zero_mx4(at, at + rows * cp, rows, cols, cp, sp)
-    return m
+def mx8_empty(rows: int, cols: int, device=None) -> MX8:
+    """An MX8 matrix of uninitialised memory."""
+    return MX8._empty(rows, cols, device)
 
 
 def _dense(t, name: str):
@@ -848,7 +892,7 @@ def _keep(side, *operands):
     if isinstance(side, _T.cuda.ExternalStream):
         return
     for t in operands:
-        if not isinstance(t, MX4):
+        if not isinstance(t, _MX):
             t.record_stream(side)
         elif t._space is not None:
             t._space.record_stream(side)
@@ -877,14 +921,19 @@ def _result(out, rows: int, cols: int, dtype, device, side, name: str = "out"):
     return out
 
 
-def _mx4_result(out, rows: int, cols: int, device, side, name: str = "out"):
+def _mx_result(kind, out, rows: int, cols: int, device, side, name: str = "out"):
     if out is None:
-        out = _new_mx4(rows, cols, device, side)
-    else:
-        if (out.rows, out.cols) != (rows, cols):
-            raise ValueError(f"{name} is {(out.rows, out.cols)}, not {(rows, cols)}")
-        _need_device(device, name, out)
+        return kind._new(rows, cols, device, side)
+    if not isinstance(out, kind):
+        raise ValueError(f"{name}: an {kind.__name__} matrix is needed")
+    if (out.rows, out.cols) != (rows, cols):
+        raise ValueError(f"{name} is {(out.rows, out.cols)}, not {(rows, cols)}")
+    _need_device(device, name, out)
     return out
+
+
+def _mx4_result(out, rows: int, cols: int, device, side, name: str = "out"):
+    return _mx_result(MX4, out, rows, cols, device, side, name)
 
 
 def _rounding(seed):
@@ -1001,17 +1050,25 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
     """(dx, dw) of ``mx4_linear``: dx = Q(dy) Q(w^T)^T and dw = Q(dy^T) Q(x^T)^T,
     each operand quantised in blocks along the axis its product sums over (dy
     stochastically when ``seed`` is given); the roundings' own gradients are
-    taken as one.  dx has x's type and dw dy's unless given (dw may be a view
-    of a rank's gradient buffer)."""
+    taken as one.  x is the layer's input, or its checkpoint, an ``MX8`` matrix.
+    dx has x's type (dy's for a checkpoint) and dw dy's unless given (dw may be
+    a view of a rank's gradient buffer)."""
     yptr, ycode, ldy, tokens, outputs = _dense(dy, "dy")
-    xptr, xcode, ldx, xtokens, inputs = _dense(x, "x")
+    kept = isinstance(x, MX8)
+    if kept:
+        xtokens, inputs, shape, dtype = x.rows, x.cols, (x.rows, x.cols), dy.dtype
+        where, xargs = "zero_mx4_linear_backward_mx8", (x._c,)
+    else:
+        xptr, xcode, ldx, xtokens, inputs = _dense(x, "x")
+        shape, dtype = tuple(x.shape), x.dtype
+        where, xargs = "zero_mx4_linear_backward", (xptr, xcode, ldx, tokens)
     if (tokens, outputs, inputs) != (xtokens, w.rows, w.cols):
-        raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} do not fit w {(w.rows, w.cols)}")
+        raise ValueError(f"dy {tuple(dy.shape)} and x {shape} do not fit w {(w.rows, w.cols)}")
     device = x.device
     _need_device(device, "dy", dy)
     _need_device(device, "w", w)
     side = _beside(device, stream)
-    dx = _result(dx, tokens, inputs, x.dtype, device, side, "dx")
+    dx = _result(dx, tokens, inputs, dtype, device, side, "dx")
     dw = _result(dw, outputs, inputs, dy.dtype, device, side, "dw")
     dxptr, dxcode, lddx, _, _ = _dense(dx, "dx")
     dwptr, dwcode, lddw, _, _ = _dense(dw, "dw")
@@ -1019,9 +1076,9 @@ def mx4_linear_backward(dy, x, w: MX4, seed: Optional[int] = None, dx=None, dw=N
     _mx4_check(zero_mx4_linear_backward_workspace(tokens, w._c, need), "zero_mx4_linear_backward_workspace")
     space = _empty(need.value, _T.uint8, device, side, False)
     rounding, seed = _rounding(seed)
-    _mx4_check(_on_device(device, stream, zero_mx4_linear_backward, yptr, ycode, ldy, xptr, xcode, ldx, tokens, w._c,
-                          rounding, seed, dxptr, dxcode, lddx, dwptr, dwcode, lddw, space.data_ptr(), need.value),
-               "zero_mx4_linear_backward")
+    _mx4_check(_on_device(device, stream, zero_mx4_linear_backward_mx8 if kept else zero_mx4_linear_backward, yptr, ycode,
+                          ldy, *xargs, w._c, rounding, seed, dxptr, dxcode, lddx, dwptr, dwcode, lddw, space.data_ptr(),
+                          need.value), where)
     if side is not None:
         _keep(side, dy, x, w, dx, dw)
     return dx, dw
@@ -1033,6 +1090,219 @@ def mx4_check(device=None, stream=None):
     torch = _torch()
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     _mx4_check(_on_device(device, stream, zero_mx4_check), "zero_mx4_check")
+
+
+# ------------------------------------------ around a layer's products ----
+#
+# What a training step keeps of its activations, the norm and the embedding.
+# ``stream`` as for the MX4 calls.
+
+def mx8_quantize(x, out: Optional[MX8] = None, stream=None) -> MX8:
+    """A matrix in 8 bits, in blocks along its rows: an activation on its way
+    into what the backward pass keeps (zero_mx8_quantize)."""
+    ptr, code, ld, rows, cols = _dense(x, "x")
+    device = x.device
+    side = _beside(device, stream)
+    out = _mx_result(MX8, out, rows, cols, device, side)
+    _mx4_check(_on_device(device, stream, zero_mx8_quantize, ptr, code, rows, cols, ld, out._c), "zero_mx8_quantize")
+    if side is not None:
+        _keep(side, x, out)
+    return out
+
+
+def mx8_dequantize(m: MX8, dtype=None, out=None, stream=None):
+    """The values of an MX8 matrix (bfloat16 unless ``dtype`` or ``out`` says otherwise)."""
+    device = m.device
+    side = _beside(device, stream)
+    out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, side)
+    ptr, code, ld, _, _ = _dense(out, "out")
+    _mx4_check(_on_device(device, stream, zero_mx8_dequantize, m._c, ptr, code, ld), "zero_mx8_dequantize")
+    if side is not None:
+        _keep(side, m, out)
+    return out
+
+
+class RMSNorm(NamedTuple):
+    """What ``rms_norm`` gives; None where it was not asked for."""
+    y: object
+    h: object
+    rstd: object
+    y8: Optional[MX8]
+    h8: Optional[MX8]
+
+
+def _vector(t, name: str, n: int, device) -> tuple:
+    """(pointer, dtype code) of a CUDA vector of n elements."""
+    if len(t.shape) != 1 or t.shape[0] != n or (n > 1 and t.stride()[0] != 1):
+        raise ValueError(f"{name}: a contiguous vector of {n} elements is needed, not {tuple(t.shape)}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} is {t.dtype}: bfloat16, float16 or float32 is needed")
+    _need_device(device, name, t)
+    return t.data_ptr(), code
+
+
+def _beside_x(t, name: str, x, rows: int, cols: int) -> tuple:
+    """(pointer, elements between rows) of a matrix of x's shape, type and device."""
+    if t.dtype != x.dtype or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} is {tuple(t.shape)} of {t.dtype}, not {(rows, cols)} of {x.dtype}")
+    _need_device(x.device, name, t)
+    ptr, _, ld, _, _ = _dense(t, name)
+    return ptr, ld
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, y=True, h=None, y8=False, h8=False, rstd=True,
+             stream=None) -> RMSNorm:
+    """Root-mean-square norm of h = x + residual: y = h (mean(h^2) + eps)^-1/2
+    weight, a row at a time (zero_rms_norm).  For each of the results y, h
+    (wanted by default where there is a residual), rstd (the root, for the
+    backward pass) and the 8-bit y8 and h8: True, False, or where to write it.
+    y or h may be x or the residual itself."""
+    ptr, code, ld, rows, cols = _dense(x, "x")
+    device = x.device
+    wptr, wcode = _vector(weight, "weight", cols, device)
+    rptr, ldr = (None, 0) if residual is None else _beside_x(residual, "residual", x, rows, cols)
+    side = _beside(device, stream)
+    if h is None:
+        h = residual is not None
+    used = [x, weight]
+    if residual is not None:
+        used.append(residual)
+    yptr, ldy, hptr, ldh, sptr, q, qc = None, cols, None, cols, None, [None, None], [None, None]
+    if y is True:
+        y = x.new_empty((rows, cols)) if side is None else _empty((rows, cols), x.dtype, device, side)
+        yptr = y.data_ptr()
+    elif y is False or y is None:
+        y = None
+    else:
+        yptr, ldy = _beside_x(y, "y", x, rows, cols)
+    if h is True:
+        h = x.new_empty((rows, cols)) if side is None else _empty((rows, cols), x.dtype, device, side)
+        hptr = h.data_ptr()
+    elif h is False:
+        h = None
+    else:
+        hptr, ldh = _beside_x(h, "h", x, rows, cols)
+    if rstd is True:
+        rstd = _empty((rows,), _T.float32, device, side)
+        sptr = rstd.data_ptr()
+    elif rstd is False or rstd is None:
+        rstd = None
+    else:
+        sptr, scode = _vector(rstd, "rstd", rows, device)
+        if scode != ZERO_DTYPE_F32:
+            raise ValueError(f"rstd is {rstd.dtype}: float32 is needed")
+    for k, (name, m) in enumerate((("y8", y8), ("h8", h8))):
+        if m is not False and m is not None:
+            q[k] = _mx_result(MX8, None if m is True else m, rows, cols, device, side, name)
+            qc[k] = q[k]._c
+    _mx4_check(_on_device(device, stream, zero_rms_norm, ptr, rptr, code, rows, cols, ld, ldr, wptr, wcode, eps, yptr, ldy,
+                          hptr, ldh, qc[0], qc[1], sptr), "zero_rms_norm")
+    if side is not None:
+        _keep(side, *used, *(t for t in (y, h, rstd, *q) if t is not None))
+    return RMSNorm(y, h, rstd, *q)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, stream=None):
+    """(dx, dw) of ``rms_norm`` from dy, h (or its checkpoint, an ``MX8``
+    matrix) and rstd; ``dh``, the gradient that reaches h by other ways, is
+    added to dx, which is x's gradient and the residual's.  dx has dy's type
+    (and may be dy or dh itself), dw the weight's unless given: it may be a view
+    of a rank's gradient buffer (zero_rms_norm_backward)."""
+    ptr, code, ld, rows, cols = _dense(dy, "dy")
+    device = dy.device
+    if isinstance(h, MX8):
+        if (h.rows, h.cols) != (rows, cols):
+            raise ValueError(f"h is {(h.rows, h.cols)}, not {(rows, cols)}")
+        _need_device(device, "h", h)
+        hptr, ldh, h8 = None, 0, h._c
+    else:
+        (hptr, ldh), h8 = _beside_x(h, "h", dy, rows, cols), None
+    wptr, wcode = _vector(weight, "weight", cols, device)
+    sptr, scode = _vector(rstd, "rstd", rows, device)
+    if scode != ZERO_DTYPE_F32:
+        raise ValueError(f"rstd is {rstd.dtype}: float32 is needed")
+    dhptr, lddh = (None, 0) if dh is None else _beside_x(dh, "dh", dy, rows, cols)
+    side = _beside(device, stream)
+    if dx is None:
+        dx = dy.new_empty((rows, cols)) if side is None else _empty((rows, cols), dy.dtype, device, side)
+        dxptr, lddx = dx.data_ptr(), cols
+    else:
+        dxptr, lddx = _beside_x(dx, "dx", dy, rows, cols)
+    if dw is None:
+        dw = _empty((cols,), weight.dtype, device, side)
+    dwptr, dwcode = _vector(dw, "dw", cols, device)
+    need = ctypes.c_int64()
+    _mx4_check(zero_rms_norm_backward_workspace(rows, cols, need), "zero_rms_norm_backward_workspace")
+    space = _empty(need.value, _T.uint8, device, side, False)
+    _mx4_check(_on_device(device, stream, zero_rms_norm_backward, ptr, code, rows, cols, ld, hptr, ldh, h8, wptr, wcode, sptr,
+                          dhptr, lddh, dxptr, lddx, dwptr, dwcode, space.data_ptr(), need.value), "zero_rms_norm_backward")
+    if side is not None:
+        _keep(side, dy, h, weight, rstd, dx, dw)
+        if dh is not None:
+            _keep(side, dh)
+    return dx, dw
+
+
+def _token_vector(tokens) -> tuple:
+    """(pointer, bytes of a token, how many) of a CUDA vector of integers."""
+    torch = _T or _torch()
+    size = 8 if tokens.dtype == torch.int64 else 4 if tokens.dtype == torch.int32 else 0
+    n = tokens.shape[0] if len(tokens.shape) == 1 else -1
+    if not size or n < 0 or not tokens.is_cuda or (n > 1 and tokens.stride()[0] != 1):
+        raise ValueError(f"tokens: a contiguous CUDA vector of int32 or int64 is needed, not {tuple(tokens.shape)} of "
+                         f"{tokens.dtype}")
+    return tokens.data_ptr(), size, n
+
+
+def embedding(tokens, table, scale: float = 1.0, dtype=None, out=None, stream=None):
+    """scale * table[token] for a vector of tokens (zero_embedding); a token
+    outside the table, such as -1, is padding: a row of zeros.  The table is a
+    matrix, or an ``MX4`` one as a rank gathers it; the result has the table's
+    type (bfloat16 for MX4) unless ``dtype`` or ``out`` says otherwise."""
+    tptr, tsize, n = _token_vector(tokens)
+    device = tokens.device
+    _need_device(device, "table", table)
+    if isinstance(table, MX4):
+        ptr, code, ld, vocab, cols, m = None, 0, 0, table.rows, table.cols, table._c
+        dtype = dtype or _T.bfloat16
+    else:
+        ptr, code, ld, vocab, cols = _dense(table, "table")
+        m, dtype = None, dtype or table.dtype
+    side = _beside(device, stream)
+    out = _result(out, n, cols, dtype, device, side)
+    optr, ocode, ldo, _, _ = _dense(out, "out")
+    _mx4_check(_on_device(device, stream, zero_embedding, tptr, tsize, n, ptr, code, vocab, cols, ld, m, scale, optr, ocode,
+                          ldo), "zero_embedding")
+    if side is not None:
+        _keep(side, tokens, table, out)
+    return out
+
+
+def embedding_backward(dy, tokens, vocab: int, scale: float = 1.0, out=None, accumulate: bool = False, stream=None):
+    """The gradient of a table of ``vocab`` rows: scale times the sum of the
+    rows of dy whose token it is, zeros for a row without tokens
+    (zero_embedding_backward).  ``out``, of dy's type unless given, may be a
+    view of a rank's gradient buffer; ``accumulate`` adds to what it holds."""
+    ptr, code, ld, n, cols = _dense(dy, "dy")
+    device = dy.device
+    tptr, tsize, tn = _token_vector(tokens)
+    if tn != n:
+        raise ValueError(f"{tn} tokens for {n} rows of dy")
+    _need_device(device, "tokens", tokens)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    side = _beside(device, stream)
+    out = _result(out, vocab, cols, dy.dtype, device, side)
+    optr, ocode, ldo, _, _ = _dense(out, "out")
+    need = ctypes.c_int64()
+    _mx4_check(zero_embedding_backward_workspace(n, vocab, cols, need), "zero_embedding_backward_workspace")
+    space = _empty(need.value, _T.uint8, device, side, False)
+    _mx4_check(_on_device(device, stream, zero_embedding_backward, ptr, code, n, cols, ld, tptr, tsize, vocab, scale, optr,
+                          ocode, ldo, 1 if accumulate else 0, space.data_ptr(), need.value), "zero_embedding_backward")
+    if side is not None:
+        _keep(side, dy, tokens, out)
+    return out
 
 
 # ------------------------------------------------ one logical rank per GPU ----

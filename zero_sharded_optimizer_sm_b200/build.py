@@ -14,6 +14,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = ["csrc/zero_api.cu", "csrc/kernels.cu", "csrc/fused_tma.cu", "csrc/fused_bulk.cu", "csrc/static_scratch.cu",
            "csrc/two_pass_tma.cu", "csrc/dist.cu", "csrc/guards.cu",
            "csrc/mx4.cu", "csrc/mx4_gemm.cu", "csrc/mx4_gemv.cu", "csrc/mx4_api.cu",
+           "csrc/mx8.cu", "csrc/rms_norm.cu", "csrc/embedding.cu", "csrc/layer_api.cu",
            "csrc/plan.cpp"]
 LIB = os.path.join(HERE, "libzero_sm.so")
 

@@ -10,36 +10,18 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_math.cuh"
 #include "mx4.cuh"
 #include "mx4_quant.cuh"
+#include "mx8.cuh"
 
 namespace zsm {
 namespace {
 
 using namespace dev;
 using namespace mx;
-
-// The two 16-bit formats: two values rounded into a word, infinity's pattern.
-template <class F>
-struct Half;
-template <>
-struct Half<Bf16> {
-  static constexpr uint32_t kInf = 0x7F80u;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162_raw r = __floats2bfloat162_rn(a, b);
-    return (uint32_t)r.x | ((uint32_t)r.y << 16);
-  }
-};
-template <>
-struct Half<F16> {
-  static constexpr uint32_t kInf = 0x7C00u;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __half2_raw r = __floats2half2_rn(a, b);
-    return (uint32_t)r.x | ((uint32_t)r.y << 16);
-  }
-};
 
 // ---------------------------------------------------- quantise along rows --
 
@@ -116,7 +98,10 @@ __global__ void __launch_bounds__(kRowThreads) mx_rows_kernel(const __grid_const
 constexpr int kTileRows = 128;
 constexpr int kTileWords = 64;  // 32-bit words of a tile's row
 
-template <class V, bool kFromMx, bool kRows, bool kStochastic>
+// What a tile is read from: a dense matrix, an MX4 one, an MX8 one.
+enum Source { kDense, kFromMx4, kFromMx8 };
+
+template <class V, Source kFrom, bool kRows, bool kStochastic>
 __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t index, uint32_t tiles_x, int vec,
                                               uint32_t (&tile)[kTileRows][kTileWords]) {
   using raw = typename V::raw;
@@ -136,16 +121,19 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
   for (int i = 0; i < kLoads; ++i) {
     const int64_t row = r0 + rv + (256 / kVecs) * i;
     const int64_t left = row < a.rows ? a.cols - col : 0;
-    if constexpr (kFromMx) {
-      // the elements' values are exact in bf16: three significant bits and
-      // the same exponent range as binary32
-      uint32_t w = 0u, sc = 0u;
+    if constexpr (kFrom != kDense) {
+      // the elements' values are exact in bf16: three or four significant bits
+      // and the same exponent range as binary32
+      using Codes = typename std::conditional<kFrom == kFromMx4, uint32_t, uint2>::type;
+      Codes w = {};
+      uint32_t sc = 0u;
       if (left > 0) {
-        w = *reinterpret_cast<const uint32_t*>(a.from.codes + row * a.from.code_pitch + (col >> 1));
+        w = *reinterpret_cast<const Codes*>(a.from.codes + row * a.from.code_pitch + (kFrom == kFromMx4 ? col >> 1 : col));
         sc = a.from.scales[row * a.from.scale_pitch + (col >> 5)];
       }
       float v[8];
-      values8(w, sc, v);
+      if constexpr (kFrom == kFromMx4) values8(w, sc, v);
+      else values8_mx8(w, sc, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[i].w[j] = pack2(Bf16::rn(v[2 * j]), Bf16::rn(v[2 * j + 1]));
@@ -222,12 +210,12 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
   }
 }
 
-template <class V, bool kFromMx, bool kRows, bool kStochastic>
+template <class V, Source kFrom, bool kRows, bool kStochastic>
 __global__ void __launch_bounds__(256, 4) mx_tile_kernel(const __grid_constant__ MxQuantArgs a, const uint32_t tiles_x,
                                                          const int vec) {
   __shared__ __align__(16) uint32_t tile[kTileRows][kTileWords];
   pdl_trigger();
-  quantize_tile<V, kFromMx, kRows, kStochastic>(a, blockIdx.x, tiles_x, vec, tile);
+  quantize_tile<V, kFrom, kRows, kStochastic>(a, blockIdx.x, tiles_x, vec, tile);
 }
 
 // The three matrices of a linear layer's backward pass, one after another in
@@ -237,31 +225,18 @@ struct TileCounts {
   uint32_t dy_x, x_x, w_x;  // tiles along a row
   int dy_vec, x_vec;
 };
-template <class V, bool kStochastic>
+template <class V, bool kStochastic, bool kX8>
 __global__ void __launch_bounds__(256, 4) mx_backward_kernel(const __grid_constant__ MxBackwardArgs a, const TileCounts n) {
   __shared__ __align__(16) uint32_t tile[kTileRows][kTileWords];
   pdl_trigger();
-  if (blockIdx.x < n.dy) quantize_tile<V, false, true, kStochastic>(a.dy, blockIdx.x, n.dy_x, n.dy_vec, tile);
-  else if (blockIdx.x < n.x) quantize_tile<V, false, false, false>(a.x, blockIdx.x - n.dy, n.x_x, n.x_vec, tile);
-  else quantize_tile<Vec16<Bf16>, true, false, false>(a.w, blockIdx.x - n.x, n.w_x, 1, tile);
+  if (blockIdx.x < n.dy) quantize_tile<V, kDense, true, kStochastic>(a.dy, blockIdx.x, n.dy_x, n.dy_vec, tile);
+  else if (blockIdx.x < n.x) {
+    if constexpr (kX8) quantize_tile<Vec16<Bf16>, kFromMx8, false, false>(a.x, blockIdx.x - n.dy, n.x_x, 1, tile);
+    else quantize_tile<V, kDense, false, false>(a.x, blockIdx.x - n.dy, n.x_x, n.x_vec, tile);
+  } else quantize_tile<Vec16<Bf16>, kFromMx4, false, false>(a.w, blockIdx.x - n.x, n.w_x, 1, tile);
 }
 
 // --------------------------------------------------------------- read back --
-
-struct TBf16 {
-  using raw = uint16_t;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) { return Half<Bf16>::pack(a, b); }
-  static __device__ __forceinline__ raw rn(float x) { return Bf16::rn(x); }
-};
-struct TF16 {
-  using raw = uint16_t;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) { return Half<F16>::pack(a, b); }
-  static __device__ __forceinline__ raw rn(float x) { return F16::rn(x); }
-};
-struct TF32 {
-  using raw = float;
-  static __device__ __forceinline__ raw rn(float x) { return x; }
-};
 
 // As mx_rows_kernel: a lane turns 4 bytes of codes into 8 elements, kUnits
 // pieces of 256 columns side by side.
@@ -291,19 +266,7 @@ __global__ void __launch_bounds__(kRowThreads) mx_dequant_kernel(const __grid_co
       values8(w[k], s[k], v);
       const int64_t n = u0 + k * warps < units ? a.in.cols - col[k] : 0;
       raw* p = dst + row[k] * a.ld + col[k];
-      if (n >= 8 && vec) {
-        if constexpr (sizeof(raw) == 2) {
-          st_stream(reinterpret_cast<uint16_t*>(p), make_uint4(T::pack(v[0], v[1]), T::pack(v[2], v[3]), T::pack(v[4], v[5]),
-                                                               T::pack(v[6], v[7])));
-        } else {
-          st_stream(reinterpret_cast<float*>(p), make_float4(v[0], v[1], v[2], v[3]));
-          st_stream(reinterpret_cast<float*>(p) + 4, make_float4(v[4], v[5], v[6], v[7]));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n) p[j] = T::rn(v[j]);
-      }
+      store8<T>(p, v, n, vec);
     }
   }
 }
@@ -457,37 +420,6 @@ __global__ void __launch_bounds__(kThreads, kWide == 8 ? 4 : 5) mx_reduce_kernel
   norm_epilogue<kThreads>(a.ns, sq, (unsigned long long)nf, a.accumulate);
 }
 
-int cap_grid(int64_t want, int cap) { return (int)std::max<int64_t>(1, std::min<int64_t>(want, cap)); }
-
-bool aligned(const void* p, int64_t pitch_bytes) {
-  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 15u) == 0;
-}
-
-// Pieces of 256 columns over all rows; a matrix whose rows lie end to end in
-// whole blocks is taken as one row, so that narrow rows fill the warps.
-struct Pieces {
-  int64_t rows, cols;
-  FastDiv per_row;
-  uint32_t units;
-};
-bool pieces_of(int64_t rows, int64_t cols, bool end_to_end, Pieces* p) {
-  if (end_to_end) {
-    cols *= rows;
-    rows = 1;
-  }
-  const int64_t per = (cols + 255) / 256;
-  // as FastDiv and the kernels' counters allow; more than 2^31 pieces of
-  // whole rows are more memory than there is
-  if (per * rows > 0x7FFFFFFFll) return false;
-  *p = Pieces{rows, cols, fast_div((uint32_t)per), (uint32_t)(per * rows)};
-  return true;
-}
-
-// CTAs to an SM of a streaming launch at most: a CTA that ends makes room for
-// one whose loads go out at once (read-back of 8192 x 2048: 11.8 us with 8, the
-// CTAs then walking on, 9.8 with 64).
-constexpr int kWaves = 64;
-
 template <class V>
 cudaError_t quantize_rows(MxQuantArgs a, int sm_count, cudaStream_t s) {
   const bool flat = a.cols % kMxBlock == 0 && a.ld == a.cols && a.out.code_pitch == a.cols / 2 &&
@@ -504,23 +436,23 @@ cudaError_t quantize_rows(MxQuantArgs a, int sm_count, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <class V, bool kFromMx>
+template <class V, Source kFrom>
 cudaError_t quantize_tiles(const MxQuantArgs& a, cudaStream_t s) {
   constexpr int kCols = kTileWords * 4 / (int)sizeof(typename V::raw);
   const int64_t tx = (a.cols + kCols - 1) / kCols, ty = (a.rows + kTileRows - 1) / kTileRows;
   if (tx * ty > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const int vec = kFromMx || aligned(a.src, a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
+  const int vec = kFrom != kDense || aligned(a.src, a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
   const unsigned grid = (unsigned)(tx * ty);
   const uint32_t x = (uint32_t)tx;
-  if constexpr (!kFromMx) {  // an MX4 matrix is only transposed
+  if constexpr (kFrom == kDense) {  // an MX4 matrix is only transposed
     if (a.out.codes) {
-      if (a.stochastic) mx_tile_kernel<V, kFromMx, true, true><<<grid, 256, 0, s>>>(a, x, vec);
-      else mx_tile_kernel<V, kFromMx, true, false><<<grid, 256, 0, s>>>(a, x, vec);
+      if (a.stochastic) mx_tile_kernel<V, kFrom, true, true><<<grid, 256, 0, s>>>(a, x, vec);
+      else mx_tile_kernel<V, kFrom, true, false><<<grid, 256, 0, s>>>(a, x, vec);
       return cudaGetLastError();
     }
   }
-  if (a.stochastic) mx_tile_kernel<V, kFromMx, false, true><<<grid, 256, 0, s>>>(a, x, vec);
-  else mx_tile_kernel<V, kFromMx, false, false><<<grid, 256, 0, s>>>(a, x, vec);
+  if (a.stochastic) mx_tile_kernel<V, kFrom, false, true><<<grid, 256, 0, s>>>(a, x, vec);
+  else mx_tile_kernel<V, kFrom, false, false><<<grid, 256, 0, s>>>(a, x, vec);
   return cudaGetLastError();
 }
 
@@ -528,23 +460,29 @@ template <class V>
 cudaError_t quantize_backward(const MxBackwardArgs& a, cudaStream_t s) {
   constexpr int kCols = kTileWords * 4 / (int)sizeof(typename V::raw), kCols16 = 2 * kTileWords;
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  const int64_t dx = up(a.dy.cols, kCols), xx = up(a.x.cols, kCols), wx = up(a.w.cols, kCols16);
+  const bool x8 = a.x.from.codes != nullptr;
+  const int64_t dx = up(a.dy.cols, kCols), xx = up(a.x.cols, x8 ? kCols16 : kCols), wx = up(a.w.cols, kCols16);
   const int64_t nd = dx * up(a.dy.rows, kTileRows), nx = xx * up(a.x.rows, kTileRows), nw = wx * up(a.w.rows, kTileRows);
   if (nd + nx + nw > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   TileCounts n;
   n.dy = (uint32_t)nd, n.x = (uint32_t)(nd + nx);
   n.dy_x = (uint32_t)dx, n.x_x = (uint32_t)xx, n.w_x = (uint32_t)wx;
   n.dy_vec = aligned(a.dy.src, a.dy.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
-  n.x_vec = aligned(a.x.src, a.x.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
+  n.x_vec = !x8 && aligned(a.x.src, a.x.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
   const unsigned grid = (unsigned)(nd + nx + nw);
-  if (a.dy.stochastic) mx_backward_kernel<V, true><<<grid, 256, 0, s>>>(a, n);
-  else mx_backward_kernel<V, false><<<grid, 256, 0, s>>>(a, n);
+  if (a.dy.stochastic) {
+    if (x8) mx_backward_kernel<V, true, true><<<grid, 256, 0, s>>>(a, n);
+    else mx_backward_kernel<V, true, false><<<grid, 256, 0, s>>>(a, n);
+  } else {
+    if (x8) mx_backward_kernel<V, false, true><<<grid, 256, 0, s>>>(a, n);
+    else mx_backward_kernel<V, false, false><<<grid, 256, 0, s>>>(a, n);
+  }
   return cudaGetLastError();
 }
 
 template <class V>
 cudaError_t quantize_from(const MxQuantArgs& a, int sm_count, cudaStream_t s) {
-  return a.out_t.codes ? quantize_tiles<V, false>(a, s) : quantize_rows<V>(a, sm_count, s);
+  return a.out_t.codes ? quantize_tiles<V, kDense>(a, s) : quantize_rows<V>(a, sm_count, s);
 }
 
 template <class T>
@@ -564,7 +502,7 @@ cudaError_t dequantize_to(MxDequantArgs a, int sm_count, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, int sm_count, cudaStream_t s) {
-  if (a.from.codes) return quantize_tiles<Vec16<Bf16>, true>(a, s);  // an MX4 matrix's transpose
+  if (a.from.codes) return quantize_tiles<Vec16<Bf16>, kFromMx4>(a, s);  // an MX4 matrix's transpose
   switch (a.type) {
     case kMxBf16: return quantize_from<Vec16<Bf16>>(a, sm_count, s);
     case kMxF16: return quantize_from<Vec16<F16>>(a, sm_count, s);
@@ -574,7 +512,7 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, int sm_count, cudaStream_t 
 }
 
 cudaError_t launch_mx_backward(const MxBackwardArgs& a, int sm_count, cudaStream_t s) {
-  if (a.dy.type == a.x.type) {
+  if (a.dy.type == a.x.type || a.x.from.codes) {
     switch (a.dy.type) {
       case kMxBf16: return quantize_backward<Vec16<Bf16>>(a, s);
       case kMxF16: return quantize_backward<Vec16<F16>>(a, s);

@@ -66,8 +66,8 @@ struct MxPieceArgs {
 };
 
 struct MxQuantArgs {
-  const void* src;      // rows x cols of `type`, ld elements between rows; or an MX4 matrix:
-  MxMatrix from;        //   (type ignored, codes set)
+  const void* src;      // rows x cols of `type`, ld elements between rows; or an MX4 or MX8 matrix:
+  MxMatrix from;        //   (type ignored, codes set; MX8 as launch_mx_backward's x only)
   int type;
   int64_t rows, cols, ld;
   MxMatrix out;         // blocks along the rows: rows x cols (codes null: not wanted)
@@ -78,7 +78,8 @@ struct MxQuantArgs {
 };
 
 // The backward pass of a linear layer's operands in one launch: dy along its
-// rows and down its columns, x down its columns (both of `type`), w's transpose.
+// rows and down its columns, x down its columns (both of `type`, or x an MX8
+// matrix), w's transpose.
 struct MxBackwardArgs {
   MxQuantArgs dy, x, w;
 };

@@ -3,12 +3,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
-#include <cstdarg>
-#include <cstdio>
-#include <cstring>
 
 #include "../../include/zero_sm.h"
+#include "api_checks.hpp"
 #include "mx4.cuh"
 #include "mx4_errors.hpp"
 
@@ -18,86 +15,11 @@ static_assert(ZERO_MX4_BLOCK == zsm::kMxBlock, "block length");
 
 namespace {
 
-zero_status fail(zero_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  zsm::set_thread_error(buf);
-  return s;
-}
-
-zero_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(ZERO_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-constexpr int64_t kMaxDim = 0x7FFFFFFF - 255;  // row and column numbers of a tile stay in 32 bits
-
-int elem_bytes(int32_t dtype) { return dtype == ZERO_DTYPE_F32 ? 4 : 2; }
-
-zero_status check_dtype(int32_t dtype) {
-  if (dtype != ZERO_DTYPE_BF16 && dtype != ZERO_DTYPE_F16 && dtype != ZERO_DTYPE_F32)
-    return fail(ZERO_EINVAL, "unknown dtype %d", dtype);
-  return ZERO_OK;
-}
-
-zero_status check_dense(const char* name, const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
-  const zero_status st = check_dtype(dtype);
-  if (st != ZERO_OK) return st;
-  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim)
-    return fail(ZERO_EINVAL, "%s: %lld x %lld is out of range", name, (long long)rows, (long long)cols);
-  if (rows == 0 || cols == 0) return ZERO_OK;
-  if (!p || (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem_bytes(dtype) - 1)))
-    return fail(ZERO_EINVAL, "%s is null or not aligned to its elements", name);
-  if (ld < cols && rows > 1)
-    return fail(ZERO_EINVAL, "%s: %lld elements between rows of %lld", name, (long long)ld, (long long)cols);
-  return ZERO_OK;
-}
-
-zero_status check_mx4(const char* name, const zero_mx4* m) {
-  if (!m) return fail(ZERO_EINVAL, "%s is NULL", name);
-  if (m->rows < 0 || m->cols < 0 || m->rows > kMaxDim || m->cols > kMaxDim)
-    return fail(ZERO_EINVAL, "%s: %lld x %lld is out of range", name, (long long)m->rows, (long long)m->cols);
-  if (m->rows == 0 || m->cols == 0) return ZERO_OK;
-  const int64_t nb = zsm::mx_blocks(m->cols);
-  if (!m->codes || (reinterpret_cast<uintptr_t>(m->codes) & 15u) || !m->scales)
-    return fail(ZERO_EINVAL, "%s: codes must be 16-byte aligned and neither codes nor scales NULL", name);
-  if (m->code_pitch % 16 || m->code_pitch < 16 * nb)
-    return fail(ZERO_EINVAL, "%s: code_pitch %lld must be a multiple of 16, at least 16 * %lld blocks", name,
-                (long long)m->code_pitch, (long long)nb);
-  if (m->scale_pitch < nb)
-    return fail(ZERO_EINVAL, "%s: scale_pitch %lld is less than the row's %lld blocks", name, (long long)m->scale_pitch,
-                (long long)nb);
-  return ZERO_OK;
-}
-
-zsm::MxMatrix matrix(const zero_mx4& m) {
-  return {static_cast<uint8_t*>(m.codes), static_cast<uint8_t*>(m.scales), m.rows, m.cols, m.code_pitch, m.scale_pitch};
-}
-
-// SMs of the current device, asked for once per device.
-cudaError_t sm_count(int* n) {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (*n = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-  e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && dev < 64) known[dev].store(*n, std::memory_order_relaxed);
-  return e;
-}
+using namespace zsm::api;
 
 zero_status check_rounding(int32_t rounding) {
   if (rounding != ZERO_MX4_NEAREST && rounding != ZERO_MX4_STOCHASTIC)
     return fail(ZERO_EINVAL, "unknown rounding %d", rounding);
-  return ZERO_OK;
-}
-
-zero_status check_workspace(const void* workspace, int64_t have, int64_t need) {
-  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || have < need))
-    return fail(ZERO_EINVAL, "the workspace must be 16-byte aligned and of at least %lld bytes (%lld given)",
-                (long long)need, (long long)have);
   return ZERO_OK;
 }
 
@@ -155,11 +77,37 @@ Backward backward_parts(uint8_t* at, int64_t tokens, int64_t o, int64_t k) {
   return p;
 }
 
-// A product over no elements: zeros.
-zero_status zero_fill(void* out, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, cudaStream_t s) {
-  const int es = elem_bytes(dtype);
-  const cudaError_t e = cudaMemset2DAsync(out, (size_t)(rows > 1 ? ld : cols) * es, 0, (size_t)cols * es, (size_t)rows, s);
-  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "clearing the product");
+// The backward pass of a linear layer, x a dense matrix or an MX8 one; the
+// arguments have been checked.
+zero_status linear_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, zsm::MxQuantArgs x, int64_t tokens,
+                            const zero_mx4* w, int32_t rounding, uint64_t seed, void* dx, int32_t dx_dtype, int64_t ld_dx,
+                            void* dw, int32_t dw_dtype, int64_t ld_dw, void* workspace, int64_t workspace_bytes,
+                            cudaStream_t s) {
+  zero_status st = ZERO_OK;
+  const int64_t o = w->rows, k = w->cols;
+  if (k == 0) return ZERO_OK;
+  if (tokens == 0) return o ? zero_fill(dw, dw_dtype, o, k, ld_dw, s) : ZERO_OK;
+  if (o == 0) return zero_fill(dx, dx_dtype, tokens, k, ld_dx, s);
+  const Backward p = backward_parts(static_cast<uint8_t*>(workspace), tokens, o, k);
+  if ((st = check_workspace(workspace, workspace_bytes, p.bytes)) != ZERO_OK) return st;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  zsm::MxBackwardArgs a = {};
+  a.dy.src = dy, a.dy.type = dy_dtype;
+  a.dy.rows = tokens, a.dy.cols = o, a.dy.ld = tokens > 1 ? ld_dy : o;
+  a.dy.out = matrix(p.dy), a.dy.out_t = matrix(p.dy_t);
+  a.dy.stochastic = rounding == ZERO_MX4_STOCHASTIC, a.dy.seed = seed;
+  a.x = x;
+  a.x.rows = tokens, a.x.cols = k;
+  a.x.out_t = matrix(p.x_t);
+  a.w.from = matrix(*w);
+  a.w.rows = o, a.w.cols = k;
+  a.w.out_t = matrix(p.w_t);
+  e = zsm::launch_mx_backward(a, sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "MX4 backward quantise launch");
+  if ((st = matmul(p.dy, p.w_t, dx, dx_dtype, ld_dx, nullptr, 1, 0, sms, s)) != ZERO_OK) return st;
+  return matmul(p.dy_t, p.x_t, dw, dw_dtype, ld_dw, nullptr, 1, 0, sms, s);
 }
 
 }  // namespace
@@ -331,30 +279,29 @@ zero_status zero_mx4_linear_backward(const void* dy, int32_t dy_dtype, int64_t l
   if ((st = check_rounding(rounding)) != ZERO_OK) return st;
   if ((st = check_dense("dx", dx, dx_dtype, tokens, k, ld_dx)) != ZERO_OK) return st;
   if ((st = check_dense("dw", dw, dw_dtype, o, k, ld_dw)) != ZERO_OK) return st;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (k == 0) return ZERO_OK;
-  if (tokens == 0) return o ? zero_fill(dw, dw_dtype, o, k, ld_dw, s) : ZERO_OK;
-  if (o == 0) return zero_fill(dx, dx_dtype, tokens, k, ld_dx, s);
-  const Backward p = backward_parts(static_cast<uint8_t*>(workspace), tokens, o, k);
-  if ((st = check_workspace(workspace, workspace_bytes, p.bytes)) != ZERO_OK) return st;
-  int sms = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return cuda_fail(e, "device query");
-  zsm::MxBackwardArgs a = {};
-  a.dy.src = dy, a.dy.type = dy_dtype;
-  a.dy.rows = tokens, a.dy.cols = o, a.dy.ld = tokens > 1 ? ld_dy : o;
-  a.dy.out = matrix(p.dy), a.dy.out_t = matrix(p.dy_t);
-  a.dy.stochastic = rounding == ZERO_MX4_STOCHASTIC, a.dy.seed = seed;
-  a.x.src = x, a.x.type = x_dtype;
-  a.x.rows = tokens, a.x.cols = k, a.x.ld = tokens > 1 ? ld_x : k;
-  a.x.out_t = matrix(p.x_t);
-  a.w.from = matrix(*w);
-  a.w.rows = o, a.w.cols = k;
-  a.w.out_t = matrix(p.w_t);
-  e = zsm::launch_mx_backward(a, sms, s);
-  if (e != cudaSuccess) return cuda_fail(e, "MX4 backward quantise launch");
-  if ((st = matmul(p.dy, p.w_t, dx, dx_dtype, ld_dx, nullptr, 1, 0, sms, s)) != ZERO_OK) return st;
-  return matmul(p.dy_t, p.x_t, dw, dw_dtype, ld_dw, nullptr, 1, 0, sms, s);
+  zsm::MxQuantArgs q = {};
+  q.src = x, q.type = x_dtype, q.ld = tokens > 1 ? ld_x : k;
+  return linear_backward(dy, dy_dtype, ld_dy, q, tokens, w, rounding, seed, dx, dx_dtype, ld_dx, dw, dw_dtype, ld_dw,
+                         workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+zero_status zero_mx4_linear_backward_mx8(const void* dy, int32_t dy_dtype, int64_t ld_dy, const zero_mx8* x,
+                                         const zero_mx4* w, int32_t rounding, uint64_t seed, void* dx, int32_t dx_dtype,
+                                         int64_t ld_dx, void* dw, int32_t dw_dtype, int64_t ld_dw, void* workspace,
+                                         int64_t workspace_bytes, void* stream) {
+  zero_status st = check_mx4("w", w);
+  if (st != ZERO_OK) return st;
+  if ((st = check_mx8("x", x)) != ZERO_OK) return st;
+  const int64_t o = w->rows, k = w->cols, tokens = x->rows;
+  if (x->cols != k) return fail(ZERO_EINVAL, "x has %lld inputs, w %lld", (long long)x->cols, (long long)k);
+  if ((st = check_dense("dy", dy, dy_dtype, tokens, o, ld_dy)) != ZERO_OK) return st;
+  if ((st = check_rounding(rounding)) != ZERO_OK) return st;
+  if ((st = check_dense("dx", dx, dx_dtype, tokens, k, ld_dx)) != ZERO_OK) return st;
+  if ((st = check_dense("dw", dw, dw_dtype, o, k, ld_dw)) != ZERO_OK) return st;
+  zsm::MxQuantArgs q = {};
+  q.from = matrix8(*x);
+  return linear_backward(dy, dy_dtype, ld_dy, q, tokens, w, rounding, seed, dx, dx_dtype, ld_dx, dw, dw_dtype, ld_dw,
+                         workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 zero_status zero_mx4_check(void* stream) {

@@ -1,7 +1,12 @@
-// Dense vectors of eight elements and their quantisation, shared by the
-// quantising kernels (mx4.cu) and the product that quantises its own operand
-// (mx4_gemm.cu).
+// Dense vectors of eight elements, their quantisation and their stores, shared
+// by the kernels that walk rows (mx4.cu, mx8.cu, rms_norm.cu, embedding.cu) and
+// the product that quantises its own operand (mx4_gemm.cu).
 #pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "device_math.cuh"
 #include "mx4.cuh"
@@ -10,6 +15,26 @@ namespace zsm {
 namespace mx {
 
 using namespace dev;
+
+// The two 16-bit formats: two values rounded into a word, infinity's pattern.
+template <class F>
+struct Half;
+template <>
+struct Half<Bf16> {
+  static constexpr uint32_t kInf = 0x7F80u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162_raw r = __floats2bfloat162_rn(a, b);
+    return (uint32_t)r.x | ((uint32_t)r.y << 16);
+  }
+};
+template <>
+struct Half<F16> {
+  static constexpr uint32_t kInf = 0x7C00u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2_raw r = __floats2half2_rn(a, b);
+    return (uint32_t)r.x | ((uint32_t)r.y << 16);
+  }
+};
 
 // Eight consecutive elements of a storage type, kept as loaded: their values,
 // and the binary32 pattern of the largest magnitude (an infinity or NaN
@@ -135,6 +160,82 @@ __device__ __forceinline__ void write_pieces(const MxPieceArgs& a, int w) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(out + 512 * j) = v[j];
 }
+
+// ---------------------------------------------------------- element types --
+
+// kFinite: the largest number, where an MX8 value may be over it.
+struct TBf16 {
+  static constexpr float kFinite = 0.0f;
+  using V = Vec16<Bf16>;
+  using raw = uint16_t;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return Half<Bf16>::pack(a, b); }
+  static __device__ __forceinline__ raw rn(float x) { return Bf16::rn(x); }
+};
+struct TF16 {
+  static constexpr float kFinite = 65504.0f;
+  using V = Vec16<F16>;
+  using raw = uint16_t;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return Half<F16>::pack(a, b); }
+  static __device__ __forceinline__ raw rn(float x) { return F16::rn(x); }
+};
+struct TF32 {
+  static constexpr float kFinite = 0.0f;
+  using V = Vec32;
+  using raw = float;
+  static __device__ __forceinline__ raw rn(float x) { return x; }
+};
+
+// Eight elements rounded into n places (all eight, on a 16-byte boundary, when
+// n >= 8 and vec).
+template <class T>
+__device__ __forceinline__ void store8(typename T::raw* p, const float (&v)[8], int64_t n, int vec) {
+  using raw = typename T::raw;
+  if (n >= 8 && vec) {
+    if constexpr (sizeof(raw) == 2) {
+      st_stream(p, make_uint4(T::pack(v[0], v[1]), T::pack(v[2], v[3]), T::pack(v[4], v[5]), T::pack(v[6], v[7])));
+    } else {
+      st_stream(p, make_float4(v[0], v[1], v[2], v[3]));
+      st_stream(p + 4, make_float4(v[4], v[5], v[6], v[7]));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = T::rn(v[j]);
+  }
+}
+
+// ------------------------------------------------------------------ launches --
+
+inline int cap_grid(int64_t want, int cap) { return (int)std::max<int64_t>(1, std::min<int64_t>(want, cap)); }
+
+inline bool aligned(const void* p, int64_t pitch_bytes) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 15u) == 0;
+}
+
+// Pieces of 256 columns over all rows; a matrix whose rows lie end to end in
+// whole blocks is taken as one row, so that narrow rows fill the warps.
+struct Pieces {
+  int64_t rows, cols;
+  FastDiv per_row;
+  uint32_t units;
+};
+inline bool pieces_of(int64_t rows, int64_t cols, bool end_to_end, Pieces* p) {
+  if (end_to_end) {
+    cols *= rows;
+    rows = 1;
+  }
+  const int64_t per = (cols + 255) / 256;
+  // as FastDiv and the kernels' counters allow; more than 2^31 pieces of
+  // whole rows are more memory than there is
+  if (per * rows > 0x7FFFFFFFll) return false;
+  *p = Pieces{rows, cols, fast_div((uint32_t)per), (uint32_t)(per * rows)};
+  return true;
+}
+
+// CTAs to an SM of a streaming launch at most: a CTA that ends makes room for
+// one whose loads go out at once (read-back of 8192 x 2048: 11.8 us with 8, the
+// CTAs then walking on, 9.8 with 64).
+constexpr int kWaves = 64;
 
 }  // namespace mx
 }  // namespace zsm
