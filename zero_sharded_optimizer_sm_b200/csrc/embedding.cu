@@ -205,55 +205,434 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
   }
 }
 
-// ---------------------------------------------------------------- gradient --
+// ------------------------------------------------------ sort of one cluster --
 
-// starts[v]: the first place of token v or a later one, for v = 0 .. vocab.
-__global__ void __launch_bounds__(256) embedding_starts_kernel(const uint32_t* keys, const uint32_t n, const uint32_t vocab,
-                                                               uint32_t* starts) {
-  const uint32_t v = blockIdx.x * 256 + threadIdx.x;
-  if (v > vocab) return;
-  uint32_t lo = 0, hi = n;
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (keys[mid] < v) lo = mid + 1;
-    else hi = mid;
-  }
-  starts[v] = lo;
+// Batches of up to kClusterMax positions are sorted by one cluster of CTAs in
+// one launch: every CTA keeps its part of the (token, position) pairs in shared
+// memory, and a pass writes them to their places in the cluster's CTAs.
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterCtas = 8;
+constexpr int kClusterBits = 9;                       // of a pass: two for up to 2^18 - 1 rows
+constexpr int kClusterDigits = 1 << kClusterBits;
+constexpr int kClusterPer = 8192;                     // positions of a CTA
+constexpr int64_t kClusterMax = (int64_t)kClusterCtas * kClusterPer;
+
+struct ClusterSort {
+  const void* tokens;
+  int token_bytes;
+  uint32_t n, vocab;
+  int ctas;        // of a cluster
+  uint32_t per;    // positions of a CTA: a multiple of 1024
+  int bits, passes;
+  uint32_t *keys, *pos;
+};
+
+struct ClusterShared {
+  uint16_t count[kClusterWarps][kClusterDigits];  // a warp's pairs of a digit, then those of the warps before it
+  uint32_t all[kClusterDigits];                   // the CTA's pairs of a digit (read by the cluster)
+  uint32_t base[kClusterDigits];                  // the place of the CTA's first pair of a digit
+  uint32_t sums[kClusterWarps];
+};
+constexpr int kClusterSmem = (int)sizeof(ClusterShared) + 2 * kClusterPer * 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+// The address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t at, uint2 v) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
 }
 
-// A warp sums 256 columns of one row of the table.
-template <class V, class T>
-__global__ void __launch_bounds__(kRowThreads) embedding_sum_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
-                                                                    const uint32_t* starts, const uint32_t* pos,
-                                                                    const uint32_t per_row, const int vec) {
-  using raw = typename T::raw;
-  const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32), units = a.vocab * per_row;
+__device__ __forceinline__ uint32_t key_of(int64_t token, uint32_t vocab) {
+  return (uint64_t)token < (uint64_t)vocab ? (uint32_t)token : vocab;
+}
+
+__global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const __grid_constant__ ClusterSort s) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  pdl_trigger();
+  ClusterShared& sh = *reinterpret_cast<ClusterShared*>(smem);
+  uint2* pairs = reinterpret_cast<uint2*>(smem + sizeof(ClusterShared));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = s.ctas > 1 ? cluster_rank() : 0;
+  const uint32_t mine = rank * s.per;                              // my first position
+  const uint32_t rounds = s.per / kClusterThreads;                 // pairs of a lane
+  const uint32_t left = s.n > mine ? min(s.n - mine, s.per) : 0u;  // my pairs
+  const uint32_t first = warp * 32 * rounds + lane;
+  for (uint32_t k = 0; k < rounds; ++k) {
+    const uint32_t i = first + 32 * k;
+    if (i < left) pairs[i] = make_uint2(key_of(token_at(s.tokens, s.token_bytes, mine + i), s.vocab), mine + i);
+  }
+  for (int pass = 0; pass < s.passes; ++pass) {
+    const uint2* from = pairs + (pass & 1) * s.per;
+    uint2* to = pairs + (~pass & 1) * s.per;
+    const int shift = pass * s.bits;
+    const uint32_t digits = 1u << s.bits;
+    for (uint32_t d = lane; d < digits; d += 32) sh.count[warp][d] = 0;
+    __syncwarp();
+    uint32_t ranks[kClusterPer / kClusterThreads];
+#pragma unroll
+    for (uint32_t k = 0; k < kClusterPer / kClusterThreads; ++k) {
+      if (k >= rounds) break;
+      const uint32_t i = first + 32 * k;
+      const uint32_t digit = i < left ? from[i].x >> shift & (digits - 1) : digits;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
+      const uint32_t before = __popc(same & ((1u << lane) - 1u));
+      ranks[k] = i < left ? sh.count[warp][digit] + before : 0u;
+      __syncwarp();
+      if (i < left && before == 0) sh.count[warp][digit] += (uint16_t)__popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (threadIdx.x < digits) {  // a digit's warps one behind another
+      uint32_t sum = 0;
+#pragma unroll 8
+      for (int w = 0; w < kClusterWarps; ++w) {
+        const uint32_t c = sh.count[w][threadIdx.x];
+        sh.count[w][threadIdx.x] = (uint16_t)sum;
+        sum += c;
+      }
+      sh.all[threadIdx.x] = sum;
+    }
+    if (s.ctas > 1) cluster_sync();
+    else __syncthreads();
+    // a digit's CTAs one behind another, behind the lower digits of all
+    uint32_t total = 0, lower = 0;
+    if (threadIdx.x < digits) {
+      for (int c = 0; c < s.ctas; ++c) {
+        const uint32_t v = s.ctas > 1 ? ld_cluster(in_cta(&sh.all[threadIdx.x], c)) : sh.all[threadIdx.x];
+        if (c < (int)rank) lower += v;
+        total += v;
+      }
+    }
+    uint32_t of_warp;
+    const uint32_t before = warp_before(total, of_warp);
+    if (lane == 0) sh.sums[warp] = of_warp;
+    __syncthreads();
+    uint32_t ignored;
+    const uint32_t part = warp_before(sh.sums[lane], ignored);
+    const uint32_t below = __shfl_sync(0xFFFFFFFFu, part, warp);  // (whole warps, however few the digits)
+    if (threadIdx.x < digits) sh.base[threadIdx.x] = lower + before + below;
+    __syncthreads();
+    const bool last = pass + 1 == s.passes;
+#pragma unroll
+    for (uint32_t k = 0; k < kClusterPer / kClusterThreads; ++k) {
+      if (k >= rounds) break;
+      const uint32_t i = first + 32 * k;
+      if (i >= left) break;
+      const uint2 v = from[i];
+      const uint32_t digit = v.x >> shift & (digits - 1);
+      const uint32_t at = sh.base[digit] + sh.count[warp][digit] + ranks[k];
+      if (last) s.keys[at] = v.x, s.pos[at] = v.y;
+      else if (s.ctas > 1) st_cluster(in_cta(to + at % s.per, at / s.per), v);
+      else to[at] = v;
+    }
+    if (s.ctas > 1) cluster_sync();  // (also: nobody leaves while its counts may be read)
+    else __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- gradient --
+
+// The sorted rows of dy are summed in segments of `seg` consecutive places, a
+// warp 256 columns of one segment, so that a token that fills half the batch
+// takes no longer than any other half.  A token's run that lies within a
+// segment is finished there; of a run that crosses into the next ones, every
+// segment leaves its part in the workspace -- slot 0 where the run came in from
+// the segment before, slot 1 where it begins -- and the join adds the parts in
+// order.
+//
+// The first CTAs of the launch clear the rows of the table that no token of
+// the batch has -- most of the gradient's bytes, as a rule.  They look for the
+// tokens in the batch itself and do not wait for the sort, which thus takes
+// next to no time of its own; for a batch that is longer than a cluster sorts,
+// they search the sorted tokens instead.
+constexpr int kSumThreads = 512;
+constexpr int kSumWarps = kSumThreads / 32;
+constexpr int kBitRows = 1 << 15;  // rows of the table that a CTA looks after at a time
+
+struct Clear {
+  uint8_t* table;
+  int64_t row_bytes, pitch_bytes;
+  int by_search;
+  uint32_t ctas;
+};
+
+struct Segments {
+  const uint32_t *keys, *pos;
+  float* parts;  // [segment][slot][cols]
+  uint32_t n, seg, count, slabs;
+};
+
+// A lane's eight columns of a slab: neighbours where vectors are aligned, every
+// 32nd column otherwise, so that a warp's loads of single elements are whole
+// sectors.
+template <bool kVec>
+struct Columns {
+  int64_t first, cols;
+  __device__ __forceinline__ int64_t at(int j) const { return kVec ? first + j : first + 32 * j; }
+  __device__ __forceinline__ bool in(int j) const { return at(j) < cols; }
+};
+template <bool kVec>
+__device__ __forceinline__ Columns<kVec> columns_of(uint32_t slab, int64_t cols) {
   const int lane = threadIdx.x & 31;
-  for (int64_t u = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
-    const int64_t row = u / per_row, col = (u - row * per_row) * 256 + lane * 8, n = a.cols - col;
-    const uint32_t lo = starts[row], hi = starts[row + 1];
-    if (a.accumulate && lo == hi) continue;
-    float acc[8], v[8];
+  return {256ll * slab + (kVec ? 8 * lane : lane), cols};
+}
+
+template <bool kVec, class V>
+__device__ __forceinline__ void load_columns(V& x, const typename V::raw* row, const Columns<kVec>& c) {
+  if constexpr (kVec) {
+    load8(x, row + c.first, c.cols - c.first, 1);
+  } else {
+    typename V::raw e[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-    for (uint32_t i = lo; i < hi; ++i) {
-      V x;
-      load8(x, static_cast<const typename V::raw*>(a.dy) + (int64_t)pos[i] * a.ld_dy + col, n, vec);
-      x.values(v);
+    for (int j = 0; j < 8; ++j) e[j] = c.in(j) ? __ldcs(row + c.at(j)) : typename V::raw(0);
+    if constexpr (sizeof(typename V::raw) == 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], v[j]);
+      for (int j = 0; j < 4; ++j) x.w[j] = pack2(e[2 * j], e[2 * j + 1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x.x[j] = e[j];
     }
+  }
+}
+
+template <class T, bool kVec>
+__device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64_t row, const Columns<kVec>& c,
+                                           const float (&sum)[8]) {
+  using raw = typename T::raw;
+  raw* out = static_cast<raw*>(a.dtable) + row * a.ld;
+  float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = __fmul_rn(acc[j], a.scale);
-    raw* out = static_cast<raw*>(a.dtable) + row * a.ld + col;
-    if (a.accumulate) {
-      typename T::V x;
-      load8(x, out, n, vec);
-      x.values(v);
+  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(sum[j], a.scale);
+  if (a.accumulate) {
+    typename T::V x;
+    float u[8];
+    load_columns<kVec>(x, out, c);
+    x.values(u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], v[j]);
+    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
+  }
+  if constexpr (kVec) {
+    store8<T>(out + c.first, v, c.cols - c.first, 1);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c.in(j)) out[c.at(j)] = T::rn(v[j]);
+  }
+}
+
+// One warp clears `bytes` bytes at p, an element's multiple.
+__device__ __forceinline__ void clear_row(uint8_t* p, int64_t bytes) {
+  const int lane = threadIdx.x & 31;
+  const int64_t head = min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15u), bytes);
+  if (2 * lane < head) *reinterpret_cast<uint16_t*>(p + 2 * lane) = 0;
+  p += head, bytes -= head;
+  for (int64_t i = 16 * lane; i + 16 <= bytes; i += 512) __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(0u, 0u, 0u, 0u));
+  const int64_t body = bytes & ~15ll;
+  if (body + 2 * lane < bytes) *reinterpret_cast<uint16_t*>(p + body + 2 * lane) = 0;
+}
+
+// A CTA's share of the rows without a token.
+__device__ __forceinline__ void clear_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, uint32_t* bits) {
+  const int64_t each = (a.vocab + z.ctas - 1) / z.ctas;
+  const int64_t end = min(a.vocab, (int64_t)(blockIdx.x + 1) * each);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (z.by_search) pdl_wait();
+  for (int64_t lo = blockIdx.x * each; lo < end; lo += kBitRows) {
+    const uint32_t rows = (uint32_t)min(end - lo, (int64_t)kBitRows);
+    if (z.by_search) {
+      for (uint32_t r = threadIdx.x; r < (rows + 31) / 32 * 32; r += kSumThreads) {
+        const uint32_t v = (uint32_t)lo + r;
+        uint32_t x = 0, y = g.n;
+        while (x < y) {
+          const uint32_t mid = x + (y - x) / 2;
+          if (g.keys[mid] < v) x = mid + 1;
+          else y = mid;
+        }
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, x < g.n && g.keys[x] == v);
+        if (lane == 0) bits[r >> 5] = word;
+      }
+    } else {
+      for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSumThreads) bits[i] = 0;
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < g.n; i += kSumThreads) {
+        const uint64_t at = (uint64_t)token_at(a.tokens, a.token_bytes, i) - (uint64_t)lo;
+        if (at < rows) atomicOr(&bits[at >> 5], 1u << (at & 31));
+      }
     }
-    store8<T>(out, acc, n, vec);
+    __syncthreads();
+    for (uint32_t r = warp; r < rows; r += kSumWarps)
+      if (!(bits[r >> 5] >> (r & 31) & 1u)) clear_row(z.table + (lo + r) * z.pitch_bytes, z.row_bytes);
+    __syncthreads();
+  }
+}
+
+template <bool kVec>
+__device__ __forceinline__ float* part_at(const Segments& g, uint32_t segment, int slot, int64_t cols) {
+  return g.parts + (2ll * segment + slot) * cols;
+}
+
+template <class V, class T, bool kVec>
+__global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
+                                                                         const __grid_constant__ Segments g,
+                                                                         const __grid_constant__ Clear z,
+                                                                         const FastDiv by_slabs) {
+  constexpr int kAhead = 8;  // rows whose loads are out at a time
+  __shared__ uint32_t bits[kBitRows / 32];
+  pdl_trigger();
+  if (blockIdx.x < z.ctas) clear_rows(a, g, z, bits);
+  pdl_wait();  // every CTA: what follows this launch relies on the sort's being over too
+  if (blockIdx.x < z.ctas) return;
+  const int lane = threadIdx.x & 31;
+  const uint32_t u = (blockIdx.x - z.ctas) * kSumWarps + (threadIdx.x >> 5);
+  if (u >= g.count * g.slabs) return;
+  const uint32_t segment = div_by(u, by_slabs), slab = u - segment * g.slabs;
+  const uint32_t lo = segment * g.seg, hi = min(lo + g.seg, g.n);
+  const Columns<kVec> c = columns_of<kVec>(slab, a.cols);
+  const uint32_t vocab = (uint32_t)a.vocab;
+  uint32_t current = g.keys[lo];
+  if (current == vocab) return;  // padding from here on
+  bool inside = lo > 0 && g.keys[lo - 1] == current;  // the run came in from the segment before
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+  auto flush = [&](bool goes_on) {
+    if (!inside && !goes_on) {
+      finish_row<T, kVec>(a, current, c, acc);
+    } else {
+      float* p = part_at<kVec>(g, segment, inside ? 0 : 1, a.cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c.in(j)) p[c.at(j)] = acc[j];
+    }
+  };
+  bool padding = false;
+  for (uint32_t at = lo; at < hi && !padding; at += 32) {
+    const uint32_t many = min(hi - at, 32u);
+    const uint32_t key = (uint32_t)lane < many ? g.keys[at + lane] : vocab;
+    const uint32_t pos = (uint32_t)lane < many ? g.pos[at + lane] : 0u;
+    for (uint32_t i = 0; i < many && !padding; i += kAhead) {
+      V x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t p = __shfl_sync(0xFFFFFFFFu, pos, (i + k) & 31);
+        if (__shfl_sync(0xFFFFFFFFu, key, (i + k) & 31) != vocab)
+          load_columns<kVec>(x[k], static_cast<const typename V::raw*>(a.dy) + (int64_t)p * a.ld_dy, c);
+        else x[k].clear();
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t next = __shfl_sync(0xFFFFFFFFu, key, (i + k) & 31);
+        if (padding || i + k >= many) continue;
+        if (next != current) {
+          flush(false);
+          inside = false;
+          current = next;
+          padding = next == vocab;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+        }
+        float v[8];
+        x[k].values(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], v[j]);
+      }
+    }
+  }
+  if (!padding) flush(hi < g.n && g.keys[hi] == current);
+}
+
+// A warp looks after the run that begins in its segment and crosses into the
+// next; runs over more than kShort segments are added by the whole CTA, an
+// eighth of the parts a warp.
+constexpr uint32_t kShort = 16;
+
+template <bool kVec>
+__device__ __forceinline__ void add_parts(const Segments& g, uint32_t from, uint32_t to, const Columns<kVec>& c,
+                                          float (&acc)[8]) {
+#pragma unroll 4
+  for (uint32_t s = from; s < to; ++s) {
+    const float* p = part_at<kVec>(g, s, 0, c.cols);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c.in(j)) acc[j] = __fadd_rn(acc[j], __ldcg(p + c.at(j)));
+  }
+}
+
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
+                                                                     const __grid_constant__ Segments g) {
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ uint32_t ends[kWarps];
+  __shared__ float sums[kWarps][8][32];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t slab = blockIdx.x % g.slabs, first = blockIdx.x / g.slabs * kWarps, segment = first + warp;
+  const Columns<kVec> c = columns_of<kVec>(slab, a.cols);
+  // the segment after the last of my run; 0: no run of mine
+  uint32_t end = 0, key = 0;
+  if (segment + 1 < g.count) {
+    const uint32_t lo = segment * g.seg, hi = lo + g.seg;
+    key = g.keys[hi - 1];
+    const bool begins = g.keys[lo] != key || lo == 0 || g.keys[lo - 1] != key;
+    if (begins && key != (uint32_t)a.vocab && g.keys[hi] == key) {
+      uint32_t x = hi, y = g.n;  // the run's end
+      while (x < y) {
+        const uint32_t mid = x + (y - x) / 2;
+        if (g.keys[mid] == key) x = mid + 1;
+        else y = mid;
+      }
+      end = (x - 1) / g.seg + 1;
+    }
+  }
+  const bool is_long = end && end - segment > kShort;
+  if (lane == 0) ends[warp] = is_long ? end : 0;
+  float acc[8];
+  if (end) {
+    const float* p = part_at<kVec>(g, segment, 1, a.cols);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = c.in(j) ? __ldcg(p + c.at(j)) : 0.0f;
+    if (!is_long) {
+      add_parts<kVec>(g, segment + 1, end, c, acc);
+      finish_row<T, kVec>(a, key, c, acc);
+    }
+  }
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) {
+    const uint32_t to = ends[w];
+    if (!to) continue;
+    const uint32_t from = first + w + 1, each = (to - from + kWarps - 1) / kWarps;
+    float part[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[j] = 0.0f;
+    add_parts<kVec>(g, min(from + warp * each, to), min(from + (warp + 1) * each, to), c, part);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[warp][j][lane] = part[j];
+    __syncthreads();
+    if (warp == w) {
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], sums[k][j][lane]);
+      finish_row<T, kVec>(a, key, c, acc);
+    }
+    __syncthreads();
   }
 }
 
@@ -284,49 +663,85 @@ cudaError_t lookup(const EmbeddingArgs& a, int sm_count, cudaStream_t s) {
   }
 }
 
-template <class V, class T>
-cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const uint32_t* starts, const uint32_t* pos, int sm_count,
-                     cudaStream_t s) {
-  const int64_t per = (a.cols + 255) / 256;
-  const int vec = aligned(a.dy, a.ld_dy * element_bytes(a.type)) && aligned(a.dtable, a.ld * element_bytes(a.dtable_type));
-  embedding_sum_kernel<V, T><<<cap_grid((per * a.vocab + 7) / 8, kWaves * sm_count), kRowThreads, 0, s>>>(
-      a, starts, pos, (uint32_t)per, vec);
-  return cudaGetLastError();
+template <class V, class T, bool kVec>
+cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, cudaStream_t s) {
+  const int64_t units = (int64_t)g.count * g.slabs;
+  if (units > 0x7FFFFFF0ll) return cudaErrorInvalidValue;
+  cudaError_t e = launch_kernel(embedding_segments_kernel<V, T, kVec>, (int)(z.ctas + (units + kSumWarps - 1) / kSumWarps),
+                                kSumThreads, 0, s, true, a, g, z, fast_div(g.slabs));
+  if (e != cudaSuccess || g.count == 1) return e;
+  return launch_kernel(embedding_join_kernel<T, kVec>, (int)((g.count + 7) / 8 * g.slabs), kRowThreads, 0, s, true, a, g);
 }
 
 template <class V>
-cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const uint32_t* starts, const uint32_t* pos, int sm_count,
-                     cudaStream_t s) {
+cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, cudaStream_t s) {
+  const bool vec = aligned(a.dy, a.ld_dy * element_bytes(a.type)) && aligned(a.dtable, a.ld * element_bytes(a.dtable_type));
   switch (a.dtable_type) {
-    case kMxBf16: return sum_rows<V, TBf16>(a, starts, pos, sm_count, s);
-    case kMxF16: return sum_rows<V, TF16>(a, starts, pos, sm_count, s);
-    case kMxF32: return sum_rows<V, TF32>(a, starts, pos, sm_count, s);
+    case kMxBf16: return vec ? sum_rows<V, TBf16, true>(a, g, z, s) : sum_rows<V, TBf16, false>(a, g, z, s);
+    case kMxF16: return vec ? sum_rows<V, TF16, true>(a, g, z, s) : sum_rows<V, TF16, false>(a, g, z, s);
+    case kMxF32: return vec ? sum_rows<V, TF32, true>(a, g, z, s) : sum_rows<V, TF32, false>(a, g, z, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
-// The workspace: two sets of keys and positions, the counts, the starts.
+// Places of a segment: 32 keeps many warps busy; of a long batch 128, so that
+// the parts take a sixteenth of dy's elements' number, not a quarter.
+uint32_t segment_of(int64_t n) { return n <= kClusterMax ? 32 : 128; }
+
+// The workspace: keys and positions (two sets and the counts for the sort of a
+// long batch), the segments' parts.
 struct Space {
-  int64_t keys[2], pos[2], counts, starts, bytes;
+  int64_t keys[2], pos[2], counts, parts, bytes;
 };
-Space space_of(int64_t n, int64_t vocab) {
-  Space p;
+Space space_of(int64_t n, int64_t cols) {
+  Space p = {};
   int64_t at = 0;
   auto part = [&](int64_t words) {
     const int64_t here = at;
     at += (4 * words + 15) / 16 * 16;
     return here;
   };
-  for (int k = 0; k < 2; ++k) p.keys[k] = part(n), p.pos[k] = part(n);
-  p.counts = part(kDigits * ((n + kChunk - 1) / kChunk));
-  p.starts = part(vocab + 1);
+  const bool is_long = n > kClusterMax;
+  for (int k = 0; k < (is_long ? 2 : 1); ++k) p.keys[k] = part(n), p.pos[k] = part(n);
+  if (is_long) p.counts = part(kDigits * ((n + kChunk - 1) / kChunk));
+  const int64_t seg = segment_of(n), count = (n + seg - 1) / seg;
+  p.parts = part(count > 1 ? 2 * count * cols : 0);
   p.bytes = at;
   return p;
 }
 
+int bits_of(int64_t v) {
+  int b = 0;
+  while (v >> b) ++b;
+  return b;
+}
+
+cudaError_t sort_in_cluster(ClusterSort c, cudaStream_t s) {
+  const int64_t thousands = (c.n + kClusterThreads - 1) / kClusterThreads;
+  c.ctas = thousands <= 1 ? 1 : thousands <= 2 ? 2 : thousands <= 4 ? 4 : kClusterCtas;
+  c.per = (uint32_t)((thousands + c.ctas - 1) / c.ctas) * kClusterThreads;
+  const int bits = bits_of(c.vocab);
+  c.passes = std::max(1, (bits + kClusterBits - 1) / kClusterBits);
+  c.bits = std::max(1, (bits + c.passes - 1) / c.passes);
+  const int smem = (int)sizeof(ClusterShared) + 2 * (int)c.per * 8;
+  const cudaError_t e = cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kClusterSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c.ctas);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)c.ctas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sort_cluster_kernel, c);
+}
+
 }  // namespace
 
-int64_t embedding_backward_workspace(int64_t n, int64_t vocab, int64_t) { return space_of(n, vocab).bytes; }
+int64_t embedding_backward_workspace(int64_t n, int64_t cols) { return space_of(n, cols).bytes; }
 
 cudaError_t launch_embedding(const EmbeddingArgs& a, int sm_count, cudaStream_t s) {
   if (a.from.codes) return lookup<Mx4Rows>(a, sm_count, s);
@@ -339,33 +754,56 @@ cudaError_t launch_embedding(const EmbeddingArgs& a, int sm_count, cudaStream_t 
 }
 
 cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_count, cudaStream_t s) {
-  const Space p = space_of(a.n, a.vocab);
+  const Space p = space_of(a.n, a.cols);
   uint8_t* base = static_cast<uint8_t*>(a.workspace);
   auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(base + at); };
-  Sort sort = {};
-  sort.tokens = a.tokens, sort.token_bytes = a.token_bytes;
-  sort.vocab = a.vocab;
-  sort.n = (uint32_t)a.n;
-  sort.chunks = (uint32_t)((a.n + kChunk - 1) / kChunk);
-  sort.counts = words(p.counts);
-  int out = 0;
-  for (int shift = 0; shift == 0 || a.vocab >> shift; shift += 8, out ^= 1) {
-    sort.shift = shift;
-    sort.keys_out = words(p.keys[out]), sort.pos_out = words(p.pos[out]);
-    sort_count_kernel<<<sort.chunks, kSortThreads, 0, s>>>(sort);
-    sort_scan_kernel<<<1, 1024, 0, s>>>(sort.counts, kDigits * sort.chunks);
-    sort_place_kernel<<<sort.chunks, kSortThreads, 0, s>>>(sort);
-    sort.tokens = nullptr;
-    sort.keys_in = sort.keys_out, sort.pos_in = sort.pos_out;
+  Segments g = {};
+  g.n = (uint32_t)a.n;
+  g.seg = segment_of(a.n);
+  g.count = (uint32_t)((a.n + g.seg - 1) / g.seg);
+  g.slabs = (uint32_t)((a.cols + 255) / 256);
+  g.parts = reinterpret_cast<float*>(base + p.parts);
+  ClusterSort c = {};
+  c.tokens = a.tokens, c.token_bytes = a.token_bytes;
+  c.n = (uint32_t)a.n, c.vocab = (uint32_t)a.vocab;
+  Clear z = {};
+  if (!a.accumulate) {
+    z.table = static_cast<uint8_t*>(a.dtable);
+    z.row_bytes = a.cols * element_bytes(a.dtable_type);
+    z.pitch_bytes = a.ld * element_bytes(a.dtable_type);
+    z.by_search = a.n > kClusterMax;
+    z.ctas = (uint32_t)std::min<int64_t>(sm_count, (a.vocab + kSumWarps - 1) / kSumWarps);
   }
-  embedding_starts_kernel<<<(unsigned)((a.vocab + 256) / 256), 256, 0, s>>>(sort.keys_in, sort.n, (uint32_t)a.vocab,
-                                                                             words(p.starts));
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (a.n <= kClusterMax) {
+    c.keys = words(p.keys[0]), c.pos = words(p.pos[0]);
+    e = sort_in_cluster(c, s);
+  } else {
+    Sort sort = {};
+    sort.tokens = a.tokens, sort.token_bytes = a.token_bytes;
+    sort.vocab = a.vocab;
+    sort.n = (uint32_t)a.n;
+    sort.chunks = (uint32_t)((a.n + kChunk - 1) / kChunk);
+    sort.counts = words(p.counts);
+    int out = 0;
+    for (int shift = 0; shift == 0 || a.vocab >> shift; shift += 8, out ^= 1) {
+      sort.shift = shift;
+      sort.keys_out = words(p.keys[out]), sort.pos_out = words(p.pos[out]);
+      sort_count_kernel<<<sort.chunks, kSortThreads, 0, s>>>(sort);
+      sort_scan_kernel<<<1, 1024, 0, s>>>(sort.counts, kDigits * sort.chunks);
+      sort_place_kernel<<<sort.chunks, kSortThreads, 0, s>>>(sort);
+      sort.tokens = nullptr;
+      sort.keys_in = sort.keys_out, sort.pos_in = sort.pos_out;
+    }
+    c.keys = sort.keys_out, c.pos = sort.pos_out;
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
+  g.keys = c.keys, g.pos = c.pos;
   switch (a.type) {
-    case kMxBf16: return sum_rows<Vec16<Bf16>>(a, words(p.starts), sort.pos_in, sm_count, s);
-    case kMxF16: return sum_rows<Vec16<F16>>(a, words(p.starts), sort.pos_in, sm_count, s);
-    case kMxF32: return sum_rows<Vec32>(a, words(p.starts), sort.pos_in, sm_count, s);
+    case kMxBf16: return sum_rows<Vec16<Bf16>>(a, g, z, s);
+    case kMxF16: return sum_rows<Vec16<F16>>(a, g, z, s);
+    case kMxF32: return sum_rows<Vec32>(a, g, z, s);
     default: return cudaErrorInvalidValue;
   }
 }

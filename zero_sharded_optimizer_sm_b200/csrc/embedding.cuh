@@ -42,6 +42,6 @@ struct EmbeddingBackwardArgs {
 
 cudaError_t launch_embedding(const EmbeddingArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_count, cudaStream_t s);
-int64_t embedding_backward_workspace(int64_t n, int64_t vocab, int64_t cols);
+int64_t embedding_backward_workspace(int64_t n, int64_t cols);
 
 }  // namespace zsm

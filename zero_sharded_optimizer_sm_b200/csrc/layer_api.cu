@@ -193,7 +193,7 @@ zero_status zero_embedding_backward_workspace(int64_t n, int64_t vocab, int64_t 
   *bytes = 0;
   if (n < 0 || vocab < 0 || cols < 0 || n > kMaxDim || vocab > kMaxDim || cols > kMaxDim)
     return fail(ZERO_EINVAL, "%lld tokens, %lld x %lld: out of range", (long long)n, (long long)vocab, (long long)cols);
-  if (n && vocab && cols) *bytes = zsm::embedding_backward_workspace(n, vocab, cols);
+  if (n && vocab && cols) *bytes = zsm::embedding_backward_workspace(n, cols);
   return ZERO_OK;
 }
 
@@ -209,7 +209,7 @@ zero_status zero_embedding_backward(const void* dy, int32_t dtype, int64_t n, in
   if (vocab == 0 || cols == 0) return ZERO_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n == 0) return accumulate ? ZERO_OK : zero_fill(dtable, dtable_dtype, vocab, cols, ld, s);
-  if ((st = check_workspace(workspace, workspace_bytes, zsm::embedding_backward_workspace(n, vocab, cols))) != ZERO_OK)
+  if ((st = check_workspace(workspace, workspace_bytes, zsm::embedding_backward_workspace(n, cols))) != ZERO_OK)
     return st;
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
