@@ -947,8 +947,9 @@ zero_status zero_mx4_reduce_scatter(zero_ctx* ctx, int64_t lo, int64_t hi, const
  * holds for them: errors through zero_last_error(NULL), matrices on the current
  * CUDA device, no state between calls, captures allowed, empty matrices
  * accepted.  Outputs must not overlap inputs or one another, except where a
- * call says so.  Sums over a row or a batch are held in binary32, in an order
- * that depends on the sizes alone: the same bits on every run.
+ * call says so.  Sums over a row or a batch are held in binary32 or more, in an
+ * order that depends on the sizes and on the matrices' alignment alone: the
+ * same bits on every run.
  */
 #define ZERO_MX8_BLOCK 32
 

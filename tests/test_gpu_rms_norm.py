@@ -81,7 +81,7 @@ def test_norm_of_strided_rows_in_place_and_one_result_alone(z, dtype, cols):
         space = normal(rows + 1, cols + pad, dtype, 3).flatten()
         x = space[off:off + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
         r, w = normal(rows, cols, dtype, 4), _weight(cols, dtype)
-        want = z.rms_norm(x.contiguous(), w, residual=r)
+        want = _check(z, x, r, w)
         # one result at a time
         assert torch.equal(z.rms_norm(x, w, residual=r, h=False, rstd=False).y, want.y)
         only = z.rms_norm(x, w, residual=r, y=False, rstd=False)
@@ -176,7 +176,7 @@ def test_norm_backward_of_strided_rows_and_in_place(z, dtype, cols):
         dy = space[off:off + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
         h, dh, w = normal(rows, cols, dtype, 4), normal(rows, cols, dtype, 5, 0.1), _weight(cols, dtype)
         rstd = ref.norm(h, w, 1e-6)[1].float()
-        want_dx, want_dw = z.rms_norm_backward(dy.contiguous(), h, w, rstd, dh=dh)
+        want_dx, want_dw = _check_backward(z, dy, h, w, dh)
         over = dh.clone()
         dx, dw = z.rms_norm_backward(dy, h, w, rstd, dh=over, dx=over)
         assert dx is over and torch.equal(dx, want_dx) and torch.equal(dw, want_dw)

@@ -8,7 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "embedding.cuh"
-#include "mx4_quant.cuh"
+#include "rows.cuh"
 
 namespace zsm {
 namespace {
@@ -379,41 +379,12 @@ struct Segments {
   uint32_t n, seg, count, slabs;
 };
 
-// A lane's eight columns of a slab: neighbours where vectors are aligned, every
-// 32nd column otherwise, so that a warp's loads of single elements are whole
-// sectors.
+// A warp's 256 columns.
 template <bool kVec>
-struct Columns {
-  int64_t first, cols;
-  __device__ __forceinline__ int64_t at(int j) const { return kVec ? first + j : first + 32 * j; }
-  __device__ __forceinline__ bool in(int j) const { return at(j) < cols; }
-};
-template <bool kVec>
-__device__ __forceinline__ Columns<kVec> columns_of(uint32_t slab, int64_t cols) {
-  const int lane = threadIdx.x & 31;
-  return {256ll * slab + (kVec ? 8 * lane : lane), cols};
-}
-
-template <bool kVec, class V>
-__device__ __forceinline__ void load_columns(V& x, const typename V::raw* row, const Columns<kVec>& c) {
-  if constexpr (kVec) {
-    load8(x, row + c.first, c.cols - c.first, 1);
-  } else {
-    typename V::raw e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = c.in(j) ? __ldcs(row + c.at(j)) : typename V::raw(0);
-    if constexpr (sizeof(typename V::raw) == 2) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x.w[j] = pack2(e[2 * j], e[2 * j + 1]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x.x[j] = e[j];
-    }
-  }
-}
+using Slab = Columns<kVec, 32>;
 
 template <class T, bool kVec>
-__device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64_t row, const Columns<kVec>& c,
+__device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64_t row, const Slab<kVec>& c,
                                            const float (&sum)[8]) {
   using raw = typename T::raw;
   raw* out = static_cast<raw*>(a.dtable) + row * a.ld;
@@ -423,18 +394,12 @@ __device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64
   if (a.accumulate) {
     typename T::V x;
     float u[8];
-    load_columns<kVec>(x, out, c);
+    load_columns(x, out, c);
     x.values(u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
   }
-  if constexpr (kVec) {
-    store8<T>(out + c.first, v, c.cols - c.first, 1);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c.in(j)) out[c.at(j)] = T::rn(v[j]);
-  }
+  store_columns<T>(out, c, v);
 }
 
 // One warp clears `bytes` bytes at p, an element's multiple.
@@ -504,7 +469,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
   if (u >= g.count * g.slabs) return;
   const uint32_t segment = div_by(u, by_slabs), slab = u - segment * g.slabs;
   const uint32_t lo = segment * g.seg, hi = min(lo + g.seg, g.n);
-  const Columns<kVec> c = columns_of<kVec>(slab, a.cols);
+  const Slab<kVec> c(256ll * slab, lane, a.cols);
   const uint32_t vocab = (uint32_t)a.vocab;
   uint32_t current = g.keys[lo];
   if (current == vocab) return;  // padding from here on
@@ -533,7 +498,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
       for (int k = 0; k < kAhead; ++k) {
         const uint32_t p = __shfl_sync(0xFFFFFFFFu, pos, (i + k) & 31);
         if (__shfl_sync(0xFFFFFFFFu, key, (i + k) & 31) != vocab)
-          load_columns<kVec>(x[k], static_cast<const typename V::raw*>(a.dy) + (int64_t)p * a.ld_dy, c);
+          load_columns(x[k], static_cast<const typename V::raw*>(a.dy) + (int64_t)p * a.ld_dy, c);
         else x[k].clear();
       }
 #pragma unroll
@@ -564,7 +529,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
 constexpr uint32_t kShort = 16;
 
 template <bool kVec>
-__device__ __forceinline__ void add_parts(const Segments& g, uint32_t from, uint32_t to, const Columns<kVec>& c,
+__device__ __forceinline__ void add_parts(const Segments& g, uint32_t from, uint32_t to, const Slab<kVec>& c,
                                           float (&acc)[8]) {
 #pragma unroll 4
   for (uint32_t s = from; s < to; ++s) {
@@ -584,7 +549,7 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t slab = blockIdx.x % g.slabs, first = blockIdx.x / g.slabs * kWarps, segment = first + warp;
-  const Columns<kVec> c = columns_of<kVec>(slab, a.cols);
+  const Slab<kVec> c(256ll * slab, lane, a.cols);
   // the segment after the last of my run; 0: no run of mine
   uint32_t end = 0, key = 0;
   if (segment + 1 < g.count) {

@@ -2,103 +2,65 @@
 //
 // Both are memory-bound: forward 2 to 4 values of the row's type and up to two
 // MX8 bytes an element, backward 3 or 4.  A row's elements are read once: they
-// stay in registers, as they were loaded, between the sum over the row and its
-// use.
+// stay in registers (forward) or shared memory (backward), as they were loaded,
+// between the sum over the row and its use.
 #include <cuda_runtime.h>
 
-#include "mx4_quant.cuh"
 #include "rms_norm.cuh"
+#include "rows.cuh"
 
 namespace zsm {
 namespace {
 
 using namespace mx;
 
-// n (at most 8) values of a vector of one of the three types, 0 past the end.
-__device__ __forceinline__ void weights8(const void* w, int type, int64_t at, int64_t n, int vec, float (&v)[8]) {
-  if (type == kMxF32) {
-    const float* p = static_cast<const float*>(w) + at;
-    if (n >= 8 && vec) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < n ? __ldg(p + j) : 0.0f;
-    }
-    return;
-  }
-  const uint16_t* p = static_cast<const uint16_t*>(w) + at;
-  uint32_t u[4];
-  if (n >= 8 && vec) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      u[j] = (2 * j < n ? (uint32_t)__ldg(p + 2 * j) : 0u) | (2 * j + 1 < n ? (uint32_t)__ldg(p + 2 * j + 1) << 16 : 0u);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = type == kMxF16 ? F16::lo(u[j]) : Bf16::lo(u[j]);
-    v[2 * j + 1] = type == kMxF16 ? F16::hi(u[j]) : Bf16::hi(u[j]);
-  }
-}
+// Threads to a block: a block of more than 32 threads to a row has one row.
+template <int kGroup>
+constexpr int kBlockOf = kGroup > 128 ? kGroup : 128;
 
-// Eight values rounded into a vector of a type.
-template <class F>
-__device__ __forceinline__ void round_to(Vec16<F>& x, const float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x.w[j] = Half<F>::pack(v[2 * j], v[2 * j + 1]);
-}
-__device__ __forceinline__ void round_to(Vec32& x, const float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x.x[j] = v[j];
-}
+// ----------------------------------------------------------------- forward --
 
 // Sum over the kGroup threads that share a row (a warp, or the whole block of
-// kGroup threads); every one of them gets the same bits.
+// kGroup threads), in binary64 from a thread's binary32 sum on: every thread
+// gets the same bits.
 template <int kGroup>
-__device__ __forceinline__ float group_sum(float v, float* smem) {
+__device__ __forceinline__ double group_sum(float mine, double* smem) {
+  double v = (double)mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = 16; o > 0; o >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   if constexpr (kGroup > 32) {
     constexpr int kWarps = kGroup / 32;
     const int lane = threadIdx.x & 31;
-    __syncthreads();  // the last call's values have been read
     if (lane == 0) smem[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = lane < kWarps ? smem[lane] : 0.0f;
+    v = lane < kWarps ? smem[lane] : 0.0;
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (int o = kWarps / 2; o > 0; o >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     v = __shfl_sync(0xFFFFFFFFu, v, 0);
   }
   return v;
 }
 
-__device__ __forceinline__ void store_mx8(const Mx8Matrix& m, int64_t row, int64_t col, int64_t nb, uint32_t s,
-                                          const float (&v)[8]) {
-  const int64_t b = col >> 5;
-  if (b >= nb) return;
-  *reinterpret_cast<uint2*>(m.codes + row * m.code_pitch + col) = encode8_mx8(v, s);
-  if ((col & 31) == 0) m.scales[row * m.scale_pitch + b] = (uint8_t)s;
+// (ss / cols + eps)^(-1/2), rounded once from binary64: the function's binary32
+// estimate and one Newton step, whose error is the square of the estimate's.
+// y's rounding to 16 and then to 8 bits turns on rstd's last bit now and then,
+// so it is the correctly rounded one but for sums next to a tie.
+__device__ __forceinline__ float rstd_of(double ss, double inv_cols, double eps) {
+  const double m = __fma_rn(ss, inv_cols, eps);
+  const float r = rsqrtf((float)m);
+  const double e = __fma_rn(-__dmul_rn(m, (double)r), (double)r, 1.0);
+  const float better = (float)__fma_rn(__dmul_rn(0.5, e), (double)r, (double)r);
+  return isfinite((float)m) ? better : r;
 }
 
-// ----------------------------------------------------------------- forward --
-
-// Threads to a block: a block of more than 32 threads to a row has one row.
-template <int kGroup>
-constexpr int kBlockOf = kGroup > 128 ? kGroup : 128;
-
-// The vectors of one row of h at a thread's column: x plus the residual,
-// rounded to their type.
-template <class T>
-__device__ __forceinline__ void load_h(const RmsNormArgs& a, int64_t row, int64_t col, int vec, typename T::V& x) {
+// A vector of one row of h: x plus the residual, rounded to their type.
+template <class T, class C>
+__device__ __forceinline__ void load_h(const RmsNormArgs& a, int64_t row, const C& c, typename T::V& x) {
   using raw = typename T::raw;
-  const int64_t n = a.cols - col;
-  load8(x, static_cast<const raw*>(a.x) + row * a.ld_x + col, n, vec);
+  load_columns(x, static_cast<const raw*>(a.x) + row * a.ld_x, c);
   if (a.residual) {
     typename T::V r;
-    load8(r, static_cast<const raw*>(a.residual) + row * a.ld_residual + col, n, vec);
+    load_columns(r, static_cast<const raw*>(a.residual) + row * a.ld_residual, c);
     float v[8], u[8];
     x.values(v);
     r.values(u);
@@ -115,209 +77,359 @@ __device__ __forceinline__ float square_sum(const float (&v)[8], float ss) {
 }
 
 // All results of one vector of h.  Called by whole warps.
-template <class T>
-__device__ __forceinline__ void finish(const RmsNormArgs& a, int64_t row, int64_t col, int64_t nb, int vec, float rstd,
+template <class T, class C>
+__device__ __forceinline__ void finish(const RmsNormArgs& a, int64_t row, const C& c, int64_t nb, float rstd,
                                        const typename T::V& x) {
   using raw = typename T::raw;
-  const int64_t n = a.cols - col;
   float v[8], w[8];
   x.values(v);
-  if (a.h) store8<T>(static_cast<raw*>(a.h) + row * a.ld_h + col, v, n, vec);
-  if (a.h8.codes) store_mx8(a.h8, row, col, nb, scale_code8(max_of_four(x.max_bits())), v);
-  weights8(a.weight, a.w_type, col, n, vec, w);
+  if (a.h) store_columns<T>(static_cast<raw*>(a.h) + row * a.ld_h, c, v);
+  if (a.h8.codes) store_columns8(a.h8, row, nb, c, x);
+  load_weights(a.weight, a.w_type, c, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], rstd), w[j]);
-  if (a.y) store8<T>(static_cast<raw*>(a.y) + row * a.ld_y + col, v, n, vec);
+  if (a.y) store_columns<T>(static_cast<raw*>(a.y) + row * a.ld_y, c, v);
   if (a.y8.codes) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!c.in(j)) v[j] = 0.0f;  // past the row: w is 0 there, but rstd need not be finite
     typename T::V y;
     round_to(y, v);
-    y.values(v);
-    if (n < 8) {  // past the row: w is 0 there, but rstd need not be finite
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j >= n) v[j] = 0.0f;
-      round_to(y, v);
-    }
-    store_mx8(a.y8, row, col, nb, scale_code8(max_of_four(y.max_bits())), v);
+    store_columns8(a.y8, row, nb, c, y);
   }
-}
-
-__device__ __forceinline__ float rstd_of(float ss, int64_t cols, float eps) {
-  return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)cols), eps)));
 }
 
 // kGroup threads to a row, kChunks vectors of eight elements a thread.
-template <class T, int kGroup, int kChunks>
-__global__ void __launch_bounds__(kBlockOf<kGroup>) rms_norm_kernel(const __grid_constant__ RmsNormArgs a, const int vec) {
+template <class T, bool kVec, int kGroup, int kChunks>
+__global__ void __launch_bounds__(kBlockOf<kGroup>) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
+                                                                    const double inv_cols) {
   constexpr int kRows = kBlockOf<kGroup> / kGroup;
-  __shared__ float smem[32];
+  __shared__ double smem[32];
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kGroup;
   if (row >= a.rows) return;  // whole groups
   const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
-  const int64_t c0 = 8 * (threadIdx.x % kGroup);
+  const int t = threadIdx.x % kGroup;
+  using C = Columns<kVec, kGroup>;
   typename T::V x[kChunks];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) load_h<T>(a, row, c0 + 8 * kGroup * c, vec, x[c]);
+  for (int k = 0; k < kChunks; ++k) load_h<T>(a, row, C(8 * kGroup * k, t, a.cols), x[k]);
   float ss = 0.0f;
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
+  for (int k = 0; k < kChunks; ++k) {
     float v[8];
-    x[c].values(v);
+    x[k].values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<kGroup>(ss, smem), a.cols, a.eps);
-  if (a.rstd && c0 == 0) a.rstd[row] = rstd;
+  const float rstd = rstd_of(group_sum<kGroup>(ss, smem), inv_cols, (double)a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = rstd;
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) finish<T>(a, row, c0 + 8 * kGroup * c, nb, vec, rstd, x[c]);
+  for (int k = 0; k < kChunks; ++k) finish<T>(a, row, C(8 * kGroup * k, t, a.cols), nb, rstd, x[k]);
 }
 
 // Rows too long for registers: read a second time (a thread reads its own
 // elements before it writes results in their place).
 constexpr int kLongThreads = 512;
-template <class T>
-__global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __grid_constant__ RmsNormArgs a, const int vec) {
-  __shared__ float smem[32];
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __grid_constant__ RmsNormArgs a,
+                                                                     const double inv_cols) {
+  __shared__ double smem[32];
   const int64_t row = blockIdx.x;
   const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
+  using C = Columns<kVec, kLongThreads>;
   float ss = 0.0f;
-  for (int64_t col = 8 * threadIdx.x; col < a.cols; col += 8 * kLongThreads) {
+  for (int64_t first = 0; first < a.cols; first += 8 * kLongThreads) {
     typename T::V x;
     float v[8];
-    load_h<T>(a, row, col, vec, x);
+    load_h<T>(a, row, C(first, threadIdx.x, a.cols), x);
     x.values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<kLongThreads>(ss, smem), a.cols, a.eps);
+  const float rstd = rstd_of(group_sum<kLongThreads>(ss, smem), inv_cols, (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-  for (int64_t first = 0; first < a.cols; first += 8 * kLongThreads) {  // whole warps take part
-    const int64_t col = first + 8 * threadIdx.x;
+  for (int64_t first = 0; first < a.cols; first += 8 * kLongThreads) {
     typename T::V x;
-    load_h<T>(a, row, col, vec, x);
-    finish<T>(a, row, col, nb, vec, rstd, x);
+    const C c(first, threadIdx.x, a.cols);
+    load_h<T>(a, row, c, x);
+    finish<T>(a, row, c, nb, rstd, x);
   }
 }
 
 // ---------------------------------------------------------------- backward --
 
-// A block's group walks over rows group, group + groups, ... and keeps its
-// columns' part of dw in registers; the parts go to the workspace, one row of
-// it a block, and a second kernel adds them in order.
-constexpr int64_t kParts = 592;          // blocks at most: 4 to an SM of 148
-constexpr int64_t kWideCols = 16384;     // longer rows go through memory twice
+// A block walks over rows block, block + blocks, ... and keeps its columns'
+// part of dw in registers; the parts go to the workspace, one row of it a
+// block, and a second kernel adds them in order.
+//
+// Rows whose vectors are aligned come through a ring in shared memory, kStages
+// rows deep, by asynchronous copies: each thread fetches the elements that it
+// reads itself, so that nothing but its own copies has to be waited for, and
+// the sum over a row -- the one place where the block's threads meet -- never
+// holds up the loads of the next ones.
+constexpr int64_t kSms = 148;
 
-int64_t parts_of(int64_t rows) { return std::max<int64_t>(1, std::min(rows, kParts)); }
+// Blocks at most, for rows of so many columns: as many as are there at a time.
+int64_t max_parts(int64_t cols) { return kSms * (cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1); }
+int64_t parts_of(int64_t rows, int64_t cols) { return std::max<int64_t>(1, std::min(rows, max_parts(cols))); }
 
-template <class T, bool kMx8>
-__device__ __forceinline__ void load_backward(const RmsNormBackwardArgs& a, int64_t row, int64_t col, int vec,
-                                              typename T::V& dy, float (&h)[8]) {
-  using raw = typename T::raw;
-  const int64_t n = a.cols - col;
-  load8(dy, static_cast<const raw*>(a.dy) + row * a.ld_dy + col, n, vec);
-  if constexpr (kMx8) {
-    uint2 w = make_uint2(0u, 0u);
-    uint32_t s = 0u;
-    if (n > 0) {
-      w = __ldcs(reinterpret_cast<const uint2*>(a.h8.codes + row * a.h8.code_pitch + col));
-      s = a.h8.scales[row * a.h8.scale_pitch + (col >> 5)];
-    }
-    values8_mx8(w, s, h);
-    if (n < 8) {
+// The longest rows that a block takes; longer ones go through memory twice.
+int64_t wide_from(int type) { return type == kMxF32 ? 8192 : 16384; }
+
+// Sum over the block (kGroup threads) in binary32; smem holds two rounds'
+// values, so that one barrier a round will do.
+template <int kGroup>
+__device__ __forceinline__ float block_sum(float v, float (*smem)[32], int round) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j >= n) h[j] = 0.0f;
+  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  constexpr int kWarps = kGroup / 32;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) smem[round & 1][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < kWarps ? smem[round & 1][lane] : 0.0f;
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+
+__device__ __forceinline__ float2 pair(const float (&v)[8], int p) { return make_float2(v[2 * p], v[2 * p + 1]); }
+
+// One vector's part of a row's sum of g xh, and of dw.
+__device__ __forceinline__ void add_vector(const float (&dy)[8], const float (&h)[8], const float (&w)[8], float rstd,
+                                           float2 (&acc)[4], float2& dot) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float2 xh = mul2(pair(h, p), make_float2(rstd, rstd));
+    dot = fma2(mul2(pair(dy, p), pair(w, p)), xh, dot);
+    acc[p] = fma2(pair(dy, p), xh, acc[p]);
+  }
+}
+
+// dx of one vector, without dh: rstd (g - xh mean).
+__device__ __forceinline__ void dx_vector(const float (&dy)[8], const float (&h)[8], const float (&w)[8], float rstd,
+                                          float mean, float (&v)[8]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float2 xh = mul2(pair(h, p), make_float2(rstd, rstd));
+    const float2 d = mul2(fma2(xh, make_float2(-mean, -mean), mul2(pair(dy, p), pair(w, p))), make_float2(rstd, rstd));
+    v[2 * p] = d.x, v[2 * p + 1] = d.y;
+  }
+}
+
+template <class C, class A>
+__device__ __forceinline__ void store_part(float* out, const C& c, const A& acc) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c.in(j)) out[c.at(j)] = j & 1 ? acc[j >> 1].y : acc[j >> 1].x;
+}
+
+// One row's stage of the ring: dy, h, dh of every thread's vectors, 16 bytes of
+// each thread next to another's.
+template <class T, int kGroup, int kChunks, bool kMx8, bool kDh>
+struct Ring {
+  using V = typename T::V;
+  using raw = typename T::raw;
+  static constexpr int kWords = sizeof(raw) / 2;                   // 16-byte words of a vector
+  static constexpr int kPlane = kGroup * kChunks * 16;             // bytes of one word of all vectors
+  static constexpr int kH = kWords * kPlane;                       // where h's begin
+  static constexpr int kD = kH + (kMx8 ? kPlane / 2 : kWords * kPlane);
+  static constexpr int kBytes = kD + (kDh ? kWords * kPlane : 0);
+  uint8_t* base;
+
+  __device__ __forceinline__ void fetch16(uint8_t* to, const void* matrix, int64_t row, int64_t ld, int64_t cols) const {
+    const raw* p = static_cast<const raw*>(matrix) + row * ld;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int v = kGroup * k + threadIdx.x;
+      if (8 * v >= cols) break;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) copy_async16(to + i * kPlane + 16 * v, p + 8 * v + 16 / (int)sizeof(raw) * i);
     }
+  }
+  // Asks for a row (none past the end; the group is there all the same).
+  __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, int64_t row, int stage) const {
+    if (row < a.rows) {
+      uint8_t* to = base + stage * kBytes;
+      fetch16(to, a.dy, row, a.ld_dy, a.cols);
+      if constexpr (kMx8) {
+        const uint8_t* p = a.h8.codes + row * a.h8.code_pitch;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const int v = kGroup * k + threadIdx.x;
+          if (8 * v < a.cols) copy_async8(to + kH + 8 * v, p + 8 * v);
+        }
+      } else {
+        fetch16(to + kH, a.h, row, a.ld_h, a.cols);
+      }
+      if constexpr (kDh) fetch16(to + kD, a.dh, row, a.ld_dh, a.cols);
+    }
+    copy_async_commit();
+  }
+  __device__ __forceinline__ void read16(int at, int stage, int k, float (&v)[8]) const {
+    const uint8_t* p = base + stage * kBytes + at + 16 * (kGroup * k + threadIdx.x);
+    V x;
+    uint4* w = reinterpret_cast<uint4*>(&x);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const uint4*>(p + i * kPlane);
+    x.values(v);
+  }
+  __device__ __forceinline__ void dy(int stage, int k, float (&v)[8]) const { read16(0, stage, k, v); }
+  __device__ __forceinline__ void dh(int stage, int k, float (&v)[8]) const { read16(kD, stage, k, v); }
+  __device__ __forceinline__ void h(int stage, int k, uint32_t scale, float (&v)[8]) const {
+    if constexpr (kMx8)
+      values8_mx8(*reinterpret_cast<const uint2*>(base + stage * kBytes + kH + 8 * (kGroup * k + threadIdx.x)), scale, v);
+    else read16(kH, stage, k, v);
+  }
+};
+
+// cols is a multiple of 8 here, and every row's vectors are aligned.
+template <class T, int kGroup, int kChunks, bool kMx8, bool kDh, int kStages>
+__global__ void __launch_bounds__(kGroup) rms_norm_backward_ring_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
+  using raw = typename T::raw;
+  using C = Columns<true, kGroup>;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ float smem[2][32];
+  pdl_trigger();
+  const Ring<T, kGroup, kChunks, kMx8, kDh> ring{ring_smem};
+  const int64_t step = gridDim.x;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) ring.fetch(a, blockIdx.x + s * step, s);
+  float2 acc[kChunks][4];
+  float w[kChunks][8];
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    if constexpr (kChunks == 1) load_weights(a.weight, a.w_type, C(0, threadIdx.x, a.cols), w[0]);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) acc[k][p] = make_float2(0.0f, 0.0f);
+  }
+  const float inv = __fdiv_rn(1.0f, (float)a.cols);
+  // the row's statistics and scales, a row ahead
+  float rstd = 0.0f, next_rstd = a.rstd[min((int64_t)blockIdx.x, a.rows - 1)];
+  uint32_t scale[kChunks] = {}, next_scale[kChunks] = {};
+  auto ahead = [&](int64_t row) {
+    if (row >= a.rows) return;
+    next_rstd = a.rstd[row];
+    if constexpr (kMx8) {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const int64_t col = 8 * (kGroup * k + threadIdx.x);
+        if (col < a.cols) next_scale[k] = a.h8.scales[row * a.h8.scale_pitch + (col >> 5)];
+      }
+    }
+  };
+  ahead(blockIdx.x);
+  int stage = 0, round = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += step, ++round) {
+    ring.fetch(a, row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    rstd = next_rstd;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) scale[k] = next_scale[k];
+    ahead(row + step);
+    copy_async_wait<kStages - 1>();
+    float2 dot = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const C c(8 * kGroup * k, threadIdx.x, a.cols);
+      if (c.first >= a.cols) break;
+      float dy[8], h[8];
+      ring.dy(stage, k, dy);
+      ring.h(stage, k, scale[k], h);
+      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, c, w[k]);
+      add_vector(dy, h, w[k], rstd, acc[k], dot);
+    }
+    const float mean = __fmul_rn(block_sum<kGroup>(__fadd_rn(dot.x, dot.y), smem, round), inv);
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const C c(8 * kGroup * k, threadIdx.x, a.cols);
+      if (c.first >= a.cols) break;
+      float dy[8], h[8], v[8];
+      ring.dy(stage, k, dy);
+      ring.h(stage, k, scale[k], h);
+      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, c, w[k]);
+      dx_vector(dy, h, w[k], rstd, mean, v);
+      if constexpr (kDh) {
+        float u[8];
+        ring.dh(stage, k, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
+      }
+      store_columns<T>(static_cast<raw*>(a.dx) + row * a.ld_dx, c, v);
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, a.cols), acc[k]);
+}
+
+// Rows of any alignment, straight from memory.
+template <class T, bool kMx8, class C>
+__device__ __forceinline__ void load_dy_h(const RmsNormBackwardArgs& a, int64_t row, const C& c, typename T::V& dy,
+                                          float (&h)[8]) {
+  using raw = typename T::raw;
+  load_columns(dy, static_cast<const raw*>(a.dy) + row * a.ld_dy, c);
+  if constexpr (kMx8) {
+    load_columns8(a.h8, row, c, h);
   } else {
     typename T::V x;
-    load8(x, static_cast<const raw*>(a.h) + row * a.ld_h + col, n, vec);
+    load_columns(x, static_cast<const raw*>(a.h) + row * a.ld_h, c);
     x.values(h);
   }
 }
 
-// dx of one vector: h here is xh, g = dy w.
-template <class T>
-__device__ __forceinline__ void store_dx(const RmsNormBackwardArgs& a, int64_t row, int64_t col, int vec, float rstd, float c,
-                                         const float (&xh)[8], const float (&g)[8]) {
+template <class T, class C>
+__device__ __forceinline__ void store_dx(const RmsNormBackwardArgs& a, int64_t row, const C& c, float (&v)[8]) {
   using raw = typename T::raw;
-  const int64_t n = a.cols - col;
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(rstd, __fmaf_rn(-xh[j], c, g[j]));
   if (a.dh) {
     typename T::V d;
     float u[8];
-    load8(d, static_cast<const raw*>(a.dh) + row * a.ld_dh + col, n, vec);
+    load_columns(d, static_cast<const raw*>(a.dh) + row * a.ld_dh, c);
     d.values(u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
   }
-  store8<T>(static_cast<raw*>(a.dx) + row * a.ld_dx + col, v, n, vec);
+  store_columns<T>(static_cast<raw*>(a.dx) + row * a.ld_dx, c, v);
 }
 
 template <class T, int kGroup, int kChunks, bool kMx8>
-__global__ void __launch_bounds__(kBlockOf<kGroup>) rms_norm_backward_kernel(const __grid_constant__ RmsNormBackwardArgs a,
-                                                                               const int vec) {
-  constexpr int kBlock = kBlockOf<kGroup>, kRows = kBlock / kGroup;
-  __shared__ float smem[32];
-  __shared__ float parts[kRows > 1 ? kRows * 8 * kGroup * kChunks : 1];
-  const int64_t c0 = 8 * (threadIdx.x % kGroup);
-  float acc[kChunks][8], w[kChunks][8];
+__global__ void __launch_bounds__(kGroup) rms_norm_backward_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
+  using C = Columns<false, kGroup>;
+  __shared__ float smem[2][32];
+  pdl_trigger();
+  float2 acc[kChunks][4];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    weights8(a.weight, a.w_type, c0 + 8 * kGroup * c, a.cols - (c0 + 8 * kGroup * c), vec, w[c]);
+  for (int k = 0; k < kChunks; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[c][j] = 0.0f;
-  }
+    for (int p = 0; p < 4; ++p) acc[k][p] = make_float2(0.0f, 0.0f);
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
-  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kGroup; row < a.rows; row += (int64_t)gridDim.x * kRows) {
+  int round = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++round) {
     typename T::V dy[kChunks];
-    float xh[kChunks][8];
+    float h[kChunks][8];
     const float rstd = a.rstd[row];
+    float2 dot = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) load_backward<T, kMx8>(a, row, c0 + 8 * kGroup * c, vec, dy[c], xh[c]);
-    float dot = 0.0f;
+    for (int k = 0; k < kChunks; ++k) load_dy_h<T, kMx8>(a, row, C(8 * kGroup * k, threadIdx.x, a.cols), dy[k], h[k]);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      float d[8];
-      dy[c].values(d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (c0 + 8 * kGroup * c + j < a.cols) xh[c][j] = __fmul_rn(xh[c][j], rstd);  // (past the row 0, whatever rstd is)
-        dot = __fmaf_rn(__fmul_rn(d[j], w[c][j]), xh[c][j], dot);
-        acc[c][j] = __fmaf_rn(d[j], xh[c][j], acc[c][j]);
-      }
+    for (int k = 0; k < kChunks; ++k) {
+      const C c(8 * kGroup * k, threadIdx.x, a.cols);
+      float d[8], w[8];
+      dy[k].values(d);
+      load_weights(a.weight, a.w_type, c, w);
+      add_vector(d, h[k], w, rstd, acc[k], dot);
     }
-    const float mean = __fmul_rn(group_sum<kGroup>(dot, smem), inv);
+    const float mean = __fmul_rn(block_sum<kGroup>(__fadd_rn(dot.x, dot.y), smem, round), inv);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      float g[8];
-      dy[c].values(g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], w[c][j]);
-      store_dx<T>(a, row, c0 + 8 * kGroup * c, vec, rstd, mean, xh[c], g);
+    for (int k = 0; k < kChunks; ++k) {
+      const C c(8 * kGroup * k, threadIdx.x, a.cols);
+      float d[8], w[8], v[8];
+      dy[k].values(d);
+      load_weights(a.weight, a.w_type, c, w);
+      dx_vector(d, h[k], w, rstd, mean, v);
+      store_dx<T>(a, row, c, v);
     }
   }
   float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
-  if constexpr (kRows > 1) {
-    constexpr int kCols = 8 * kGroup * kChunks;
-    float* mine = parts + (threadIdx.x / kGroup) * kCols;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mine[c0 + 8 * kGroup * c + j] = acc[c][j];
-    __syncthreads();
-    for (int col = threadIdx.x; col < kCols && col < a.cols; col += kBlock) {
-      float s = parts[col];
-#pragma unroll
-      for (int r = 1; r < kRows; ++r) s = __fadd_rn(s, parts[r * kCols + col]);
-      out[col] = s;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c0 + 8 * kGroup * c + j < a.cols) out[c0 + 8 * kGroup * c + j] = acc[c][j];
-  }
+  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, a.cols), acc[k]);
 }
 
 // Longer rows: the rows' dot products first (into the workspace's head), then
@@ -327,82 +439,96 @@ constexpr int kWideParts = 64;
 int64_t wide_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, kWideParts)); }
 int64_t dots_floats(int64_t rows) { return (rows + 3) / 4 * 4; }
 
-template <class T, bool kMx8>
-__global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __grid_constant__ RmsNormBackwardArgs a,
-                                                                     const int vec) {
-  __shared__ float smem[32];
+template <class T, bool kVec, bool kMx8>
+__global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
+  using C = Columns<kVec, kWideThreads>;
+  __shared__ float smem[2][32];
+  pdl_trigger();
   const int64_t row = blockIdx.x;
   const float rstd = a.rstd[row];
-  float dot = 0.0f;
-  for (int64_t col = 8 * threadIdx.x; col < a.cols; col += 8 * kWideThreads) {
+  float2 dot = make_float2(0.0f, 0.0f);
+  for (int64_t first = 0; first < a.cols; first += 8 * kWideThreads) {
+    const C c(first, threadIdx.x, a.cols);
+    if (!c.in(0)) break;
     typename T::V dy;
     float h[8], w[8], d[8];
-    load_backward<T, kMx8>(a, row, col, vec, dy, h);
-    weights8(a.weight, a.w_type, col, a.cols - col, vec, w);
+    float2 unused[4] = {};
+    load_dy_h<T, kMx8>(a, row, c, dy, h);
+    load_weights(a.weight, a.w_type, c, w);
     dy.values(d);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + j < a.cols) dot = __fmaf_rn(__fmul_rn(d[j], w[j]), __fmul_rn(h[j], rstd), dot);
+    add_vector(d, h, w, rstd, unused, dot);
   }
-  dot = group_sum<kWideThreads>(dot, smem);
-  if (threadIdx.x == 0) static_cast<float*>(a.workspace)[row] = dot;
+  const float all = block_sum<kWideThreads>(__fadd_rn(dot.x, dot.y), smem, 0);
+  if (threadIdx.x == 0) static_cast<float*>(a.workspace)[row] = all;
 }
 
-template <class T, bool kMx8>
+template <class T, bool kVec, bool kMx8>
 __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(const __grid_constant__ RmsNormBackwardArgs a,
-                                                                              const int64_t dots, const int vec) {
-  const int64_t col = 8 * ((int64_t)blockIdx.x * kWideThreads + threadIdx.x);
-  if (col >= a.cols) return;
-  float acc[8], w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-  weights8(a.weight, a.w_type, col, a.cols - col, vec, w);
+                                                                              const int64_t dots) {
+  const Columns<kVec, kWideThreads> c(8ll * kWideThreads * blockIdx.x, threadIdx.x, a.cols);
+  pdl_trigger();
+  pdl_wait();
+  if (!c.in(0)) return;
+  float2 acc[4] = {}, unused = make_float2(0.0f, 0.0f);
+  float w[8];
+  load_weights(a.weight, a.w_type, c, w);
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     typename T::V dy;
-    float xh[8], g[8];
+    float h[8], d[8], v[8];
     const float rstd = a.rstd[row];
-    load_backward<T, kMx8>(a, row, col, vec, dy, xh);
-    dy.values(g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      xh[j] = __fmul_rn(xh[j], rstd);
-      acc[j] = __fmaf_rn(g[j], xh[j], acc[j]);
-      g[j] = __fmul_rn(g[j], w[j]);
-    }
-    store_dx<T>(a, row, col, vec, rstd, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv), xh, g);
+    load_dy_h<T, kMx8>(a, row, c, dy, h);
+    dy.values(d);
+    add_vector(d, h, w, rstd, acc, unused);
+    dx_vector(d, h, w, rstd, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv), v);
+    store_dx<T>(a, row, c, v);
   }
-  float* out = static_cast<float*>(a.workspace) + dots + blockIdx.y * a.cols;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (col + j < a.cols) out[col + j] = acc[j];
+  store_part(static_cast<float*>(a.workspace) + dots + blockIdx.y * a.cols, c, acc);
 }
 
-// dw from the parts: 32 columns a block, eight threads a column that take every
-// eighth part, then their sums in order.
-__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float* __restrict__ parts, const int64_t n, const int64_t cols,
-                                                          void* dw, const int type) {
-  __shared__ float smem[8][33];
+// dw from the parts: 32 columns a block, a warp every 32nd part of them, then
+// the warps' sums in order.
+constexpr int kDwWarps = 32;
+__global__ void __launch_bounds__(32 * kDwWarps) rms_norm_dw_kernel(const float* parts, const int64_t n, const int64_t cols,
+                                                                    void* dw, const int type) {
+  __shared__ float smem[kDwWarps][33];
   const int x = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + x;
+  pdl_wait();
   float s = 0.0f;
-  if (col < cols)
-    for (int64_t p = q; p < n; p += 8) s = __fadd_rn(s, parts[p * cols + col]);
+  if (col < cols) {
+#pragma unroll 8
+    for (int64_t p = q; p < n; p += kDwWarps) s = __fadd_rn(s, __ldcg(parts + p * cols + col));
+  }
   smem[q][x] = s;
   __syncthreads();
   if (q || col >= cols) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) s = __fadd_rn(s, smem[k][x]);
+  for (int k = 1; k < kDwWarps; ++k) s = __fadd_rn(s, smem[k][x]);
   if (type == kMxF32) static_cast<float*>(dw)[col] = s;
   else static_cast<uint16_t*>(dw)[col] = type == kMxF16 ? F16::rn(s) : Bf16::rn(s);
 }
 
 // ------------------------------------------------------------------ launch --
 
-template <class T, int kGroup, int kChunks>
-cudaError_t forward(const RmsNormArgs& a, int vec, cudaStream_t s) {
+template <class T, bool kVec, int kGroup, int kChunks>
+cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
   constexpr int kRows = kBlockOf<kGroup> / kGroup;
-  rms_norm_kernel<T, kGroup, kChunks><<<(unsigned)((a.rows + kRows - 1) / kRows), kBlockOf<kGroup>, 0, s>>>(a, vec);
+  rms_norm_kernel<T, kVec, kGroup, kChunks><<<(unsigned)((a.rows + kRows - 1) / kRows), kBlockOf<kGroup>, 0, s>>>(
+      a, 1.0 / (double)a.cols);
+  return cudaGetLastError();
+}
+
+template <class T, bool kVec>
+cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
+  if (a.cols <= 256) return forward<T, kVec, 32, 1>(a, s);
+  if (a.cols <= 512) return forward<T, kVec, 32, 2>(a, s);
+  if (a.cols <= 1024) return forward<T, kVec, 128, 1>(a, s);
+  if (a.cols <= 2048) return forward<T, kVec, 256, 1>(a, s);
+  if (a.cols <= 4096) return forward<T, kVec, 256, 2>(a, s);
+  if (a.cols <= 8192) return forward<T, kVec, 512, 2>(a, s);
+  if (a.cols <= 16384) return forward<T, kVec, 512, 4>(a, s);
+  rms_norm_long_kernel<T, kVec><<<(unsigned)a.rows, kLongThreads, 0, s>>>(a, 1.0 / (double)a.cols);
   return cudaGetLastError();
 }
 
@@ -410,49 +536,69 @@ template <class T>
 cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
   const int64_t b = sizeof(typename T::raw);
   auto fits = [&](const void* p, int64_t ld) { return !p || aligned(p, ld * b); };
-  const int vec = fits(a.x, a.ld_x) && fits(a.residual, a.ld_residual) && fits(a.y, a.ld_y) && fits(a.h, a.ld_h) &&
-                  aligned(a.weight, 0);
-  if (a.cols <= 256) return forward<T, 32, 1>(a, vec, s);
-  if (a.cols <= 512) return forward<T, 32, 2>(a, vec, s);
-  if (a.cols <= 1024) return forward<T, 128, 1>(a, vec, s);
-  if (a.cols <= 2048) return forward<T, 256, 1>(a, vec, s);
-  if (a.cols <= 4096) return forward<T, 256, 2>(a, vec, s);
-  if (a.cols <= 8192) return forward<T, 512, 2>(a, vec, s);
-  if (a.cols <= 16384) return forward<T, 512, 4>(a, vec, s);
-  rms_norm_long_kernel<T><<<(unsigned)a.rows, kLongThreads, 0, s>>>(a, vec);
+  const bool vec = fits(a.x, a.ld_x) && fits(a.residual, a.ld_residual) && fits(a.y, a.ld_y) && fits(a.h, a.ld_h) &&
+                   aligned(a.weight, 0);
+  return vec ? forward<T, true>(a, s) : forward<T, false>(a, s);
+}
+
+cudaError_t add_dw(const RmsNormBackwardArgs& a, int64_t first, int64_t parts, cudaStream_t s) {
+  return launch_kernel(rms_norm_dw_kernel, (int)((a.cols + 31) / 32), 32 * kDwWarps, 0, s, true,
+                       static_cast<const float*>(a.workspace) + first, parts, a.cols, a.dw, a.dw_type);
+}
+
+template <class T, bool kMx8, int kGroup, int kChunks, bool kDh>
+cudaError_t backward_ring(const RmsNormBackwardArgs& a, int64_t parts, cudaStream_t s) {
+  // as deep as lets the blocks of max_parts fit an SM together
+  constexpr int kStage = Ring<T, kGroup, kChunks, kMx8, kDh>::kBytes;
+  constexpr int kShare = 220 * 1024 / (kGroup <= 128 ? 8 : kGroup <= 256 ? 4 : kChunks == 1 ? 2 : 1);
+  constexpr int kStages = kShare / kStage < 2 ? 2 : kShare / kStage > 5 ? 5 : kShare / kStage;
+  static_assert(kStages * kStage <= 220 * 1024, "the ring fits");
+  auto kernel = rms_norm_backward_ring_kernel<T, kGroup, kChunks, kMx8, kDh, kStages>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kStage);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)parts, kGroup, kStages * kStage, s>>>(a);
   return cudaGetLastError();
 }
 
 template <class T, bool kMx8, int kGroup, int kChunks>
-cudaError_t backward(const RmsNormBackwardArgs& a, int vec, cudaStream_t s) {
-  constexpr int kRows = kBlockOf<kGroup> / kGroup;
-  const int64_t parts = std::min<int64_t>((a.rows + kRows - 1) / kRows, parts_of(a.rows));
-  rms_norm_backward_kernel<T, kGroup, kChunks, kMx8><<<(unsigned)parts, kBlockOf<kGroup>, 0, s>>>(a, vec);
-  rms_norm_dw_kernel<<<(unsigned)((a.cols + 31) / 32), 256, 0, s>>>(static_cast<const float*>(a.workspace), parts, a.cols,
-                                                                    a.dw, a.dw_type);
-  return cudaGetLastError();
+cudaError_t backward(const RmsNormBackwardArgs& a, bool vec, cudaStream_t s) {
+  const int64_t parts = parts_of(a.rows, a.cols);
+  cudaError_t e;
+  if (vec) {
+    e = a.dh ? backward_ring<T, kMx8, kGroup, kChunks, true>(a, parts, s)
+             : backward_ring<T, kMx8, kGroup, kChunks, false>(a, parts, s);
+  } else {
+    rms_norm_backward_kernel<T, kGroup, kChunks, kMx8><<<(unsigned)parts, kGroup, 0, s>>>(a);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? add_dw(a, 0, parts, s) : e;
+}
+
+template <class T, bool kMx8, bool kVec>
+cudaError_t backward_wide(const RmsNormBackwardArgs& a, cudaStream_t s) {
+  const int64_t dots = dots_floats(a.rows), parts = wide_parts(a.rows);
+  rms_norm_dots_kernel<T, kVec, kMx8><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
+  const dim3 grid((unsigned)((a.cols + 8 * kWideThreads - 1) / (8 * kWideThreads)), (unsigned)parts);
+  rms_norm_backward_wide_kernel<T, kVec, kMx8><<<grid, kWideThreads, 0, s>>>(a, dots);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? add_dw(a, dots, parts, s) : e;
 }
 
 template <class T, bool kMx8>
 cudaError_t backward(const RmsNormBackwardArgs& a, cudaStream_t s) {
   const int64_t b = sizeof(typename T::raw);
   auto fits = [&](const void* p, int64_t ld) { return !p || aligned(p, ld * b); };
-  const int vec = fits(a.dy, a.ld_dy) && fits(a.h, a.ld_h) && fits(a.dh, a.ld_dh) && fits(a.dx, a.ld_dx) &&
-                  aligned(a.weight, 0);
+  const bool vec = a.cols % 8 == 0 && fits(a.dy, a.ld_dy) && fits(a.h, a.ld_h) && fits(a.dh, a.ld_dh) &&
+                   fits(a.dx, a.ld_dx) && aligned(a.weight, 0);
+  if (a.cols > wide_from(a.type)) return vec ? backward_wide<T, kMx8, true>(a, s) : backward_wide<T, kMx8, false>(a, s);
   if (a.cols <= 256) return backward<T, kMx8, 32, 1>(a, vec, s);
-  if (a.cols <= 512) return backward<T, kMx8, 32, 2>(a, vec, s);
+  if (a.cols <= 512) return backward<T, kMx8, 64, 1>(a, vec, s);
   if (a.cols <= 1024) return backward<T, kMx8, 128, 1>(a, vec, s);
   if (a.cols <= 2048) return backward<T, kMx8, 256, 1>(a, vec, s);
-  if (a.cols <= 4096) return backward<T, kMx8, 256, 2>(a, vec, s);
+  if (a.cols <= 4096) return backward<T, kMx8, 512, 1>(a, vec, s);
   if (a.cols <= 8192) return backward<T, kMx8, 512, 2>(a, vec, s);
-  if (a.cols <= kWideCols) return backward<T, kMx8, 512, 4>(a, vec, s);
-  const int64_t dots = dots_floats(a.rows), parts = wide_parts(a.rows);
-  rms_norm_dots_kernel<T, kMx8><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a, vec);
-  const dim3 grid((unsigned)((a.cols + 8 * kWideThreads - 1) / (8 * kWideThreads)), (unsigned)parts);
-  rms_norm_backward_wide_kernel<T, kMx8><<<grid, kWideThreads, 0, s>>>(a, dots, vec);
-  rms_norm_dw_kernel<<<(unsigned)((a.cols + 31) / 32), 256, 0, s>>>(static_cast<const float*>(a.workspace) + dots, parts,
-                                                                    a.cols, a.dw, a.dw_type);
-  return cudaGetLastError();
+  if constexpr (sizeof(typename T::raw) == 2) return backward<T, kMx8, 512, 4>(a, vec, s);
+  return cudaErrorInvalidValue;
 }
 
 template <class T>
@@ -463,7 +609,9 @@ cudaError_t backward(const RmsNormBackwardArgs& a, cudaStream_t s) {
 }  // namespace
 
 int64_t rms_norm_backward_workspace(int64_t rows, int64_t cols) {
-  return 4 * (cols > kWideCols ? dots_floats(rows) + wide_parts(rows) * cols : parts_of(rows) * cols);
+  // for every type: binary32's rows go through memory twice from 8192 columns on
+  const int64_t once = parts_of(rows, cols) * cols, twice = dots_floats(rows) + wide_parts(rows) * cols;
+  return 4 * (cols <= wide_from(kMxF32) ? once : cols <= wide_from(kMxBf16) ? std::max(once, twice) : twice);
 }
 
 cudaError_t launch_rms_norm(const RmsNormArgs& a, int, cudaStream_t s) {
