@@ -391,15 +391,16 @@ __device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(sum[j], a.scale);
+  typename T::V x;
   if (a.accumulate) {
-    typename T::V x;
     float u[8];
     load_columns(x, out, c);
     x.values(u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
   }
-  store_columns<T>(out, c, v);
+  round_to(x, v);
+  store_columns(out, c, x);
 }
 
 // One warp clears `bytes` bytes at p, an element's multiple.
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
   if (u >= g.count * g.slabs) return;
   const uint32_t segment = div_by(u, by_slabs), slab = u - segment * g.slabs;
   const uint32_t lo = segment * g.seg, hi = min(lo + g.seg, g.n);
-  const Slab<kVec> c(256ll * slab, lane, a.cols);
+  const Slab<kVec> c(256u * slab, lane, (uint32_t)a.cols);
   const uint32_t vocab = (uint32_t)a.vocab;
   uint32_t current = g.keys[lo];
   if (current == vocab) return;  // padding from here on
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t slab = blockIdx.x % g.slabs, first = blockIdx.x / g.slabs * kWarps, segment = first + warp;
-  const Slab<kVec> c(256ll * slab, lane, a.cols);
+  const Slab<kVec> c(256u * slab, lane, (uint32_t)a.cols);
   // the segment after the last of my run; 0: no run of mine
   uint32_t end = 0, key = 0;
   if (segment + 1 < g.count) {
@@ -640,7 +641,8 @@ cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Cl
 
 template <class V>
 cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, cudaStream_t s) {
-  const bool vec = aligned(a.dy, a.ld_dy * element_bytes(a.type)) && aligned(a.dtable, a.ld * element_bytes(a.dtable_type));
+  const bool vec = a.cols % 8 == 0 && aligned(a.dy, a.ld_dy * element_bytes(a.type)) &&
+                   aligned(a.dtable, a.ld * element_bytes(a.dtable_type));
   switch (a.dtable_type) {
     case kMxBf16: return vec ? sum_rows<V, TBf16, true>(a, g, z, s) : sum_rows<V, TBf16, false>(a, g, z, s);
     case kMxF16: return vec ? sum_rows<V, TF16, true>(a, g, z, s) : sum_rows<V, TF16, false>(a, g, z, s);

@@ -21,23 +21,19 @@ constexpr int kBlockOf = kGroup > 128 ? kGroup : 128;
 // ----------------------------------------------------------------- forward --
 
 // Sum over the kGroup threads that share a row (a warp, or the whole block of
-// kGroup threads), in binary64 from a thread's binary32 sum on: every thread
-// gets the same bits.
+// kGroup threads), from a warp's binary32 sum on in binary64: every thread gets
+// the same bits.
 template <int kGroup>
-__device__ __forceinline__ double group_sum(float mine, double* smem) {
-  double v = (double)mine;
+__device__ __forceinline__ double group_sum(float mine, float* smem) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  if constexpr (kGroup > 32) {
-    constexpr int kWarps = kGroup / 32;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) smem[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < kWarps ? smem[lane] : 0.0;
+  for (int o = 16; o > 0; o >>= 1) mine = __fadd_rn(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
+  if constexpr (kGroup == 32) return (double)mine;
+  constexpr int kWarps = kGroup / 32;
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  double v = 0.0;
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    v = __shfl_sync(0xFFFFFFFFu, v, 0);
-  }
+  for (int w = 0; w < kWarps; ++w) v = __dadd_rn(v, (double)smem[w]);
   return v;
 }
 
@@ -53,49 +49,59 @@ __device__ __forceinline__ float rstd_of(double ss, double inv_cols, double eps)
   return isfinite((float)m) ? better : r;
 }
 
+// The addresses of a row of the operands and results.
+template <class T>
+struct NormRow {
+  using raw = typename T::raw;
+  const raw *x, *r;
+  raw *h, *y;
+  Row8 h8, y8;
+  __device__ __forceinline__ NormRow(const RmsNormArgs& a, int64_t row)
+      : x(row_of<T>(a.x, row, a.ld_x)), r(row_of<T>(a.residual, row, a.ld_residual)), h(row_of<T>(a.h, row, a.ld_h)),
+        y(row_of<T>(a.y, row, a.ld_y)), h8(row_of(a.h8, row)), y8(row_of(a.y8, row)) {}
+};
+
 // A vector of one row of h: x plus the residual, rounded to their type.
 template <class T, class C>
-__device__ __forceinline__ void load_h(const RmsNormArgs& a, int64_t row, const C& c, typename T::V& x) {
-  using raw = typename T::raw;
-  load_columns(x, static_cast<const raw*>(a.x) + row * a.ld_x, c);
+__device__ __forceinline__ void load_h(const RmsNormArgs& a, const NormRow<T>& row, const C& c, typename T::V& x) {
+  load_columns(x, row.x, c);
   if (a.residual) {
     typename T::V r;
-    load_columns(r, static_cast<const raw*>(a.residual) + row * a.ld_residual, c);
-    float v[8], u[8];
-    x.values(v);
-    r.values(u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
-    round_to(x, v);
+    load_columns(r, row.r, c);
+    add_to(x, r);
   }
 }
 
-__device__ __forceinline__ float square_sum(const float (&v)[8], float ss) {
+__device__ __forceinline__ float2 square_sum(const float (&v)[8], float2 ss) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ss = __fmaf_rn(v[j], v[j], ss);
+  for (int p = 0; p < 4; ++p) ss = fma2(pair(v, p), pair(v, p), ss);
   return ss;
 }
 
 // All results of one vector of h.  Called by whole warps.
 template <class T, class C>
-__device__ __forceinline__ void finish(const RmsNormArgs& a, int64_t row, const C& c, int64_t nb, float rstd,
+__device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& row, const C& c, float rstd,
                                        const typename T::V& x) {
-  using raw = typename T::raw;
   float v[8], w[8];
   x.values(v);
-  if (a.h) store_columns<T>(static_cast<raw*>(a.h) + row * a.ld_h, c, v);
-  if (a.h8.codes) store_columns8(a.h8, row, nb, c, x);
+  if (a.h) store_columns(row.h, c, x);
+  if (a.h8.codes) store_columns8(row.h8, c, x, v);
+  if (!a.y && !a.y8.codes) return;
   load_weights(a.weight, a.w_type, c, w);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], rstd), w[j]);
-  if (a.y) store_columns<T>(static_cast<raw*>(a.y) + row * a.ld_y, c, v);
+  scale8(v, rstd);
+  times8(v, w);
+  typename T::V y;
+  round_to(y, v);
+  if (a.y) store_columns(row.y, c, y);
   if (a.y8.codes) {
+    if (!isfinite(rstd)) {  // past the row x and w are 0, but 0 times this is not
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (!c.in(j)) v[j] = 0.0f;  // past the row: w is 0 there, but rstd need not be finite
-    typename T::V y;
-    round_to(y, v);
-    store_columns8(a.y8, row, nb, c, y);
+      for (int j = 0; j < 8; ++j)
+        if (!c.in(j)) v[j] = 0.0f;
+      round_to(y, v);
+    }
+    y.values(v);
+    store_columns8(row.y8, c, y, v);
   }
 }
 
@@ -104,26 +110,26 @@ template <class T, bool kVec, int kGroup, int kChunks>
 __global__ void __launch_bounds__(kBlockOf<kGroup>) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
                                                                     const double inv_cols) {
   constexpr int kRows = kBlockOf<kGroup> / kGroup;
-  __shared__ double smem[32];
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kGroup;
-  if (row >= a.rows) return;  // whole groups
-  const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
-  const int t = threadIdx.x % kGroup;
+  __shared__ float smem[32];
+  const uint32_t number = blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / kGroup : 0);
+  if (number >= (uint32_t)a.rows) return;  // whole groups
+  const NormRow<T> row(a, number);
+  const uint32_t t = threadIdx.x % kGroup, cols = (uint32_t)a.cols;
   using C = Columns<kVec, kGroup>;
   typename T::V x[kChunks];
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) load_h<T>(a, row, C(8 * kGroup * k, t, a.cols), x[k]);
-  float ss = 0.0f;
+  for (int k = 0; k < kChunks; ++k) load_h<T>(a, row, C(8 * kGroup * k, t, cols), x[k]);
+  float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     float v[8];
     x[k].values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<kGroup>(ss, smem), inv_cols, (double)a.eps);
-  if (a.rstd && t == 0) a.rstd[row] = rstd;
+  const float rstd = rstd_of(group_sum<kGroup>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  if (a.rstd && t == 0) a.rstd[number] = rstd;
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) finish<T>(a, row, C(8 * kGroup * k, t, a.cols), nb, rstd, x[k]);
+  for (int k = 0; k < kChunks; ++k) finish<T>(a, row, C(8 * kGroup * k, t, cols), rstd, x[k]);
 }
 
 // Rows too long for registers: read a second time (a thread reads its own
@@ -132,25 +138,25 @@ constexpr int kLongThreads = 512;
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __grid_constant__ RmsNormArgs a,
                                                                      const double inv_cols) {
-  __shared__ double smem[32];
-  const int64_t row = blockIdx.x;
-  const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
+  __shared__ float smem[32];
+  const NormRow<T> row(a, blockIdx.x);
+  const uint32_t cols = (uint32_t)a.cols;
   using C = Columns<kVec, kLongThreads>;
-  float ss = 0.0f;
-  for (int64_t first = 0; first < a.cols; first += 8 * kLongThreads) {
+  float2 ss = make_float2(0.0f, 0.0f);
+  for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
     typename T::V x;
     float v[8];
-    load_h<T>(a, row, C(first, threadIdx.x, a.cols), x);
+    load_h<T>(a, row, C(first, threadIdx.x, cols), x);
     x.values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<kLongThreads>(ss, smem), inv_cols, (double)a.eps);
-  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-  for (int64_t first = 0; first < a.cols; first += 8 * kLongThreads) {
+  const float rstd = rstd_of(group_sum<kLongThreads>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
+  for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
     typename T::V x;
-    const C c(first, threadIdx.x, a.cols);
+    const C c(first, threadIdx.x, cols);
     load_h<T>(a, row, c, x);
-    finish<T>(a, row, c, nb, rstd, x);
+    finish<T>(a, row, c, rstd, x);
   }
 }
 
@@ -190,28 +196,38 @@ __device__ __forceinline__ float block_sum(float v, float (*smem)[32], int round
   return __shfl_sync(0xFFFFFFFFu, v, 0);
 }
 
-__device__ __forceinline__ float2 pair(const float (&v)[8], int p) { return make_float2(v[2 * p], v[2 * p + 1]); }
-
-// One vector's part of a row's sum of g xh, and of dw.
-__device__ __forceinline__ void add_vector(const float (&dy)[8], const float (&h)[8], const float (&w)[8], float rstd,
-                                           float2 (&acc)[4], float2& dot) {
+// One vector's part of a row's sum of g xh, and of dw; dy becomes g.
+__device__ __forceinline__ void add_vector(float (&dy)[8], const float (&xh)[8], const float (&w)[8], float2 (&acc)[4],
+                                           float2& dot) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const float2 xh = mul2(pair(h, p), make_float2(rstd, rstd));
-    dot = fma2(mul2(pair(dy, p), pair(w, p)), xh, dot);
-    acc[p] = fma2(pair(dy, p), xh, acc[p]);
-  }
+  for (int p = 0; p < 4; ++p) acc[p] = fma2(pair(dy, p), pair(xh, p), acc[p]);
+  times8(dy, w);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) dot = fma2(pair(dy, p), pair(xh, p), dot);
 }
 
-// dx of one vector, without dh: rstd (g - xh mean).
-__device__ __forceinline__ void dx_vector(const float (&dy)[8], const float (&h)[8], const float (&w)[8], float rstd,
-                                          float mean, float (&v)[8]) {
+// dx of one vector, without dh, in g's place: rstd (g - xh mean).
+__device__ __forceinline__ void dx_vector(float (&g)[8], const float (&xh)[8], float rstd, float mean) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const float2 xh = mul2(pair(h, p), make_float2(rstd, rstd));
-    const float2 d = mul2(fma2(xh, make_float2(-mean, -mean), mul2(pair(dy, p), pair(w, p))), make_float2(rstd, rstd));
-    v[2 * p] = d.x, v[2 * p + 1] = d.y;
+    const float2 d = fma2(pair(xh, p), make_float2(-mean, -mean), pair(g, p));
+    g[2 * p] = d.x, g[2 * p + 1] = d.y;
   }
+  scale8(g, rstd);
+}
+
+// dx, rounded, with dh (a vector of the type) added if there is one.
+template <class T, class C>
+__device__ __forceinline__ void store_dx(typename T::raw* row, const C& c, const typename T::V* dh, float (&v)[8]) {
+  if (dh) {
+    float u[8];
+    dh->values(u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
+  }
+  typename T::V x;
+  round_to(x, v);
+  store_columns(row, c, x);
 }
 
 template <class C, class A>
@@ -227,166 +243,157 @@ template <class T, int kGroup, int kChunks, bool kMx8, bool kDh>
 struct Ring {
   using V = typename T::V;
   using raw = typename T::raw;
-  static constexpr int kWords = sizeof(raw) / 2;                   // 16-byte words of a vector
-  static constexpr int kPlane = kGroup * kChunks * 16;             // bytes of one word of all vectors
-  static constexpr int kH = kWords * kPlane;                       // where h's begin
+  static constexpr int kWords = sizeof(raw) / 2;        // 16-byte words of a vector
+  static constexpr int kPlane = kGroup * kChunks * 16;  // bytes of one word of all vectors
+  static constexpr int kH = kWords * kPlane;            // where h's begin
   static constexpr int kD = kH + (kMx8 ? kPlane / 2 : kWords * kPlane);
   static constexpr int kBytes = kD + (kDh ? kWords * kPlane : 0);
-  uint8_t* base;
 
-  __device__ __forceinline__ void fetch16(uint8_t* to, const void* matrix, int64_t row, int64_t ld, int64_t cols) const {
-    const raw* p = static_cast<const raw*>(matrix) + row * ld;
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      const int v = kGroup * k + threadIdx.x;
-      if (8 * v >= cols) break;
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) copy_async16(to + i * kPlane + 16 * v, p + 8 * v + 16 / (int)sizeof(raw) * i);
-    }
-  }
   // Asks for a row (none past the end; the group is there all the same).
-  __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, int64_t row, int stage) const {
+  static __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, int64_t row, uint8_t* to) {
     if (row < a.rows) {
-      uint8_t* to = base + stage * kBytes;
-      fetch16(to, a.dy, row, a.ld_dy, a.cols);
-      if constexpr (kMx8) {
-        const uint8_t* p = a.h8.codes + row * a.h8.code_pitch;
+      const raw* dy = row_of<T>(a.dy, row, a.ld_dy);
+      const raw* h = row_of<T>(a.h, row, a.ld_h);
+      const raw* dh = row_of<T>(a.dh, row, a.ld_dh);
+      const uint8_t* h8 = a.h8.codes + row * a.h8.code_pitch;
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const int v = kGroup * k + threadIdx.x;
-          if (8 * v < a.cols) copy_async8(to + kH + 8 * v, p + 8 * v);
+      for (int k = 0; k < kChunks; ++k) {
+        const uint32_t v = kGroup * k + threadIdx.x;
+        if (8 * v >= (uint32_t)a.cols) break;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          constexpr int kIn = 16 / (int)sizeof(raw);
+          copy_async16(to + i * kPlane + 16 * v, dy + 8 * v + kIn * i);
+          if constexpr (!kMx8) copy_async16(to + kH + i * kPlane + 16 * v, h + 8 * v + kIn * i);
+          if constexpr (kDh) copy_async16(to + kD + i * kPlane + 16 * v, dh + 8 * v + kIn * i);
         }
-      } else {
-        fetch16(to + kH, a.h, row, a.ld_h, a.cols);
+        if constexpr (kMx8) copy_async8(to + kH + 8 * v, h8 + 8 * v);
       }
-      if constexpr (kDh) fetch16(to + kD, a.dh, row, a.ld_dh, a.cols);
     }
     copy_async_commit();
   }
-  __device__ __forceinline__ void read16(int at, int stage, int k, float (&v)[8]) const {
-    const uint8_t* p = base + stage * kBytes + at + 16 * (kGroup * k + threadIdx.x);
-    V x;
+  static __device__ __forceinline__ void read(const uint8_t* plane, int k, V& x) {
+    const uint8_t* p = plane + 16 * (kGroup * k + threadIdx.x);
     uint4* w = reinterpret_cast<uint4*>(&x);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const uint4*>(p + i * kPlane);
-    x.values(v);
   }
-  __device__ __forceinline__ void dy(int stage, int k, float (&v)[8]) const { read16(0, stage, k, v); }
-  __device__ __forceinline__ void dh(int stage, int k, float (&v)[8]) const { read16(kD, stage, k, v); }
-  __device__ __forceinline__ void h(int stage, int k, uint32_t scale, float (&v)[8]) const {
-    if constexpr (kMx8)
-      values8_mx8(*reinterpret_cast<const uint2*>(base + stage * kBytes + kH + 8 * (kGroup * k + threadIdx.x)), scale, v);
-    else read16(kH, stage, k, v);
+  // xh of a vector.
+  static __device__ __forceinline__ void read_xh(const uint8_t* stage, int k, uint32_t scale, float rstd, float (&v)[8]) {
+    if constexpr (kMx8) {
+      elements8(*reinterpret_cast<const uint2*>(stage + kH + 8 * (kGroup * k + threadIdx.x)), v);
+      scale8(v, __fmul_rn(scale_value(scale), rstd));
+    } else {
+      V x;
+      read(stage + kH, k, x);
+      x.values(v);
+      scale8(v, rstd);
+    }
   }
 };
 
-// cols is a multiple of 8 here, and every row's vectors are aligned.
+// A row's vectors are whole and aligned here.  One vector a thread: xh and g
+// stay in registers over the sum; more: they are read and made a second time.
 template <class T, int kGroup, int kChunks, bool kMx8, bool kDh, int kStages>
 __global__ void __launch_bounds__(kGroup) rms_norm_backward_ring_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
-  using raw = typename T::raw;
+  using R = Ring<T, kGroup, kChunks, kMx8, kDh>;
   using C = Columns<true, kGroup>;
-  extern __shared__ __align__(16) uint8_t ring_smem[];
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float smem[2][32];
   pdl_trigger();
-  const Ring<T, kGroup, kChunks, kMx8, kDh> ring{ring_smem};
   const int64_t step = gridDim.x;
+  const uint32_t cols = (uint32_t)a.cols;
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) ring.fetch(a, blockIdx.x + s * step, s);
+  for (int s = 0; s < kStages - 1; ++s) R::fetch(a, blockIdx.x + s * step, ring + s * R::kBytes);
   float2 acc[kChunks][4];
-  float w[kChunks][8];
+  float w[8];
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) {
-    if constexpr (kChunks == 1) load_weights(a.weight, a.w_type, C(0, threadIdx.x, a.cols), w[0]);
+  for (int k = 0; k < kChunks; ++k)
 #pragma unroll
     for (int p = 0; p < 4; ++p) acc[k][p] = make_float2(0.0f, 0.0f);
-  }
+  if constexpr (kChunks == 1) load_weights(a.weight, a.w_type, C(0, threadIdx.x, cols), w);
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
   // the row's statistics and scales, a row ahead
-  float rstd = 0.0f, next_rstd = a.rstd[min((int64_t)blockIdx.x, a.rows - 1)];
+  float next_rstd = 0.0f;
   uint32_t scale[kChunks] = {}, next_scale[kChunks] = {};
   auto ahead = [&](int64_t row) {
     if (row >= a.rows) return;
     next_rstd = a.rstd[row];
     if constexpr (kMx8) {
+      const uint8_t* scales = a.h8.scales + row * a.h8.scale_pitch;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
-        const int64_t col = 8 * (kGroup * k + threadIdx.x);
-        if (col < a.cols) next_scale[k] = a.h8.scales[row * a.h8.scale_pitch + (col >> 5)];
+        const C c(8 * kGroup * k, threadIdx.x, cols);
+        if (c.in(0)) next_scale[k] = scales[c.first >> 5];
       }
     }
   };
   ahead(blockIdx.x);
-  int stage = 0, round = 0;
+  uint32_t now = 0, later = (kStages - 1) * R::kBytes;  // the stages of this row and of the one to ask for
+  int round = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += step, ++round) {
-    ring.fetch(a, row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-    rstd = next_rstd;
+    R::fetch(a, row + (kStages - 1) * step, ring + later);
+    later = now;
+    const uint8_t* stage = ring + now;
+    now = now + R::kBytes == kStages * R::kBytes ? 0 : now + R::kBytes;
+    const float rstd = next_rstd;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) scale[k] = next_scale[k];
     ahead(row + step);
     copy_async_wait<kStages - 1>();
     float2 dot = make_float2(0.0f, 0.0f);
+    float g[8], xh[8];
+    auto vector = [&](int k, bool sums) {
+      const C c(8 * kGroup * k, threadIdx.x, cols);
+      typename T::V dy;
+      R::read(stage, k, dy);
+      dy.values(g);
+      R::read_xh(stage, k, scale[k], rstd, xh);
+      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, c, w);
+      if (sums) add_vector(g, xh, w, acc[k], dot);
+      else times8(g, w);
+    };
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * kGroup * k, threadIdx.x, a.cols);
-      if (c.first >= a.cols) break;
-      float dy[8], h[8];
-      ring.dy(stage, k, dy);
-      ring.h(stage, k, scale[k], h);
-      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, c, w[k]);
-      add_vector(dy, h, w[k], rstd, acc[k], dot);
-    }
+    for (int k = 0; k < kChunks; ++k)
+      if (C(8 * kGroup * k, threadIdx.x, cols).in(0)) vector(k, true);
     const float mean = __fmul_rn(block_sum<kGroup>(__fadd_rn(dot.x, dot.y), smem, round), inv);
+    typename T::raw* to = row_of<T>(a.dx, row, a.ld_dx);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * kGroup * k, threadIdx.x, a.cols);
-      if (c.first >= a.cols) break;
-      float dy[8], h[8], v[8];
-      ring.dy(stage, k, dy);
-      ring.h(stage, k, scale[k], h);
-      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, c, w[k]);
-      dx_vector(dy, h, w[k], rstd, mean, v);
-      if constexpr (kDh) {
-        float u[8];
-        ring.dh(stage, k, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
-      }
-      store_columns<T>(static_cast<raw*>(a.dx) + row * a.ld_dx, c, v);
+      const C c(8 * kGroup * k, threadIdx.x, cols);
+      if (!c.in(0)) break;
+      if constexpr (kChunks > 1) vector(k, false);
+      dx_vector(g, xh, rstd, mean);
+      typename T::V dh;
+      if constexpr (kDh) R::read(stage + R::kD, k, dh);
+      store_dx<T>(to, c, kDh ? &dh : nullptr, g);
     }
-    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, a.cols), acc[k]);
+  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, cols), acc[k]);
 }
 
 // Rows of any alignment, straight from memory.
 template <class T, bool kMx8, class C>
-__device__ __forceinline__ void load_dy_h(const RmsNormBackwardArgs& a, int64_t row, const C& c, typename T::V& dy,
-                                          float (&h)[8]) {
-  using raw = typename T::raw;
-  load_columns(dy, static_cast<const raw*>(a.dy) + row * a.ld_dy, c);
+__device__ __forceinline__ void load_dy_xh(const RmsNormBackwardArgs& a, int64_t row, const C& c, float rstd,
+                                           typename T::V& dy, float (&xh)[8]) {
+  load_columns(dy, row_of<T>(a.dy, row, a.ld_dy), c);
   if constexpr (kMx8) {
-    load_columns8(a.h8, row, c, h);
+    load_columns8(row_of(a.h8, row), c, rstd, xh);
   } else {
     typename T::V x;
-    load_columns(x, static_cast<const raw*>(a.h) + row * a.ld_h, c);
-    x.values(h);
+    load_columns(x, row_of<T>(a.h, row, a.ld_h), c);
+    x.values(xh);
+    scale8(xh, rstd);
   }
 }
 
 template <class T, class C>
-__device__ __forceinline__ void store_dx(const RmsNormBackwardArgs& a, int64_t row, const C& c, float (&v)[8]) {
-  using raw = typename T::raw;
-  if (a.dh) {
-    typename T::V d;
-    float u[8];
-    load_columns(d, static_cast<const raw*>(a.dh) + row * a.ld_dh, c);
-    d.values(u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
-  }
-  store_columns<T>(static_cast<raw*>(a.dx) + row * a.ld_dx, c, v);
+__device__ __forceinline__ void finish_dx(const RmsNormBackwardArgs& a, int64_t row, const C& c, float (&v)[8]) {
+  typename T::V dh;
+  if (a.dh) load_columns(dh, row_of<T>(a.dh, row, a.ld_dh), c);
+  store_dx<T>(row_of<T>(a.dx, row, a.ld_dx), c, a.dh ? &dh : nullptr, v);
 }
 
 template <class T, int kGroup, int kChunks, bool kMx8>
@@ -394,6 +401,7 @@ __global__ void __launch_bounds__(kGroup) rms_norm_backward_kernel(const __grid_
   using C = Columns<false, kGroup>;
   __shared__ float smem[2][32];
   pdl_trigger();
+  const uint32_t cols = (uint32_t)a.cols;
   float2 acc[kChunks][4];
 #pragma unroll
   for (int k = 0; k < kChunks; ++k)
@@ -403,33 +411,33 @@ __global__ void __launch_bounds__(kGroup) rms_norm_backward_kernel(const __grid_
   int round = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++round) {
     typename T::V dy[kChunks];
-    float h[kChunks][8];
+    float xh[kChunks][8], w[8], g[8];
     const float rstd = a.rstd[row];
     float2 dot = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) load_dy_h<T, kMx8>(a, row, C(8 * kGroup * k, threadIdx.x, a.cols), dy[k], h[k]);
+    for (int k = 0; k < kChunks; ++k) load_dy_xh<T, kMx8>(a, row, C(8 * kGroup * k, threadIdx.x, cols), rstd, dy[k], xh[k]);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * kGroup * k, threadIdx.x, a.cols);
-      float d[8], w[8];
-      dy[k].values(d);
-      load_weights(a.weight, a.w_type, c, w);
-      add_vector(d, h[k], w, rstd, acc[k], dot);
+      dy[k].values(g);
+      load_weights(a.weight, a.w_type, C(8 * kGroup * k, threadIdx.x, cols), w);
+      add_vector(g, xh[k], w, acc[k], dot);
     }
     const float mean = __fmul_rn(block_sum<kGroup>(__fadd_rn(dot.x, dot.y), smem, round), inv);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * kGroup * k, threadIdx.x, a.cols);
-      float d[8], w[8], v[8];
-      dy[k].values(d);
-      load_weights(a.weight, a.w_type, c, w);
-      dx_vector(d, h[k], w, rstd, mean, v);
-      store_dx<T>(a, row, c, v);
+      const C c(8 * kGroup * k, threadIdx.x, cols);
+      if constexpr (kChunks > 1) {
+        dy[k].values(g);
+        load_weights(a.weight, a.w_type, c, w);
+        times8(g, w);
+      }
+      dx_vector(g, xh[k], rstd, mean);
+      finish_dx<T>(a, row, c, g);
     }
   }
   float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, a.cols), acc[k]);
+  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, cols), acc[k]);
 }
 
 // Longer rows: the rows' dot products first (into the workspace's head), then
@@ -445,18 +453,19 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __gri
   __shared__ float smem[2][32];
   pdl_trigger();
   const int64_t row = blockIdx.x;
+  const uint32_t cols = (uint32_t)a.cols;
   const float rstd = a.rstd[row];
   float2 dot = make_float2(0.0f, 0.0f);
-  for (int64_t first = 0; first < a.cols; first += 8 * kWideThreads) {
-    const C c(first, threadIdx.x, a.cols);
+  for (uint32_t first = 0; first < cols; first += 8 * kWideThreads) {
+    const C c(first, threadIdx.x, cols);
     if (!c.in(0)) break;
     typename T::V dy;
-    float h[8], w[8], d[8];
+    float xh[8], w[8], d[8];
     float2 unused[4] = {};
-    load_dy_h<T, kMx8>(a, row, c, dy, h);
+    load_dy_xh<T, kMx8>(a, row, c, rstd, dy, xh);
     load_weights(a.weight, a.w_type, c, w);
     dy.values(d);
-    add_vector(d, h, w, rstd, unused, dot);
+    add_vector(d, xh, w, unused, dot);
   }
   const float all = block_sum<kWideThreads>(__fadd_rn(dot.x, dot.y), smem, 0);
   if (threadIdx.x == 0) static_cast<float*>(a.workspace)[row] = all;
@@ -465,9 +474,8 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __gri
 template <class T, bool kVec, bool kMx8>
 __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(const __grid_constant__ RmsNormBackwardArgs a,
                                                                               const int64_t dots) {
-  const Columns<kVec, kWideThreads> c(8ll * kWideThreads * blockIdx.x, threadIdx.x, a.cols);
+  const Columns<kVec, kWideThreads> c(8u * kWideThreads * blockIdx.x, threadIdx.x, (uint32_t)a.cols);
   pdl_trigger();
-  pdl_wait();
   if (!c.in(0)) return;
   float2 acc[4] = {}, unused = make_float2(0.0f, 0.0f);
   float w[8];
@@ -475,13 +483,13 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(co
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     typename T::V dy;
-    float h[8], d[8], v[8];
+    float xh[8], g[8];
     const float rstd = a.rstd[row];
-    load_dy_h<T, kMx8>(a, row, c, dy, h);
-    dy.values(d);
-    add_vector(d, h, w, rstd, acc, unused);
-    dx_vector(d, h, w, rstd, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv), v);
-    store_dx<T>(a, row, c, v);
+    load_dy_xh<T, kMx8>(a, row, c, rstd, dy, xh);
+    dy.values(g);
+    add_vector(g, xh, w, acc, unused);
+    dx_vector(g, xh, rstd, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv));
+    finish_dx<T>(a, row, c, g);
   }
   store_part(static_cast<float*>(a.workspace) + dots + blockIdx.y * a.cols, c, acc);
 }
@@ -536,7 +544,7 @@ template <class T>
 cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
   const int64_t b = sizeof(typename T::raw);
   auto fits = [&](const void* p, int64_t ld) { return !p || aligned(p, ld * b); };
-  const bool vec = fits(a.x, a.ld_x) && fits(a.residual, a.ld_residual) && fits(a.y, a.ld_y) && fits(a.h, a.ld_h) &&
+  const bool vec = a.cols % 8 == 0 && fits(a.x, a.ld_x) && fits(a.residual, a.ld_residual) && fits(a.y, a.ld_y) && fits(a.h, a.ld_h) &&
                    aligned(a.weight, 0);
   return vec ? forward<T, true>(a, s) : forward<T, false>(a, s);
 }
