@@ -22,69 +22,69 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int bytes, int64
 // ------------------------------------------------------------------ lookup --
 
 constexpr int kRowThreads = 256;
-constexpr int kUnits = 4;
+constexpr int kPieces = 4;  // of 256 columns
 
-// A source of rows, eight elements at a time: a dense table of one of the
-// three types, or an MX4 one.
-template <class V>
+// A source of rows: a dense table of one of the three types, or an MX4 one.
+template <class T, bool kWhole>
 struct Dense {
-  static __device__ __forceinline__ void row8(const EmbeddingArgs& a, int64_t row, int64_t col, int vec, float (&v)[8]) {
-    V x;
-    const typename V::raw* p = static_cast<const typename V::raw*>(a.table) + row * a.ld + col;
-    const int64_t n = a.cols - col;
-    if (n >= 8 && vec) x.load_if(p, true);
-    else if (n > 0) x.load(p, n);
-    else x.clear();
+  const typename T::raw* row;
+  Span span;
+  Fetched<typename T::V, kWhole> f[kPieces];
+  __device__ __forceinline__ Dense(const EmbeddingArgs& a, int64_t r)
+      : row(row_of<T>(a.table, r, a.ld)), span(span_of<T>(a.table, a.vocab, a.cols, a.ld)) {}
+  __device__ __forceinline__ void load(int k, const Columns<kWhole>& c) { fetch_columns(f[k], row, c, span); }
+  __device__ __forceinline__ void values(int k, const Columns<kWhole>& c, float scale, float (&v)[8]) {
+    typename T::V x;
+    take_columns(x, f[k], row, c);
     x.values(v);
+    scale8(v, scale);
   }
 };
+template <bool kWhole>
 struct Mx4Rows {
-  static __device__ __forceinline__ void row8(const EmbeddingArgs& a, int64_t row, int64_t col, int, float (&v)[8]) {
-    uint32_t w = 0u, s = 0u;
-    if (col < a.cols) {
-      w = __ldg(reinterpret_cast<const uint32_t*>(a.from.codes + row * a.from.code_pitch + (col >> 1)));
-      s = __ldg(a.from.scales + row * a.from.scale_pitch + (col >> 5));
-    }
-    values8(w, s, v);
+  const uint8_t *codes, *scales;
+  uint32_t w[kPieces], s[kPieces];
+  __device__ __forceinline__ Mx4Rows(const EmbeddingArgs& a, int64_t r)
+      : codes(a.from.codes + r * a.from.code_pitch), scales(a.from.scales + r * a.from.scale_pitch) {}
+  __device__ __forceinline__ void load(int k, const Columns<kWhole>& c) {
+    w[k] = s[k] = 0u;
+    if (!c.any()) return;
+    w[k] = __ldg(reinterpret_cast<const uint32_t*>(codes + (c.first >> 1)));
+    s[k] = __ldg(scales + (c.first >> 5));
+  }
+  __device__ __forceinline__ void values(int k, const Columns<kWhole>&, float scale, float (&v)[8]) const {
+    values8(w[k], s[k], v);
+    scale8(v, scale);
   }
 };
 
-// A warp takes 256 consecutive columns of one token at a time, kUnits of them
-// side by side.
-template <class S, class T>
+// A warp takes up to kPieces pieces of 256 columns of one token, side by side.
+template <class S, class T, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads) embedding_kernel(const __grid_constant__ EmbeddingArgs a, const FastDiv per_row,
-                                                                const uint32_t units, const int vec) {
-  using raw = typename T::raw;
-  const uint32_t warps = gridDim.x * (kRowThreads / 32);
-  const int lane = threadIdx.x & 31;
-  for (uint32_t u0 = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += kUnits * warps) {
-    uint32_t t[kUnits];
-    int64_t col[kUnits], token[kUnits];
-    float v[kUnits][8];
+                                                                const uint32_t units) {
+  const uint32_t u = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (u >= units) return;
+  const uint32_t t = div_by(u, per_row), first = (u - t * per_row.d) * (256 * kPieces), cols = (uint32_t)a.cols;
+  const int64_t token = token_at(a.tokens, a.token_bytes, t);
+  const bool there = (uint64_t)token < (uint64_t)a.vocab;
+  typename T::raw* out = row_of<T>(a.out, t, a.ld_out);
+  S source(a, there ? token : 0);
+  if (there) {
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const uint32_t u = min(u0 + k * warps, units - 1);
-      t[k] = div_by(u, per_row);
-      col[k] = (int64_t)(u - t[k] * per_row.d) * 256 + lane * 8;
-      token[k] = token_at(a.tokens, a.token_bytes, t[k]);
+    for (int k = 0; k < kPieces; ++k)
+      if (first + 256 * k < cols) source.load(k, Columns<kWhole>(first + 256 * k, threadIdx.x & 31, cols));
+  }
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    if (first + 256 * k >= cols) break;
+    typename T::V x;
+    x.clear();
+    if (there) {
+      float v[8];
+      source.values(k, Columns<kWhole>(first + 256 * k, threadIdx.x & 31, cols), a.scale, v);
+      round_to(x, v);
     }
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      if ((uint64_t)token[k] < (uint64_t)a.vocab) {
-        S::row8(a, token[k], col[k], vec, v[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      if ((uint64_t)token[k] < (uint64_t)a.vocab) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = __fmul_rn(v[k][j], a.scale);
-      }
-      store8<T>(static_cast<raw*>(a.out) + t[k] * a.ld_out + col[k], v[k], u0 + k * warps < units ? a.cols - col[k] : 0, vec);
-    }
+    store_columns(out, Columns<kWhole>(first + 256 * k, threadIdx.x & 31, cols), x);
   }
 }
 
@@ -380,11 +380,11 @@ struct Segments {
 };
 
 // A warp's 256 columns.
-template <bool kVec>
-using Slab = Columns<kVec, 32>;
+template <bool kWhole>
+using Slab = Columns<kWhole>;
 
-template <class T, bool kVec>
-__device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64_t row, const Slab<kVec>& c,
+template <class T, bool kWhole>
+__device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64_t row, const Slab<kWhole>& c,
                                            const float (&sum)[8]) {
   using raw = typename T::raw;
   raw* out = static_cast<raw*>(a.dtable) + row * a.ld;
@@ -394,7 +394,7 @@ __device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64
   typename T::V x;
   if (a.accumulate) {
     float u[8];
-    load_columns(x, out, c);
+    load_columns(x, out, c, span_of<T>(a.dtable, a.vocab, a.cols, a.ld));
     x.values(u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
@@ -449,17 +449,18 @@ __device__ __forceinline__ void clear_rows(const EmbeddingBackwardArgs& a, const
   }
 }
 
-template <bool kVec>
+template <bool kWhole>
 __device__ __forceinline__ float* part_at(const Segments& g, uint32_t segment, int slot, int64_t cols) {
   return g.parts + (2ll * segment + slot) * cols;
 }
 
-template <class V, class T, bool kVec>
+template <class D, class T, bool kWhole>
 __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
                                                                          const __grid_constant__ Segments g,
                                                                          const __grid_constant__ Clear z,
                                                                          const FastDiv by_slabs) {
-  constexpr int kAhead = 8;  // rows whose loads are out at a time
+  constexpr int kAhead = kWhole && sizeof(typename D::raw) == 2 ? 8 : 4;  // rows whose loads are out at a time
+  using V = typename D::V;
   __shared__ uint32_t bits[kBitRows / 32];
   pdl_trigger();
   if (blockIdx.x < z.ctas) clear_rows(a, g, z, bits);
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
   if (u >= g.count * g.slabs) return;
   const uint32_t segment = div_by(u, by_slabs), slab = u - segment * g.slabs;
   const uint32_t lo = segment * g.seg, hi = min(lo + g.seg, g.n);
-  const Slab<kVec> c(256u * slab, lane, (uint32_t)a.cols);
+  const Slab<kWhole> c(256u * slab, lane, (uint32_t)a.cols);
   const uint32_t vocab = (uint32_t)a.vocab;
   uint32_t current = g.keys[lo];
   if (current == vocab) return;  // padding from here on
@@ -480,27 +481,27 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
   for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
   auto flush = [&](bool goes_on) {
     if (!inside && !goes_on) {
-      finish_row<T, kVec>(a, current, c, acc);
+      finish_row<T, kWhole>(a, current, c, acc);
     } else {
-      float* p = part_at<kVec>(g, segment, inside ? 0 : 1, a.cols);
+      float* p = part_at<kWhole>(g, segment, inside ? 0 : 1, a.cols);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (c.in(j)) p[c.at(j)] = acc[j];
+        if (c.in(j)) p[c.first + j] = acc[j];
     }
   };
   bool padding = false;
+  const Span span = span_of<D>(a.dy, a.n, a.cols, a.ld_dy);
   for (uint32_t at = lo; at < hi && !padding; at += 32) {
     const uint32_t many = min(hi - at, 32u);
     const uint32_t key = (uint32_t)lane < many ? g.keys[at + lane] : vocab;
     const uint32_t pos = (uint32_t)lane < many ? g.pos[at + lane] : 0u;
     for (uint32_t i = 0; i < many && !padding; i += kAhead) {
-      V x[kAhead];
+      Fetched<V, kWhole> f[kAhead];
+      const typename D::raw* row[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const uint32_t p = __shfl_sync(0xFFFFFFFFu, pos, (i + k) & 31);
-        if (__shfl_sync(0xFFFFFFFFu, key, (i + k) & 31) != vocab)
-          load_columns(x[k], static_cast<const typename V::raw*>(a.dy) + (int64_t)p * a.ld_dy, c);
-        else x[k].clear();
+      for (int k = 0; k < kAhead; ++k) {  // (of a place that is not summed the batch's first row)
+        row[k] = row_of<D>(a.dy, __shfl_sync(0xFFFFFFFFu, pos, (i + k) & 31), a.ld_dy);
+        fetch_columns(f[k], row[k], c, span);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -514,8 +515,10 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
         }
+        V x;
         float v[8];
-        x[k].values(v);
+        take_columns(x, f[k], row[k], c);
+        x.values(v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], v[j]);
       }
@@ -529,19 +532,19 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
 // eighth of the parts a warp.
 constexpr uint32_t kShort = 16;
 
-template <bool kVec>
-__device__ __forceinline__ void add_parts(const Segments& g, uint32_t from, uint32_t to, const Slab<kVec>& c,
+template <bool kWhole>
+__device__ __forceinline__ void add_parts(const Segments& g, uint32_t from, uint32_t to, const Slab<kWhole>& c,
                                           float (&acc)[8]) {
 #pragma unroll 4
   for (uint32_t s = from; s < to; ++s) {
-    const float* p = part_at<kVec>(g, s, 0, c.cols);
+    const float* p = part_at<kWhole>(g, s, 0, c.cols);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c.in(j)) acc[j] = __fadd_rn(acc[j], __ldcg(p + c.at(j)));
+      if (c.in(j)) acc[j] = __fadd_rn(acc[j], __ldcg(p + c.first + j));
   }
 }
 
-template <class T, bool kVec>
+template <class T, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
                                                                      const __grid_constant__ Segments g) {
   constexpr int kWarps = kRowThreads / 32;
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t slab = blockIdx.x % g.slabs, first = blockIdx.x / g.slabs * kWarps, segment = first + warp;
-  const Slab<kVec> c(256u * slab, lane, (uint32_t)a.cols);
+  const Slab<kWhole> c(256u * slab, lane, (uint32_t)a.cols);
   // the segment after the last of my run; 0: no run of mine
   uint32_t end = 0, key = 0;
   if (segment + 1 < g.count) {
@@ -571,12 +574,12 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
   if (lane == 0) ends[warp] = is_long ? end : 0;
   float acc[8];
   if (end) {
-    const float* p = part_at<kVec>(g, segment, 1, a.cols);
+    const float* p = part_at<kWhole>(g, segment, 1, a.cols);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = c.in(j) ? __ldcg(p + c.at(j)) : 0.0f;
+    for (int j = 0; j < 8; ++j) acc[j] = c.in(j) ? __ldcg(p + c.first + j) : 0.0f;
     if (!is_long) {
-      add_parts<kVec>(g, segment + 1, end, c, acc);
-      finish_row<T, kVec>(a, key, c, acc);
+      add_parts<kWhole>(g, segment + 1, end, c, acc);
+      finish_row<T, kWhole>(a, key, c, acc);
     }
   }
   __syncthreads();
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
     float part[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[j] = 0.0f;
-    add_parts<kVec>(g, min(from + warp * each, to), min(from + (warp + 1) * each, to), c, part);
+    add_parts<kWhole>(g, min(from + warp * each, to), min(from + (warp + 1) * each, to), c, part);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[warp][j][lane] = part[j];
     __syncthreads();
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
       for (int k = 0; k < kWarps; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], sums[k][j][lane]);
-      finish_row<T, kVec>(a, key, c, acc);
+      finish_row<T, kWhole>(a, key, c, acc);
     }
     __syncthreads();
   }
@@ -606,47 +609,53 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
 
 int64_t element_bytes(int type) { return type == kMxF32 ? 4 : 2; }
 
-template <class S, class T>
-cudaError_t lookup(const EmbeddingArgs& a, int sm_count, cudaStream_t s) {
-  const int64_t per = (a.cols + 255) / 256;
-  if (per * a.n > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const uint32_t units = (uint32_t)(per * a.n);
-  const int vec = (a.from.codes || aligned(a.table, a.ld * element_bytes(a.type))) &&
-                  aligned(a.out, a.ld_out * element_bytes(a.out_type));
-  const int per_cta = kUnits * kRowThreads / 32;
-  embedding_kernel<S, T><<<cap_grid((units + per_cta - 1) / per_cta, kWaves * sm_count), kRowThreads, 0, s>>>(
-      a, fast_div((uint32_t)per), units, vec);
+template <template <bool> class S, class T>
+cudaError_t lookup(const EmbeddingArgs& a, cudaStream_t s) {
+  const int64_t per = (a.cols + 256 * kPieces - 1) / (256 * kPieces), units = per * a.n;
+  if (units > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const bool whole = a.cols % 8 == 0 && (a.from.codes || aligned(a.table, a.ld * element_bytes(a.type))) &&
+                     aligned(a.out, a.ld_out * element_bytes(a.out_type));
+  const unsigned grid = (unsigned)((units + kRowThreads / 32 - 1) / (kRowThreads / 32));
+  if (whole) embedding_kernel<S<true>, T, true><<<grid, kRowThreads, 0, s>>>(a, fast_div((uint32_t)per), (uint32_t)units);
+  else embedding_kernel<S<false>, T, false><<<grid, kRowThreads, 0, s>>>(a, fast_div((uint32_t)per), (uint32_t)units);
   return cudaGetLastError();
 }
 
-template <class S>
-cudaError_t lookup(const EmbeddingArgs& a, int sm_count, cudaStream_t s) {
+template <template <bool> class S>
+cudaError_t lookup(const EmbeddingArgs& a, cudaStream_t s) {
   switch (a.out_type) {
-    case kMxBf16: return lookup<S, TBf16>(a, sm_count, s);
-    case kMxF16: return lookup<S, TF16>(a, sm_count, s);
-    case kMxF32: return lookup<S, TF32>(a, sm_count, s);
+    case kMxBf16: return lookup<S, TBf16>(a, s);
+    case kMxF16: return lookup<S, TF16>(a, s);
+    case kMxF32: return lookup<S, TF32>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
-template <class V, class T, bool kVec>
+template <bool kWhole>
+using DenseBf16 = Dense<TBf16, kWhole>;
+template <bool kWhole>
+using DenseF16 = Dense<TF16, kWhole>;
+template <bool kWhole>
+using DenseF32 = Dense<TF32, kWhole>;
+
+template <class D, class T, bool kWhole>
 cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, cudaStream_t s) {
   const int64_t units = (int64_t)g.count * g.slabs;
   if (units > 0x7FFFFFF0ll) return cudaErrorInvalidValue;
-  cudaError_t e = launch_kernel(embedding_segments_kernel<V, T, kVec>, (int)(z.ctas + (units + kSumWarps - 1) / kSumWarps),
+  cudaError_t e = launch_kernel(embedding_segments_kernel<D, T, kWhole>, (int)(z.ctas + (units + kSumWarps - 1) / kSumWarps),
                                 kSumThreads, 0, s, true, a, g, z, fast_div(g.slabs));
   if (e != cudaSuccess || g.count == 1) return e;
-  return launch_kernel(embedding_join_kernel<T, kVec>, (int)((g.count + 7) / 8 * g.slabs), kRowThreads, 0, s, true, a, g);
+  return launch_kernel(embedding_join_kernel<T, kWhole>, (int)((g.count + 7) / 8 * g.slabs), kRowThreads, 0, s, true, a, g);
 }
 
-template <class V>
+template <class D>
 cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && aligned(a.dy, a.ld_dy * element_bytes(a.type)) &&
                    aligned(a.dtable, a.ld * element_bytes(a.dtable_type));
   switch (a.dtable_type) {
-    case kMxBf16: return vec ? sum_rows<V, TBf16, true>(a, g, z, s) : sum_rows<V, TBf16, false>(a, g, z, s);
-    case kMxF16: return vec ? sum_rows<V, TF16, true>(a, g, z, s) : sum_rows<V, TF16, false>(a, g, z, s);
-    case kMxF32: return vec ? sum_rows<V, TF32, true>(a, g, z, s) : sum_rows<V, TF32, false>(a, g, z, s);
+    case kMxBf16: return vec ? sum_rows<D, TBf16, true>(a, g, z, s) : sum_rows<D, TBf16, false>(a, g, z, s);
+    case kMxF16: return vec ? sum_rows<D, TF16, true>(a, g, z, s) : sum_rows<D, TF16, false>(a, g, z, s);
+    case kMxF32: return vec ? sum_rows<D, TF32, true>(a, g, z, s) : sum_rows<D, TF32, false>(a, g, z, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -710,12 +719,12 @@ cudaError_t sort_in_cluster(ClusterSort c, cudaStream_t s) {
 
 int64_t embedding_backward_workspace(int64_t n, int64_t cols) { return space_of(n, cols).bytes; }
 
-cudaError_t launch_embedding(const EmbeddingArgs& a, int sm_count, cudaStream_t s) {
-  if (a.from.codes) return lookup<Mx4Rows>(a, sm_count, s);
+cudaError_t launch_embedding(const EmbeddingArgs& a, int, cudaStream_t s) {
+  if (a.from.codes) return lookup<Mx4Rows>(a, s);
   switch (a.type) {
-    case kMxBf16: return lookup<Dense<Vec16<Bf16>>>(a, sm_count, s);
-    case kMxF16: return lookup<Dense<Vec16<F16>>>(a, sm_count, s);
-    case kMxF32: return lookup<Dense<Vec32>>(a, sm_count, s);
+    case kMxBf16: return lookup<DenseBf16>(a, s);
+    case kMxF16: return lookup<DenseF16>(a, s);
+    case kMxF32: return lookup<DenseF32>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -768,9 +777,9 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_cou
   if (e != cudaSuccess) return e;
   g.keys = c.keys, g.pos = c.pos;
   switch (a.type) {
-    case kMxBf16: return sum_rows<Vec16<Bf16>>(a, g, z, s);
-    case kMxF16: return sum_rows<Vec16<F16>>(a, g, z, s);
-    case kMxF32: return sum_rows<Vec32>(a, g, z, s);
+    case kMxBf16: return sum_rows<TBf16>(a, g, z, s);
+    case kMxF16: return sum_rows<TF16>(a, g, z, s);
+    case kMxF32: return sum_rows<TF32>(a, g, z, s);
     default: return cudaErrorInvalidValue;
   }
 }

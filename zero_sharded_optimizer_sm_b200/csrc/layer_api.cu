@@ -102,7 +102,7 @@ zero_status zero_rms_norm(const void* x, const void* residual, int32_t dtype, in
   a.rows = rows, a.cols = cols;
   const bool one = rows == 1;
   a.ld_x = one ? cols : ld_x, a.ld_residual = one ? cols : ld_residual;
-  a.weight = weight, a.w_type = weight_dtype;
+  a.weight = weight, a.w_type = weight_dtype, a.w_aligned = (reinterpret_cast<uintptr_t>(weight) & 15u) == 0;
   a.eps = (float)eps;
   a.y = y, a.ld_y = one ? cols : ld_y;
   a.h = h, a.ld_h = one ? cols : ld_h;
@@ -150,7 +150,7 @@ zero_status zero_rms_norm_backward(const void* dy, int32_t dtype, int64_t rows, 
   a.ld_dy = one ? cols : ld_dy;
   a.h = h, a.ld_h = one ? cols : ld_h;
   if (h8) a.h8 = matrix8(*h8);
-  a.weight = weight, a.w_type = weight_dtype;
+  a.weight = weight, a.w_type = weight_dtype, a.w_aligned = (reinterpret_cast<uintptr_t>(weight) & 15u) == 0;
   a.rstd = rstd;
   a.dh = dh, a.ld_dh = one ? cols : ld_dh;
   a.dx = dx, a.ld_dx = one ? cols : ld_dx;

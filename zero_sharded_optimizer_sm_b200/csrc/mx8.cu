@@ -5,8 +5,8 @@
 // Both are memory-bound streams: per 16-bit element 2 + 33/32 bytes.
 #include <cuda_runtime.h>
 
-#include "mx4_quant.cuh"
 #include "mx8.cuh"
+#include "rows.cuh"
 
 namespace zsm {
 namespace {
@@ -14,118 +14,247 @@ namespace {
 using namespace mx;
 
 constexpr int kRowThreads = 256;
+constexpr int kUnits = 4;
 
-// A warp takes 256 consecutive columns of one row at a time, a lane 8 of them
-// and four lanes a block; V::kUnits such pieces go through each step side by
-// side.
-template <class V>
+// The pieces of 256 columns that a warp takes: kUnits consecutive ones of the
+// rows one after another, a lane eight columns of each and four lanes a block.
+// They go through every step side by side.
+struct Walk {
+  uint32_t row, piece, pieces;
+  __device__ __forceinline__ Walk(uint32_t unit, const FastDiv& per_row) : pieces(per_row.d) {
+    row = div_by(unit, per_row);
+    piece = unit - row * per_row.d;
+  }
+  __device__ __forceinline__ void next() {
+    if (++piece == pieces) piece = 0, ++row;
+  }
+  template <bool kWhole>
+  __device__ __forceinline__ Columns<kWhole> columns(int64_t cols) const {
+    return {256 * piece, threadIdx.x & 31, (uint32_t)cols};
+  }
+};
+
+template <class T, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads) mx8_quant_kernel(const __grid_constant__ Mx8QuantArgs a,
-                                                                const FastDiv per_row, const uint32_t units, const int vec) {
-  constexpr int kUnits = V::kUnits;
-  const typename V::raw* src = static_cast<const typename V::raw*>(a.src);
-  const uint32_t warps = gridDim.x * (kRowThreads / 32);
-  const int lane = threadIdx.x & 31;
-  const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
-  for (uint32_t u0 = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += kUnits * warps) {
-    V x[kUnits];
-    uint32_t row[kUnits];
-    int64_t col[kUnits];
+                                                                const FastDiv per_row, const uint32_t units) {
+  const uint32_t u0 = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kUnits;
+  if (u0 >= units) return;
+  Fetched<typename T::V, kWhole> f[kUnits];
+  const Span span = span_of<T>(a.src, a.rows, a.cols, a.ld);
+  Walk w(u0, per_row);
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const uint32_t u = min(u0 + k * warps, units - 1);  // past the end: the last piece again, not stored
-      row[k] = div_by(u, per_row);
-      col[k] = (int64_t)(u - row[k] * per_row.d) * 256 + lane * 8;
-      load8(x[k], src + row[k] * a.ld + col[k], a.cols - col[k], vec);
-    }
+  for (int k = 0; k < kUnits; ++k) {
+    if (u0 + k < units) fetch_columns(f[k], row_of<T>(a.src, w.row, a.ld), w.columns<kWhole>(a.cols), span);
+    w.next();
+  }
+  w = Walk(u0, per_row);
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const uint32_t s = scale_code8(max_of_four(x[k].max_bits()));
-      const int64_t b = col[k] >> 5;
+  for (int k = 0; k < kUnits; ++k) {
+    if (u0 + k < units) {
+      const Columns<kWhole> c = w.columns<kWhole>(a.cols);
+      typename T::V x;
       float v[8];
-      x[k].values(v);
-      if (b < nb && u0 + k * warps < units) {
-        *reinterpret_cast<uint2*>(a.out.codes + row[k] * a.out.code_pitch + col[k]) = encode8_mx8(v, s);
-        if ((lane & 3) == 0) a.out.scales[row[k] * a.out.scale_pitch + b] = (uint8_t)s;
-      }
+      take_columns(x, f[k], row_of<T>(a.src, w.row, a.ld), c);
+      x.values(v);
+      store_columns8(row_of(a.out, w.row), c, x, v);
+    }
+    w.next();
+  }
+}
+
+template <class T, bool kWhole>
+__global__ void __launch_bounds__(kRowThreads) mx8_dequant_kernel(const __grid_constant__ Mx8DequantArgs a,
+                                                                  const FastDiv per_row, const uint32_t units) {
+  const uint32_t u0 = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kUnits;
+  if (u0 >= units) return;
+  Fetched8 f[kUnits];
+  Walk w(u0, per_row);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    if (u0 + k < units) fetch_columns8(f[k], row_of(a.in, w.row), w.columns<kWhole>(a.in.cols));
+    w.next();
+  }
+  w = Walk(u0, per_row);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    if (u0 + k < units) {
+      const Columns<kWhole> c = w.columns<kWhole>(a.in.cols);
+      float v[8];
+      typename T::V x;
+      take_columns8(v, f[k], c, 1.0f);
+      finite_in<T>(v);
+      round_to(x, v);
+      store_columns(row_of<T>(a.dst, w.row, a.ld), c, x);
+    }
+    w.next();
+  }
+}
+
+// A matrix whose rows lie end to end in whole blocks, as most activations do,
+// is one long row: a lane takes sixteen neighbouring elements, two lanes a
+// block, and nothing but one address has to be worked out for them.
+constexpr int kFlat = 2;  // groups of 16 elements of a thread, side by side
+
+// The index of a thread's group k.
+__device__ __forceinline__ int64_t flat_at(int k) { return ((int64_t)blockIdx.x * kFlat + k) * kRowThreads + threadIdx.x; }
+
+template <class T>
+__device__ __forceinline__ void load16(typename T::V (&x)[2], const typename T::raw* p, bool wide) {
+  if constexpr (sizeof(typename T::raw) == 2) {
+    if (wide) {  // aligned to 32 bytes: one load
+      uint32_t *a = words(x[0]), *b = words(x[1]);
+      asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                   : "l"(p)
+                   : "memory");
+      return;
+    }
+  }
+  x[0].load(p);
+  x[1].load(p + 8);
+}
+template <class T>
+__device__ __forceinline__ void store16(typename T::raw* p, const typename T::V (&x)[2], bool wide) {
+  if constexpr (sizeof(typename T::raw) == 2) {
+    if (wide) {
+      const uint32_t *a = words(x[0]), *b = words(x[1]);
+      asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]),
+                   "r"(a[3]), "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
+                   : "memory");
+      return;
+    }
+  }
+  store_whole(p, words(x[0]));
+  store_whole(p + 8, words(x[1]));
+}
+
+template <class T>
+__global__ void __launch_bounds__(kRowThreads) mx8_quant_flat_kernel(const typename T::raw* src, uint8_t* codes,
+                                                                     uint8_t* scales, const int64_t groups, const bool wide) {
+  typename T::V x[kFlat][2];
+#pragma unroll
+  for (int k = 0; k < kFlat; ++k) {
+    const int64_t i = flat_at(k);
+    if (i < groups) load16<T>(x[k], src + 16 * i, wide);
+    else x[k][0].clear(), x[k][1].clear();
+  }
+#pragma unroll
+  for (int k = 0; k < kFlat; ++k) {
+    const int64_t i = flat_at(k);
+    uint32_t m = max(x[k][0].max_bits(), x[k][1].max_bits());
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    const uint32_t s = scale_code8(m);
+    float v[8], u[8];
+    x[k][0].values(v);
+    x[k][1].values(u);
+    const uint2 a = encode8_mx8(v, s), b = encode8_mx8(u, s);
+    if (i < groups) {
+      *reinterpret_cast<uint4*>(codes + 16 * i) = make_uint4(a.x, a.y, b.x, b.y);
+      if ((i & 1) == 0) scales[i >> 1] = (uint8_t)s;
     }
   }
 }
 
 template <class T>
-__global__ void __launch_bounds__(kRowThreads) mx8_dequant_kernel(const __grid_constant__ Mx8DequantArgs a,
-                                                                  const FastDiv per_row, const uint32_t units, const int vec) {
-  using raw = typename T::raw;
-  constexpr int kUnits = 4;
-  raw* dst = static_cast<raw*>(a.dst);
-  const uint32_t warps = gridDim.x * (kRowThreads / 32);
-  const int lane = threadIdx.x & 31;
-  for (uint32_t u0 = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += kUnits * warps) {
-    uint32_t s[kUnits], row[kUnits];
-    uint2 w[kUnits];
-    int64_t col[kUnits];
+__global__ void __launch_bounds__(kRowThreads) mx8_dequant_flat_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                       typename T::raw* dst, const int64_t groups,
+                                                                       const bool wide) {
+  uint4 w[kFlat];
+  uint32_t s[kFlat];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const uint32_t u = min(u0 + k * warps, units - 1);
-      row[k] = div_by(u, per_row);
-      col[k] = (int64_t)(u - row[k] * per_row.d) * 256 + lane * 8;
-      const int64_t at = min(col[k], a.in.cols - 1);  // lanes past the row read its last block, and store nothing
-      w[k] = __ldcs(reinterpret_cast<const uint2*>(a.in.codes + row[k] * a.in.code_pitch + (at & ~7ll)));
-      s[k] = a.in.scales[row[k] * a.in.scale_pitch + (at >> 5)];
-    }
+  for (int k = 0; k < kFlat; ++k) {
+    const int64_t i = flat_at(k);
+    if (i >= groups) continue;
+    w[k] = __ldcs(reinterpret_cast<const uint4*>(codes + 16 * i));
+    s[k] = scales[i >> 1];
+  }
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      float v[8];
-      values8_mx8(w[k], s[k], v);
-      finite_in<T>(v);
-      store8<T>(dst + row[k] * a.ld + col[k], v, u0 + k * warps < units ? a.in.cols - col[k] : 0, vec);
-    }
+  for (int k = 0; k < kFlat; ++k) {
+    const int64_t i = flat_at(k);
+    if (i >= groups) continue;
+    const float sc = scale_value(s[k]);
+    float v[8];
+    typename T::V x[2];
+    elements8(make_uint2(w[k].x, w[k].y), v);
+    scale8(v, sc);
+    finite_in<T>(v);
+    round_to(x[0], v);
+    elements8(make_uint2(w[k].z, w[k].w), v);
+    scale8(v, sc);
+    finite_in<T>(v);
+    round_to(x[1], v);
+    store16<T>(dst + 16 * i, x, wide);
   }
 }
 
-template <class V>
-cudaError_t quantize_from(Mx8QuantArgs a, int sm_count, cudaStream_t s) {
-  const bool flat = a.cols % kMxBlock == 0 && a.ld == a.cols && a.out.code_pitch == a.cols &&
-                    a.out.scale_pitch == a.cols / kMxBlock;
+// The launch over an MX8 matrix, with a dense one beside it.
+struct Launch {
+  FastDiv per_row;
+  uint32_t units;
+  bool flat, whole, wide;
+  unsigned grid;
+  int64_t groups;
+};
+template <class T>
+bool launch_of(const void* dense, int64_t ld, const Mx8Matrix& m, Launch* l) {
+  const int64_t b = sizeof(typename T::raw);
+  l->flat = m.cols % kMxBlock == 0 && ld == m.cols && m.code_pitch == m.cols && m.scale_pitch == m.cols / kMxBlock &&
+            aligned(dense, 0);
+  if (l->flat) {
+    l->groups = m.rows * m.cols / 16;
+    l->wide = (reinterpret_cast<uintptr_t>(dense) & 31u) == 0;
+    const int64_t grid = (l->groups + kFlat * kRowThreads - 1) / (kFlat * kRowThreads);
+    l->grid = (unsigned)grid;
+    return grid <= 0x7FFFFFFFll;
+  }
   Pieces p;
-  if (!pieces_of(a.rows, a.cols, flat, &p)) return cudaErrorInvalidValue;
-  a.rows = p.rows, a.cols = p.cols;
-  const int vec = aligned(a.src, flat ? 0 : a.ld * (int64_t)sizeof(typename V::raw)) ? 1 : 0;
-  const int per_cta = V::kUnits * kRowThreads / 32;
-  mx8_quant_kernel<V><<<cap_grid((p.units + per_cta - 1) / per_cta, kWaves * sm_count), kRowThreads, 0, s>>>(
-      a, p.per_row, p.units, vec);
+  if (!pieces_of(m.rows, m.cols, false, &p)) return false;
+  l->per_row = p.per_row, l->units = p.units;
+  l->whole = m.cols % 8 == 0 && aligned(dense, ld * b);
+  l->grid = (p.units + kUnits * kRowThreads / 32 - 1) / (kUnits * kRowThreads / 32);
+  return true;
+}
+
+template <class T>
+cudaError_t quantize_from(const Mx8QuantArgs& a, cudaStream_t s) {
+  Launch l;
+  if (!launch_of<T>(a.src, a.ld, a.out, &l)) return cudaErrorInvalidValue;
+  if (l.flat)
+    mx8_quant_flat_kernel<T><<<l.grid, kRowThreads, 0, s>>>(static_cast<const typename T::raw*>(a.src), a.out.codes,
+                                                            a.out.scales, l.groups, l.wide);
+  else if (l.whole) mx8_quant_kernel<T, true><<<l.grid, kRowThreads, 0, s>>>(a, l.per_row, l.units);
+  else mx8_quant_kernel<T, false><<<l.grid, kRowThreads, 0, s>>>(a, l.per_row, l.units);
   return cudaGetLastError();
 }
 
 template <class T>
-cudaError_t dequantize_to(Mx8DequantArgs a, int sm_count, cudaStream_t s) {
-  const bool flat = a.in.cols % kMxBlock == 0 && a.ld == a.in.cols && a.in.code_pitch == a.in.cols &&
-                    a.in.scale_pitch == a.in.cols / kMxBlock;
-  Pieces p;
-  if (!pieces_of(a.in.rows, a.in.cols, flat, &p)) return cudaErrorInvalidValue;
-  a.in.rows = p.rows, a.in.cols = p.cols;
-  const int vec = aligned(a.dst, flat ? 0 : a.ld * (int64_t)sizeof(typename T::raw)) ? 1 : 0;
-  const int per_cta = 4 * kRowThreads / 32;
-  mx8_dequant_kernel<T><<<cap_grid((p.units + per_cta - 1) / per_cta, kWaves * sm_count), kRowThreads, 0, s>>>(
-      a, p.per_row, p.units, vec);
+cudaError_t dequantize_to(const Mx8DequantArgs& a, cudaStream_t s) {
+  Launch l;
+  if (!launch_of<T>(a.dst, a.ld, a.in, &l)) return cudaErrorInvalidValue;
+  if (l.flat)
+    mx8_dequant_flat_kernel<T><<<l.grid, kRowThreads, 0, s>>>(a.in.codes, a.in.scales, static_cast<typename T::raw*>(a.dst),
+                                                              l.groups, l.wide);
+  else if (l.whole) mx8_dequant_kernel<T, true><<<l.grid, kRowThreads, 0, s>>>(a, l.per_row, l.units);
+  else mx8_dequant_kernel<T, false><<<l.grid, kRowThreads, 0, s>>>(a, l.per_row, l.units);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_mx8_quantize(const Mx8QuantArgs& a, int sm_count, cudaStream_t s) {
+cudaError_t launch_mx8_quantize(const Mx8QuantArgs& a, int, cudaStream_t s) {
   switch (a.type) {
-    case kMxBf16: return quantize_from<Vec16<Bf16>>(a, sm_count, s);
-    case kMxF16: return quantize_from<Vec16<F16>>(a, sm_count, s);
-    case kMxF32: return quantize_from<Vec32>(a, sm_count, s);
+    case kMxBf16: return quantize_from<TBf16>(a, s);
+    case kMxF16: return quantize_from<TF16>(a, s);
+    case kMxF32: return quantize_from<TF32>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
-cudaError_t launch_mx8_dequantize(const Mx8DequantArgs& a, int sm_count, cudaStream_t s) {
+cudaError_t launch_mx8_dequantize(const Mx8DequantArgs& a, int, cudaStream_t s) {
   switch (a.type) {
-    case kMxBf16: return dequantize_to<TBf16>(a, sm_count, s);
-    case kMxF16: return dequantize_to<TF16>(a, sm_count, s);
-    case kMxF32: return dequantize_to<TF32>(a, sm_count, s);
+    case kMxBf16: return dequantize_to<TBf16>(a, s);
+    case kMxF16: return dequantize_to<TF16>(a, s);
+    case kMxF32: return dequantize_to<TF32>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -14,26 +14,21 @@ namespace {
 
 using namespace mx;
 
-// Threads to a block: a block of more than 32 threads to a row has one row.
-template <int kGroup>
-constexpr int kBlockOf = kGroup > 128 ? kGroup : 128;
-
 // ----------------------------------------------------------------- forward --
 
-// Sum over the kGroup threads that share a row (a warp, or the whole block of
-// kGroup threads), from a warp's binary32 sum on in binary64: every thread gets
-// the same bits.
-template <int kGroup>
+// Sum over a warp, and from the warps' binary32 sums on in binary64 over the
+// block (kWarp: a warp has its own row): every thread gets the same bits.
+template <bool kWarp>
 __device__ __forceinline__ double group_sum(float mine, float* smem) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine = __fadd_rn(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
-  if constexpr (kGroup == 32) return (double)mine;
-  constexpr int kWarps = kGroup / 32;
+  if constexpr (kWarp) return (double)mine;
+  const uint32_t warps = blockDim.x / 32;
   if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = mine;
   __syncthreads();
   double v = 0.0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) v = __dadd_rn(v, (double)smem[w]);
+#pragma unroll 4
+  for (uint32_t w = 0; w < warps; ++w) v = __dadd_rn(v, (double)smem[w]);
   return v;
 }
 
@@ -61,14 +56,27 @@ struct NormRow {
         y(row_of<T>(a.y, row, a.ld_y)), h8(row_of(a.h8, row)), y8(row_of(a.y8, row)) {}
 };
 
-// A vector of one row of h: x plus the residual, rounded to their type.
-template <class T, class C>
-__device__ __forceinline__ void load_h(const RmsNormArgs& a, const NormRow<T>& row, const C& c, typename T::V& x) {
-  load_columns(x, row.x, c);
+// Vectors of one row of h: x plus the residual, rounded to their type.  All
+// loads go out before the first is waited for.
+template <class T, bool kWhole, int kN>
+__device__ __forceinline__ void load_h(const RmsNormArgs& a, const NormRow<T>& row, const Columns<kWhole> (&c)[kN],
+                                       typename T::V (&x)[kN]) {
+  Fetched<typename T::V, kWhole> fx[kN], fr[kN];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) fetch_columns(fx[k], row.x, c[k], span_of<T>(a.x, a.rows, a.cols, a.ld_x));
   if (a.residual) {
-    typename T::V r;
-    load_columns(r, row.r, c);
-    add_to(x, r);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) fetch_columns(fr[k], row.r, c[k], span_of<T>(a.residual, a.rows, a.cols, a.ld_residual));
+  }
+#pragma unroll
+  for (int k = 0; k < kN; ++k) take_columns(x[k], fx[k], row.x, c[k]);
+  if (a.residual) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      typename T::V r;
+      take_columns(r, fr[k], row.r, c[k]);
+      add_to(x[k], r);
+    }
   }
 }
 
@@ -87,7 +95,7 @@ __device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& r
   if (a.h) store_columns(row.h, c, x);
   if (a.h8.codes) store_columns8(row.h8, c, x, v);
   if (!a.y && !a.y8.codes) return;
-  load_weights(a.weight, a.w_type, c, w);
+  load_weights(a.weight, a.w_type, a.w_aligned, c, w);
   scale8(v, rstd);
   times8(v, w);
   typename T::V y;
@@ -105,20 +113,29 @@ __device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& r
   }
 }
 
-// kGroup threads to a row, kChunks vectors of eight elements a thread.
-template <class T, bool kVec, int kGroup, int kChunks>
-__global__ void __launch_bounds__(kBlockOf<kGroup>) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
-                                                                    const double inv_cols) {
-  constexpr int kRows = kBlockOf<kGroup> / kGroup;
+// A block to a row, or (kWarp) a warp, kChunks vectors of eight elements a
+// thread; the host picks the block's threads to fit the row.
+constexpr int kWarpRows = 4;  // of a block
+template <class T, bool kWhole, bool kWarp, int kChunks>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 512) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
+                                                                                const double inv_cols) {
   __shared__ float smem[32];
-  const uint32_t number = blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / kGroup : 0);
-  if (number >= (uint32_t)a.rows) return;  // whole groups
+  const uint32_t number = kWarp ? blockIdx.x * kWarpRows + threadIdx.x / 32 : blockIdx.x;
+  if (kWarp && number >= (uint32_t)a.rows) return;
   const NormRow<T> row(a, number);
-  const uint32_t t = threadIdx.x % kGroup, cols = (uint32_t)a.cols;
-  using C = Columns<kVec, kGroup>;
+  const uint32_t group = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  using C = Columns<kWhole>;
   typename T::V x[kChunks];
+  if constexpr (kChunks == 1) {
+    const C c[1] = {C(0, t, (uint32_t)a.cols)};
+    load_h<T>(a, row, c, x);
+  } else {
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) load_h<T>(a, row, C(8 * kGroup * k, t, cols), x[k]);
+    for (int k = 0; k < kChunks; k += 2) {
+      const C c[2] = {C(8 * group * k, t, (uint32_t)a.cols), C(8 * group * (k + 1), t, (uint32_t)a.cols)};
+      load_h<T>(a, row, c, reinterpret_cast<typename T::V(&)[2]>(x[k]));
+    }
+  }
   float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
@@ -126,37 +143,38 @@ __global__ void __launch_bounds__(kBlockOf<kGroup>) rms_norm_kernel(const __grid
     x[k].values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<kGroup>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  const float rstd = rstd_of(group_sum<kWarp>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
   if (a.rstd && t == 0) a.rstd[number] = rstd;
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) finish<T>(a, row, C(8 * kGroup * k, t, cols), rstd, x[k]);
+  for (int k = 0; k < kChunks; ++k) finish<T>(a, row, C(8 * group * k, t, (uint32_t)a.cols), rstd, x[k]);
 }
 
 // Rows too long for registers: read a second time (a thread reads its own
 // elements before it writes results in their place).
 constexpr int kLongThreads = 512;
-template <class T, bool kVec>
+template <class T, bool kWhole>
 __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __grid_constant__ RmsNormArgs a,
                                                                      const double inv_cols) {
   __shared__ float smem[32];
   const NormRow<T> row(a, blockIdx.x);
   const uint32_t cols = (uint32_t)a.cols;
-  using C = Columns<kVec, kLongThreads>;
+  using C = Columns<kWhole>;
   float2 ss = make_float2(0.0f, 0.0f);
   for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
-    typename T::V x;
+    typename T::V x[1];
+    const C c[1] = {C(first, threadIdx.x, cols)};
     float v[8];
-    load_h<T>(a, row, C(first, threadIdx.x, cols), x);
-    x.values(v);
+    load_h<T>(a, row, c, x);
+    x[0].values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<kLongThreads>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  const float rstd = rstd_of(group_sum<false>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
   for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
-    typename T::V x;
-    const C c(first, threadIdx.x, cols);
+    typename T::V x[1];
+    const C c[1] = {C(first, threadIdx.x, cols)};
     load_h<T>(a, row, c, x);
-    finish<T>(a, row, c, rstd, x);
+    finish<T>(a, row, c[0], rstd, x[0]);
   }
 }
 
@@ -166,35 +184,50 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __gri
 // part of dw in registers; the parts go to the workspace, one row of it a
 // block, and a second kernel adds them in order.
 //
-// Rows whose vectors are aligned come through a ring in shared memory, kStages
-// rows deep, by asynchronous copies: each thread fetches the elements that it
-// reads itself, so that nothing but its own copies has to be waited for, and
-// the sum over a row -- the one place where the block's threads meet -- never
-// holds up the loads of the next ones.
+// The rows come through a ring in shared memory, kStages rows deep, by
+// asynchronous copies: each thread fetches the words that it reads itself (of
+// an unaligned row one more than it has, which its neighbour fetches too), so
+// that nothing but its own copies has to be waited for, and the sum over a row
+// -- the one place where the block's threads meet -- never holds up the loads of
+// the next ones.
 constexpr int64_t kSms = 148;
+constexpr uint32_t kMaxThreads = 512;
 
-// Blocks at most, for rows of so many columns: as many as are there at a time.
-int64_t max_parts(int64_t cols) { return kSms * (cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1); }
-int64_t parts_of(int64_t rows, int64_t cols) { return std::max<int64_t>(1, std::min(rows, max_parts(cols))); }
+// Threads of a block and vectors of a thread for rows of so many columns.
+struct Shape {
+  uint32_t threads, chunks;
+};
+Shape shape_of(int64_t cols) {
+  const uint32_t vectors = (uint32_t)((cols + 7) / 8);
+  const uint32_t chunks = vectors <= kMaxThreads ? 1 : vectors <= 2 * kMaxThreads ? 2 : 4;
+  return {std::max(32u, ((vectors + chunks - 1) / chunks + 31) / 32 * 32), chunks};
+}
 
-// The longest rows that a block takes; longer ones go through memory twice.
-int64_t wide_from(int type) { return type == kMxF32 ? 8192 : 16384; }
+// Blocks to an SM, and blocks at most: as many as are there at a time (the
+// kernels' registers allow 1024 threads).
+uint32_t blocks_to_sm(const Shape& p) { return std::max(1u, std::min(1024 / p.threads / p.chunks, 16u)); }
+int64_t parts_of(int64_t rows, int64_t cols) {
+  return std::max<int64_t>(1, std::min(rows, kSms * blocks_to_sm(shape_of(cols))));
+}
 
-// Sum over the block (kGroup threads) in binary32; smem holds two rounds'
-// values, so that one barrier a round will do.
-template <int kGroup>
+// The longest rows of which two stages fit; longer ones go through memory twice.
+int64_t wide_from(int type, bool whole) { return (type == kMxF32 ? 4096 : 8192) * (whole ? 2 : 1); }
+
+// Sum over the block in binary32; smem holds two rounds' values, so that one
+// barrier a round will do.
 __device__ __forceinline__ float block_sum(float v, float (*smem)[32], int round) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  constexpr int kWarps = kGroup / 32;
-  const int lane = threadIdx.x & 31;
+  const uint32_t lane = threadIdx.x & 31, warps = blockDim.x / 32;
+  if (warps == 1) return v;
   if (lane == 0) smem[round & 1][threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < kWarps ? smem[round & 1][lane] : 0.0f;
+  v = lane < warps ? smem[round & 1][lane] : 0.0f;
 #pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = 8; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return __shfl_sync(0xFFFFFFFFu, v, 0);
 }
+static_assert(kMaxThreads <= 512, "sixteen warps at most are added");
 
 // One vector's part of a row's sum of g xh, and of dw; dy becomes g.
 __device__ __forceinline__ void add_vector(float (&dy)[8], const float (&xh)[8], const float (&w)[8], float2 (&acc)[4],
@@ -234,84 +267,88 @@ template <class C, class A>
 __device__ __forceinline__ void store_part(float* out, const C& c, const A& acc) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (c.in(j)) out[c.at(j)] = j & 1 ? acc[j >> 1].y : acc[j >> 1].x;
+    if (c.in(j)) out[c.first + j] = j & 1 ? acc[j >> 1].y : acc[j >> 1].x;
 }
 
 // One row's stage of the ring: dy, h, dh of every thread's vectors, 16 bytes of
 // each thread next to another's.
-template <class T, int kGroup, int kChunks, bool kMx8, bool kDh>
+template <class T, bool kWhole, int kChunks, bool kMx8, bool kDh>
 struct Ring {
   using V = typename T::V;
   using raw = typename T::raw;
-  static constexpr int kWords = sizeof(raw) / 2;        // 16-byte words of a vector
-  static constexpr int kPlane = kGroup * kChunks * 16;  // bytes of one word of all vectors
-  static constexpr int kH = kWords * kPlane;            // where h's begin
-  static constexpr int kD = kH + (kMx8 ? kPlane / 2 : kWords * kPlane);
-  static constexpr int kBytes = kD + (kDh ? kWords * kPlane : 0);
+  static constexpr int kWords = sizeof(raw) / 2 + (kWhole ? 0 : 1);  // 16-byte words fetched of a vector
+  static constexpr uint32_t kPlanes = kWords * (1 + (kMx8 ? 0 : 1) + (kDh ? 1 : 0));
+  // bytes of a stage for so many vectors, and where h's and dh's words begin
+  static __host__ __device__ __forceinline__ constexpr uint32_t bytes(uint32_t vectors) { return vectors * (16 * kPlanes + (kMx8 ? 8 : 0)); }
+  static __host__ __device__ __forceinline__ uint32_t h_at(uint32_t vectors) { return 16 * kWords * vectors * (kDh ? 2 : 1); }
+  static __host__ __device__ __forceinline__ uint32_t dh_at(uint32_t vectors) { return 16 * kWords * vectors; }
 
+  static __device__ __forceinline__ void fetch16(uint8_t* to, uint32_t vectors, const raw* row, const Columns<kWhole>& c,
+                                                 const void* m, int64_t rows, int64_t ld) {
+    if constexpr (kWhole) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) copy_async16(to + 16 * i * vectors, row + c.first + 16 / (int)sizeof(raw) * i);
+    } else {
+      const Span span = span_of<T>(m, rows, c.cols, ld);
+      const uintptr_t from = reinterpret_cast<uintptr_t>(row + c.first) & ~(uintptr_t)15;
+      const uintptr_t end = reinterpret_cast<uintptr_t>(row + c.cols);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uintptr_t at = from + 16 * i;
+        if (at >= end) break;
+        if (at >= span.lo && at + 16 <= span.hi) copy_async16_shared(to + 16 * i * vectors, at);
+        else *reinterpret_cast<uint4*>(to + 16 * i * vectors) = load_within<WordsOf<V>::kPer>(at, span);
+      }
+    }
+  }
   // Asks for a row (none past the end; the group is there all the same).
   static __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, int64_t row, uint8_t* to) {
     if (row < a.rows) {
-      const raw* dy = row_of<T>(a.dy, row, a.ld_dy);
-      const raw* h = row_of<T>(a.h, row, a.ld_h);
-      const raw* dh = row_of<T>(a.dh, row, a.ld_dh);
-      const uint8_t* h8 = a.h8.codes + row * a.h8.code_pitch;
+      const uint32_t vectors = blockDim.x * kChunks;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
-        const uint32_t v = kGroup * k + threadIdx.x;
-        if (8 * v >= (uint32_t)a.cols) break;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          constexpr int kIn = 16 / (int)sizeof(raw);
-          copy_async16(to + i * kPlane + 16 * v, dy + 8 * v + kIn * i);
-          if constexpr (!kMx8) copy_async16(to + kH + i * kPlane + 16 * v, h + 8 * v + kIn * i);
-          if constexpr (kDh) copy_async16(to + kD + i * kPlane + 16 * v, dh + 8 * v + kIn * i);
-        }
-        if constexpr (kMx8) copy_async8(to + kH + 8 * v, h8 + 8 * v);
+        const uint32_t v = blockDim.x * k + threadIdx.x;
+        const Columns<kWhole> c(0, v, (uint32_t)a.cols);
+        if (!c.any()) break;
+        fetch16(to + 16 * v, vectors, row_of<T>(a.dy, row, a.ld_dy), c, a.dy, a.rows, a.ld_dy);
+        if constexpr (kDh) fetch16(to + dh_at(vectors) + 16 * v, vectors, row_of<T>(a.dh, row, a.ld_dh), c, a.dh, a.rows, a.ld_dh);
+        if constexpr (kMx8) copy_async8(to + h_at(vectors) + 8 * v, a.h8.codes + row * a.h8.code_pitch + c.first);
+        else fetch16(to + h_at(vectors) + 16 * v, vectors, row_of<T>(a.h, row, a.ld_h), c, a.h, a.rows, a.ld_h);
       }
     }
     copy_async_commit();
   }
-  static __device__ __forceinline__ void read(const uint8_t* plane, int k, V& x) {
-    const uint8_t* p = plane + 16 * (kGroup * k + threadIdx.x);
-    uint4* w = reinterpret_cast<uint4*>(&x);
+  static __device__ __forceinline__ void read(const uint8_t* at, uint32_t vectors, const raw* row, const Columns<kWhole>& c, V& x) {
+    Fetched<V, kWhole> f;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const uint4*>(p + i * kPlane);
-  }
-  // xh of a vector.
-  static __device__ __forceinline__ void read_xh(const uint8_t* stage, int k, uint32_t scale, float rstd, float (&v)[8]) {
-    if constexpr (kMx8) {
-      elements8(*reinterpret_cast<const uint2*>(stage + kH + 8 * (kGroup * k + threadIdx.x)), v);
-      scale8(v, __fmul_rn(scale_value(scale), rstd));
-    } else {
-      V x;
-      read(stage + kH, k, x);
-      x.values(v);
-      scale8(v, rstd);
+    for (int i = 0; i < kWords; ++i) {
+      const uint4 w = *reinterpret_cast<const uint4*>(at + 16 * i * vectors);
+      f.w[4 * i] = w.x, f.w[4 * i + 1] = w.y, f.w[4 * i + 2] = w.z, f.w[4 * i + 3] = w.w;
     }
+    take_columns(x, f, row, c);
   }
 };
 
-// A row's vectors are whole and aligned here.  One vector a thread: xh and g
-// stay in registers over the sum; more: they are read and made a second time.
-template <class T, int kGroup, int kChunks, bool kMx8, bool kDh, int kStages>
-__global__ void __launch_bounds__(kGroup) rms_norm_backward_ring_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
-  using R = Ring<T, kGroup, kChunks, kMx8, kDh>;
-  using C = Columns<true, kGroup>;
+// One vector a thread: xh and g stay in registers over the sum; more: they are
+// read and made a second time.
+template <class T, bool kWhole, int kChunks, bool kMx8, bool kDh>
+__global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
+    rms_norm_backward_kernel(const __grid_constant__ RmsNormBackwardArgs a, const int stages) {
+  using R = Ring<T, kWhole, kChunks, kMx8, kDh>;
+  using C = Columns<kWhole>;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float smem[2][32];
   pdl_trigger();
   const int64_t step = gridDim.x;
-  const uint32_t cols = (uint32_t)a.cols;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) R::fetch(a, blockIdx.x + s * step, ring + s * R::kBytes);
+  const uint32_t cols = (uint32_t)a.cols, group = blockDim.x, vectors = group * kChunks, size = R::bytes(vectors);
+  for (int s = 0; s < stages - 1; ++s) R::fetch(a, blockIdx.x + s * step, ring + s * size);
   float2 acc[kChunks][4];
   float w[8];
 #pragma unroll
   for (int k = 0; k < kChunks; ++k)
 #pragma unroll
     for (int p = 0; p < 4; ++p) acc[k][p] = make_float2(0.0f, 0.0f);
-  if constexpr (kChunks == 1) load_weights(a.weight, a.w_type, C(0, threadIdx.x, cols), w);
+  if constexpr (kChunks == 1) load_weights(a.weight, a.w_type, a.w_aligned, C(0, threadIdx.x, cols), w);
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
   // the row's statistics and scales, a row ahead
   float next_rstd = 0.0f;
@@ -323,121 +360,68 @@ __global__ void __launch_bounds__(kGroup) rms_norm_backward_ring_kernel(const __
       const uint8_t* scales = a.h8.scales + row * a.h8.scale_pitch;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
-        const C c(8 * kGroup * k, threadIdx.x, cols);
-        if (c.in(0)) next_scale[k] = scales[c.first >> 5];
+        const C c(8 * group * k, threadIdx.x, cols);
+        if (c.any()) next_scale[k] = scales[c.first >> 5];
       }
     }
   };
   ahead(blockIdx.x);
-  uint32_t now = 0, later = (kStages - 1) * R::kBytes;  // the stages of this row and of the one to ask for
+  uint32_t now = 0, later = (stages - 1) * size;  // the stages of this row and of the one to ask for
   int round = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += step, ++round) {
-    R::fetch(a, row + (kStages - 1) * step, ring + later);
+    R::fetch(a, row + (stages - 1) * step, ring + later);
     later = now;
     const uint8_t* stage = ring + now;
-    now = now + R::kBytes == kStages * R::kBytes ? 0 : now + R::kBytes;
+    now = now + size == stages * size ? 0 : now + size;
     const float rstd = next_rstd;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) scale[k] = next_scale[k];
     ahead(row + step);
-    copy_async_wait<kStages - 1>();
+    if (stages == 4) copy_async_wait<3>();
+    else if (stages == 3) copy_async_wait<2>();
+    else copy_async_wait<1>();
     float2 dot = make_float2(0.0f, 0.0f);
     float g[8], xh[8];
-    auto vector = [&](int k, bool sums) {
-      const C c(8 * kGroup * k, threadIdx.x, cols);
-      typename T::V dy;
-      R::read(stage, k, dy);
-      dy.values(g);
-      R::read_xh(stage, k, scale[k], rstd, xh);
-      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, c, w);
+    auto vector = [&](int k, const C& c, bool sums) {
+      const uint32_t v = group * k + threadIdx.x;
+      typename T::V x;
+      R::read(stage + 16 * v, vectors, row_of<T>(a.dy, row, a.ld_dy), c, x);
+      x.values(g);
+      if constexpr (kMx8) {
+        take_columns8(xh, Fetched8{*reinterpret_cast<const uint2*>(stage + R::h_at(vectors) + 8 * v), scale[k]}, c, rstd);
+      } else {
+        R::read(stage + R::h_at(vectors) + 16 * v, vectors, row_of<T>(a.h, row, a.ld_h), c, x);
+        x.values(xh);
+        scale8(xh, rstd);
+      }
+      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, a.w_aligned, c, w);
       if (sums) add_vector(g, xh, w, acc[k], dot);
       else times8(g, w);
     };
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k)
-      if (C(8 * kGroup * k, threadIdx.x, cols).in(0)) vector(k, true);
-    const float mean = __fmul_rn(block_sum<kGroup>(__fadd_rn(dot.x, dot.y), smem, round), inv);
+    for (int k = 0; k < kChunks; ++k) {
+      const C c(8 * group * k, threadIdx.x, cols);
+      if (c.any()) vector(k, c, true);
+    }
+    const float mean = __fmul_rn(block_sum(__fadd_rn(dot.x, dot.y), smem, round), inv);
     typename T::raw* to = row_of<T>(a.dx, row, a.ld_dx);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * kGroup * k, threadIdx.x, cols);
-      if (!c.in(0)) break;
-      if constexpr (kChunks > 1) vector(k, false);
-      dx_vector(g, xh, rstd, mean);
+      const C c(8 * group * k, threadIdx.x, cols);
+      if (kWhole && !c.any()) break;
       typename T::V dh;
-      if constexpr (kDh) R::read(stage + R::kD, k, dh);
-      store_dx<T>(to, c, kDh ? &dh : nullptr, g);
-    }
-  }
-  float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, cols), acc[k]);
-}
-
-// Rows of any alignment, straight from memory.
-template <class T, bool kMx8, class C>
-__device__ __forceinline__ void load_dy_xh(const RmsNormBackwardArgs& a, int64_t row, const C& c, float rstd,
-                                           typename T::V& dy, float (&xh)[8]) {
-  load_columns(dy, row_of<T>(a.dy, row, a.ld_dy), c);
-  if constexpr (kMx8) {
-    load_columns8(row_of(a.h8, row), c, rstd, xh);
-  } else {
-    typename T::V x;
-    load_columns(x, row_of<T>(a.h, row, a.ld_h), c);
-    x.values(xh);
-    scale8(xh, rstd);
-  }
-}
-
-template <class T, class C>
-__device__ __forceinline__ void finish_dx(const RmsNormBackwardArgs& a, int64_t row, const C& c, float (&v)[8]) {
-  typename T::V dh;
-  if (a.dh) load_columns(dh, row_of<T>(a.dh, row, a.ld_dh), c);
-  store_dx<T>(row_of<T>(a.dx, row, a.ld_dx), c, a.dh ? &dh : nullptr, v);
-}
-
-template <class T, int kGroup, int kChunks, bool kMx8>
-__global__ void __launch_bounds__(kGroup) rms_norm_backward_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
-  using C = Columns<false, kGroup>;
-  __shared__ float smem[2][32];
-  pdl_trigger();
-  const uint32_t cols = (uint32_t)a.cols;
-  float2 acc[kChunks][4];
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-    for (int p = 0; p < 4; ++p) acc[k][p] = make_float2(0.0f, 0.0f);
-  const float inv = __fdiv_rn(1.0f, (float)a.cols);
-  int round = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++round) {
-    typename T::V dy[kChunks];
-    float xh[kChunks][8], w[8], g[8];
-    const float rstd = a.rstd[row];
-    float2 dot = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) load_dy_xh<T, kMx8>(a, row, C(8 * kGroup * k, threadIdx.x, cols), rstd, dy[k], xh[k]);
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      dy[k].values(g);
-      load_weights(a.weight, a.w_type, C(8 * kGroup * k, threadIdx.x, cols), w);
-      add_vector(g, xh[k], w, acc[k], dot);
-    }
-    const float mean = __fmul_rn(block_sum<kGroup>(__fadd_rn(dot.x, dot.y), smem, round), inv);
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * kGroup * k, threadIdx.x, cols);
-      if constexpr (kChunks > 1) {
-        dy[k].values(g);
-        load_weights(a.weight, a.w_type, c, w);
-        times8(g, w);
+      if (c.any()) {
+        if constexpr (kChunks > 1) vector(k, c, false);
+        dx_vector(g, xh, rstd, mean);
+        if constexpr (kDh)
+          R::read(stage + R::dh_at(vectors) + 16 * (group * k + threadIdx.x), vectors, row_of<T>(a.dh, row, a.ld_dh), c, dh);
       }
-      dx_vector(g, xh[k], rstd, mean);
-      finish_dx<T>(a, row, c, g);
+      store_dx<T>(to, c, kDh ? &dh : nullptr, g);  // (by whole warps)
     }
   }
   float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * kGroup * k, threadIdx.x, cols), acc[k]);
+  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * group * k, threadIdx.x, cols), acc[k]);
 }
 
 // Longer rows: the rows' dot products first (into the workspace's head), then
@@ -447,9 +431,32 @@ constexpr int kWideParts = 64;
 int64_t wide_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, kWideParts)); }
 int64_t dots_floats(int64_t rows) { return (rows + 3) / 4 * 4; }
 
-template <class T, bool kVec, bool kMx8>
+// dy and xh of a vector.
+template <class T, bool kMx8, bool kWhole>
+__device__ __forceinline__ void load_dy_xh(const RmsNormBackwardArgs& a, int64_t row, const Columns<kWhole>& c, float rstd,
+                                           float (&dy)[8], float (&xh)[8]) {
+  using V = typename T::V;
+  const typename T::raw *at = row_of<T>(a.dy, row, a.ld_dy), *h_at = row_of<T>(a.h, row, a.ld_h);
+  Fetched<V, kWhole> f, fh;
+  Fetched8 f8;
+  V x;
+  fetch_columns(f, at, c, span_of<T>(a.dy, a.rows, a.cols, a.ld_dy));
+  if constexpr (kMx8) fetch_columns8(f8, row_of(a.h8, row), c);
+  else fetch_columns(fh, h_at, c, span_of<T>(a.h, a.rows, a.cols, a.ld_h));
+  take_columns(x, f, at, c);
+  x.values(dy);
+  if constexpr (kMx8) {
+    take_columns8(xh, f8, c, rstd);
+  } else {
+    take_columns(x, fh, h_at, c);
+    x.values(xh);
+    scale8(xh, rstd);
+  }
+}
+
+template <class T, bool kWhole, bool kMx8>
 __global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
-  using C = Columns<kVec, kWideThreads>;
+  using C = Columns<kWhole>;
   __shared__ float smem[2][32];
   pdl_trigger();
   const int64_t row = blockIdx.x;
@@ -458,38 +465,34 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __gri
   float2 dot = make_float2(0.0f, 0.0f);
   for (uint32_t first = 0; first < cols; first += 8 * kWideThreads) {
     const C c(first, threadIdx.x, cols);
-    if (!c.in(0)) break;
-    typename T::V dy;
     float xh[8], w[8], d[8];
     float2 unused[4] = {};
-    load_dy_xh<T, kMx8>(a, row, c, rstd, dy, xh);
-    load_weights(a.weight, a.w_type, c, w);
-    dy.values(d);
+    load_dy_xh<T, kMx8>(a, row, c, rstd, d, xh);
+    load_weights(a.weight, a.w_type, a.w_aligned, c, w);
     add_vector(d, xh, w, unused, dot);
   }
-  const float all = block_sum<kWideThreads>(__fadd_rn(dot.x, dot.y), smem, 0);
+  const float all = block_sum(__fadd_rn(dot.x, dot.y), smem, 0);
   if (threadIdx.x == 0) static_cast<float*>(a.workspace)[row] = all;
 }
 
-template <class T, bool kVec, bool kMx8>
+template <class T, bool kWhole, bool kMx8>
 __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(const __grid_constant__ RmsNormBackwardArgs a,
                                                                               const int64_t dots) {
-  const Columns<kVec, kWideThreads> c(8u * kWideThreads * blockIdx.x, threadIdx.x, (uint32_t)a.cols);
+  const Columns<kWhole> c(8u * kWideThreads * blockIdx.x, threadIdx.x, (uint32_t)a.cols);
   pdl_trigger();
-  if (!c.in(0)) return;
   float2 acc[4] = {}, unused = make_float2(0.0f, 0.0f);
   float w[8];
-  load_weights(a.weight, a.w_type, c, w);
+  load_weights(a.weight, a.w_type, a.w_aligned, c, w);
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    typename T::V dy;
+    typename T::V dh;
     float xh[8], g[8];
     const float rstd = a.rstd[row];
-    load_dy_xh<T, kMx8>(a, row, c, rstd, dy, xh);
-    dy.values(g);
+    load_dy_xh<T, kMx8>(a, row, c, rstd, g, xh);
+    if (a.dh) load_columns(dh, row_of<T>(a.dh, row, a.ld_dh), c, span_of<T>(a.dh, a.rows, a.cols, a.ld_dh));
     add_vector(g, xh, w, acc, unused);
     dx_vector(g, xh, rstd, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv));
-    finish_dx<T>(a, row, c, g);
+    store_dx<T>(row_of<T>(a.dx, row, a.ld_dx), c, a.dh ? &dh : nullptr, g);
   }
   store_part(static_cast<float*>(a.workspace) + dots + blockIdx.y * a.cols, c, acc);
 }
@@ -519,24 +522,20 @@ __global__ void __launch_bounds__(32 * kDwWarps) rms_norm_dw_kernel(const float*
 
 // ------------------------------------------------------------------ launch --
 
-template <class T, bool kVec, int kGroup, int kChunks>
+// A warp to a row up to 512 columns; above, a block of as many threads as the
+// row has vectors, or half or a quarter of them.
+template <class T, bool kWhole>
 cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
-  constexpr int kRows = kBlockOf<kGroup> / kGroup;
-  rms_norm_kernel<T, kVec, kGroup, kChunks><<<(unsigned)((a.rows + kRows - 1) / kRows), kBlockOf<kGroup>, 0, s>>>(
-      a, 1.0 / (double)a.cols);
-  return cudaGetLastError();
-}
-
-template <class T, bool kVec>
-cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
-  if (a.cols <= 256) return forward<T, kVec, 32, 1>(a, s);
-  if (a.cols <= 512) return forward<T, kVec, 32, 2>(a, s);
-  if (a.cols <= 1024) return forward<T, kVec, 128, 1>(a, s);
-  if (a.cols <= 2048) return forward<T, kVec, 256, 1>(a, s);
-  if (a.cols <= 4096) return forward<T, kVec, 256, 2>(a, s);
-  if (a.cols <= 8192) return forward<T, kVec, 512, 2>(a, s);
-  if (a.cols <= 16384) return forward<T, kVec, 512, 4>(a, s);
-  rms_norm_long_kernel<T, kVec><<<(unsigned)a.rows, kLongThreads, 0, s>>>(a, 1.0 / (double)a.cols);
+  const double inv = 1.0 / (double)a.cols;
+  const unsigned rows = (unsigned)a.rows, warps = (rows + kWarpRows - 1) / kWarpRows;
+  const uint32_t vectors = (uint32_t)((a.cols + 7) / 8);
+  auto threads = [&](uint32_t chunks) { return ((vectors + chunks - 1) / chunks + 31) / 32 * 32; };
+  if (vectors <= 32) rms_norm_kernel<T, kWhole, true, 1><<<warps, 32 * kWarpRows, 0, s>>>(a, inv);
+  else if (vectors <= 64) rms_norm_kernel<T, kWhole, true, 2><<<warps, 32 * kWarpRows, 0, s>>>(a, inv);
+  else if (vectors <= 256) rms_norm_kernel<T, kWhole, false, 1><<<rows, threads(1), 0, s>>>(a, inv);
+  else if (vectors <= 1024) rms_norm_kernel<T, kWhole, false, 2><<<rows, threads(2), 0, s>>>(a, inv);
+  else if (vectors <= 2048) rms_norm_kernel<T, kWhole, false, 4><<<rows, threads(4), 0, s>>>(a, inv);
+  else rms_norm_long_kernel<T, kWhole><<<rows, kLongThreads, 0, s>>>(a, inv);
   return cudaGetLastError();
 }
 
@@ -544,9 +543,9 @@ template <class T>
 cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
   const int64_t b = sizeof(typename T::raw);
   auto fits = [&](const void* p, int64_t ld) { return !p || aligned(p, ld * b); };
-  const bool vec = a.cols % 8 == 0 && fits(a.x, a.ld_x) && fits(a.residual, a.ld_residual) && fits(a.y, a.ld_y) && fits(a.h, a.ld_h) &&
-                   aligned(a.weight, 0);
-  return vec ? forward<T, true>(a, s) : forward<T, false>(a, s);
+  const bool whole = a.cols % 8 == 0 && fits(a.x, a.ld_x) && fits(a.residual, a.ld_residual) && fits(a.y, a.ld_y) &&
+                     fits(a.h, a.ld_h) && a.w_aligned;
+  return whole ? forward<T, true>(a, s) : forward<T, false>(a, s);
 }
 
 cudaError_t add_dw(const RmsNormBackwardArgs& a, int64_t first, int64_t parts, cudaStream_t s) {
@@ -554,59 +553,54 @@ cudaError_t add_dw(const RmsNormBackwardArgs& a, int64_t first, int64_t parts, c
                        static_cast<const float*>(a.workspace) + first, parts, a.cols, a.dw, a.dw_type);
 }
 
-template <class T, bool kMx8, int kGroup, int kChunks, bool kDh>
-cudaError_t backward_ring(const RmsNormBackwardArgs& a, int64_t parts, cudaStream_t s) {
-  // as deep as lets the blocks of max_parts fit an SM together
-  constexpr int kStage = Ring<T, kGroup, kChunks, kMx8, kDh>::kBytes;
-  constexpr int kShare = 220 * 1024 / (kGroup <= 128 ? 8 : kGroup <= 256 ? 4 : kChunks == 1 ? 2 : 1);
-  constexpr int kStages = kShare / kStage < 2 ? 2 : kShare / kStage > 5 ? 5 : kShare / kStage;
-  static_assert(kStages * kStage <= 220 * 1024, "the ring fits");
-  auto kernel = rms_norm_backward_ring_kernel<T, kGroup, kChunks, kMx8, kDh, kStages>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kStage);
+template <class T, bool kMx8, bool kWhole, int kChunks, bool kDh>
+cudaError_t backward(const RmsNormBackwardArgs& a, const Shape& p, cudaStream_t s) {
+  // as deep as lets the blocks of parts_of fit an SM together
+  constexpr int kRoom = 220 * 1024;
+  const int stage = (int)Ring<T, kWhole, kChunks, kMx8, kDh>::bytes(p.threads * kChunks);
+  const int stages = std::max(2, std::min(4, kRoom / (int)blocks_to_sm(p) / stage));
+  if (stages * stage > kRoom) return cudaErrorInvalidValue;
+  auto kernel = rms_norm_backward_kernel<T, kWhole, kChunks, kMx8, kDh>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)parts, kGroup, kStages * kStage, s>>>(a);
-  return cudaGetLastError();
-}
-
-template <class T, bool kMx8, int kGroup, int kChunks>
-cudaError_t backward(const RmsNormBackwardArgs& a, bool vec, cudaStream_t s) {
   const int64_t parts = parts_of(a.rows, a.cols);
-  cudaError_t e;
-  if (vec) {
-    e = a.dh ? backward_ring<T, kMx8, kGroup, kChunks, true>(a, parts, s)
-             : backward_ring<T, kMx8, kGroup, kChunks, false>(a, parts, s);
-  } else {
-    rms_norm_backward_kernel<T, kGroup, kChunks, kMx8><<<(unsigned)parts, kGroup, 0, s>>>(a);
-    e = cudaGetLastError();
-  }
-  return e == cudaSuccess ? add_dw(a, 0, parts, s) : e;
+  kernel<<<(unsigned)parts, p.threads, stages * stage, s>>>(a, stages);
+  const cudaError_t r = cudaGetLastError();
+  return r == cudaSuccess ? add_dw(a, 0, parts, s) : r;
 }
 
-template <class T, bool kMx8, bool kVec>
+template <class T, bool kMx8, bool kWhole, int kChunks>
+cudaError_t backward(const RmsNormBackwardArgs& a, const Shape& p, cudaStream_t s) {
+  return a.dh ? backward<T, kMx8, kWhole, kChunks, true>(a, p, s) : backward<T, kMx8, kWhole, kChunks, false>(a, p, s);
+}
+
+template <class T, bool kMx8, bool kWhole>
 cudaError_t backward_wide(const RmsNormBackwardArgs& a, cudaStream_t s) {
   const int64_t dots = dots_floats(a.rows), parts = wide_parts(a.rows);
-  rms_norm_dots_kernel<T, kVec, kMx8><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
+  rms_norm_dots_kernel<T, kWhole, kMx8><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
   const dim3 grid((unsigned)((a.cols + 8 * kWideThreads - 1) / (8 * kWideThreads)), (unsigned)parts);
-  rms_norm_backward_wide_kernel<T, kVec, kMx8><<<grid, kWideThreads, 0, s>>>(a, dots);
+  rms_norm_backward_wide_kernel<T, kWhole, kMx8><<<grid, kWideThreads, 0, s>>>(a, dots);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? add_dw(a, dots, parts, s) : e;
+}
+
+template <class T, bool kMx8, bool kWhole>
+cudaError_t backward(const RmsNormBackwardArgs& a, cudaStream_t s) {
+  const Shape p = shape_of(a.cols);
+  if (a.cols > wide_from(a.type, kWhole)) return backward_wide<T, kMx8, kWhole>(a, s);
+  if (p.chunks == 1) return backward<T, kMx8, kWhole, 1>(a, p, s);
+  if (p.chunks == 2) return backward<T, kMx8, kWhole, 2>(a, p, s);
+  if constexpr (kWhole && sizeof(typename T::raw) == 2) return backward<T, kMx8, kWhole, 4>(a, p, s);
+  return cudaErrorInvalidValue;
 }
 
 template <class T, bool kMx8>
 cudaError_t backward(const RmsNormBackwardArgs& a, cudaStream_t s) {
   const int64_t b = sizeof(typename T::raw);
   auto fits = [&](const void* p, int64_t ld) { return !p || aligned(p, ld * b); };
-  const bool vec = a.cols % 8 == 0 && fits(a.dy, a.ld_dy) && fits(a.h, a.ld_h) && fits(a.dh, a.ld_dh) &&
-                   fits(a.dx, a.ld_dx) && aligned(a.weight, 0);
-  if (a.cols > wide_from(a.type)) return vec ? backward_wide<T, kMx8, true>(a, s) : backward_wide<T, kMx8, false>(a, s);
-  if (a.cols <= 256) return backward<T, kMx8, 32, 1>(a, vec, s);
-  if (a.cols <= 512) return backward<T, kMx8, 64, 1>(a, vec, s);
-  if (a.cols <= 1024) return backward<T, kMx8, 128, 1>(a, vec, s);
-  if (a.cols <= 2048) return backward<T, kMx8, 256, 1>(a, vec, s);
-  if (a.cols <= 4096) return backward<T, kMx8, 512, 1>(a, vec, s);
-  if (a.cols <= 8192) return backward<T, kMx8, 512, 2>(a, vec, s);
-  if constexpr (sizeof(typename T::raw) == 2) return backward<T, kMx8, 512, 4>(a, vec, s);
-  return cudaErrorInvalidValue;
+  const bool whole = a.cols % 8 == 0 && fits(a.dy, a.ld_dy) && fits(a.h, a.ld_h) && fits(a.dh, a.ld_dh) &&
+                     fits(a.dx, a.ld_dx) && a.w_aligned;
+  return whole ? backward<T, kMx8, true>(a, s) : backward<T, kMx8, false>(a, s);
 }
 
 template <class T>
@@ -617,9 +611,9 @@ cudaError_t backward(const RmsNormBackwardArgs& a, cudaStream_t s) {
 }  // namespace
 
 int64_t rms_norm_backward_workspace(int64_t rows, int64_t cols) {
-  // for every type: binary32's rows go through memory twice from 8192 columns on
+  // whatever the type and alignment, on which it depends whether rows go through memory twice
   const int64_t once = parts_of(rows, cols) * cols, twice = dots_floats(rows) + wide_parts(rows) * cols;
-  return 4 * (cols <= wide_from(kMxF32) ? once : cols <= wide_from(kMxBf16) ? std::max(once, twice) : twice);
+  return 4 * (cols <= wide_from(kMxF32, false) ? once : cols <= wide_from(kMxBf16, true) ? std::max(once, twice) : twice);
 }
 
 cudaError_t launch_rms_norm(const RmsNormArgs& a, int, cudaStream_t s) {

@@ -17,6 +17,7 @@ struct RmsNormArgs {
   int64_t rows, cols, ld_x, ld_residual;
   const void* weight;
   int w_type;
+  bool w_aligned;  // to 16 bytes
   float eps;
   void *y, *h;  // of `type`; any of the five results may be null (or have null codes)
   int64_t ld_y, ld_h;
@@ -31,6 +32,7 @@ struct RmsNormBackwardArgs {
   Mx8Matrix h8;
   const void* weight;
   int w_type;
+  bool w_aligned;  // to 16 bytes
   const float* rstd;
   void *dx, *dw;
   int64_t ld_dx;

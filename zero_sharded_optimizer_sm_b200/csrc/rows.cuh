@@ -1,5 +1,6 @@
-// A thread's eight columns of a row, and their loads and stores, for kernels
-// that give a row to a group of threads (rms_norm.cu, embedding.cu).
+// A thread's eight columns of a row, and their loads and stores at any
+// alignment, for kernels that give neighbouring vectors of a row to the lanes of
+// a warp (mx8.cu, rms_norm.cu, embedding.cu).
 #pragma once
 
 #include "mx4_quant.cuh"
@@ -8,30 +9,17 @@
 namespace zsm {
 namespace mx {
 
-// Neighbours where a row is made of whole, 16-byte aligned vectors of eight
-// (kVec), every kStride-th column otherwise, so that a warp's loads of single
-// elements are whole sectors and 32 columns, a block of an MX matrix, lie
-// across its lanes.  Rows are given by their address and columns in 32 bits:
+// Eight neighbouring columns.  kWhole: the row is made of whole, 16-byte
+// aligned vectors.  Rows are given by their address and columns in 32 bits:
 // these kernels are bound by instructions as much as by memory, and 64-bit
 // products of rows and pitches for every access were a third of them.
-template <bool kVec, int kStride>
+template <bool kWhole>
 struct Columns {
   uint32_t first, cols;
-  __device__ __forceinline__ Columns(uint32_t base, uint32_t thread, uint32_t n)
-      : first(base + (kVec ? 8 * thread : thread)), cols(n) {}
-  __device__ __forceinline__ uint32_t at(int j) const { return kVec ? first + j : first + kStride * j; }
-  __device__ __forceinline__ bool in(int j) const { return kVec ? first < cols : at(j) < cols; }
+  __device__ __forceinline__ Columns(uint32_t base, uint32_t vector, uint32_t n) : first(base + 8 * vector), cols(n) {}
+  __device__ __forceinline__ bool any() const { return first < cols; }
+  __device__ __forceinline__ bool in(int j) const { return kWhole ? first < cols : first + j < cols; }
 };
-
-template <class F>
-__device__ __forceinline__ void set(Vec16<F>& x, const uint16_t (&e)[8]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x.w[j] = pack2(e[2 * j], e[2 * j + 1]);
-}
-__device__ __forceinline__ void set(Vec32& x, const float (&e)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x.x[j] = e[j];
-}
 
 // A matrix's row.
 template <class T>
@@ -49,42 +37,200 @@ __device__ __forceinline__ Row8 row_of(const Mx8Matrix& m, int64_t row) {
   return {m.codes + row * m.code_pitch, m.scales + row * m.scale_pitch};
 }
 
-// The row's elements at a thread's columns, 0 past its end.
-template <class V, bool kVec, int kStride>
-__device__ __forceinline__ void load_columns(V& x, const typename V::raw* row, const Columns<kVec, kStride>& c) {
-  if constexpr (kVec) {
-    if (c.in(0)) x.load(row + c.first);
-    else x.clear();
-  } else {
-    typename V::raw e[8];
+// Rows that are not aligned (every row but the first of a matrix with an odd
+// number of columns) are read in their aligned 16-byte words all the same: a
+// lane reads the word that its vector begins in and the next one, most of
+// which is in L1 then, and shifts the two by the row's offset, which is the
+// same for all lanes.  (Loading a vector as eight elements took four times the
+// instructions.)  A word may reach past the row's ends, into what lies before
+// or after it in the matrix; those elements are dropped, whatever another
+// block is writing there.  It never reaches past the matrix: such a word is
+// read element by element.
+
+// Words of kPer elements each, moved down by `by` elements (less than four words).
+template <int kWords, int kPer>
+__device__ __forceinline__ void shift_down(uint32_t (&w)[kWords], uint32_t by) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = c.in(j) ? __ldcs(row + c.at(j)) : typename V::raw(0);
-    set(x, e);
+  for (int i = 0; i + 2 < kWords; ++i) w[i] = by & (2u * kPer) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i + 1 < kWords; ++i) w[i] = by & kPer ? w[i + 1] : w[i];
+  if constexpr (kPer == 2) {
+    const uint32_t bits = 16u * (by & 1u);
+#pragma unroll
+    for (int i = 0; i + 1 < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
   }
 }
 
-// A vector as it is.
-template <class F, bool kVec, int kStride>
-__device__ __forceinline__ void store_columns(uint16_t* row, const Columns<kVec, kStride>& c, const Vec16<F>& x) {
-  if constexpr (kVec) {
-    if (c.in(0)) st_stream(row + c.first, make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]));
-  } else {
+template <class V>
+struct WordsOf;  // how a vector lies in words
+template <class F>
+struct WordsOf<Vec16<F>> {
+  static constexpr int kN = 4, kPer = 2;
+};
+template <>
+struct WordsOf<Vec32> {
+  static constexpr int kN = 8, kPer = 1;
+};
+template <class V>
+__device__ __forceinline__ uint32_t (&words(V& x))[WordsOf<V>::kN] {
+  return reinterpret_cast<uint32_t(&)[WordsOf<V>::kN]>(x);
+}
+template <class V>
+__device__ __forceinline__ const uint32_t (&words(const V& x))[WordsOf<V>::kN] {
+  return reinterpret_cast<const uint32_t(&)[WordsOf<V>::kN]>(x);
+}
+
+// The elements by which a row is past a 16-byte boundary.
+template <class raw>
+__device__ __forceinline__ uint32_t offset_of(const raw* row) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u) / (uint32_t)sizeof(raw);
+}
+
+// A matrix's memory, from its first to behind its last element.
+struct Span {
+  uintptr_t lo, hi;
+};
+template <class T>
+__device__ __forceinline__ Span span_of(const void* m, int64_t rows, int64_t cols, int64_t ld) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(m);
+  return {lo, lo + sizeof(typename T::raw) * ((rows - 1) * ld + cols)};
+}
+
+// A vector as it was loaded: its words, and the ones after them for an
+// unaligned row.
+template <class V, bool kWhole>
+struct Fetched {
+  static constexpr int kN = WordsOf<V>::kN, kAll = kWhole ? kN : kN + 4;
+  uint32_t w[kAll];
+};
+
+// Sixteen bytes at an aligned address, of which only those within the span are
+// read.
+template <int kPer>
+__device__ __noinline__ uint4 load_within(uintptr_t at, Span m) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int j = 0; j < 4 * kPer; ++j) {
+    const uintptr_t p = at + (4 / kPer) * j;
+    if (p < m.lo || p >= m.hi) continue;
+    const uint32_t e = kPer == 2 ? *reinterpret_cast<const uint16_t*>(p) : *reinterpret_cast<const uint32_t*>(p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c.in(j)) row[c.at(j)] = (uint16_t)(x.w[j >> 1] >> (16 * (j & 1)));
+    for (int i = 0; i < 4; ++i)
+      if (i == j / kPer) w[i] |= kPer == 2 ? e << (16 * (j & 1)) : e;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <class V, bool kWhole>
+__device__ __forceinline__ void fetch_columns(Fetched<V, kWhole>& f, const typename V::raw* row, const Columns<kWhole>& c,
+                                              const Span& m) {
+  constexpr int kN = Fetched<V, kWhole>::kN;
+  if constexpr (kWhole) {
+    V x;
+    if (c.any()) x.load(row + c.first);
+    else x.clear();
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f.w[i] = words(x)[i];
+  } else {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(row + c.first) & ~(uintptr_t)15;
+    const uintptr_t end = reinterpret_cast<uintptr_t>(row + c.cols);  // of the row
+#pragma unroll
+    for (int i = 0; i < kN / 4 + 1; ++i) {
+      const uintptr_t at = from + 16 * i;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (at < end) {
+        if (at >= m.lo && at + 16 <= m.hi) x = *reinterpret_cast<const uint4*>(at);
+        else x = load_within<WordsOf<V>::kPer>(at, m);
+      }
+      f.w[4 * i] = x.x, f.w[4 * i + 1] = x.y, f.w[4 * i + 2] = x.z, f.w[4 * i + 3] = x.w;
+    }
   }
 }
-template <bool kVec, int kStride>
-__device__ __forceinline__ void store_columns(float* row, const Columns<kVec, kStride>& c, const Vec32& x) {
-  if constexpr (kVec) {
-    if (c.in(0)) {
-      st_stream(row + c.first, make_float4(x.x[0], x.x[1], x.x[2], x.x[3]));
-      st_stream(row + c.first + 4, make_float4(x.x[4], x.x[5], x.x[6], x.x[7]));
-    }
-  } else {
+
+// The vector: 0 past the row's end.
+template <class V, bool kWhole>
+__device__ __forceinline__ void take_columns(V& x, Fetched<V, kWhole>& f, const typename V::raw* row, const Columns<kWhole>& c) {
+  constexpr int kN = Fetched<V, kWhole>::kN, kPer = WordsOf<V>::kPer;
+  if constexpr (!kWhole) shift_down<kN + 4, kPer>(f.w, offset_of(row));
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c.in(j)) row[c.at(j)] = x.x[j];
+  for (int i = 0; i < kN; ++i) words(x)[i] = f.w[i];
+  if constexpr (!kWhole) {
+    if (!c.in(7)) {
+      const uint32_t left = c.any() ? c.cols - c.first : 0u;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        if (kPer * i >= (int)left) words(x)[i] = 0u;
+        else if (kPer == 2 && 2 * i + 1 >= (int)left) words(x)[i] &= 0xFFFFu;
+      }
+    }
+  }
+}
+
+// Both at once.
+template <class V, bool kWhole>
+__device__ __forceinline__ void load_columns(V& x, const typename V::raw* row, const Columns<kWhole>& c, const Span& m) {
+  Fetched<V, kWhole> f;
+  fetch_columns(f, row, c, m);
+  take_columns(x, f, row, c);
+}
+
+// A vector as it is, into its row: an unaligned one's words are put together
+// from two neighbouring lanes' vectors; the row's ends and what a warp's first
+// and last lanes lack a neighbour for go element by element.  Called by whole
+// warps whose lanes have neighbouring vectors.
+__device__ __forceinline__ void store_whole(uint16_t* p, const uint32_t (&w)[4]) {
+  st_stream(p, make_uint4(w[0], w[1], w[2], w[3]));
+}
+__device__ __forceinline__ void store_whole(float* p, const uint32_t (&w)[8]) {
+  // one 32-byte store where that is aligned: of two of 16 each would touch every sector of the warp's
+  if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+    return;
+  }
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+}
+__device__ __forceinline__ void store_some(uint16_t* p, const uint32_t (&w)[4], int from, int to) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j >= from && j < to) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+}
+__device__ __forceinline__ void store_some(float* p, const uint32_t (&w)[8], int from, int to) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j >= from && j < to) p[j] = __uint_as_float(w[j]);
+}
+template <class V, bool kWhole>
+__device__ __forceinline__ void store_columns(typename V::raw* row, const Columns<kWhole>& c, const V& x) {
+  constexpr int kN = WordsOf<V>::kN;
+  if constexpr (kWhole) {
+    if (c.any()) store_whole(row + c.first, words(x));
+  } else {
+    const uint32_t off = offset_of(row);
+    const int left = c.any() ? (int)min(c.cols - c.first, 8u) : 0;  // my elements
+    if (off == 0) {
+      if (left == 8) store_whole(row + c.first, words(x));
+      else store_some(row + c.first, words(x), 0, left);
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    // the neighbour's last elements before mine: the words from 8 - off on of
+    // both vectors one after another
+    uint32_t w[kN + 4], out[kN];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xFFFFFFFFu, words(x)[kN - 4 + i], 1);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) w[4 + i] = words(x)[i];
+    shift_down<kN + 4, WordsOf<V>::kPer>(w, 4 * WordsOf<V>::kPer - off);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) out[i] = w[i];
+    // elements -off .. 7 - off of mine: all of them, or those that are there
+    const int end = min((int)off + (c.any() ? left : min((int)(c.cols - c.first), 0)), 8);
+    if (lane > 0 && end == 8) store_whole(row + c.first - off, out);
+    else store_some(row + (int64_t)c.first - off, out, lane > 0 ? 0 : (int)off, end);
+    if (lane == 31 && left + (int)off > 8) store_some(row + c.first, words(x), 8 - (int)off, left);
   }
 }
 
@@ -117,76 +263,56 @@ __device__ __forceinline__ void elements8(uint2 w, float (&v)[8]) {
   }
 }
 
-// An MX8 row's values at a thread's columns, 0 past its end, in multiples of
-// `unit` (a power of two or any other number: one rounding).
-template <bool kVec, int kStride>
-__device__ __forceinline__ void load_columns8(const Row8& row, const Columns<kVec, kStride>& c, float unit, float (&v)[8]) {
-  if constexpr (kVec) {
-    uint2 w = make_uint2(0u, 0u);
-    uint32_t s = 0u;
-    if (c.in(0)) {
-      w = __ldcs(reinterpret_cast<const uint2*>(row.codes + c.first));
-      s = row.scales[c.first >> 5];
-    }
-    elements8(w, v);
-    scale8(v, __fmul_rn(scale_value(s), unit));
-  } else {
-    uint32_t w[8], s[8];
+// An MX8 row's codes and scale byte at a thread's columns.
+struct Fetched8 {
+  uint2 w;
+  uint32_t s;
+};
+template <bool kWhole>
+__device__ __forceinline__ void fetch_columns8(Fetched8& f, const Row8& row, const Columns<kWhole>& c) {
+  f.w = make_uint2(0u, 0u), f.s = 0u;
+  if (!c.any()) return;
+  f.w = __ldcs(reinterpret_cast<const uint2*>(row.codes + c.first));
+  f.s = row.scales[c.first >> 5];
+}
+// Its values, 0 past its end, in multiples of `unit` (a power of two or any
+// other number: one rounding).
+template <bool kWhole>
+__device__ __forceinline__ void take_columns8(float (&v)[8], const Fetched8& f, const Columns<kWhole>& c, float unit) {
+  elements8(f.w, v);
+  scale8(v, __fmul_rn(scale_value(f.s), unit));
+  if constexpr (!kWhole) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] = c.in(j) ? row.codes[c.at(j)] : 0u;
-      s[j] = c.in(j) ? row.scales[c.at(j) >> 5] : 0u;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      uint32_t h, none;
-      decode_e4m3(w[j] | w[j + 1] << 8, h, none);
-      const float2 f = half2_float2(h);
-      v[j] = __fmul_rn(f.x, __fmul_rn(scale_value(s[j]), unit));
-      v[j + 1] = __fmul_rn(f.y, __fmul_rn(scale_value(s[j + 1]), unit));
-    }
+    for (int j = 0; j < 8; ++j)
+      if (!c.in(j)) v[j] = 0.0f;  // (what fills up the last block is not the row's)
   }
 }
 
 // A vector of a row, 0 past its end, into an MX8 row; v holds x's values.
-// Called by whole warps whose columns are neighbours'.
-template <class V, bool kVec, int kStride>
-__device__ __forceinline__ void store_columns8(const Row8& row, const Columns<kVec, kStride>& c, const V& x,
-                                               const float (&v)[8]) {
-  const uint32_t padded = (c.cols + 31u) & ~31u;
-  if constexpr (kVec) {
-    const uint32_t s = scale_code8(max_of_four(x.max_bits()));
-    if (c.first >= padded) return;
-    *reinterpret_cast<uint2*>(row.codes + c.first) = encode8_mx8(v, s);
-    if ((c.first & 31u) == 0) row.scales[c.first >> 5] = (uint8_t)s;
-  } else {
-    static_assert(kVec || kStride % 32 == 0, "a warp's columns are a block");
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t s = scale_code8(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[j]) & 0x7FFFFFFFu));
-      if (c.at(j) >= padded) continue;
-      const float u = __fmul_rn(v[j], inverse_scale(s));
-      row.codes[c.at(j)] = s == 255u ? 0 : (uint8_t)encode_e4m3(u, 0.0f, 0.0f, 0.0f);
-      if ((c.at(j) & 31u) == 0) row.scales[c.at(j) >> 5] = (uint8_t)s;
-    }
-  }
+// Called by whole warps whose lanes have neighbouring vectors.
+template <class V, bool kWhole>
+__device__ __forceinline__ void store_columns8(const Row8& row, const Columns<kWhole>& c, const V& x, const float (&v)[8]) {
+  const uint32_t s = scale_code8(max_of_four(x.max_bits()));
+  if (c.first >= ((c.cols + 31u) & ~31u)) return;
+  *reinterpret_cast<uint2*>(row.codes + c.first) = encode8_mx8(v, s);
+  if ((c.first & 31u) == 0) row.scales[c.first >> 5] = (uint8_t)s;
 }
 
 // A vector of one of the three types at a thread's columns, 0 past its end.
-template <bool kVec, int kStride>
-__device__ __forceinline__ void load_weights(const void* w, int type, const Columns<kVec, kStride>& c, float (&v)[8]) {
-  if constexpr (kVec) {
+// `vec`: it is 16-byte aligned.
+template <bool kWhole>
+__device__ __forceinline__ void load_weights(const void* w, int type, bool vec, const Columns<kWhole>& c, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  if (kWhole || (vec && c.in(7))) {
+    if (!c.any()) return;
     if (type == kMxF32) {
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-      if (c.in(0)) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c.first);
-        a = __ldg(p), b = __ldg(p + 1);
-      }
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c.first);
+      const float4 a = __ldg(p), b = __ldg(p + 1);
       v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
       return;
     }
-    uint4 a = make_uint4(0u, 0u, 0u, 0u);
-    if (c.in(0)) a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c.first));
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c.first));
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
     if (type == kMxBf16) {
 #pragma unroll
@@ -195,15 +321,16 @@ __device__ __forceinline__ void load_weights(const void* w, int type, const Colu
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[2 * j] = F16::lo(u[j]), v[2 * j + 1] = F16::hi(u[j]);
     }
-  } else {
+    return;
+  }
+  if constexpr (!kWhole) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = 0.0f;
       if (!c.in(j)) continue;
       if (type == kMxF32) {
-        v[j] = __ldg(static_cast<const float*>(w) + c.at(j));
+        v[j] = __ldg(static_cast<const float*>(w) + c.first + j);
       } else {
-        const uint16_t u = __ldg(static_cast<const uint16_t*>(w) + c.at(j));
+        const uint16_t u = __ldg(static_cast<const uint16_t*>(w) + c.first + j);
         v[j] = type == kMxF16 ? F16::f32(u) : Bf16::f32(u);
       }
     }
@@ -241,6 +368,10 @@ __device__ __forceinline__ void round_to(Vec32& x, const float (&v)[8]) {
 // thread's copies arrive in the order of its groups.
 __device__ __forceinline__ void copy_async16(void* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+// (for words that a neighbour copies too)
+__device__ __forceinline__ void copy_async16_shared(void* to, uintptr_t from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy_async8(void* to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
