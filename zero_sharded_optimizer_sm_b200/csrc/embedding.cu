@@ -396,8 +396,7 @@ __device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64
     float u[8];
     load_columns(x, out, c, span_of<T>(a.dtable, a.vocab, a.cols, a.ld));
     x.values(u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
+    plus8(v, u);
   }
   round_to(x, v);
   store_columns(out, c, x);
@@ -437,9 +436,16 @@ __device__ __forceinline__ void clear_rows(const EmbeddingBackwardArgs& a, const
     } else {
       for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSumThreads) bits[i] = 0;
       __syncthreads();
-      for (uint32_t i = threadIdx.x; i < g.n; i += kSumThreads) {
-        const uint64_t at = (uint64_t)token_at(a.tokens, a.token_bytes, i) - (uint64_t)lo;
-        if (at < rows) atomicOr(&bits[at >> 5], 1u << (at & 31));
+      constexpr int kTokens = 8;  // loads of a thread that are out at a time
+      for (uint32_t i = threadIdx.x; i < g.n; i += kTokens * kSumThreads) {
+        int64_t token[kTokens];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) token[k] = i + k * kSumThreads < g.n ? token_at(a.tokens, a.token_bytes, i + k * kSumThreads) : -1;
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+          const uint64_t at = (uint64_t)token[k] - (uint64_t)lo;
+          if (at < rows) atomicOr(&bits[at >> 5], 1u << (at & 31));
+        }
       }
     }
     __syncthreads();
@@ -455,10 +461,9 @@ __device__ __forceinline__ float* part_at(const Segments& g, uint32_t segment, i
 }
 
 template <class D, class T, bool kWhole>
-__global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
-                                                                         const __grid_constant__ Segments g,
-                                                                         const __grid_constant__ Clear z,
-                                                                         const FastDiv by_slabs) {
+__global__ void __launch_bounds__(kSumThreads, kWhole ? 2 : 1)
+    embedding_segments_kernel(const __grid_constant__ EmbeddingBackwardArgs a, const __grid_constant__ Segments g,
+                              const __grid_constant__ Clear z, const FastDiv by_slabs) {
   constexpr int kAhead = kWhole && sizeof(typename D::raw) == 2 ? 8 : 4;  // rows whose loads are out at a time
   using V = typename D::V;
   __shared__ uint32_t bits[kBitRows / 32];
@@ -519,8 +524,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_segments_kernel(const _
         float v[8];
         take_columns(x, f[k], row[k], c);
         x.values(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], v[j]);
+        plus8(acc, v);
       }
     }
   }
@@ -559,15 +563,17 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
   if (segment + 1 < g.count) {
     const uint32_t lo = segment * g.seg, hi = lo + g.seg;
     key = g.keys[hi - 1];
-    const bool begins = g.keys[lo] != key || lo == 0 || g.keys[lo - 1] != key;
-    if (begins && key != (uint32_t)a.vocab && g.keys[hi] == key) {
-      uint32_t x = hi, y = g.n;  // the run's end
-      while (x < y) {
-        const uint32_t mid = x + (y - x) / 2;
-        if (g.keys[mid] == key) x = mid + 1;
-        else y = mid;
+    const uint32_t before = lo ? g.keys[lo - 1] : ~0u, first_key = g.keys[lo], next = g.keys[hi];
+    if (next == key && key != (uint32_t)a.vocab && (first_key != key || before != key)) {
+      // 32 segments at a time: those that end in my run are followed by another with a part of it
+      for (end = segment + 2;; end += 32) {
+        const uint32_t s = end - 1 + lane;  // whether this segment's last place and the next one's first are the run's
+        const uint32_t in = __ballot_sync(0xFFFFFFFFu, s + 1 < g.count && g.keys[(s + 1) * g.seg] == key);
+        if (in != 0xFFFFFFFFu) {
+          end += __ffs(~in) - 1;
+          break;
+        }
       }
-      end = (x - 1) / g.seg + 1;
     }
   }
   const bool is_long = end && end - segment > kShort;
@@ -660,9 +666,16 @@ cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Cl
   }
 }
 
-// Places of a segment: 32 keeps many warps busy; of a long batch 128, so that
-// the parts take a sixteenth of dy's elements' number, not a quarter.
-uint32_t segment_of(int64_t n) { return n <= kClusterMax ? 32 : 128; }
+// Places of a segment, for a warp to add one after another: as many as leave
+// every warp that the SMs hold a segment's slab, from 8 rows, whose loads go out
+// together, to 128, whose parts take a sixteenth of dy's elements' number.
+constexpr int64_t kManyWarps = 148 * 2 * kSumWarps;
+uint32_t segment_of(int64_t n, int64_t cols) {
+  const int64_t slabs = (cols + 255) / 256;
+  uint32_t seg = 8;
+  while (seg < 128 && 2 * seg * kManyWarps <= n * slabs) seg *= 2;
+  return seg;
+}
 
 // The workspace: keys and positions (two sets and the counts for the sort of a
 // long batch), the segments' parts.
@@ -680,7 +693,7 @@ Space space_of(int64_t n, int64_t cols) {
   const bool is_long = n > kClusterMax;
   for (int k = 0; k < (is_long ? 2 : 1); ++k) p.keys[k] = part(n), p.pos[k] = part(n);
   if (is_long) p.counts = part(kDigits * ((n + kChunk - 1) / kChunk));
-  const int64_t seg = segment_of(n), count = (n + seg - 1) / seg;
+  const int64_t seg = segment_of(n, cols), count = (n + seg - 1) / seg;
   p.parts = part(count > 1 ? 2 * count * cols : 0);
   p.bytes = at;
   return p;
@@ -735,7 +748,7 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_cou
   auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(base + at); };
   Segments g = {};
   g.n = (uint32_t)a.n;
-  g.seg = segment_of(a.n);
+  g.seg = segment_of(a.n, a.cols);
   g.count = (uint32_t)((a.n + g.seg - 1) / g.seg);
   g.slabs = (uint32_t)((a.cols + 255) / 256);
   g.parts = reinterpret_cast<float*>(base + p.parts);

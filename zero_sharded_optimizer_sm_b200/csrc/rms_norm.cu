@@ -255,8 +255,7 @@ __device__ __forceinline__ void store_dx(typename T::raw* row, const C& c, const
   if (dh) {
     float u[8];
     dh->values(u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], u[j]);
+    plus8(v, u);
   }
   typename T::V x;
   round_to(x, v);
@@ -270,7 +269,7 @@ __device__ __forceinline__ void store_part(float* out, const C& c, const A& acc)
     if (c.in(j)) out[c.first + j] = j & 1 ? acc[j >> 1].y : acc[j >> 1].x;
 }
 
-// One row's stage of the ring: dy, h, dh of every thread's vectors, 16 bytes of
+// One row's stage of the ring: dy, dh, h of every thread's vectors, 16 bytes of
 // each thread next to another's.
 template <class T, bool kWhole, int kChunks, bool kMx8, bool kDh>
 struct Ring {
@@ -278,10 +277,26 @@ struct Ring {
   using raw = typename T::raw;
   static constexpr int kWords = sizeof(raw) / 2 + (kWhole ? 0 : 1);  // 16-byte words fetched of a vector
   static constexpr uint32_t kPlanes = kWords * (1 + (kMx8 ? 0 : 1) + (kDh ? 1 : 0));
-  // bytes of a stage for so many vectors, and where h's and dh's words begin
-  static __host__ __device__ __forceinline__ constexpr uint32_t bytes(uint32_t vectors) { return vectors * (16 * kPlanes + (kMx8 ? 8 : 0)); }
-  static __host__ __device__ __forceinline__ uint32_t h_at(uint32_t vectors) { return 16 * kWords * vectors * (kDh ? 2 : 1); }
-  static __host__ __device__ __forceinline__ uint32_t dh_at(uint32_t vectors) { return 16 * kWords * vectors; }
+  // bytes of a stage for so many vectors, and where dh's and h's words begin
+  static __host__ __device__ __forceinline__ uint32_t bytes(uint32_t vectors) { return vectors * (16 * kPlanes + (kMx8 ? 8 : 0)); }
+  static __device__ __forceinline__ uint32_t dh_at(uint32_t vectors) { return 16 * kWords * vectors; }
+  static __device__ __forceinline__ uint32_t h_at(uint32_t vectors) { return 16 * kWords * vectors * (kDh ? 2 : 1); }
+
+  // The rows' addresses, moved on from row to row.
+  struct Rows {
+    const raw *dy, *dh, *h;
+    const uint8_t* codes;
+    __device__ __forceinline__ Rows(const RmsNormBackwardArgs& a, int64_t row)
+        : dy(row_of<T>(a.dy, row, a.ld_dy)), dh(row_of<T>(a.dh, row, a.ld_dh)), h(row_of<T>(a.h, row, a.ld_h)),
+          codes(a.h8.codes + row * a.h8.code_pitch) {}
+    __device__ __forceinline__ void next(const RmsNormBackwardArgs& a) {
+      const uint32_t step = gridDim.x;
+      dy += step * a.ld_dy;
+      if constexpr (kDh) dh += step * a.ld_dh;
+      if constexpr (kMx8) codes += step * a.h8.code_pitch;
+      else h += step * a.ld_h;
+    }
+  };
 
   static __device__ __forceinline__ void fetch16(uint8_t* to, uint32_t vectors, const raw* row, const Columns<kWhole>& c,
                                                  const void* m, int64_t rows, int64_t ld) {
@@ -290,42 +305,44 @@ struct Ring {
       for (int i = 0; i < kWords; ++i) copy_async16(to + 16 * i * vectors, row + c.first + 16 / (int)sizeof(raw) * i);
     } else {
       const Span span = span_of<T>(m, rows, c.cols, ld);
+      const uint32_t off = offset_of(row);
+      const bool inside = span.holds(row, c.cols, off);
       const uintptr_t from = reinterpret_cast<uintptr_t>(row + c.first) & ~(uintptr_t)15;
-      const uintptr_t end = reinterpret_cast<uintptr_t>(row + c.cols);
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        const uintptr_t at = from + 16 * i;
-        if (at >= end) break;
-        if (at >= span.lo && at + 16 <= span.hi) copy_async16_shared(to + 16 * i * vectors, at);
-        else *reinterpret_cast<uint4*>(to + 16 * i * vectors) = load_within<WordsOf<V>::kPer>(at, span);
+        if (c.first + 16 / (uint32_t)sizeof(raw) * i >= c.cols + off) break;
+        if (inside) copy_async16_shared(to + 16 * i * vectors, from + 16 * i);
+        else *reinterpret_cast<uint4*>(to + 16 * i * vectors) = load_within<WordsOf<V>::kPer>(from + 16 * i, span);
       }
     }
   }
-  // Asks for a row (none past the end; the group is there all the same).
-  static __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, int64_t row, uint8_t* to) {
-    if (row < a.rows) {
+  // Asks for a row if there is one; the group is there all the same.
+  static __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, const Rows& row, bool there, uint8_t* to) {
+    if (there) {
       const uint32_t vectors = blockDim.x * kChunks;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         const uint32_t v = blockDim.x * k + threadIdx.x;
         const Columns<kWhole> c(0, v, (uint32_t)a.cols);
         if (!c.any()) break;
-        fetch16(to + 16 * v, vectors, row_of<T>(a.dy, row, a.ld_dy), c, a.dy, a.rows, a.ld_dy);
-        if constexpr (kDh) fetch16(to + dh_at(vectors) + 16 * v, vectors, row_of<T>(a.dh, row, a.ld_dh), c, a.dh, a.rows, a.ld_dh);
-        if constexpr (kMx8) copy_async8(to + h_at(vectors) + 8 * v, a.h8.codes + row * a.h8.code_pitch + c.first);
-        else fetch16(to + h_at(vectors) + 16 * v, vectors, row_of<T>(a.h, row, a.ld_h), c, a.h, a.rows, a.ld_h);
+        fetch16(to + 16 * v, vectors, row.dy, c, a.dy, a.rows, a.ld_dy);
+        if constexpr (kDh) fetch16(to + dh_at(vectors) + 16 * v, vectors, row.dh, c, a.dh, a.rows, a.ld_dh);
+        if constexpr (kMx8) copy_async8(to + h_at(vectors) + 8 * v, row.codes + c.first);
+        else fetch16(to + h_at(vectors) + 16 * v, vectors, row.h, c, a.h, a.rows, a.ld_h);
       }
     }
     copy_async_commit();
   }
-  static __device__ __forceinline__ void read(const uint8_t* at, uint32_t vectors, const raw* row, const Columns<kWhole>& c, V& x) {
+  // `m` and `ld`: of whose row the offset is taken.
+  static __device__ __forceinline__ void read(const uint8_t* at, uint32_t vectors, const void* m, uint32_t row, int64_t ld,
+                                              const Columns<kWhole>& c, V& x) {
     Fetched<V, kWhole> f;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const uint4 w = *reinterpret_cast<const uint4*>(at + 16 * i * vectors);
       f.w[4 * i] = w.x, f.w[4 * i + 1] = w.y, f.w[4 * i + 2] = w.z, f.w[4 * i + 3] = w.w;
     }
-    take_columns(x, f, row, c);
+    take_columns(x, f, row_of<T>(m, row, ld), c);
   }
 };
 
@@ -339,9 +356,14 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float smem[2][32];
   pdl_trigger();
-  const int64_t step = gridDim.x;
+  const uint32_t step = gridDim.x, rows = (uint32_t)a.rows;
   const uint32_t cols = (uint32_t)a.cols, group = blockDim.x, vectors = group * kChunks, size = R::bytes(vectors);
-  for (int s = 0; s < stages - 1; ++s) R::fetch(a, blockIdx.x + s * step, ring + s * size);
+  uint32_t ahead = blockIdx.x;  // the row to ask for
+  typename R::Rows from(a, ahead);
+  for (int s = 0; s < stages - 1; ++s, ahead += step) {
+    R::fetch(a, from, ahead < rows, ring + s * size);
+    from.next(a);
+  }
   float2 acc[kChunks][4];
   float w[8];
 #pragma unroll
@@ -351,13 +373,13 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
   if constexpr (kChunks == 1) load_weights(a.weight, a.w_type, a.w_aligned, C(0, threadIdx.x, cols), w);
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
   // the row's statistics and scales, a row ahead
+  const float* stats = a.rstd + blockIdx.x;
+  const uint8_t* scales = a.h8.scales + blockIdx.x * a.h8.scale_pitch;
   float next_rstd = 0.0f;
   uint32_t scale[kChunks] = {}, next_scale[kChunks] = {};
-  auto ahead = [&](int64_t row) {
-    if (row >= a.rows) return;
-    next_rstd = a.rstd[row];
+  auto look = [&]() {
+    next_rstd = *stats;
     if constexpr (kMx8) {
-      const uint8_t* scales = a.h8.scales + row * a.h8.scale_pitch;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         const C c(8 * group * k, threadIdx.x, cols);
@@ -365,18 +387,22 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
       }
     }
   };
-  ahead(blockIdx.x);
+  look();
+  typename T::raw* to = row_of<T>(a.dx, blockIdx.x, a.ld_dx);
   uint32_t now = 0, later = (stages - 1) * size;  // the stages of this row and of the one to ask for
   int round = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += step, ++round) {
-    R::fetch(a, row + (stages - 1) * step, ring + later);
+  for (uint32_t row = blockIdx.x; row < rows; row += step, ahead += step, ++round) {
+    R::fetch(a, from, ahead < rows, ring + later);
+    from.next(a);
     later = now;
     const uint8_t* stage = ring + now;
     now = now + size == stages * size ? 0 : now + size;
     const float rstd = next_rstd;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) scale[k] = next_scale[k];
-    ahead(row + step);
+    stats += step;
+    scales += step * a.h8.scale_pitch;
+    if (row + step < rows) look();
     if (stages == 4) copy_async_wait<3>();
     else if (stages == 3) copy_async_wait<2>();
     else copy_async_wait<1>();
@@ -385,12 +411,12 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
     auto vector = [&](int k, const C& c, bool sums) {
       const uint32_t v = group * k + threadIdx.x;
       typename T::V x;
-      R::read(stage + 16 * v, vectors, row_of<T>(a.dy, row, a.ld_dy), c, x);
+      R::read(stage + 16 * v, vectors, a.dy, row, a.ld_dy, c, x);
       x.values(g);
       if constexpr (kMx8) {
         take_columns8(xh, Fetched8{*reinterpret_cast<const uint2*>(stage + R::h_at(vectors) + 8 * v), scale[k]}, c, rstd);
       } else {
-        R::read(stage + R::h_at(vectors) + 16 * v, vectors, row_of<T>(a.h, row, a.ld_h), c, x);
+        R::read(stage + R::h_at(vectors) + 16 * v, vectors, a.h, row, a.ld_h, c, x);
         x.values(xh);
         scale8(xh, rstd);
       }
@@ -404,7 +430,6 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
       if (c.any()) vector(k, c, true);
     }
     const float mean = __fmul_rn(block_sum(__fadd_rn(dot.x, dot.y), smem, round), inv);
-    typename T::raw* to = row_of<T>(a.dx, row, a.ld_dx);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       const C c(8 * group * k, threadIdx.x, cols);
@@ -414,10 +439,11 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
         if constexpr (kChunks > 1) vector(k, c, false);
         dx_vector(g, xh, rstd, mean);
         if constexpr (kDh)
-          R::read(stage + R::dh_at(vectors) + 16 * (group * k + threadIdx.x), vectors, row_of<T>(a.dh, row, a.ld_dh), c, dh);
+          R::read(stage + R::dh_at(vectors) + 16 * (group * k + threadIdx.x), vectors, a.dh, row, a.ld_dh, c, dh);
       }
       store_dx<T>(to, c, kDh ? &dh : nullptr, g);  // (by whole warps)
     }
+    to += step * a.ld_dx;
   }
   float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
 #pragma unroll

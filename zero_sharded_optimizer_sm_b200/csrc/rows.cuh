@@ -89,6 +89,13 @@ __device__ __forceinline__ uint32_t offset_of(const raw* row) {
 // A matrix's memory, from its first to behind its last element.
 struct Span {
   uintptr_t lo, hi;
+  // Whether all 16-byte words with an element of a row are the matrix's (of all
+  // rows but the first and the last they are).
+  template <class raw>
+  __device__ __forceinline__ bool holds(const raw* row, uint32_t cols, uint32_t off) const {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(row) - sizeof(raw) * off;
+    return from >= lo && from + sizeof(raw) * ((off + cols + (16 / sizeof(raw) - 1)) & ~(uint32_t)(16 / sizeof(raw) - 1)) <= hi;
+  }
 };
 template <class T>
 __device__ __forceinline__ Span span_of(const void* m, int64_t rows, int64_t cols, int64_t ld) {
@@ -132,15 +139,16 @@ __device__ __forceinline__ void fetch_columns(Fetched<V, kWhole>& f, const typen
 #pragma unroll
     for (int i = 0; i < kN; ++i) f.w[i] = words(x)[i];
   } else {
-    const uintptr_t from = reinterpret_cast<uintptr_t>(row + c.first) & ~(uintptr_t)15;
-    const uintptr_t end = reinterpret_cast<uintptr_t>(row + c.cols);  // of the row
+    const uint32_t off = offset_of(row);
+    const bool inside = m.holds(row, c.cols, off);  // (the same for the whole warp)
+    const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row + c.first) & ~(uintptr_t)15);
+    constexpr uint32_t kIn = 16 / sizeof(typename V::raw);
 #pragma unroll
     for (int i = 0; i < kN / 4 + 1; ++i) {
-      const uintptr_t at = from + 16 * i;
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (at < end) {
-        if (at >= m.lo && at + 16 <= m.hi) x = *reinterpret_cast<const uint4*>(at);
-        else x = load_within<WordsOf<V>::kPer>(at, m);
+      if (c.first + kIn * i < c.cols + off) {  // the word holds an element of the row
+        if (inside) x = from[i];
+        else x = load_within<WordsOf<V>::kPer>(reinterpret_cast<uintptr_t>(from + i), m);
       }
       f.w[4 * i] = x.x, f.w[4 * i + 1] = x.y, f.w[4 * i + 2] = x.z, f.w[4 * i + 3] = x.w;
     }
@@ -234,7 +242,14 @@ __device__ __forceinline__ void store_columns(typename V::raw* row, const Column
   }
 }
 
-// Products of pairs.
+// Pairs at once.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
 __device__ __forceinline__ float2 pair(const float (&v)[8], int p) { return make_float2(v[2 * p], v[2 * p + 1]); }
 __device__ __forceinline__ void scale8(float (&v)[8], float s) {
 #pragma unroll
@@ -247,6 +262,14 @@ __device__ __forceinline__ void times8(float (&v)[8], const float (&w)[8]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const float2 f = mul2(pair(v, p), pair(w, p));
+    v[2 * p] = f.x, v[2 * p + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ void plus8(float (&v)[8], const float (&w)[8]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float2 f = add2(pair(v, p), pair(w, p));
     v[2 * p] = f.x, v[2 * p + 1] = f.y;
   }
 }
