@@ -357,25 +357,29 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
 // the segment before, slot 1 where it begins -- and the join adds the parts in
 // order.
 //
-// The first CTAs of the launch clear the rows of the table that no token of
+// Half the warps of every CTA first clear the rows of the table that no token of
 // the batch has -- most of the gradient's bytes, as a rule.  They look for the
 // tokens in the batch itself and do not wait for the sort, which thus takes
 // next to no time of its own; for a batch that is longer than a cluster sorts,
-// they search the sorted tokens instead.
-constexpr int kSumThreads = 512;
-constexpr int kSumWarps = kSumThreads / 32;
-constexpr int kBitRows = 1 << 15;  // rows of the table that a CTA looks after at a time
+// they search the sorted tokens instead.  The other half waits for the sort and
+// walks over the units (a slab of a segment), which takes it less time than the
+// clearing.  One CTA an SM: of two kinds of CTAs, the clearing ones came to lie
+// in pairs on half the SMs and took 47 us for 206 MB instead of 36.
+constexpr int kSumThreads = 1024;
+constexpr int kBitRows = 1 << 15;
 
 struct Clear {
   uint8_t* table;
   int64_t row_bytes, pitch_bytes;
-  int by_search;
-  uint32_t ctas;
+  bool by_search, end_to_end;  // rows of one piece
+  FastDiv by_row;              // a row's elements of 2 bytes
+  uint32_t rows;               // of the table that a CTA looks after at a time
 };
 
 struct Segments {
   const uint32_t *keys, *pos;
-  float* parts;  // [segment][slot][cols]
+  float* parts;  // [segment][slot][pitch], the columns rounded up to eights
+  int64_t pitch;
   uint32_t n, seg, count, slabs;
 };
 
@@ -403,26 +407,39 @@ __device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64
 }
 
 // One warp clears `bytes` bytes at p, an element's multiple.
-__device__ __forceinline__ void clear_row(uint8_t* p, int64_t bytes) {
-  const int lane = threadIdx.x & 31;
-  const int64_t head = min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15u), bytes);
-  if (2 * lane < head) *reinterpret_cast<uint16_t*>(p + 2 * lane) = 0;
-  p += head, bytes -= head;
-  for (int64_t i = 16 * lane; i + 16 <= bytes; i += 512) __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(0u, 0u, 0u, 0u));
-  const int64_t body = bytes & ~15ll;
-  if (body + 2 * lane < bytes) *reinterpret_cast<uint16_t*>(p + body + 2 * lane) = 0;
+__device__ __forceinline__ void clear_row(uint8_t* p, uint32_t bytes) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t head = min((uint32_t)(-reinterpret_cast<uintptr_t>(p) & 15u), bytes);
+  if (head) {
+    if (2 * lane < head) *reinterpret_cast<uint16_t*>(p + 2 * lane) = 0;
+    p += head, bytes -= head;
+  }
+  const uint32_t n = bytes / 16;
+  uint4* q = reinterpret_cast<uint4*>(p) + lane;
+  uint32_t i = 0;
+  for (; i + 128 <= n; i += 128) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) __stcs(q + i + 32 * k, make_uint4(0u, 0u, 0u, 0u));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + 32 * k + lane < n) __stcs(q + i + 32 * k, make_uint4(0u, 0u, 0u, 0u));
+  if (const uint32_t tail = bytes & 15u)
+    if (2 * lane < tail) *reinterpret_cast<uint16_t*>(p + 16 * n + 2 * lane) = 0;
 }
 
-// A CTA's share of the rows without a token.
+// The CTA's share of the rows without a token, by its first kThreads threads.
+template <int kThreads>
 __device__ __forceinline__ void clear_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, uint32_t* bits) {
-  const int64_t each = (a.vocab + z.ctas - 1) / z.ctas;
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
+  const int64_t each = (a.vocab + gridDim.x - 1) / gridDim.x;
   const int64_t end = min(a.vocab, (int64_t)(blockIdx.x + 1) * each);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (z.by_search) pdl_wait();
-  for (int64_t lo = blockIdx.x * each; lo < end; lo += kBitRows) {
-    const uint32_t rows = (uint32_t)min(end - lo, (int64_t)kBitRows);
+  for (int64_t lo = blockIdx.x * each; lo < end; lo += z.rows) {
+    const uint32_t rows = (uint32_t)min(end - lo, (int64_t)z.rows);
     if (z.by_search) {
-      for (uint32_t r = threadIdx.x; r < (rows + 31) / 32 * 32; r += kSumThreads) {
+      for (uint32_t r = threadIdx.x; r < (rows + 31) / 32 * 32; r += kThreads) {
         const uint32_t v = (uint32_t)lo + r;
         uint32_t x = 0, y = g.n;
         while (x < y) {
@@ -434,46 +451,78 @@ __device__ __forceinline__ void clear_rows(const EmbeddingBackwardArgs& a, const
         if (lane == 0) bits[r >> 5] = word;
       }
     } else {
-      for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSumThreads) bits[i] = 0;
-      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kThreads) bits[i] = 0;
+      sync();
       constexpr int kTokens = 8;  // loads of a thread that are out at a time
-      for (uint32_t i = threadIdx.x; i < g.n; i += kTokens * kSumThreads) {
+      for (uint32_t i = threadIdx.x; i < g.n; i += kTokens * kThreads) {
         int64_t token[kTokens];
 #pragma unroll
-        for (int k = 0; k < kTokens; ++k) token[k] = i + k * kSumThreads < g.n ? token_at(a.tokens, a.token_bytes, i + k * kSumThreads) : -1;
+        for (int k = 0; k < kTokens; ++k) token[k] = i + k * kThreads < g.n ? token_at(a.tokens, a.token_bytes, i + k * kThreads) : -1;
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
           const uint64_t at = (uint64_t)token[k] - (uint64_t)lo;
-          if (at < rows) atomicOr(&bits[at >> 5], 1u << (at & 31));
+          // (a token that fills half the batch is marked once, not in turn by every thread)
+          if (at < rows && !(reinterpret_cast<volatile uint32_t*>(bits)[at >> 5] >> (at & 31) & 1u))
+            atomicOr(&bits[at >> 5], 1u << (at & 31));
         }
       }
     }
-    __syncthreads();
-    for (uint32_t r = warp; r < rows; r += kSumWarps)
-      if (!(bits[r >> 5] >> (r & 31) & 1u)) clear_row(z.table + (lo + r) * z.pitch_bytes, z.row_bytes);
-    __syncthreads();
+    sync();
+    auto present = [&](uint32_t r) { return (bits[r >> 5] >> (r & 31) & 1u) != 0; };
+    if (z.end_to_end) {
+      // the rows as one piece of memory, its aligned words shared out among all
+      // threads: a warp to a row of its own was 13 us slower over 206 MB, for
+      // memory that is written in 16 places of a CTA at a time
+      uint8_t* from = z.table + lo * z.row_bytes;
+      const uint32_t bytes = (uint32_t)(rows * z.row_bytes), head = (uint32_t)(-reinterpret_cast<uintptr_t>(from) & 15u);
+      auto row_at = [&](uint32_t byte) { return div_by(byte >> 1, z.by_row); };
+      auto clear_some = [&](uint32_t at, uint32_t to) {
+        for (; at < to; at += 2)
+          if (!present(row_at(at))) *reinterpret_cast<uint16_t*>(from + at) = 0;
+      };
+      if (threadIdx.x == 0) clear_some(0, min(head, bytes));
+      if (bytes > head) {
+        const uint32_t words = (bytes - head) / 16;
+#pragma unroll 4
+        for (uint32_t i = threadIdx.x; i < words; i += kThreads) {
+          const uint32_t at = head + 16 * i, r = row_at(at);
+          // the row of the word's last element: rows of a word or more, the same or the next
+          const uint32_t last = z.row_bytes < 16 ? row_at(at + 14) : r + (at + 14 >= (r + 1) * (uint32_t)z.row_bytes);
+          if (!present(r) && !present(last) && last - r < 2) __stcs(reinterpret_cast<uint4*>(from + at), make_uint4(0u, 0u, 0u, 0u));
+          else if (r != last) clear_some(at, at + 16);
+        }
+        if (threadIdx.x == 0) clear_some(head + 16 * words, bytes);
+      }
+    } else {
+      uint8_t* row = z.table + (lo + warp) * z.pitch_bytes;
+      for (uint32_t r = warp; r < rows; r += (kThreads / 32), row += (kThreads / 32) * z.pitch_bytes)
+        if (!present(r)) clear_row(row, (uint32_t)z.row_bytes);
+    }
+    sync();
   }
 }
 
-template <bool kWhole>
-__device__ __forceinline__ float* part_at(const Segments& g, uint32_t segment, int slot, int64_t cols) {
-  return g.parts + (2ll * segment + slot) * cols;
+// A part's row of the workspace, eight columns of it a lane.
+__device__ __forceinline__ float* part_at(const Segments& g, uint32_t segment, int slot) {
+  return g.parts + (2ll * segment + slot) * g.pitch;
+}
+__device__ __forceinline__ void load_part(const float* p, float (&v)[8]) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store_part(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// A slab of a segment.
 template <class D, class T, bool kWhole>
-__global__ void __launch_bounds__(kSumThreads, kWhole ? 2 : 1)
-    embedding_segments_kernel(const __grid_constant__ EmbeddingBackwardArgs a, const __grid_constant__ Segments g,
-                              const __grid_constant__ Clear z, const FastDiv by_slabs) {
-  constexpr int kAhead = kWhole && sizeof(typename D::raw) == 2 ? 8 : 4;  // rows whose loads are out at a time
+__device__ __forceinline__ void sum_unit(const EmbeddingBackwardArgs& a, const Segments& g, const FastDiv& by_slabs,
+                                         const uint32_t u) {
+  // rows whose loads are out at a time, as many as 64 registers hold
+  constexpr int kAhead = sizeof(typename D::raw) == 2 ? (kWhole ? 8 : 3) : (kWhole ? 4 : 2);
   using V = typename D::V;
-  __shared__ uint32_t bits[kBitRows / 32];
-  pdl_trigger();
-  if (blockIdx.x < z.ctas) clear_rows(a, g, z, bits);
-  pdl_wait();  // every CTA: what follows this launch relies on the sort's being over too
-  if (blockIdx.x < z.ctas) return;
   const int lane = threadIdx.x & 31;
-  const uint32_t u = (blockIdx.x - z.ctas) * kSumWarps + (threadIdx.x >> 5);
-  if (u >= g.count * g.slabs) return;
   const uint32_t segment = div_by(u, by_slabs), slab = u - segment * g.slabs;
   const uint32_t lo = segment * g.seg, hi = min(lo + g.seg, g.n);
   const Slab<kWhole> c(256u * slab, lane, (uint32_t)a.cols);
@@ -488,10 +537,7 @@ __global__ void __launch_bounds__(kSumThreads, kWhole ? 2 : 1)
     if (!inside && !goes_on) {
       finish_row<T, kWhole>(a, current, c, acc);
     } else {
-      float* p = part_at<kWhole>(g, segment, inside ? 0 : 1, a.cols);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c.in(j)) p[c.first + j] = acc[j];
+      if (c.any()) store_part(part_at(g, segment, inside ? 0 : 1) + c.first, acc);
     }
   };
   bool padding = false;
@@ -531,27 +577,44 @@ __global__ void __launch_bounds__(kSumThreads, kWhole ? 2 : 1)
   if (!padding) flush(hi < g.n && g.keys[hi] == current);
 }
 
+template <class D, class T, bool kWhole>
+__global__ void __launch_bounds__(kSumThreads, 1)
+    embedding_segments_kernel(const __grid_constant__ EmbeddingBackwardArgs a, const __grid_constant__ Segments g,
+                              const __grid_constant__ Clear z, const FastDiv by_slabs) {
+  __shared__ uint32_t bits[kBitRows / 32];
+  constexpr int kClearing = kSumThreads / 2;
+  pdl_trigger();
+  if (z.table && threadIdx.x < kClearing) clear_rows<kClearing>(a, g, z, bits);
+  pdl_wait();  // (every thread, whether it takes a unit or not: the join relies on the sort's being over too)
+  // the warps that do not clear: all of an accumulating call
+  const uint32_t skip = z.table ? kClearing / 32 : 0, warps = kSumThreads / 32 - skip, warp = threadIdx.x >> 5;
+  if (warp < skip) return;
+  for (uint32_t u = blockIdx.x * warps + warp - skip; u < g.count * g.slabs; u += gridDim.x * warps)
+    sum_unit<D, T, kWhole>(a, g, by_slabs, u);
+}
+
 // A warp looks after the run that begins in its segment and crosses into the
-// next; runs over more than kShort segments are added by the whole CTA, an
-// eighth of the parts a warp.
+// next; runs over more than kShort segments are added by the whole CTA, a share
+// of the parts a warp.
 constexpr uint32_t kShort = 16;
+constexpr int kJoinThreads = 256;
 
 template <bool kWhole>
 __device__ __forceinline__ void add_parts(const Segments& g, uint32_t from, uint32_t to, const Slab<kWhole>& c,
                                           float (&acc)[8]) {
-#pragma unroll 4
+  if (!c.any()) return;
+#pragma unroll 8
   for (uint32_t s = from; s < to; ++s) {
-    const float* p = part_at<kWhole>(g, s, 0, c.cols);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c.in(j)) acc[j] = __fadd_rn(acc[j], __ldcg(p + c.first + j));
+    float v[8];
+    load_part(part_at(g, s, 0) + c.first, v);
+    plus8(acc, v);
   }
 }
 
 template <class T, bool kWhole>
-__global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
-                                                                     const __grid_constant__ Segments g) {
-  constexpr int kWarps = kRowThreads / 32;
+__global__ void __launch_bounds__(kJoinThreads) embedding_join_kernel(const __grid_constant__ EmbeddingBackwardArgs a,
+                                                                      const __grid_constant__ Segments g) {
+  constexpr int kWarps = kJoinThreads / 32;
   __shared__ uint32_t ends[kWarps];
   __shared__ float sums[kWarps][8][32];
   pdl_wait();
@@ -565,24 +628,27 @@ __global__ void __launch_bounds__(kRowThreads) embedding_join_kernel(const __gri
     key = g.keys[hi - 1];
     const uint32_t before = lo ? g.keys[lo - 1] : ~0u, first_key = g.keys[lo], next = g.keys[hi];
     if (next == key && key != (uint32_t)a.vocab && (first_key != key || before != key)) {
-      // 32 segments at a time: those that end in my run are followed by another with a part of it
-      for (end = segment + 2;; end += 32) {
-        const uint32_t s = end - 1 + lane;  // whether this segment's last place and the next one's first are the run's
-        const uint32_t in = __ballot_sync(0xFFFFFFFFu, s + 1 < g.count && g.keys[(s + 1) * g.seg] == key);
-        if (in != 0xFFFFFFFFu) {
-          end += __ffs(~in) - 1;
-          break;
-        }
+      // the last segment that begins with the run's token: 32 segments ahead
+      // in steps of 1, then of 32, 1024, ... until one does not, and back
+      uint32_t last = segment + 1, step = 1;
+      for (bool back = false;;) {
+        const uint32_t s = last + (lane + 1) * step;
+        const uint32_t ahead = __popc(__ballot_sync(0xFFFFFFFFu, s < g.count && g.keys[s * g.seg] == key));
+        last += ahead * step;
+        if (ahead < 32) back = true;
+        if (back && step == 1) break;
+        step = back ? step / 32 : step * 32;
       }
+      end = last + 1;
     }
   }
   const bool is_long = end && end - segment > kShort;
   if (lane == 0) ends[warp] = is_long ? end : 0;
   float acc[8];
   if (end) {
-    const float* p = part_at<kWhole>(g, segment, 1, a.cols);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = c.in(j) ? __ldcg(p + c.first + j) : 0.0f;
+    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    if (c.any()) load_part(part_at(g, segment, 1) + c.first, acc);
     if (!is_long) {
       add_parts<kWhole>(g, segment + 1, end, c, acc);
       finish_row<T, kWhole>(a, key, c, acc);
@@ -645,23 +711,25 @@ template <bool kWhole>
 using DenseF32 = Dense<TF32, kWhole>;
 
 template <class D, class T, bool kWhole>
-cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, cudaStream_t s) {
+cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, int sm_count, cudaStream_t s) {
   const int64_t units = (int64_t)g.count * g.slabs;
   if (units > 0x7FFFFFF0ll) return cudaErrorInvalidValue;
-  cudaError_t e = launch_kernel(embedding_segments_kernel<D, T, kWhole>, (int)(z.ctas + (units + kSumWarps - 1) / kSumWarps),
-                                kSumThreads, 0, s, true, a, g, z, fast_div(g.slabs));
+  const int grid = z.table ? sm_count : (int)std::min<int64_t>(sm_count, units);
+  cudaError_t e = launch_kernel(embedding_segments_kernel<D, T, kWhole>, grid, kSumThreads, 0, s, true, a, g, z,
+                                fast_div(g.slabs));
   if (e != cudaSuccess || g.count == 1) return e;
-  return launch_kernel(embedding_join_kernel<T, kWhole>, (int)((g.count + 7) / 8 * g.slabs), kRowThreads, 0, s, true, a, g);
+  return launch_kernel(embedding_join_kernel<T, kWhole>, (int)((g.count + kJoinThreads / 32 - 1) / (kJoinThreads / 32) * g.slabs),
+                       kJoinThreads, 0, s, true, a, g);
 }
 
 template <class D>
-cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, cudaStream_t s) {
+cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, int sm_count, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && aligned(a.dy, a.ld_dy * element_bytes(a.type)) &&
                    aligned(a.dtable, a.ld * element_bytes(a.dtable_type));
   switch (a.dtable_type) {
-    case kMxBf16: return vec ? sum_rows<D, TBf16, true>(a, g, z, s) : sum_rows<D, TBf16, false>(a, g, z, s);
-    case kMxF16: return vec ? sum_rows<D, TF16, true>(a, g, z, s) : sum_rows<D, TF16, false>(a, g, z, s);
-    case kMxF32: return vec ? sum_rows<D, TF32, true>(a, g, z, s) : sum_rows<D, TF32, false>(a, g, z, s);
+    case kMxBf16: return vec ? sum_rows<D, TBf16, true>(a, g, z, sm_count, s) : sum_rows<D, TBf16, false>(a, g, z, sm_count, s);
+    case kMxF16: return vec ? sum_rows<D, TF16, true>(a, g, z, sm_count, s) : sum_rows<D, TF16, false>(a, g, z, sm_count, s);
+    case kMxF32: return vec ? sum_rows<D, TF32, true>(a, g, z, sm_count, s) : sum_rows<D, TF32, false>(a, g, z, sm_count, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -669,7 +737,7 @@ cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Cl
 // Places of a segment, for a warp to add one after another: as many as leave
 // every warp that the SMs hold a segment's slab, from 8 rows, whose loads go out
 // together, to 128, whose parts take a sixteenth of dy's elements' number.
-constexpr int64_t kManyWarps = 148 * 2 * kSumWarps;
+constexpr int64_t kManyWarps = 148 * 32;
 uint32_t segment_of(int64_t n, int64_t cols) {
   const int64_t slabs = (cols + 255) / 256;
   uint32_t seg = 8;
@@ -679,6 +747,7 @@ uint32_t segment_of(int64_t n, int64_t cols) {
 
 // The workspace: keys and positions (two sets and the counts for the sort of a
 // long batch), the segments' parts.
+int64_t pitch_of(int64_t cols) { return (cols + 7) / 8 * 8; }
 struct Space {
   int64_t keys[2], pos[2], counts, parts, bytes;
 };
@@ -694,7 +763,7 @@ Space space_of(int64_t n, int64_t cols) {
   for (int k = 0; k < (is_long ? 2 : 1); ++k) p.keys[k] = part(n), p.pos[k] = part(n);
   if (is_long) p.counts = part(kDigits * ((n + kChunk - 1) / kChunk));
   const int64_t seg = segment_of(n, cols), count = (n + seg - 1) / seg;
-  p.parts = part(count > 1 ? 2 * count * cols : 0);
+  p.parts = part(count > 1 ? 2 * count * pitch_of(cols) : 0);
   p.bytes = at;
   return p;
 }
@@ -752,6 +821,7 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_cou
   g.count = (uint32_t)((a.n + g.seg - 1) / g.seg);
   g.slabs = (uint32_t)((a.cols + 255) / 256);
   g.parts = reinterpret_cast<float*>(base + p.parts);
+  g.pitch = pitch_of(a.cols);
   ClusterSort c = {};
   c.tokens = a.tokens, c.token_bytes = a.token_bytes;
   c.n = (uint32_t)a.n, c.vocab = (uint32_t)a.vocab;
@@ -761,7 +831,11 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_cou
     z.row_bytes = a.cols * element_bytes(a.dtable_type);
     z.pitch_bytes = a.ld * element_bytes(a.dtable_type);
     z.by_search = a.n > kClusterMax;
-    z.ctas = (uint32_t)std::min<int64_t>(sm_count, (a.vocab + kSumWarps - 1) / kSumWarps);
+    z.end_to_end = z.pitch_bytes == z.row_bytes;
+    z.by_row = fast_div((uint32_t)(z.row_bytes / 2));
+    // so many that their bytes are counted in 31 bits
+    z.rows = (uint32_t)std::max<int64_t>(1, std::min<int64_t>(kBitRows, 0x7FFFFFF0ll / z.row_bytes));
+    z.end_to_end = z.end_to_end && z.row_bytes <= 0x7FFFFFF0ll;
   }
   cudaError_t e;
   if (a.n <= kClusterMax) {
@@ -790,9 +864,9 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_cou
   if (e != cudaSuccess) return e;
   g.keys = c.keys, g.pos = c.pos;
   switch (a.type) {
-    case kMxBf16: return sum_rows<TBf16>(a, g, z, s);
-    case kMxF16: return sum_rows<TF16>(a, g, z, s);
-    case kMxF32: return sum_rows<TF32>(a, g, z, s);
+    case kMxBf16: return sum_rows<TBf16>(a, g, z, sm_count, s);
+    case kMxF16: return sum_rows<TF16>(a, g, z, sm_count, s);
+    case kMxF32: return sum_rows<TF32>(a, g, z, sm_count, s);
     default: return cudaErrorInvalidValue;
   }
 }
