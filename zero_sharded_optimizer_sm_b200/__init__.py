@@ -22,8 +22,10 @@ from typing import Callable, List, NamedTuple, Optional, Sequence
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzero_sm.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
+CALLS_PATH = os.path.join(_HERE, "_calls.so")
+
+if not (os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH)):
+    raise ImportError(f"{LIB_PATH if not os.path.exists(LIB_PATH) else CALLS_PATH} is missing: build it with __graft_entry__.build() "
                       "(the ZeRO step has no fallback implementation)")
 
 lib = ctypes.CDLL(LIB_PATH)
@@ -712,7 +714,11 @@ class ZeroOptimizer:
 # after it.  Operands may be freed once the call returns, but for a stream that
 # torch does not own (a handle, an ExternalStream): those the caller keeps
 # until their work has run.
+#
+# The calls around a layer's products have a compiled way for their plain use
+# (csrc/calls.cpp); None from it means that this one has to look closer.
 
+_CALLS = None        # the compiled calls, after the first use
 _T = None            # torch, after the first use
 _RAW_STREAM = None   # device index -> the current stream's handle
 _DTYPE_CODES: dict = {}
@@ -731,6 +737,21 @@ def _torch():
     return _T
 
 
+def _calls():
+    global _CALLS
+    if _CALLS is None:
+        import importlib.machinery
+        import importlib.util
+
+        _torch()  # (whose libraries it is linked to)
+        loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+        loader.exec_module(module)
+        module.bind(MX4, MX8)
+        _CALLS = module
+    return _CALLS
+
+
 def _on_device(device, stream, fn, *args) -> int:
     """fn(*args, stream handle) with ``device`` as the current CUDA device."""
     cuda = (_T or _torch()).cuda
@@ -746,7 +767,7 @@ class _MX:
     ``codes`` [rows, pitch] and ``scales`` [rows, pitch], each with contiguous
     rows."""
 
-    __slots__ = ("_codes", "_scales", "_space", "rows", "cols", "device", "_c")
+    __slots__ = ("_codes", "_scales", "_space", "rows", "cols", "device", "_at", "_struct_")
     _struct, _block_bytes = None, 0
 
     def __init__(self, codes, scales, rows: int, cols: int):
@@ -765,7 +786,15 @@ class _MX:
         self.device = codes.device
         if not codes.is_cuda or scales.device != self.device:
             raise ValueError("codes and scales must be on the same CUDA device")
-        self._c = self._struct(codes.data_ptr(), scales.data_ptr(), rows, cols, pitches[0], pitches[1])
+        self._at, self._struct_ = (codes.data_ptr(), scales.data_ptr(), *pitches), None
+
+    @property
+    def _c(self):
+        """The library's structure of it."""
+        if self._struct_ is None:
+            codes, scales, code_pitch, scale_pitch = self._at
+            self._struct_ = self._struct(codes, scales, self.rows, self.cols, code_pitch, scale_pitch)
+        return self._struct_
 
     @property
     def codes(self):
@@ -780,10 +809,10 @@ class _MX:
         return self._scales
 
     def _views(self):
-        c = self._c
-        n = self.rows * c.code_pitch
-        self._codes = self._space[:n].view(self.rows, c.code_pitch)
-        self._scales = self._space[n:].view(self.rows, c.scale_pitch)
+        _, _, code_pitch, scale_pitch = self._at
+        n = self.rows * code_pitch
+        self._codes = self._space[:n].view(self.rows, code_pitch)
+        self._scales = self._space[n:].view(self.rows, scale_pitch)
 
     @classmethod
     def _empty(cls, rows: int, cols: int, device):
@@ -806,7 +835,7 @@ class _MX:
         m._codes = m._scales = None
         m.rows, m.cols, m.device = rows, cols, m._space.device
         at = m._space.data_ptr()
-        m._c = cls._struct(at, at + rows * cp, rows, cols, cp, sp)
+        m._at, m._struct_ = (at, at + rows * cp, cp, sp), None
         return m
 
 
@@ -1100,6 +1129,10 @@ def mx4_check(device=None, stream=None):
 def mx8_quantize(x, out: Optional[MX8] = None, stream=None) -> MX8:
     """A matrix in 8 bits, in blocks along its rows: an activation on its way
     into what the backward pass keeps (zero_mx8_quantize)."""
+    if stream is None and out is None:
+        m = (_CALLS or _calls()).mx8_quantize(x)
+        if m is not None:
+            return m
     ptr, code, ld, rows, cols = _dense(x, "x")
     device = x.device
     side = _beside(device, stream)
@@ -1112,6 +1145,10 @@ def mx8_quantize(x, out: Optional[MX8] = None, stream=None) -> MX8:
 
 def mx8_dequantize(m: MX8, dtype=None, out=None, stream=None):
     """The values of an MX8 matrix (bfloat16 unless ``dtype`` or ``out`` says otherwise)."""
+    if stream is None and out is None:
+        x = (_CALLS or _calls()).mx8_dequantize(m, dtype or _T.bfloat16)
+        if x is not None:
+            return x
     device = m.device
     side = _beside(device, stream)
     out = _result(out, m.rows, m.cols, dtype or _torch().bfloat16, device, side)
@@ -1158,6 +1195,10 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, y=True, h=None, y8=Fal
     (wanted by default where there is a residual), rstd (the root, for the
     backward pass) and the 8-bit y8 and h8: True, False, or where to write it.
     y or h may be x or the residual itself."""
+    if stream is None and y is True and y8 is False and h8 is False:
+        got = (_CALLS or _calls()).rms_norm(x, weight, eps, residual, residual is not None if h is None else h, rstd)
+        if got is not None:
+            return RMSNorm(*got, None, None)
     ptr, code, ld, rows, cols = _dense(x, "x")
     device = x.device
     wptr, wcode = _vector(weight, "weight", cols, device)
@@ -1209,6 +1250,10 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, stream=Non
     added to dx, which is x's gradient and the residual's.  dx has dy's type
     (and may be dy or dh itself), dw the weight's unless given: it may be a view
     of a rank's gradient buffer (zero_rms_norm_backward)."""
+    if stream is None and dx is None and dw is None:
+        got = (_CALLS or _calls()).rms_norm_backward(dy, h, weight, rstd, dh)
+        if got is not None:
+            return got
     ptr, code, ld, rows, cols = _dense(dy, "dy")
     device = dy.device
     if isinstance(h, MX8):
@@ -1260,6 +1305,10 @@ def embedding(tokens, table, scale: float = 1.0, dtype=None, out=None, stream=No
     outside the table, such as -1, is padding: a row of zeros.  The table is a
     matrix, or an ``MX4`` one as a rank gathers it; the result has the table's
     type (bfloat16 for MX4) unless ``dtype`` or ``out`` says otherwise."""
+    if stream is None and out is None:
+        got = (_CALLS or _calls()).embedding(tokens, table, float(scale), dtype)
+        if got is not None:
+            return got
     tptr, tsize, n = _token_vector(tokens)
     device = tokens.device
     _need_device(device, "table", table)
@@ -1284,6 +1333,10 @@ def embedding_backward(dy, tokens, vocab: int, scale: float = 1.0, out=None, acc
     rows of dy whose token it is, zeros for a row without tokens
     (zero_embedding_backward).  ``out``, of dy's type unless given, may be a
     view of a rank's gradient buffer; ``accumulate`` adds to what it holds."""
+    if stream is None and out is None and not accumulate:
+        got = (_CALLS or _calls()).embedding_backward(dy, tokens, vocab, float(scale))
+        if got is not None:
+            return got
     ptr, code, ld, n, cols = _dense(dy, "dy")
     device = dy.device
     tptr, tsize, tn = _token_vector(tokens)

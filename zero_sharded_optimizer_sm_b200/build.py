@@ -1,4 +1,5 @@
-"""Build step of the ZeRO step library: ``libzero_sm.so`` for sm_100a.
+"""Build step of the ZeRO step library: ``libzero_sm.so`` for sm_100a, and
+``_calls.so``, the compiled Python calls.
 
 nvcc cross-compiles without a GPU.  Floating-point flags keep every device
 operation IEEE-conformant (no fast-math, no flush to zero, correctly rounded
@@ -17,6 +18,7 @@ SOURCES = ["csrc/zero_api.cu", "csrc/kernels.cu", "csrc/fused_tma.cu", "csrc/fus
            "csrc/mx8.cu", "csrc/rms_norm.cu", "csrc/embedding.cu", "csrc/layer_api.cu",
            "csrc/plan.cpp"]
 LIB = os.path.join(HERE, "libzero_sm.so")
+CALLS = os.path.join(HERE, "_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -65,7 +67,29 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         print(" ".join(link))
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
+    build_calls(verbose)
     return LIB
+
+
+def build_calls(verbose: bool = False) -> str:
+    """``_calls.so``: the compiled Python calls, linked to the library beside it
+    and to the torch that is installed."""
+    import importlib.util
+    import sysconfig
+
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch_dir, "include")
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           os.path.join(HERE, "csrc", "calls.cpp"), "-o", tmp, "-L" + HERE, "-l:libzero_sm.so", "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 if __name__ == "__main__":
