@@ -153,6 +153,9 @@ zero_status zero_rms_norm_backward(const void* dy, int32_t dtype, int64_t rows, 
   a.weight = weight, a.w_type = weight_dtype, a.w_aligned = (reinterpret_cast<uintptr_t>(weight) & 15u) == 0;
   a.rstd = rstd;
   a.dh = dh, a.ld_dh = one ? cols : ld_dh;
+  const int64_t size = elem_bytes(dtype);
+  auto end = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) + size * ((rows - 1) * ld + cols); };
+  a.dy_end = end(dy, a.ld_dy), a.h_end = end(h, a.ld_h), a.dh_end = end(dh, a.ld_dh);
   a.dx = dx, a.ld_dx = one ? cols : ld_dx;
   a.dw = dw, a.dw_type = dw_dtype;
   a.workspace = workspace;

@@ -207,7 +207,10 @@ Shape shape_of(int64_t cols) {
 // kernels' registers allow 1024 threads).
 uint32_t blocks_to_sm(const Shape& p) { return std::max(1u, std::min(1024 / p.threads / p.chunks, 16u)); }
 int64_t parts_of(int64_t rows, int64_t cols) {
-  return std::max<int64_t>(1, std::min(rows, kSms * blocks_to_sm(shape_of(cols))));
+  // four rows a block where that leaves every SM one: a block's start and its
+  // part of dw cost as much as some rows do (1237 x 771: one row a block 14 us)
+  const int64_t few = std::max((rows + 3) / 4, std::min(rows, kSms));
+  return std::max<int64_t>(1, std::min(few, kSms * blocks_to_sm(shape_of(cols))));
 }
 
 // The longest rows of which two stages fit; longer ones go through memory twice.
@@ -299,19 +302,19 @@ struct Ring {
   };
 
   static __device__ __forceinline__ void fetch16(uint8_t* to, uint32_t vectors, const raw* row, const Columns<kWhole>& c,
-                                                 const void* m, int64_t rows, int64_t ld) {
+                                                 const void* m, uintptr_t m_end) {
     if constexpr (kWhole) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) copy_async16(to + 16 * i * vectors, row + c.first + 16 / (int)sizeof(raw) * i);
     } else {
-      const Span span = span_of<T>(m, rows, c.cols, ld);
+      const Span span = {reinterpret_cast<uintptr_t>(m), m_end};
       const uint32_t off = offset_of(row);
       const bool inside = span.holds(row, c.cols, off);
       const uintptr_t from = reinterpret_cast<uintptr_t>(row + c.first) & ~(uintptr_t)15;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         if (c.first + 16 / (uint32_t)sizeof(raw) * i >= c.cols + off) break;
-        if (inside) copy_async16_shared(to + 16 * i * vectors, from + 16 * i);
+        if (inside || span.holds(reinterpret_cast<const uint4*>(from + 16 * i))) copy_async16_shared(to + 16 * i * vectors, from + 16 * i);
         else *reinterpret_cast<uint4*>(to + 16 * i * vectors) = load_within<WordsOf<V>::kPer>(from + 16 * i, span);
       }
     }
@@ -325,24 +328,28 @@ struct Ring {
         const uint32_t v = blockDim.x * k + threadIdx.x;
         const Columns<kWhole> c(0, v, (uint32_t)a.cols);
         if (!c.any()) break;
-        fetch16(to + 16 * v, vectors, row.dy, c, a.dy, a.rows, a.ld_dy);
-        if constexpr (kDh) fetch16(to + dh_at(vectors) + 16 * v, vectors, row.dh, c, a.dh, a.rows, a.ld_dh);
+        fetch16(to + 16 * v, vectors, row.dy, c, a.dy, a.dy_end);
+        if constexpr (kDh) fetch16(to + dh_at(vectors) + 16 * v, vectors, row.dh, c, a.dh, a.dh_end);
         if constexpr (kMx8) copy_async8(to + h_at(vectors) + 8 * v, row.codes + c.first);
-        else fetch16(to + h_at(vectors) + 16 * v, vectors, row.h, c, a.h, a.rows, a.ld_h);
+        else fetch16(to + h_at(vectors) + 16 * v, vectors, row.h, c, a.h, a.h_end);
       }
     }
     copy_async_commit();
   }
-  // `m` and `ld`: of whose row the offset is taken.
-  static __device__ __forceinline__ void read(const uint8_t* at, uint32_t vectors, const void* m, uint32_t row, int64_t ld,
-                                              const Columns<kWhole>& c, V& x) {
+  // The elements by which row `row` of a matrix is past a 16-byte boundary.
+  static __device__ __forceinline__ uint32_t offset(const void* m, uint32_t row, int64_t ld) {
+    if constexpr (kWhole) return 0u;
+    const uint32_t bytes = (uint32_t)reinterpret_cast<uintptr_t>(m) + row * ((uint32_t)ld * (uint32_t)sizeof(raw));
+    return (bytes & 15u) / (uint32_t)sizeof(raw);
+  }
+  static __device__ __forceinline__ void read(const uint8_t* at, uint32_t vectors, uint32_t off, const Columns<kWhole>& c, V& x) {
     Fetched<V, kWhole> f;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const uint4 w = *reinterpret_cast<const uint4*>(at + 16 * i * vectors);
       f.w[4 * i] = w.x, f.w[4 * i + 1] = w.y, f.w[4 * i + 2] = w.z, f.w[4 * i + 3] = w.w;
     }
-    take_columns(x, f, row_of<T>(m, row, ld), c);
+    take_columns(x, f, off, c);
   }
 };
 
@@ -411,12 +418,12 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
     auto vector = [&](int k, const C& c, bool sums) {
       const uint32_t v = group * k + threadIdx.x;
       typename T::V x;
-      R::read(stage + 16 * v, vectors, a.dy, row, a.ld_dy, c, x);
+      R::read(stage + 16 * v, vectors, R::offset(a.dy, row, a.ld_dy), c, x);
       x.values(g);
       if constexpr (kMx8) {
         take_columns8(xh, Fetched8{*reinterpret_cast<const uint2*>(stage + R::h_at(vectors) + 8 * v), scale[k]}, c, rstd);
       } else {
-        R::read(stage + R::h_at(vectors) + 16 * v, vectors, a.h, row, a.ld_h, c, x);
+        R::read(stage + R::h_at(vectors) + 16 * v, vectors, R::offset(a.h, row, a.ld_h), c, x);
         x.values(xh);
         scale8(xh, rstd);
       }
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
         if constexpr (kChunks > 1) vector(k, c, false);
         dx_vector(g, xh, rstd, mean);
         if constexpr (kDh)
-          R::read(stage + R::dh_at(vectors) + 16 * (group * k + threadIdx.x), vectors, a.dh, row, a.ld_dh, c, dh);
+          R::read(stage + R::dh_at(vectors) + 16 * (group * k + threadIdx.x), vectors, R::offset(a.dh, row, a.ld_dh), c, dh);
       }
       store_dx<T>(to, c, kDh ? &dh : nullptr, g);  // (by whole warps)
     }
@@ -534,8 +541,9 @@ __global__ void __launch_bounds__(32 * kDwWarps) rms_norm_dw_kernel(const float*
   pdl_wait();
   float s = 0.0f;
   if (col < cols) {
+    const float* from = parts + col;
 #pragma unroll 8
-    for (int64_t p = q; p < n; p += kDwWarps) s = __fadd_rn(s, __ldcg(parts + p * cols + col));
+    for (uint32_t p = q; p < (uint32_t)n; p += kDwWarps) s = __fadd_rn(s, __ldcg(from + p * cols));
   }
   smem[q][x] = s;
   __syncthreads();

@@ -29,6 +29,7 @@ struct RmsNormBackwardArgs {
   const void *dy, *h, *dh;  // of `type`; h null: h8; dh may be null
   int type;
   int64_t rows, cols, ld_dy, ld_h, ld_dh;
+  uintptr_t dy_end, h_end, dh_end;  // behind the matrices' last elements
   Mx8Matrix h8;
   const void* weight;
   int w_type;

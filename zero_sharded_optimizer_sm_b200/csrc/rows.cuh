@@ -89,6 +89,9 @@ __device__ __forceinline__ uint32_t offset_of(const raw* row) {
 // A matrix's memory, from its first to behind its last element.
 struct Span {
   uintptr_t lo, hi;
+  __device__ __forceinline__ bool holds(const uint4* word) const {
+    return reinterpret_cast<uintptr_t>(word) >= lo && reinterpret_cast<uintptr_t>(word) + 16 <= hi;
+  }
   // Whether all 16-byte words with an element of a row are the matrix's (of all
   // rows but the first and the last they are).
   template <class raw>
@@ -115,17 +118,15 @@ struct Fetched {
 // read.
 template <int kPer>
 __device__ __noinline__ uint4 load_within(uintptr_t at, Span m) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
+  uint32_t e[4 * kPer];
+#pragma unroll
   for (int j = 0; j < 4 * kPer; ++j) {
     const uintptr_t p = at + (4 / kPer) * j;
-    if (p < m.lo || p >= m.hi) continue;
-    const uint32_t e = kPer == 2 ? *reinterpret_cast<const uint16_t*>(p) : *reinterpret_cast<const uint32_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i == j / kPer) w[i] |= kPer == 2 ? e << (16 * (j & 1)) : e;
+    e[j] = 0u;
+    if (p >= m.lo && p < m.hi) e[j] = kPer == 2 ? *reinterpret_cast<const uint16_t*>(p) : *reinterpret_cast<const uint32_t*>(p);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (kPer == 2) return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  else return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
 template <class V, bool kWhole>
@@ -147,7 +148,7 @@ __device__ __forceinline__ void fetch_columns(Fetched<V, kWhole>& f, const typen
     for (int i = 0; i < kN / 4 + 1; ++i) {
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
       if (c.first + kIn * i < c.cols + off) {  // the word holds an element of the row
-        if (inside) x = from[i];
+        if (inside || m.holds(from + i)) x = from[i];
         else x = load_within<WordsOf<V>::kPer>(reinterpret_cast<uintptr_t>(from + i), m);
       }
       f.w[4 * i] = x.x, f.w[4 * i + 1] = x.y, f.w[4 * i + 2] = x.z, f.w[4 * i + 3] = x.w;
@@ -157,9 +158,9 @@ __device__ __forceinline__ void fetch_columns(Fetched<V, kWhole>& f, const typen
 
 // The vector: 0 past the row's end.
 template <class V, bool kWhole>
-__device__ __forceinline__ void take_columns(V& x, Fetched<V, kWhole>& f, const typename V::raw* row, const Columns<kWhole>& c) {
+__device__ __forceinline__ void take_columns(V& x, Fetched<V, kWhole>& f, uint32_t off, const Columns<kWhole>& c) {
   constexpr int kN = Fetched<V, kWhole>::kN, kPer = WordsOf<V>::kPer;
-  if constexpr (!kWhole) shift_down<kN + 4, kPer>(f.w, offset_of(row));
+  if constexpr (!kWhole) shift_down<kN + 4, kPer>(f.w, off);
 #pragma unroll
   for (int i = 0; i < kN; ++i) words(x)[i] = f.w[i];
   if constexpr (!kWhole) {
@@ -172,6 +173,11 @@ __device__ __forceinline__ void take_columns(V& x, Fetched<V, kWhole>& f, const 
       }
     }
   }
+}
+
+template <class V, bool kWhole>
+__device__ __forceinline__ void take_columns(V& x, Fetched<V, kWhole>& f, const typename V::raw* row, const Columns<kWhole>& c) {
+  take_columns(x, f, kWhole ? 0u : offset_of(row), c);
 }
 
 // Both at once.
