@@ -16,77 +16,55 @@ using namespace mx;
 constexpr int kRowThreads = 256;
 constexpr int kUnits = 4;
 
-// The pieces of 256 columns that a warp takes: kUnits consecutive ones of the
-// rows one after another, a lane eight columns of each and four lanes a block.
-// They go through every step side by side.
-struct Walk {
-  uint32_t row, piece, pieces;
-  __device__ __forceinline__ Walk(uint32_t unit, const FastDiv& per_row) : pieces(per_row.d) {
-    row = div_by(unit, per_row);
-    piece = unit - row * per_row.d;
-  }
-  __device__ __forceinline__ void next() {
-    if (++piece == pieces) piece = 0, ++row;
-  }
-  template <bool kWhole>
-  __device__ __forceinline__ Columns<kWhole> columns(int64_t cols) const {
-    return {256 * piece, threadIdx.x & 31, (uint32_t)cols};
-  }
-};
-
+// A warp takes up to kUnits pieces of 256 columns of one row, a lane eight columns
+// of each and four lanes a block; they go through every step side by side.
 template <class T, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads) mx8_quant_kernel(const __grid_constant__ Mx8QuantArgs a,
                                                                 const FastDiv per_row, const uint32_t units) {
-  const uint32_t u0 = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kUnits;
-  if (u0 >= units) return;
+  const uint32_t u = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (u >= units) return;
+  const uint32_t number = div_by(u, per_row), first = (u - number * per_row.d) * (256 * kUnits), cols = (uint32_t)a.cols;
+  const typename T::raw* row = row_of<T>(a.src, number, a.ld);
+  const Row8 out = row_of(a.out, number);
   Fetched<typename T::V, kWhole> f[kUnits];
   const Span span = span_of<T>(a.src, a.rows, a.cols, a.ld);
-  Walk w(u0, per_row);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k)
+    if (first + 256 * k < cols) fetch_columns(f[k], row, Columns<kWhole>(first + 256 * k, lane, cols), span);
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
-    if (u0 + k < units) fetch_columns(f[k], row_of<T>(a.src, w.row, a.ld), w.columns<kWhole>(a.cols), span);
-    w.next();
-  }
-  w = Walk(u0, per_row);
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    if (u0 + k < units) {
-      const Columns<kWhole> c = w.columns<kWhole>(a.cols);
-      typename T::V x;
-      float v[8];
-      take_columns(x, f[k], row_of<T>(a.src, w.row, a.ld), c);
-      x.values(v);
-      store_columns8(row_of(a.out, w.row), c, x, v);
-    }
-    w.next();
+    if (first + 256 * k >= cols) break;
+    const Columns<kWhole> c(first + 256 * k, lane, cols);
+    typename T::V x;
+    float v[8];
+    take_columns(x, f[k], row, c);
+    x.values(v);
+    store_columns8(out, c, x, v);
   }
 }
 
 template <class T, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads) mx8_dequant_kernel(const __grid_constant__ Mx8DequantArgs a,
                                                                   const FastDiv per_row, const uint32_t units) {
-  const uint32_t u0 = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kUnits;
-  if (u0 >= units) return;
+  const uint32_t u = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (u >= units) return;
+  const uint32_t number = div_by(u, per_row), first = (u - number * per_row.d) * (256 * kUnits), cols = (uint32_t)a.in.cols;
+  const Row8 in = row_of(a.in, number);
+  typename T::raw* row = row_of<T>(a.dst, number, a.ld);
   Fetched8 f[kUnits];
-  Walk w(u0, per_row);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k)
+    if (first + 256 * k < cols) fetch_columns8(f[k], in, Columns<kWhole>(first + 256 * k, lane, cols));
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
-    if (u0 + k < units) fetch_columns8(f[k], row_of(a.in, w.row), w.columns<kWhole>(a.in.cols));
-    w.next();
-  }
-  w = Walk(u0, per_row);
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    if (u0 + k < units) {
-      const Columns<kWhole> c = w.columns<kWhole>(a.in.cols);
-      float v[8];
-      typename T::V x;
-      take_columns8(v, f[k], c, 1.0f);
-      finite_in<T>(v);
-      round_to(x, v);
-      store_columns(row_of<T>(a.dst, w.row, a.ld), c, x);
-    }
-    w.next();
+    if (first + 256 * k >= cols) break;
+    float v[8];
+    typename T::V x;
+    elements8(f[k].w, v);
+    scale8(v, scale_value(f[k].s));
+    finite_in<T>(v);
+    round_to(x, v);
+    store_columns(row, Columns<kWhole>(first + 256 * k, lane, cols), x);
   }
 }
 
@@ -207,12 +185,12 @@ bool launch_of(const void* dense, int64_t ld, const Mx8Matrix& m, Launch* l) {
     l->grid = (unsigned)grid;
     return grid <= 0x7FFFFFFFll;
   }
-  Pieces p;
-  if (!pieces_of(m.rows, m.cols, false, &p)) return false;
-  l->per_row = p.per_row, l->units = p.units;
+  const int64_t per = (m.cols + 256 * kUnits - 1) / (256 * kUnits), units = per * m.rows;
+  l->per_row = fast_div((uint32_t)per), l->units = (uint32_t)units;
   l->whole = m.cols % 8 == 0 && aligned(dense, ld * b);
-  l->grid = (p.units + kUnits * kRowThreads / 32 - 1) / (kUnits * kRowThreads / 32);
-  return true;
+  l->grid = (unsigned)((units + kRowThreads / 32 - 1) / (kRowThreads / 32));
+  // as FastDiv allows; more whole rows of so many columns are more memory than there is
+  return units <= 0x7FFFFFFFll;
 }
 
 template <class T>

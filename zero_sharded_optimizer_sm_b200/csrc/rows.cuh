@@ -189,13 +189,14 @@ __device__ __forceinline__ void load_columns(V& x, const typename V::raw* row, c
 }
 
 // A vector as it is, into its row: an unaligned one's words are put together
-// from two neighbouring lanes' vectors; the row's ends and what a warp's first
-// and last lanes lack a neighbour for go element by element.  Called by whole
-// warps whose lanes have neighbouring vectors.
-__device__ __forceinline__ void store_whole(uint16_t* p, const uint32_t (&w)[4]) {
+// from two neighbouring lanes' vectors; what a warp's first and last lanes lack a
+// neighbour for -- eight elements of 16 bits, four of 32 -- goes to as many lanes
+// and out in one store; the row's last word goes element by element.  Called by
+// whole warps whose lanes have neighbouring vectors.
+__device__ __forceinline__ void store_whole(uint16_t* p, const uint32_t* w) {
   st_stream(p, make_uint4(w[0], w[1], w[2], w[3]));
 }
-__device__ __forceinline__ void store_whole(float* p, const uint32_t (&w)[8]) {
+__device__ __forceinline__ void store_whole(float* p, const uint32_t* w) {
   // one 32-byte store where that is aligned: of two of 16 each would touch every sector of the warp's
   if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
     asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -206,45 +207,65 @@ __device__ __forceinline__ void store_whole(float* p, const uint32_t (&w)[8]) {
   __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
   __stcs(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
 }
-__device__ __forceinline__ void store_some(uint16_t* p, const uint32_t (&w)[4], int from, int to) {
+template <class raw>
+__device__ __forceinline__ void store_some(raw* p, const uint32_t* w, int from, int to) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j >= from && j < to) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+  for (int j = 0; j < 8; ++j) {
+    if (j < from || j >= to) continue;
+    if constexpr (sizeof(raw) == 2) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    else p[j] = __uint_as_float(w[j]);
+  }
 }
-__device__ __forceinline__ void store_some(float* p, const uint32_t (&w)[8], int from, int to) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j >= from && j < to) p[j] = __uint_as_float(w[j]);
-}
+
 template <class V, bool kWhole>
 __device__ __forceinline__ void store_columns(typename V::raw* row, const Columns<kWhole>& c, const V& x) {
-  constexpr int kN = WordsOf<V>::kN;
+  using raw = typename V::raw;
+  constexpr int kN = WordsOf<V>::kN, kPer = WordsOf<V>::kPer;
   if constexpr (kWhole) {
     if (c.any()) store_whole(row + c.first, words(x));
   } else {
-    const uint32_t off = offset_of(row);
-    const int left = c.any() ? (int)min(c.cols - c.first, 8u) : 0;  // my elements
+    const uint32_t off = offset_of(row), lane = threadIdx.x & 31;
+    const int there = (int)(c.cols - c.first);  // elements of the row from mine on (below 0: it ended before)
     if (off == 0) {
-      if (left == 8) store_whole(row + c.first, words(x));
-      else store_some(row + c.first, words(x), 0, left);
+      if (there >= 8) store_whole(row + c.first, words(x));
+      else store_some(row + c.first, words(x), 0, there);
       return;
     }
-    const int lane = threadIdx.x & 31;
-    // the neighbour's last elements before mine: the words from 8 - off on of
-    // both vectors one after another
-    uint32_t w[kN + 4], out[kN];
+    // the neighbour's last elements before mine: of both vectors one after
+    // another what is from 8 - off on
+    uint32_t w[kN + 4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xFFFFFFFFu, words(x)[kN - 4 + i], 1);
 #pragma unroll
     for (int i = 0; i < kN; ++i) w[4 + i] = words(x)[i];
-    shift_down<kN + 4, WordsOf<V>::kPer>(w, 4 * WordsOf<V>::kPer - off);
+    shift_down<kN + 4, kPer>(w, 4 * kPer - off);
+    raw* p = row + (int64_t)c.first - off;  // elements -off .. 7 - off of mine
+    const int end = min(there + (int)off, 8);
+    if (end == 8) {
+      if (lane > 0) store_whole(p, w);
+      else if constexpr (kN == 8) __stcs(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    } else if (end > 0) {
+      store_some(p, w, lane > 0 ? 0 : (int)off, end);
+    }
+    // lane j: of the elements that begin lane 0's vector and end lane 31's, in a word each, the jth
+    constexpr uint32_t kIn = 16 / sizeof(raw);  // elements of a word
+    const bool last = lane >= kIn - off;
+    uint32_t e[4];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) out[i] = w[i];
-    // elements -off .. 7 - off of mine: all of them, or those that are there
-    const int end = min((int)off + (c.any() ? left : min((int)(c.cols - c.first), 0)), 8);
-    if (lane > 0 && end == 8) store_whole(row + c.first - off, out);
-    else store_some(row + (int64_t)c.first - off, out, lane > 0 ? 0 : (int)off, end);
-    if (lane == 31 && left + (int)off > 8) store_some(row + c.first, words(x), 8 - (int)off, left);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t mine = lane == 31 ? words(x)[kN - 4 + i] : words(x)[i];
+      e[i] = __shfl_sync(0xFFFFFFFFu, mine, last ? 31 : 0);
+    }
+    const int first_there = __shfl_sync(0xFFFFFFFFu, there, 0);
+    const uint32_t at = last ? 32 * 8 - kIn + lane : lane;  // from the warp's first column on
+    // (of a lane 0 whose word the row's end is in, the elements have gone out above)
+    if (lane < kIn && (int)at < first_there && (last || first_there + (int)off >= 8)) {
+      const uint32_t i = lane / kPer;
+      const uint32_t v = i < 2 ? (i < 1 ? e[0] : e[1]) : (i < 3 ? e[2] : e[3]);
+      raw* q = row + (c.first - 8 * lane) + at;
+      if constexpr (kPer == 2) *q = (uint16_t)(v >> (16 * (lane & 1)));
+      else *q = __uint_as_float(v);
+    }
   }
 }
 
@@ -311,9 +332,11 @@ __device__ __forceinline__ void take_columns8(float (&v)[8], const Fetched8& f, 
   elements8(f.w, v);
   scale8(v, __fmul_rn(scale_value(f.s), unit));
   if constexpr (!kWhole) {
+    if (!c.in(7)) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (!c.in(j)) v[j] = 0.0f;  // (what fills up the last block is not the row's)
+      for (int j = 0; j < 8; ++j)
+        if (!c.in(j)) v[j] = 0.0f;  // (what fills up the last block is not the row's)
+    }
   }
 }
 
