@@ -170,6 +170,35 @@ def test_backward_into_a_gradient_buffer(z, dtype, out):
         assert torch.equal(flat[rest], before[rest])
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("cols", [1, 3, 5, 8, 40, 257, 771])
+def test_both_are_the_same_at_every_offset(z, cols, dtype):
+    """The table, dy and the results at every offset of a 16-byte word, rows end
+    to end and apart: the bits of the same call on aligned rows; what is beside
+    the results stays."""
+    from test_gpu_rms_norm import _laid
+    n, vocab, up = 150, 70, -(-cols // 8) * 8
+    table, dy, t = normal(vocab, cols, dtype, 1), normal(n, cols, dtype, 2), tokens_of(n, vocab, 3, "outside")
+    t[t == 11] = 12
+    t[20:90] = 5
+    want = z.embedding(t, _laid(table, 0, up)[0], 1.5)
+    grad = z.embedding_backward(_laid(dy, 0, up)[0], t, vocab, 1.5, out=_laid(table, 0, up)[0])
+    added = z.embedding_backward(_laid(dy, 0, up)[0], t, vocab, 1.5, out=_laid(table, 0, up)[0], accumulate=True)
+    for off in range(8):
+        for pitch in (cols, cols + 1 + off % 4):
+            out, space = _laid(dy, (off + 3) % 8, pitch)
+            into, other = _laid(table, off, pitch)
+            assert torch.equal(z.embedding(t, _laid(table, off, pitch)[0], 1.5, out=out), want)
+            z.embedding_backward(_laid(dy, (off + 5) % 8, pitch)[0], t, vocab, 1.5, out=into, accumulate=True)
+            assert torch.equal(into, added), (off, pitch)
+            z.embedding_backward(_laid(dy, (off + 5) % 8, pitch)[0], t, vocab, 1.5, out=into)
+            assert torch.equal(into, grad), (off, pitch)
+            for view, memory in ((out, space), (into, other)):
+                rest = torch.ones(memory.shape[0], dtype=torch.bool, device="cuda")
+                rest.as_strided(view.shape, view.stride(), storage_offset=view.storage_offset()).fill_(False)
+                assert (memory[rest] == 7.0).all()
+
+
 def test_backward_is_the_lookups_gradient_by_differences(z):
     """The lookup is linear in the table: with whole numbers its differences are
     the gradient, exactly."""

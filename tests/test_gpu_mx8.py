@@ -131,6 +131,30 @@ def test_strides_alignments_and_pitches(z, dtype, pitch, off):
     assert (back[rest] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_every_offset_and_many_lengths(z, dtype):
+    """Rows that begin and end anywhere in a 16-byte word, of less than a word to
+    several warps': the last row's last word is the last of its memory."""
+    rows, each = 3, 16 // torch.empty(0, dtype=DTYPES[dtype]).element_size()
+    for cols in [*range(1, 26), 31, 32, 33, 64, 65, *range(248, 266), 511, 513, 1023, 1025, 1030]:
+        for off in range(each):
+            for pitch in (cols, cols + 1, cols + 3):
+                n = off + (rows - 1) * pitch + cols
+                space = normal(1, n, dtype, cols)[0]
+                x = space[off:].as_strided((rows, cols), (pitch, 1), storage_offset=off)
+                m = z.mx8_quantize(x)
+                back = torch.full((n,), 7.0, dtype=DTYPES[dtype], device="cuda")
+                out = back.as_strided((rows, cols), (pitch, 1), storage_offset=off)
+                z.mx8_dequantize(m, out=out)
+                want = z.mx8_quantize(x.contiguous())
+                assert torch.equal(m.codes[:, :cols], want.codes[:, :cols]), (cols, off, pitch)
+                flat = torch.empty(rows, cols + 8 - cols % 8, dtype=DTYPES[dtype], device="cuda")[:, :cols]
+                assert torch.equal(out, z.mx8_dequantize(want, out=flat)), (cols, off, pitch)
+                rest = torch.ones(n, dtype=torch.bool, device="cuda")
+                rest.as_strided((rows, cols), (pitch, 1), storage_offset=off).fill_(False)
+                assert (back[rest] == 7.0).all(), (cols, off, pitch)
+
+
 def test_empty(z):
     for shape in ((0, 64), (4, 0)):
         x = torch.empty(*shape, dtype=torch.bfloat16, device="cuda")

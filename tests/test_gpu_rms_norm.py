@@ -188,6 +188,43 @@ def test_norm_backward_of_strided_rows_and_in_place(z, dtype, cols):
         assert torch.equal(space[rest], before[rest])
 
 
+def _laid(x, off, pitch):
+    """The matrix `off` elements into memory of its own, rows `pitch` apart, and that memory."""
+    rows, cols = x.shape
+    space = torch.full((off + (rows - 1) * pitch + cols,), 7.0, dtype=x.dtype, device="cuda")
+    view = space.as_strided((rows, cols), (pitch, 1), storage_offset=off)
+    view.copy_(x)
+    return view, space
+
+
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("cols", [1, 5, 8, 40, 257, 771, 1032, 2600])
+def test_norm_and_its_gradients_are_the_same_at_every_offset(z, cols, dtype, kept):
+    """Every matrix at another offset, ends of rows anywhere in a 16-byte word:
+    the bits of the same call on rows that begin on 16 bytes."""
+    rows, up = 6, -(-cols // 8) * 8
+    x, r, dy, dh = (normal(rows, cols, dtype, k) for k in range(4))
+    w = _weight(cols, dtype)
+    aligned = lambda t: _laid(t, 0, up)[0]  # noqa: E731
+    want = z.rms_norm(aligned(x), w, residual=aligned(r), y8=True, h8=True)
+    h = want.h8 if kept else aligned(want.h)
+    want_dx, want_dw = z.rms_norm_backward(aligned(dy), h, w, want.rstd, dh=aligned(dh))
+    for off in range(8):
+        at = [((off + k) % 8, cols + (off * k) % 5) for k in range(4)]
+        n = z.rms_norm(_laid(x, *at[0])[0], w, residual=_laid(r, *at[1])[0], y=_laid(x, *at[2])[0], h=_laid(x, *at[3])[0],
+                       y8=True, h8=True)
+        assert torch.equal(n.y, want.y) and torch.equal(n.h, want.h) and torch.equal(n.rstd, want.rstd)
+        assert torch.equal(n.y8.codes, want.y8.codes) and torch.equal(n.h8.codes, want.h8.codes)
+        into, space = _laid(x, *at[2])
+        dx, dw = z.rms_norm_backward(_laid(dy, *at[0])[0], h if kept else _laid(want.h, *at[1])[0], w, n.rstd,
+                                     dh=_laid(dh, *at[3])[0], dx=into)
+        assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw), (off, at)
+        rest = torch.ones(space.shape[0], dtype=torch.bool, device="cuda")
+        rest.as_strided(dx.shape, dx.stride(), storage_offset=at[2][0]).fill_(False)
+        assert (space[rest] == 7.0).all()
+
+
 def test_norm_backward_twice_is_the_same(z):
     h, dy, w = normal(3001, 1000, "bf16", 1), normal(3001, 1000, "bf16", 2), _weight(1000, "bf16")
     rstd = ref.norm(h, w, 1e-6)[1].float()

@@ -394,13 +394,15 @@ __device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64
   raw* out = static_cast<raw*>(a.dtable) + row * a.ld;
   float v[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(sum[j], a.scale);
+  for (int j = 0; j < 8; ++j) v[j] = sum[j];
   typename T::V x;
   if (a.accumulate) {
     float u[8];
     load_columns(x, out, c, span_of<T>(a.dtable, a.vocab, a.cols, a.ld));
     x.values(u);
-    plus8(v, u);
+    scale_plus8(v, a.scale, u);
+  } else {
+    scale8(v, a.scale);
   }
   round_to(x, v);
   store_columns(out, c, x);

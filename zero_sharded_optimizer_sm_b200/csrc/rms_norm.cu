@@ -242,23 +242,24 @@ __device__ __forceinline__ void add_vector(float (&dy)[8], const float (&xh)[8],
   for (int p = 0; p < 4; ++p) dot = fma2(pair(dy, p), pair(xh, p), dot);
 }
 
-// dx of one vector, without dh, in g's place: rstd (g - xh mean).
-__device__ __forceinline__ void dx_vector(float (&g)[8], const float (&xh)[8], float rstd, float mean) {
+// g - xh mean of one vector, in g's place.
+__device__ __forceinline__ void dx_vector(float (&g)[8], const float (&xh)[8], float mean) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const float2 d = fma2(pair(xh, p), make_float2(-mean, -mean), pair(g, p));
     g[2 * p] = d.x, g[2 * p + 1] = d.y;
   }
-  scale8(g, rstd);
 }
 
-// dx, rounded, with dh (a vector of the type) added if there is one.
+// dx of that, rounded: times rstd, plus dh (a vector of the type) if there is one.
 template <class T, class C>
-__device__ __forceinline__ void store_dx(typename T::raw* row, const C& c, const typename T::V* dh, float (&v)[8]) {
+__device__ __forceinline__ void store_dx(typename T::raw* row, const C& c, float rstd, const typename T::V* dh, float (&v)[8]) {
   if (dh) {
     float u[8];
     dh->values(u);
-    plus8(v, u);
+    scale_plus8(v, rstd, u);
+  } else {
+    scale8(v, rstd);
   }
   typename T::V x;
   round_to(x, v);
@@ -444,11 +445,11 @@ __global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
       typename T::V dh;
       if (c.any()) {
         if constexpr (kChunks > 1) vector(k, c, false);
-        dx_vector(g, xh, rstd, mean);
+        dx_vector(g, xh, mean);
         if constexpr (kDh)
           R::read(stage + R::dh_at(vectors) + 16 * (group * k + threadIdx.x), vectors, R::offset(a.dh, row, a.ld_dh), c, dh);
       }
-      store_dx<T>(to, c, kDh ? &dh : nullptr, g);  // (by whole warps)
+      store_dx<T>(to, c, rstd, kDh ? &dh : nullptr, g);  // (by whole warps)
     }
     to += step * a.ld_dx;
   }
@@ -524,8 +525,8 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(co
     load_dy_xh<T, kMx8>(a, row, c, rstd, g, xh);
     if (a.dh) load_columns(dh, row_of<T>(a.dh, row, a.ld_dh), c, span_of<T>(a.dh, a.rows, a.cols, a.ld_dh));
     add_vector(g, xh, w, acc, unused);
-    dx_vector(g, xh, rstd, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv));
-    store_dx<T>(row_of<T>(a.dx, row, a.ld_dx), c, a.dh ? &dh : nullptr, g);
+    dx_vector(g, xh, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv));
+    store_dx<T>(row_of<T>(a.dx, row, a.ld_dx), c, rstd, a.dh ? &dh : nullptr, g);
   }
   store_part(static_cast<float*>(a.workspace) + dots + blockIdx.y * a.cols, c, acc);
 }

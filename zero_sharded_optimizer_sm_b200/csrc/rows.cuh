@@ -269,7 +269,9 @@ __device__ __forceinline__ void store_columns(typename V::raw* row, const Column
   }
 }
 
-// Pairs at once.
+// Pairs at once.  (The assembler rounds a packed product and the packed sum that
+// takes it once, as a multiply-add, in spite of .rn on both: where the two meet
+// the multiply-add is written, so that it does not depend on the code around.)
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("add.rn.f32x2 %0, %1, %2;"
@@ -297,6 +299,15 @@ __device__ __forceinline__ void plus8(float (&v)[8], const float (&w)[8]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const float2 f = add2(pair(v, p), pair(w, p));
+    v[2 * p] = f.x, v[2 * p + 1] = f.y;
+  }
+}
+
+// v s + w
+__device__ __forceinline__ void scale_plus8(float (&v)[8], float s, const float (&w)[8]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float2 f = fma2(pair(v, p), make_float2(s, s), pair(w, p));
     v[2 * p] = f.x, v[2 * p + 1] = f.y;
   }
 }
