@@ -274,7 +274,7 @@ def test_wrappers_refuse_what_does_not_fit(z):
                  lambda: z.embedding_backward(dy.double(), t, 9)):
         with pytest.raises(ValueError):
             call()
-    for call in (lambda: z.embedding(t, table, float("nan")), lambda: z.embedding_backward(dy, t, 9, float("inf")),
+    for call in (lambda: z.embedding_backward(dy, t, -1), lambda: z.embedding(t, table, float("nan")), lambda: z.embedding_backward(dy, t, 9, float("inf")),
                  lambda: z.embedding_backward(dy[:1].expand(4, 64), t, 9)):
         with pytest.raises(z.ZeroError):
             call()

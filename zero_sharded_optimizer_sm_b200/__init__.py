@@ -1346,10 +1346,10 @@ def embedding_backward(dy, tokens, vocab: int, scale: float = 1.0, out=None, acc
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     side = _beside(device, stream)
-    out = _result(out, vocab, cols, dy.dtype, device, side)
-    optr, ocode, ldo, _, _ = _dense(out, "out")
     need = ctypes.c_int64()
     _mx4_check(zero_embedding_backward_workspace(n, vocab, cols, need), "zero_embedding_backward_workspace")
+    out = _result(out, vocab, cols, dy.dtype, device, side)
+    optr, ocode, ldo, _, _ = _dense(out, "out")
     space = _empty(need.value, _T.uint8, device, side, False)
     _mx4_check(_on_device(device, stream, zero_embedding_backward, ptr, code, n, cols, ld, tptr, tsize, vocab, scale, optr,
                           ocode, ldo, 1 if accumulate else 0, space.data_ptr(), need.value), "zero_embedding_backward")

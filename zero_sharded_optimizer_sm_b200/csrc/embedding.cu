@@ -58,7 +58,11 @@ struct Mx4Rows {
   }
 };
 
-// A warp takes up to kPieces pieces of 256 columns of one token, side by side.
+// A warp takes up to kPieces pieces of 256 columns of one token, side by side: the
+// token is read once for them.  8192 tokens of an MX4 table of 32000 x 4096 take
+// 13.4 us, 74 MB of which 67 are written (11.3 at the copy's rate; a warp to
+// scattered pieces of four tokens 21); rows of odd length, 8000 of 2421 bf16, 24
+// of 12, bound by instructions (69 % of the issue slots).
 template <class S, class T, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads) embedding_kernel(const __grid_constant__ EmbeddingArgs a, const FastDiv per_row,
                                                                 const uint32_t units) {
@@ -209,7 +213,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
 
 // Batches of up to kClusterMax positions are sorted by one cluster of CTAs in
 // one launch: every CTA keeps its part of the (token, position) pairs in shared
-// memory, and a pass writes them to their places in the cluster's CTAs.
+// memory, and a pass writes them to their places in the cluster's CTAs.  16384
+// positions of 16-bit tokens take some 8 us (as three launches a pass of 8 bits
+// 30), latency throughout: three barriers and two trips through the cluster's
+// memory a pass.
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterCtas = 8;
@@ -409,25 +416,16 @@ __device__ __forceinline__ void finish_row(const EmbeddingBackwardArgs& a, int64
 }
 
 // One warp clears `bytes` bytes at p, an element's multiple.
-__device__ __forceinline__ void clear_row(uint8_t* p, uint32_t bytes) {
-  const uint32_t lane = threadIdx.x & 31;
-  const uint32_t head = min((uint32_t)(-reinterpret_cast<uintptr_t>(p) & 15u), bytes);
-  if (head) {
-    if (2 * lane < head) *reinterpret_cast<uint16_t*>(p + 2 * lane) = 0;
-    p += head, bytes -= head;
-  }
-  const uint32_t n = bytes / 16;
-  uint4* q = reinterpret_cast<uint4*>(p) + lane;
-  uint32_t i = 0;
-  for (; i + 128 <= n; i += 128) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) __stcs(q + i + 32 * k, make_uint4(0u, 0u, 0u, 0u));
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (i + 32 * k + lane < n) __stcs(q + i + 32 * k, make_uint4(0u, 0u, 0u, 0u));
-  if (const uint32_t tail = bytes & 15u)
-    if (2 * lane < tail) *reinterpret_cast<uint16_t*>(p + 16 * n + 2 * lane) = 0;
+__device__ __forceinline__ void clear_row(uint8_t* p, int64_t bytes) {
+  const int lane = threadIdx.x & 31;
+  const int64_t head = min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15u), bytes);
+  if (2 * lane < head) *reinterpret_cast<uint16_t*>(p + 2 * lane) = 0;
+  p += head, bytes -= head;
+  const int64_t n = bytes / 16;
+  uint4* q = reinterpret_cast<uint4*>(p);
+#pragma unroll 4
+  for (int64_t i = lane; i < n; i += 32) __stcs(q + i, make_uint4(0u, 0u, 0u, 0u));
+  if (2 * lane < (int)(bytes & 15)) *reinterpret_cast<uint16_t*>(p + 16 * n + 2 * lane) = 0;
 }
 
 // The CTA's share of the rows without a token, by its first kThreads threads.
@@ -498,7 +496,7 @@ __device__ __forceinline__ void clear_rows(const EmbeddingBackwardArgs& a, const
     } else {
       uint8_t* row = z.table + (lo + warp) * z.pitch_bytes;
       for (uint32_t r = warp; r < rows; r += (kThreads / 32), row += (kThreads / 32) * z.pitch_bytes)
-        if (!present(r)) clear_row(row, (uint32_t)z.row_bytes);
+        if (!present(r)) clear_row(row, z.row_bytes);
     }
     sync();
   }

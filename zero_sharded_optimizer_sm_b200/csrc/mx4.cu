@@ -181,9 +181,10 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     x32[j] = column[j * kTileWords];
-    if constexpr (kPer == 2) m = __vmaxu2(m, x32[j] & 0x7FFF7FFFu);
+    if constexpr (kPer == 2) m = V::larger(m, x32[j]);
     else m = max(m, x32[j] & 0x7FFFFFFFu);
   }
+  m &= kPer == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
 #pragma unroll
   for (int h = 0; h < kPer; ++h) {
     if (oc + h >= a.cols) break;
@@ -201,7 +202,8 @@ __device__ __forceinline__ void quantize_tile(const MxQuantArgs& a, uint32_t ind
     for (int k = 0; k < 4; ++k) {
       float e[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = __fmul_rn(value(8 * k + j), inv);
+      for (int j = 0; j < 8; ++j) e[j] = value(8 * k + j);
+      scale_by(e, inv);
       w[k] = kStochastic ? encode8_stochastic(e, (uint64_t)((oc + h) * nbt + b), k, a.seed) : encode8(e);
       if (s == 255u) w[k] = 0u;
     }

@@ -36,6 +36,23 @@ struct Half<F16> {
   }
 };
 
+// Of two words of two elements each, the larger magnitudes (their signs are of no
+// use; a NaN counts as larger than any number).
+template <class F>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t larger2<Bf16>(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+template <>
+__device__ __forceinline__ uint32_t larger2<F16>(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+
 // Eight consecutive elements of a storage type, kept as loaded: their values,
 // and the binary32 pattern of the largest magnitude (an infinity or NaN
 // counts as larger than any number).
@@ -65,11 +82,12 @@ struct Vec16 {  // bf16 or binary16
       w[j] = (2 * j < n ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)p[2 * j + 1] << 16 : 0u);
   }
   __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return larger2<F>(a, b); }
   static __device__ __forceinline__ float lo(uint32_t x) { return F::lo(x); }
   static __device__ __forceinline__ float hi(uint32_t x) { return F::hi(x); }
   __device__ __forceinline__ uint32_t max_bits() const {
     // 16-bit patterns without their signs order as their magnitudes do
-    uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    uint32_t m = larger(larger(w[0], w[1]), larger(w[2], w[3])) & 0x7FFF7FFFu;
     m = max(m & 0xFFFFu, m >> 16);
     return __float_as_uint(F::f32((uint16_t)m));
   }
@@ -125,15 +143,22 @@ __device__ __forceinline__ void load8(V& x, const typename V::raw* p, int64_t n,
   else x.clear();
 }
 
+// Eight products with a power of two, in pairs.
+__device__ __forceinline__ void scale_by(float (&v)[8], float s) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 f = mul2(make_float2(v[j], v[j + 1]), make_float2(s, s));
+    v[j] = f.x, v[j + 1] = f.y;
+  }
+}
+
 // The codes of eight elements from their block's scale byte.  `block` and c
 // (the vector's place in the block) number the random numbers.
 template <bool kStochastic, class V>
 __device__ __forceinline__ uint32_t encode(const V& x, uint32_t s, uint64_t block, int c, uint64_t seed) {
   float v[8];
   x.values(v);
-  const float inv = inverse_scale(s);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
+  scale_by(v, inverse_scale(s));
   const uint32_t w = kStochastic ? encode8_stochastic(v, block, c, seed) : encode8(v);
   return s == 255u ? 0u : w;
 }
