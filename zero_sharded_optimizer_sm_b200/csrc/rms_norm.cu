@@ -17,12 +17,13 @@ using namespace mx;
 // ----------------------------------------------------------------- forward --
 
 // Sum over a warp, and from the warps' binary32 sums on in binary64 over the
-// block (kWarp: a warp has its own row): every thread gets the same bits.
-template <bool kWarp>
+// block; or over the kLanes (of a warp, not 0) that share a row: every thread of
+// a row gets the same bits.
+template <int kLanes>
 __device__ __forceinline__ double group_sum(float mine, float* smem) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine = __fadd_rn(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
-  if constexpr (kWarp) return (double)mine;
+  for (int o = kLanes ? kLanes / 2 : 16; o > 0; o >>= 1) mine = __fadd_rn(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
+  if constexpr (kLanes > 0) return (double)mine;
   const uint32_t warps = blockDim.x / 32;
   if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = mine;
   __syncthreads();
@@ -87,12 +88,12 @@ __device__ __forceinline__ float2 square_sum(const float (&v)[8], float2 ss) {
 }
 
 // All results of one vector of h.  Called by whole warps.
-template <class T, class C>
+template <class T, int kLanes, class C>
 __device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& row, const C& c, float rstd,
                                        const typename T::V& x) {
   float v[8], w[8];
   x.values(v);
-  if (a.h) store_columns(row.h, c, x);
+  if (a.h) store_columns<kLanes>(row.h, c, x);
   if (a.h8.codes) store_columns8(row.h8, c, x, v);
   if (!a.y && !a.y8.codes) return;
   load_weights(a.weight, a.w_type, a.w_aligned, c, w);
@@ -100,7 +101,7 @@ __device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& r
   times8(v, w);
   typename T::V y;
   round_to(y, v);
-  if (a.y) store_columns(row.y, c, y);
+  if (a.y) store_columns<kLanes>(row.y, c, y);
   if (a.y8.codes) {
     if (!isfinite(rstd)) {  // past the row x and w are 0, but 0 times this is not
 #pragma unroll
@@ -113,7 +114,7 @@ __device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& r
   }
 }
 
-// A block to a row, or (kWarp) a warp, kChunks vectors of eight elements a
+// A block to a row, or kLanes of a warp, kChunks vectors of eight elements a
 // thread; the host picks the block's threads to fit the row.  Blocks that end
 // make room for others whose loads go out at once, so that nothing has to be
 // fetched ahead: 8192 x 4096 bf16 with a residual and all results, 338 MB, takes
@@ -122,24 +123,26 @@ __device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& r
 // too.  Rows of odd length, 6000 x 2421 binary16 with all results, take 46 of 22:
 // instructions (75 %).  One token of 4096 takes 2.7, its launch and two trips to
 // memory.
-constexpr int kWarpRows = 4;  // of a block
-template <class T, bool kWhole, bool kWarp, int kChunks>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 512) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
+constexpr int kLanesThreads = 128;  // of a block whose warps have rows of their own
+template <class T, bool kWhole, int kLanes, int kChunks>
+__global__ void __launch_bounds__(kLanes ? kLanesThreads : 512) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
                                                                                 const double inv_cols) {
+  static_assert(kLanes % 4 == 0, "whole blocks of MX8");
   __shared__ float smem[32];
-  const uint32_t number = kWarp ? blockIdx.x * kWarpRows + threadIdx.x / 32 : blockIdx.x;
-  if (kWarp && number >= (uint32_t)a.rows) return;
-  const NormRow<T> row(a, number);
-  const uint32_t group = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const uint32_t group = kLanes ? kLanes : blockDim.x, t = kLanes ? threadIdx.x & (kLanes - 1) : threadIdx.x;
+  const uint32_t number = kLanes ? (blockIdx.x * kLanesThreads + threadIdx.x) / group : blockIdx.x;
+  const bool there = kLanes == 0 || number < (uint32_t)a.rows;  // past the end: a row of no columns, for the shuffles' sake
+  const NormRow<T> row(a, there ? number : 0);
+  const uint32_t cols = there ? (uint32_t)a.cols : 0u;
   using C = Columns<kWhole>;
   typename T::V x[kChunks];
   if constexpr (kChunks == 1) {
-    const C c[1] = {C(0, t, (uint32_t)a.cols)};
+    const C c[1] = {C(0, t, cols)};
     load_h<T>(a, row, c, x);
   } else {
 #pragma unroll
     for (int k = 0; k < kChunks; k += 2) {
-      const C c[2] = {C(8 * group * k, t, (uint32_t)a.cols), C(8 * group * (k + 1), t, (uint32_t)a.cols)};
+      const C c[2] = {C(8 * group * k, t, cols), C(8 * group * (k + 1), t, cols)};
       load_h<T>(a, row, c, reinterpret_cast<typename T::V(&)[2]>(x[k]));
     }
   }
@@ -150,10 +153,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : 512) rms_norm_kernel(
     x[k].values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<kWarp>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
-  if (a.rstd && t == 0) a.rstd[number] = rstd;
+  const float rstd = rstd_of(group_sum<kLanes>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  if (a.rstd && t == 0 && there) a.rstd[number] = rstd;
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) finish<T>(a, row, C(8 * group * k, t, (uint32_t)a.cols), rstd, x[k]);
+  for (int k = 0; k < kChunks; ++k) finish<T, kLanes ? kLanes : 32>(a, row, C(8 * group * k, t, cols), rstd, x[k]);
 }
 
 // Rows too long for registers: read a second time (a thread reads its own
@@ -175,13 +178,13 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __gri
     x[0].values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<false>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  const float rstd = rstd_of(group_sum<0>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
   for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
     typename T::V x[1];
     const C c[1] = {C(first, threadIdx.x, cols)};
     load_h<T>(a, row, c, x);
-    finish<T>(a, row, c[0], rstd, x[0]);
+    finish<T, 32>(a, row, c[0], rstd, x[0]);
   }
 }
 
@@ -204,34 +207,28 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __gri
 constexpr int64_t kSms = 148;
 constexpr uint32_t kMaxThreads = 512;
 
-// Threads of a block and vectors of a thread for rows of so many columns.
-struct Shape {
-  uint32_t threads, chunks;
-};
-Shape shape_of(int64_t cols) {
-  const uint32_t vectors = (uint32_t)((cols + 7) / 8);
-  const uint32_t chunks = vectors <= kMaxThreads ? 1 : vectors <= 2 * kMaxThreads ? 2 : 4;
-  return {std::max(32u, ((vectors + chunks - 1) / chunks + 31) / 32 * 32), chunks};
-}
+// The longest rows that a block takes, a vector a thread; longer ones go through
+// memory twice (see below).
+constexpr int64_t kRingCols = 8 * kMaxThreads;
 
-// Blocks to an SM, and blocks at most: as many as are there at a time (the
-// kernels' registers allow 1024 threads).
-uint32_t blocks_to_sm(const Shape& p) { return std::max(1u, std::min(1024 / p.threads / p.chunks, 16u)); }
+// Threads of a block, blocks to an SM (the kernel's registers allow 1024
+// threads), and blocks at most: as many as are there at a time.
+uint32_t threads_of(int64_t cols) { return (uint32_t)((cols + 255) / 256 * 32); }
+uint32_t blocks_to_sm(int64_t cols) { return std::min(1024 / threads_of(cols), 16u); }
 int64_t parts_of(int64_t rows, int64_t cols) {
   // four rows a block where that leaves every SM one: a block's start and its
   // part of dw cost as much as some rows do (1237 x 771: one row a block 14 us)
   const int64_t few = std::max((rows + 3) / 4, std::min(rows, kSms));
-  return std::max<int64_t>(1, std::min(few, kSms * blocks_to_sm(shape_of(cols))));
+  return std::max<int64_t>(1, std::min(few, kSms * blocks_to_sm(cols)));
 }
 
-// The longest rows of which two stages fit; longer ones go through memory twice.
-int64_t wide_from(int type, bool whole) { return (type == kMxF32 ? 4096 : 8192) * (whole ? 2 : 1); }
-
-// Sum over the block in binary32; smem holds two rounds' values, so that one
-// barrier a round will do.
+// Sum over the block in binary32 (smem holds two rounds' values, so that one
+// barrier a round will do), or over the kLanes of a warp that share a row.
+template <int kLanes>
 __device__ __forceinline__ float block_sum(float v, float (*smem)[32], int round) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = kLanes ? kLanes / 2 : 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if constexpr (kLanes > 0) return v;
   const uint32_t lane = threadIdx.x & 31, warps = blockDim.x / 32;
   if (warps == 1) return v;
   if (lane == 0) smem[round & 1][threadIdx.x >> 5] = v;
@@ -262,8 +259,11 @@ __device__ __forceinline__ void dx_vector(float (&g)[8], const float (&xh)[8], f
   }
 }
 
+// The rows of a block at a time: of one warp, kLanes to a row, or (0) one.
+__host__ __device__ constexpr int rows_at_once(int lanes) { return lanes ? 32 / lanes : 1; }
+
 // dx of that, rounded: times rstd, plus dh (a vector of the type) if there is one.
-template <class T, class C>
+template <class T, int kLanes, class C>
 __device__ __forceinline__ void store_dx(typename T::raw* row, const C& c, float rstd, const typename T::V* dh, float (&v)[8]) {
   if (dh) {
     float u[8];
@@ -274,7 +274,7 @@ __device__ __forceinline__ void store_dx(typename T::raw* row, const C& c, float
   }
   typename T::V x;
   round_to(x, v);
-  store_columns(row, c, x);
+  store_columns<kLanes>(row, c, x);
 }
 
 template <class C, class A>
@@ -286,7 +286,7 @@ __device__ __forceinline__ void store_part(float* out, const C& c, const A& acc)
 
 // One row's stage of the ring: dy, dh, h of every thread's vectors, 16 bytes of
 // each thread next to another's.
-template <class T, bool kWhole, int kChunks, bool kMx8, bool kDh>
+template <class T, bool kWhole, bool kMx8, bool kDh>
 struct Ring {
   using V = typename T::V;
   using raw = typename T::raw;
@@ -304,8 +304,7 @@ struct Ring {
     __device__ __forceinline__ Rows(const RmsNormBackwardArgs& a, int64_t row)
         : dy(row_of<T>(a.dy, row, a.ld_dy)), dh(row_of<T>(a.dh, row, a.ld_dh)), h(row_of<T>(a.h, row, a.ld_h)),
           codes(a.h8.codes + row * a.h8.code_pitch) {}
-    __device__ __forceinline__ void next(const RmsNormBackwardArgs& a) {
-      const uint32_t step = gridDim.x;
+    __device__ __forceinline__ void next(const RmsNormBackwardArgs& a, uint32_t step) {
       dy += step * a.ld_dy;
       if constexpr (kDh) dh += step * a.ld_dh;
       if constexpr (kMx8) codes += step * a.h8.code_pitch;
@@ -332,19 +331,14 @@ struct Ring {
     }
   }
   // Asks for a row if there is one; the group is there all the same.
-  static __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, const Rows& row, bool there, uint8_t* to) {
-    if (there) {
-      const uint32_t vectors = blockDim.x * kChunks;
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        const uint32_t v = blockDim.x * k + threadIdx.x;
-        const Columns<kWhole> c(0, v, (uint32_t)a.cols);
-        if (!c.any()) break;
-        fetch16(to + 16 * v, vectors, row.dy, c, a.dy, a.dy_end);
-        if constexpr (kDh) fetch16(to + dh_at(vectors) + 16 * v, vectors, row.dh, c, a.dh, a.dh_end);
-        if constexpr (kMx8) copy_async8(to + h_at(vectors) + 8 * v, row.codes + c.first);
-        else fetch16(to + h_at(vectors) + 16 * v, vectors, row.h, c, a.h, a.h_end);
-      }
+  static __device__ __forceinline__ void fetch(const RmsNormBackwardArgs& a, const Rows& row, const Columns<kWhole>& c,
+                                               bool there, uint8_t* to) {
+    if (there && c.any()) {
+      const uint32_t vectors = blockDim.x, v = threadIdx.x;
+      fetch16(to + 16 * v, vectors, row.dy, c, a.dy, a.dy_end);
+      if constexpr (kDh) fetch16(to + dh_at(vectors) + 16 * v, vectors, row.dh, c, a.dh, a.dh_end);
+      if constexpr (kMx8) copy_async8(to + h_at(vectors) + 8 * v, row.codes + c.first);
+      else fetch16(to + h_at(vectors) + 16 * v, vectors, row.h, c, a.h, a.h_end);
     }
     copy_async_commit();
   }
@@ -365,115 +359,113 @@ struct Ring {
   }
 };
 
-// One vector a thread: xh and g stay in registers over the sum; more: they are
-// read and made a second time.
-template <class T, bool kWhole, int kChunks, bool kMx8, bool kDh>
-__global__ void __launch_bounds__(kMaxThreads, kChunks == 1 ? 2 : 1)
+// xh and g stay in registers over the sum.  kLanes: a block of one warp, that many
+// lanes to a row (0: the block to a row).
+template <class T, bool kWhole, bool kMx8, bool kDh, int kLanes>
+__global__ void __launch_bounds__(kMaxThreads, 2)
     rms_norm_backward_kernel(const __grid_constant__ RmsNormBackwardArgs a, const int stages) {
-  using R = Ring<T, kWhole, kChunks, kMx8, kDh>;
-  using C = Columns<kWhole>;
+  using R = Ring<T, kWhole, kMx8, kDh>;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float smem[2][32];
   pdl_trigger();
-  const uint32_t step = gridDim.x, rows = (uint32_t)a.rows;
-  const uint32_t cols = (uint32_t)a.cols, group = blockDim.x, vectors = group * kChunks, size = R::bytes(vectors);
-  uint32_t ahead = blockIdx.x;  // the row to ask for
-  typename R::Rows from(a, ahead);
+  constexpr uint32_t kRows = rows_at_once(kLanes);
+  const uint32_t lane = kLanes ? threadIdx.x % (32 / kRows) : threadIdx.x;
+  const uint32_t first = blockIdx.x * kRows + (kLanes ? threadIdx.x / (32 / kRows) : 0);
+  const uint32_t step = gridDim.x * kRows, rows = (uint32_t)a.rows, vectors = blockDim.x, size = R::bytes(vectors);
+  const Columns<kWhole> c(0, lane, (uint32_t)a.cols);
+  uint32_t ahead = first;  // the row to ask for
+  typename R::Rows from(a, first);
   for (int s = 0; s < stages - 1; ++s, ahead += step) {
-    R::fetch(a, from, ahead < rows, ring + s * size);
-    from.next(a);
+    R::fetch(a, from, c, ahead < rows, ring + s * size);
+    from.next(a, step);
   }
-  float2 acc[kChunks][4];
+  float2 acc[4];
   float w[8];
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-    for (int p = 0; p < 4; ++p) acc[k][p] = make_float2(0.0f, 0.0f);
-  if constexpr (kChunks == 1) load_weights(a.weight, a.w_type, a.w_aligned, C(0, threadIdx.x, cols), w);
+  for (int p = 0; p < 4; ++p) acc[p] = make_float2(0.0f, 0.0f);
+  load_weights(a.weight, a.w_type, a.w_aligned, c, w);
   const float inv = __fdiv_rn(1.0f, (float)a.cols);
   // the row's statistics and scales, a row ahead
-  const float* stats = a.rstd + blockIdx.x;
-  const uint8_t* scales = a.h8.scales + blockIdx.x * a.h8.scale_pitch;
+  const float* stats = a.rstd + first;
+  const uint8_t* scales = a.h8.scales + first * a.h8.scale_pitch + (c.first >> 5);
   float next_rstd = 0.0f;
-  uint32_t scale[kChunks] = {}, next_scale[kChunks] = {};
-  auto look = [&]() {
+  uint32_t next_scale = 0u;
+  if (first < rows) {
     next_rstd = *stats;
-    if constexpr (kMx8) {
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        const C c(8 * group * k, threadIdx.x, cols);
-        if (c.any()) next_scale[k] = scales[c.first >> 5];
-      }
-    }
-  };
-  look();
-  typename T::raw* to = row_of<T>(a.dx, blockIdx.x, a.ld_dx);
+    if (kMx8 && c.any()) next_scale = *scales;
+  }
+  typename T::raw* to = row_of<T>(a.dx, first, a.ld_dx);
   uint32_t now = 0, later = (stages - 1) * size;  // the stages of this row and of the one to ask for
   int round = 0;
-  for (uint32_t row = blockIdx.x; row < rows; row += step, ahead += step, ++round) {
-    R::fetch(a, from, ahead < rows, ring + later);
-    from.next(a);
+  for (uint32_t base = blockIdx.x * kRows; base < rows; base += step, ahead += step, ++round) {
+    const uint32_t row = base + (first - blockIdx.x * kRows);
+    const bool there = kRows == 1 || row < rows, mine = there && c.any();
+    R::fetch(a, from, c, ahead < rows, ring + later);
+    from.next(a, step);
     later = now;
-    const uint8_t* stage = ring + now;
+    const uint8_t* stage = ring + now + 16 * threadIdx.x;
     now = now + size == stages * size ? 0 : now + size;
     const float rstd = next_rstd;
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) scale[k] = next_scale[k];
+    const uint32_t scale = next_scale;
     stats += step;
     scales += step * a.h8.scale_pitch;
-    if (row + step < rows) look();
+    if (row + step < rows) {
+      next_rstd = *stats;
+      if (kMx8 && c.any()) next_scale = *scales;
+    }
     if (stages == 4) copy_async_wait<3>();
     else if (stages == 3) copy_async_wait<2>();
     else copy_async_wait<1>();
     float2 dot = make_float2(0.0f, 0.0f);
     float g[8], xh[8];
-    auto vector = [&](int k, const C& c, bool sums) {
-      const uint32_t v = group * k + threadIdx.x;
+    typename T::V dh;
+    if (mine) {
       typename T::V x;
-      R::read(stage + 16 * v, vectors, R::offset(a.dy, row, a.ld_dy), c, x);
+      R::read(stage, vectors, R::offset(a.dy, row, a.ld_dy), c, x);
       x.values(g);
       if constexpr (kMx8) {
-        take_columns8(xh, Fetched8{*reinterpret_cast<const uint2*>(stage + R::h_at(vectors) + 8 * v), scale[k]}, c, rstd);
+        take_columns8(xh, Fetched8{*reinterpret_cast<const uint2*>(stage + R::h_at(vectors) - 8 * threadIdx.x), scale}, c, rstd);
       } else {
-        R::read(stage + R::h_at(vectors) + 16 * v, vectors, R::offset(a.h, row, a.ld_h), c, x);
+        R::read(stage + R::h_at(vectors), vectors, R::offset(a.h, row, a.ld_h), c, x);
         x.values(xh);
         scale8(xh, rstd);
       }
-      if constexpr (kChunks > 1) load_weights(a.weight, a.w_type, a.w_aligned, c, w);
-      if (sums) add_vector(g, xh, w, acc[k], dot);
-      else times8(g, w);
-    };
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * group * k, threadIdx.x, cols);
-      if (c.any()) vector(k, c, true);
+      add_vector(g, xh, w, acc, dot);
     }
-    const float mean = __fmul_rn(block_sum(__fadd_rn(dot.x, dot.y), smem, round), inv);
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      const C c(8 * group * k, threadIdx.x, cols);
-      if (kWhole && !c.any()) break;
-      typename T::V dh;
-      if (c.any()) {
-        if constexpr (kChunks > 1) vector(k, c, false);
-        dx_vector(g, xh, mean);
-        if constexpr (kDh)
-          R::read(stage + R::dh_at(vectors) + 16 * (group * k + threadIdx.x), vectors, R::offset(a.dh, row, a.ld_dh), c, dh);
-      }
-      store_dx<T>(to, c, rstd, kDh ? &dh : nullptr, g);  // (by whole warps)
+    const float mean = __fmul_rn(block_sum<kLanes>(__fadd_rn(dot.x, dot.y), smem, round), inv);
+    if (mine) {
+      dx_vector(g, xh, mean);
+      if constexpr (kDh) R::read(stage + R::dh_at(vectors), vectors, R::offset(a.dh, row, a.ld_dh), c, dh);
     }
+    // (an unaligned row's by whole warps; past the last row to one of no columns)
+    const Columns<kWhole> of(0, lane, there ? (uint32_t)a.cols : 0u);
+    if (!kWhole || mine) store_dx<T, kLanes ? kLanes : 32>(to, of, rstd, kDh ? &dh : nullptr, g);
     to += step * a.ld_dx;
   }
-  float* out = static_cast<float*>(a.workspace) + blockIdx.x * a.cols;
+  if constexpr (kLanes > 0) {  // the warp's rows together
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) store_part(out, C(8 * group * k, threadIdx.x, cols), acc[k]);
+    for (int o = kLanes; o < 32; o <<= 1)
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        acc[p].x = __fadd_rn(acc[p].x, __shfl_xor_sync(0xFFFFFFFFu, acc[p].x, o));
+        acc[p].y = __fadd_rn(acc[p].y, __shfl_xor_sync(0xFFFFFFFFu, acc[p].y, o));
+      }
+    if (threadIdx.x >= kLanes) return;
+  }
+  store_part(static_cast<float*>(a.workspace) + blockIdx.x * a.cols, c, acc);
 }
 
 // Longer rows: the rows' dot products first (into the workspace's head), then
-// pieces of 2048 columns.
-constexpr int kWideThreads = 256;
-constexpr int kWideParts = 64;
-int64_t wide_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, kWideParts)); }
+// pieces of 1024 columns, as many blocks as fill the SMs.  The second reading of
+// dy and h comes from L2 up to some 100 MB: 2048 x 8192 bf16 takes 40 us, 4088 x
+// 4104 48.  (Two or four vectors a thread in the ring, whose blocks then are one
+// to an SM: 46 and 59.)
+constexpr int kDotThreads = 256;
+constexpr int kWideThreads = 128;
+int64_t wide_parts(int64_t rows, int64_t cols) {
+  const int64_t slabs = (cols + 8 * kWideThreads - 1) / (8 * kWideThreads);
+  return std::max<int64_t>(1, std::min(rows, 16 * kSms / slabs));
+}
 int64_t dots_floats(int64_t rows) { return (rows + 3) / 4 * 4; }
 
 // dy and xh of a vector.
@@ -500,7 +492,7 @@ __device__ __forceinline__ void load_dy_xh(const RmsNormBackwardArgs& a, int64_t
 }
 
 template <class T, bool kWhole, bool kMx8>
-__global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
+__global__ void __launch_bounds__(kDotThreads) rms_norm_dots_kernel(const __grid_constant__ RmsNormBackwardArgs a) {
   using C = Columns<kWhole>;
   __shared__ float smem[2][32];
   pdl_trigger();
@@ -508,7 +500,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __gri
   const uint32_t cols = (uint32_t)a.cols;
   const float rstd = a.rstd[row];
   float2 dot = make_float2(0.0f, 0.0f);
-  for (uint32_t first = 0; first < cols; first += 8 * kWideThreads) {
+  for (uint32_t first = 0; first < cols; first += 8 * kDotThreads) {
     const C c(first, threadIdx.x, cols);
     float xh[8], w[8], d[8];
     float2 unused[4] = {};
@@ -516,7 +508,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_dots_kernel(const __gri
     load_weights(a.weight, a.w_type, a.w_aligned, c, w);
     add_vector(d, xh, w, unused, dot);
   }
-  const float all = block_sum(__fadd_rn(dot.x, dot.y), smem, 0);
+  const float all = block_sum<0>(__fadd_rn(dot.x, dot.y), smem, 0);
   if (threadIdx.x == 0) static_cast<float*>(a.workspace)[row] = all;
 }
 
@@ -537,7 +529,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(co
     if (a.dh) load_columns(dh, row_of<T>(a.dh, row, a.ld_dh), c, span_of<T>(a.dh, a.rows, a.cols, a.ld_dh));
     add_vector(g, xh, w, acc, unused);
     dx_vector(g, xh, __fmul_rn(static_cast<const float*>(a.workspace)[row], inv));
-    store_dx<T>(row_of<T>(a.dx, row, a.ld_dx), c, rstd, a.dh ? &dh : nullptr, g);
+    store_dx<T, 32>(row_of<T>(a.dx, row, a.ld_dx), c, rstd, a.dh ? &dh : nullptr, g);
   }
   store_part(static_cast<float*>(a.workspace) + dots + blockIdx.y * a.cols, c, acc);
 }
@@ -568,19 +560,24 @@ __global__ void __launch_bounds__(32 * kDwWarps) rms_norm_dw_kernel(const float*
 
 // ------------------------------------------------------------------ launch --
 
-// A warp to a row up to 512 columns; above, a block of as many threads as the
-// row has vectors, or half or a quarter of them.
+// As many lanes to a row as it has vectors, in powers of two, up to a warp's with
+// two vectors each; above, a block of as many threads as the row has vectors, or
+// half or a quarter of them.
 template <class T, bool kWhole>
 cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
   const double inv = 1.0 / (double)a.cols;
-  const unsigned rows = (unsigned)a.rows, warps = (rows + kWarpRows - 1) / kWarpRows;
-  const uint32_t vectors = (uint32_t)((a.cols + 7) / 8);
-  auto threads = [&](uint32_t chunks) { return ((vectors + chunks - 1) / chunks + 31) / 32 * 32; };
-  if (vectors <= 32) rms_norm_kernel<T, kWhole, true, 1><<<warps, 32 * kWarpRows, 0, s>>>(a, inv);
-  else if (vectors <= 64) rms_norm_kernel<T, kWhole, true, 2><<<warps, 32 * kWarpRows, 0, s>>>(a, inv);
-  else if (vectors <= 256) rms_norm_kernel<T, kWhole, false, 1><<<rows, threads(1), 0, s>>>(a, inv);
-  else if (vectors <= 1024) rms_norm_kernel<T, kWhole, false, 2><<<rows, threads(2), 0, s>>>(a, inv);
-  else if (vectors <= 2048) rms_norm_kernel<T, kWhole, false, 4><<<rows, threads(4), 0, s>>>(a, inv);
+  const int64_t vectors = (a.cols + 7) / 8;
+  auto blocks = [&](int lanes) { return (unsigned)((a.rows * lanes + kLanesThreads - 1) / kLanesThreads); };
+  auto threads = [&](int64_t chunks) { return (unsigned)(((vectors + chunks - 1) / chunks + 31) / 32 * 32); };
+  const unsigned rows = (unsigned)a.rows;
+  // (131072 x 128 bf16 with all results: 46 us with a warp to a row, 28 with 16 lanes)
+  if (vectors <= 8) rms_norm_kernel<T, kWhole, 8, 1><<<blocks(8), kLanesThreads, 0, s>>>(a, inv);
+  else if (vectors <= 16) rms_norm_kernel<T, kWhole, 16, 1><<<blocks(16), kLanesThreads, 0, s>>>(a, inv);
+  else if (vectors <= 32) rms_norm_kernel<T, kWhole, 32, 1><<<blocks(32), kLanesThreads, 0, s>>>(a, inv);
+  else if (vectors <= 64) rms_norm_kernel<T, kWhole, 32, 2><<<blocks(32), kLanesThreads, 0, s>>>(a, inv);
+  else if (vectors <= 256) rms_norm_kernel<T, kWhole, 0, 1><<<rows, threads(1), 0, s>>>(a, inv);
+  else if (vectors <= 1024) rms_norm_kernel<T, kWhole, 0, 2><<<rows, threads(2), 0, s>>>(a, inv);
+  else if (vectors <= 2048) rms_norm_kernel<T, kWhole, 0, 4><<<rows, threads(4), 0, s>>>(a, inv);
   else rms_norm_long_kernel<T, kWhole><<<rows, kLongThreads, 0, s>>>(a, inv);
   return cudaGetLastError();
 }
@@ -599,31 +596,35 @@ cudaError_t add_dw(const RmsNormBackwardArgs& a, int64_t first, int64_t parts, c
                        static_cast<const float*>(a.workspace) + first, parts, a.cols, a.dw, a.dw_type);
 }
 
-template <class T, bool kMx8, bool kWhole, int kChunks, bool kDh>
-cudaError_t backward(const RmsNormBackwardArgs& a, const Shape& p, cudaStream_t s) {
+template <class T, bool kMx8, bool kWhole, bool kDh, int kLanes>
+cudaError_t backward_ring(const RmsNormBackwardArgs& a, cudaStream_t s) {
   // as deep as lets the blocks of parts_of fit an SM together
-  constexpr int kRoom = 220 * 1024;
-  const int stage = (int)Ring<T, kWhole, kChunks, kMx8, kDh>::bytes(p.threads * kChunks);
-  const int stages = std::max(2, std::min(4, kRoom / (int)blocks_to_sm(p) / stage));
-  if (stages * stage > kRoom) return cudaErrorInvalidValue;
-  auto kernel = rms_norm_backward_kernel<T, kWhole, kChunks, kMx8, kDh>;
+  constexpr int kRoom = 220 * 1024, kRows = rows_at_once(kLanes);
+  const uint32_t threads = threads_of(a.cols);
+  const int stage = (int)Ring<T, kWhole, kMx8, kDh>::bytes(threads);
+  const int stages = std::max(2, std::min(4, kRoom / (int)blocks_to_sm(a.cols) / stage));
+  static_assert(2 * kMaxThreads * (3 * 48) <= kRoom, "two stages fit, of an unaligned binary32 row too");
+  auto kernel = rms_norm_backward_kernel<T, kWhole, kMx8, kDh, kLanes>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
   if (e != cudaSuccess) return e;
-  const int64_t parts = parts_of(a.rows, a.cols);
-  kernel<<<(unsigned)parts, p.threads, stages * stage, s>>>(a, stages);
+  const int64_t parts = parts_of((a.rows + kRows - 1) / kRows, a.cols);
+  kernel<<<(unsigned)parts, threads, stages * stage, s>>>(a, stages);
   const cudaError_t r = cudaGetLastError();
   return r == cudaSuccess ? add_dw(a, 0, parts, s) : r;
 }
 
-template <class T, bool kMx8, bool kWhole, int kChunks>
-cudaError_t backward(const RmsNormBackwardArgs& a, const Shape& p, cudaStream_t s) {
-  return a.dh ? backward<T, kMx8, kWhole, kChunks, true>(a, p, s) : backward<T, kMx8, kWhole, kChunks, false>(a, p, s);
+template <class T, bool kMx8, bool kWhole, bool kDh>
+cudaError_t backward_ring(const RmsNormBackwardArgs& a, cudaStream_t s) {
+  // (131072 x 128 bf16 from the checkpoint: 50 us with a warp to a row, 34 with 16 lanes)
+  if (a.cols <= 64) return backward_ring<T, kMx8, kWhole, kDh, 8>(a, s);
+  if (a.cols <= 128) return backward_ring<T, kMx8, kWhole, kDh, 16>(a, s);
+  return backward_ring<T, kMx8, kWhole, kDh, 0>(a, s);
 }
 
 template <class T, bool kMx8, bool kWhole>
 cudaError_t backward_wide(const RmsNormBackwardArgs& a, cudaStream_t s) {
-  const int64_t dots = dots_floats(a.rows), parts = wide_parts(a.rows);
-  rms_norm_dots_kernel<T, kWhole, kMx8><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
+  const int64_t dots = dots_floats(a.rows), parts = wide_parts(a.rows, a.cols);
+  rms_norm_dots_kernel<T, kWhole, kMx8><<<(unsigned)a.rows, kDotThreads, 0, s>>>(a);
   const dim3 grid((unsigned)((a.cols + 8 * kWideThreads - 1) / (8 * kWideThreads)), (unsigned)parts);
   rms_norm_backward_wide_kernel<T, kWhole, kMx8><<<grid, kWideThreads, 0, s>>>(a, dots);
   const cudaError_t e = cudaGetLastError();
@@ -632,12 +633,8 @@ cudaError_t backward_wide(const RmsNormBackwardArgs& a, cudaStream_t s) {
 
 template <class T, bool kMx8, bool kWhole>
 cudaError_t backward(const RmsNormBackwardArgs& a, cudaStream_t s) {
-  const Shape p = shape_of(a.cols);
-  if (a.cols > wide_from(a.type, kWhole)) return backward_wide<T, kMx8, kWhole>(a, s);
-  if (p.chunks == 1) return backward<T, kMx8, kWhole, 1>(a, p, s);
-  if (p.chunks == 2) return backward<T, kMx8, kWhole, 2>(a, p, s);
-  if constexpr (kWhole && sizeof(typename T::raw) == 2) return backward<T, kMx8, kWhole, 4>(a, p, s);
-  return cudaErrorInvalidValue;
+  if (a.cols > kRingCols) return backward_wide<T, kMx8, kWhole>(a, s);
+  return a.dh ? backward_ring<T, kMx8, kWhole, true>(a, s) : backward_ring<T, kMx8, kWhole, false>(a, s);
 }
 
 template <class T, bool kMx8>
@@ -657,9 +654,7 @@ cudaError_t backward(const RmsNormBackwardArgs& a, cudaStream_t s) {
 }  // namespace
 
 int64_t rms_norm_backward_workspace(int64_t rows, int64_t cols) {
-  // whatever the type and alignment, on which it depends whether rows go through memory twice
-  const int64_t once = parts_of(rows, cols) * cols, twice = dots_floats(rows) + wide_parts(rows) * cols;
-  return 4 * (cols <= wide_from(kMxF32, false) ? once : cols <= wide_from(kMxBf16, true) ? std::max(once, twice) : twice);
+  return 4 * (cols <= kRingCols ? parts_of(rows, cols) * cols : dots_floats(rows) + wide_parts(rows, cols) * cols);
 }
 
 cudaError_t launch_rms_norm(const RmsNormArgs& a, int, cudaStream_t s) {

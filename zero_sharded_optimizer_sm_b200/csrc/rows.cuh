@@ -192,7 +192,7 @@ __device__ __forceinline__ void load_columns(V& x, const typename V::raw* row, c
 // from two neighbouring lanes' vectors; what a warp's first and last lanes lack a
 // neighbour for -- eight elements of 16 bits, four of 32 -- goes to as many lanes
 // and out in one store; the row's last word goes element by element.  Called by
-// whole warps whose lanes have neighbouring vectors.
+// whole warps, every kLanes of which have neighbouring vectors of a row.
 __device__ __forceinline__ void store_whole(uint16_t* p, const uint32_t* w) {
   st_stream(p, make_uint4(w[0], w[1], w[2], w[3]));
 }
@@ -217,14 +217,17 @@ __device__ __forceinline__ void store_some(raw* p, const uint32_t* w, int from, 
   }
 }
 
-template <class V, bool kWhole>
+template <int kLanes = 32, class V, bool kWhole>
 __device__ __forceinline__ void store_columns(typename V::raw* row, const Columns<kWhole>& c, const V& x) {
   using raw = typename V::raw;
   constexpr int kN = WordsOf<V>::kN, kPer = WordsOf<V>::kPer;
   if constexpr (kWhole) {
     if (c.any()) store_whole(row + c.first, words(x));
   } else {
-    const uint32_t off = offset_of(row), lane = threadIdx.x & 31;
+    static_assert(kLanes >= 8, "a word's elements have a lane each");
+    const uint32_t off = offset_of(row), lane = threadIdx.x & (kLanes - 1);
+    // (rows of one warp may begin at different offsets in their words)
+    const uint32_t mask = kLanes == 32 ? 0xFFFFFFFFu : ((1u << (kLanes & 31)) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
     const int there = (int)(c.cols - c.first);  // elements of the row from mine on (below 0: it ended before)
     if (off == 0) {
       if (there >= 8) store_whole(row + c.first, words(x));
@@ -235,7 +238,7 @@ __device__ __forceinline__ void store_columns(typename V::raw* row, const Column
     // another what is from 8 - off on
     uint32_t w[kN + 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xFFFFFFFFu, words(x)[kN - 4 + i], 1);
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(mask, words(x)[kN - 4 + i], 1, kLanes);
 #pragma unroll
     for (int i = 0; i < kN; ++i) w[4 + i] = words(x)[i];
     shift_down<kN + 4, kPer>(w, 4 * kPer - off);
@@ -247,17 +250,17 @@ __device__ __forceinline__ void store_columns(typename V::raw* row, const Column
     } else if (end > 0) {
       store_some(p, w, lane > 0 ? 0 : (int)off, end);
     }
-    // lane j: of the elements that begin lane 0's vector and end lane 31's, in a word each, the jth
+    // lane j: of the elements that begin the first lane's vector and end the last one's, in a word each, the jth
     constexpr uint32_t kIn = 16 / sizeof(raw);  // elements of a word
     const bool last = lane >= kIn - off;
     uint32_t e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t mine = lane == 31 ? words(x)[kN - 4 + i] : words(x)[i];
-      e[i] = __shfl_sync(0xFFFFFFFFu, mine, last ? 31 : 0);
+      const uint32_t mine = lane == kLanes - 1 ? words(x)[kN - 4 + i] : words(x)[i];
+      e[i] = __shfl_sync(mask, mine, last ? kLanes - 1 : 0, kLanes);
     }
-    const int first_there = __shfl_sync(0xFFFFFFFFu, there, 0);
-    const uint32_t at = last ? 32 * 8 - kIn + lane : lane;  // from the warp's first column on
+    const int first_there = __shfl_sync(mask, there, 0, kLanes);
+    const uint32_t at = last ? kLanes * 8 - kIn + lane : lane;  // from the first lane's first column on
     // (of a lane 0 whose word the row's end is in, the elements have gone out above)
     if (lane < kIn && (int)at < first_there && (last || first_there + (int)off >= 8)) {
       const uint32_t i = lane / kPer;
