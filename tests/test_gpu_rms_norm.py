@@ -232,6 +232,20 @@ def test_norm_backward_twice_is_the_same(z):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("cols", [64, 300, 512, 1024, 2048, 3000, 4096, 8192, 20000])
+def test_a_rows_results_are_the_same_in_every_batch(z, cols):
+    """However many rows there are, and with them other blocks and lanes."""
+    rows = (1 << 22) // cols + 3
+    x, w = normal(rows, cols, "bf16", 11), _weight(cols, "bf16")
+    all_rows = z.rms_norm(x, w, y8=True)
+    for first, last in ((0, 1), (5, 22), (rows - 40, rows)):
+        some = z.rms_norm(x[first:last], w, y8=True)
+        assert torch.equal(some.rstd, all_rows.rstd[first:last]) and torch.equal(some.y, all_rows.y[first:last])
+        assert torch.equal(some.y8.codes[:, :cols], all_rows.y8.codes[first:last, :cols])
+        blocks = -(-cols // 32)  # (what is behind them is nobody's)
+        assert torch.equal(some.y8.scales[:, :blocks], all_rows.y8.scales[first:last, :blocks])
+
+
 @pytest.mark.parametrize("cols", [48, 800, 20000])
 def test_norm_backward_against_differences(z, cols):
     """Central differences of the 64-bit norm: their own error is of the order

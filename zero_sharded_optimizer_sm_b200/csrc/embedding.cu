@@ -214,9 +214,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
 // Batches of up to kClusterMax positions are sorted by one cluster of CTAs in
 // one launch: every CTA keeps its part of the (token, position) pairs in shared
 // memory, and a pass writes them to their places in the cluster's CTAs.  16384
-// positions of 16-bit tokens take some 8 us (as three launches a pass of 8 bits
-// 30), latency throughout: three barriers and two trips through the cluster's
-// memory a pass.
+// positions of 16-bit tokens take some 8 us, latency throughout: three barriers
+// and two trips through the cluster's memory a pass.  (A whole call, 64 columns,
+// this way and with three launches a pass: 16385 positions 29 and 38 us, 32768 33
+// and 40, of 300000 rows 40 and 55, 65536 56 and 57.)
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterCtas = 8;

@@ -16,20 +16,31 @@ using namespace mx;
 
 // ----------------------------------------------------------------- forward --
 
-// Sum over a warp, and from the warps' binary32 sums on in binary64 over the
-// block; or over the kLanes (of a warp, not 0) that share a row: every thread of
-// a row gets the same bits.
-template <int kLanes>
-__device__ __forceinline__ double group_sum(float mine, float* smem) {
+// The row's sum: of every 32 neighbouring vectors in binary32 in one order, of
+// those in binary64 in theirs, so that its bits are the same whether a thread has
+// one vector or two, and with them a row's results in every batch.  kLanes of a
+// warp share the row (0: the block does); every thread of it gets the sum.  A
+// warp adds up two sums in its halves, after one exchange: as many shuffles as
+// for one.
+template <int kLanes, int kSums>
+__device__ __forceinline__ double group_sum(const float (&of)[kSums], float* smem) {
+  static_assert(kSums == 1 || (kSums == 2 && (kLanes == 0 || kLanes == 32)), "halves of warps");
+  const bool upper = kSums == 2 && (threadIdx.x & 16);
+  float mine = upper ? of[kSums - 1] : of[0];
+  if constexpr (kSums == 2) mine = __fadd_rn(mine, __shfl_xor_sync(0xFFFFFFFFu, upper ? of[0] : of[1], 16));
 #pragma unroll
-  for (int o = kLanes ? kLanes / 2 : 16; o > 0; o >>= 1) mine = __fadd_rn(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
-  if constexpr (kLanes > 0) return (double)mine;
-  const uint32_t warps = blockDim.x / 32;
-  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = mine;
+  for (int o = (kLanes ? kLanes / 2 : 16) / kSums; o > 0; o >>= 1) mine = __fadd_rn(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
+  if constexpr (kLanes > 0) {
+    if constexpr (kSums == 1) return (double)mine;
+    return __dadd_rn((double)mine, (double)__shfl_xor_sync(0xFFFFFFFFu, mine, 16));
+  }
+  const uint32_t warps = blockDim.x / 32, n = warps * kSums;  // up to 32
+  if ((threadIdx.x & (32 / kSums - 1)) == 0) smem[(upper ? warps : 0) + (threadIdx.x >> 5)] = mine;
   __syncthreads();
-  double v = 0.0;
-#pragma unroll 4
-  for (uint32_t w = 0; w < warps; ++w) v = __dadd_rn(v, (double)smem[w]);
+  // (a tree: every thread adding up all of them took 3 us more of 31 at 2048 x 8192)
+  const uint32_t powers = n > 1 ? 1u << (32 - __clz(n - 1)) : 1u, w = threadIdx.x & (powers - 1);
+  double v = w < n ? (double)smem[w] : 0.0;
+  for (uint32_t o = powers / 2; o > 0; o >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
 
@@ -128,7 +139,8 @@ template <class T, bool kWhole, int kLanes, int kChunks>
 __global__ void __launch_bounds__(kLanes ? kLanesThreads : 512) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
                                                                                 const double inv_cols) {
   static_assert(kLanes % 4 == 0, "whole blocks of MX8");
-  __shared__ float smem[32];
+  constexpr int kSums = kChunks == 4 ? 1 : kChunks;  // (of four a thread, each thread's at once: rows that always go so)
+  __shared__ float smem[512 / 32 * kSums];
   const uint32_t group = kLanes ? kLanes : blockDim.x, t = kLanes ? threadIdx.x & (kLanes - 1) : threadIdx.x;
   const uint32_t number = kLanes ? (blockIdx.x * kLanesThreads + threadIdx.x) / group : blockIdx.x;
   const bool there = kLanes == 0 || number < (uint32_t)a.rows;  // past the end: a row of no columns, for the shuffles' sake
@@ -146,14 +158,16 @@ __global__ void __launch_bounds__(kLanes ? kLanesThreads : 512) rms_norm_kernel(
       load_h<T>(a, row, c, reinterpret_cast<typename T::V(&)[2]>(x[k]));
     }
   }
-  float2 ss = make_float2(0.0f, 0.0f);
+  float ss[kSums];
+  float2 of = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     float v[8];
     x[k].values(v);
-    ss = square_sum(v, ss);
+    of = square_sum(v, kSums == 1 ? of : make_float2(0.0f, 0.0f));
+    ss[kSums == 1 ? 0 : k] = __fadd_rn(of.x, of.y);
   }
-  const float rstd = rstd_of(group_sum<kLanes>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  const float rstd = rstd_of(group_sum<kLanes>(ss, smem), inv_cols, (double)a.eps);
   if (a.rstd && t == 0 && there) a.rstd[number] = rstd;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) finish<T, kLanes ? kLanes : 32>(a, row, C(8 * group * k, t, cols), rstd, x[k]);
@@ -165,7 +179,7 @@ constexpr int kLongThreads = 512;
 template <class T, bool kWhole>
 __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __grid_constant__ RmsNormArgs a,
                                                                      const double inv_cols) {
-  __shared__ float smem[32];
+  __shared__ float smem[kLongThreads / 32];
   const NormRow<T> row(a, blockIdx.x);
   const uint32_t cols = (uint32_t)a.cols;
   using C = Columns<kWhole>;
@@ -178,7 +192,8 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __gri
     x[0].values(v);
     ss = square_sum(v, ss);
   }
-  const float rstd = rstd_of(group_sum<0>(__fadd_rn(ss.x, ss.y), smem), inv_cols, (double)a.eps);
+  float sum[1] = {__fadd_rn(ss.x, ss.y)};
+  const float rstd = rstd_of(group_sum<0>(sum, smem), inv_cols, (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
   for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
     typename T::V x[1];
@@ -562,7 +577,18 @@ __global__ void __launch_bounds__(32 * kDwWarps) rms_norm_dw_kernel(const float*
 
 // As many lanes to a row as it has vectors, in powers of two, up to a warp's with
 // two vectors each; above, a block of as many threads as the row has vectors, or
-// half or a quarter of them.
+// half or a quarter of them.  Measured, bf16 with a residual and all results, us:
+//   131072 x 128       a warp to a row 46, 16 lanes 28
+//   32768 x 512        a block of one vector a thread 27.6, a warp of two 26.4
+//   32263 x 520        one vector a thread 37.4, two 42.2 (whose threads have
+//   21845 x 768        28.5 and 30.8               twice the row's vectors in part)
+//   16384 x 1024       28.0 and 26.7, 8192 x 2048 29.3 and 26.5
+//   4096 x 4096        32.7 and 27.8, four 30.0
+//   2048 x 8192        two 32.3, four 32.9
+// and while the SMs hold all rows' threads at once, latency counts:
+//   64 x 512           a block of one 2.4, a warp of two 2.8; 4096 x 512 4.6, 4.4
+//   64 x 2048          one 2.6, two 3.1; 2048 x 2048 8.0, 7.6
+//   64 x 4096          one 3.0, two 3.4; 592 x 4096 5.6, 5.2
 template <class T, bool kWhole>
 cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
   const double inv = 1.0 / (double)a.cols;
@@ -570,12 +596,12 @@ cudaError_t forward(const RmsNormArgs& a, cudaStream_t s) {
   auto blocks = [&](int lanes) { return (unsigned)((a.rows * lanes + kLanesThreads - 1) / kLanesThreads); };
   auto threads = [&](int64_t chunks) { return (unsigned)(((vectors + chunks - 1) / chunks + 31) / 32 * 32); };
   const unsigned rows = (unsigned)a.rows;
-  // (131072 x 128 bf16 with all results: 46 us with a warp to a row, 28 with 16 lanes)
+  const bool few = a.rows * vectors <= 148 * 1024;
   if (vectors <= 8) rms_norm_kernel<T, kWhole, 8, 1><<<blocks(8), kLanesThreads, 0, s>>>(a, inv);
   else if (vectors <= 16) rms_norm_kernel<T, kWhole, 16, 1><<<blocks(16), kLanesThreads, 0, s>>>(a, inv);
   else if (vectors <= 32) rms_norm_kernel<T, kWhole, 32, 1><<<blocks(32), kLanesThreads, 0, s>>>(a, inv);
-  else if (vectors <= 64) rms_norm_kernel<T, kWhole, 32, 2><<<blocks(32), kLanesThreads, 0, s>>>(a, inv);
-  else if (vectors <= 256) rms_norm_kernel<T, kWhole, 0, 1><<<rows, threads(1), 0, s>>>(a, inv);
+  else if (vectors <= 64 && !few) rms_norm_kernel<T, kWhole, 32, 2><<<blocks(32), kLanesThreads, 0, s>>>(a, inv);
+  else if (few ? vectors <= 512 : vectors <= 256 && threads(1) != 2 * threads(2)) rms_norm_kernel<T, kWhole, 0, 1><<<rows, threads(1), 0, s>>>(a, inv);
   else if (vectors <= 1024) rms_norm_kernel<T, kWhole, 0, 2><<<rows, threads(2), 0, s>>>(a, inv);
   else if (vectors <= 2048) rms_norm_kernel<T, kWhole, 0, 4><<<rows, threads(4), 0, s>>>(a, inv);
   else rms_norm_long_kernel<T, kWhole><<<rows, kLongThreads, 0, s>>>(a, inv);
