@@ -246,6 +246,26 @@ def test_a_rows_results_are_the_same_in_every_batch(z, cols):
         assert torch.equal(some.y8.scales[:, :blocks], all_rows.y8.scales[first:last, :blocks])
 
 
+@pytest.mark.parametrize("cols,rows", [(1, (1 << 29) + 1003), (72, (1 << 26) + 1003)])
+def test_more_rows_than_32_bits_count_lanes_of(z, cols, rows):
+    """Rows share blocks: their lanes' number passes 2^32, their elements' too."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("wants 40 GB")
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    w = _weight(cols, "bf16")
+    ends = (slice(0, 777), slice(rows - 777, rows))
+    for k, e in enumerate(ends):
+        x[e] = normal(777, cols, "bf16", 5 + k)
+    small = [(x[e].clone(), z.rms_norm(x[e], w)) for e in ends]
+    y = torch.empty_like(x)
+    n = z.rms_norm(x, w, y=y)
+    for e, (_, want) in zip(ends, small):
+        assert torch.equal(n.y[e], want.y) and torch.equal(n.rstd[e], want.rstd)
+    dx, _ = z.rms_norm_backward(y, x, w, n.rstd, dx=y)  # y as dy, its gradient in its place
+    for e, (h, want) in zip(ends, small):
+        assert torch.equal(dx[e], z.rms_norm_backward(want.y, h, w, want.rstd)[0])
+
+
 @pytest.mark.parametrize("cols", [48, 800, 20000])
 def test_norm_backward_against_differences(z, cols):
     """Central differences of the 64-bit norm: their own error is of the order

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kLanes ? kLanesThreads : 512) rms_norm_kernel(
   constexpr int kSums = kChunks == 4 ? 1 : kChunks;  // (of four a thread, each thread's at once: rows that always go so)
   __shared__ float smem[512 / 32 * kSums];
   const uint32_t group = kLanes ? kLanes : blockDim.x, t = kLanes ? threadIdx.x & (kLanes - 1) : threadIdx.x;
-  const uint32_t number = kLanes ? (blockIdx.x * kLanesThreads + threadIdx.x) / group : blockIdx.x;
+  const uint32_t number = kLanes ? blockIdx.x * (kLanesThreads / group) + threadIdx.x / group : blockIdx.x;
   const bool there = kLanes == 0 || number < (uint32_t)a.rows;  // past the end: a row of no columns, for the shuffles' sake
   const NormRow<T> row(a, there ? number : 0);
   const uint32_t cols = there ? (uint32_t)a.cols : 0u;
