@@ -144,6 +144,25 @@ def test_backward_gives_the_same_bits_every_time(z):
         assert torch.equal(z.embedding_backward(dy, t, 500, 0.37), first)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n", [1, 16, 17, 31, 32, 33, 500, 511, 512, 513, 800])
+@pytest.mark.parametrize("vocab,cols", [(1, 8), (1, 2100), (3, 260), (40, 771), (5000, 40), (9, 50000)])
+def test_backward_of_few_tokens(z, vocab, cols, n, accumulate):
+    """Tokens of one, some and many positions among up to 512, and a few more.
+    Whole numbers, as above."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    dy = torch.randint(-8, 9, (n, cols), generator=g, device="cuda").float()
+    for kind in ("outside", "few", "one"):
+        t = tokens_of(n, vocab, 6, kind)
+        if kind == "outside" and n > 40:
+            t[3:n // 2:2] = vocab - 1  # one token over and over between others
+        held = torch.full((vocab, cols), 3.0, device="cuda")
+        inside = (t >= 0) & (t < vocab)
+        want = torch.zeros(vocab, cols, dtype=torch.float64, device="cuda").index_add_(0, t[inside], dy[inside].double())
+        got = z.embedding_backward(dy, t, vocab, 1.0, out=held, accumulate=accumulate)
+        assert torch.equal(got.double(), want + 3 if accumulate else want), kind
+
+
 @pytest.mark.parametrize("out", list(DTYPES))
 @pytest.mark.parametrize("dtype", list(DTYPES))
 def test_backward_into_a_gradient_buffer(z, dtype, out):

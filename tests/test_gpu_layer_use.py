@@ -252,11 +252,12 @@ def test_the_workspace_is_all_that_is_written(z):
         assert torch.equal(dx[1:-1], want_dx) and torch.equal(dw[8:-8], want_dw)
         assert (dx[0] == 3).all() and (dx[-1] == 3).all() and (dw[:8] == 3).all() and (dw[-8:] == 3).all()
         assert (space[:256] == 0xA5).all() and (space[256 + need.value:] == 0xA5).all()
-        want = z.embedding_backward(dy, o["tokens"], V, 2.0)
-        assert z.zero_embedding_backward_workspace(T, V, cols, need) == 0
+        dy, tokens = dy.repeat(3, 1), o["tokens"].repeat(3)  # (few tokens need none)
+        want = z.embedding_backward(dy, tokens, V, 2.0)
+        assert z.zero_embedding_backward_workspace(3 * T, V, cols, need) == 0 and need.value > 0
         space = torch.full((need.value + 512,), 0xA5, dtype=torch.uint8, device="cuda")
         out = torch.full((V + 2, cols), 3.0, dtype=torch.bfloat16, device="cuda")
-        args = lambda at, n: (dy.data_ptr(), 0, T, cols, cols, o["tokens"].data_ptr(), 8, V, 2.0, out[1:].data_ptr(), 0, cols, 0,  # noqa: E731
+        args = lambda at, n: (dy.data_ptr(), 0, 3 * T, cols, cols, tokens.data_ptr(), 8, V, 2.0, out[1:].data_ptr(), 0, cols, 0,  # noqa: E731
                               at, n, stream)
         assert z.zero_embedding_backward(*args(space.data_ptr() + 256, need.value - 1)) == z.ZERO_EINVAL
         assert z.zero_embedding_backward(*args(space.data_ptr() + 256, need.value)) == 0

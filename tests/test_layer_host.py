@@ -146,7 +146,8 @@ def test_embedding_arguments(kw, words):
 @pytest.mark.parametrize("kw,words", TOKENS + [
     (dict(dy=None), ["dy"]), (dict(dtype=3), ["dtype"]), (dict(ld_dy=8), ["dy: 8"]), (dict(dtable=None), ["dtable"]),
     (dict(dtable_dtype=3), ["dtype"]), (dict(ld=8), ["dtable: 8"]), (dict(accumulate=2), ["accumulate"]),
-    (dict(workspace=None), ["workspace"]), (dict(workspace=A + 8), ["workspace"]), (dict(bytes=8), ["workspace"]),
+    (dict(workspace=None, n=1000), ["workspace"]), (dict(workspace=A + 8, n=1000), ["workspace"]),
+    (dict(bytes=8, n=1000), ["workspace"]),
 ])
 def test_embedding_backward_arguments(kw, words):
     _refused(z.zero_embedding_backward(*embed_back_args(**kw)), *words)
@@ -168,7 +169,8 @@ def test_workspaces():
     assert z.zero_rms_norm_backward_workspace(0, 64, n) == 0 and n.value == 0
     assert z.zero_rms_norm_backward_workspace(3, 64, n) == 0 and n.value > 0
     assert z.zero_embedding_backward_workspace(0, 10, 64, n) == 0 and n.value == 0
-    assert z.zero_embedding_backward_workspace(5, 10, 64, n) == 0 and n.value > 0
+    assert z.zero_embedding_backward_workspace(5, 10, 64, n) == 0 and n.value == 0  # (few tokens are not sorted)
+    assert z.zero_embedding_backward_workspace(1000, 10, 64, n) == 0 and n.value > 0
     _refused(z.zero_rms_norm_backward_workspace(-1, 64, n), "out of range")
     _refused(z.zero_rms_norm_backward_workspace(3, 64, None), "NULL")
     _refused(z.zero_embedding_backward_workspace(5, 1 << 31, 64, n), "out of range")

@@ -678,6 +678,144 @@ __global__ void __launch_bounds__(kJoinThreads) embedding_join_kernel(const __gr
   }
 }
 
+// ------------------------------------------------------------ a few tokens --
+
+// Up to kFew tokens need no sort: a warp takes a position and a slab, looks
+// through all tokens for an earlier one of its kind (whose warp it leaves the sum
+// to) and for the later ones, and adds their rows in the batch's order; a token of
+// more than kAlone positions is left to all warps of the CTA, a share each.  As
+// long as the warps have two units each at most; us for a whole call, here and
+// sorted, spread tokens and one token over and over:
+//   301 tokens, 5003 x 768 binary16      4.6 and 10.4, 8.9 and 11.0
+//   512 tokens of the same               5.3 and 11.9, 11.4 and 11.5
+//   512 tokens, 50304 x 1024 bf16        18.5 and 21.4, 20.0 and 24.3
+//   128 tokens, 2000 x 8192 bf16         9.8 and 13.4, 10.2 and 16.1
+//   301 tokens of the same (five units)  20.1 and 14.6, 17.8 and 16.4
+// What bounds it is latency: the launch, the tokens, two searches, the rows.
+constexpr uint32_t kFew = 512;
+constexpr uint32_t kAlone = 16;
+bool few_tokens(int64_t n, int64_t cols) { return n <= kFew && n * ((cols + 255) / 256) <= 2 * 148 * (kSumThreads / 64); }
+
+struct FewShared {
+  uint32_t keys[kFew];
+  uint32_t bits[kBitRows / 32];
+  uint16_t lists[kSumThreads / 32][32];  // a warp's positions: up to kAlone, or a share of kFew
+  uint32_t longs[kSumThreads / 32];      // the warps' units that all are to add up, plus 1
+  float sums[kSumThreads / 32][8][32];
+};
+
+// Sums the rows at the positions of a warp's list, in order.
+template <class D, bool kWhole>
+__device__ __forceinline__ void add_listed(const EmbeddingBackwardArgs& a, const uint16_t* list, uint32_t many,
+                                           const Slab<kWhole>& c, float (&acc)[8]) {
+  constexpr int kAhead = sizeof(typename D::raw) == 2 ? (kWhole ? 8 : 3) : (kWhole ? 4 : 2);
+  using V = typename D::V;
+  const Span span = span_of<D>(a.dy, a.n, a.cols, a.ld_dy);
+  for (uint32_t i = 0; i < many; i += kAhead) {
+    Fetched<V, kWhole> f[kAhead];
+    const typename D::raw* row[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {  // (past the list's end its last row again, not summed)
+      row[k] = row_of<D>(a.dy, list[min(i + k, many - 1)], a.ld_dy);
+      fetch_columns(f[k], row[k], c, span);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i + k >= many) break;
+      V x;
+      float v[8];
+      take_columns(x, f[k], row[k], c);
+      x.values(v);
+      plus8(acc, v);
+    }
+  }
+}
+
+template <class D, class T, bool kWhole>
+__global__ void __launch_bounds__(kSumThreads, 1)
+    embedding_few_kernel(const __grid_constant__ EmbeddingBackwardArgs a, const __grid_constant__ Segments g,
+                         const __grid_constant__ Clear z, const FastDiv by_slabs) {
+  __shared__ FewShared sh;
+  constexpr int kClearing = kSumThreads / 2;
+  if (z.table && threadIdx.x < kClearing) {
+    clear_rows<kClearing>(a, g, z, sh.bits);
+    return;
+  }
+  const uint32_t skip = z.table ? kClearing / 32 : 0, warps = kSumThreads / 32 - skip, warp = (threadIdx.x >> 5) - skip;
+  const uint32_t lane = threadIdx.x & 31, vocab = (uint32_t)a.vocab, chunks = (g.n + 31) / 32;
+  auto sync = [&] { asm volatile("bar.sync 2, %0;" ::"r"(32 * warps) : "memory"); };
+  for (uint32_t i = 32 * warp + lane; i < 32 * chunks; i += 32 * warps) {
+    const int64_t t = i < g.n ? token_at(a.tokens, a.token_bytes, i) : -1;
+    sh.keys[i] = (uint64_t)t < (uint64_t)a.vocab ? (uint32_t)t : vocab;
+  }
+  sync();
+  uint16_t* list = sh.lists[warp];
+  float acc[8];
+  // a list of the positions of `key` from `from` on whose number among them is
+  // the share's (of `shares`), and how many there are
+  auto collect = [&](uint32_t key, uint32_t from, uint32_t share, uint32_t shares) {
+    uint32_t count = 0;
+    for (uint32_t k = from / 32; k < chunks; ++k) {
+      const uint32_t at = 32 * k + lane;
+      const bool mine = sh.keys[at] == key;
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, mine), nth = count + __popc(all & ((1u << lane) - 1u));
+      if (mine && nth % shares == share && nth / shares < 32) list[nth / shares] = (uint16_t)at;
+      count += __popc(all);
+    }
+    __syncwarp();
+    return count;
+  };
+  // units go round the CTAs first: a token's slabs to as many of them
+  const uint32_t units = g.n * g.slabs;
+  for (uint32_t round = 0; round * warps * gridDim.x < units; ++round) {
+    const uint32_t u = blockIdx.x + gridDim.x * (warp + warps * round);
+    uint32_t is_long = 0;
+    if (u < units) {
+      const uint32_t i = div_by(u, by_slabs), key = sh.keys[i];
+      bool first = key != vocab;
+      for (uint32_t k = 0; first && k <= i / 32; ++k)
+        first = !__any_sync(0xFFFFFFFFu, 32 * k + lane < i && sh.keys[32 * k + lane] == key);
+      if (first) {
+        const uint32_t many = collect(key, i, 0, 1);
+        if (many <= kAlone) {
+          const Slab<kWhole> c(256u * (u - i * g.slabs), lane, (uint32_t)a.cols);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+          add_listed<D, kWhole>(a, list, many, c, acc);
+          finish_row<T, kWhole>(a, key, c, acc);
+        } else {
+          is_long = u + 1;
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) sh.longs[warp] = is_long;
+    sync();
+    for (uint32_t w = 0; w < warps; ++w) {
+      const uint32_t of = sh.longs[w];
+      if (!of) continue;
+      const uint32_t i = div_by(of - 1, by_slabs), key = sh.keys[i], all = collect(key, i, warp, warps);
+      const Slab<kWhole> c(256u * (of - 1 - i * g.slabs), lane, (uint32_t)a.cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+      if (all > warp) add_listed<D, kWhole>(a, list, (all - warp + warps - 1) / warps, c, acc);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sh.sums[warp][j][lane] = acc[j];
+      sync();
+      if (warp == w) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = sh.sums[0][j][lane];
+        for (uint32_t k = 1; k < warps; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], sh.sums[k][j][lane]);
+        finish_row<T, kWhole>(a, key, c, acc);
+      }
+      sync();
+    }
+    sync();  // (the list of long units is read by all before it is written again)
+  }
+}
+
 // ------------------------------------------------------------------ launch --
 
 int64_t element_bytes(int type) { return type == kMxF32 ? 4 : 2; }
@@ -713,6 +851,11 @@ using DenseF32 = Dense<TF32, kWhole>;
 
 template <class D, class T, bool kWhole>
 cudaError_t sum_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, int sm_count, cudaStream_t s) {
+  if (few_tokens(g.n, a.cols)) {
+    const unsigned grid = (unsigned)(z.table ? sm_count : std::min<int64_t>(sm_count, (int64_t)g.n * g.slabs));
+    embedding_few_kernel<D, T, kWhole><<<grid, kSumThreads, 0, s>>>(a, g, z, fast_div(g.slabs));
+    return cudaGetLastError();
+  }
   const int64_t units = (int64_t)g.count * g.slabs;
   if (units > 0x7FFFFFF0ll) return cudaErrorInvalidValue;
   const int grid = z.table ? sm_count : (int)std::min<int64_t>(sm_count, units);
@@ -754,6 +897,7 @@ struct Space {
 };
 Space space_of(int64_t n, int64_t cols) {
   Space p = {};
+  if (few_tokens(n, cols)) return p;
   int64_t at = 0;
   auto part = [&](int64_t words) {
     const int64_t here = at;
@@ -838,8 +982,9 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_cou
     z.rows = (uint32_t)std::max<int64_t>(1, std::min<int64_t>(kBitRows, 0x7FFFFFF0ll / z.row_bytes));
     z.end_to_end = z.end_to_end && z.row_bytes <= 0x7FFFFFF0ll;
   }
-  cudaError_t e;
-  if (a.n <= kClusterMax) {
+  cudaError_t e = cudaSuccess;
+  if (few_tokens(a.n, a.cols)) {  // (no sort)
+  } else if (a.n <= kClusterMax) {
     c.keys = words(p.keys[0]), c.pos = words(p.pos[0]);
     e = sort_in_cluster(c, s);
   } else {
