@@ -686,20 +686,23 @@ __global__ void __launch_bounds__(kJoinThreads) embedding_join_kernel(const __gr
 // more than kAlone positions is left to all warps of the CTA, a share each.  As
 // long as the warps have two units each at most; us for a whole call, here and
 // sorted, spread tokens and one token over and over:
-//   301 tokens, 5003 x 768 binary16      4.6 and 10.4, 8.9 and 11.0
-//   512 tokens of the same               5.3 and 11.9, 11.4 and 11.5
-//   512 tokens, 50304 x 1024 bf16        18.5 and 21.4, 20.0 and 24.3
+//   301 tokens, 5003 x 768 binary16      4.9 and 10.4, 8.3 and 11.0
+//   512 tokens of the same               5.4 and 11.9, 10.1 and 11.5
+//   512 tokens, 50304 x 1024 bf16        18.2 and 21.4, 19.6 and 24.3
 //   128 tokens, 2000 x 8192 bf16         9.8 and 13.4, 10.2 and 16.1
 //   301 tokens of the same (five units)  20.1 and 14.6, 17.8 and 16.4
-// What bounds it is latency: the launch, the tokens, two searches, the rows.
+// What bounds it is latency: the launch, the tokens, two searches, the rows.  (A
+// warp alone for up to 16 positions instead of 32: tokens of a text, 301, 7.4 us
+// instead of 6.2.)
 constexpr uint32_t kFew = 512;
-constexpr uint32_t kAlone = 16;
+constexpr uint32_t kAlone = 32;
+static_assert(kFew <= kAlone * (kSumThreads / 64), "a warp's share fits its list");
 bool few_tokens(int64_t n, int64_t cols) { return n <= kFew && n * ((cols + 255) / 256) <= 2 * 148 * (kSumThreads / 64); }
 
 struct FewShared {
   uint32_t keys[kFew];
   uint32_t bits[kBitRows / 32];
-  uint16_t lists[kSumThreads / 32][32];  // a warp's positions: up to kAlone, or a share of kFew
+  uint16_t lists[kSumThreads / 32][kAlone];  // a warp's positions, all or a share
   uint32_t longs[kSumThreads / 32];      // the warps' units that all are to add up, plus 1
   float sums[kSumThreads / 32][8][32];
 };
@@ -752,14 +755,15 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   uint16_t* list = sh.lists[warp];
   float acc[8];
   // a list of the positions of `key` from `from` on whose number among them is
-  // the share's (of `shares`), and how many there are
-  auto collect = [&](uint32_t key, uint32_t from, uint32_t share, uint32_t shares) {
+  // the share's (of 2^shift), and how many there are
+  auto collect = [&](uint32_t key, uint32_t from, uint32_t share, uint32_t shift) {
     uint32_t count = 0;
+#pragma unroll 4
     for (uint32_t k = from / 32; k < chunks; ++k) {
       const uint32_t at = 32 * k + lane;
       const bool mine = sh.keys[at] == key;
       const uint32_t all = __ballot_sync(0xFFFFFFFFu, mine), nth = count + __popc(all & ((1u << lane) - 1u));
-      if (mine && nth % shares == share && nth / shares < 32) list[nth / shares] = (uint16_t)at;
+      if (mine && nth - (nth >> shift << shift) == share && nth >> shift < kAlone) list[nth >> shift] = (uint16_t)at;
       count += __popc(all);
     }
     __syncwarp();
@@ -776,7 +780,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       for (uint32_t k = 0; first && k <= i / 32; ++k)
         first = !__any_sync(0xFFFFFFFFu, 32 * k + lane < i && sh.keys[32 * k + lane] == key);
       if (first) {
-        const uint32_t many = collect(key, i, 0, 1);
+        const uint32_t many = collect(key, i, 0, 0);
         if (many <= kAlone) {
           const Slab<kWhole> c(256u * (u - i * g.slabs), lane, (uint32_t)a.cols);
 #pragma unroll
@@ -794,7 +798,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     for (uint32_t w = 0; w < warps; ++w) {
       const uint32_t of = sh.longs[w];
       if (!of) continue;
-      const uint32_t i = div_by(of - 1, by_slabs), key = sh.keys[i], all = collect(key, i, warp, warps);
+      const uint32_t i = div_by(of - 1, by_slabs), key = sh.keys[i], all = collect(key, i, warp, 31 - __clz(warps));
       const Slab<kWhole> c(256u * (of - 1 - i * g.slabs), lane, (uint32_t)a.cols);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
