@@ -382,6 +382,7 @@ struct Clear {
   bool by_search, end_to_end;  // rows of one piece
   FastDiv by_row;              // a row's elements of 2 bytes
   uint32_t rows;               // of the table that a CTA looks after at a time
+  uint32_t each, late, each_late;  // a CTA's rows, and the last CTAs', how many those are
 };
 
 struct Segments {
@@ -433,11 +434,12 @@ __device__ __forceinline__ void clear_row(uint8_t* p, int64_t bytes) {
 template <int kThreads>
 __device__ __forceinline__ void clear_rows(const EmbeddingBackwardArgs& a, const Segments& g, const Clear& z, uint32_t* bits) {
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
-  const int64_t each = (a.vocab + gridDim.x - 1) / gridDim.x;
-  const int64_t end = min(a.vocab, (int64_t)(blockIdx.x + 1) * each);
+  const uint32_t soon = gridDim.x - z.late, mine = blockIdx.x < soon ? z.each : z.each_late;
+  const int64_t begin = (int64_t)min(blockIdx.x, soon) * z.each + (blockIdx.x < soon ? 0 : (int64_t)(blockIdx.x - soon) * mine);
+  const int64_t end = min(a.vocab, begin + mine);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (z.by_search) pdl_wait();
-  for (int64_t lo = blockIdx.x * each; lo < end; lo += z.rows) {
+  for (int64_t lo = begin; lo < end; lo += z.rows) {
     const uint32_t rows = (uint32_t)min(end - lo, (int64_t)z.rows);
     if (z.by_search) {
       for (uint32_t r = threadIdx.x; r < (rows + 31) / 32 * 32; r += kThreads) {
@@ -923,9 +925,17 @@ int bits_of(int64_t v) {
   return b;
 }
 
+int cluster_ctas(int64_t n) { return n <= kClusterThreads ? 1 : n <= 2 * kClusterThreads ? 2 : n <= 4 * kClusterThreads ? 4 : kClusterCtas; }
+
+// What a CTA clears while the cluster sorts.  The segments' CTAs start while it
+// does; the last ones find its SMs taken and begin when it is done, so that they
+// get so much less to clear (8192 tokens, 32000 x 768 bf16: 25.0 us, shared equally
+// 26.2; 16384 tokens, 50304 x 2048: 61.2 and 61.8).
+int64_t late_bytes(int64_t n) { return (4 + n / 4096) * 38000; }
+
 cudaError_t sort_in_cluster(ClusterSort c, cudaStream_t s) {
   const int64_t thousands = (c.n + kClusterThreads - 1) / kClusterThreads;
-  c.ctas = thousands <= 1 ? 1 : thousands <= 2 ? 2 : thousands <= 4 ? 4 : kClusterCtas;
+  c.ctas = cluster_ctas(c.n);
   c.per = (uint32_t)((thousands + c.ctas - 1) / c.ctas) * kClusterThreads;
   const int bits = bits_of(c.vocab);
   c.passes = std::max(1, (bits + kClusterBits - 1) / kClusterBits);
@@ -985,6 +995,9 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int sm_cou
     // so many that their bytes are counted in 31 bits
     z.rows = (uint32_t)std::max<int64_t>(1, std::min<int64_t>(kBitRows, 0x7FFFFFF0ll / z.row_bytes));
     z.end_to_end = z.end_to_end && z.row_bytes <= 0x7FFFFFF0ll;
+    if (a.n <= kClusterMax && !few_tokens(a.n, a.cols)) z.late = std::min(cluster_ctas(a.n), sm_count - 1);
+    z.each_late = z.late ? (uint32_t)std::max<int64_t>(0, a.vocab / sm_count - late_bytes(a.n) / z.row_bytes) : 0;
+    z.each = (uint32_t)((a.vocab - (int64_t)z.late * z.each_late + sm_count - z.late - 1) / (sm_count - z.late));
   }
   cudaError_t e = cudaSuccess;
   if (few_tokens(a.n, a.cols)) {  // (no sort)
