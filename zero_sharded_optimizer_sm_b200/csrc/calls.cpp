@@ -271,9 +271,10 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 4 || !dy.read(a[0], here) || !t.read(a[1], here) || t.n != dy.rows || !whole(a[2], &vocab) || !PyFloat_Check(a[3]))
       return nullptr;
     if (zero_embedding_backward_workspace(t.n, vocab, dy.cols, &need) != ZERO_OK) return nullptr;
-    at::Tensor out = here.empty({vocab, dy.cols}, dy.t->scalar_type()), space = here.empty({need}, at::kByte);
+    at::Tensor out = here.empty({vocab, dy.cols}, dy.t->scalar_type()), space;
+    if (need) space = here.empty({need}, at::kByte);  // (few tokens need none)
     if (zero_embedding_backward(dy.at, dy.code, dy.rows, dy.cols, dy.ld, t.at, t.size, vocab, PyFloat_AS_DOUBLE(a[3]),
-                                out.data_ptr(), dy.code, dy.cols, 0, space.data_ptr(), need, here.stream) != ZERO_OK)
+                                out.data_ptr(), dy.code, dy.cols, 0, need ? space.data_ptr() : nullptr, need, here.stream) != ZERO_OK)
       return nullptr;
     return wrap(std::move(out));
   });
