@@ -6,6 +6,8 @@
 // between the sum over the row and its use.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "rms_norm.cuh"
 #include "rows.cuh"
 
@@ -44,17 +46,35 @@ __device__ __forceinline__ double group_sum(const float (&of)[kSums], float* sme
   return v;
 }
 
-// (ss / cols + eps)^(-1/2), rounded once from binary64: the function's binary32
-// estimate and one Newton step, whose error is the square of the estimate's.
-// y's rounding to 16 and then to 8 bits turns on rstd's last bit now and then,
-// so it is the correctly rounded one but for sums next to a tie.
-__device__ __forceinline__ float rstd_of(double ss, double inv_cols, double eps) {
-  const double m = __fma_rn(ss, inv_cols, eps);
+// rstd = m^(-1/2), m = ss / cols + eps: the function's binary32 estimate and one
+// Newton step in binary64, whose error is the square of the estimate's, rounded to
+// binary32 once.  (y's rounding to 16 and then to 8 bits turns on rstd's last bit
+// now and then.  The sum that m comes from is binary32's of 256 columns each: one
+// rstd in twenty of rows of 4096 is not the correctly rounded one.)
+__device__ __forceinline__ double root_of(double m) {
   const float r = rsqrtf((float)m);
   const double e = __fma_rn(-__dmul_rn(m, (double)r), (double)r, 1.0);
-  const float better = (float)__fma_rn(__dmul_rn(0.5, e), (double)r, (double)r);
-  return isfinite((float)m) ? better : r;
+  return __fma_rn(__dmul_rn(0.5, e), (double)r, (double)r);
 }
+
+// Whether m is below 2^-100, 2^126 and more, infinite or not a number: near or past
+// the ends of binary32, as the squares may have been.
+__device__ __forceinline__ bool is_far(double m) {
+  return (uint32_t)__double2hiint(m) - ((1023u - 100u) << 20) >= 226u << 20;
+}
+// rstd of any m: moved by a power of four.
+__device__ __forceinline__ float far_root_of(double m) {
+  if (isinf(m)) return 0.0f;
+  const bool above = m > 1.0;
+  return (float)__dmul_rn(root_of(__dmul_rn(m, above ? 0x1p-160 : 0x1p160)), above ? 0x1p-80 : 0x1p80);
+}
+// The squares of such a row are added up once more in units of 2^80 or 2^-80.
+// Above, where one |h| is 2^64 or 256 are 2^60, no sum of up to 2^31 columns is
+// infinite then; below, where the mean counts beside an eps of that size, no square
+// that counts is lost.  (Binary16's squares, 2^-48 to 2^32, are right as
+// they are.)
+__device__ __forceinline__ float unit_of(double m) { return m > 1.0 ? 0x1p-80f : 0x1p80f; }
+__device__ __forceinline__ double in_units(double ss, float unit) { return __dmul_rn(ss, unit < 1.0f ? 0x1p160 : 0x1p-160); }
 
 // The addresses of a row of the operands and results.
 template <class T>
@@ -96,6 +116,28 @@ __device__ __forceinline__ float2 square_sum(const float (&v)[8], float2 ss) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) ss = fma2(pair(v, p), pair(v, p), ss);
   return ss;
+}
+
+// For a row that is far: a vector's squares in units, by a call, so that this rare
+// way takes no registers from the other (inlined, 6000 x 2421 bf16 took 47.1 us
+// instead of 46.2).
+template <class V>
+__device__ __noinline__ float far_squares(const V x, float unit) {
+  float v[8];
+  x.values(v);
+  scale8(v, unit);
+  const float2 ss = square_sum(v, make_float2(0.0f, 0.0f));
+  return __fadd_rn(ss.x, ss.y);
+}
+// Of aligned rows the values are formed anew after it: kept in registers past it,
+// 8192 x 4096 with all results took 59.7 us instead of 54.9.  (Unaligned ones have
+// them in registers anyway.)
+template <class V, int kN>
+__device__ __forceinline__ void as_loaded(V (&x)[kN]) {
+#pragma unroll
+  for (int k = 0; k < kN; ++k)
+#pragma unroll
+    for (int i = 0; i < WordsOf<V>::kN; ++i) asm volatile("" : "+r"(words(x[k])[i]));
 }
 
 // All results of one vector of h.  Called by whole warps.
@@ -167,7 +209,25 @@ __global__ void __launch_bounds__(kLanes ? kLanesThreads : 512) rms_norm_kernel(
     of = square_sum(v, kSums == 1 ? of : make_float2(0.0f, 0.0f));
     ss[kSums == 1 ? 0 : k] = __fadd_rn(of.x, of.y);
   }
-  const float rstd = rstd_of(group_sum<kLanes>(ss, smem), inv_cols, (double)a.eps);
+  const double m = __fma_rn(group_sum<kLanes>(ss, smem), inv_cols, (double)a.eps);
+  float rstd;
+  if (kLanes ? __any_sync(0xFFFFFFFFu, is_far(m)) : is_far(m)) {  // (whole warps, or the whole block)
+    double far = m;
+    if constexpr (!std::is_same<T, TF16>::value) {
+      const float unit = unit_of(m);
+      if constexpr (kWhole) as_loaded(x);
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const float f = far_squares(x[k], unit);
+        ss[kSums == 1 ? 0 : k] = kSums == 1 && k > 0 ? __fadd_rn(ss[0], f) : f;
+      }
+      if constexpr (kLanes == 0) __syncthreads();  // (the first sum's shared memory)
+      far = __fma_rn(in_units(group_sum<kLanes>(ss, smem), unit), inv_cols, (double)a.eps);
+    }
+    rstd = is_far(m) ? far_root_of(far) : (float)root_of(m);
+  } else {
+    rstd = (float)root_of(m);
+  }
   if (a.rstd && t == 0 && there) a.rstd[number] = rstd;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) finish<T, kLanes ? kLanes : 32>(a, row, C(8 * group * k, t, cols), rstd, x[k]);
@@ -183,17 +243,29 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(const __gri
   const NormRow<T> row(a, blockIdx.x);
   const uint32_t cols = (uint32_t)a.cols;
   using C = Columns<kWhole>;
-  float2 ss = make_float2(0.0f, 0.0f);
-  for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
-    typename T::V x[1];
-    const C c[1] = {C(first, threadIdx.x, cols)};
-    float v[8];
-    load_h<T>(a, row, c, x);
-    x[0].values(v);
-    ss = square_sum(v, ss);
+  auto row_sum = [&](auto far, float unit) {  // (of a far row in units)
+    float2 ss = make_float2(0.0f, 0.0f);
+    for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
+      typename T::V x[1];
+      const C c[1] = {C(first, threadIdx.x, cols)};
+      float v[8];
+      load_h<T>(a, row, c, x);
+      x[0].values(v);
+      if constexpr (decltype(far)::value) scale8(v, unit);
+      ss = square_sum(v, ss);
+    }
+    float sum[1] = {__fadd_rn(ss.x, ss.y)};
+    return group_sum<0>(sum, smem);
+  };
+  const double m = __fma_rn(row_sum(std::false_type(), 1.0f), inv_cols, (double)a.eps);
+  float rstd;
+  if (is_far(m)) {
+    __syncthreads();  // (the sum's shared memory)
+    const float unit = unit_of(m);
+    rstd = far_root_of(__fma_rn(in_units(row_sum(std::true_type(), unit), unit), inv_cols, (double)a.eps));
+  } else {
+    rstd = (float)root_of(m);
   }
-  float sum[1] = {__fadd_rn(ss.x, ss.y)};
-  const float rstd = rstd_of(group_sum<0>(sum, smem), inv_cols, (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
   for (uint32_t first = 0; first < cols; first += 8 * kLongThreads) {
     typename T::V x[1];
