@@ -995,8 +995,8 @@ zero_status zero_mx4_linear_backward_mx8(const void* dy, int32_t dy_dtype, int64
  * the residual's own memory, with the same ld.  eps > 0.  A row is computed in
  * binary32 from the rounded h, whatever its size: squares that leave binary32's
  * range are added up in other units.  (rstd is binary32: below 2^-126, of rows
- * whose mean square is past 2^252, it has fewer bits, and y with it.)  No passage
- * of the pages defines it. */
+ * whose mean square is past 2^252, it has fewer bits, and y with it; of rows
+ * without columns it is not a number.)  No passage of the pages defines it. */
 zero_status zero_rms_norm(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x,
                           int64_t ld_residual, const void* weight, int32_t weight_dtype, double eps, void* y, int64_t ld_y,
                           void* h, int64_t ld_h, const zero_mx8* y8, const zero_mx8* h8, float* rstd, void* stream);

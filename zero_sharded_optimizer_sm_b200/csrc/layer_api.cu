@@ -92,6 +92,10 @@ zero_status zero_rms_norm(const void* x, const void* residual, int32_t dtype, in
   if (y8 && (st = check_shape8("y8", y8, rows, cols)) != ZERO_OK) return st;
   if (h8 && (st = check_shape8("h8", h8, rows, cols)) != ZERO_OK) return st;
   if (reinterpret_cast<uintptr_t>(rstd) & 3u) return fail(ZERO_EINVAL, "rstd is not aligned to its elements");
+  if (rows && cols == 0 && rstd) {  // the mean of nothing: not a number (four bytes of 0xFF are one)
+    const cudaError_t e = cudaMemsetAsync(rstd, 0xFF, sizeof(float) * (size_t)rows, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "rows without columns");
+  }
   if (rows == 0 || cols == 0) return ZERO_OK;  // (the results' addresses may be null then)
   if (!y && !h && !y8 && !h8 && !rstd) return fail(ZERO_EINVAL, "no result is given");
   int sms = 0;
