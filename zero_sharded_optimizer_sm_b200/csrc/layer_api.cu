@@ -182,6 +182,8 @@ zero_status zero_embedding(const void* tokens, int32_t token_bytes, int64_t n, c
   if ((st = check_scale(scale)) != ZERO_OK) return st;
   if ((st = check_dense("out", out, out_dtype, n, cols, ld_out)) != ZERO_OK) return st;
   if (n == 0 || cols == 0) return ZERO_OK;
+  // (an MX4 table's codes, by which the launch knows it, may be null here)
+  if (vocab == 0) return zero_fill(out, out_dtype, n, cols, ld_out, static_cast<cudaStream_t>(stream));
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
