@@ -948,8 +948,9 @@ zero_status zero_mx4_reduce_scatter(zero_ctx* ctx, int64_t lo, int64_t hi, const
  * CUDA device, no state between calls, captures allowed, empty matrices
  * accepted.  Outputs must not overlap inputs or one another, except where a
  * call says so.  Sums over a row or a batch are held in binary32 or more, in an
- * order that the sizes alone fix: the same bits on every run.  A row of the
- * norm's y, h and dx does not depend on how many other rows there are.
+ * order that the sizes fix, and for the embedding's gradient the tokens too: the
+ * same bits on every run.  A row of the norm's y, h and dx does not depend on how
+ * many other rows there are.
  */
 #define ZERO_MX8_BLOCK 32
 

@@ -2,9 +2,11 @@
 //
 // The lookup is a gather of rows, memory-bound.  The gradient is bound by the
 // table that it writes whole: the batch's rows are sorted by their token, so
-// that each row of the table is summed in binary32 in the batch's order,
-// rounded once, and written once -- the same bits on every run, which atomic
-// additions would not give.
+// that each row of the table is summed in binary32, rounded once, and written
+// once.  A token's rows are added in the batch's order as far as one warp adds
+// them, and the sums of several warps after that; who adds what follows from the
+// sizes and the tokens: the same bits on every run, which atomic additions would
+// not give.
 #include <cuda_runtime.h>
 
 #include "embedding.cuh"
@@ -685,9 +687,11 @@ __global__ void __launch_bounds__(kJoinThreads) embedding_join_kernel(const __gr
 // Up to kFew tokens need no sort: a warp takes a position and a slab, looks
 // through all tokens for an earlier one of its kind (whose warp it leaves the sum
 // to) and for the later ones, and adds their rows in the batch's order; a token of
-// more than kAlone positions is left to all warps of the CTA, a share each.  As
-// long as the warps have two units each at most; us for a whole call, here and
-// sorted, spread tokens and one token over and over:
+// more than kAlone positions is left to kShares warps of the CTA, every kShares-th
+// of them each, whose sums are added in order -- as many whether half the warps
+// clear or not, so that adding to zeros gives the bits that writing does.  As long
+// as the warps have two units each at most; us for a whole call, here and sorted,
+// spread tokens and one token over and over:
 //   301 tokens, 5003 x 768 binary16      4.9 and 10.4, 8.3 and 11.0
 //   512 tokens of the same               5.4 and 11.9, 10.1 and 11.5
 //   512 tokens, 50304 x 1024 bf16        18.2 and 21.4, 19.6 and 24.3
@@ -698,7 +702,9 @@ __global__ void __launch_bounds__(kJoinThreads) embedding_join_kernel(const __gr
 // instead of 6.2.)
 constexpr uint32_t kFew = 512;
 constexpr uint32_t kAlone = 32;
-static_assert(kFew <= kAlone * (kSumThreads / 64), "a warp's share fits its list");
+constexpr int kShareBits = 4;
+constexpr uint32_t kShares = 1u << kShareBits;
+static_assert(kFew <= kAlone * kShares && kShares <= kSumThreads / 64, "a share fits a warp's list, and there are as many warps");
 bool few_tokens(int64_t n, int64_t cols) { return n <= kFew && n * ((cols + 255) / 256) <= 2 * 148 * (kSumThreads / 64); }
 
 struct FewShared {
@@ -706,7 +712,7 @@ struct FewShared {
   uint32_t bits[kBitRows / 32];
   uint16_t lists[kSumThreads / 32][kAlone];  // a warp's positions, all or a share
   uint32_t longs[kSumThreads / 32];      // the warps' units that all are to add up, plus 1
-  float sums[kSumThreads / 32][8][32];
+  float sums[kShares][8][32];
 };
 
 // Sums the rows at the positions of a warp's list, in order.
@@ -800,18 +806,21 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     for (uint32_t w = 0; w < warps; ++w) {
       const uint32_t of = sh.longs[w];
       if (!of) continue;
-      const uint32_t i = div_by(of - 1, by_slabs), key = sh.keys[i], all = collect(key, i, warp, 31 - __clz(warps));
+      const uint32_t i = div_by(of - 1, by_slabs), key = sh.keys[i];
       const Slab<kWhole> c(256u * (of - 1 - i * g.slabs), lane, (uint32_t)a.cols);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-      if (all > warp) add_listed<D, kWhole>(a, list, (all - warp + warps - 1) / warps, c, acc);
+      if (warp < kShares) {
+        const uint32_t all = collect(key, i, warp, kShareBits);
+        if (all > warp) add_listed<D, kWhole>(a, list, (all - warp + kShares - 1) / kShares, c, acc);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sh.sums[warp][j][lane] = acc[j];
+        for (int j = 0; j < 8; ++j) sh.sums[warp][j][lane] = acc[j];
+      }
       sync();
       if (warp == w) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = sh.sums[0][j][lane];
-        for (uint32_t k = 1; k < warps; ++k)
+        for (uint32_t k = 1; k < kShares; ++k)
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] = __fadd_rn(acc[j], sh.sums[k][j][lane]);
         finish_row<T, kWhole>(a, key, c, acc);
