@@ -4,6 +4,11 @@
 // and calling through ctypes took 9 to 16 on the host (norm of one token 13 us
 // a call, 20 with its backward pass), and from here 3 to 6.
 //
+// Python's lock is let go of while memory is taken and kernels are launched, as
+// ctypes does: a launch waits where the stream's queue is full, and what it waits
+// for may be another Python thread's to enqueue.  The operands are their caller's
+// meanwhile; nothing of Python is touched.
+//
 // A function returns None for whatever is not plain -- another stream or device,
 // a wrong type or shape, an error of the library -- and the caller, which has
 // every check and every message, goes the long way.
@@ -128,20 +133,24 @@ bool put(PyObject* o, PyObject* name, PyObject* value) {  // takes the value's r
   return ok;
 }
 
-// A new MX8 matrix, as the package's own class makes it.
-PyObject* new_mx8(int64_t rows, int64_t cols, const Here& h, zero_mx8* m) {
+// Memory of a new MX8 matrix, and the package's own object of it.
+at::Tensor mx8_memory(int64_t rows, int64_t cols, const Here& h, zero_mx8* m) {
   const int64_t nb = (cols + 31) / 32, cp = 32 * nb, sp = (nb + 15) / 16 * 16;
   at::Tensor space = h.empty({rows * (cp + sp)}, at::kByte);
   uint8_t* at = static_cast<uint8_t*>(space.data_ptr());
   *m = {at, at + rows * cp, rows, cols, cp, sp};
+  return space;
+}
+PyObject* mx8_object(at::Tensor&& space, const Here& h, const zero_mx8& m) {
   PyTypeObject* type = (PyTypeObject*)g_mx8;
   PyObject* o = type->tp_new(type, g_no_args, nullptr);
   if (!o) return nullptr;
   const bool ok = put(o, s_space, THPVariable_Wrap(std::move(space))) && put(o, s_codes, Py_NewRef(Py_None)) &&
                   put(o, s_scales, Py_NewRef(Py_None)) && put(o, s_struct, Py_NewRef(Py_None)) &&
-                  put(o, s_rows, PyLong_FromLongLong(rows)) && put(o, s_cols, PyLong_FromLongLong(cols)) &&
+                  put(o, s_rows, PyLong_FromLongLong(m.rows)) && put(o, s_cols, PyLong_FromLongLong(m.cols)) &&
                   put(o, s_device, THPDevice_New(at::Device(at::kCUDA, h.device))) &&
-                  put(o, s_at, Py_BuildValue("(LLLL)", (long long)m->codes, (long long)m->scales, (long long)cp, (long long)sp));
+                  put(o, s_at, Py_BuildValue("(LLLL)", (long long)m.codes, (long long)m.scales, (long long)m.code_pitch,
+                                            (long long)m.scale_pitch));
   if (!ok) Py_CLEAR(o);
   return o;
 }
@@ -162,6 +171,19 @@ PyObject* plainly(F f) {
   Py_RETURN_NONE;
 }
 
+// Python's lock let go of, until the end of the scope.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class F>
+zero_status unlocked(F f) {
+  const Unlocked scope;
+  return f();
+}
+
 PyObject* wrap(at::Tensor&& t) { return t.defined() ? THPVariable_Wrap(std::move(t)) : Py_NewRef(Py_None); }
 
 // mx8_quantize(x)
@@ -171,9 +193,12 @@ PyObject* mx8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Matrix x;
     zero_mx8 m;
     if (n != 1 || !x.read(a[0], here)) return nullptr;
-    PyObject* o = new_mx8(x.rows, x.cols, here, &m);
-    if (o && zero_mx8_quantize(x.at, x.code, x.rows, x.cols, x.ld, &m, here.stream) != ZERO_OK) Py_CLEAR(o);
-    return o;
+    at::Tensor space;
+    const zero_status st = unlocked([&] {
+      space = mx8_memory(x.rows, x.cols, here, &m);
+      return zero_mx8_quantize(x.at, x.code, x.rows, x.cols, x.ld, &m, here.stream);
+    });
+    return st == ZERO_OK ? mx8_object(std::move(space), here, m) : nullptr;
   });
 }
 
@@ -185,9 +210,12 @@ PyObject* mx8_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 2 || !read_mx(a[0], g_mx8, here, &m) || !THPDtype_Check(a[1])) return nullptr;
     const at::ScalarType type = ((THPDtype*)a[1])->scalar_type;
     if (code_of(type) < 0) return nullptr;
-    at::Tensor out = here.empty({m.rows, m.cols}, type);
-    if (zero_mx8_dequantize(&m, out.data_ptr(), code_of(type), m.cols, here.stream) != ZERO_OK) return nullptr;
-    return wrap(std::move(out));
+    at::Tensor out;
+    const zero_status st = unlocked([&] {
+      out = here.empty({m.rows, m.cols}, type);
+      return zero_mx8_dequantize(&m, out.data_ptr(), code_of(type), m.cols, here.stream);
+    });
+    return st == ZERO_OK ? wrap(std::move(out)) : nullptr;
   });
 }
 
@@ -201,13 +229,18 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] != Py_None && !r.like(a[3], here, x)) return nullptr;
     if (!PyBool_Check(a[4]) || !PyBool_Check(a[5])) return nullptr;
     const at::ScalarType type = x.t->scalar_type();
-    at::Tensor y = here.empty({x.rows, x.cols}, type), h, s;
-    if (a[4] == Py_True) h = here.empty({x.rows, x.cols}, type);
-    if (a[5] == Py_True) s = here.empty({x.rows}, at::kFloat);
-    if (zero_rms_norm(x.at, r.at, x.code, x.rows, x.cols, x.ld, r.ld, w.at, w.code, PyFloat_AS_DOUBLE(a[2]), y.data_ptr(),
-                      x.cols, h.defined() ? h.data_ptr() : nullptr, x.cols, nullptr, nullptr,
-                      s.defined() ? static_cast<float*>(s.data_ptr()) : nullptr, here.stream) != ZERO_OK)
-      return nullptr;
+    const bool want_h = a[4] == Py_True, want_s = a[5] == Py_True;
+    const double eps = PyFloat_AS_DOUBLE(a[2]);
+    at::Tensor y, h, s;
+    const zero_status st = unlocked([&] {
+      y = here.empty({x.rows, x.cols}, type);
+      if (want_h) h = here.empty({x.rows, x.cols}, type);
+      if (want_s) s = here.empty({x.rows}, at::kFloat);
+      return zero_rms_norm(x.at, r.at, x.code, x.rows, x.cols, x.ld, r.ld, w.at, w.code, eps, y.data_ptr(), x.cols,
+                           want_h ? h.data_ptr() : nullptr, x.cols, nullptr, nullptr,
+                           want_s ? static_cast<float*>(s.data_ptr()) : nullptr, here.stream);
+    });
+    if (st != ZERO_OK) return nullptr;
     return Py_BuildValue("(NNN)", wrap(std::move(y)), wrap(std::move(h)), wrap(std::move(s)));
   });
 }
@@ -226,12 +259,16 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[4] != Py_None && !dh.like(a[4], here, dy)) return nullptr;
     int64_t need = 0;
     if (zero_rms_norm_backward_workspace(dy.rows, dy.cols, &need) != ZERO_OK) return nullptr;
-    at::Tensor dx = here.empty({dy.rows, dy.cols}, dy.t->scalar_type()), dw = here.empty({dy.cols}, w.type),
-               space = here.empty({need}, at::kByte);
-    if (zero_rms_norm_backward(dy.at, dy.code, dy.rows, dy.cols, dy.ld, h.at, h.ld, kept ? &m : nullptr, w.at, w.code,
-                               static_cast<const float*>(s.at), dh.at, dh.ld, dx.data_ptr(), dy.cols, dw.data_ptr(), w.code,
-                               space.data_ptr(), need, here.stream) != ZERO_OK)
-      return nullptr;
+    const at::ScalarType type = dy.t->scalar_type();
+    at::Tensor dx, dw;
+    const zero_status st = unlocked([&] {
+      dx = here.empty({dy.rows, dy.cols}, type), dw = here.empty({dy.cols}, w.type);
+      at::Tensor space = here.empty({need}, at::kByte);
+      return zero_rms_norm_backward(dy.at, dy.code, dy.rows, dy.cols, dy.ld, h.at, h.ld, kept ? &m : nullptr, w.at, w.code,
+                                    static_cast<const float*>(s.at), dh.at, dh.ld, dx.data_ptr(), dy.cols, dw.data_ptr(),
+                                    w.code, space.data_ptr(), need, here.stream);
+    });
+    if (st != ZERO_OK) return nullptr;
     return Py_BuildValue("(NN)", wrap(std::move(dx)), wrap(std::move(dw)));
   });
 }
@@ -253,11 +290,14 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (code_of(type) < 0) return nullptr;
     }
     const int64_t vocab = mx ? m.rows : table.rows, cols = mx ? m.cols : table.cols;
-    at::Tensor out = here.empty({t.n, cols}, type);
-    if (zero_embedding(t.at, t.size, t.n, table.at, mx ? 0 : table.code, vocab, cols, table.ld, mx ? &m : nullptr,
-                       PyFloat_AS_DOUBLE(a[2]), out.data_ptr(), code_of(type), cols, here.stream) != ZERO_OK)
-      return nullptr;
-    return wrap(std::move(out));
+    const double scale = PyFloat_AS_DOUBLE(a[2]);
+    at::Tensor out;
+    const zero_status st = unlocked([&] {
+      out = here.empty({t.n, cols}, type);
+      return zero_embedding(t.at, t.size, t.n, table.at, mx ? 0 : table.code, vocab, cols, table.ld, mx ? &m : nullptr, scale,
+                            out.data_ptr(), code_of(type), cols, here.stream);
+    });
+    return st == ZERO_OK ? wrap(std::move(out)) : nullptr;
   });
 }
 
@@ -271,12 +311,17 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 4 || !dy.read(a[0], here) || !t.read(a[1], here) || t.n != dy.rows || !whole(a[2], &vocab) || !PyFloat_Check(a[3]))
       return nullptr;
     if (zero_embedding_backward_workspace(t.n, vocab, dy.cols, &need) != ZERO_OK) return nullptr;
-    at::Tensor out = here.empty({vocab, dy.cols}, dy.t->scalar_type()), space;
-    if (need) space = here.empty({need}, at::kByte);  // (few tokens need none)
-    if (zero_embedding_backward(dy.at, dy.code, dy.rows, dy.cols, dy.ld, t.at, t.size, vocab, PyFloat_AS_DOUBLE(a[3]),
-                                out.data_ptr(), dy.code, dy.cols, 0, need ? space.data_ptr() : nullptr, need, here.stream) != ZERO_OK)
-      return nullptr;
-    return wrap(std::move(out));
+    const double scale = PyFloat_AS_DOUBLE(a[3]);
+    const at::ScalarType type = dy.t->scalar_type();
+    at::Tensor out;
+    const zero_status st = unlocked([&] {
+      out = here.empty({vocab, dy.cols}, type);
+      at::Tensor space;
+      if (need) space = here.empty({need}, at::kByte);  // (few tokens need none)
+      return zero_embedding_backward(dy.at, dy.code, dy.rows, dy.cols, dy.ld, t.at, t.size, vocab, scale, out.data_ptr(),
+                                     dy.code, dy.cols, 0, need ? space.data_ptr() : nullptr, need, here.stream);
+    });
+    return st == ZERO_OK ? wrap(std::move(out)) : nullptr;
   });
 }
 
