@@ -16,16 +16,16 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from dataclasses import dataclass
 from typing import Callable, List, NamedTuple, Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzero_sm.so")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")  # a shortcut to some of its calls, loaded on first use
 
-CALLS_PATH = os.path.join(_HERE, "_calls.so")
-
-if not (os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH)):
-    raise ImportError(f"{LIB_PATH if not os.path.exists(LIB_PATH) else CALLS_PATH} is missing: build it with __graft_entry__.build() "
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(the ZeRO step has no fallback implementation)")
 
 lib = ctypes.CDLL(LIB_PATH)
@@ -716,7 +716,8 @@ class ZeroOptimizer:
 # until their work has run.
 #
 # The calls around a layer's products have a compiled way for their plain use
-# (csrc/calls.cpp); None from it means that this one has to look closer.
+# (csrc/calls.cpp); None from it means that this one has to look closer.  Where
+# it was not built, or for another torch, every call goes this way.
 
 _CALLS = None        # the compiled calls, after the first use
 _T = None            # torch, after the first use
@@ -737,18 +738,33 @@ def _torch():
     return _T
 
 
+class _LongWay:
+    """In the compiled calls' place: None from each."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _calls():
     global _CALLS
     if _CALLS is None:
         import importlib.machinery
         import importlib.util
 
-        _torch()  # (whose libraries it is linked to)
-        loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
-        loader.exec_module(module)
-        module.bind(MX4, MX8)
-        _CALLS = module
+        torch = _torch()  # (whose libraries they are linked to)
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
+            calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+            loader.exec_module(calls)
+            made_for = getattr(calls, "torch_version", "another")
+            if not torch.__version__.startswith(made_for):
+                raise ImportError(f"built for torch {made_for}, this is {torch.__version__}")
+            calls.bind(MX4, MX8)
+        except ImportError as e:
+            warnings.warn(f"{CALLS_PATH} cannot be used ({e}): small calls take a few microseconds more of the host's time; "
+                          "build it with __graft_entry__.build()", RuntimeWarning, stacklevel=3)
+            calls = _LongWay()
+        _CALLS = calls
     return _CALLS
 
 

@@ -19,6 +19,7 @@
 #include <torch/csrc/Device.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "../../include/zero_sm.h"
 
@@ -350,5 +351,8 @@ PyMODINIT_FUNC PyInit__calls() {
   s_cols = PyUnicode_InternFromString("cols"), s_device = PyUnicode_InternFromString("device");
   s_at = PyUnicode_InternFromString("_at"), s_struct = PyUnicode_InternFromString("_struct_");
   g_no_args = PyTuple_New(0);
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  // (torch's C++ interface is its version's own)
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
 }
