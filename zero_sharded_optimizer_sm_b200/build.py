@@ -59,37 +59,45 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
                 print(res.stderr, end="")
             if res.returncode != 0:
                 raise subprocess.CalledProcessError(res.returncode, res.args, res.stdout, res.stderr)
-    # link beside the library and rename over it: a reader never sees a
-    # half-written file
-    tmp = LIB + ".tmp"
-    link = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
+    # both are made before either is renamed into its place: a reader never sees
+    # a half-written file, nor a step that failed half of a new pair
+    lib = os.path.join(bdir, os.path.basename(LIB))
+    link = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", lib, *objs]
     if verbose:
         print(" ".join(link))
     subprocess.run(link, check=True)
-    os.replace(tmp, LIB)
-    build_calls(verbose)
+    calls = build_calls(bdir, verbose)
+    if calls is None and os.path.exists(CALLS):
+        os.remove(CALLS)  # (another library's)
+    os.replace(lib, LIB)
+    if calls is not None:
+        os.replace(calls, CALLS)
     return LIB
 
 
-def build_calls(verbose: bool = False) -> str:
-    """``_calls.so``: the compiled Python calls, linked to the library beside it
-    and to the torch that is installed."""
+def build_calls(bdir: str, verbose: bool = False):
+    """``_calls.so`` in ``bdir``: the compiled Python calls, linked to the library
+    there and to the torch that is installed.  None where there is none: the
+    calls are a shortcut."""
     import importlib.util
     import sysconfig
 
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch = importlib.util.find_spec("torch")
+    if torch is None or not torch.origin:
+        print("torch is not installed: the library is built without its compiled Python calls")
+        return None
+    torch_dir = os.path.dirname(torch.origin)
     inc = os.path.join(torch_dir, "include")
-    tmp = CALLS + ".tmp"
+    out = os.path.join(bdir, os.path.basename(CALLS))
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
-           os.path.join(HERE, "csrc", "calls.cpp"), "-o", tmp, "-L" + HERE, "-l:libzero_sm.so", "-Wl,-rpath,$ORIGIN",
+           os.path.join(HERE, "csrc", "calls.cpp"), "-o", out, "-L" + bdir, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
            "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(tmp, CALLS)
-    return CALLS
+    return out
 
 
 if __name__ == "__main__":
