@@ -1,7 +1,9 @@
 """GPU tests of calls around a layer's products at the edges of their ranges:
-rows without columns, tables without rows."""
+rows without columns, tables without rows, results whose rows are far apart."""
 import pytest
 import torch
+
+from test_gpu_mx8 import normal
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +41,24 @@ def test_an_mx4_table_without_rows(z, dtype):
         assert not big[:, :64].any() and (big[:, 64:] == 7).all()
     m = z.MX4(torch.empty(0, 32, dtype=torch.uint8, device="cuda"), torch.empty(0, 2, dtype=torch.uint8, device="cuda"), 0, 64)
     assert not z.embedding(t, m).any()
+
+
+def test_zeros_into_rows_that_are_far_apart(z):
+    """A gradient of no tokens, whose rows are more than 2^31 bytes apart; and one
+    row of more."""
+    pitch = (1 << 30) + 72
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("wants 8 GB")
+    memory = torch.full((2 * pitch,), 3.0, dtype=torch.bfloat16, device="cuda")
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    table = memory.as_strided((2, 40), (pitch, 1))
+    z.embedding_backward(normal(0, 40, "bf16", 1), none, 2, out=table)
+    assert not table.any() and (memory[40:80] == 3).all() and (memory[pitch + 40:pitch + 80] == 3).all()
+    table.fill_(3)
+    w = z.mx4_quantize(normal(2, 40, "bf16", 2))
+    z.mx4_linear_backward(normal(0, 2, "bf16", 1), normal(0, 40, "bf16", 1), w, dw=table)
+    assert not table.any() and (memory[40:80] == 3).all()
+    wide = memory[:(1 << 30) + 9]
+    x = torch.empty(0, wide.shape[0], dtype=torch.bfloat16, device="cuda")
+    z.rms_norm_backward(x, x, wide, none.float(), dw=wide)
+    assert not wide.any() and memory[(1 << 30) + 9] == 3
