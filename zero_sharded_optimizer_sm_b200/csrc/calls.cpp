@@ -2,7 +2,7 @@
 // tensor on the current device, the current stream, new results.  A small
 // call's kernels take a few microseconds; checking the operands, taking memory
 // and calling through ctypes took 9 to 16 on the host (norm of one token 13 us
-// a call, 20 with its backward pass), and from here 3 to 6.
+// a call, 20 with its backward pass), and from here 3 to 7.
 //
 // Python's lock is let go of while memory is taken and kernels are launched, as
 // ctypes does: a launch waits where the stream's queue is full, and what it waits

@@ -369,11 +369,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
 //
 // Half the warps of every CTA first clear the rows of the table that no token of
 // the batch has -- most of the gradient's bytes, as a rule.  They look for the
-// tokens in the batch itself and do not wait for the sort, which thus takes
-// next to no time of its own; for a batch that is longer than a cluster sorts,
-// they search the sorted tokens instead.  The other half waits for the sort and
-// walks over the units (a slab of a segment), which takes it less time than the
-// clearing.  One CTA an SM: of two kinds of CTAs, the clearing ones came to lie
+// tokens in the batch itself and clear while the cluster sorts; for a batch that
+// is longer than a cluster sorts, they search the sorted tokens instead.  The
+// other half waits for the sort and walks over the units (a slab of a segment),
+// so that a short call is the sort's latency, the sums' and the join's one after
+// another (8192 tokens, 32000 x 768: 24 us, 9.4 at the copy's rate).  One CTA an SM: of two kinds of CTAs, the clearing ones came to lie
 // in pairs on half the SMs and took 47 us for 206 MB instead of 36.
 constexpr int kSumThreads = 1024;
 constexpr int kBitRows = 1 << 15;

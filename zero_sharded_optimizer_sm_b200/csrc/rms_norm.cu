@@ -1,9 +1,10 @@
 // Root-mean-square norm, forward and backward (rms_norm.cuh has the formulas).
 //
 // Both are memory-bound: forward 2 to 4 values of the row's type and up to two
-// MX8 bytes an element, backward 3 or 4.  A row's elements are read once: they
-// stay in registers (forward) or shared memory (backward), as they were loaded,
-// between the sum over the row and its use.
+// MX8 bytes an element, backward 3 or 4.  Elements of rows of up to 16384 columns
+// forward, 4096 backward, are read once: they stay in registers (forward) or
+// shared memory (backward), as they were loaded, between the sum over the row and
+// its use.  Longer rows are read twice.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -49,8 +50,9 @@ __device__ __forceinline__ double group_sum(const float (&of)[kSums], float* sme
 // rstd = m^(-1/2), m = ss / cols + eps: the function's binary32 estimate and one
 // Newton step in binary64, whose error is the square of the estimate's, rounded to
 // binary32 once.  (y's rounding to 16 and then to 8 bits turns on rstd's last bit
-// now and then.  The sum that m comes from is binary32's of 256 columns each: one
-// rstd in twenty of rows of 4096 is not the correctly rounded one.)
+// now and then.  The sum that m comes from is binary32's of 256 columns each: of
+// normal numbers 8 rstd in a hundred of rows of 4096 are not the correctly rounded
+// ones, 15 of rows of 512.)
 __device__ __forceinline__ double root_of(double m) {
   const float r = rsqrtf((float)m);
   const double e = __fma_rn(-__dmul_rn(m, (double)r), (double)r, 1.0);
@@ -171,11 +173,10 @@ __device__ __forceinline__ void finish(const RmsNormArgs& a, const NormRow<T>& r
 // thread; the host picks the block's threads to fit the row.  Blocks that end
 // make room for others whose loads go out at once, so that nothing has to be
 // fetched ahead: 8192 x 4096 bf16 with a residual and all results, 338 MB, takes
-// 52 us, the copy's rate (with 64-bit addresses for every access and single
-// products 70, issue slots 73 % busy; now 62 %); without MX8 41, the copy's rate
-// too.  Rows of odd length, 6000 x 2421 binary16 with all results, take 46 of 22:
-// instructions (75 %).  One token of 4096 takes 2.7, its launch and two trips to
-// memory.
+// 55 us, 52 at the copy's rate (with 64-bit addresses for every access and single
+// products 70), issue slots 75 % busy; without MX8 41.7 of 41.0.  Rows of odd
+// length, 6000 x 2421 binary16 with all results, take 46 of 22: instructions.  One
+// token of 4096 takes 2.6, its launch and two trips to memory.
 constexpr int kLanesThreads = 128;  // of a block whose warps have rows of their own
 template <class T, bool kWhole, int kLanes, int kChunks>
 __global__ void __launch_bounds__(kLanes ? kLanesThreads : 512) rms_norm_kernel(const __grid_constant__ RmsNormArgs a,
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(32 * kDwWarps) rms_norm_dw_kernel(const float*
 //   21845 x 768        28.5 and 30.8               twice the row's vectors in part)
 //   16384 x 1024       28.0 and 26.7, 8192 x 2048 29.3 and 26.5
 //   4096 x 4096        32.7 and 27.8, four 30.0
-//   2048 x 8192        two 32.3, four 32.9
+//   2048 x 8192        two 30.8, four 35.9
 // and while the SMs hold all rows' threads at once, latency counts:
 //   64 x 512           a block of one 2.4, a warp of two 2.8; 4096 x 512 4.6, 4.4
 //   64 x 2048          one 2.6, two 3.1; 2048 x 2048 8.0, 7.6
