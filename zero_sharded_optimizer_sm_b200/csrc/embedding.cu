@@ -373,8 +373,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
 // is longer than a cluster sorts, they search the sorted tokens instead.  The
 // other half waits for the sort and walks over the units (a slab of a segment),
 // so that a short call is the sort's latency, the sums' and the join's one after
-// another (8192 tokens, 32000 x 768: 24 us, 9.4 at the copy's rate).  One CTA an SM: of two kinds of CTAs, the clearing ones came to lie
-// in pairs on half the SMs and took 47 us for 206 MB instead of 36.
+// another (8192 tokens, 32000 x 768: 24 us, 9.4 at the copy's rate).  One CTA an
+// SM: of two kinds of CTAs, the clearing ones came to lie in pairs on half the SMs
+// and took 47 us for 206 MB instead of 36.
 constexpr int kSumThreads = 1024;
 constexpr int kBitRows = 1 << 15;
 
